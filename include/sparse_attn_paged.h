@@ -309,6 +309,146 @@ int sparse_attn_indexer_logits(const void* q, const float* weights, int32_t num_
 int sparse_attn_indexer_topk(const float* logits, int32_t num_tokens, int32_t num_cols,
                              const int32_t* cand, int32_t k, int32_t* topk_idx, void* stream);
 
+/*
+ * ---- Latent attention: keys and values from ONE shared latent vector a token ----
+ *
+ * A cached row x = [c | r] has a latent part c of latent_dim values, which is the value and most of
+ * the key of every head, and a rotary part r of rope_dim values, which belongs to the key only.
+ * The rows live in a paged pool of their own, addressed like the K/V pools: the entry at position x
+ * of sequence b is row block_table[b][x / page_size] * page_size + x % page_size.
+ *   bf16 rows (entry points without suffix): [c | r], latent_dim + rope_dim values.
+ *   e4m3 rows (_fp8 entry points): latent_dim + 2 * rope_dim codes, [c | r high | r low], and one
+ *     fp32 scale a row: c = scale * code, r = scale * (high + low).  The rotary part carries the
+ *     position, so it keeps the second code's bits; a row is latent_dim + 2 * rope_dim + 4 bytes.
+ * latent_dim: a multiple of 64, 64 .. 512.  rope_dim: a multiple of 8, 0 .. 64.
+ * num_blocks * page_size <= 2^30, and rows 16-byte aligned.
+ */
+typedef struct spa_latent_pool {
+  const void* rows;             /* device [num_blocks][page_size][row], bf16 or e4m3 codes    */
+  const float* scale;           /* device [num_blocks * page_size], e4m3 pools only           */
+  const int32_t* block_table;   /* device [num_seqs][bt_stride]; -1 marks an unmapped page    */
+  int64_t num_blocks;
+  int32_t page_size;
+  int32_t bt_stride;
+  int32_t latent_dim;
+  int32_t rope_dim;
+} spa_latent_pool_t;
+
+/*
+ * Write the rows of new tokens into the pool.
+ *   latent: bf16 [num_tokens] rows of latent_dim, row stride latent_stride elements;
+ *   rope:   bf16 [num_tokens] rows of rope_dim, row stride rope_stride (NULL when rope_dim == 0);
+ *   both 16-byte aligned with strides a multiple of 8 elements (>= 0).
+ *   positions, seq_of_token (NULL: sequence 0), num_seqs: as for the K/V write.
+ * _fp8: over the row's latent_dim + rope_dim values, scale = max|x| / 448 (IEEE fp32 division; 1
+ * for an all-zero row), codes e4m3(x / scale) by IEEE fp32 division and round to nearest even; the
+ * rotary part's high code likewise and its low code e4m3(x / scale - high), the difference in fp32
+ * (exact).  A NaN element gives NaN codes and does not enter the maximum.
+ * A token that cannot be placed is skipped and sets SPA_ERR_INDEX, as in the K/V write; slots that
+ * no token addresses keep their bytes.  Two tokens writing one slot: the later write is not
+ * defined.
+ */
+int sparse_attn_latent_write(const void* latent, int64_t latent_stride, const void* rope,
+                             int64_t rope_stride, int32_t num_tokens, const int32_t* positions,
+                             const int32_t* seq_of_token, int32_t num_seqs,
+                             const spa_latent_pool_t* pool, void* stream);
+int sparse_attn_latent_write_fp8(const void* latent, int64_t latent_stride, const void* rope,
+                                 int64_t rope_stride, int32_t num_tokens, const int32_t* positions,
+                                 const int32_t* seq_of_token, int32_t num_seqs,
+                                 const spa_latent_pool_t* pool, void* stream);
+
+/*
+ * Read rows of the pool back: out[i][:] = the row of (seq_of_token[i], positions[i]) as bf16
+ * [c | r] of latent_dim + rope_dim values (out: row stride out_stride elements, a multiple of 8,
+ * 16-byte aligned).  _fp8: scale * code, scale * (high + low) in fp32, rounded to nearest even.
+ * What the expanded form needs of a cached prefix, before its up-projection.  A row that cannot be
+ * found is written as zeros and sets SPA_ERR_INDEX.
+ */
+int sparse_attn_latent_read(const spa_latent_pool_t* pool, int32_t num_rows,
+                            const int32_t* positions, const int32_t* seq_of_token, int32_t num_seqs,
+                            void* out, int64_t out_stride, void* stream);
+int sparse_attn_latent_read_fp8(const spa_latent_pool_t* pool, int32_t num_rows,
+                                const int32_t* positions, const int32_t* seq_of_token,
+                                int32_t num_seqs, void* out, int64_t out_stride, void* stream);
+
+/*
+ * Absorbed latent attention over the paged cache (decode: one token a sequence or a few).  Query
+ * token t of sequence b = seq_of_token[t] attends to every entry j <= positions[t]:
+ *     s_j = scale * (q_latent[t][h] . c_j + q_rope[t][h] . r_j)
+ *     out[t][h][:] = sum_j softmax(s)_j c_j               (bf16, round to nearest even)
+ * q_latent = q_nope W_uk is the caller's product, as is the up-projection of out by W_uv.
+ *   q_latent: bf16 [num_tokens][num_heads] rows of latent_dim, strides in elements (token, head);
+ *   q_rope:   the same with rope_dim (NULL when rope_dim == 0);
+ *   both 16-byte aligned, strides multiples of 8 elements (>= 0).
+ *   out:      bf16 [num_tokens][num_heads][latent_dim], 16-byte aligned, not overlapping an input.
+ * A negative position attends to nothing: its output rows are zero (padding of a batch).  Entries
+ * on unmapped pages, past the block table or outside the pool are left out and set SPA_ERR_INDEX,
+ * as does a sequence id outside [0, num_seqs), whose output rows are zero.  What is left out never
+ * enters the sums, whatever its bytes hold (rows past a sequence's last may be uninitialised).
+ * Softmax statistics, scores and sums are fp32; the probabilities enter the value product as bf16
+ * (bf16 pools) or as an e5m2 and an e4m3 term (e4m3 pools).
+ * workspace: device memory, 16-byte aligned, of at least
+ * sparse_attn_latent_decode_workspace_size(prob, pool) bytes for partial results of sequences that
+ * are split over several SMs; contents scratch, nothing has to be cleared.  Calls that can run at
+ * the same time need workspaces of their own; calls ordered on one stream (or graphs launched one
+ * after the other) may share one.
+ */
+typedef struct spa_latent_problem {
+  int32_t num_tokens;
+  int32_t num_seqs;             /* rows of the block table                                    */
+  int32_t num_heads;
+  float scale;
+  const int32_t* positions;     /* device [T]                                                 */
+  const int32_t* seq_of_token;  /* device [T] or NULL (all in sequence 0)                     */
+  const void* q_latent;
+  const void* q_rope;
+  int64_t q_latent_stride_t, q_latent_stride_h;
+  int64_t q_rope_stride_t, q_rope_stride_h;
+} spa_latent_problem_t;
+
+size_t sparse_attn_latent_decode_workspace_size(const spa_latent_problem_t* prob,
+                                                const spa_latent_pool_t* pool);
+int sparse_attn_latent_decode(const spa_latent_pool_t* pool, const spa_latent_problem_t* prob,
+                              void* out, void* workspace, size_t workspace_bytes, void* stream);
+int sparse_attn_latent_decode_fp8(const spa_latent_pool_t* pool, const spa_latent_problem_t* prob,
+                                  void* out, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Expanded latent attention (prefill): ragged causal sequences with per-head keys [k_nope | k_rope]
+ * and values, k_rope shared by all heads.  Sequence b owns query rows cu_q[b] .. cu_q[b+1] and key
+ * rows cu_k[b] .. cu_k[b+1]; its last query sees its last key:
+ *     query i sees keys j <= i + n_k - n_q      (n_q, n_k the sequence's query and key rows)
+ *     out[i][h][:] = sum_j softmax_j(scale * (q[i][h] . [k_nope[j][h] | k_rope[j]])) v[j][h][:]
+ * so n_k > n_q is a chunk after a prefix.  A query that sees no key (n_k < n_q) gives zeros.
+ *   q:      bf16 [num_q] x [num_heads] rows of nope_dim + rope_dim   (strides: token, head)
+ *   k_nope: bf16 [num_k] x [num_heads] rows of nope_dim;  v: the same, rows of v_dim
+ *   k_rope: bf16 [num_k] rows of rope_dim (NULL when rope_dim == 0)
+ *   out:    bf16 [num_q][num_heads][v_dim], 16-byte aligned, not overlapping an input
+ *   cu_q, cu_k: device int32 [num_seqs + 1], non-decreasing, within [0, num_q] and [0, num_k].  A
+ *           sequence whose bounds are not is left out (its output rows keep their bytes) and sets
+ *           SPA_ERR_INDEX.  Query rows of no sequence keep their bytes.
+ * nope_dim, v_dim: multiples of 8, 8 .. 128; rope_dim: a multiple of 8, 0 .. 64.  Pointers 16-byte
+ * aligned, strides multiples of 8 elements and >= the row's width where the dimension is over 1.
+ * Rows of other sequences never enter a sequence's sums, whatever they hold.  Within a sequence a
+ * value row that is not finite may reach the queries of the 127 tokens before it (a masked
+ * probability of zero times it); keys and scores have no such limit.
+ * Scores, softmax statistics and sums are fp32; the probabilities enter the value product as bf16.
+ * Needs no workspace.
+ */
+typedef struct spa_latent_prefill {
+  int32_t num_q, num_k, num_seqs, num_heads;
+  int32_t nope_dim, rope_dim, v_dim;
+  float scale;
+  const void *q, *k_nope, *k_rope, *v;
+  int64_t q_stride_t, q_stride_h;
+  int64_t k_nope_stride_t, k_nope_stride_h;
+  int64_t k_rope_stride_t;
+  int64_t v_stride_t, v_stride_h;
+  const int32_t *cu_q, *cu_k;   /* device [num_seqs + 1] */
+} spa_latent_prefill_t;
+
+int sparse_attn_latent_prefill(const spa_latent_prefill_t* prob, void* out, void* stream);
+
 /* Synchronises `stream`, returns the device error word (an OR of SPA_ERR_INDEX and
  * SPA_ERR_TIMEOUT, 0 if clean) accumulated since the last check on the current device, and
  * clears it.  Returns SPA_ERR_CUDA if the synchronisation itself fails. */

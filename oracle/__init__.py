@@ -23,7 +23,8 @@ to nearest even, one scale per row, slot placement) by ``tests/test_oracle_kv_wr
 compressor's gated pool (``oracle.gated_pool``: a per-channel softmax over R rows weighting the kv
 rows, a stated reading) by ``tests/test_oracle_gated_pool.py``; the indexer logits over packed fp4
 key rows (``oracle.indexer``: OCP E2M1/E8M0 decoding, a stated logit reading) by
-``tests/test_oracle_indexer.py``.
+``tests/test_oracle_indexer.py``; latent attention (``oracle.latent``: the latent cache's write and
+read, the absorbed and the expanded form) by ``tests/test_oracle_latent.py``.
 """
 from .sparse_attention import (  # noqa: F401
     COL_POOL_SHIFT,
@@ -36,4 +37,4 @@ from .sparse_attention import (  # noqa: F401
     resolve_columns,
     sparse_paged_attention,
 )
-from . import gated_pool, indexer, kv_write  # noqa: F401
+from . import gated_pool, indexer, kv_write, latent  # noqa: F401

@@ -25,7 +25,10 @@ __all__ = [
     "sparse_attn_paged_kv_write_fp8", "sparse_attn_gated_pool", "sparse_attn_indexer_logits",
     "sparse_attn_indexer_topk", "sparse_attn_paged_prefill_host",
     "sparse_attn_paged_prefill_host_fp8", "BoundCall", "bind_prefill", "bind_prefill_host",
-    "bind_decode",
+    "bind_decode", "LatentPool", "sparse_attn_latent_write", "sparse_attn_latent_write_fp8",
+    "sparse_attn_latent_read", "sparse_attn_latent_read_fp8", "sparse_attn_latent_decode",
+    "sparse_attn_latent_decode_fp8", "sparse_attn_latent_decode_workspace_size",
+    "bind_latent_decode", "sparse_attn_latent_prefill",
     "sparse_attn_paged_check_errors", "sparse_attn_paged_strerror", "SPA_STATUS",
 ]
 
@@ -55,6 +58,36 @@ class SpaProblemC(ctypes.Structure):
                 ("window", ctypes.c_int32), ("topk", ctypes.c_int32), ("ratio", ctypes.c_int32),
                 ("scale", ctypes.c_float), ("positions", ctypes.c_void_p),
                 ("seq_of_token", ctypes.c_void_p), ("topk_idx", ctypes.c_void_p)]
+
+
+class SpaLatentPoolC(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_void_p), ("scale", ctypes.c_void_p),
+                ("block_table", ctypes.c_void_p), ("num_blocks", ctypes.c_int64),
+                ("page_size", ctypes.c_int32), ("bt_stride", ctypes.c_int32),
+                ("latent_dim", ctypes.c_int32), ("rope_dim", ctypes.c_int32)]
+
+
+class SpaLatentProblemC(ctypes.Structure):
+    _fields_ = [("num_tokens", ctypes.c_int32), ("num_seqs", ctypes.c_int32),
+                ("num_heads", ctypes.c_int32), ("scale", ctypes.c_float),
+                ("positions", ctypes.c_void_p), ("seq_of_token", ctypes.c_void_p),
+                ("q_latent", ctypes.c_void_p), ("q_rope", ctypes.c_void_p),
+                ("q_latent_stride_t", ctypes.c_int64), ("q_latent_stride_h", ctypes.c_int64),
+                ("q_rope_stride_t", ctypes.c_int64), ("q_rope_stride_h", ctypes.c_int64)]
+
+
+class SpaLatentPrefillC(ctypes.Structure):
+    _fields_ = [("num_q", ctypes.c_int32), ("num_k", ctypes.c_int32),
+                ("num_seqs", ctypes.c_int32), ("num_heads", ctypes.c_int32),
+                ("nope_dim", ctypes.c_int32), ("rope_dim", ctypes.c_int32),
+                ("v_dim", ctypes.c_int32), ("scale", ctypes.c_float),
+                ("q", ctypes.c_void_p), ("k_nope", ctypes.c_void_p),
+                ("k_rope", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("q_stride_t", ctypes.c_int64), ("q_stride_h", ctypes.c_int64),
+                ("k_nope_stride_t", ctypes.c_int64), ("k_nope_stride_h", ctypes.c_int64),
+                ("k_rope_stride_t", ctypes.c_int64),
+                ("v_stride_t", ctypes.c_int64), ("v_stride_h", ctypes.c_int64),
+                ("cu_q", ctypes.c_void_p), ("cu_k", ctypes.c_void_p)]
 
 
 class SpaError(RuntimeError):
@@ -112,6 +145,23 @@ def load_library():
     lib.sparse_attn_indexer_logits.restype = ctypes.c_int
     lib.sparse_attn_indexer_topk.argtypes = [P, I32, I32, P, I32, P, P]
     lib.sparse_attn_indexer_topk.restype = ctypes.c_int
+    PL, PLP = ctypes.POINTER(SpaLatentPoolC), ctypes.POINTER(SpaLatentProblemC)
+    for name in ("sparse_attn_latent_write", "sparse_attn_latent_write_fp8"):
+        f = getattr(lib, name)
+        f.argtypes = [P, I64, P, I64, I32, P, P, I32, PL, P]
+        f.restype = ctypes.c_int
+    for name in ("sparse_attn_latent_read", "sparse_attn_latent_read_fp8"):
+        f = getattr(lib, name)
+        f.argtypes = [PL, I32, P, P, I32, P, I64, P]
+        f.restype = ctypes.c_int
+    lib.sparse_attn_latent_decode_workspace_size.argtypes = [PLP, PL]
+    lib.sparse_attn_latent_decode_workspace_size.restype = ctypes.c_size_t
+    for name in ("sparse_attn_latent_decode", "sparse_attn_latent_decode_fp8"):
+        f = getattr(lib, name)
+        f.argtypes = [PL, PLP, P, P, ctypes.c_size_t, P]
+        f.restype = ctypes.c_int
+    lib.sparse_attn_latent_prefill.argtypes = [ctypes.POINTER(SpaLatentPrefillC), P, P]
+    lib.sparse_attn_latent_prefill.restype = ctypes.c_int
     lib.sparse_attn_paged_check_errors.argtypes = [P]
     lib.sparse_attn_paged_check_errors.restype = ctypes.c_int
     lib.sparse_attn_paged_strerror.argtypes = [ctypes.c_int]
@@ -483,6 +533,284 @@ def sparse_attn_indexer_topk(logits, k, *, cand=None, out=None, stream=None):
                                       out.data_ptr(), _stream(stream))
     if st != 0:
         raise SpaError(st, "sparse_attn_indexer_topk")
+    return out
+
+
+# ---- latent attention -----------------------------------------------------------------------
+class LatentPool(NamedTuple):
+    """A paged pool of latent rows ``[c | r]`` (see the C header).
+
+    ``rows``: bf16 [num_blocks, page_size, latent_dim + rope_dim], or uint8 e4m3 codes
+    [num_blocks, page_size, latent_dim + 2 * rope_dim] with ``scale`` fp32 [num_blocks * page_size];
+    ``block_table``: int32 [num_seqs, stride], -1 marks an unmapped page.
+    """
+    rows: torch.Tensor
+    block_table: torch.Tensor
+    rope_dim: int
+    scale: Optional[torch.Tensor] = None
+
+
+def _latent_pool_c(pool, fp8: bool) -> SpaLatentPoolC:
+    rows, bt, R = pool.rows, pool.block_table, int(pool.rope_dim)
+    want = torch.uint8 if fp8 else torch.bfloat16
+    if rows.dtype != want:
+        raise TypeError(f"pool rows must be {want}, got {rows.dtype}")
+    if rows.dim() != 3 or not rows.is_contiguous():
+        raise ValueError("pool rows must be a contiguous [num_blocks, page_size, row] tensor")
+    if bt.dtype != torch.int32 or bt.dim() != 2 or not bt.is_contiguous():
+        raise ValueError("block_table must be a contiguous int32 [num_seqs, stride] tensor")
+    nb, ps, width = rows.shape
+    if fp8 and (pool.scale is None or pool.scale.dtype != torch.float32 or
+                not pool.scale.is_contiguous() or pool.scale.numel() != nb * ps):
+        raise ValueError("an e4m3 pool needs a contiguous fp32 scale of num_blocks * page_size")
+    L = width - (2 * R if fp8 else R)
+    if R < 0 or L < 1:
+        raise ValueError("rope_dim does not fit the pool's rows")
+    return SpaLatentPoolC(rows.data_ptr(), pool.scale.data_ptr() if fp8 else None, bt.data_ptr(),
+                          nb, ps, bt.shape[1], L, R)
+
+
+def _one_device(named):
+    """The one CUDA device of the tensors given (None entries skipped), or ValueError."""
+    dev = None
+    for name, t in named:
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor")
+        if dev is None:
+            dev = t.device
+        elif t.device != dev:
+            raise ValueError(f"{name} is on {t.device}, other arguments on {dev}")
+    if dev.index != torch.cuda.current_device():
+        raise ValueError(f"the arguments are on {dev}, which is not the current device "
+                         f"(cuda:{torch.cuda.current_device()})")
+    return dev
+
+
+def _stride(t, dim) -> int:
+    """A stride in elements; 0 for an absent tensor or a dimension of one (whose stride is free)."""
+    return 0 if t is None or t.shape[dim] <= 1 else t.stride(dim)
+
+
+def _latent_index(positions, seq_of_token, n):
+    for name, t in (("positions", positions), ("seq_of_token", seq_of_token)):
+        if t is not None and (t.dtype != torch.int32 or not t.is_contiguous() or t.numel() != n):
+            raise ValueError(f"{name} must be a contiguous int32 tensor of {n} entries")
+
+
+def _latent_rows(name, t, dims, width):
+    """A bf16 tensor of `dims` dimensions with unit last stride and (if given) last size."""
+    if t.dtype != torch.bfloat16 or t.dim() != dims or (t.shape[-1] > 1 and t.stride(-1) != 1) or \
+            (width is not None and t.shape[-1] != width):
+        raise ValueError(f"{name} must be a bf16 tensor of {dims} dimensions with unit last stride"
+                         + ("" if width is None else f" and {width} values a row"))
+
+
+def _latent_write(fp8, latent, rope, positions, pool, *, seq_of_token=None, num_seqs=None,
+                  stream=None):
+    lib = load_library()
+    c = _latent_pool_c(pool, fp8)
+    _latent_rows("latent", latent, 2, c.latent_dim)
+    T = int(latent.shape[0])
+    if c.rope_dim > 0:
+        if rope is None:
+            raise ValueError("the pool's rows have a rotary part: rope is missing")
+        _latent_rows("rope", rope, 2, c.rope_dim)
+        if rope.shape[0] != T:
+            raise ValueError("latent and rope must have the same number of rows")
+    else:
+        rope = None
+    _latent_index(positions, seq_of_token, T)
+    _one_device((("latent", latent), ("rope", rope), ("positions", positions),
+                 ("seq_of_token", seq_of_token), ("pool rows", pool.rows),
+                 ("block_table", pool.block_table), ("pool scale", pool.scale if fp8 else None)))
+    B = int(pool.block_table.shape[0]) if num_seqs is None else int(num_seqs)
+    if B > pool.block_table.shape[0]:
+        raise ValueError("num_seqs exceeds the block table's rows")
+    fn = lib.sparse_attn_latent_write_fp8 if fp8 else lib.sparse_attn_latent_write
+    st = fn(latent.data_ptr(), _stride(latent, 0), _ptr(rope), _stride(rope, 0), T, positions.data_ptr(),
+            _ptr(seq_of_token), B, ctypes.byref(c), _stream(stream))
+    if st != 0:
+        raise SpaError(st, fn.__name__)
+
+
+def sparse_attn_latent_write(latent, rope, positions, pool, **kw):
+    """Copy the rows of new tokens (bf16 ``latent`` [T, L] and ``rope`` [T, R], None without a rotary
+    part) into their slots of a bf16 latent pool."""
+    _latent_write(False, latent, rope, positions, pool, **kw)
+
+
+def sparse_attn_latent_write_fp8(latent, rope, positions, pool, **kw):
+    """Quantise the rows of new tokens to e4m3 (one scale a row, two codes a rotary value) into an
+    e4m3 latent pool."""
+    _latent_write(True, latent, rope, positions, pool, **kw)
+
+
+def _latent_read(fp8, positions, pool, *, seq_of_token=None, num_seqs=None, out=None, stream=None):
+    lib = load_library()
+    c = _latent_pool_c(pool, fp8)
+    n, width = int(positions.numel()), c.latent_dim + c.rope_dim
+    _latent_index(positions, seq_of_token, n)
+    if out is None:
+        out = torch.empty((n, width), dtype=torch.bfloat16, device=pool.rows.device)
+    _latent_rows("out", out, 2, width)
+    if out.shape[0] != n:
+        raise ValueError(f"out must have {n} rows")
+    _one_device((("positions", positions), ("seq_of_token", seq_of_token),
+                 ("pool rows", pool.rows), ("block_table", pool.block_table),
+                 ("pool scale", pool.scale if fp8 else None), ("out", out)))
+    B = int(pool.block_table.shape[0]) if num_seqs is None else int(num_seqs)
+    if B > pool.block_table.shape[0]:
+        raise ValueError("num_seqs exceeds the block table's rows")
+    fn = lib.sparse_attn_latent_read_fp8 if fp8 else lib.sparse_attn_latent_read
+    st = fn(ctypes.byref(c), n, positions.data_ptr(), _ptr(seq_of_token), B, out.data_ptr(),
+            _stride(out, 0), _stream(stream))
+    if st != 0:
+        raise SpaError(st, fn.__name__)
+    return out
+
+
+def sparse_attn_latent_read(positions, pool, **kw):
+    """Rows of a bf16 latent pool: bf16 [n, L + R], row i that of (seq_of_token[i], positions[i])."""
+    return _latent_read(False, positions, pool, **kw)
+
+
+def sparse_attn_latent_read_fp8(positions, pool, **kw):
+    """The same from an e4m3 pool, dequantised to bf16."""
+    return _latent_read(True, positions, pool, **kw)
+
+
+def _latent_decode_args(fp8, q_latent, q_rope, pool, positions, *, scale, seq_of_token=None,
+                        num_seqs=None, out=None, workspace=None, stream=None):
+    """Checked arguments of a latent decode: (C function, its arguments, out, workspace, what the
+    arguments point into)."""
+    lib = load_library()
+    c = _latent_pool_c(pool, fp8)
+    _latent_rows("q_latent", q_latent, 3, c.latent_dim)
+    T, H = int(q_latent.shape[0]), int(q_latent.shape[1])
+    if c.rope_dim > 0:
+        if q_rope is None:
+            raise ValueError("the pool's rows have a rotary part: q_rope is missing")
+        _latent_rows("q_rope", q_rope, 3, c.rope_dim)
+        if q_rope.shape[0] != T or q_rope.shape[1] != H:
+            raise ValueError("q_latent and q_rope must have the same tokens and heads")
+    else:
+        q_rope = None
+    _latent_index(positions, seq_of_token, T)
+    if out is None:
+        out = torch.empty((T, H, c.latent_dim), dtype=torch.bfloat16, device=q_latent.device)
+    elif out.dtype != torch.bfloat16 or tuple(out.shape) != (T, H, c.latent_dim) or \
+            not out.is_contiguous():
+        raise ValueError("out must be a contiguous bf16 [num_tokens, num_heads, latent_dim] tensor")
+    B = int(pool.block_table.shape[0]) if num_seqs is None else int(num_seqs)
+    if B > pool.block_table.shape[0]:
+        raise ValueError("num_seqs exceeds the block table's rows")
+    dev = _one_device((("q_latent", q_latent), ("q_rope", q_rope), ("positions", positions),
+                       ("seq_of_token", seq_of_token), ("pool rows", pool.rows),
+                       ("block_table", pool.block_table),
+                       ("pool scale", pool.scale if fp8 else None), ("out", out),
+                       ("workspace", workspace)))
+    prob = SpaLatentProblemC(T, B, H, float(scale), positions.data_ptr(), _ptr(seq_of_token),
+                             q_latent.data_ptr(), _ptr(q_rope), _stride(q_latent, 0),
+                             _stride(q_latent, 1), _stride(q_rope, 0), _stride(q_rope, 1))
+    if workspace is None:
+        nbytes = int(lib.sparse_attn_latent_decode_workspace_size(ctypes.byref(prob),
+                                                                  ctypes.byref(c)))
+        workspace = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=dev)
+    fn = lib.sparse_attn_latent_decode_fp8 if fp8 else lib.sparse_attn_latent_decode
+    args = (ctypes.byref(c), ctypes.byref(prob), out.data_ptr(), workspace.data_ptr(),
+            workspace.numel() * workspace.element_size())
+    return fn, args, out, workspace, (q_latent, q_rope, pool, positions, seq_of_token, c, prob)
+
+
+def _latent_decode(fp8, q_latent, q_rope, pool, positions, stream=None, **kw):
+    fn, args, out, workspace, keep = _latent_decode_args(fp8, q_latent, q_rope, pool, positions,
+                                                         stream=stream, **kw)
+    st = fn(*args, _stream(stream))
+    if st != 0:
+        raise SpaError(st, fn.__name__)
+    return out
+
+
+def sparse_attn_latent_decode(q_latent, q_rope, pool, positions, **kw):
+    """Absorbed latent attention of ``q_latent`` [T, H, L] and ``q_rope`` [T, H, R] (None without a
+    rotary part) over a paged bf16 latent pool: bf16 [T, H, L] (see the C header).  Token t attends
+    to entries 0 .. positions[t] of its sequence; the workspace is allocated with torch if none is
+    given."""
+    return _latent_decode(False, q_latent, q_rope, pool, positions, **kw)
+
+
+def sparse_attn_latent_decode_fp8(q_latent, q_rope, pool, positions, **kw):
+    """The same over an e4m3 latent pool."""
+    return _latent_decode(True, q_latent, q_rope, pool, positions, **kw)
+
+
+def sparse_attn_latent_decode_workspace_size(q_latent, pool, positions, *, fp8=False,
+                                             num_seqs=None) -> int:
+    """Bytes of workspace that a latent decode of these shapes needs."""
+    lib = load_library()
+    c = _latent_pool_c(pool, fp8)
+    B = int(pool.block_table.shape[0]) if num_seqs is None else int(num_seqs)
+    prob = SpaLatentProblemC(int(q_latent.shape[0]), B, int(q_latent.shape[1]), 1.0,
+                             positions.data_ptr(), None, q_latent.data_ptr(), None, 0, 0, 0, 0)
+    return int(lib.sparse_attn_latent_decode_workspace_size(ctypes.byref(prob), ctypes.byref(c)))
+
+
+def bind_latent_decode(q_latent, q_rope, pool, positions, *, fp8=False, stream=None,
+                       **kw) -> BoundCall:
+    """``sparse_attn_latent_decode[_fp8]`` on fixed tensors, as a zero-argument callable (workspace
+    and output are allocated here once when not given)."""
+    fn, args, out, workspace, keep = _latent_decode_args(fp8, q_latent, q_rope, pool, positions,
+                                                         stream=stream, **kw)
+    call = BoundCall(fn, args, keep + (out, workspace), stream)
+    call.out = out
+    call.workspace = workspace
+    return call
+
+
+def sparse_attn_latent_prefill(q, k_nope, k_rope, v, cu_q, cu_k, *, scale, out=None, stream=None):
+    """Expanded latent attention of ragged causal sequences: bf16 [Tq, H, v_dim].
+
+    ``q`` [Tq, H, nope + rope], ``k_nope`` [Tk, H, nope], ``v`` [Tk, H, v_dim] (views of one
+    up-projection's output will do), ``k_rope`` [Tk, rope] shared by the heads (None without a rotary
+    part); ``cu_q``, ``cu_k``: int32 [num_seqs + 1] row bounds of the sequences, whose last query
+    sees their last key (see the C header)."""
+    lib = load_library()
+    _latent_rows("q", q, 3, None)
+    _latent_rows("k_nope", k_nope, 3, None)
+    _latent_rows("v", v, 3, None)
+    Tq, H, dk = (int(x) for x in q.shape)
+    Tk, dn, dv = int(k_nope.shape[0]), int(k_nope.shape[2]), int(v.shape[2])
+    dr = dk - dn
+    if k_nope.shape[1] != H or v.shape[1] != H or v.shape[0] != Tk or dr < 0:
+        raise ValueError("q, k_nope and v must agree in heads, keys and widths")
+    if dr > 0:
+        if k_rope is None:
+            raise ValueError("q has a rotary part: k_rope is missing")
+        _latent_rows("k_rope", k_rope, 2, dr)
+        if k_rope.shape[0] != Tk:
+            raise ValueError("k_rope must have as many rows as k_nope")
+    else:
+        k_rope = None
+    for name, t in (("cu_q", cu_q), ("cu_k", cu_k)):
+        if t.dtype != torch.int32 or t.dim() != 1 or not t.is_contiguous() or t.numel() < 1 or \
+                t.numel() != cu_q.numel():
+            raise ValueError(f"{name} must be a contiguous int32 [num_seqs + 1] tensor")
+    if out is None:
+        out = torch.empty((Tq, H, dv), dtype=torch.bfloat16, device=q.device)
+    elif out.dtype != torch.bfloat16 or tuple(out.shape) != (Tq, H, dv) or not out.is_contiguous():
+        raise ValueError("out must be a contiguous bf16 [num_q, num_heads, v_dim] tensor")
+    _one_device((("q", q), ("k_nope", k_nope), ("k_rope", k_rope), ("v", v), ("cu_q", cu_q),
+                 ("cu_k", cu_k), ("out", out)))
+    prob = SpaLatentPrefillC(Tq, Tk, cu_q.numel() - 1, H, dn, dr, dv, float(scale), q.data_ptr(),
+                             k_nope.data_ptr(), _ptr(k_rope), v.data_ptr(), _stride(q, 0),
+                             _stride(q, 1), _stride(k_nope, 0), _stride(k_nope, 1),
+                             _stride(k_rope, 0), _stride(v, 0), _stride(v, 1),
+                             cu_q.data_ptr(), cu_k.data_ptr())
+    st = lib.sparse_attn_latent_prefill(ctypes.byref(prob), out.data_ptr(), _stream(stream))
+    if st != 0:
+        raise SpaError(st, "sparse_attn_latent_prefill")
     return out
 
 

@@ -8,6 +8,7 @@
 
 #include "sparse_attn_paged.h"
 #include "spa_indexer.h"
+#include "spa_latent.h"
 #include "spa_launch.h"
 #include "spa_plan.h"
 
@@ -325,6 +326,9 @@ int run(const void* q, const spa_pool_t* win, const spa_pool_t* cmp, const spa_p
 }  // namespace
 
 namespace spa {
+int api_current_device(int* dev, int* sms) { return current_device(dev, sms); }
+int api_cuda_fail(cudaError_t e, const char* what) { return cuda_fail(e, what); }
+
 size_t decode_partials_bytes(const spa_problem_t* prob, size_t cap_bytes) {
   if (!prob || prob->num_tokens < 0 || prob->num_heads < 1 || prob->head_dim < 1) return 0;
   int dev = 0, sms = 0;
@@ -721,7 +725,16 @@ int sparse_attn_paged_check_errors(void* stream) {
   int x = 0;
   e = spa::read_and_clear_indexer_error_word(&x);
   if (e != cudaSuccess) return cuda_fail(e, "device error word");
-  return v | w | x;
+  int latent = 0;
+  for (cudaError_t (*word)(int*) : {spa::read_and_clear_latent_cache_error_word,
+                                    spa::read_and_clear_latent_decode_error_word,
+                                    spa::read_and_clear_latent_prefill_error_word}) {
+    int y = 0;
+    e = word(&y);
+    if (e != cudaSuccess) return cuda_fail(e, "device error word");
+    latent |= y;
+  }
+  return v | w | x | latent;
 }
 
 const char* sparse_attn_paged_strerror(int status) {

@@ -100,4 +100,9 @@ int decode_with_partials(const void* q, const spa_pool_t* win, const spa_pool_t*
                          const spa_problem_t* prob, void* out, void* ws, size_t ws_bytes,
                          void* stream);
 
+// What the other files of the C ABI share: the current device and its SM count (prepared on its
+// first use), and the record of a failed CUDA call (returns SPA_ERR_CUDA).
+int api_current_device(int* dev, int* sms);
+int api_cuda_fail(cudaError_t e, const char* what);
+
 }  // namespace spa

@@ -409,6 +409,45 @@ def kv_write_inputs(seq_positions: Sequence[np.ndarray], head_dim: int, page_siz
                          torch.from_numpy(sid.astype(np.int32)), table, num_blocks, page_size)
 
 
+@dataclass
+class LatentInputs:
+    """Inputs of the latent-attention operators over one paged pool of rows [c | r]."""
+
+    latent: torch.Tensor          # bf16 [T, L]: the rows of all tokens, sequence after sequence
+    rope: torch.Tensor            # bf16 [T, R]
+    positions: torch.Tensor       # int32 [T]
+    seq_of_token: torch.Tensor    # int32 [T]
+    block_table: torch.Tensor     # int32 [B, stride]
+    num_blocks: int
+    page_size: int
+
+    def pool(self, fp8: bool):
+        """Empty pool rows (bf16 NaN, or e4m3 NaN codes and NaN scales)."""
+        L, R = self.latent.shape[1], self.rope.shape[1]
+        if fp8:
+            return (torch.full((self.num_blocks, self.page_size, L + 2 * R), E4M3_NAN_CODE,
+                               dtype=torch.uint8),
+                    torch.full((self.num_blocks * self.page_size,), math.nan))
+        return torch.full((self.num_blocks, self.page_size, L + R), math.nan,
+                          dtype=torch.bfloat16), None
+
+
+def latent_inputs(lens: Sequence[int], latent_dim: int, rope_dim: int, page_size: int,
+                  seed: int = 0, oversize: int = 2) -> LatentInputs:
+    """Seeded rows of whole sequences: N(0, 1) latents (as after their norm), rotary parts three
+    times larger, random pages from a pool `oversize` times larger than needed."""
+    g = torch.Generator().manual_seed(seed)
+    pages = [max(1, -(-int(n) // page_size)) for n in lens]
+    num_blocks, table = _assign_pages(g, pages, oversize)
+    T = int(sum(lens))
+    pos = np.concatenate([np.arange(n) for n in lens]) if T else np.zeros(0)
+    sid = np.concatenate([np.full(n, b) for b, n in enumerate(lens)]) if T else np.zeros(0)
+    return LatentInputs(torch.randn(T, latent_dim, generator=g).to(torch.bfloat16),
+                        (3.0 * torch.randn(T, rope_dim, generator=g)).to(torch.bfloat16),
+                        torch.from_numpy(pos.astype(np.int32)),
+                        torch.from_numpy(sid.astype(np.int32)), table, num_blocks, page_size)
+
+
 # gated-pool shapes timed on the pages (FreeToken PR 633, "Kernel time": B, R, D)
 GATED_POOL_SHAPES = [(b, r, d) for b in (1, 8) for r in (8, 128) for d in (128, 512)]
 
