@@ -379,7 +379,8 @@ int sparse_attn_latent_read_fp8(const spa_latent_pool_t* pool, int32_t num_rows,
  * q_latent = q_nope W_uk is the caller's product, as is the up-projection of out by W_uv.
  *   q_latent: bf16 [num_tokens][num_heads] rows of latent_dim, strides in elements (token, head);
  *   q_rope:   the same with rope_dim (NULL when rope_dim == 0);
- *   both 16-byte aligned, strides multiples of 8 elements (>= 0).
+ *   both 16-byte aligned, strides multiples of 8 elements and, where the dimension is over 1, at
+ *   least the row's width.
  *   out:      bf16 [num_tokens][num_heads][latent_dim], 16-byte aligned, not overlapping an input.
  * A negative position attends to nothing: its output rows are zero (padding of a batch).  Entries
  * on unmapped pages, past the block table or outside the pool are left out and set SPA_ERR_INDEX,

@@ -329,6 +329,33 @@ namespace spa {
 int api_current_device(int* dev, int* sms) { return current_device(dev, sms); }
 int api_cuda_fail(cudaError_t e, const char* what) { return cuda_fail(e, what); }
 
+bool encode_rows(CUtensorMap* m, const void* base, long long rows, int row_bytes, int box_rows) {
+  const EncodeTiledFn enc = encode_tiled();
+  if (!enc) return false;
+  const cuuint64_t dims[2] = {(cuuint64_t)row_bytes, (cuuint64_t)rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)row_bytes};
+  const cuuint32_t box[2] = {128, (cuuint32_t)box_rows};
+  const cuuint32_t elem[2] = {1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, elem,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool encode_bf16_3d(CUtensorMap* m, const void* base, int width, int n1, long long stride1, int n2,
+                    long long stride2, int box1, int box2) {
+  const EncodeTiledFn enc = encode_tiled();
+  if (!enc) return false;
+  const cuuint64_t dims[3] = {(cuuint64_t)width, (cuuint64_t)n1, (cuuint64_t)n2};
+  // a dimension of one has no stride of its own: any legal one will do
+  const cuuint64_t s1 = n1 > 1 ? (cuuint64_t)stride1 : (cuuint64_t)2 * width;
+  const cuuint64_t strides[2] = {s1, n2 > 1 ? (cuuint64_t)stride2 : s1 * (cuuint64_t)n1};
+  const cuuint32_t box[3] = {64, (cuuint32_t)box1, (cuuint32_t)box2};
+  const cuuint32_t elem[3] = {1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box,
+             elem, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 size_t decode_partials_bytes(const spa_problem_t* prob, size_t cap_bytes) {
   if (!prob || prob->num_tokens < 0 || prob->num_heads < 1 || prob->head_dim < 1) return 0;
   int dev = 0, sms = 0;

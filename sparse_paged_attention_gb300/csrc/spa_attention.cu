@@ -156,28 +156,10 @@ __device__ __forceinline__ float warp_max(float v) {
   return v;
 }
 
-// A wait whose outcome is the same on every lane of the warp (the softmax warps shuffle right
-// after their waits, so a lane must never leave the loop alone).
-__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
-  const bool ok = mbar_wait(bar, parity, abort_flag);
-  return __all_sync(0xffffffffu, ok);
-}
-
 // The same for phases completed by arrivals from the CTAs of the cluster (parity 0: one use).
 __device__ __forceinline__ bool warp_wait_cl(uint32_t bar, volatile int* abort_flag) {
   const bool ok = mbar_wait_cluster(bar, 0, abort_flag);
   return __all_sync(0xffffffffu, ok);
-}
-
-// A wait that must end even when the CTA is aborting (drain before releasing TMEM).
-__device__ __forceinline__ void mbar_wait_drain(uint32_t bar, uint32_t parity) {
-  const uint64_t t0 = globaltimer();
-  for (uint32_t it = 1; !mbar_try_wait(bar, parity); ++it) {
-    if (it >= kWaitLimitPolls && globaltimer() - t0 > kWaitLimitNs) {
-      flag_error(SPA_ERR_TIMEOUT);
-      return;
-    }
-  }
 }
 
 // Storage position of compacted column i in a column list.  Tensor-map gathers take four
@@ -188,16 +170,6 @@ __device__ __forceinline__ int list_pos(int i, bool natural) {
   return natural ? i : ((i & ~127) | ((i & 15) << 3) | ((i >> 4) & 7));
 }
 
-// 2^floor(log2 x) for finite x > 0 (clears the mantissa; x is kept within the normal range).
-__device__ __forceinline__ float pow2_floor(float x) {
-  x = fminf(fmaxf(x, 1.17549435e-38f), 1.0e38f);
-  return __int_as_float(__float_as_int(x) & 0x7F800000);
-}
-
-// Two fp32 values -> two e4m3 codes (round to nearest even, saturating), first value low byte.
-__device__ __forceinline__ uint32_t e4m3x2(float a, float b) {
-  return (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
-}
 // (a, b) -> hi = e4m3(a, b), lo = e4m3(a - hi_a, b - hi_b): hi + lo carries about 8 bits.  The
 // pair is rounded to f16 first (11 bits, far finer than the split's 8; the values are at most 448
 // here) so that the codes, their values and the residual are all packed half arithmetic.
@@ -210,30 +182,6 @@ __device__ __forceinline__ void split_e4m3x2(float a, float b, uint32_t& hi, uin
   lo = (uint32_t)__nv_cvt_halfraw2_to_fp8x2(*reinterpret_cast<const __half2_raw*>(&res),
                                             __NV_SATFINITE, __NV_E4M3);
 }
-
-// Two fp32 values -> packed bf16x2 (round to nearest even), first value in the low half.
-__device__ __forceinline__ uint32_t pack_bf16x2(float a, float b) {
-  __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
-  return *reinterpret_cast<uint32_t*>(&v);
-}
-__device__ __forceinline__ float bf16_lo(uint32_t u) { return __uint_as_float(u << 16); }
-__device__ __forceinline__ float bf16_hi(uint32_t u) { return __uint_as_float(u & 0xFFFF0000u); }
-
-// tcgen05 shared-memory descriptor, 64-byte swizzle (used for the e4m3 P^T operand).
-__device__ __forceinline__ uint64_t sdesc64(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
-  uint64_t d = 0;
-  d |= (uint64_t)((saddr >> 4) & 0x3FFFu);
-  d |= (uint64_t)((lbo >> 4) & 0x3FFFu) << 16;
-  d |= (uint64_t)((sbo >> 4) & 0x3FFFu) << 32;
-  d |= (uint64_t)1 << 46;
-  d |= (uint64_t)4 << 61;  // 64-byte swizzle
-  return d;
-}
-
-// A descriptor moved by `bytes` within shared memory: the start address is bits [0, 14) in 16-byte
-// units, and every address of the CTA's shared memory fits them, so the sum never carries into the
-// next field.
-__device__ __forceinline__ uint64_t desc_add(uint64_t d, uint32_t bytes) { return d + (bytes >> 4); }
 
 // kRes: a resolver warp (the last) walks the page tables of a CTA's next item while the gather
 // warps copy the current one; launched only when CTAs have more than one item.

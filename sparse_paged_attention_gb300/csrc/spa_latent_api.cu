@@ -10,7 +10,8 @@
 namespace {
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-bool stride_ok(int64_t s) { return s >= 0 && s <= (1ll << 40); }   // (byte offsets stay in 63 bits)
+// element strides up to 2^38: byte offsets stay in 63 bits, and a tensor map holds 2^40 bytes
+bool stride_ok(int64_t s) { return s >= 0 && s <= (1ll << 38); }
 
 // Geometry that needs no pointer: checked even when there is nothing to do.
 int check_dims(const spa_latent_pool_t* pl) {
@@ -141,6 +142,13 @@ int latent_decode(const spa_latent_pool_t* pool, const spa_latent_problem_t* pr,
   int st = check_decode(pool, pr, &work);
   if (st || !work) return st;
   const bool has_rope = pool->rope_dim > 0;
+  // rows that overlap or repeat are refused: a tensor map walks distinct rows
+  const auto rows_ok = [&](int64_t st, int64_t sh, int width) {
+    return (pr->num_tokens <= 1 || st >= width) && (pr->num_heads <= 1 || sh >= width);
+  };
+  if (!rows_ok(pr->q_latent_stride_t, pr->q_latent_stride_h, pool->latent_dim) ||
+      (has_rope && !rows_ok(pr->q_rope_stride_t, pr->q_rope_stride_h, pool->rope_dim)))
+    return SPA_ERR_SHAPE;
   if (!pr->positions || !pr->q_latent || (has_rope && !pr->q_rope) || !out) return SPA_ERR_NULL;
   st = check_pool(pool, fp8);
   if (st) return st;
@@ -251,8 +259,6 @@ int sparse_attn_latent_prefill(const spa_latent_prefill_t* pr, void* out, void* 
     if (!stride_ok(x.st) || !stride_ok(x.sh)) return SPA_ERR_SHAPE;
     if ((x.rows > 1 && x.st < x.width) || (x.heads && H > 1 && x.sh < x.width))
       return SPA_ERR_SHAPE;
-    // strides up to 2^38 elements: what a tensor map can hold (2^40 bytes)
-    if (x.st > (1ll << 38) || x.sh > (1ll << 38)) return SPA_ERR_UNSUPPORTED;
     if (!aligned16(x.p) || x.st % 8 != 0 || x.sh % 8 != 0) return SPA_ERR_ALIGN;
   }
   if (!aligned16(out)) return SPA_ERR_ALIGN;

@@ -101,7 +101,8 @@ def test_decode_refusals(lib):
     p = pool()
     assert decode(lib, None, problem()) == decode(lib, p, None) == S["SPA_ERR_NULL"]
     for bad in (dict(num_tokens=-1), dict(num_seqs=0), dict(num_heads=0), dict(scale=float("nan")),
-                dict(scale=float("inf")), dict(q_latent_stride_t=-8), dict(q_rope_stride_h=-8)):
+                dict(scale=float("inf")), dict(q_latent_stride_t=-8), dict(q_rope_stride_h=-8),
+                dict(q_latent_stride_h=504), dict(q_latent_stride_t=0), dict(q_rope_stride_t=56)):
         assert decode(lib, p, problem(**bad)) == S["SPA_ERR_SHAPE"]
     assert decode(lib, p, problem(num_tokens=1 << 20, num_heads=1 << 12)) == S["SPA_ERR_UNSUPPORTED"]
     assert decode(lib, p, problem(num_tokens=0)) == S["SPA_OK"]
@@ -109,7 +110,7 @@ def test_decode_refusals(lib):
         assert decode(lib, p, problem(**bad)) == S["SPA_ERR_NULL"]
     assert decode(lib, p, problem(), out=None) == S["SPA_ERR_NULL"]
     for bad in (dict(q_latent=0x80008), dict(q_rope=0x90002), dict(q_latent_stride_t=64 * 512 + 4),
-                dict(q_latent_stride_h=508), dict(q_rope_stride_t=4), dict(q_rope_stride_h=68)):
+                dict(q_latent_stride_h=516), dict(q_rope_stride_t=68), dict(q_rope_stride_h=68)):
         assert decode(lib, p, problem(**bad)) == S["SPA_ERR_ALIGN"]
     assert decode(lib, p, problem(), out=0xA0008) == S["SPA_ERR_ALIGN"]
     assert decode(lib, p, problem()) == S["SPA_ERR_CUDA"]
@@ -133,11 +134,11 @@ def test_prefill_refusals(lib):
                 dict(nope_dim=0), dict(v_dim=0), dict(rope_dim=-8), dict(scale=float("nan")),
                 dict(q_stride_t=-8), dict(q_stride_t=184), dict(q_stride_h=184),
                 dict(k_nope_stride_h=120), dict(k_nope_stride_t=0), dict(k_rope_stride_t=56),
-                dict(v_stride_h=120), dict(v_stride_t=120)):
+                dict(v_stride_h=120), dict(v_stride_t=120),
+                dict(v_stride_t=1 << 39)):
         assert prefill(lib, **bad) == S["SPA_ERR_SHAPE"], bad
     for bad in (dict(nope_dim=132), dict(nope_dim=136), dict(v_dim=4), dict(v_dim=136),
-                dict(rope_dim=4), dict(rope_dim=72), dict(num_q=1 << 20, num_heads=1 << 12),
-                dict(v_stride_t=1 << 39)):
+                dict(rope_dim=4), dict(rope_dim=72), dict(num_q=1 << 20, num_heads=1 << 12)):
         assert prefill(lib, **bad) == S["SPA_ERR_UNSUPPORTED"], bad
     for bad in (dict(q=None), dict(k_nope=None), dict(k_rope=None), dict(v=None), dict(cu_q=None),
                 dict(cu_k=None), dict(out=None)):
