@@ -6,22 +6,29 @@
 // Each row is read once from HBM and used by every head: 2 (2L + R) flops a head and row, so 64 heads
 // do about 121 flops a byte of a bf16 row (L = 512, R = 64) and 128 heads 242, where the machine
 // turns from HBM-bound to tensor-bound.  Both limits matter, so the products run on the tcgen05 tensor
-// cores from one copy of the row in shared memory:
+// cores from one copy of the row in shared memory, in tiles of 64 entries and 64 heads:
 //
-//   S^T[j][h] = x_j . q_h          M = 64 entries, N = heads: A = rows (K-major)
-//   O^T[d][h] += c_j[d] P^T[j][h]  M = 128 latent channels, N = 64 heads: A = the same rows read
-//                                  MN-major, B = P^T
+//   S[h][j]   = q_h . x_j           bf16: M = 128 stacks the two halves of the latent dimension,
+//                                   [q_h first half; q_h second half] against [rows' first half;
+//                                   rows' second half] with N = 128, and the two diagonal blocks
+//                                   add up to S (an MMA of M = 64 runs at half the rate of M = 128:
+//                                   measured 46 cycles for N = 64, and 64 for M = N = 128).
+//                                   e4m3: M = 128 stacks q_hi over q_lo, the blocks add up likewise.
+//   O^T[d][h] += c_j[d] P[h][j]     M = 128 latent channels, N = 64 heads, K = 64 entries: A = the
+//                                   same rows read MN-major, B = P.
 //
-// A CTA holds q of one token's 64 heads and streams tiles of 64 entries through two (bf16) or three
-// (e4m3) buffers by tensor-map copies, so that a tile is loaded while another is multiplied.  O^T
-// takes 256 TMEM columns, which leaves room for two S^T buffers: S of the next tile is computed
-// before the softmax of the current one is done.
+// bf16 queries sit in TMEM (the A operand of S), which leaves shared memory for three tiles of rows:
+// one is loaded, one multiplied, one waits for its softmax.  P takes the place of its own tile's
+// rotary chunk, which nobody reads any more.  TMEM: O^T 256 columns, S 128, q 128.
 //
-//   warps 0-3   softmax: S^T from TMEM as fragments (16 entries x 64 heads a warp, two rows and 16
-//               heads a thread), online maximum and sums, P^T to shared memory, epilogue
-//   warp 4      issues the MMAs
-//   warp 5      schedule, page tables, tensor-map copies
-//   warps 6-9   (e4m3 only) q as two e4m3 terms
+//   warps 0-3   softmax: a thread has one head and half a tile's entries; it adds the other half's
+//               part of S (through shared memory), then maximum and sum are in registers; epilogue
+//   warps 4-7   the next token's q: into TMEM (bf16), or as two e4m3 terms into shared memory; and
+//               the rows by cp.async where a tile is not one box of a page
+//   warp 8      issues the MMAs of S, warp 10 those of O: two warps, so that neither one's waits keep
+//               the tensor core idle while the other has work
+//   warp 9      schedule, page tables, tensor-map copies (pages of a multiple of 64 entries: a tile
+//               is then one box of rows by 128-byte chunks, a single copy)
 //
 // Schedule: the tiles of all tokens are one long line; each slice of CTAs (one CTA for every 64
 // heads) takes an equal stretch of it.  So the work is balanced whatever the sequence lengths,
@@ -29,10 +36,10 @@
 // the parts of a token that was cut go to the workspace, normalised, with their log-sum-exp, and
 // latent_merge_kernel joins them in the order of the slices.
 //
-// e4m3 rows enter the MMAs as codes.  q becomes q_hi + q_lo (e4m3, times a power of two per token
-// and 64 heads), read as N = 128; the row's scale multiplies the score.  The weights p_j scale_j
-// enter as an e5m2 and an e4m3 term: the first has the exponents to keep small weights of long
-// sequences (24 bits below the largest), the second the mantissa of the large ones.
+// e4m3 rows enter the MMAs as codes.  q becomes q_hi + q_lo (e4m3, times a power of two per head);
+// the row's scale multiplies the score.  The weights p_j scale_j enter as an e5m2 and an e4m3 term:
+// the first has the exponents to keep small weights of long sequences (24 bits below the largest),
+// the second the mantissa of the large ones.
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
@@ -46,55 +53,57 @@ namespace {
 constexpr int kHeads = 64;        // heads of a CTA
 constexpr int kKeys = 64;         // entries of a tile
 constexpr int kChunkBytes = kKeys * 128;
+constexpr int kBufs = 3;          // tiles of rows in shared memory
 constexpr int kRing = 4;          // tile infos in flight
 constexpr int kTmemCols = 512;
-constexpr int kOCol = 256;        // first TMEM column of O^T
+constexpr int kSCol = 256, kQCol = 384;   // TMEM columns: O^T from 0, S, q
+constexpr int kThreads = 352;
 constexpr int kMinTiles = 2;      // tiles of a slice at least: fewer would cost more in merging
 
-enum { kFirst = 1, kLast = 2, kEnd = 4 };
+// first and last tile of this CTA's part of a token, its last tile of all, no tile at all
+enum { kFirst = 1, kLast = 2, kFinal = 4, kEnd = 8 };
 
 template <bool kFp8>
 struct Cfg {
-  static constexpr int kBufs = kFp8 ? 3 : 2;
-  static constexpr int kChunks = kFp8 ? 5 : 9;       // 128-byte chunks of a row
-  static constexpr int kGroupChunks = kFp8 ? 1 : 2;  // chunks of 128 channels
-  static constexpr int kGroups = 5;                  // barriers a buffer
-  static constexpr int kBufBytes = kChunks * kChunkBytes;
-  static constexpr int kQRows = kFp8 ? 2 * kHeads : kHeads;
-  static constexpr int kQChunk = kQRows * 128;
-  static constexpr int kSCols = kFp8 ? 128 : 64;
-  static constexpr int kThreads = kFp8 ? 320 : 192;
-  static constexpr float kTau = kFp8 ? 1.f : 8.f;    // lazy rescale threshold (log2 units)
+  static constexpr int kSlots = kFp8 ? 5 : 9;        // 128-byte chunks of a row
+  static constexpr int kPerTile = kFp8 ? 1 : 2;      // slots of 128 channels
+  static constexpr int kBufBytes = kSlots * kChunkBytes;
+  static constexpr int kSBufs = kFp8 ? 2 : 1;        // S buffers in TMEM (64 or 128 columns)
+  static constexpr float kTau = kFp8 ? 4.f : 8.f;    // lazy rescale threshold (log2 units)
   struct Info {
     int t, flags, slot, pad;
-    uint32_t even, odd;                              // bit k: entry 2k (2k + 1) takes part
+    uint32_t valid[2];                               // bit j: entry j (32 + j) takes part
     uint32_t pad2[2];
-    float scale[kFp8 ? kKeys : 4];
+    int row[kKeys];                                  // pool rows (-1: none), for cp.async
+    float scale[kFp8 ? kKeys : 4];                   // the rows' scales, and log2 of them
+    float lscale[kFp8 ? kKeys : 4];
   };
-  static constexpr int kKOff = 0;
-  static constexpr int kQOff = kBufs * kBufBytes;
-  static constexpr int kPOff = kQOff + kChunks * kQChunk;
-  static constexpr int kRedOff = kPOff + 8192;                       // float2 [2][4][32]
-  static constexpr int kInfoOff = kRedOff + 2 * 4 * 32 * 8;
+  // q first: bf16 has its rotary chunk there (64 rows; the MMA reads 128, the rest is ignored)
+  static constexpr int kQBytes = kFp8 ? 5 * 16384 : 8192;
+  static constexpr int kQOff = 0;
+  static constexpr int kKOff = kQBytes;
+  static constexpr int kPOff = kKOff + kBufs * kBufBytes;            // e4m3: two P buffers
+  static constexpr int kRedOff = kPOff + (kFp8 ? 2 * 8192 : 0);      // float [2][2][64]
+  static constexpr int kQScaleOff = kRedOff + 2 * 2 * kHeads * 4;    // e4m3: float [4][64]
+  static constexpr int kInfoOff = kQScaleOff + (kFp8 ? 4 * kHeads * 4 : 0);
   static constexpr int kBarOff = kInfoOff + kRing * (int)sizeof(Info);
   // barriers
-  static constexpr int kFullB = 0, kEmptyB = kBufs * kGroups, kQFullB = 2 * kBufs * kGroups,
-                       kQEmptyB = kQFullB + 1, kSFullB = kQFullB + 2, kSEmptyB = kSFullB + 2,
-                       kPFullB = kSEmptyB + 2, kPvDoneB = kPFullB + 1, kOFreeB = kPFullB + 2,
-                       kInfoFullB = kPFullB + 3, kInfoEmptyB = kInfoFullB + kRing,
-                       kDrainB = kInfoEmptyB + kRing, kRedB = kDrainB + 1, kQRedB = kRedB + 2,
-                       kNumB = kQRedB + 1;
-  // TMEM base, abort flag, q scales [4], q maxima of the q warps [2][4]
-  static constexpr int kMiscOff = kBarOff + kNumB * 8;
-  static constexpr int kSmem = kMiscOff + 8 + 16 + 32;
+  static constexpr int kFullB = 0, kEmptyB = kFullB + kBufs, kQFullB = kEmptyB + kBufs,
+                       kQEmptyB = kQFullB + 1, kSFullB = kQEmptyB + 1, kSEmptyB = kSFullB + 2,
+                       kPFullB = kSEmptyB + 2, kPvDoneB = kPFullB + 2, kOFreeB = kPvDoneB + 2,
+                       kInfoFullB = kOFreeB + 1, kInfoEmptyB = kInfoFullB + kRing,
+                       kDrainB = kInfoEmptyB + kRing, kTokenB = kDrainB + 2, kNumB = kTokenB + 1;
+  static constexpr int kMiscOff = kBarOff + kNumB * 8;   // TMEM base, abort flag, first token
+  static constexpr int kSmem = kMiscOff + 12;
   static_assert(kSmem <= 232448, "shared memory budget");
 };
 
 struct DecodeParams {
-  CUtensorMap rows;            // the pool's rows, boxes of box_rows rows (one row for gathers)
-  CUtensorMap ql, qr;          // bf16 pools: q as [T][H][width], boxes of 64 heads
+  // With `boxed`: the pool's 128-byte chunks of 64 rows, one chunk a box; and all whole chunks of 64
+  // rows in one box, in slot order (`whole` of them, 0: none).
+  CUtensorMap chunk, block;
   LatentDecodeArgs a;
-  int box_rows;                // 0: gathers of four single rows
+  int boxed, whole;
   int groups;                  // of 64 heads
   int slices;
   float scale_log2;
@@ -117,59 +126,61 @@ __device__ __forceinline__ int token_len(const LatentDecodeArgs& a, int t, int& 
 }
 
 template <bool kFp8>
-__global__ void __launch_bounds__(Cfg<kFp8>::kThreads, 1)
+__global__ void __launch_bounds__(kThreads, 1)
     latent_decode_kernel(const __grid_constant__ DecodeParams p) {
   using C = Cfg<kFp8>;
   extern __shared__ __align__(1024) uint8_t sm[];
   const uint32_t sb = smem_u32(sm);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = (int)warp_uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + C::kMiscOff + 4);
-  volatile float* q_scales = reinterpret_cast<volatile float*>(sm + C::kMiscOff + 8);
   typename C::Info* infos = reinterpret_cast<typename C::Info*>(sm + C::kInfoOff);
 #define BAR(i) (sb + (uint32_t)C::kBarOff + 8u * (uint32_t)(i))
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < C::kBufs * C::kGroups; ++i) {
-      mbar_init(BAR(C::kFullB + i), 1);
+    for (int i = 0; i < kBufs; ++i) {
+      mbar_init(BAR(C::kFullB + i), p.boxed ? 1 : 128);   // armed by the loader, or cp.async's threads
       mbar_init(BAR(C::kEmptyB + i), 1);
     }
-    mbar_init(BAR(C::kQFullB), kFp8 ? 128 : 1);
+    mbar_init(BAR(C::kQFullB), 128);
     mbar_init(BAR(C::kQEmptyB), 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(BAR(C::kSFullB + i), 1);
       mbar_init(BAR(C::kSEmptyB + i), 128);
+      mbar_init(BAR(C::kPvDoneB + i), 1);
+      mbar_init(BAR(C::kPFullB + i), 128);
+      mbar_init(BAR(C::kDrainB + i), 1);
     }
-    mbar_init(BAR(C::kPFullB), 128);
-    mbar_init(BAR(C::kPvDoneB), 1);
     mbar_init(BAR(C::kOFreeB), 128);
     for (int i = 0; i < kRing; ++i) {
       mbar_init(BAR(C::kInfoFullB + i), 1);
-      mbar_init(BAR(C::kInfoEmptyB + i), kFp8 ? 9 : 5);
+      mbar_init(BAR(C::kInfoEmptyB + i), 10);  // two MMA, four softmax and four q warps
     }
-    mbar_init(BAR(C::kDrainB), 1);
-    mbar_init(BAR(C::kRedB), 4);
-    mbar_init(BAR(C::kRedB + 1), 4);
-    mbar_init(BAR(C::kQRedB), 4);
+    mbar_init(BAR(C::kTokenB), 1);
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == 4) tmem_alloc(sb + C::kMiscOff, kTmemCols);
+  if (warp == 8) tmem_alloc(sb + C::kMiscOff, kTmemCols);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(sm + C::kMiscOff);
+  const uint32_t tmem = warp_uniform(*reinterpret_cast<volatile uint32_t*>(sm + C::kMiscOff));
   pdl_launch_dependents();
   pdl_wait();   // nothing global before the grid before this one is done
 
   const LatentDecodeArgs& a = p.a;
   const int L = a.pool.L, R = a.pool.R, W = a.pool.row_bytes;
   const int n_chunks = (W + 127) >> 7;
-  const int n_groups = (n_chunks + C::kGroupChunks - 1) / C::kGroupChunks;
-  const int n_mt = (L + 127) >> 7;             // 128-channel tiles of O^T (groups that hold values)
-  const int g = blockIdx.x % p.groups;         // this CTA's 64 heads
+  // bf16: latent chunk c goes to slot 2c (c < nh) or 2(c - nh) + 1, so that slots 2i, 2i + 1 hold the
+  // same columns of the two halves; the rotary chunk follows in slot 2 nh.  e4m3: slot = chunk.
+  const int nl = L >> 6, nh = (nl + 1) >> 1;
+  const int n_mt = kFp8 ? (L + 127) >> 7 : nh;          // 128-channel tiles of O^T
+  const auto slot_of = [&](int c) {
+    return kFp8 ? c : (c < nh ? 2 * c : (c < nl ? 2 * (c - nh) + 1 : 2 * nh));
+  };
+  const int g = blockIdx.x % p.groups;                  // this CTA's 64 heads
   const int slice = blockIdx.x / p.groups;
 
-  if (warp == 5) {
+  if (warp == 9) {
     // ================================ schedule and loads ==================================
     long long total = 0;
     for (int t = lane; t < a.T; t += 32) {
@@ -220,13 +231,20 @@ __global__ void __launch_bounds__(Cfg<kFp8>::kThreads, 1)
         before += all;
       }
     }
+    const int ps_shift = (a.pool.ps & (a.pool.ps - 1)) == 0 ? __ffs(a.pool.ps) - 1 : -1;
+    if (lane == 0) {                           // the first token's q can be on its way
+      *reinterpret_cast<volatile int*>(sm + C::kMiscOff + 8) = begin < end ? it_t : -1;
+      mbar_arrive(BAR(C::kTokenB));
+    }
     struct Tile {
       int t, flags, slot, n;                   // n: entries of the tile that are in the sequence
-      int blk[2], off[2];                      // block of entries 2 lane, 2 lane + 1 (-1: none)
+      int blk[2], off[2];                      // block and slot in it of entries lane, 32 + lane
     };
     int started = it_j == 0;                   // the current token's first tile is this CTA's
     bool fresh = true;
     int2 cut = make_int2(-1, 0);
+    // Boxed tiles lie in one page each: lane i holds the block of tile c_tile + i of token c_t.
+    int c_t = -1, c_tile = 0, c_blk = -1;
     auto next_tile = [&](Tile& x) {            // the next tile, its block-table reads under way
       x.t = -1;
       if (it_pos >= end) return;
@@ -234,27 +252,43 @@ __global__ void __launch_bounds__(Cfg<kFp8>::kThreads, 1)
       const int k = it_t - t0;
       const int len = __shfl_sync(0xffffffffu, c_len, k);
       const int b = __shfl_sync(0xffffffffu, c_seq, k);
-      const int bad = __shfl_sync(0xffffffffu, c_bad, k);
-      if (bad && it_j == 0 && lane == 0) flag_error(SPA_ERR_INDEX);
       const int nt = tiles_of(len);
+      if (it_j == 0 && __shfl_sync(0xffffffffu, c_bad, k) && lane == 0) flag_error(SPA_ERR_INDEX);
       x.t = it_t;
       x.n = min(kKeys, len - it_j * kKeys);
-      const bool item_end = it_j == nt - 1;
-      const bool last = item_end || it_pos == end - 1;
-      x.flags = (fresh ? kFirst : 0) | (last ? kLast : 0);
+      const bool item_end = it_j == nt - 1, all_end = it_pos == end - 1;
+      const bool last = item_end || all_end;
+      x.flags = (fresh ? kFirst : 0) | (last ? kLast : 0) | (all_end ? kFinal : 0);
       x.slot = started && item_end ? -1 : started;
       if (last && !item_end && started)
         cut = make_int2(it_t, (int)((it_pos + (nt - 1 - it_j)) / per));
+      if (p.boxed) {
+        if (c_t != it_t || it_j >= c_tile + 32) {
+          c_t = it_t;
+          c_tile = it_j;
+          const int page = ((it_j + lane) * kKeys) / a.pool.ps;
+          c_blk = it_j + lane < nt && page < a.pool.bt_stride
+                      ? __ldg(a.pool.bt + (size_t)b * a.pool.bt_stride + page) : -1;
+        }
+        const int blk = __shfl_sync(0xffffffffu, c_blk, it_j - c_tile);
+        const int off = (it_j * kKeys) % a.pool.ps;
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int j = 2 * lane + e;
-        x.blk[e] = -2;                         // not of the sequence
-        x.off[e] = 0;
-        if (j < x.n) {
-          const int key = it_j * kKeys + j;
-          const int page = key / a.pool.ps;
-          x.off[e] = key - page * a.pool.ps;
-          x.blk[e] = __ldg(a.pool.bt + (size_t)b * a.pool.bt_stride + page);
+        for (int e = 0; e < 2; ++e) {
+          x.blk[e] = lane + 32 * e < x.n ? blk : -2;   // -2: not of the sequence
+          x.off[e] = off + lane + 32 * e;
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int j = lane + 32 * e;
+          x.blk[e] = -2;
+          x.off[e] = 0;
+          if (j < x.n) {
+            const int key = it_j * kKeys + j;
+            const int page = key / a.pool.ps;
+            x.off[e] = key - page * a.pool.ps;
+            x.blk[e] = __ldg(a.pool.bt + (size_t)b * a.pool.bt_stride + page);
+          }
         }
       }
       fresh = last;
@@ -266,9 +300,7 @@ __global__ void __launch_bounds__(Cfg<kFp8>::kThreads, 1)
         started = 1;
       }
     };
-    Tile cur, nxt, nxt2;
-    float sc_cur[2] = {0.f, 0.f};
-    int row_cur[2] = {-1, -1};
+    // Rows of a tile (-1: no such entry) and, e4m3, their scales.
     auto resolve = [&](const Tile& x, int (&row)[2], float (&sc)[2]) {
       row[0] = row[1] = -1;
       if (x.t < 0) return;
@@ -281,94 +313,82 @@ __global__ void __launch_bounds__(Cfg<kFp8>::kThreads, 1)
         sc[e] = kFp8 && row[e] >= 0 ? __ldg(a.pool.scale + row[e]) : 0.f;
       }
     };
+    // Three tiles under way: the one being issued, the next with its scales, and the one after with its
+    // blocks on the way.
+    Tile cur, nxt;
+    int row_cur[2], row_nxt[2];
+    float sc_cur[2] = {0.f, 0.f}, sc_nxt[2] = {0.f, 0.f};
     next_tile(cur);
     next_tile(nxt);
-    next_tile(nxt2);
     resolve(cur, row_cur, sc_cur);
     const int total_rows = (int)(a.pool.num_blocks * a.pool.ps);
-    const int nb = p.box_rows > 0 ? kKeys / p.box_rows : kKeys / 4;   // copies a chunk
-    int k = 0, items = 0;
+    int k = 0, buf = 0;
+    uint32_t buf_ph = 0;
     bool ok = true;
-    for (; cur.t >= 0 && ok; ++k) {
-      int row_nxt[2];
-      float sc_nxt[2] = {0.f, 0.f};
+    if (cur.t < 0) {                           // nothing to do: tell the others
+      if (lane == 0) {
+        infos[0].flags = kEnd;
+        __threadfence_block();
+        mbar_arrive(BAR(C::kInfoFullB));
+      }
+    }
+    for (; cur.t >= 0; ++k) {
       resolve(nxt, row_nxt, sc_nxt);
-      Tile nxt3;
-      next_tile(nxt3);
+      Tile nxt2;
+      next_tile(nxt2);
       // publish the tile
       const int ri = k % kRing;
-      if (lane == 0) ok = mbar_wait(BAR(C::kInfoEmptyB + ri), ((k / kRing) & 1) ^ 1, abort_flag);
-      ok = __shfl_sync(0xffffffffu, ok, 0);
+      ok = warp_wait(BAR(C::kInfoEmptyB + ri), ((k / kRing) & 1) ^ 1, abort_flag);
       if (!ok) break;
-      const unsigned even = __ballot_sync(0xffffffffu, row_cur[0] >= 0);
-      const unsigned odd = __ballot_sync(0xffffffffu, row_cur[1] >= 0);
+      const unsigned lo = __ballot_sync(0xffffffffu, row_cur[0] >= 0);
+      const unsigned hi = __ballot_sync(0xffffffffu, row_cur[1] >= 0);
       typename C::Info& info = infos[ri];
+      if (!p.boxed) {
+        info.row[lane] = row_cur[0];
+        info.row[lane + 32] = row_cur[1];
+      }
       if (kFp8) {
-        info.scale[2 * lane] = sc_cur[0];
-        info.scale[2 * lane + 1] = sc_cur[1];
+        // the maximum of a tile is taken over p_j |scale_j|, the weights that enter the value
+        // product (a scale below 2^-60 counts as that: the sums of p_j alone must stay finite)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          info.scale[lane + 32 * e] = 128.f * sc_cur[e];
+          info.lscale[lane + 32 * e] = row_cur[e] >= 0 ? fmaxf(__log2f(fabsf(sc_cur[e])), -60.f) : -INFINITY;
+        }
       }
       if (lane == 0) {
         info.t = cur.t;
         info.flags = cur.flags;
         info.slot = cur.slot;
-        info.even = even;
-        info.odd = odd;
+        info.valid[0] = lo;
+        info.valid[1] = hi;
       }
       __threadfence_block();
       __syncwarp();
       if (lane == 0) mbar_arrive(BAR(C::kInfoFullB + ri));
-      // q of a new token
-      if (!kFp8 && (cur.flags & kFirst)) {
-        if (lane == 0) {
-          ok = mbar_wait(BAR(C::kQEmptyB), (items & 1) ^ 1, abort_flag);
-          if (ok) {
-            mbar_arrive_expect_tx(BAR(C::kQFullB), (uint32_t)(n_chunks * C::kQChunk));
-            for (int c = 0; c < n_chunks; ++c) {
-              const uint32_t dst = sb + C::kQOff + c * C::kQChunk;
-              if (64 * c < L)
-                tma_box3(dst, &p.ql, 64 * c, g * kHeads, cur.t, BAR(C::kQFullB));
-              else
-                tma_box3(dst, &p.qr, 0, g * kHeads, cur.t, BAR(C::kQFullB));
-            }
-          }
-        }
-        ok = __shfl_sync(0xffffffffu, ok, 0);
-        ++items;
+      if (p.boxed) {
+        ok = warp_wait(BAR(C::kEmptyB + buf), buf_ph ^ 1, abort_flag);
         if (!ok) break;
-      }
-      // the rows, group by group: lane o issues copy o of the group
-      const int buf = k % C::kBufs;
-      for (int gr = 0; gr < n_groups && ok; ++gr) {
-        const int bi = buf * C::kGroups + gr;
-        const int nc = min(C::kGroupChunks, n_chunks - gr * C::kGroupChunks);
-        if (lane == 0) {
-          ok = mbar_wait(BAR(C::kEmptyB + bi), ((k / C::kBufs) & 1) ^ 1, abort_flag);
-          mbar_arrive_expect_tx(BAR(C::kFullB + bi), ok ? (uint32_t)(nc * kChunkBytes) : 0u);
+        // a tile without entries starts past the last row and is filled with zeros
+        const int row = (int)warp_uniform(row_cur[0] >= 0 ? row_cur[0] : total_rows);
+        if (elect_one()) {
+          const uint32_t dst = sb + C::kKOff + buf * C::kBufBytes, full = BAR(C::kFullB + buf);
+          mbar_arrive_expect_tx(full, (uint32_t)(n_chunks * kChunkBytes));
+          if (p.whole > 0) {
+            if (kFp8) tma_box3(dst, &p.block, 0, row, 0, full);
+            else tma_box4(dst, &p.block, 0, row, 0, 0, full);
+          }
+          for (int c = p.whole; c < n_chunks; ++c)
+            tma_row(dst + slot_of(c) * kChunkBytes, &p.chunk, c * 128, row, full);
         }
-        ok = __shfl_sync(0xffffffffu, ok, 0);
-        const int cc = lane / nb, box = lane % nb;   // (at most 16 copies a chunk, two chunks)
-        const int c = gr * C::kGroupChunks + cc;
-        const uint32_t dst0 = sb + C::kKOff + buf * C::kBufBytes + c * kChunkBytes;
-        if (p.box_rows > 0) {
-          const int row = __shfl_sync(0xffffffffu, row_cur[0], (box * p.box_rows) >> 1);
-          // a box with no entry starts past the last row and is filled with zeros
-          if (ok && cc < nc)
-            tma_row(dst0 + box * p.box_rows * 128, &p.rows, c * 128, row >= 0 ? row : total_rows,
-                    BAR(C::kFullB + bi));
-        } else {
-          const int r0 = __shfl_sync(0xffffffffu, row_cur[0], 2 * box);
-          const int r1 = __shfl_sync(0xffffffffu, row_cur[1], 2 * box);
-          const int r2 = __shfl_sync(0xffffffffu, row_cur[0], 2 * box + 1);
-          const int r3 = __shfl_sync(0xffffffffu, row_cur[1], 2 * box + 1);
-          // (a missing row is read as row 0; the softmax warps blank it)
-          if (ok && cc < nc)
-            tma_gather4(dst0 + box * 4 * 128, &p.rows, c * 128, max(r0, 0), max(r1, 0), max(r2, 0),
-                        max(r3, 0), BAR(C::kFullB + bi));
+        __syncwarp();
+        if (++buf == kBufs) {
+          buf = 0;
+          buf_ph ^= 1;
         }
       }
       cur = nxt;
       nxt = nxt2;
-      nxt2 = nxt3;
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         row_cur[e] = row_nxt[e];
@@ -376,440 +396,563 @@ __global__ void __launch_bounds__(Cfg<kFp8>::kThreads, 1)
       }
     }
     if (lane == 0) {
-      if (ok && !*abort_flag) {
-        const int ri = k % kRing;
-        if (mbar_wait(BAR(C::kInfoEmptyB + ri), ((k / kRing) & 1) ^ 1, abort_flag)) {
-          infos[ri].flags = kEnd;
-          __threadfence_block();
-          mbar_arrive(BAR(C::kInfoFullB + ri));
-        }
-      }
       p.cut[blockIdx.x] = cut;
       // copies in flight must land before the CTA ends (at once after a normal run)
-      for (int q = max(0, k - C::kBufs); q < k; ++q)
-        for (int gr = 0; gr < n_groups; ++gr)
-          mbar_wait_drain(BAR(C::kFullB + (q % C::kBufs) * C::kGroups + gr),
-                          (uint32_t)((q / C::kBufs) & 1));
-      if (!kFp8 && items > 0) mbar_wait_drain(BAR(C::kQFullB), (uint32_t)((items - 1) & 1));
+      if (p.boxed)
+        for (int q = max(0, k - kBufs); q < k; ++q)
+          mbar_wait_drain(BAR(C::kFullB + q % kBufs), (uint32_t)((q / kBufs) & 1));
     }
-  } else if (warp == 4) {
-    // ====================================== MMA ===========================================
-    if (lane == 0) {
-      const uint32_t idS = kFp8 ? idesc_e4m3(64, 128, 0, 0) : idesc_bf16(64, 64, 0, 0);
-      const uint32_t idO = kFp8 ? idesc_e4m3(128, 64, 1, 1) : idesc_bf16(128, 64, 1, 1);
-      const uint32_t idO5 = idO | (1u << 10);            // B in e5m2: the high term of P
-      const uint64_t dq0 = sdesc(sb + C::kQOff, 16, 1024);
-      const uint64_t dp0 = kFp8 ? sdesc64(sb + C::kPOff, 4096, 512) : sdesc(sb + C::kPOff, 8192, 1024);
-      int ks = 0, kp = 0;                                 // tiles whose S, PV were issued
-      uint32_t q_ph = 0, o_ph = 0;
-      auto issue_s = [&](int flags) -> bool {
-        const int buf = ks % C::kBufs, s = ks & 1;
-        if (flags & kFirst) {
-          if (!mbar_wait(BAR(C::kQFullB), q_ph, abort_flag)) return false;
-          q_ph ^= 1;
-        }
-        if (!mbar_wait(BAR(C::kSEmptyB + s), ((ks >> 1) & 1) ^ 1, abort_flag)) return false;
-        fence_proxy_async_smem();
-        tc_fence_after();
-        const uint32_t dS = tmem + s * C::kSCols;
-        for (int gr = 0; gr < n_groups; ++gr) {
-          const int bi = buf * C::kGroups + gr;
-          if (!mbar_wait(BAR(C::kFullB + bi), (uint32_t)((ks / C::kBufs) & 1), abort_flag)) return false;
-          tc_fence_after();
-          for (int cc = 0; cc < C::kGroupChunks; ++cc) {
-            const int c = gr * C::kGroupChunks + cc;
-            if (c >= n_chunks) break;
-            const uint64_t da = sdesc(sb + C::kKOff + buf * C::kBufBytes + c * kChunkBytes, 16, 1024);
-            const uint64_t db = desc_add(dq0, c * C::kQChunk);
-            const int steps = min(4, (W - c * 128 + 31) >> 5);
-            for (int st = 0; st < steps; ++st) {
-              if (kFp8)
-                mma_f8(dS, desc_add(da, st * 32), desc_add(db, st * 32), idS, (c | st) != 0);
-              else
-                mma_bf16(dS, desc_add(da, st * 32), desc_add(db, st * 32), idS, (c | st) != 0);
-            }
-          }
-          if (gr >= n_mt) mma_commit(BAR(C::kEmptyB + bi));   // no values in this group
-        }
-        mma_commit(BAR(C::kSFullB + s));
-        if (flags & kLast) mma_commit(BAR(C::kQEmptyB));
-        ++ks;
-        return true;
-      };
-      auto issue_pv = [&](int flags) -> bool {
-        const int buf = kp % C::kBufs;
-        if (!mbar_wait(BAR(C::kPFullB), (uint32_t)(kp & 1), abort_flag)) return false;
-        const bool first = flags & kFirst;
-        if (first) {
-          if (!mbar_wait(BAR(C::kOFreeB), o_ph ^ 1, abort_flag)) return false;
-          o_ph ^= 1;
-        }
-        fence_proxy_async_smem();
-        tc_fence_after();
-        for (int mt = 0; mt < n_mt; ++mt) {
-          const uint32_t dO = tmem + kOCol + mt * 64;
-          const uint32_t kv = sb + C::kKOff + buf * C::kBufBytes + mt * C::kGroupChunks * kChunkBytes;
-          const uint64_t dv = sdesc(kv, kChunkBytes, 1024);
-          if (!kFp8) {
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk)               // 16 entries a step
-              mma_bf16(dO, desc_add(dv, kk * 2048), desc_add(dp0, kk * 2048), idO,
-                       (first && kk == 0) ? 0u : 1u);
-          } else {
-#pragma unroll
-            for (int kk = 0; kk < 2; ++kk) {             // 32 entries a step
-              mma_f8(dO, desc_add(dv, kk * 4096), desc_add(dp0, kk * 2048), idO5,
-                     (first && kk == 0) ? 0u : 1u);
-              mma_f8(dO, desc_add(dv, kk * 4096), desc_add(dp0, 4096 + kk * 2048), idO, 1u);
-            }
-          }
-          mma_commit(BAR(C::kEmptyB + buf * C::kGroups + mt));
-        }
-        mma_commit(BAR(C::kPvDoneB));
-        ++kp;
-        return true;
-      };
-      // S of tile k + 1 is issued before PV of tile k, except where a new token begins
-      int flags_s = 0, ki = 0;
-      auto read_info = [&](int& flags) -> bool {
-        const int ri = ki % kRing;
-        if (!mbar_wait(BAR(C::kInfoFullB + ri), (uint32_t)((ki / kRing) & 1), abort_flag)) return false;
-        flags = *reinterpret_cast<volatile int*>(&infos[ri].flags);
-        mbar_arrive(BAR(C::kInfoEmptyB + ri));
-        ++ki;
-        return true;
-      };
-      bool ok = read_info(flags_s);
-      while (ok && !(flags_s & kEnd)) {
-        ok = issue_s(flags_s);
-        while (ok) {
-          const int flags_p = flags_s;
-          if (!(flags_p & kLast)) {
-            ok = read_info(flags_s) && issue_s(flags_s);
-            if (!ok) break;
-          }
-          ok = issue_pv(flags_p);
-          if (flags_p & kLast) break;
-        }
-        if (ok) ok = read_info(flags_s);
+  } else if (warp == 8) {
+    // ================================= MMAs of S ==========================================
+    // The warp runs as one (its waits too); one elected lane issues.  The MMAs of one tile execute in
+    // the order of issue.
+    const uint32_t idS2 = idesc_bf16(128, 128, 0, 0), idS1 = idesc_bf16(128, 64, 0, 0);
+    const uint32_t idS8 = idesc_e4m3(128, 64, 0, 0);
+    const uint64_t dq0 = sdesc(sb + C::kQOff, 16, 1024);
+    const uint64_t dk0 = sdesc(sb + C::kKOff, 16, 1024);            // rows, K-major
+    const bool lead = elect_one();
+    int buf = 0;
+    uint32_t full_ph = 0, q_ph = 0;
+    for (int k = 0;; ++k) {
+      const int ri = k % kRing, sn = k % C::kSBufs;
+      if (!warp_wait(BAR(C::kInfoFullB + ri), (uint32_t)((k / kRing) & 1), abort_flag)) break;
+      const int flags = (int)warp_uniform(*reinterpret_cast<volatile int*>(&infos[ri].flags));
+      if (lead) mbar_arrive(BAR(C::kInfoEmptyB + ri));
+      if (flags & kEnd) break;
+      if (flags & kFirst) {
+        if (!warp_wait(BAR(C::kQFullB), q_ph, abort_flag)) break;
+        q_ph ^= 1;
       }
-      // nothing may still write TMEM when it is released
+      if (!warp_wait(BAR(C::kFullB + buf), full_ph, abort_flag)) break;
+      if (!warp_wait(BAR(C::kSEmptyB + sn), ((k / C::kSBufs) & 1) ^ 1, abort_flag)) break;
+      fence_proxy_async_smem();                 // (rows copied by cp.async)
+      tc_fence_after();
+      if (lead) {
+        const uint32_t dS = tmem + kSCol + sn * 64;
+        const uint64_t dk = desc_add(dk0, buf * C::kBufBytes);
+        if (kFp8) {
+          for (int c = 0; c < n_chunks; ++c) {
+            const int steps = (W - c * 128 + 31) >> 5;             // 32-byte steps left in the row
+#pragma unroll
+            for (int st = 0; st < 4; ++st)
+              if (st < steps)
+                mma_f8(dS, desc_add(dq0, c * 16384 + st * 32), desc_add(dk, c * kChunkBytes + st * 32),
+                       idS8, (c | st) != 0);
+          }
+        } else {
+          for (int i = 0; i < nh; ++i) {
+            const uint32_t id = nh + i < nl ? idS2 : idS1;         // (an odd last chunk stands alone)
+#pragma unroll
+            for (int st = 0; st < 4; ++st)
+              mma_bf16_ts(dS, tmem + kQCol + i * 32 + st * 8,
+                          desc_add(dk, 2 * i * kChunkBytes + st * 32), id, (i | st) != 0);
+          }
+          const int steps = (2 * R + 31) >> 5;
+#pragma unroll
+          for (int st = 0; st < 4; ++st)
+            if (st < steps)
+              mma_bf16(dS, desc_add(dq0, st * 32), desc_add(dk, 2 * nh * kChunkBytes + st * 32), idS1, 1u);
+        }
+        mma_commit(BAR(C::kSFullB + sn));
+        if (flags & kLast) mma_commit(BAR(C::kQEmptyB));
+      }
+      __syncwarp();
+      if (++buf == kBufs) {
+        buf = 0;
+        full_ph ^= 1;
+      }
+      if (flags & kFinal) break;
+    }
+    // nothing may still write TMEM when it is released
+    if (lead) {
       mma_commit(BAR(C::kDrainB));
       mbar_wait_drain(BAR(C::kDrainB), 0);
     }
     __syncwarp();
-  } else if (warp >= 6) {
-    // ======================= q as two e4m3 terms (e4m3 pools only) ========================
-    if constexpr (kFp8) {
-      const int tid = threadIdx.x - 192;
-      volatile float* qmax = reinterpret_cast<volatile float*>(sm + C::kMiscOff + 24);
-      int items = 0;
-      for (int k = 0;; ++k) {
-        const int ri = k % kRing;
-        if (!warp_wait(BAR(C::kInfoFullB + ri), (uint32_t)((k / kRing) & 1), abort_flag)) break;
-        const int flags = infos[ri].flags, t = infos[ri].t;
-        __syncwarp();
-        if (lane == 0) mbar_arrive(BAR(C::kInfoEmptyB + ri));
-        if (flags & kEnd) break;
-        if (!(flags & kFirst)) continue;
-        const int nl = L >> 3, nr = R >> 3, np = nl + 2 * nr;    // pieces of eight values of K
-        const int npad = n_chunks * 16;                          // pieces of the padded row
-        auto piece = [&](int h, int i) {                         // q's values of piece i, or zeros
-          const int hg = g * kHeads + h;
-          if (hg >= a.H || i >= np) return make_uint4(0, 0, 0, 0);
-          const uint8_t* src = i < nl ? a.q_latent + t * a.ql_st + hg * a.ql_sh + 16 * i
-                                      : a.q_rope + t * a.qr_st + hg * a.qr_sh + 16 * ((i - nl) % nr);
-          return __ldg(reinterpret_cast<const uint4*>(src));
+  } else if (warp == 10) {
+    // ================================= MMAs of O ==========================================
+    const uint32_t idO = kFp8 ? idesc_e4m3(128, 64, 1, 0) : idesc_bf16(128, 64, 1, 0);
+    const uint32_t idO5 = idO | (1u << 10);            // B in e5m2: the high term of P
+    const uint64_t dv0 = sdesc(sb + C::kKOff, kChunkBytes, 1024);   // rows, MN-major
+    const uint64_t dp0 = kFp8 ? sdesc64(sb + C::kPOff, 16, 512)
+                              : sdesc(sb + C::kKOff + 8 * kChunkBytes, 16, 1024);
+    const bool lead = elect_one();
+    int buf = 0;
+    uint32_t o_ph = 0;
+    bool any = warp_wait(BAR(C::kInfoFullB), 0, abort_flag);
+    if (any) any = !(warp_uniform(*reinterpret_cast<volatile int*>(&infos[0].flags)) & kEnd);
+    for (int k = 0; any; ++k) {
+      const int ri = k % kRing;
+      if (!warp_wait(BAR(C::kPFullB + (k & 1)), (uint32_t)((k >> 1) & 1), abort_flag)) break;
+      // (P of the tile comes after its S, and that after its info)
+      const int flags = (int)warp_uniform(*reinterpret_cast<volatile int*>(&infos[ri].flags));
+      if (lead) mbar_arrive(BAR(C::kInfoEmptyB + ri));
+      const bool first = flags & kFirst;
+      if (first) {
+        if (!warp_wait(BAR(C::kOFreeB), o_ph ^ 1, abort_flag)) break;
+        o_ph ^= 1;
+      }
+      fence_proxy_async_smem();
+      tc_fence_after();
+      if (lead) {
+        const uint32_t acc0 = first ? 0u : 1u;
+        const uint64_t dp = desc_add(dp0, kFp8 ? (k & 1) * 8192 : buf * C::kBufBytes);
+        for (int mt = 0; mt < n_mt; ++mt) {
+          const uint32_t dO = tmem + mt * 64;
+          const uint64_t dv = desc_add(dv0, buf * C::kBufBytes + mt * C::kPerTile * kChunkBytes);
+          if (!kFp8) {
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)               // 16 entries a step
+              mma_bf16(dO, desc_add(dv, kk * 2048), desc_add(dp, kk * 32), idO, kk ? 1u : acc0);
+          } else {
+#pragma unroll
+            for (int kk = 0; kk < 2; ++kk) {             // 32 entries a step
+              mma_f8(dO, desc_add(dv, kk * 4096), desc_add(dp, kk * 32), idO5, kk ? 1u : acc0);
+              mma_f8(dO, desc_add(dv, kk * 4096), desc_add(dp, 4096 + kk * 32), idO, 1u);
+            }
+          }
+        }
+        mma_commit(BAR(C::kEmptyB + buf));
+        mma_commit(BAR(C::kPvDoneB + (k & 1)));
+      }
+      __syncwarp();
+      if (++buf == kBufs) buf = 0;
+      if (flags & kFinal) break;
+    }
+    if (lead) {
+      mma_commit(BAR(C::kDrainB + 1));
+      mbar_wait_drain(BAR(C::kDrainB + 1), 0);
+    }
+    __syncwarp();
+  } else if (warp >= 4) {
+    // =================================== queries ==========================================
+    // Each token's q is read into registers as soon as its first tile is announced, and put in
+    // place once the token before has no S left to compute.
+    const int tid = threadIdx.x - 128;
+    int items = 0, buf = 0, flags = 0;
+    auto put_q = [&](int t) -> bool {
+      if constexpr (!kFp8) {
+        // TMEM lane 32w + l is head 32(w & 1) + l; its first (w < 2) or second half of the latents
+        const int qw = warp - 4, h = g * kHeads + (qw & 1) * 32 + lane;
+        const int c0 = qw < 2 ? 0 : nh, nc = qw < 2 ? nh : nl - nh;
+        const uint4* src = reinterpret_cast<const uint4*>(a.q_latent + t * a.ql_st + h * a.ql_sh) + 8 * c0;
+        uint4 u[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+          u[i] = (h < a.H && i < 8 * nc) ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
+        uint4 v[4];                     // rotary part: 64 rows of eight 16-byte units
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int hr = (tid >> 3) + 16 * i, hg = g * kHeads + hr;
+          v[i] = make_uint4(0, 0, 0, 0);
+          if (hg < a.H && (tid & 7) * 8 < R)
+            v[i] = __ldg(reinterpret_cast<const uint4*>(a.q_rope + t * a.qr_st + hg * a.qr_sh) + (tid & 7));
+        }
+        if (!warp_wait(BAR(C::kQEmptyB), (uint32_t)((items & 1) ^ 1), abort_flag)) return false;
+        tc_fence_after();
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          float w[32];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            w[4 * i] = __uint_as_float(u[8 * q + i].x);
+            w[4 * i + 1] = __uint_as_float(u[8 * q + i].y);
+            w[4 * i + 2] = __uint_as_float(u[8 * q + i].z);
+            w[4 * i + 3] = __uint_as_float(u[8 * q + i].w);
+          }
+          tmem_st32(tmem + ((uint32_t)(qw * 32) << 16) + kQCol + 32 * q, w);
+        }
+        tmem_wait_st();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int hr = (tid >> 3) + 16 * i;
+          *reinterpret_cast<uint4*>(sm + C::kQOff + hr * 128 + (((tid & 7) ^ (hr & 7)) << 4)) = v[i];
+        }
+      } else {
+        // two threads a head, its pieces of eight values in turn
+        const int h = tid >> 1, hg = g * kHeads + h;
+        const int np = (L + R) >> 3, nlp = L >> 3, nrp = R >> 3;
+        constexpr int kPieces = (kLatMaxDim + kLatMaxRope) / 16, kBatch = 12;
+        static_assert(kPieces % kBatch == 0, "batches of loads");
+        const uint4* ql = reinterpret_cast<const uint4*>(a.q_latent + t * a.ql_st + hg * a.ql_sh);
+        const uint4* qr = reinterpret_cast<const uint4*>(a.q_rope + t * a.qr_st + hg * a.qr_sh);
+        const auto load = [&](int i0, uint4 (&u)[kBatch]) {   // a batch's loads in flight together
+#pragma unroll
+          for (int i = 0; i < kBatch; ++i) {
+            const int pc = 2 * (i0 + i) + (tid & 1);
+            u[i] = make_uint4(0, 0, 0, 0);
+            if (hg < a.H && pc < np) u[i] = __ldg(pc < nlp ? ql + pc : qr + (pc - nlp));
+          }
         };
         float m = 0.f;
-        for (int i = tid; i < kHeads * (nl + nr); i += 128) {
-          const uint4 u = piece(i / (nl + nr), i % (nl + nr));
-          const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll 1
+        for (int i0 = 0; i0 < kPieces; i0 += kBatch) {
+          uint4 u[kBatch];
+          load(i0, u);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) m = fmaxf(m, fmaxf(fabsf(bf16_lo(w[e])), fabsf(bf16_hi(w[e]))));
-        }
+          for (int i = 0; i < kBatch; ++i) {
+            const uint32_t w[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        volatile float* qm = qmax + 4 * (items & 1);
-        if (lane == 0) {
-          qm[warp - 6] = m;
-          mbar_arrive(BAR(C::kQRedB));
-        }
-        if (!warp_wait(BAR(C::kQRedB), (uint32_t)(items & 1), abort_flag)) break;
-        m = fmaxf(fmaxf(qm[0], qm[1]), fmaxf(qm[2], qm[3]));
-        const float qs = m > 0.f ? pow2_floor(448.f / m) : 1.f;
-        if (!warp_wait(BAR(C::kQEmptyB), (uint32_t)((items & 1) ^ 1), abort_flag)) break;
-        if (tid == 0) q_scales[items & 3] = qs;
-        for (int i = tid; i < kHeads * npad; i += 128) {
-          const int h = i / npad, pc = i % npad;
-          const uint4 u = piece(h, pc);
-          const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-          uint32_t hi[4], lo[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float x = bf16_lo(w[e]) * qs, y = bf16_hi(w[e]) * qs;
-            hi[e] = e4m3x2(x, y);
-            const __half2_raw hr = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)hi[e], __NV_E4M3);
-            const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&hr));
-            lo[e] = e4m3x2(x - v.x, y - v.y);
+            for (int e = 0; e < 4; ++e) m = fmaxf(m, fmaxf(fabsf(bf16_lo(w[e])), fabsf(bf16_hi(w[e]))));
           }
-          // piece pc: bytes 8 pc of the row, chunk pc / 16, 16-byte unit (pc / 2) & 7 swizzled by row
-          const uint32_t off = (pc >> 4) * C::kQChunk + h * 128 + ((((pc >> 1) & 7) ^ (h & 7)) << 4) + (pc & 1) * 8;
-          *reinterpret_cast<uint2*>(sm + C::kQOff + off) = make_uint2(hi[0] | (hi[1] << 16), hi[2] | (hi[3] << 16));
-          *reinterpret_cast<uint2*>(sm + C::kQOff + off + 64 * 128) = make_uint2(lo[0] | (lo[1] << 16), lo[2] | (lo[3] << 16));
         }
-        fence_proxy_async_smem();
-        mbar_arrive(BAR(C::kQFullB));
-        ++items;
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+        const float qs = m > 0.f ? pow2_floor(448.f / m) : 1.f;
+        if (!warp_wait(BAR(C::kQEmptyB), (uint32_t)((items & 1) ^ 1), abort_flag)) return false;
+        if ((tid & 1) == 0)
+          reinterpret_cast<float*>(sm + C::kQScaleOff)[(items & 3) * kHeads + h] = qs;
+        // piece pc: bytes 8 pc of the row: chunk pc / 16, 16-byte unit (pc / 2) & 7, swizzled by row
+        const auto put = [&](int pc, uint2 hi, uint2 lo) {
+          uint8_t* d = sm + C::kQOff + (pc >> 4) * 16384 + h * 128 + ((((pc >> 1) & 7) ^ (h & 7)) << 4) +
+                       (pc & 1) * 8;
+          *reinterpret_cast<uint2*>(d) = hi;
+          *reinterpret_cast<uint2*>(d + 64 * 128) = lo;
+        };
+#pragma unroll 1
+        for (int i0 = 0; i0 < kPieces; i0 += kBatch) {
+          uint4 u[kBatch];
+          load(i0, u);
+#pragma unroll
+          for (int i = 0; i < kBatch; ++i) {
+            const int pc = 2 * (i0 + i) + (tid & 1);
+            const uint32_t w[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float x = bf16_lo(w[e]) * qs, y = bf16_hi(w[e]) * qs;
+              hi[e] = e4m3x2(x, y);
+              const __half2_raw hr = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)hi[e], __NV_E4M3);
+              const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&hr));
+              lo[e] = e4m3x2(x - v.x, y - v.y);
+            }
+            const uint2 h2 = make_uint2(hi[0] | (hi[1] << 16), hi[2] | (hi[3] << 16));
+            const uint2 l2 = make_uint2(lo[0] | (lo[1] << 16), lo[2] | (lo[3] << 16));
+            if (pc < np) put(pc, h2, l2);
+            if (pc >= nlp && pc < np) put(pc + nrp, h2, l2);   // against the low codes of the rows too
+          }
+        }
+        for (int pc = np + nrp + (tid & 1); pc < 16 * n_chunks; pc += 2)
+          put(pc, make_uint2(0, 0), make_uint2(0, 0));
       }
+      fence_proxy_async_smem();
+      tc_fence_before();
+      mbar_arrive(BAR(C::kQFullB));
+      ++items;
+      return true;
+    };
+    // (a boxed CTA's first token does not wait for the page table; cp.async copies rows first)
+    bool ok = true;
+    if (p.boxed) {
+      ok = warp_wait(BAR(C::kTokenB), 0, abort_flag);
+      const int t = *reinterpret_cast<volatile int*>(sm + C::kMiscOff + 8);
+      if (ok && t >= 0) ok = put_q(t);
     }
+    uint32_t buf_ph = 0;
+    for (int k = 0; ok && !(flags & kFinal); ++k) {
+      const int ri = k % kRing;
+      if (!warp_wait(BAR(C::kInfoFullB + ri), (uint32_t)((k / kRing) & 1), abort_flag)) break;
+      const int t = infos[ri].t;
+      flags = infos[ri].flags;
+      if (flags & kEnd) break;
+      if (!p.boxed) {
+        // the tile's rows by cp.async: unit jj (16 bytes) of every chunk of rows r0, r0 + 16, ..;
+        // what is no entry, or past the row, is filled with zeros
+        const int jj = tid & 7, r0 = tid >> 3;
+        const uint8_t* src[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int row = infos[ri].row[r0 + 16 * i];
+          src[i] = row >= 0 ? a.pool.rows + (size_t)row * W : nullptr;
+        }
+        if (!warp_wait(BAR(C::kEmptyB + buf), buf_ph ^ 1, abort_flag)) break;
+        const uint32_t dst = sb + C::kKOff + buf * C::kBufBytes + r0 * 128 + ((jj ^ (r0 & 7)) << 4);
+        for (int c = 0; c < n_chunks; ++c) {
+          const int at = c * 128 + jj * 16;
+          const uint32_t d = dst + slot_of(c) * kChunkBytes;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const bool has = src[i] != nullptr && at < W;
+            cp_async_16(d + i * 2048, has ? src[i] + at : a.pool.rows, has ? 16u : 0u);
+          }
+        }
+        cp_async_arrive_noinc(BAR(C::kFullB + buf));
+        if (++buf == kBufs) {
+          buf = 0;
+          buf_ph ^= 1;
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(BAR(C::kInfoEmptyB + ri));
+      if ((flags & kFirst) && !(p.boxed && k == 0) && !put_q(t)) break;
+    }
+    cp_async_wait_all();
   } else {
     // ================================ softmax and epilogue ================================
     const int tid = threadIdx.x;
-    const int fr = lane >> 2, fc = lane & 3;       // fragment row, column pair
-    const int r0 = 16 * warp + fr, r1 = r0 + 8;    // this thread's entries of the tile
+    const int half = warp >> 1, pair = warp & 1;   // half of the tile's entries; half of the heads
+    const int head = pair * 32 + lane;
     const uint32_t lane_base = tmem + ((uint32_t)(warp * 32) << 16);
-    float2* red = reinterpret_cast<float2*>(sm + C::kRedOff);
-    float2 m = make_float2(-INFINITY, -INFINITY);  // running maxima of heads 2 lane, 2 lane + 1
-    float l[16];                                   // this thread's sums of heads 8i + 2fc + e
-    int items = -1, reds = 0;                      // tokens begun, exchanges between the warps done
-    // The warps' values of heads 2 lane, 2 lane + 1, all four in every thread: through one of two
-    // buffers in turn, with a wait that ends (false) when the CTA gives up.
-    auto exchange = [&](float2 mine, float2 (&all)[4]) -> bool {
-      float2* rr = red + (reds & 1) * 128;
-      rr[warp * 32 + lane] = mine;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(BAR(C::kRedB + (reds & 1)));
-      if (!warp_wait(BAR(C::kRedB + (reds & 1)), (uint32_t)((reds >> 1) & 1), abort_flag)) return false;
+    float* red = reinterpret_cast<float*>(sm + C::kRedOff);
+    const bool two = kFp8 || nl > 1;               // the second stacked block holds anything
+    // own head and head ^ 32 (every warp follows all heads, whose channels it may have to rescale)
+    float m = -INFINITY, mo = -INFINITY, l = 0.f;
+    int items = -1, reds = 0;
+    // Named barriers join the four warps (1) and the two that share heads (2, 3).  A wait that gives up
+    // does not leave the loop: every warp reaches every barrier, and the four leave together, where
+    // they agree that one of them gave up.
+    bool ok = true;
+    // Both halves' values of the own head and of head ^ 32, through one of two buffers in turn.
+    auto exchange = [&](float mine, float (&own)[2], float (&other)[2]) -> bool {
+      float* r = red + (reds & 1) * 128;
+      r[half * 64 + head] = mine;
+      ok = named_bar_and(1, 128, ok);
       ++reds;
 #pragma unroll
-      for (int w = 0; w < 4; ++w) all[w] = rr[w * 32 + lane];
-      return true;
+      for (int e = 0; e < 2; ++e) {
+        own[e] = r[e * 64 + head];
+        other[e] = r[e * 64 + (head ^ 32)];
+      }
+      return ok;
     };
-    for (int k = 0;; ++k) {
-      const int ri = k % kRing, s = k & 1;
-      if (!warp_wait(BAR(C::kInfoFullB + ri), (uint32_t)((k / kRing) & 1), abort_flag)) break;
+    // Factor of head c (lane c of the warps that own it, or their own copy) for columns c of O^T
+    auto column = [&](float own, float other, int c) {
+      return __shfl_sync(0xffffffffu, (c >= 32) == (pair != 0) ? own : other, c & 31);
+    };
+    int flags = 0, buf = kBufs - 1;
+    ok = warp_wait(BAR(C::kInfoFullB), 0, abort_flag);
+    const bool any = named_bar_and(1, 128, ok && !(infos[0].flags & kEnd));
+    for (int k = 0; any && !(flags & kFinal); ++k) {
+      const int ri = k % kRing, s = k % C::kSBufs;
+      if (++buf == kBufs) buf = 0;
+      ok = warp_wait(BAR(C::kSFullB + s), (uint32_t)((k / C::kSBufs) & 1), abort_flag) && ok;
+      tc_fence_after();
+      // (S of the tile comes after its info)
       const typename C::Info& info = infos[ri];
-      const int t = info.t, flags = info.flags, slot = info.slot;
-      const uint32_t even = info.even, odd = info.odd;
-      float ks0 = 1.f, ks1 = 1.f;
-      if (kFp8) ks0 = info.scale[r0], ks1 = info.scale[r1];
-      __syncwarp();
-      if (lane == 0) mbar_arrive(BAR(C::kInfoEmptyB + ri));
-      if (flags & kEnd) break;
+      const int t = info.t, slot = info.slot;
+      flags = info.flags;
+      const uint32_t va = info.valid[0], vb = info.valid[1];
       const bool first = flags & kFirst, last = flags & kLast;
-      // (r1 = r0 + 8 has r0's parity)
-      const uint32_t word = (r0 & 1) ? odd : even;
-      const bool v0 = (word >> (r0 >> 1)) & 1u, v1 = (word >> (r1 >> 1)) & 1u;
       if (first) {
         ++items;
-        m = make_float2(-INFINITY, -INFINITY);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) l[i] = 0.f;
+        m = mo = -INFINITY;
+        l = 0.f;
       }
-      if (!warp_wait(BAR(C::kSFullB + s), (uint32_t)((k >> 1) & 1), abort_flag)) break;
-      tc_fence_after();
       float x[32];
-      tmem_ld_frag64(lane_base + s * C::kSCols, x);
-      float c0 = p.scale_log2, c1 = p.scale_log2, b0 = 0.f, b1 = 0.f;
+      uint8_t* pb = kFp8 ? sm + C::kPOff + (k & 1) * 8192
+                         : sm + C::kKOff + buf * C::kBufBytes + 8 * kChunkBytes;   // P of this tile
+      {
+        float th[32];
+        const uint32_t sa = lane_base + kSCol + (kFp8 ? s * 64 : half * 64);
+        tmem_ld32(sa + (half ^ 1) * 32, th);
+        tmem_ld32(sa + half * 32, x);
+        tmem_wait_ld();
+        tc_fence_before();
+        mbar_arrive(BAR(C::kSEmptyB + s));
+        if (!two && half == 1) {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) th[j] = x[j] = 0.f;
+        }
+        // e4m3: PV of the tile two before has read the P buffer
+        if (kFp8 && k >= 2)
+          ok = warp_wait(BAR(C::kPvDoneB + (k & 1)), (uint32_t)(((k - 2) >> 1) & 1), abort_flag) && ok;
+        // The other half of the warps has the other part of S: swap the entries that are not one's
+        // own, sixteen at a time, through the rows of P that the two warps will write.  A warp's
+        // second sixteen go where it has just read, so one barrier a round is enough.
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          float4* put = reinterpret_cast<float4*>(pb + (kFp8 ? (half ^ 1 ^ r) * 4096 + pair * 2048
+                                                             : pair * 4096 + (half ^ 1 ^ r) * 2048));
+          const float4* get = reinterpret_cast<const float4*>(
+              pb + (kFp8 ? (half ^ r) * 4096 + pair * 2048 : pair * 4096 + (half ^ r) * 2048));
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            put[j * 32 + lane] = make_float4(th[16 * r + 4 * j], th[16 * r + 4 * j + 1],
+                                             th[16 * r + 4 * j + 2], th[16 * r + 4 * j + 3]);
+          named_bar_sync(2 + pair, 64);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float4 o = get[j * 32 + lane];
+            x[16 * r + 4 * j] += o.x;
+            x[16 * r + 4 * j + 1] += o.y;
+            x[16 * r + 4 * j + 2] += o.z;
+            x[16 * r + 4 * j + 3] += o.w;
+          }
+        }
+      }
+      const uint32_t valid = half ? vb : va;       // of this thread's entries 32 half + j
+      float mt = -INFINITY, arg = 1.f;              // log2 of the weights: arg x
       if (kFp8) {
-        float y[32];
-        tmem_ld_frag64(lane_base + s * C::kSCols + 64, y);
-        tmem_wait_ld();
+        // info.scale holds 2^7 times the rows' scales
+        arg = p.scale_log2 * 0.0078125f /
+              reinterpret_cast<const float*>(sm + C::kQScaleOff)[(items & 3) * kHeads + head];
+        const float4* ks4 = reinterpret_cast<const float4*>(info.scale + 32 * half);
 #pragma unroll
-        for (int i = 0; i < 32; ++i) x[i] += y[i];
-        const float qi = p.scale_log2 / q_scales[items & 3];
-        c0 = qi * ks0;
-        c1 = qi * ks1;
-        // the maximum is taken over p_j |scale_j|, the weights that enter the value product (a scale
-        // below 2^-60 counts as that: the sums of p_j alone must stay finite)
-        b0 = fmaxf(__log2f(fabsf(ks0)), -60.f);
-        b1 = fmaxf(__log2f(fabsf(ks1)), -60.f);
+        for (int j = 0; j < 8; ++j) {
+          const float4 c = ks4[j];
+          x[4 * j] *= c.x;
+          x[4 * j + 1] *= c.y;
+          x[4 * j + 2] *= c.z;
+          x[4 * j + 3] *= c.w;
+        }
+        const float4* ls4 = reinterpret_cast<const float4*>(info.lscale + 32 * half);
+        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {                // (lscale is -inf where no entry takes part)
+          const float4 c = ls4[j];
+          mx[0] = fmaxf(mx[0], fmaf(arg, x[4 * j], c.x));
+          mx[1] = fmaxf(mx[1], fmaf(arg, x[4 * j + 1], c.y));
+          mx[2] = fmaxf(mx[2], fmaf(arg, x[4 * j + 2], c.z));
+          mx[3] = fmaxf(mx[3], fmaf(arg, x[4 * j + 3], c.w));
+        }
+        mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
       } else {
-        tmem_wait_ld();
-      }
-      tc_fence_before();
-      mbar_arrive(BAR(C::kSEmptyB + s));
 #pragma unroll
-      for (int i = 0; i < 32; ++i) x[i] = (i & 2) ? (v1 ? x[i] * c1 : -INFINITY) : (v0 ? x[i] * c0 : -INFINITY);
-      // tile maxima: over this thread's two entries, then over the eight lanes of equal fc, halving
-      // the columns each step so that lane 4i + fc ends with columns 8i + 2fc, + 1
-      float mx[16];
+        for (int j = 0; j < 32; ++j) x[j] *= p.scale_log2;
+        if (valid != 0xffffffffu) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        mx[2 * i] = fmaxf(x[4 * i] + b0, x[4 * i + 2] + b1);
-        mx[2 * i + 1] = fmaxf(x[4 * i + 1] + b0, x[4 * i + 3] + b1);
-      }
-#pragma unroll
-      for (int w = 8; w >= 2; w >>= 1) {           // 16 -> 8 -> 4 -> 2 values; lane bits 4, 3, 2
-        const bool up = lane & (2 * w);
-#pragma unroll
-        for (int i = 0; i < w; ++i) {
-          const float send = up ? mx[i] : mx[i + w], keep = up ? mx[i + w] : mx[i];
-          mx[i] = fmaxf(keep, __shfl_xor_sync(0xffffffffu, send, 2 * w));
+          for (int j = 0; j < 32; ++j) x[j] = (valid >> j) & 1u ? x[j] : -INFINITY;
         }
-      }
-      float2 ex[4];
-      if (!exchange(make_float2(mx[0], mx[1]), ex)) break;
-      const float2 mt = make_float2(fmaxf(fmaxf(ex[0].x, ex[1].x), fmaxf(ex[2].x, ex[3].x)),
-                                    fmaxf(fmaxf(ex[0].y, ex[1].y), fmaxf(ex[2].y, ex[3].y)));
-      const float2 mn = make_float2(mt.x > m.x + C::kTau ? mt.x : m.x, mt.y > m.y + C::kTau ? mt.y : m.y);
-      const bool grow = __any_sync(0xffffffffu, mn.x != m.x || mn.y != m.y);
-      // a head without any entry so far: everything is masked, the reference does not matter
-      const float2 ref = make_float2(mn.x == -INFINITY ? 0.f : mn.x, mn.y == -INFINITY ? 0.f : mn.y);
-      const float2 al = make_float2(fast_exp2(m.x - ref.x), fast_exp2(m.y - ref.y));
-      m = mn;
-      if (grow && !first) {
+        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          l[2 * i] *= __shfl_sync(0xffffffffu, al.x, 4 * i + fc);
-          l[2 * i + 1] *= __shfl_sync(0xffffffffu, al.y, 4 * i + fc);
-        }
+        for (int j = 0; j < 32; ++j) mx[j & 3] = fmaxf(mx[j & 3], x[j]);
+        mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
       }
+      float own[2], other[2];
+      if (!exchange(mt, own, other)) break;   // (all four warps, or none)
+      const float t0 = fmaxf(own[0], own[1]), t1 = fmaxf(other[0], other[1]);
+      const float n0 = t0 > m + C::kTau ? t0 : m, n1 = t1 > mo + C::kTau ? t1 : mo;
+      const uint32_t grow0 = __ballot_sync(0xffffffffu, n0 != m), grow1 = __ballot_sync(0xffffffffu, n1 != mo);
+      const bool grow = (grow0 | grow1) != 0;
+      // (a head without any entry so far: everything is masked, the reference does not matter)
+      const float ref = n0 == -INFINITY ? 0.f : n0, refo = n1 == -INFINITY ? 0.f : n1;
+      const float al = fast_exp2(m - ref), alo = fast_exp2(mo - refo);
+      if (grow) l *= al;
+      m = n0;
+      mo = n1;
+      float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float mc0 = __shfl_sync(0xffffffffu, ref.x, 4 * i + fc);
-        const float mc1 = __shfl_sync(0xffffffffu, ref.y, 4 * i + fc);
-        x[4 * i] = fast_exp2(x[4 * i] - mc0);
-        x[4 * i + 1] = fast_exp2(x[4 * i + 1] - mc1);
-        x[4 * i + 2] = fast_exp2(x[4 * i + 2] - mc0);
-        x[4 * i + 3] = fast_exp2(x[4 * i + 3] - mc1);
-        l[2 * i] += x[4 * i] + x[4 * i + 2];
-        l[2 * i + 1] += x[4 * i + 1] + x[4 * i + 3];
+      for (int j = 0; j < 32; ++j) {
+        x[j] = kFp8 ? fast_exp2(fmaf(arg, x[j], -ref)) : fast_exp2(x[j] - ref);
+        if (kFp8 && valid != 0xffffffffu) x[j] = (valid >> j) & 1u ? x[j] : 0.f;
+        sum[j & 3] += x[j];
       }
-      // P^T words: bf16 pairs, or four codes of each term gathered over a lane pair
-      uint32_t pw[16];
+      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
       if (!kFp8) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          pw[2 * i] = pack_bf16x2(x[4 * i], x[4 * i + 1]);
-          pw[2 * i + 1] = pack_bf16x2(x[4 * i + 2], x[4 * i + 3]);
+        for (int u = 0; u < 4; ++u) {              // 16-byte unit: eight entries
+          const float* e = x + 8 * u;
+          *reinterpret_cast<uint4*>(pb + head * 128 + (((4 * half + u) ^ (head & 7)) << 4)) =
+              make_uint4(pack_bf16x2(e[0], e[1]), pack_bf16x2(e[2], e[3]), pack_bf16x2(e[4], e[5]),
+                         pack_bf16x2(e[6], e[7]));
         }
       } else {
-        // u = 2^7 p scale (at most 2^8, as tau = 1): e5m2, then e4m3 of what that leaves.  Invalid
-        // rows have p = 0, but a scale that may be anything.
-        const float s0 = v0 ? ks0 * 128.f : 0.f, s1 = v1 ? ks1 * 128.f : 0.f;
+        // u = 2^7 p scale (at most 2^11, as tau = 4) in f16, whose upper byte is an e5m2 number: that
+        // byte rounded to nearest is the high term, what it leaves (an eighth at most, exact in f16)
+        // the low term in e4m3
+        const float4* ks4 = reinterpret_cast<const float4*>(info.scale + 32 * half);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          uint32_t w2[2];
+        for (int u = 0; u < 2; ++u) {              // 16-byte unit: sixteen entries
+          uint32_t hw[4], lw[4];
 #pragma unroll
-          for (int r = 0; r < 2; ++r) {
-            const float ua = x[4 * i + 2 * r] * (r ? s1 : s0), ub = x[4 * i + 2 * r + 1] * (r ? s1 : s0);
-            const uint32_t hi = (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(ua, ub), __NV_SATFINITE, __NV_E5M2);
-            const __half2_raw hr = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)hi, __NV_E5M2);
-            const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&hr));
-            w2[r] = hi | (e4m3x2(ua - v.x, ub - v.y) << 16);
-          }
-          // even lanes take row r0's four codes (heads 8i + 2fc ..+3), odd lanes row r1's
-          const uint32_t o = __shfl_xor_sync(0xffffffffu, (lane & 1) ? w2[0] : w2[1], 1);
-          const uint32_t mine = (lane & 1) ? w2[1] : w2[0];
-          const uint32_t lo_h = (lane & 1) ? o : mine, hi_h = (lane & 1) ? mine : o;
-          pw[2 * i] = __byte_perm(lo_h, hi_h, 0x5410);       // high terms
-          pw[2 * i + 1] = __byte_perm(lo_h, hi_h, 0x7632);   // low terms
-        }
-      }
-      if (!first) {
-        // PV of the tile before: then O can be rescaled and the P buffer reused
-        if (!warp_wait(BAR(C::kPvDoneB), (uint32_t)((k - 1) & 1), abort_flag)) break;
-        tc_fence_after();
-        if (grow) {
-          for (int hf = 0; hf < 2; ++hf) {
-            for (int i = 0; i < n_mt; ++i) {
-              float o[32];
-              const uint32_t ta = lane_base + kOCol + i * 64 + hf * 32;
-              tmem_ld32(ta, o);
-              tmem_wait_ld();
+          for (int q = 0; q < 4; ++q) {
+            const float4 c = ks4[4 * u + q];
+            const float* e = x + 16 * u + 4 * q;
+            uint32_t h2[2], l2[2];
 #pragma unroll
-              for (int c = 0; c < 32; ++c)
-                o[c] *= __shfl_sync(0xffffffffu, (c & 1) ? al.y : al.x, hf * 16 + (c >> 1));
-              tmem_st32(ta, o);
+            for (int z = 0; z < 2; ++z) {
+              const __half2 y = z ? __floats2half2_rn(e[2] * c.z, e[3] * c.w) : __floats2half2_rn(e[0] * c.x, e[1] * c.y);
+              h2[z] = (*reinterpret_cast<const uint32_t*>(&y) + 0x00800080u) & 0xff00ff00u;
+              const __half2 rest = __hsub2(y, *reinterpret_cast<const __half2*>(&h2[z]));
+              l2[z] = (uint32_t)__nv_cvt_halfraw2_to_fp8x2(*reinterpret_cast<const __half2_raw*>(&rest),
+                                                           __NV_SATFINITE, __NV_E4M3);
             }
+            hw[q] = __byte_perm(h2[0], h2[1], 0x7531);
+            lw[q] = __byte_perm(l2[0], l2[1], 0x5410);
           }
-          tmem_wait_st();
+          uint8_t* d = pb + head * 64 + (((2 * half + u) ^ ((head >> 1) & 3)) << 4);
+          *reinterpret_cast<uint4*>(d) = make_uint4(hw[0], hw[1], hw[2], hw[3]);
+          *reinterpret_cast<uint4*>(d + 4096) = make_uint4(lw[0], lw[1], lw[2], lw[3]);
         }
       }
-      if (!kFp8) {
-        uint8_t* p0 = sm + C::kPOff + r0 * 128 + fc * 4;     // (r1's swizzle is r0's: 8 apart)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          *reinterpret_cast<uint32_t*>(p0 + ((i ^ (r0 & 7)) << 4)) = pw[2 * i];
-          *reinterpret_cast<uint32_t*>(p0 + 1024 + ((i ^ (r0 & 7)) << 4)) = pw[2 * i + 1];
-        }
-      } else {
-        const int row = (lane & 1) ? r1 : r0;
-        uint8_t* pr = sm + C::kPOff + row * 64 + (fc >> 1) * 4;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {      // heads 8i + 4(fc / 2): 16-byte unit i / 2, half i & 1
-          const int off = (((i >> 1) ^ ((row >> 1) & 3)) << 4) + (i & 1) * 8;
-          *reinterpret_cast<uint32_t*>(pr + off) = pw[2 * i];
-          *reinterpret_cast<uint32_t*>(pr + 4096 + off) = pw[2 * i + 1];
-        }
-      }
-      if ((even & odd) != 0xffffffffu) {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(BAR(C::kInfoEmptyB + ri));
+      if ((va & vb) != 0xffffffffu) {
         // entries that take no part: their rows hold other data or none, and a probability of zero
         // times a NaN would still be one
-        const int buf = k % C::kBufs;
-        const int u16 = n_mt * C::kGroupChunks * 8;          // 16-byte units of a row's values
         for (int e = 0; e < 2; ++e) {
-          uint32_t gone = ~(e ? odd : even);
+          uint32_t gone = ~(e ? vb : va);
           while (gone) {
-            const int r = 2 * (__ffs(gone) - 1) + e;
+            const int r = 32 * e + __ffs(gone) - 1;
             gone &= gone - 1;
-            for (int u = tid; u < u16 && (u >> 3) < n_chunks; u += 128)
+            for (int u = tid; u < n_mt * C::kPerTile * 8; u += 128)   // 16-byte units of its values
               *reinterpret_cast<uint4*>(sm + C::kKOff + buf * C::kBufBytes + (u >> 3) * kChunkBytes +
                                         r * 128 + (u & 7) * 16) = make_uint4(0, 0, 0, 0);
           }
         }
       }
+      if (grow && !first) {
+        // the running maximum of some head moved: rescale its quarter of O (sixteen heads) once PV of
+        // the tile before is done
+        ok = warp_wait(BAR(C::kPvDoneB + ((k - 1) & 1)), (uint32_t)(((k - 1) >> 1) & 1), abort_flag) && ok;
+        tc_fence_after();
+        const uint32_t g0 = pair ? grow1 : grow0, g1 = pair ? grow0 : grow1;   // heads 0-31, 32-63
+#pragma unroll 1
+        for (int q = 0; q < 4; ++q) {
+          if ((((q >= 2 ? g1 : g0) >> (16 * (q & 1))) & 0xffffu) == 0) continue;
+          float f[16];
+#pragma unroll
+          for (int c = 0; c < 16; ++c) f[c] = column(al, alo, q * 16 + c);
+#pragma unroll 1
+          for (int i = 0; i < n_mt; i += 2) {
+            const uint32_t ta = lane_base + i * 64 + q * 16;
+            float o[2][16];
+            tmem_ld16(ta, o[0]);
+            if (i + 1 < n_mt) tmem_ld16(ta + 64, o[1]);
+            tmem_wait_ld();
+#pragma unroll
+            for (int z = 0; z < 2; ++z) {
+              uint32_t w[16];
+#pragma unroll
+              for (int c = 0; c < 16; ++c) w[c] = __float_as_uint(o[z][c] * f[c]);
+              if (i + z < n_mt) tmem_st16(ta + z * 64, w);
+            }
+          }
+        }
+        tmem_wait_st();
+      }
       fence_proxy_async_smem();
       tc_fence_before();
-      mbar_arrive(BAR(C::kPFullB));
+      mbar_arrive(BAR(C::kPFullB + (k & 1)));
       if (!last) continue;
 
       // ---- epilogue: denominators, then O ----
-#pragma unroll
-      for (int w = 8; w >= 2; w >>= 1) {
-        const bool up = lane & (2 * w);
-#pragma unroll
-        for (int i = 0; i < w; ++i) {
-          const float send = up ? l[i] : l[i + w], keep = up ? l[i + w] : l[i];
-          l[i] = keep + __shfl_xor_sync(0xffffffffu, send, 2 * w);
-        }
-      }
-      if (!exchange(make_float2(l[0], l[1]), ex)) break;
-      const float2 ls = make_float2((ex[0].x + ex[1].x) + (ex[2].x + ex[3].x),
-                                    (ex[0].y + ex[1].y) + (ex[2].y + ex[3].y));
+      if (!exchange(l, own, other)) break;
+      const float ls = own[0] + own[1], lso = other[0] + other[1];
       constexpr float kUnit = kFp8 ? 1.f / 128.f : 1.f;
-      const float2 inv = make_float2(m.x == -INFINITY ? 0.f : kUnit / ls.x, m.y == -INFINITY ? 0.f : kUnit / ls.y);
+      const float inv = m == -INFINITY ? 0.f : kUnit / ls, invo = mo == -INFINITY ? 0.f : kUnit / lso;
       const int Hg = min(kHeads, a.H - g * kHeads);
       const size_t pslot = (size_t)blockIdx.x * 2 + (slot > 0 ? 1 : 0);
-      if (slot >= 0 && warp == 0) {
-        float* le = p.lse + pslot * kHeads;
-        le[2 * lane] = m.x == -INFINITY ? -INFINITY : m.x + __log2f(ls.x);
-        le[2 * lane + 1] = m.y == -INFINITY ? -INFINITY : m.y + __log2f(ls.y);
-      }
-      if (!warp_wait(BAR(C::kPvDoneB), (uint32_t)(k & 1), abort_flag)) break;
+      if (slot >= 0 && half == 0)
+        p.lse[pslot * kHeads + head] = m == -INFINITY ? -INFINITY : m + __log2f(ls);
+      ok = warp_wait(BAR(C::kPvDoneB + (k & 1)), (uint32_t)((k >> 1) & 1), abort_flag) && ok;
       tc_fence_after();
+      // channel of this thread in tile i of O^T
+      const int d0 = kFp8 || tid < 64 ? tid : 64 * nh + tid - 64, dstep = kFp8 ? 128 : 64;
 #pragma unroll 1
       for (int hf = 0; hf < 2; ++hf) {
         if (hf * 32 >= Hg) break;
         float iv[32];
 #pragma unroll
-        for (int c = 0; c < 32; ++c)
-          iv[c] = __shfl_sync(0xffffffffu, (c & 1) ? inv.y : inv.x, hf * 16 + (c >> 1));
-        const int nh = min(32, Hg - hf * 32);
-#pragma unroll 1
-        for (int i = 0; i < n_mt; ++i) {
-          const int d = i * 128 + tid;
-          float o[32];
-          tmem_ld32(lane_base + kOCol + i * 64 + hf * 32, o);
-          tmem_wait_ld();
+        for (int c = 0; c < 32; ++c) iv[c] = column(inv, invo, hf * 32 + c);
+        const int n_h = min(32, Hg - hf * 32);
+        const auto store = [&](int i, const float (&o)[32]) {
+          const int d = d0 + i * dstep;
           if (slot >= 0) {
             float* wo = p.part + (pslot * kHeads + hf * 32) * L + d;
             if (d < L) {
 #pragma unroll
               for (int c = 0; c < 32; ++c)
-                if (c < nh) wo[(uint32_t)(c * L)] = o[c] * iv[c];
+                if (c < n_h) wo[(uint32_t)(c * L)] = o[c] * iv[c];
             }
           } else {
             // lanes 2m and 2m + 1 swap halves so that each stores two adjacent channels
@@ -822,9 +965,20 @@ __global__ void __launch_bounds__(Cfg<kFp8>::kThreads, 1)
               const float recv = __shfl_xor_sync(0xffffffffu, up ? x0 : x1, 1);
               const uint32_t pr = up ? pack_bf16x2(recv, x1) : pack_bf16x2(x0, recv);
               const int hh = c + (up ? 1 : 0);
-              if (hh < nh && d < L) *reinterpret_cast<uint32_t*>(ob + (uint32_t)(hh * L)) = pr;
+              if (hh < n_h && d < L) *reinterpret_cast<uint32_t*>(ob + (uint32_t)(hh * L)) = pr;
             }
           }
+        };
+        // two tiles of O^T a round: the next one is read from TMEM while one is stored
+#pragma unroll 1
+        for (int i = 0; i < n_mt; i += 2) {
+          float o0[32], o1[32];
+          tmem_ld32(lane_base + i * 64 + hf * 32, o0);
+          tmem_wait_ld();
+          if (i + 1 < n_mt) tmem_ld32(lane_base + (i + 1) * 64 + hf * 32, o1);
+          store(i, o0);
+          tmem_wait_ld();
+          if (i + 1 < n_mt) store(i + 1, o1);
         }
       }
       tc_fence_before();
@@ -834,63 +988,133 @@ __global__ void __launch_bounds__(Cfg<kFp8>::kThreads, 1)
 #undef BAR
   tc_fence_before();
   __syncthreads();
-  if (warp == 4) {
+  if (warp == 8) {
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);
   }
 }
 
 // Joins the parts of the tokens that were cut: out = sum_i 2^(lse_i - M) O_i / sum_i 2^(lse_i - M).
-// A unit is one head of one such token; the eight warps of a block take every eighth part each, and
-// add up in warp order.
+// Most tokens are cut in two or three: a warp takes a head of one, with all its loads in flight at
+// once.  A token of more than kWarpParts parts (few long sequences) takes a block a head, its eight warps
+// every eighth part each, added up in warp order.  Bound by reading the parts.
 constexpr int kMergeWarps = 8;
 constexpr int kMergeMaxCuts = 1024;
+constexpr int kWarpParts = 8;
 
 __global__ void __launch_bounds__(32 * kMergeWarps)
     latent_merge_kernel(const int2* __restrict__ cut, const float* __restrict__ lse,
                         const float* __restrict__ part, __nv_bfloat16* __restrict__ out, int slices,
                         int groups, int H, int L) {
   __shared__ __align__(16) float sum[kMergeWarps][kLatMaxDim];
-  __shared__ __align__(16) int2 item[kMergeMaxCuts];   // slice where the token begins, its last slice
-  __shared__ int n_items;
+  // of every cut token: the slice where it begins, its last slice, itself, units of the tokens before it
+  __shared__ __align__(16) int4 item[kMergeMaxCuts];
+  __shared__ int n_items, n_units;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   pdl_wait();
   if (warp == 0) {
-    int n = 0;
+    int n = 0, units = 0;
     for (int s0 = 0; s0 < slices; s0 += 32) {
       const int s = s0 + lane;
       const int2 c = s < slices ? cut[(size_t)s * groups] : make_int2(-1, 0);
       const unsigned m = __ballot_sync(0xffffffffu, c.x >= 0);
-      if (c.x >= 0) item[n + __popc(m & ((1u << lane) - 1u))] = make_int2(s, c.y);
+      const int mine = c.x < 0 ? 0 : (c.y - s + 1 <= kWarpParts ? (H + kMergeWarps - 1) / kMergeWarps : H);
+      int scan = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, scan, o);
+        if (lane >= o) scan += x;
+      }
+      if (c.x >= 0) item[n + __popc(m & ((1u << lane) - 1u))] = make_int4(s, c.y, c.x, units + scan - mine);
       n += __popc(m);
+      units += __shfl_sync(0xffffffffu, scan, 31);
     }
-    if (lane == 0) n_items = n;
+    if (lane == 0) {
+      n_items = n;
+      n_units = units;
+    }
   }
   __syncthreads();
-  const long long units = (long long)n_items * H;
-  for (long long u = blockIdx.x; u < units; u += gridDim.x) {
-    const int2 it = item[u / H];
-    const int h = (int)(u % H), g = h / kHeads, hl = h % kHeads;
+  for (int u = blockIdx.x; u < n_units; u += gridDim.x) {
+    int lo = 0, hi = n_items - 1;          // the last token whose units begin at or before u
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (item[mid].w <= u) lo = mid; else hi = mid - 1;
+    }
+    const int4 it = item[lo];
     const int n = it.y - it.x + 1;
+    const bool by_warp = n <= kWarpParts;
+    const int h = by_warp ? (u - it.w) * kMergeWarps + warp : u - it.w;
+    const int g = h / kHeads, hl = h % kHeads;
     // part i: the first slice's second slot, then every later slice's first
-    const auto slot = [&](int i) { return ((size_t)(it.x + i) * groups + g) * 2 + (i == 0 ? 1 : 0); };
+    const auto slot = [&](int i) { return (((size_t)(it.x + i) * groups + g) * 2 + (i == 0 ? 1 : 0)) * kHeads + hl; };
+    __nv_bfloat16* row = out + ((size_t)it.z * H + h) * L;
+    if (by_warp) {
+      if (h >= H) continue;
+      // (a lane's four channels of every 128; parts past n count as the first with weight 0)
+      const float mine = lane < n ? lse[slot(lane)] : -INFINITY;
+      float4 acc[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) acc[q] = make_float4(0.f, 0.f, 0.f, 0.f);
+      float M = mine;
+#pragma unroll
+      for (int o = 4; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+      const float ref = M == -INFINITY ? 0.f : M;
+      const float w = exp2f(mine - ref);
+      float tot = w;
+#pragma unroll
+      for (int o = 4; o > 0; o >>= 1) tot += __shfl_xor_sync(0xffffffffu, tot, o);
+      const float inv = M == -INFINITY ? 0.f : 1.f / tot;
+      for (int i0 = 0; i0 < n; i0 += 2) {
+        float4 v[2][4];
+#pragma unroll
+        for (int z = 0; z < 2; ++z) {
+          const float* src = part + slot(i0 + z < n ? i0 + z : i0) * L;
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const int d = 4 * lane + 128 * q;
+            v[z][q] = d < L ? *reinterpret_cast<const float4*>(src + d) : make_float4(0.f, 0.f, 0.f, 0.f);
+          }
+        }
+#pragma unroll
+        for (int z = 0; z < 2; ++z) {
+          const float f = __shfl_sync(0xffffffffu, w * inv, i0 + z);
+          if (i0 + z >= n) break;
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            acc[q].x = fmaf(f, v[z][q].x, acc[q].x);
+            acc[q].y = fmaf(f, v[z][q].y, acc[q].y);
+            acc[q].z = fmaf(f, v[z][q].z, acc[q].z);
+            acc[q].w = fmaf(f, v[z][q].w, acc[q].w);
+          }
+        }
+      }
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int d = 4 * lane + 128 * q;
+        if (d < L)
+          *reinterpret_cast<uint2*>(row + d) = make_uint2(pack_bf16x2(acc[q].x, acc[q].y),
+                                                          pack_bf16x2(acc[q].z, acc[q].w));
+      }
+      continue;
+    }
     float M = -INFINITY;
-    for (int i = lane; i < n; i += 32) M = fmaxf(M, lse[slot(i) * kHeads + hl]);
+    for (int i = lane; i < n; i += 32) M = fmaxf(M, lse[slot(i)]);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
     // (a NaN among the parts' sums is not seen by the maximum but comes back in its weight)
     const float ref = M == -INFINITY ? 0.f : M;
     float tot = 0.f;
-    for (int i = lane; i < n; i += 32) tot += exp2f(lse[slot(i) * kHeads + hl] - ref);
+    for (int i = lane; i < n; i += 32) tot += exp2f(lse[slot(i)] - ref);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) tot += __shfl_xor_sync(0xffffffffu, tot, o);
     float4 acc[4];
 #pragma unroll
     for (int q = 0; q < 4; ++q) acc[q] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 2
+#pragma unroll 4
     for (int i = warp; i < n; i += kMergeWarps) {
-      const float w = exp2f(lse[slot(i) * kHeads + hl] - ref);
-      const float* src = part + (slot(i) * kHeads + hl) * L;
+      const float w = exp2f(lse[slot(i)] - ref);
+      const float* src = part + slot(i) * L;
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         const int d = 4 * lane + 128 * q;
@@ -906,7 +1130,6 @@ __global__ void __launch_bounds__(32 * kMergeWarps)
 #pragma unroll
     for (int q = 0; q < 4; ++q) *reinterpret_cast<float4*>(&sum[warp][4 * lane + 128 * q]) = acc[q];
     __syncthreads();
-    const int t = cut[(size_t)it.x * groups].x;
     const float inv = M == -INFINITY ? 0.f : 1.f / tot;
     for (int d = 2 * threadIdx.x; d < L; d += 2 * 32 * kMergeWarps) {
       float x = 0.f, y = 0.f;
@@ -915,7 +1138,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps)
         x += sum[w][d];
         y += sum[w][d + 1];
       }
-      *reinterpret_cast<uint32_t*>(out + ((size_t)t * H + h) * L + d) = pack_bf16x2(x * inv, y * inv);
+      *reinterpret_cast<uint32_t*>(row + d) = pack_bf16x2(x * inv, y * inv);
     }
     __syncthreads();
   }
@@ -949,7 +1172,7 @@ cudaError_t launch(const DecodeParams& p, cudaStream_t stream, unsigned grid) {
   const cudaError_t e = cudaFuncSetAttribute(latent_decode_kernel<kFp8>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (e != cudaSuccess) return e;
-  return launch_with_pdl(latent_decode_kernel<kFp8>, dim3(grid), dim3(C::kThreads), C::kSmem, stream,
+  return launch_with_pdl(latent_decode_kernel<kFp8>, dim3(grid), dim3(kThreads), C::kSmem, stream,
                          false, p);
 }
 
@@ -971,20 +1194,29 @@ cudaError_t launch_latent_decode(const LatentDecodeArgs& a, bool fp8, void* work
   p.cut = reinterpret_cast<int2*>(ws + w.cut);
   p.lse = reinterpret_cast<float*>(ws + w.lse);
   p.part = reinterpret_cast<float*>(ws + w.part);
-  // Boxes of as many rows as divide a page and a tile: a box then lies in one page.  Pages that
-  // leave fewer than four rows take gathers of four single rows instead.
-  int box = a.pool.ps & -a.pool.ps;
-  box = box > kKeys ? kKeys : box;
-  p.box_rows = box >= 4 ? box : 0;
-  const long long rows = a.pool.num_blocks * a.pool.ps;
-  if (!encode_rows(&p.rows, a.pool.rows, rows, a.pool.row_bytes, p.box_rows > 0 ? p.box_rows : 1))
-    return cudaErrorInvalidValue;
-  if (!fp8) {
-    if (!encode_bf16_3d(&p.ql, a.q_latent, a.pool.L, a.H, a.ql_sh, a.T, a.ql_st, kHeads, 1))
-      return cudaErrorInvalidValue;
-    if (a.pool.R > 0 &&
-        !encode_bf16_3d(&p.qr, a.q_rope, a.pool.R, a.H, a.qr_sh, a.T, a.qr_st, kHeads, 1))
-      return cudaErrorInvalidValue;
+  // Pages of a multiple of 64 entries: a tile is 64 consecutive rows, and one tensor-map copy brings all
+  // its whole 128-byte chunks in slot order (bf16: pairs of the two halves, so only where they pair
+  // up); the chunks left over come one by one.  Other pages: cp.async, any row anywhere.
+  p.boxed = a.pool.ps % kKeys == 0;
+  if (p.boxed) {
+    const long long rows = a.pool.num_blocks * a.pool.ps;
+    const unsigned long long W = a.pool.row_bytes;
+    const int nl = a.pool.L / 64;
+    const unsigned long long cd[2] = {W, (unsigned long long)rows}, cs[1] = {W};
+    const unsigned cb[2] = {128, kKeys};
+    if (!encode_bytes(&p.chunk, a.pool.rows, 2, cd, cs, cb)) return cudaErrorInvalidValue;
+    if (fp8 && W >= 128) {
+      p.whole = (int)(W / 128);
+      const unsigned long long d[3] = {128, (unsigned long long)rows, W / 128}, st[2] = {W, 128};
+      const unsigned bx[3] = {128, kKeys, (unsigned)p.whole};
+      if (!encode_bytes(&p.block, a.pool.rows, 3, d, st, bx)) return cudaErrorInvalidValue;
+    } else if (!fp8 && nl % 2 == 0) {
+      p.whole = nl;
+      const unsigned long long half = nl / 2;
+      const unsigned long long d[4] = {128, (unsigned long long)rows, 2, half}, st[3] = {W, half * 128, 128};
+      const unsigned bx[4] = {128, kKeys, 2, (unsigned)half};
+      if (!encode_bytes(&p.block, a.pool.rows, 4, d, st, bx)) return cudaErrorInvalidValue;
+    }
   }
   const unsigned grid = (unsigned)p.slices * (unsigned)p.groups;
   cudaError_t e = fp8 ? launch<true>(p, stream, grid) : launch<false>(p, stream, grid);

@@ -104,10 +104,12 @@ int decode_with_partials(const void* q, const spa_pool_t* win, const spa_pool_t*
 // first use), and the record of a failed CUDA call (returns SPA_ERR_CUDA).
 int api_current_device(int* dev, int* sms);
 int api_cuda_fail(cudaError_t e, const char* what);
-// Tensor maps with 128-byte boxes and the 128-byte swizzle, zero where a box leaves the tensor:
-// rows of row_bytes bytes as a 2D byte tensor, boxes of box_rows rows; and a bf16 [n2][n1][width]
-// tensor with byte strides, boxes of 64 values, box1 and box2.  False when the driver refuses.
-bool encode_rows(CUtensorMap* m, const void* base, long long rows, int row_bytes, int box_rows);
+// Tensor maps with the 128-byte swizzle, zero where a box leaves the tensor: a byte tensor of `rank`
+// dimensions (strides in bytes, of all but the first; boxes 128 bytes wide); and a bf16
+// [n2][n1][width] tensor with byte strides, boxes of 64 values, box1 and box2.  False when the
+// driver refuses.
+bool encode_bytes(CUtensorMap* m, const void* base, int rank, const unsigned long long* dims,
+                  const unsigned long long* strides, const unsigned* box);
 bool encode_bf16_3d(CUtensorMap* m, const void* base, int width, int n1, long long stride1, int n2,
                     long long stride2, int box1, int box2);
 

@@ -7,9 +7,9 @@ Bounds of an attention output, per element (``A = sum_j p_j |v_j|``, from the or
 * the output's rounding to bf16: ``2^-8 |out|``;
 * probabilities rounded to bf16 before the value product: ``2^-8 A``.  e4m3 pools: a weight
   ``w = p * scale`` enters as an e5m2 and an e4m3 term of ``u = w * 2^k`` where 2^k brings the
-  largest weight to at least 2^7: the first term leaves ``2^-3 u``, the second ``2^-4`` of that or
-  half of e4m3's smallest step, so the error is at most
-  ``min(2^-3 w, 2^-7 w + 2^-10 2^-7 w_max)``;
+  largest weight to at least 2^7: u is rounded to f16 (``2^-11 u``), the first term leaves
+  ``2^-3 u``, the second ``2^-4`` of that or half of e4m3's smallest step, so the error is at most
+  ``2^-11 w + min(2^-3 w, 2^-7 w + 2^-10 2^-7 w_max)``;
 * a score's error d (absolute, natural units) changes every p by at most a factor ``e^(2d)``:
   ``(e^(2d) - 1) A``.  d = the accumulation of W products in fp32 (tensor cores may truncate where
   they align a group: ``W 2^-23`` of the terms' sum ``qk``) + the score times log2(e) in fp32 and
@@ -59,7 +59,7 @@ def tolerance(out, terms, n_products, v=None, rows=None, row_scale=None, qmax=No
         if p.shape[1]:
             w = p * row_scale[None]
             wmax = w.max(1, keepdims=True)
-            werr = np.minimum(2.0 ** -3 * w, 2.0 ** -7 * w + 2.0 ** -17 * wmax)
+            werr = 2.0 ** -11 * w + np.minimum(2.0 ** -3 * w, 2.0 ** -7 * w + 2.0 ** -17 * wmax)
             codes = np.abs(rows[:, :out.shape[1]]) / row_scale[:, None]
             weights = werr @ codes
             d = d + abs(scale) * 2.0 ** -17 * qmax * np.abs(rows).sum(1).max()
@@ -275,6 +275,10 @@ DECODE_CASES = {
     "l448_r40_p1": dict(lens=[150], H=32, L=448, R=40, ps=1),
     "l128_r8_p16": dict(lens=[333, 17], H=64, L=128, R=8, ps=16),
     "l192_r64_p2": dict(lens=[131], H=64, L=192, R=64, ps=2),
+    "l192_p64": dict(lens=[200, 64], H=64, L=192, R=64, ps=64),
+    "l64_norope_p64": dict(lens=[130, 7], H=20, L=64, R=0, ps=64),
+    "l320_r8_p128": dict(lens=[300], H=64, L=320, R=8, ps=128),
+    "l384_r24_p192": dict(lens=[450, 191, 193], H=64, L=384, R=24, ps=192),
     "q3": dict(lens=[260, 66, 3], H=64, L=512, R=64, ps=64, q=3),
     "long": dict(lens=[9000], H=64, L=512, R=64, ps=64),
     "many_tokens": dict(lens=[5 + 7 * i for i in range(170)], H=8, L=64, R=16, ps=16),
