@@ -21,13 +21,15 @@
 // one is loaded, one multiplied, one waits for its softmax.  P takes the place of its own tile's
 // rotary chunk, which nobody reads any more.  TMEM: O^T 256 columns, S 128, q 128.
 //
-//   warps 0-3   softmax: a thread has one head and half a tile's entries; it adds the other half's
-//               part of S (through shared memory), then maximum and sum are in registers; epilogue
-//   warps 4-7   the next token's q: into TMEM (bf16), or as two e4m3 terms into shared memory; and
+//   warps 0-7   softmax: a thread has one head and a quarter of a tile's entries; it adds the other
+//               stacked block's part of S (through shared memory), then maximum and sum are in
+//               registers; epilogue.  (With four warps, half a tile a thread, the softmax took longer
+//               than the tile's MMAs.)
+//   warps 8-11  the next token's q: into TMEM (bf16), or as two e4m3 terms into shared memory; and
 //               the rows by cp.async where a tile is not one box of a page
-//   warp 8      issues the MMAs of S, warp 10 those of O: two warps, so that neither one's waits keep
+//   warp 12     issues the MMAs of S, warp 14 those of O: two warps, so that neither one's waits keep
 //               the tensor core idle while the other has work
-//   warp 9      schedule, page tables, tensor-map copies (pages of a multiple of 64 entries: a tile
+//   warp 13     schedule and page tables, two tiles ahead; tensor-map copies (pages of a multiple of 64 entries: a tile
 //               is then one box of rows by 128-byte chunks, a single copy)
 //
 // Schedule: the tiles of all tokens are one long line; each slice of CTAs (one CTA for every 64
@@ -57,7 +59,8 @@ constexpr int kBufs = 3;          // tiles of rows in shared memory
 constexpr int kRing = 4;          // tile infos in flight
 constexpr int kTmemCols = 512;
 constexpr int kSCol = 256, kQCol = 384;   // TMEM columns: O^T from 0, S, q
-constexpr int kThreads = 352;
+constexpr int kSoftmax = 256;     // threads of the softmax warps
+constexpr int kThreads = kSoftmax + 224;
 constexpr int kMinTiles = 2;      // tiles of a slice at least: fewer would cost more in merging
 
 // first and last tile of this CTA's part of a token, its last tile of all, no tile at all
@@ -83,24 +86,25 @@ struct Cfg {
   static constexpr int kQOff = 0;
   static constexpr int kKOff = kQBytes;
   static constexpr int kPOff = kKOff + kBufs * kBufBytes;            // e4m3: two P buffers
-  static constexpr int kRedOff = kPOff + (kFp8 ? 2 * 8192 : 0);      // float [2][2][64]
-  static constexpr int kQScaleOff = kRedOff + 2 * 2 * kHeads * 4;    // e4m3: float [4][64]
+  static constexpr int kRedOff = kPOff + (kFp8 ? 2 * 8192 : 0);      // float [4][64]
+  static constexpr int kQScaleOff = kRedOff + 4 * kHeads * 4;    // e4m3: float [4][64]
   static constexpr int kInfoOff = kQScaleOff + (kFp8 ? 4 * kHeads * 4 : 0);
   static constexpr int kBarOff = kInfoOff + kRing * (int)sizeof(Info);
-  // barriers
+  // barriers (each in its own word; those of one kind side by side)
   static constexpr int kFullB = 0, kEmptyB = kFullB + kBufs, kQFullB = kEmptyB + kBufs,
                        kQEmptyB = kQFullB + 1, kSFullB = kQEmptyB + 1, kSEmptyB = kSFullB + 2,
                        kPFullB = kSEmptyB + 2, kPvDoneB = kPFullB + 2, kOFreeB = kPvDoneB + 2,
                        kInfoFullB = kOFreeB + 1, kInfoEmptyB = kInfoFullB + kRing,
-                       kDrainB = kInfoEmptyB + kRing, kTokenB = kDrainB + 2, kNumB = kTokenB + 1;
+                       kDrainB = kInfoEmptyB + kRing, kTokenB = kDrainB + 2, kRedFreeB = kTokenB + 1,
+                       kNumB = kRedFreeB + 1;
   static constexpr int kMiscOff = kBarOff + kNumB * 8;   // TMEM base, abort flag, first token
   static constexpr int kSmem = kMiscOff + 12;
   static_assert(kSmem <= 232448, "shared memory budget");
 };
 
 struct DecodeParams {
-  // With `boxed`: the pool's 128-byte chunks of 64 rows, one chunk a box; and all whole chunks of 64
-  // rows in one box, in slot order (`whole` of them, 0: none).
+  // With `boxed`: the pool's 128-byte chunks of 64 rows, one chunk a box; and the first `whole` slots of
+  // 64 rows in one box (0: none).
   CUtensorMap chunk, block;
   LatentDecodeArgs a;
   int boxed, whole;
@@ -141,25 +145,28 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(BAR(C::kFullB + i), p.boxed ? 1 : 128);   // armed by the loader, or cp.async's threads
       mbar_init(BAR(C::kEmptyB + i), 1);
     }
-    mbar_init(BAR(C::kQFullB), 128);
+    mbar_init(BAR(C::kQFullB), 4);
     mbar_init(BAR(C::kQEmptyB), 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(BAR(C::kSFullB + i), 1);
-      mbar_init(BAR(C::kSEmptyB + i), 128);
+      // (lane 0 of every warp arrives for it: an arrival of every thread on one barrier takes the
+      // barrier a cycle or two each, hundreds of cycles a tile)
+      mbar_init(BAR(C::kSEmptyB + i), 8);
       mbar_init(BAR(C::kPvDoneB + i), 1);
-      mbar_init(BAR(C::kPFullB + i), 128);
+      mbar_init(BAR(C::kPFullB + i), 8);
       mbar_init(BAR(C::kDrainB + i), 1);
     }
-    mbar_init(BAR(C::kOFreeB), 128);
+    mbar_init(BAR(C::kOFreeB), 8);
     for (int i = 0; i < kRing; ++i) {
       mbar_init(BAR(C::kInfoFullB + i), 1);
-      mbar_init(BAR(C::kInfoEmptyB + i), 10);  // two MMA, four softmax and four q warps
+      mbar_init(BAR(C::kInfoEmptyB + i), 14);  // two MMA, eight softmax and four q warps
     }
     mbar_init(BAR(C::kTokenB), 1);
+    mbar_init(BAR(C::kRedFreeB), 8);         // lane 0 of every softmax warp
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == 8) tmem_alloc(sb + C::kMiscOff, kTmemCols);
+  if (warp == 12) tmem_alloc(sb + C::kMiscOff, kTmemCols);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -180,7 +187,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int g = blockIdx.x % p.groups;                  // this CTA's 64 heads
   const int slice = blockIdx.x / p.groups;
 
-  if (warp == 9) {
+  if (warp == 13) {
     // ================================ schedule and loads ==================================
     long long total = 0;
     for (int t = lane; t < a.T; t += 32) {
@@ -208,7 +215,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     };
     int it_t = 0, it_j = 0;                    // next tile: token, tile of the token
-    long long it_pos = begin;                  // its place in the line
     if (begin < end) {
       long long before = 0;
       for (load_chunk(0);; load_chunk(t0 + 32)) {
@@ -237,68 +243,75 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_arrive(BAR(C::kTokenB));
     }
     struct Tile {
-      int t, flags, slot, n;                   // n: entries of the tile that are in the sequence
+      int t, flags, slot;
       int blk[2], off[2];                      // block and slot in it of entries lane, 32 + lane
     };
-    int started = it_j == 0;                   // the current token's first tile is this CTA's
+    int left_all = begin < end ? (int)min(end - begin, (long long)0x7fffffff) : 0;   // tiles to go
+    // The token of the next tile: its sequence, tiles to go, entries to go, whether its first tile is
+    // this CTA's; and, boxed (tiles lie in one page each), the slot in the page and the blocks of tiles
+    // c_tile .. c_tile + 31, one a lane.
+    int b_t = 0, left = 0, entries = 0, started = 0, off = 0, c_tile = 0, c_blk = -1;
     bool fresh = true;
     int2 cut = make_int2(-1, 0);
-    // Boxed tiles lie in one page each: lane i holds the block of tile c_tile + i of token c_t.
-    int c_t = -1, c_tile = 0, c_blk = -1;
-    auto next_tile = [&](Tile& x) {            // the next tile, its block-table reads under way
-      x.t = -1;
-      if (it_pos >= end) return;
+    const auto begin_token = [&]() {
       if (it_t >= t0 + 32) load_chunk(it_t);
       const int k = it_t - t0;
       const int len = __shfl_sync(0xffffffffu, c_len, k);
-      const int b = __shfl_sync(0xffffffffu, c_seq, k);
-      const int nt = tiles_of(len);
-      if (it_j == 0 && __shfl_sync(0xffffffffu, c_bad, k) && lane == 0) flag_error(SPA_ERR_INDEX);
+      b_t = __shfl_sync(0xffffffffu, c_seq, k);
+      started = it_j == 0;
+      if (started && __shfl_sync(0xffffffffu, c_bad, k) && lane == 0) flag_error(SPA_ERR_INDEX);
+      left = tiles_of(len) - it_j;
+      entries = len - it_j * kKeys;
+      if (started && left > left_all)          // (the line ends inside it: the slice where it ends)
+        cut = make_int2(it_t, (int)((end - left_all + left - 1) / per));
+      if (p.boxed) off = (int)(((long long)it_j * kKeys) % a.pool.ps);
+      c_tile = it_j - 32;
+      fresh = true;
+    };
+    if (left_all > 0) begin_token();
+    auto next_tile = [&](Tile& x) {            // the next tile, its block-table reads under way
+      x.t = -1;
+      if (left_all == 0) return;
+      if (left == 0) {
+        ++it_t;
+        it_j = 0;
+        begin_token();
+      }
       x.t = it_t;
-      x.n = min(kKeys, len - it_j * kKeys);
-      const bool item_end = it_j == nt - 1, all_end = it_pos == end - 1;
-      const bool last = item_end || all_end;
-      x.flags = (fresh ? kFirst : 0) | (last ? kLast : 0) | (all_end ? kFinal : 0);
-      x.slot = started && item_end ? -1 : started;
-      if (last && !item_end && started)
-        cut = make_int2(it_t, (int)((it_pos + (nt - 1 - it_j)) / per));
+      const bool last = left == 1 || left_all == 1;
+      x.flags = (fresh ? kFirst : 0) | (last ? kLast : 0) | (left_all == 1 ? kFinal : 0);
+      x.slot = started && left == 1 ? -1 : started;
       if (p.boxed) {
-        if (c_t != it_t || it_j >= c_tile + 32) {
-          c_t = it_t;
+        if (it_j >= c_tile + 32) {
           c_tile = it_j;
-          const int page = ((it_j + lane) * kKeys) / a.pool.ps;
-          c_blk = it_j + lane < nt && page < a.pool.bt_stride
-                      ? __ldg(a.pool.bt + (size_t)b * a.pool.bt_stride + page) : -1;
+          const int page = (it_j * kKeys + min(lane, left - 1) * kKeys) / a.pool.ps;
+          c_blk = entries > 0 ? __ldg(a.pool.bt + (size_t)b_t * a.pool.bt_stride + page) : -1;
         }
         const int blk = __shfl_sync(0xffffffffu, c_blk, it_j - c_tile);
-        const int off = (it_j * kKeys) % a.pool.ps;
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          x.blk[e] = lane + 32 * e < x.n ? blk : -2;   // -2: not of the sequence
+          x.blk[e] = lane + 32 * e < entries ? blk : -2;   // -2: not of the sequence
           x.off[e] = off + lane + 32 * e;
         }
+        off = off + kKeys == a.pool.ps ? 0 : off + kKeys;
       } else {
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const int j = lane + 32 * e;
           x.blk[e] = -2;
           x.off[e] = 0;
-          if (j < x.n) {
-            const int key = it_j * kKeys + j;
+          if (lane + 32 * e < entries) {
+            const int key = it_j * kKeys + lane + 32 * e;
             const int page = key / a.pool.ps;
             x.off[e] = key - page * a.pool.ps;
-            x.blk[e] = __ldg(a.pool.bt + (size_t)b * a.pool.bt_stride + page);
+            x.blk[e] = __ldg(a.pool.bt + (size_t)b_t * a.pool.bt_stride + page);
           }
         }
       }
-      fresh = last;
-      ++it_pos;
+      fresh = false;
+      --left_all;
+      --left;
       ++it_j;
-      if (item_end) {
-        ++it_t;
-        it_j = 0;
-        started = 1;
-      }
+      entries -= kKeys;
     };
     // Rows of a tile (-1: no such entry) and, e4m3, their scales.
     auto resolve = [&](const Tile& x, int (&row)[2], float (&sc)[2]) {
@@ -307,102 +320,99 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         if (x.blk[e] >= 0 && (long long)x.blk[e] < a.pool.num_blocks)
-          row[e] = (int)((long long)x.blk[e] * a.pool.ps + x.off[e]);
+          row[e] = x.blk[e] * a.pool.ps + x.off[e];        // (below 2^30)
         else if (x.blk[e] != -2)
           flag_error(SPA_ERR_INDEX);
         sc[e] = kFp8 && row[e] >= 0 ? __ldg(a.pool.scale + row[e]) : 0.f;
       }
     };
-    // Three tiles under way: the one being issued, the next with its scales, and the one after with its
-    // blocks on the way.
-    Tile cur, nxt;
-    int row_cur[2], row_nxt[2];
-    float sc_cur[2] = {0.f, 0.f}, sc_nxt[2] = {0.f, 0.f};
-    next_tile(cur);
+    // A tile's blocks are read two tiles ahead of its copy and its scales one ahead; nothing loaded is
+    // touched (not even copied to another register) before it is needed.
+    Tile nxt = {};
+    int row[2], t_cur, flags_cur, slot_cur;
+    float sc[2] = {0.f, 0.f};
+    const auto take = [&]() {                  // the tile read last becomes the current one
+      t_cur = nxt.t;
+      flags_cur = nxt.flags;
+      slot_cur = nxt.slot;
+      resolve(nxt, row, sc);
+      next_tile(nxt);
+    };
     next_tile(nxt);
-    resolve(cur, row_cur, sc_cur);
+    take();
     const int total_rows = (int)(a.pool.num_blocks * a.pool.ps);
-    int k = 0, buf = 0;
+    int k = 0, buf = 0, fills = 0;
     uint32_t buf_ph = 0;
     bool ok = true;
-    if (cur.t < 0) {                           // nothing to do: tell the others
+    if (t_cur < 0) {                           // nothing to do: tell the others
       if (lane == 0) {
         infos[0].flags = kEnd;
         __threadfence_block();
         mbar_arrive(BAR(C::kInfoFullB));
       }
     }
-    for (; cur.t >= 0; ++k) {
-      resolve(nxt, row_nxt, sc_nxt);
-      Tile nxt2;
-      next_tile(nxt2);
+    for (; t_cur >= 0; ++k) {
+      if (p.boxed) {                           // its copy first: everything else can wait for that
+        ok = warp_wait(BAR(C::kEmptyB + buf), buf_ph ^ 1, abort_flag);
+        if (!ok) break;
+        // a tile without entries starts past the last row and is filled with zeros
+        const int base = (int)warp_uniform(row[0] >= 0 ? row[0] : total_rows);
+        if (elect_one()) {
+          const uint32_t dst = sb + C::kKOff + buf * C::kBufBytes, full = BAR(C::kFullB + buf);
+          mbar_arrive_expect_tx(full, (uint32_t)(n_chunks * kChunkBytes));
+          if (p.whole > 0) {
+            if (kFp8) tma_box3(dst, &p.block, 0, base, 0, full);
+            else tma_box4(dst, &p.block, 0, base, 0, 0, full);
+          }
+          for (int c = p.whole; c < n_chunks; ++c)
+            tma_row(dst + slot_of(c) * kChunkBytes, &p.chunk, c * 128, base, full);
+        }
+        __syncwarp();
+        ++fills;
+        if (++buf == kBufs) {
+          buf = 0;
+          buf_ph ^= 1;
+        }
+      }
       // publish the tile
       const int ri = k % kRing;
       ok = warp_wait(BAR(C::kInfoEmptyB + ri), ((k / kRing) & 1) ^ 1, abort_flag);
       if (!ok) break;
-      const unsigned lo = __ballot_sync(0xffffffffu, row_cur[0] >= 0);
-      const unsigned hi = __ballot_sync(0xffffffffu, row_cur[1] >= 0);
+      const unsigned lo = __ballot_sync(0xffffffffu, row[0] >= 0);
+      const unsigned hi = __ballot_sync(0xffffffffu, row[1] >= 0);
       typename C::Info& info = infos[ri];
       if (!p.boxed) {
-        info.row[lane] = row_cur[0];
-        info.row[lane + 32] = row_cur[1];
+        info.row[lane] = row[0];
+        info.row[lane + 32] = row[1];
       }
       if (kFp8) {
         // the maximum of a tile is taken over p_j |scale_j|, the weights that enter the value
         // product (a scale below 2^-60 counts as that: the sums of p_j alone must stay finite)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          info.scale[lane + 32 * e] = 128.f * sc_cur[e];
-          info.lscale[lane + 32 * e] = row_cur[e] >= 0 ? fmaxf(__log2f(fabsf(sc_cur[e])), -60.f) : -INFINITY;
+          info.scale[lane + 32 * e] = 128.f * sc[e];
+          info.lscale[lane + 32 * e] = row[e] >= 0 ? fmaxf(__log2f(fabsf(sc[e])), -60.f) : -INFINITY;
         }
       }
       if (lane == 0) {
-        info.t = cur.t;
-        info.flags = cur.flags;
-        info.slot = cur.slot;
+        info.t = t_cur;
+        info.flags = flags_cur;
+        info.slot = slot_cur;
         info.valid[0] = lo;
         info.valid[1] = hi;
       }
       __threadfence_block();
       __syncwarp();
       if (lane == 0) mbar_arrive(BAR(C::kInfoFullB + ri));
-      if (p.boxed) {
-        ok = warp_wait(BAR(C::kEmptyB + buf), buf_ph ^ 1, abort_flag);
-        if (!ok) break;
-        // a tile without entries starts past the last row and is filled with zeros
-        const int row = (int)warp_uniform(row_cur[0] >= 0 ? row_cur[0] : total_rows);
-        if (elect_one()) {
-          const uint32_t dst = sb + C::kKOff + buf * C::kBufBytes, full = BAR(C::kFullB + buf);
-          mbar_arrive_expect_tx(full, (uint32_t)(n_chunks * kChunkBytes));
-          if (p.whole > 0) {
-            if (kFp8) tma_box3(dst, &p.block, 0, row, 0, full);
-            else tma_box4(dst, &p.block, 0, row, 0, 0, full);
-          }
-          for (int c = p.whole; c < n_chunks; ++c)
-            tma_row(dst + slot_of(c) * kChunkBytes, &p.chunk, c * 128, row, full);
-        }
-        __syncwarp();
-        if (++buf == kBufs) {
-          buf = 0;
-          buf_ph ^= 1;
-        }
-      }
-      cur = nxt;
-      nxt = nxt2;
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        row_cur[e] = row_nxt[e];
-        sc_cur[e] = sc_nxt[e];
-      }
+      take();
     }
     if (lane == 0) {
       p.cut[blockIdx.x] = cut;
       // copies in flight must land before the CTA ends (at once after a normal run)
-      if (p.boxed)
-        for (int q = max(0, k - kBufs); q < k; ++q)
-          mbar_wait_drain(BAR(C::kFullB + q % kBufs), (uint32_t)((q / kBufs) & 1));
+      for (int q = max(0, fills - kBufs); q < fills; ++q)
+        mbar_wait_drain(BAR(C::kFullB + q % kBufs), (uint32_t)((q / kBufs) & 1));
     }
-  } else if (warp == 8) {
+  } else if (warp == 12) {
     // ================================= MMAs of S ==========================================
     // The warp runs as one (its waits too); one elected lane issues.  The MMAs of one tile execute in
     // the order of issue.
@@ -425,7 +435,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!warp_wait(BAR(C::kFullB + buf), full_ph, abort_flag)) break;
       if (!warp_wait(BAR(C::kSEmptyB + sn), ((k / C::kSBufs) & 1) ^ 1, abort_flag)) break;
-      fence_proxy_async_smem();                 // (rows copied by cp.async)
+      if (!p.boxed) fence_proxy_async_smem();   // (rows copied by cp.async)
       tc_fence_after();
       if (lead) {
         const uint32_t dS = tmem + kSCol + sn * 64;
@@ -469,7 +479,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_wait_drain(BAR(C::kDrainB), 0);
     }
     __syncwarp();
-  } else if (warp == 10) {
+  } else if (warp == 14) {
     // ================================= MMAs of O ==========================================
     const uint32_t idO = kFp8 ? idesc_e4m3(128, 64, 1, 0) : idesc_bf16(128, 64, 1, 0);
     const uint32_t idO5 = idO | (1u << 10);            // B in e5m2: the high term of P
@@ -492,7 +502,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!warp_wait(BAR(C::kOFreeB), o_ph ^ 1, abort_flag)) break;
         o_ph ^= 1;
       }
-      fence_proxy_async_smem();
+      if (!p.boxed) fence_proxy_async_smem();
       tc_fence_after();
       if (lead) {
         const uint32_t acc0 = first ? 0u : 1u;
@@ -524,22 +534,42 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_wait_drain(BAR(C::kDrainB + 1), 0);
     }
     __syncwarp();
-  } else if (warp >= 4) {
+  } else if (warp >= 8) {
     // =================================== queries ==========================================
     // Each token's q is read into registers as soon as its first tile is announced, and put in
     // place once the token before has no S left to compute.
-    const int tid = threadIdx.x - 128;
+    const int tid = threadIdx.x - kSoftmax;
     int items = 0, buf = 0, flags = 0;
     auto put_q = [&](int t) -> bool {
       if constexpr (!kFp8) {
         // TMEM lane 32w + l is head 32(w & 1) + l; its first (w < 2) or second half of the latents
-        const int qw = warp - 4, h = g * kHeads + (qw & 1) * 32 + lane;
+        const int qw = warp - 8, h = g * kHeads + (qw & 1) * 32 + lane;
         const int c0 = qw < 2 ? 0 : nh, nc = qw < 2 ? nh : nl - nh;
         const uint4* src = reinterpret_cast<const uint4*>(a.q_latent + t * a.ql_st + h * a.ql_sh) + 8 * c0;
-        uint4 u[32];
+        const auto load = [&](int b, uint4 (&u)[16]) {      // sixteen 16-byte units in flight
 #pragma unroll
-        for (int i = 0; i < 32; ++i)
-          u[i] = (h < a.H && i < 8 * nc) ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
+          for (int i = 0; i < 16; ++i)
+            u[i] = (h < a.H && 16 * b + i < 8 * nc) ? __ldg(src + 16 * b + i) : make_uint4(0, 0, 0, 0);
+        };
+        const auto put = [&](int b, const uint4 (&u)[16]) {
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            float w[32];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              w[4 * i] = __uint_as_float(u[8 * q + i].x);
+              w[4 * i + 1] = __uint_as_float(u[8 * q + i].y);
+              w[4 * i + 2] = __uint_as_float(u[8 * q + i].z);
+              w[4 * i + 3] = __uint_as_float(u[8 * q + i].w);
+            }
+            tmem_st32(tmem + ((uint32_t)(qw * 32) << 16) + kQCol + 64 * b + 32 * q, w);
+          }
+        };
+        if (h < a.H)                    // the second sixteen units on their way to L2
+          for (int i = 16; i < 8 * nc; i += 8)
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(src + i));
+        uint4 u[16];
+        load(0, u);
         uint4 v[4];                     // rotary part: 64 rows of eight 16-byte units
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -550,18 +580,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (!warp_wait(BAR(C::kQEmptyB), (uint32_t)((items & 1) ^ 1), abort_flag)) return false;
         tc_fence_after();
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          float w[32];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            w[4 * i] = __uint_as_float(u[8 * q + i].x);
-            w[4 * i + 1] = __uint_as_float(u[8 * q + i].y);
-            w[4 * i + 2] = __uint_as_float(u[8 * q + i].z);
-            w[4 * i + 3] = __uint_as_float(u[8 * q + i].w);
-          }
-          tmem_st32(tmem + ((uint32_t)(qw * 32) << 16) + kQCol + 32 * q, w);
-        }
+        put(0, u);
+        load(1, u);
+        put(1, u);
         tmem_wait_st();
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -600,7 +621,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float qs = m > 0.f ? pow2_floor(448.f / m) : 1.f;
         if (!warp_wait(BAR(C::kQEmptyB), (uint32_t)((items & 1) ^ 1), abort_flag)) return false;
         if ((tid & 1) == 0)
-          reinterpret_cast<float*>(sm + C::kQScaleOff)[(items & 3) * kHeads + h] = qs;
+          reinterpret_cast<float*>(sm + C::kQScaleOff)[(items & 3) * kHeads + h] = 0.0078125f / qs;
         // piece pc: bytes 8 pc of the row: chunk pc / 16, 16-byte unit (pc / 2) & 7, swizzled by row
         const auto put = [&](int pc, uint2 hi, uint2 lo) {
           uint8_t* d = sm + C::kQOff + (pc >> 4) * 16384 + h * 128 + ((((pc >> 1) & 7) ^ (h & 7)) << 4) +
@@ -636,7 +657,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       fence_proxy_async_smem();
       tc_fence_before();
-      mbar_arrive(BAR(C::kQFullB));
+      __syncwarp();
+      if (lane == 0) mbar_arrive(BAR(C::kQFullB));
       ++items;
       return true;
     };
@@ -664,8 +686,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int row = infos[ri].row[r0 + 16 * i];
           src[i] = row >= 0 ? a.pool.rows + (size_t)row * W : nullptr;
         }
-        if (!warp_wait(BAR(C::kEmptyB + buf), buf_ph ^ 1, abort_flag)) break;
         const uint32_t dst = sb + C::kKOff + buf * C::kBufBytes + r0 * 128 + ((jj ^ (r0 & 7)) << 4);
+        if (!warp_wait(BAR(C::kEmptyB + buf), buf_ph ^ 1, abort_flag)) break;
         for (int c = 0; c < n_chunks; ++c) {
           const int at = c * 128 + jj * 16;
           const uint32_t d = dst + slot_of(c) * kChunkBytes;
@@ -689,29 +711,33 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else {
     // ================================ softmax and epilogue ================================
     const int tid = threadIdx.x;
-    const int half = warp >> 1, pair = warp & 1;   // half of the tile's entries; half of the heads
-    const int head = pair * 32 + lane;
-    const uint32_t lane_base = tmem + ((uint32_t)(warp * 32) << 16);
+    // TMEM lanes 32 quad ..: stacked block `half` of heads 32 pair ..; this warp takes columns of part
+    // `ch`: entries 32 half + 16 ch .. of the tile, and channels' heads 32 ch .. of O^T
+    const int quad = warp & 3, ch = warp >> 2, half = quad >> 1, pair = quad & 1;
+    const int head = pair * 32 + lane, part = 2 * half + ch;
+    const uint32_t lane_base = tmem + ((uint32_t)(quad * 32) << 16);
     float* red = reinterpret_cast<float*>(sm + C::kRedOff);
     const bool two = kFp8 || nl > 1;               // the second stacked block holds anything
-    // own head and head ^ 32 (every warp follows all heads, whose channels it may have to rescale)
+    // own head and head ^ 32 (whose channels this warp may have to rescale)
     float m = -INFINITY, mo = -INFINITY, l = 0.f;
     int items = -1, reds = 0;
-    // Named barriers join the four warps (1) and the two that share heads (2, 3).  A wait that gives up
-    // does not leave the loop: every warp reaches every barrier, and the four leave together, where
+    // Named barriers join the eight warps (1) and the two that swap parts of S (2 .. 5).  A wait that
+    // gives up does not leave the loop: every warp reaches every barrier, and all leave together, where
     // they agree that one of them gave up.
     bool ok = true;
-    // Both halves' values of the own head and of head ^ 32, through one of two buffers in turn.
-    auto exchange = [&](float mine, float (&own)[2], float (&other)[2]) -> bool {
-      float* r = red + (reds & 1) * 128;
-      r[half * 64 + head] = mine;
-      ok = named_bar_and(1, 128, ok);
-      ++reds;
+    // The four parts' values of the own head and of head ^ 32 (the buffer: once all have read the last)
+    auto exchange = [&](float mine, float (&own)[4], float (&other)[4]) -> bool {
+      if (reds > 0) ok = warp_wait(BAR(C::kRedFreeB), (uint32_t)((reds - 1) & 1), abort_flag) && ok;
+      red[part * 64 + head] = mine;
+      ok = named_bar_and(1, kSoftmax, ok);
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        own[e] = r[e * 64 + head];
-        other[e] = r[e * 64 + (head ^ 32)];
+      for (int e = 0; e < 4; ++e) {
+        own[e] = red[e * 64 + head];
+        other[e] = red[e * 64 + (head ^ 32)];
       }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(BAR(C::kRedFreeB));
+      ++reds;
       return ok;
     };
     // Factor of head c (lane c of the warps that own it, or their own copy) for columns c of O^T
@@ -720,7 +746,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     int flags = 0, buf = kBufs - 1;
     ok = warp_wait(BAR(C::kInfoFullB), 0, abort_flag);
-    const bool any = named_bar_and(1, 128, ok && !(infos[0].flags & kEnd));
+    const bool any = named_bar_and(1, kSoftmax, ok && !(infos[0].flags & kEnd));
     for (int k = 0; any && !(flags & kFinal); ++k) {
       const int ri = k % kRing, s = k % C::kSBufs;
       if (++buf == kBufs) buf = 0;
@@ -737,89 +763,87 @@ __global__ void __launch_bounds__(kThreads, 1)
         m = mo = -INFINITY;
         l = 0.f;
       }
-      float x[32];
+      float x[16];
       uint8_t* pb = kFp8 ? sm + C::kPOff + (k & 1) * 8192
                          : sm + C::kKOff + buf * C::kBufBytes + 8 * kChunkBytes;   // P of this tile
       {
-        float th[32];
-        const uint32_t sa = lane_base + kSCol + (kFp8 ? s * 64 : half * 64);
-        tmem_ld32(sa + (half ^ 1) * 32, th);
-        tmem_ld32(sa + half * 32, x);
+        float th[16];
+        const uint32_t sa = lane_base + kSCol + (kFp8 ? s * 64 : half * 64) + 16 * ch;
+        tmem_ld16(sa + (half ^ 1) * 32, th);
+        tmem_ld16(sa + half * 32, x);
         tmem_wait_ld();
         tc_fence_before();
-        mbar_arrive(BAR(C::kSEmptyB + s));
+        __syncwarp();
+        if (lane == 0) mbar_arrive(BAR(C::kSEmptyB + s));
         if (!two && half == 1) {
 #pragma unroll
-          for (int j = 0; j < 32; ++j) th[j] = x[j] = 0.f;
+          for (int j = 0; j < 16; ++j) th[j] = x[j] = 0.f;
         }
         // e4m3: PV of the tile two before has read the P buffer
         if (kFp8 && k >= 2)
           ok = warp_wait(BAR(C::kPvDoneB + (k & 1)), (uint32_t)(((k - 2) >> 1) & 1), abort_flag) && ok;
-        // The other half of the warps has the other part of S: swap the entries that are not one's
-        // own, sixteen at a time, through the rows of P that the two warps will write.  A warp's
-        // second sixteen go where it has just read, so one barrier a round is enough.
+        // The warps of the other block have the other part of S: swap the entries that are not one's
+        // own with one of them, eight at a time, through a quarter of P's rows.  A warp's second eight
+        // go where it has just read, so one barrier a round is enough.
+        uint8_t* quarter = pb + (2 * pair + ch) * 2048;
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-          float4* put = reinterpret_cast<float4*>(pb + (kFp8 ? (half ^ 1 ^ r) * 4096 + pair * 2048
-                                                             : pair * 4096 + (half ^ 1 ^ r) * 2048));
-          const float4* get = reinterpret_cast<const float4*>(
-              pb + (kFp8 ? (half ^ r) * 4096 + pair * 2048 : pair * 4096 + (half ^ r) * 2048));
+          float4* put = reinterpret_cast<float4*>(quarter + (half ^ 1 ^ r) * 1024);
+          const float4* get = reinterpret_cast<const float4*>(quarter + (half ^ r) * 1024);
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            put[j * 32 + lane] = make_float4(th[16 * r + 4 * j], th[16 * r + 4 * j + 1],
-                                             th[16 * r + 4 * j + 2], th[16 * r + 4 * j + 3]);
-          named_bar_sync(2 + pair, 64);
+          for (int j = 0; j < 2; ++j)
+            put[j * 32 + lane] = make_float4(th[8 * r + 4 * j], th[8 * r + 4 * j + 1],
+                                             th[8 * r + 4 * j + 2], th[8 * r + 4 * j + 3]);
+          named_bar_sync(2 + 2 * pair + ch, 64);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
+          for (int j = 0; j < 2; ++j) {
             const float4 o = get[j * 32 + lane];
-            x[16 * r + 4 * j] += o.x;
-            x[16 * r + 4 * j + 1] += o.y;
-            x[16 * r + 4 * j + 2] += o.z;
-            x[16 * r + 4 * j + 3] += o.w;
+            x[8 * r + 4 * j] += o.x;
+            x[8 * r + 4 * j + 1] += o.y;
+            x[8 * r + 4 * j + 2] += o.z;
+            x[8 * r + 4 * j + 3] += o.w;
           }
         }
       }
-      const uint32_t valid = half ? vb : va;       // of this thread's entries 32 half + j
+      const int e0 = 32 * half + 16 * ch;          // this thread's first entry
+      const uint32_t valid = ((half ? vb : va) >> (16 * ch)) & 0xffffu;
       float mt = -INFINITY, arg = 1.f;              // log2 of the weights: arg x
       if (kFp8) {
-        // info.scale holds 2^7 times the rows' scales
-        arg = p.scale_log2 * 0.0078125f /
+        // (info.scale holds 2^7 times the rows' scales, and this table 2^-7 over the heads')
+        arg = p.scale_log2 *
               reinterpret_cast<const float*>(sm + C::kQScaleOff)[(items & 3) * kHeads + head];
-        const float4* ks4 = reinterpret_cast<const float4*>(info.scale + 32 * half);
+        const float4* ks4 = reinterpret_cast<const float4*>(info.scale + e0);
+        const float4* ls4 = reinterpret_cast<const float4*>(info.lscale + e0);
+        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float4 c = ks4[j];
+        for (int j = 0; j < 4; ++j) {                // (lscale is -inf where no entry takes part)
+          const float4 c = ks4[j], d = ls4[j];
           x[4 * j] *= c.x;
           x[4 * j + 1] *= c.y;
           x[4 * j + 2] *= c.z;
           x[4 * j + 3] *= c.w;
-        }
-        const float4* ls4 = reinterpret_cast<const float4*>(info.lscale + 32 * half);
-        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {                // (lscale is -inf where no entry takes part)
-          const float4 c = ls4[j];
-          mx[0] = fmaxf(mx[0], fmaf(arg, x[4 * j], c.x));
-          mx[1] = fmaxf(mx[1], fmaf(arg, x[4 * j + 1], c.y));
-          mx[2] = fmaxf(mx[2], fmaf(arg, x[4 * j + 2], c.z));
-          mx[3] = fmaxf(mx[3], fmaf(arg, x[4 * j + 3], c.w));
+          mx[0] = fmaxf(mx[0], fmaf(arg, x[4 * j], d.x));
+          mx[1] = fmaxf(mx[1], fmaf(arg, x[4 * j + 1], d.y));
+          mx[2] = fmaxf(mx[2], fmaf(arg, x[4 * j + 2], d.z));
+          mx[3] = fmaxf(mx[3], fmaf(arg, x[4 * j + 3], d.w));
         }
         mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
       } else {
 #pragma unroll
-        for (int j = 0; j < 32; ++j) x[j] *= p.scale_log2;
-        if (valid != 0xffffffffu) {
+        for (int j = 0; j < 16; ++j) x[j] *= p.scale_log2;
+        if (valid != 0xffffu) {
 #pragma unroll
-          for (int j = 0; j < 32; ++j) x[j] = (valid >> j) & 1u ? x[j] : -INFINITY;
+          for (int j = 0; j < 16; ++j) x[j] = (valid >> j) & 1u ? x[j] : -INFINITY;
         }
         float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int j = 0; j < 32; ++j) mx[j & 3] = fmaxf(mx[j & 3], x[j]);
+        for (int j = 0; j < 16; ++j) mx[j & 3] = fmaxf(mx[j & 3], x[j]);
         mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
       }
-      float own[2], other[2];
+      float own[4], other[4];
       if (!exchange(mt, own, other)) break;   // (all four warps, or none)
-      const float t0 = fmaxf(own[0], own[1]), t1 = fmaxf(other[0], other[1]);
+      const float t0 = fmaxf(fmaxf(own[0], own[1]), fmaxf(own[2], own[3]));
+      const float t1 = fmaxf(fmaxf(other[0], other[1]), fmaxf(other[2], other[3]));
       const float n0 = t0 > m + C::kTau ? t0 : m, n1 = t1 > mo + C::kTau ? t1 : mo;
       const uint32_t grow0 = __ballot_sync(0xffffffffu, n0 != m), grow1 = __ballot_sync(0xffffffffu, n1 != mo);
       const bool grow = (grow0 | grow1) != 0;
@@ -829,19 +853,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (grow) l *= al;
       m = n0;
       mo = n1;
-      float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int j = 0; j < 32; ++j) {
+      for (int j = 0; j < 16; ++j) {
         x[j] = kFp8 ? fast_exp2(fmaf(arg, x[j], -ref)) : fast_exp2(x[j] - ref);
-        if (kFp8 && valid != 0xffffffffu) x[j] = (valid >> j) & 1u ? x[j] : 0.f;
-        sum[j & 3] += x[j];
+        if (kFp8 && valid != 0xffffu) x[j] = (valid >> j) & 1u ? x[j] : 0.f;
       }
-      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
       if (!kFp8) {
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {              // 16-byte unit: eight entries
+        for (int u = 0; u < 2; ++u) {              // 16-byte unit: eight entries
           const float* e = x + 8 * u;
-          *reinterpret_cast<uint4*>(pb + head * 128 + (((4 * half + u) ^ (head & 7)) << 4)) =
+          *reinterpret_cast<uint4*>(pb + head * 128 + (((2 * part + u) ^ (head & 7)) << 4)) =
               make_uint4(pack_bf16x2(e[0], e[1]), pack_bf16x2(e[2], e[3]), pack_bf16x2(e[4], e[5]),
                          pack_bf16x2(e[6], e[7]));
         }
@@ -849,33 +870,28 @@ __global__ void __launch_bounds__(kThreads, 1)
         // u = 2^7 p scale (at most 2^11, as tau = 4) in f16, whose upper byte is an e5m2 number: that
         // byte rounded to nearest is the high term, what it leaves (an eighth at most, exact in f16)
         // the low term in e4m3
-        const float4* ks4 = reinterpret_cast<const float4*>(info.scale + 32 * half);
+        const float4* ks4 = reinterpret_cast<const float4*>(info.scale + e0);
+        uint32_t hw[4], lw[4];                     // one 16-byte unit: sixteen entries
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {              // 16-byte unit: sixteen entries
-          uint32_t hw[4], lw[4];
+        for (int q = 0; q < 4; ++q) {
+          const float4 c = ks4[q];
+          const float* e = x + 4 * q;
+          uint32_t h2[2], l2[2];
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const float4 c = ks4[4 * u + q];
-            const float* e = x + 16 * u + 4 * q;
-            uint32_t h2[2], l2[2];
-#pragma unroll
-            for (int z = 0; z < 2; ++z) {
-              const __half2 y = z ? __floats2half2_rn(e[2] * c.z, e[3] * c.w) : __floats2half2_rn(e[0] * c.x, e[1] * c.y);
-              h2[z] = (*reinterpret_cast<const uint32_t*>(&y) + 0x00800080u) & 0xff00ff00u;
-              const __half2 rest = __hsub2(y, *reinterpret_cast<const __half2*>(&h2[z]));
-              l2[z] = (uint32_t)__nv_cvt_halfraw2_to_fp8x2(*reinterpret_cast<const __half2_raw*>(&rest),
-                                                           __NV_SATFINITE, __NV_E4M3);
-            }
-            hw[q] = __byte_perm(h2[0], h2[1], 0x7531);
-            lw[q] = __byte_perm(l2[0], l2[1], 0x5410);
+          for (int z = 0; z < 2; ++z) {
+            const __half2 y = z ? __floats2half2_rn(e[2] * c.z, e[3] * c.w) : __floats2half2_rn(e[0] * c.x, e[1] * c.y);
+            h2[z] = (*reinterpret_cast<const uint32_t*>(&y) + 0x00800080u) & 0xff00ff00u;
+            const __half2 rest = __hsub2(y, *reinterpret_cast<const __half2*>(&h2[z]));
+            l2[z] = (uint32_t)__nv_cvt_halfraw2_to_fp8x2(*reinterpret_cast<const __half2_raw*>(&rest),
+                                                         __NV_SATFINITE, __NV_E4M3);
           }
-          uint8_t* d = pb + head * 64 + (((2 * half + u) ^ ((head >> 1) & 3)) << 4);
-          *reinterpret_cast<uint4*>(d) = make_uint4(hw[0], hw[1], hw[2], hw[3]);
-          *reinterpret_cast<uint4*>(d + 4096) = make_uint4(lw[0], lw[1], lw[2], lw[3]);
+          hw[q] = __byte_perm(h2[0], h2[1], 0x7531);
+          lw[q] = __byte_perm(l2[0], l2[1], 0x5410);
         }
+        uint8_t* d = pb + head * 64 + ((part ^ ((head >> 1) & 3)) << 4);
+        *reinterpret_cast<uint4*>(d) = make_uint4(hw[0], hw[1], hw[2], hw[3]);
+        *reinterpret_cast<uint4*>(d + 4096) = make_uint4(lw[0], lw[1], lw[2], lw[3]);
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(BAR(C::kInfoEmptyB + ri));
       if ((va & vb) != 0xffffffffu) {
         // entries that take no part: their rows hold other data or none, and a probability of zero
         // times a NaN would still be one
@@ -884,7 +900,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           while (gone) {
             const int r = 32 * e + __ffs(gone) - 1;
             gone &= gone - 1;
-            for (int u = tid; u < n_mt * C::kPerTile * 8; u += 128)   // 16-byte units of its values
+            for (int u = tid; u < n_mt * C::kPerTile * 8; u += kSoftmax)   // 16-byte units of its values
               *reinterpret_cast<uint4*>(sm + C::kKOff + buf * C::kBufBytes + (u >> 3) * kChunkBytes +
                                         r * 128 + (u & 7) * 16) = make_uint4(0, 0, 0, 0);
           }
@@ -897,7 +913,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         const uint32_t g0 = pair ? grow1 : grow0, g1 = pair ? grow0 : grow1;   // heads 0-31, 32-63
 #pragma unroll 1
-        for (int q = 0; q < 4; ++q) {
+        for (int q = 2 * ch; q < 2 * ch + 2; ++q) {
           if ((((q >= 2 ? g1 : g0) >> (16 * (q & 1))) & 0xffffu) == 0) continue;
           float f[16];
 #pragma unroll
@@ -922,45 +938,56 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       fence_proxy_async_smem();
       tc_fence_before();
-      mbar_arrive(BAR(C::kPFullB + (k & 1)));
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(BAR(C::kPFullB + (k & 1)));
+        mbar_arrive(BAR(C::kInfoEmptyB + ri));
+      }
+      // (nobody waits for the denominators)
+      float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int j = 0; j < 16; ++j) sum[j & 3] += x[j];
+      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
       if (!last) continue;
 
       // ---- epilogue: denominators, then O ----
       if (!exchange(l, own, other)) break;
-      const float ls = own[0] + own[1], lso = other[0] + other[1];
+      const float ls = (own[0] + own[1]) + (own[2] + own[3]);
+      const float lso = (other[0] + other[1]) + (other[2] + other[3]);
       constexpr float kUnit = kFp8 ? 1.f / 128.f : 1.f;
       const float inv = m == -INFINITY ? 0.f : kUnit / ls, invo = mo == -INFINITY ? 0.f : kUnit / lso;
       const int Hg = min(kHeads, a.H - g * kHeads);
       const size_t pslot = (size_t)blockIdx.x * 2 + (slot > 0 ? 1 : 0);
-      if (slot >= 0 && half == 0)
+      if (slot >= 0 && part == 0)
         p.lse[pslot * kHeads + head] = m == -INFINITY ? -INFINITY : m + __log2f(ls);
       ok = warp_wait(BAR(C::kPvDoneB + (k & 1)), (uint32_t)((k >> 1) & 1), abort_flag) && ok;
       tc_fence_after();
-      // channel of this thread in tile i of O^T
-      const int d0 = kFp8 || tid < 64 ? tid : 64 * nh + tid - 64, dstep = kFp8 ? 128 : 64;
+      // TMEM lane -> channel of tile i of O^T: d0 + i dstep; sixteen heads (columns) at a time
+      const int ln = quad * 32 + lane;
+      const int d0 = kFp8 || ln < 64 ? ln : 64 * nh + ln - 64, dstep = kFp8 ? 128 : 64;
 #pragma unroll 1
-      for (int hf = 0; hf < 2; ++hf) {
-        if (hf * 32 >= Hg) break;
-        float iv[32];
+      for (int q = 2 * ch; q < 2 * ch + 2; ++q) {
+        const int n_h = min(16, Hg - q * 16);
+        if (n_h <= 0) break;
+        float iv[16];
 #pragma unroll
-        for (int c = 0; c < 32; ++c) iv[c] = column(inv, invo, hf * 32 + c);
-        const int n_h = min(32, Hg - hf * 32);
-        const auto store = [&](int i, const float (&o)[32]) {
+        for (int c = 0; c < 16; ++c) iv[c] = column(inv, invo, q * 16 + c);
+        const auto store = [&](int i, const float (&o)[16]) {
           const int d = d0 + i * dstep;
           if (slot >= 0) {
-            float* wo = p.part + (pslot * kHeads + hf * 32) * L + d;
+            float* wo = p.part + (pslot * kHeads + q * 16) * L + d;
             if (d < L) {
 #pragma unroll
-              for (int c = 0; c < 32; ++c)
+              for (int c = 0; c < 16; ++c)
                 if (c < n_h) wo[(uint32_t)(c * L)] = o[c] * iv[c];
             }
           } else {
             // lanes 2m and 2m + 1 swap halves so that each stores two adjacent channels
             const bool up = lane & 1;
             __nv_bfloat16* ob = reinterpret_cast<__nv_bfloat16*>(a.out) +
-                                ((size_t)t * a.H + g * kHeads + hf * 32) * L + (d & ~1);
+                                ((size_t)t * a.H + g * kHeads + q * 16) * L + (d & ~1);
 #pragma unroll
-            for (int c = 0; c < 32; c += 2) {
+            for (int c = 0; c < 16; c += 2) {
               const float x0 = o[c] * iv[c], x1 = o[c + 1] * iv[c + 1];
               const float recv = __shfl_xor_sync(0xffffffffu, up ? x0 : x1, 1);
               const uint32_t pr = up ? pack_bf16x2(recv, x1) : pack_bf16x2(x0, recv);
@@ -972,23 +999,24 @@ __global__ void __launch_bounds__(kThreads, 1)
         // two tiles of O^T a round: the next one is read from TMEM while one is stored
 #pragma unroll 1
         for (int i = 0; i < n_mt; i += 2) {
-          float o0[32], o1[32];
-          tmem_ld32(lane_base + i * 64 + hf * 32, o0);
+          float o0[16], o1[16];
+          tmem_ld16(lane_base + i * 64 + q * 16, o0);
           tmem_wait_ld();
-          if (i + 1 < n_mt) tmem_ld32(lane_base + (i + 1) * 64 + hf * 32, o1);
+          if (i + 1 < n_mt) tmem_ld16(lane_base + (i + 1) * 64 + q * 16, o1);
           store(i, o0);
           tmem_wait_ld();
           if (i + 1 < n_mt) store(i + 1, o1);
         }
       }
       tc_fence_before();
-      mbar_arrive(BAR(C::kOFreeB));
+      __syncwarp();
+      if (lane == 0) mbar_arrive(BAR(C::kOFreeB));
     }
   }
 #undef BAR
   tc_fence_before();
   __syncthreads();
-  if (warp == 8) {
+  if (warp == 12) {
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);
   }
@@ -1195,7 +1223,7 @@ cudaError_t launch_latent_decode(const LatentDecodeArgs& a, bool fp8, void* work
   p.lse = reinterpret_cast<float*>(ws + w.lse);
   p.part = reinterpret_cast<float*>(ws + w.part);
   // Pages of a multiple of 64 entries: a tile is 64 consecutive rows, and one tensor-map copy brings all
-  // its whole 128-byte chunks in slot order (bf16: pairs of the two halves, so only where they pair
+  // its whole 128-byte chunks in slot order (bf16: pairs of the two halves, so only where all pair
   // up); the chunks left over come one by one.  Other pages: cp.async, any row anywhere.
   p.boxed = a.pool.ps % kKeys == 0;
   if (p.boxed) {
