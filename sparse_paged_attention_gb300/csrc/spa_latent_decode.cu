@@ -19,7 +19,13 @@
 //
 // bf16 queries sit in TMEM (the A operand of S), which leaves shared memory for three tiles of rows:
 // one is loaded, one multiplied, one waits for its softmax.  P takes the place of its own tile's
-// rotary chunk, which nobody reads any more.  TMEM: O^T 256 columns, S 128, q 128.
+// rotary chunk, which nobody reads any more.  TMEM: O^T 256 columns, S 128, q 128.  (e4m3 queries stay
+// in shared memory: there is room, and TMEM then has two S buffers, which measured faster, 194 us
+// against 217 for 48 sequences of 1 to 12,000 entries, two tokens each.)
+//
+// What bounds a tile is shared memory's 128 bytes a cycle as much as the tensor core (bf16, L = 512,
+// R = 64: the MMAs read 184 KB, the copy writes 74, the softmax moves 40: 2,330 cycles, against 2,090
+// of the MMAs alone).
 //
 //   warps 0-7   softmax: a thread has one head and a quarter of a tile's entries; it adds the other
 //               stacked block's part of S (through shared memory), then maximum and sum are in
@@ -40,8 +46,8 @@
 //
 // e4m3 rows enter the MMAs as codes.  q becomes q_hi + q_lo (e4m3, times a power of two per head);
 // the row's scale multiplies the score.  The weights p_j scale_j enter as an e5m2 and an e4m3 term:
-// the first has the exponents to keep small weights of long sequences (24 bits below the largest),
-// the second the mantissa of the large ones.
+// the first has the exponents to keep small weights of long sequences (22 bits below the largest and
+// more), the second the mantissa of the large ones.
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
@@ -72,7 +78,7 @@ struct Cfg {
   static constexpr int kPerTile = kFp8 ? 1 : 2;      // slots of 128 channels
   static constexpr int kBufBytes = kSlots * kChunkBytes;
   static constexpr int kSBufs = kFp8 ? 2 : 1;        // S buffers in TMEM (64 or 128 columns)
-  static constexpr float kTau = kFp8 ? 4.f : 8.f;    // lazy rescale threshold (log2 units)
+  static constexpr float kTau = kFp8 ? 6.f : 8.f;    // lazy rescale threshold (log2 units)
   struct Info {
     int t, flags, slot, pad;
     uint32_t valid[2];                               // bit j: entry j (32 + j) takes part
@@ -86,8 +92,8 @@ struct Cfg {
   static constexpr int kQOff = 0;
   static constexpr int kKOff = kQBytes;
   static constexpr int kPOff = kKOff + kBufs * kBufBytes;            // e4m3: two P buffers
-  static constexpr int kRedOff = kPOff + (kFp8 ? 2 * 8192 : 0);      // float [4][64]
-  static constexpr int kQScaleOff = kRedOff + 4 * kHeads * 4;    // e4m3: float [4][64]
+  static constexpr int kRedOff = kPOff + (kFp8 ? 2 * 8192 : 0);      // float [4][64], e4m3 two of them
+  static constexpr int kQScaleOff = kRedOff + (kFp8 ? 2 : 1) * 4 * kHeads * 4;    // e4m3: float [4][64]
   static constexpr int kInfoOff = kQScaleOff + (kFp8 ? 4 * kHeads * 4 : 0);
   static constexpr int kBarOff = kInfoOff + kRing * (int)sizeof(Info);
   // barriers (each in its own word; those of one kind side by side)
@@ -95,8 +101,7 @@ struct Cfg {
                        kQEmptyB = kQFullB + 1, kSFullB = kQEmptyB + 1, kSEmptyB = kSFullB + 2,
                        kPFullB = kSEmptyB + 2, kPvDoneB = kPFullB + 2, kOFreeB = kPvDoneB + 2,
                        kInfoFullB = kOFreeB + 1, kInfoEmptyB = kInfoFullB + kRing,
-                       kDrainB = kInfoEmptyB + kRing, kTokenB = kDrainB + 2, kRedFreeB = kTokenB + 1,
-                       kNumB = kRedFreeB + 1;
+                       kDrainB = kInfoEmptyB + kRing, kTokenB = kDrainB + 2, kNumB = kTokenB + 1;
   static constexpr int kMiscOff = kBarOff + kNumB * 8;   // TMEM base, abort flag, first token
   static constexpr int kSmem = kMiscOff + 12;
   static_assert(kSmem <= 232448, "shared memory budget");
@@ -162,7 +167,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(BAR(C::kInfoEmptyB + i), 14);  // two MMA, eight softmax and four q warps
     }
     mbar_init(BAR(C::kTokenB), 1);
-    mbar_init(BAR(C::kRedFreeB), 8);         // lane 0 of every softmax warp
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -390,7 +394,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // product (a scale below 2^-60 counts as that: the sums of p_j alone must stay finite)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          info.scale[lane + 32 * e] = 128.f * sc[e];
+          info.scale[lane + 32 * e] = 32.f * sc[e];
           info.lscale[lane + 32 * e] = row[e] >= 0 ? fmaxf(__log2f(fabsf(sc[e])), -60.f) : -INFINITY;
         }
       }
@@ -621,7 +625,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float qs = m > 0.f ? pow2_floor(448.f / m) : 1.f;
         if (!warp_wait(BAR(C::kQEmptyB), (uint32_t)((items & 1) ^ 1), abort_flag)) return false;
         if ((tid & 1) == 0)
-          reinterpret_cast<float*>(sm + C::kQScaleOff)[(items & 3) * kHeads + h] = 0.0078125f / qs;
+          reinterpret_cast<float*>(sm + C::kQScaleOff)[(items & 3) * kHeads + h] = 0.03125f / qs;
         // piece pc: bytes 8 pc of the row: chunk pc / 16, 16-byte unit (pc / 2) & 7, swizzled by row
         const auto put = [&](int pc, uint2 hi, uint2 lo) {
           uint8_t* d = sm + C::kQOff + (pc >> 4) * 16384 + h * 128 + ((((pc >> 1) & 7) ^ (h & 7)) << 4) +
@@ -725,19 +729,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     // gives up does not leave the loop: every warp reaches every barrier, and all leave together, where
     // they agree that one of them gave up.
     bool ok = true;
-    // The four parts' values of the own head and of head ^ 32 (the buffer: once all have read the last)
+    // The four parts' values of the own head and of head ^ 32.  (All eight warps pass a barrier between
+    // one use of a buffer and its next: e4m3 the other buffer's, bf16 that of the vote.)
     auto exchange = [&](float mine, float (&own)[4], float (&other)[4]) -> bool {
-      if (reds > 0) ok = warp_wait(BAR(C::kRedFreeB), (uint32_t)((reds - 1) & 1), abort_flag) && ok;
-      red[part * 64 + head] = mine;
+      float* r = red + (kFp8 ? (reds & 1) * 256 : 0);
+      ++reds;
+      r[part * 64 + head] = mine;
       ok = named_bar_and(1, kSoftmax, ok);
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        own[e] = red[e * 64 + head];
-        other[e] = red[e * 64 + (head ^ 32)];
+        own[e] = r[e * 64 + head];
+        other[e] = r[e * 64 + (head ^ 32)];
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(BAR(C::kRedFreeB));
-      ++reds;
       return ok;
     };
     // Factor of head c (lane c of the warps that own it, or their own copy) for columns c of O^T
@@ -809,7 +812,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t valid = ((half ? vb : va) >> (16 * ch)) & 0xffffu;
       float mt = -INFINITY, arg = 1.f;              // log2 of the weights: arg x
       if (kFp8) {
-        // (info.scale holds 2^7 times the rows' scales, and this table 2^-7 over the heads')
+        // (info.scale holds 2^5 times the rows' scales, and this table 2^-5 over the heads')
         arg = p.scale_log2 *
               reinterpret_cast<const float*>(sm + C::kQScaleOff)[(items & 3) * kHeads + head];
         const float4* ks4 = reinterpret_cast<const float4*>(info.scale + e0);
@@ -840,19 +843,29 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int j = 0; j < 16; ++j) mx[j & 3] = fmaxf(mx[j & 3], x[j]);
         mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
       }
-      float own[4], other[4];
-      if (!exchange(mt, own, other)) break;   // (all four warps, or none)
-      const float t0 = fmaxf(fmaxf(own[0], own[1]), fmaxf(own[2], own[3]));
-      const float t1 = fmaxf(fmaxf(other[0], other[1]), fmaxf(other[2], other[3]));
-      const float n0 = t0 > m + C::kTau ? t0 : m, n1 = t1 > mo + C::kTau ? t1 : mo;
-      const uint32_t grow0 = __ballot_sync(0xffffffffu, n0 != m), grow1 = __ballot_sync(0xffffffffu, n1 != mo);
+      // bf16: most tiles leave every running maximum within tau of what it was: one vote tells (and tells
+      // that the swaps are over), and the maxima are exchanged only where one head's has to move.  (With
+      // e4m3's smaller tau so many tiles would need both that the exchange alone measured faster.)
+      float own[4], other[4], al = 1.f, alo = 1.f;
+      uint32_t grow0 = 0, grow1 = 0;
+      if (kFp8 || !named_bar_and(1, kSoftmax, ok && !(mt > m + C::kTau))) {
+        if (!exchange(mt, own, other)) break;      // (all eight warps, or none)
+        const float t0 = fmaxf(fmaxf(own[0], own[1]), fmaxf(own[2], own[3]));
+        const float t1 = fmaxf(fmaxf(other[0], other[1]), fmaxf(other[2], other[3]));
+        const float n0 = t0 > m + C::kTau ? t0 : m, n1 = t1 > mo + C::kTau ? t1 : mo;
+        grow0 = __ballot_sync(0xffffffffu, n0 != m);
+        grow1 = __ballot_sync(0xffffffffu, n1 != mo);
+        al = fast_exp2(m - n0);                    // (only used where n0 is not -inf)
+        alo = fast_exp2(mo - n1);
+        if (n0 != m) l *= al;
+        else al = 1.f;
+        if (n1 == mo) alo = 1.f;
+        m = n0;
+        mo = n1;
+      }
       const bool grow = (grow0 | grow1) != 0;
       // (a head without any entry so far: everything is masked, the reference does not matter)
-      const float ref = n0 == -INFINITY ? 0.f : n0, refo = n1 == -INFINITY ? 0.f : n1;
-      const float al = fast_exp2(m - ref), alo = fast_exp2(mo - refo);
-      if (grow) l *= al;
-      m = n0;
-      mo = n1;
+      const float ref = m == -INFINITY ? 0.f : m;
 #pragma unroll
       for (int j = 0; j < 16; ++j) {
         x[j] = kFp8 ? fast_exp2(fmaf(arg, x[j], -ref)) : fast_exp2(x[j] - ref);
@@ -867,7 +880,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                          pack_bf16x2(e[6], e[7]));
         }
       } else {
-        // u = 2^7 p scale (at most 2^11, as tau = 4) in f16, whose upper byte is an e5m2 number: that
+        // u = 2^5 p scale (at most 2^11, as tau = 6) in f16, whose upper byte is an e5m2 number: that
         // byte rounded to nearest is the high term, what it leaves (an eighth at most, exact in f16)
         // the low term in e4m3
         const float4* ks4 = reinterpret_cast<const float4*>(info.scale + e0);
@@ -951,10 +964,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!last) continue;
 
       // ---- epilogue: denominators, then O ----
+      if (!kFp8) named_bar_sync(1, kSoftmax);      // (the last exchange has been read by all)
       if (!exchange(l, own, other)) break;
       const float ls = (own[0] + own[1]) + (own[2] + own[3]);
       const float lso = (other[0] + other[1]) + (other[2] + other[3]);
-      constexpr float kUnit = kFp8 ? 1.f / 128.f : 1.f;
+      constexpr float kUnit = kFp8 ? 1.f / 32.f : 1.f;
       const float inv = m == -INFINITY ? 0.f : kUnit / ls, invo = mo == -INFINITY ? 0.f : kUnit / lso;
       const int Hg = min(kHeads, a.H - g * kHeads);
       const size_t pslot = (size_t)blockIdx.x * 2 + (slot > 0 ? 1 : 0);
@@ -1024,8 +1038,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // Joins the parts of the tokens that were cut: out = sum_i 2^(lse_i - M) O_i / sum_i 2^(lse_i - M).
 // Most tokens are cut in two or three: a warp takes a head of one, with all its loads in flight at
-// once.  A token of more than kWarpParts parts (few long sequences) takes a block a head, its eight warps
-// every eighth part each, added up in warp order.  Bound by reading the parts.
+// once.  A token of more than kWarpParts parts (few long sequences) takes a block for every 128 channels
+// of a head, its eight warps every eighth part each, added up in warp order.  Bound by reading the
+// parts.
 constexpr int kMergeWarps = 8;
 constexpr int kMergeMaxCuts = 1024;
 constexpr int kWarpParts = 8;
@@ -1034,11 +1049,12 @@ __global__ void __launch_bounds__(32 * kMergeWarps)
     latent_merge_kernel(const int2* __restrict__ cut, const float* __restrict__ lse,
                         const float* __restrict__ part, __nv_bfloat16* __restrict__ out, int slices,
                         int groups, int H, int L) {
-  __shared__ __align__(16) float sum[kMergeWarps][kLatMaxDim];
+  __shared__ __align__(16) float sum[kMergeWarps][128];
   // of every cut token: the slice where it begins, its last slice, itself, units of the tokens before it
   __shared__ __align__(16) int4 item[kMergeMaxCuts];
   __shared__ int n_items, n_units;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int nq = (L + 127) >> 7;
   pdl_wait();
   if (warp == 0) {
     int n = 0, units = 0;
@@ -1046,7 +1062,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps)
       const int s = s0 + lane;
       const int2 c = s < slices ? cut[(size_t)s * groups] : make_int2(-1, 0);
       const unsigned m = __ballot_sync(0xffffffffu, c.x >= 0);
-      const int mine = c.x < 0 ? 0 : (c.y - s + 1 <= kWarpParts ? (H + kMergeWarps - 1) / kMergeWarps : H);
+      const int mine = c.x < 0 ? 0 : (c.y - s + 1 <= kWarpParts ? (H + kMergeWarps - 1) / kMergeWarps : H * nq);
       int scan = mine;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -1072,7 +1088,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps)
     const int4 it = item[lo];
     const int n = it.y - it.x + 1;
     const bool by_warp = n <= kWarpParts;
-    const int h = by_warp ? (u - it.w) * kMergeWarps + warp : u - it.w;
+    const int h = by_warp ? (u - it.w) * kMergeWarps + warp : (u - it.w) / nq;
     const int g = h / kHeads, hl = h % kHeads;
     // part i: the first slice's second slot, then every later slice's first
     const auto slot = [&](int i) { return (((size_t)(it.x + i) * groups + g) * 2 + (i == 0 ? 1 : 0)) * kHeads + hl; };
@@ -1136,37 +1152,30 @@ __global__ void __launch_bounds__(32 * kMergeWarps)
     for (int i = lane; i < n; i += 32) tot += exp2f(lse[slot(i)] - ref);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) tot += __shfl_xor_sync(0xffffffffu, tot, o);
-    float4 acc[4];
-#pragma unroll
-    for (int q = 0; q < 4; ++q) acc[q] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
+    const int d = 128 * ((u - it.w) % nq) + 4 * lane;      // (L may end inside the last 128)
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
     for (int i = warp; i < n; i += kMergeWarps) {
-      const float w = exp2f(lse[slot(i)] - ref);
-      const float* src = part + slot(i) * L;
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int d = 4 * lane + 128 * q;
-        if (d < L) {
-          const float4 v = *reinterpret_cast<const float4*>(src + d);
-          acc[q].x = fmaf(w, v.x, acc[q].x);
-          acc[q].y = fmaf(w, v.y, acc[q].y);
-          acc[q].z = fmaf(w, v.z, acc[q].z);
-          acc[q].w = fmaf(w, v.w, acc[q].w);
-        }
-      }
+      const size_t at = slot(i);
+      const float w = exp2f(lse[at] - ref);
+      const float4 v = d < L ? *reinterpret_cast<const float4*>(part + at * L + d) : make_float4(0.f, 0.f, 0.f, 0.f);
+      acc.x = fmaf(w, v.x, acc.x);
+      acc.y = fmaf(w, v.y, acc.y);
+      acc.z = fmaf(w, v.z, acc.z);
+      acc.w = fmaf(w, v.w, acc.w);
     }
-#pragma unroll
-    for (int q = 0; q < 4; ++q) *reinterpret_cast<float4*>(&sum[warp][4 * lane + 128 * q]) = acc[q];
+    *reinterpret_cast<float4*>(&sum[warp][4 * lane]) = acc;
     __syncthreads();
     const float inv = M == -INFINITY ? 0.f : 1.f / tot;
-    for (int d = 2 * threadIdx.x; d < L; d += 2 * 32 * kMergeWarps) {
+    const int e = 2 * threadIdx.x, de = 128 * ((u - it.w) % nq) + e;
+    if (threadIdx.x < 64 && de < L) {
       float x = 0.f, y = 0.f;
 #pragma unroll
       for (int w = 0; w < kMergeWarps; ++w) {
-        x += sum[w][d];
-        y += sum[w][d + 1];
+        x += sum[w][e];
+        y += sum[w][e + 1];
       }
-      *reinterpret_cast<uint32_t*>(row + d) = pack_bf16x2(x * inv, y * inv);
+      *reinterpret_cast<uint32_t*>(row + de) = pack_bf16x2(x * inv, y * inv);
     }
     __syncthreads();
   }

@@ -7,9 +7,10 @@ Bounds of an attention output, per element (``A = sum_j p_j |v_j|``, from the or
 * the output's rounding to bf16: ``2^-8 |out|``;
 * probabilities rounded to bf16 before the value product: ``2^-8 A``.  e4m3 pools: a weight
   ``w = p * scale`` enters as an e5m2 and an e4m3 term of ``u = w * 2^k`` where 2^k brings the
-  largest weight to at least 2^7: u is rounded to f16 (``2^-11 u``), the first term leaves
-  ``2^-3 u``, the second ``2^-4`` of that or half of e4m3's smallest step, so the error is at most
-  ``2^-11 w + min(2^-3 w, 2^-7 w + 2^-10 2^-7 w_max)``;
+  largest weight to at least 2^5: u is rounded to f16 (``2^-11 u``), the first term leaves
+  ``2^-3 u``, the second ``2^-4`` of that or half of e4m3's smallest step, and below 2^-17 nothing of u
+  is left, so the error is at most
+  ``2^-11 w + min(2^-3 w + 2^-17 2^-5 w_max, 2^-7 w + 2^-10 2^-5 w_max)``;
 * a score's error d (absolute, natural units) changes every p by at most a factor ``e^(2d)``:
   ``(e^(2d) - 1) A``.  d = the accumulation of W products in fp32 (tensor cores may truncate where
   they align a group: ``W 2^-23`` of the terms' sum ``qk``) + the score times log2(e) in fp32 and
@@ -59,7 +60,8 @@ def tolerance(out, terms, n_products, v=None, rows=None, row_scale=None, qmax=No
         if p.shape[1]:
             w = p * row_scale[None]
             wmax = w.max(1, keepdims=True)
-            werr = 2.0 ** -11 * w + np.minimum(2.0 ** -3 * w, 2.0 ** -7 * w + 2.0 ** -17 * wmax)
+            werr = 2.0 ** -11 * w + np.minimum(2.0 ** -3 * w + 2.0 ** -22 * wmax,
+                                               2.0 ** -7 * w + 2.0 ** -15 * wmax)
             codes = np.abs(rows[:, :out.shape[1]]) / row_scale[:, None]
             weights = werr @ codes
             d = d + abs(scale) * 2.0 ** -17 * qmax * np.abs(rows).sum(1).max()
