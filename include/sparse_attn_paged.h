@@ -426,8 +426,9 @@ int sparse_attn_latent_decode_fp8(const spa_latent_pool_t* pool, const spa_laten
  *   k_rope: bf16 [num_k] rows of rope_dim (NULL when rope_dim == 0)
  *   out:    bf16 [num_q][num_heads][v_dim], 16-byte aligned, not overlapping an input
  *   cu_q, cu_k: device int32 [num_seqs + 1], non-decreasing, within [0, num_q] and [0, num_k].  A
- *           sequence whose bounds are not is left out (its output rows keep their bytes) and sets
- *           SPA_ERR_INDEX.  Query rows of no sequence keep their bytes.
+ *           sequence whose bounds are not, or that begins before an earlier one ends, is left out
+ *           (its output rows keep their bytes) and sets SPA_ERR_INDEX.  Query rows of no sequence keep
+ *           their bytes.
  * nope_dim, v_dim: multiples of 8, 8 .. 128; rope_dim: a multiple of 8, 0 .. 64.  Pointers 16-byte
  * aligned, strides multiples of 8 elements and >= the row's width where the dimension is over 1.
  * Rows of other sequences never enter a sequence's sums, whatever they hold.  Within a sequence a

@@ -13,6 +13,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from typing import NamedTuple, Optional
 
 import torch
@@ -145,22 +146,22 @@ def load_library():
     lib.sparse_attn_indexer_logits.restype = ctypes.c_int
     lib.sparse_attn_indexer_topk.argtypes = [P, I32, I32, P, I32, P, P]
     lib.sparse_attn_indexer_topk.restype = ctypes.c_int
-    PL, PLP = ctypes.POINTER(SpaLatentPoolC), ctypes.POINTER(SpaLatentProblemC)
+    # (the latent calls take their structs by address: packed bytes, or ctypes structures by reference)
     for name in ("sparse_attn_latent_write", "sparse_attn_latent_write_fp8"):
         f = getattr(lib, name)
-        f.argtypes = [P, I64, P, I64, I32, P, P, I32, PL, P]
+        f.argtypes = [P, I64, P, I64, I32, P, P, I32, P, P]
         f.restype = ctypes.c_int
     for name in ("sparse_attn_latent_read", "sparse_attn_latent_read_fp8"):
         f = getattr(lib, name)
-        f.argtypes = [PL, I32, P, P, I32, P, I64, P]
+        f.argtypes = [P, I32, P, P, I32, P, I64, P]
         f.restype = ctypes.c_int
-    lib.sparse_attn_latent_decode_workspace_size.argtypes = [PLP, PL]
+    lib.sparse_attn_latent_decode_workspace_size.argtypes = [P, P]
     lib.sparse_attn_latent_decode_workspace_size.restype = ctypes.c_size_t
     for name in ("sparse_attn_latent_decode", "sparse_attn_latent_decode_fp8"):
         f = getattr(lib, name)
-        f.argtypes = [PL, PLP, P, P, ctypes.c_size_t, P]
+        f.argtypes = [P, P, P, P, ctypes.c_size_t, P]
         f.restype = ctypes.c_int
-    lib.sparse_attn_latent_prefill.argtypes = [ctypes.POINTER(SpaLatentPrefillC), P, P]
+    lib.sparse_attn_latent_prefill.argtypes = [P, P, P]
     lib.sparse_attn_latent_prefill.restype = ctypes.c_int
     lib.sparse_attn_paged_check_errors.argtypes = [P]
     lib.sparse_attn_paged_check_errors.restype = ctypes.c_int
@@ -550,87 +551,114 @@ class LatentPool(NamedTuple):
     scale: Optional[torch.Tensor] = None
 
 
-def _latent_pool_c(pool, fp8: bool) -> SpaLatentPoolC:
+# The C structs as packed bytes (the layouts of SpaLatentPoolC, SpaLatentProblemC, SpaLatentPrefillC): a
+# decoding step makes these calls at every layer, where building ctypes objects would take as long as
+# the kernel.
+_LATENT_POOL = struct.Struct("=QQQqiiii")
+_LATENT_PROBLEM = struct.Struct("=iiifQQQQqqqq")
+_LATENT_PREFILL = struct.Struct("=iiiiiiifQQQQqqqqqqqQQ")
+
+
+def _latent_pool(pool, fp8: bool):
+    """(packed struct, latent_dim, rope_dim, device index, block table rows) of a checked pool."""
     rows, bt, R = pool.rows, pool.block_table, int(pool.rope_dim)
     want = torch.uint8 if fp8 else torch.bfloat16
-    if rows.dtype != want:
+    if rows.dtype is not want:
         raise TypeError(f"pool rows must be {want}, got {rows.dtype}")
     if rows.dim() != 3 or not rows.is_contiguous():
         raise ValueError("pool rows must be a contiguous [num_blocks, page_size, row] tensor")
-    if bt.dtype != torch.int32 or bt.dim() != 2 or not bt.is_contiguous():
+    if bt.dtype is not torch.int32 or bt.dim() != 2 or not bt.is_contiguous():
         raise ValueError("block_table must be a contiguous int32 [num_seqs, stride] tensor")
     nb, ps, width = rows.shape
-    if fp8 and (pool.scale is None or pool.scale.dtype != torch.float32 or
-                not pool.scale.is_contiguous() or pool.scale.numel() != nb * ps):
-        raise ValueError("an e4m3 pool needs a contiguous fp32 scale of num_blocks * page_size")
+    scale = 0
+    if fp8:
+        t = pool.scale
+        if t is None or t.dtype is not torch.float32 or not t.is_contiguous() or t.numel() != nb * ps:
+            raise ValueError("an e4m3 pool needs a contiguous fp32 scale of num_blocks * page_size")
+        _same_device("pool scale", t, rows.get_device())
+        scale = t.data_ptr()
     L = width - (2 * R if fp8 else R)
     if R < 0 or L < 1:
         raise ValueError("rope_dim does not fit the pool's rows")
-    return SpaLatentPoolC(rows.data_ptr(), pool.scale.data_ptr() if fp8 else None, bt.data_ptr(),
-                          nb, ps, bt.shape[1], L, R)
+    seqs, stride = bt.shape
+    packed = _LATENT_POOL.pack(rows.data_ptr(), scale, bt.data_ptr(), nb, ps, stride, L, R)
+    return packed, L, R, rows.get_device(), seqs
 
 
-def _one_device(named):
-    """The one CUDA device of the tensors given (None entries skipped), or ValueError."""
-    dev = None
-    for name, t in named:
-        if t is None:
-            continue
-        if not t.is_cuda:
-            raise ValueError(f"{name} must be a CUDA tensor")
-        if dev is None:
-            dev = t.device
-        elif t.device != dev:
-            raise ValueError(f"{name} is on {t.device}, other arguments on {dev}")
-    if dev.index != torch.cuda.current_device():
-        raise ValueError(f"the arguments are on {dev}, which is not the current device "
-                         f"(cuda:{torch.cuda.current_device()})")
-    return dev
+def _same_device(name, t, dev: int):
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be a CUDA tensor on the pool's device" if dev >= 0 else
+                         f"{name} and the pool must be CUDA tensors on one device")
+
+
+def _current_device(dev: int):
+    """The device of the arguments has to be the current one (the library launches there)."""
+    if dev < 0:
+        raise ValueError("the arguments must be CUDA tensors")
+    if torch._C._cuda_getDevice() != dev:
+        raise ValueError(f"the arguments are on cuda:{dev}, which is not the current device")
+
+
+def _launch_stream(stream, dev: int) -> int:
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
 
 
 def _stride(t, dim) -> int:
-    """A stride in elements; 0 for an absent tensor or a dimension of one (whose stride is free)."""
-    return 0 if t is None or t.shape[dim] <= 1 else t.stride(dim)
+    """A stride in elements; 0 for a dimension of one (whose stride is free)."""
+    return 0 if t.shape[dim] <= 1 else t.stride(dim)
 
 
-def _latent_index(positions, seq_of_token, n):
-    for name, t in (("positions", positions), ("seq_of_token", seq_of_token)):
-        if t is not None and (t.dtype != torch.int32 or not t.is_contiguous() or t.numel() != n):
-            raise ValueError(f"{name} must be a contiguous int32 tensor of {n} entries")
+def _latent_index(positions, seq_of_token, n, dev):
+    """Checked positions and sequence ids of n tokens: their addresses (0: none)."""
+    if positions.dtype is not torch.int32 or not positions.is_contiguous() or positions.numel() != n:
+        raise ValueError(f"positions must be a contiguous int32 tensor of {n} entries")
+    _same_device("positions", positions, dev)
+    if seq_of_token is None:
+        return positions.data_ptr(), 0
+    if seq_of_token.dtype is not torch.int32 or not seq_of_token.is_contiguous() or \
+            seq_of_token.numel() != n:
+        raise ValueError(f"seq_of_token must be a contiguous int32 tensor of {n} entries")
+    _same_device("seq_of_token", seq_of_token, dev)
+    return positions.data_ptr(), seq_of_token.data_ptr()
 
 
-def _latent_rows(name, t, dims, width):
-    """A bf16 tensor of `dims` dimensions with unit last stride and (if given) last size."""
-    if t.dtype != torch.bfloat16 or t.dim() != dims or (t.shape[-1] > 1 and t.stride(-1) != 1) or \
-            (width is not None and t.shape[-1] != width):
+def _latent_rows(name, t, dims, width, dev):
+    """A bf16 tensor of `dims` dimensions with unit last stride and (if given) last size, on `dev`."""
+    if t.dtype is not torch.bfloat16 or t.dim() != dims or \
+            (width is not None and t.shape[-1] != width) or (t.stride(-1) != 1 and t.shape[-1] > 1):
         raise ValueError(f"{name} must be a bf16 tensor of {dims} dimensions with unit last stride"
                          + ("" if width is None else f" and {width} values a row"))
+    _same_device(name, t, dev)
+
+
+def _num_seqs(num_seqs, rows):
+    if num_seqs is None:
+        return rows
+    if int(num_seqs) > rows:
+        raise ValueError("num_seqs exceeds the block table's rows")
+    return int(num_seqs)
 
 
 def _latent_write(fp8, latent, rope, positions, pool, *, seq_of_token=None, num_seqs=None,
                   stream=None):
     lib = load_library()
-    c = _latent_pool_c(pool, fp8)
-    _latent_rows("latent", latent, 2, c.latent_dim)
-    T = int(latent.shape[0])
-    if c.rope_dim > 0:
+    packed, L, R, dev, seqs = _latent_pool(pool, fp8)
+    _latent_rows("latent", latent, 2, L, dev)
+    T = latent.shape[0]
+    rope_ptr = rope_stride = 0
+    if R > 0:
         if rope is None:
             raise ValueError("the pool's rows have a rotary part: rope is missing")
-        _latent_rows("rope", rope, 2, c.rope_dim)
+        _latent_rows("rope", rope, 2, R, dev)
         if rope.shape[0] != T:
             raise ValueError("latent and rope must have the same number of rows")
-    else:
-        rope = None
-    _latent_index(positions, seq_of_token, T)
-    _one_device((("latent", latent), ("rope", rope), ("positions", positions),
-                 ("seq_of_token", seq_of_token), ("pool rows", pool.rows),
-                 ("block_table", pool.block_table), ("pool scale", pool.scale if fp8 else None)))
-    B = int(pool.block_table.shape[0]) if num_seqs is None else int(num_seqs)
-    if B > pool.block_table.shape[0]:
-        raise ValueError("num_seqs exceeds the block table's rows")
+        rope_ptr, rope_stride = rope.data_ptr(), _stride(rope, 0)
+    pos, seq = _latent_index(positions, seq_of_token, T, dev)
+    B = _num_seqs(num_seqs, seqs)
+    _current_device(dev)
     fn = lib.sparse_attn_latent_write_fp8 if fp8 else lib.sparse_attn_latent_write
-    st = fn(latent.data_ptr(), _stride(latent, 0), _ptr(rope), _stride(rope, 0), T, positions.data_ptr(),
-            _ptr(seq_of_token), B, ctypes.byref(c), _stream(stream))
+    st = fn(latent.data_ptr(), _stride(latent, 0), rope_ptr, rope_stride, T, pos, seq, B, packed,
+            _launch_stream(stream, dev))
     if st != 0:
         raise SpaError(st, fn.__name__)
 
@@ -649,23 +677,19 @@ def sparse_attn_latent_write_fp8(latent, rope, positions, pool, **kw):
 
 def _latent_read(fp8, positions, pool, *, seq_of_token=None, num_seqs=None, out=None, stream=None):
     lib = load_library()
-    c = _latent_pool_c(pool, fp8)
-    n, width = int(positions.numel()), c.latent_dim + c.rope_dim
-    _latent_index(positions, seq_of_token, n)
+    packed, L, R, dev, seqs = _latent_pool(pool, fp8)
+    n, width = positions.numel(), L + R
+    pos, seq = _latent_index(positions, seq_of_token, n, dev)
+    _current_device(dev)
     if out is None:
         out = torch.empty((n, width), dtype=torch.bfloat16, device=pool.rows.device)
-    _latent_rows("out", out, 2, width)
-    if out.shape[0] != n:
-        raise ValueError(f"out must have {n} rows")
-    _one_device((("positions", positions), ("seq_of_token", seq_of_token),
-                 ("pool rows", pool.rows), ("block_table", pool.block_table),
-                 ("pool scale", pool.scale if fp8 else None), ("out", out)))
-    B = int(pool.block_table.shape[0]) if num_seqs is None else int(num_seqs)
-    if B > pool.block_table.shape[0]:
-        raise ValueError("num_seqs exceeds the block table's rows")
+    else:
+        _latent_rows("out", out, 2, width, dev)
+        if out.shape[0] != n:
+            raise ValueError(f"out must have {n} rows")
     fn = lib.sparse_attn_latent_read_fp8 if fp8 else lib.sparse_attn_latent_read
-    st = fn(ctypes.byref(c), n, positions.data_ptr(), _ptr(seq_of_token), B, out.data_ptr(),
-            _stride(out, 0), _stream(stream))
+    st = fn(packed, n, pos, seq, _num_seqs(num_seqs, seqs), out.data_ptr(), _stride(out, 0),
+            _launch_stream(stream, dev))
     if st != 0:
         raise SpaError(st, fn.__name__)
     return out
@@ -682,52 +706,46 @@ def sparse_attn_latent_read_fp8(positions, pool, **kw):
 
 
 def _latent_decode_args(fp8, q_latent, q_rope, pool, positions, *, scale, seq_of_token=None,
-                        num_seqs=None, out=None, workspace=None, stream=None):
-    """Checked arguments of a latent decode: (C function, its arguments, out, workspace, what the
-    arguments point into)."""
+                        num_seqs=None, out=None, workspace=None):
+    """Checked arguments of a latent decode: (C function, its arguments, device index, out, workspace)."""
     lib = load_library()
-    c = _latent_pool_c(pool, fp8)
-    _latent_rows("q_latent", q_latent, 3, c.latent_dim)
-    T, H = int(q_latent.shape[0]), int(q_latent.shape[1])
-    if c.rope_dim > 0:
+    packed, L, R, dev, seqs = _latent_pool(pool, fp8)
+    _latent_rows("q_latent", q_latent, 3, L, dev)
+    T, H = q_latent.shape[0], q_latent.shape[1]
+    qr = qr_st = qr_sh = 0
+    if R > 0:
         if q_rope is None:
             raise ValueError("the pool's rows have a rotary part: q_rope is missing")
-        _latent_rows("q_rope", q_rope, 3, c.rope_dim)
+        _latent_rows("q_rope", q_rope, 3, R, dev)
         if q_rope.shape[0] != T or q_rope.shape[1] != H:
             raise ValueError("q_latent and q_rope must have the same tokens and heads")
-    else:
-        q_rope = None
-    _latent_index(positions, seq_of_token, T)
+        qr, qr_st, qr_sh = q_rope.data_ptr(), _stride(q_rope, 0), _stride(q_rope, 1)
+    pos, seq = _latent_index(positions, seq_of_token, T, dev)
+    B = _num_seqs(num_seqs, seqs)
+    if out is not None:
+        if out.dtype is not torch.bfloat16 or tuple(out.shape) != (T, H, L) or not out.is_contiguous():
+            raise ValueError("out must be a contiguous bf16 [num_tokens, num_heads, latent_dim] tensor")
+        _same_device("out", out, dev)
+    if workspace is not None:
+        _same_device("workspace", workspace, dev)
+    _current_device(dev)
     if out is None:
-        out = torch.empty((T, H, c.latent_dim), dtype=torch.bfloat16, device=q_latent.device)
-    elif out.dtype != torch.bfloat16 or tuple(out.shape) != (T, H, c.latent_dim) or \
-            not out.is_contiguous():
-        raise ValueError("out must be a contiguous bf16 [num_tokens, num_heads, latent_dim] tensor")
-    B = int(pool.block_table.shape[0]) if num_seqs is None else int(num_seqs)
-    if B > pool.block_table.shape[0]:
-        raise ValueError("num_seqs exceeds the block table's rows")
-    dev = _one_device((("q_latent", q_latent), ("q_rope", q_rope), ("positions", positions),
-                       ("seq_of_token", seq_of_token), ("pool rows", pool.rows),
-                       ("block_table", pool.block_table),
-                       ("pool scale", pool.scale if fp8 else None), ("out", out),
-                       ("workspace", workspace)))
-    prob = SpaLatentProblemC(T, B, H, float(scale), positions.data_ptr(), _ptr(seq_of_token),
-                             q_latent.data_ptr(), _ptr(q_rope), _stride(q_latent, 0),
-                             _stride(q_latent, 1), _stride(q_rope, 0), _stride(q_rope, 1))
+        out = torch.empty((T, H, L), dtype=torch.bfloat16, device=q_latent.device)
+    prob = _LATENT_PROBLEM.pack(T, B, H, scale, pos, seq, q_latent.data_ptr(), qr, _stride(q_latent, 0),
+                                _stride(q_latent, 1), qr_st, qr_sh)
     if workspace is None:
-        nbytes = int(lib.sparse_attn_latent_decode_workspace_size(ctypes.byref(prob),
-                                                                  ctypes.byref(c)))
-        workspace = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=dev)
+        nbytes = lib.sparse_attn_latent_decode_workspace_size(prob, packed)
+        workspace = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=q_latent.device)
+        nbytes = workspace.numel()
+    else:
+        nbytes = workspace.numel() * workspace.element_size()
     fn = lib.sparse_attn_latent_decode_fp8 if fp8 else lib.sparse_attn_latent_decode
-    args = (ctypes.byref(c), ctypes.byref(prob), out.data_ptr(), workspace.data_ptr(),
-            workspace.numel() * workspace.element_size())
-    return fn, args, out, workspace, (q_latent, q_rope, pool, positions, seq_of_token, c, prob)
+    return fn, (packed, prob, out.data_ptr(), workspace.data_ptr(), nbytes), dev, out, workspace
 
 
 def _latent_decode(fp8, q_latent, q_rope, pool, positions, stream=None, **kw):
-    fn, args, out, workspace, keep = _latent_decode_args(fp8, q_latent, q_rope, pool, positions,
-                                                         stream=stream, **kw)
-    st = fn(*args, _stream(stream))
+    fn, args, dev, out, workspace = _latent_decode_args(fp8, q_latent, q_rope, pool, positions, **kw)
+    st = fn(*args, _launch_stream(stream, dev))
     if st != 0:
         raise SpaError(st, fn.__name__)
     return out
@@ -750,20 +768,19 @@ def sparse_attn_latent_decode_workspace_size(q_latent, pool, positions, *, fp8=F
                                              num_seqs=None) -> int:
     """Bytes of workspace that a latent decode of these shapes needs."""
     lib = load_library()
-    c = _latent_pool_c(pool, fp8)
-    B = int(pool.block_table.shape[0]) if num_seqs is None else int(num_seqs)
-    prob = SpaLatentProblemC(int(q_latent.shape[0]), B, int(q_latent.shape[1]), 1.0,
-                             positions.data_ptr(), None, q_latent.data_ptr(), None, 0, 0, 0, 0)
-    return int(lib.sparse_attn_latent_decode_workspace_size(ctypes.byref(prob), ctypes.byref(c)))
+    packed, _, _, _, seqs = _latent_pool(pool, fp8)
+    prob = _LATENT_PROBLEM.pack(q_latent.shape[0], _num_seqs(num_seqs, seqs), q_latent.shape[1], 1.0,
+                                positions.data_ptr(), 0, q_latent.data_ptr(), 0, 0, 0, 0, 0)
+    return int(lib.sparse_attn_latent_decode_workspace_size(prob, packed))
 
 
 def bind_latent_decode(q_latent, q_rope, pool, positions, *, fp8=False, stream=None,
                        **kw) -> BoundCall:
     """``sparse_attn_latent_decode[_fp8]`` on fixed tensors, as a zero-argument callable (workspace
     and output are allocated here once when not given)."""
-    fn, args, out, workspace, keep = _latent_decode_args(fp8, q_latent, q_rope, pool, positions,
-                                                         stream=stream, **kw)
-    call = BoundCall(fn, args, keep + (out, workspace), stream)
+    fn, args, _, out, workspace = _latent_decode_args(fp8, q_latent, q_rope, pool, positions, **kw)
+    call = BoundCall(fn, args, (q_latent, q_rope, pool, positions, kw.get("seq_of_token"), out,
+                                workspace), stream)
     call.out = out
     call.workspace = workspace
     return call
@@ -777,38 +794,41 @@ def sparse_attn_latent_prefill(q, k_nope, k_rope, v, cu_q, cu_k, *, scale, out=N
     part); ``cu_q``, ``cu_k``: int32 [num_seqs + 1] row bounds of the sequences, whose last query
     sees their last key (see the C header)."""
     lib = load_library()
-    _latent_rows("q", q, 3, None)
-    _latent_rows("k_nope", k_nope, 3, None)
-    _latent_rows("v", v, 3, None)
-    Tq, H, dk = (int(x) for x in q.shape)
-    Tk, dn, dv = int(k_nope.shape[0]), int(k_nope.shape[2]), int(v.shape[2])
+    dev = q.get_device()
+    for name, t in (("q", q), ("k_nope", k_nope), ("v", v)):
+        _latent_rows(name, t, 3, None, dev)
+    Tq, H, dk = q.shape
+    Tk, _, dn = k_nope.shape
+    dv = v.shape[2]
     dr = dk - dn
     if k_nope.shape[1] != H or v.shape[1] != H or v.shape[0] != Tk or dr < 0:
         raise ValueError("q, k_nope and v must agree in heads, keys and widths")
+    kr = kr_st = 0
     if dr > 0:
         if k_rope is None:
             raise ValueError("q has a rotary part: k_rope is missing")
-        _latent_rows("k_rope", k_rope, 2, dr)
+        _latent_rows("k_rope", k_rope, 2, dr, dev)
         if k_rope.shape[0] != Tk:
             raise ValueError("k_rope must have as many rows as k_nope")
-    else:
-        k_rope = None
+        kr, kr_st = k_rope.data_ptr(), _stride(k_rope, 0)
+    n = cu_q.numel()
     for name, t in (("cu_q", cu_q), ("cu_k", cu_k)):
-        if t.dtype != torch.int32 or t.dim() != 1 or not t.is_contiguous() or t.numel() < 1 or \
-                t.numel() != cu_q.numel():
+        if t.dtype is not torch.int32 or t.dim() != 1 or not t.is_contiguous() or n < 1 or \
+                t.numel() != n:
             raise ValueError(f"{name} must be a contiguous int32 [num_seqs + 1] tensor")
+        _same_device(name, t, dev)
+    if out is not None:
+        if out.dtype is not torch.bfloat16 or tuple(out.shape) != (Tq, H, dv) or not out.is_contiguous():
+            raise ValueError("out must be a contiguous bf16 [num_q, num_heads, v_dim] tensor")
+        _same_device("out", out, dev)
+    _current_device(dev)
     if out is None:
         out = torch.empty((Tq, H, dv), dtype=torch.bfloat16, device=q.device)
-    elif out.dtype != torch.bfloat16 or tuple(out.shape) != (Tq, H, dv) or not out.is_contiguous():
-        raise ValueError("out must be a contiguous bf16 [num_q, num_heads, v_dim] tensor")
-    _one_device((("q", q), ("k_nope", k_nope), ("k_rope", k_rope), ("v", v), ("cu_q", cu_q),
-                 ("cu_k", cu_k), ("out", out)))
-    prob = SpaLatentPrefillC(Tq, Tk, cu_q.numel() - 1, H, dn, dr, dv, float(scale), q.data_ptr(),
-                             k_nope.data_ptr(), _ptr(k_rope), v.data_ptr(), _stride(q, 0),
-                             _stride(q, 1), _stride(k_nope, 0), _stride(k_nope, 1),
-                             _stride(k_rope, 0), _stride(v, 0), _stride(v, 1),
-                             cu_q.data_ptr(), cu_k.data_ptr())
-    st = lib.sparse_attn_latent_prefill(ctypes.byref(prob), out.data_ptr(), _stream(stream))
+    prob = _LATENT_PREFILL.pack(Tq, Tk, n - 1, H, dn, dr, dv, scale, q.data_ptr(), k_nope.data_ptr(),
+                                kr, v.data_ptr(), _stride(q, 0), _stride(q, 1), _stride(k_nope, 0),
+                                _stride(k_nope, 1), kr_st, _stride(v, 0), _stride(v, 1),
+                                cu_q.data_ptr(), cu_k.data_ptr())
+    st = lib.sparse_attn_latent_prefill(prob, out.data_ptr(), _launch_stream(stream, dev))
     if st != 0:
         raise SpaError(st, "sparse_attn_latent_prefill")
     return out

@@ -57,6 +57,7 @@ struct LatentDecodeArgs {
   float scale;
   int T, H;
 };
+cudaError_t prepare_latent_decode();   // per-device one-time attributes (dynamic shared memory)
 size_t latent_decode_workspace(const LatentDecodeArgs& a, int sms);
 cudaError_t launch_latent_decode(const LatentDecodeArgs& a, bool fp8, void* workspace, int sms,
                                  cudaStream_t stream);
@@ -70,6 +71,7 @@ struct LatentPrefillArgs {
   float scale;
   int num_q, num_k, B, H, dn, dr, dv;
 };
+cudaError_t prepare_latent_prefill();
 cudaError_t launch_latent_prefill(const LatentPrefillArgs& a, int sms, cudaStream_t stream);
 cudaError_t read_and_clear_latent_prefill_error_word(int* value);
 

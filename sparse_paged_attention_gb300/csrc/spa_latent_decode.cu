@@ -1206,14 +1206,18 @@ Workspace workspace_layout(const LatentDecodeArgs& a, int sms) {
 template <bool kFp8>
 cudaError_t launch(const DecodeParams& p, cudaStream_t stream, unsigned grid) {
   using C = Cfg<kFp8>;
-  const cudaError_t e = cudaFuncSetAttribute(latent_decode_kernel<kFp8>,
-                                             cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
-  if (e != cudaSuccess) return e;
   return launch_with_pdl(latent_decode_kernel<kFp8>, dim3(grid), dim3(kThreads), C::kSmem, stream,
                          false, p);
 }
 
 }  // namespace
+
+cudaError_t prepare_latent_decode() {
+  const auto most = cudaFuncAttributeMaxDynamicSharedMemorySize;
+  cudaError_t e = cudaFuncSetAttribute(latent_decode_kernel<false>, most, Cfg<false>::kSmem);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(latent_decode_kernel<true>, most, Cfg<true>::kSmem);
+  return e;
+}
 
 size_t latent_decode_workspace(const LatentDecodeArgs& a, int sms) {
   return workspace_layout(a, sms).bytes;

@@ -1,82 +1,569 @@
-// spa_latent_prefill.cu - expanded latent attention over ragged causal sequences, first form: one
-// CTA a (query row, head), fp32 arithmetic, an online softmax over tiles of 128 keys.
+// spa_latent_prefill.cu - expanded latent attention over ragged causal sequences: per head, keys
+// [k_nope | k_rope] (k_rope shared by all heads) and values v.
+//
+//   s_ij = scale q_i . [k_nope_j | k_rope_j],   out_i = sum_{j <= i + n_k - n_q} softmax(s_i)_j v_j
+//
+// Bound by the tensor cores: 2 (d_k + d_v) flops a visible (query, key) pair and head against a few
+// bytes.  A CTA takes 256 queries of one head as two tiles of 128 and streams tiles of 128 keys:
+//
+//   S_t = Q_t K^T    tcgen05, M = 128 queries, N = 128 keys, both operands in shared memory
+//   O_t += P_t V     M = 128 queries, N = d_v, A = P_t from TMEM (bf16, in the columns of its own S_t)
+//
+// TMEM holds S_0, S_1, O_0, O_1 (128 columns each, fp32): while the softmax works on one query tile, the
+// tensor core works on the other.
+//
+//   warps 0-3, 4-7   softmax of tile 0, 1: a thread has one query's row of S: maximum, exponentials and
+//                    sum without any exchange; P back to TMEM; O rescaled only when a row's maximum has
+//                    grown by more than 2^8; epilogue
+//   warp 8           MMAs of S;  warp 9: MMAs of O (apart, so that neither one's waits keep the tensor
+//                    core idle)
+//   warp 10          schedule and tensor-map copies: Q once an item; K (nope) and V in turn through a ring
+//                    of three 32 KB slots, K (rope) through two of 16 KB
+//
+// Items (256 queries, head) go to CTAs statically, in an order that starts with the last queries (the
+// longest rows) of all heads and folds back and forth over the CTAs, so that long and short items add up
+// alike.  The copies zero-fill what lies past a width (any multiple of 8); rows past a sequence's end are
+// other data: masked as keys, blanked as values, not stored as queries.
 #include "spa_latent.h"
+#include "spa_launch.h"
 
 namespace spa {
 
 namespace {
 
-constexpr int kTile = 128;
+constexpr int kTile = 128;                       // queries of a tile, keys of a step
+constexpr int kChunk = kTile * 128;              // 128 rows of 64 bf16 values
+constexpr int kPairs = 3, kRopes = 2;            // ring slots
+constexpr int kThreads = 352;
+constexpr int kItems = 2;                        // item infos in flight
+constexpr int kTmemCols = 512;
+constexpr int kOCol = 256;
+constexpr float kTau = 8.f;                      // lazy rescale threshold (log2 units)
 
-__device__ __forceinline__ float bf(const uint8_t* p, int i) {
-  return __uint_as_float((uint32_t)reinterpret_cast<const uint16_t*>(p)[i] << 16);
-}
+constexpr int kQOff = 0;                                     // [2 tiles][3 chunks]
+constexpr int kPairOff = kQOff + 6 * kChunk;
+constexpr int kRopeOff = kPairOff + kPairs * 2 * kChunk;
+constexpr int kInfoOff = kRopeOff + kRopes * kChunk;
 
-// Sequence bounds of sequence b; false (and the error word) when they are not usable.
-__device__ __forceinline__ bool bounds(const LatentPrefillArgs& a, int b, int& q0, int& q1, int& k0,
-                                       int& k1) {
-  q0 = a.cu_q[b], q1 = a.cu_q[b + 1], k0 = a.cu_k[b], k1 = a.cu_k[b + 1];
-  return 0 <= q0 && q0 <= q1 && q1 <= a.num_q && 0 <= k0 && k0 <= k1 && k1 <= a.num_k;
-}
+struct Item {
+  int q0, n;          // first query row, queries of the item (0: no more items)
+  int k0, nk;         // first key row, keys of the sequence
+  int pos;            // position of the item's first query (may be negative: it sees no key)
+  int head;
+  int steps[2];       // key tiles of query tile 0, 1
+};
 
-__global__ void __launch_bounds__(kTile) latent_prefill_simple(const LatentPrefillArgs a) {
-  __shared__ float q[192], pr[kTile], red[4];
-  const int t = blockIdx.x / a.H, h = blockIdx.x % a.H, tid = threadIdx.x;
-  int q0 = 0, q1 = 0, k0 = 0, k1 = 0;
-  bool own = false;
-  for (int b = 0; b < a.B && !own; ++b) {
-    const bool ok = bounds(a, b, q0, q1, k0, k1);
-    if (!ok && tid == 0) flag_error(SPA_ERR_INDEX);
-    own = ok && q0 <= t && t < q1;
-  }
-  if (!own) return;
-  const uint8_t* qr = a.q + t * a.q_st + h * a.q_sh;
-  for (int i = tid; i < a.dn + a.dr; i += kTile) q[i] = bf(qr, i);
-  const long long n = (long long)(t - q0) + 1 + (k1 - k0) - (q1 - q0);   // keys seen
-  float m = -INFINITY, l = 0.f, o = 0.f;
-  for (long long j0 = 0; j0 < n; j0 += kTile) {
-    __syncthreads();
-    const long long j = k0 + j0 + tid;
-    float s = -INFINITY;
-    if (j0 + tid < n) {
-      const uint8_t* kn = a.k_nope + j * a.kn_st + h * a.kn_sh;
-      const uint8_t* kr = a.k_rope + j * a.kr_st;
-      s = 0.f;
-      for (int i = 0; i < a.dn; ++i) s += q[i] * bf(kn, i);
-      for (int i = 0; i < a.dr; ++i) s += q[a.dn + i] * bf(kr, i);
-      s *= a.scale;
+enum {
+  B_QFULL = 0, B_QEMPTY, B_PFULL_SLOT, B_PEMPTY_SLOT = B_PFULL_SLOT + kPairs,
+  B_RFULL = B_PEMPTY_SLOT + kPairs, B_REMPTY = B_RFULL + kRopes, B_SFULL = B_REMPTY + kRopes,
+  B_PREADY = B_SFULL + 2, B_PVDONE = B_PREADY + 2, B_OFREE = B_PVDONE + 2, B_IFULL = B_OFREE + 2,
+  B_IEMPTY = B_IFULL + kItems, B_DRAIN = B_IEMPTY + kItems, B_COUNT = B_DRAIN + 2
+};
+constexpr int kBarOff = kInfoOff + kItems * (int)sizeof(Item);
+constexpr int kMiscOff = kBarOff + B_COUNT * 8;
+constexpr int kSmem = kMiscOff + 8;
+static_assert(kSmem <= 232448, "shared memory budget");
+
+struct PrefillParams {
+  CUtensorMap q, kn, kr, v;
+  LatentPrefillArgs a;
+  float scale_log2;        // |scale| log2(e)
+  int negate;              // scale < 0
+};
+
+__global__ void __launch_bounds__(kThreads, 1)
+    latent_prefill_kernel(const __grid_constant__ PrefillParams p) {
+  extern __shared__ __align__(1024) uint8_t sm[];
+  const uint32_t sb = smem_u32(sm);
+  const int warp = (int)warp_uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + kMiscOff + 4);
+  Item* items = reinterpret_cast<Item*>(sm + kInfoOff);
+#define BAR(i) (sb + (uint32_t)kBarOff + 8u * (uint32_t)(i))
+  if (threadIdx.x == 0) {
+    mbar_init(BAR(B_QFULL), 1);
+    mbar_init(BAR(B_QEMPTY), 1);
+    for (int i = 0; i < kPairs; ++i) {
+      mbar_init(BAR(B_PFULL_SLOT + i), 1);
+      mbar_init(BAR(B_PEMPTY_SLOT + i), 1);
     }
-    float mx = s;
-    for (int k = 16; k > 0; k >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, k));
-    if ((tid & 31) == 0) red[tid >> 5] = mx;
-    __syncthreads();
-    const float mn = fmaxf(m, fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3])));
-    const float ref = mn == -INFINITY ? 0.f : mn;
-    const float c = expf(m - ref);
-    pr[tid] = j0 + tid < n ? expf(s - ref) : 0.f;
-    __syncthreads();
-    l *= c;
-    o *= c;
-    for (int k = 0; k < kTile && j0 + k < n; ++k) {
-      l += pr[k];
-      if (tid < a.dv) o += pr[k] * bf(a.v + (k0 + j0 + k) * a.v_st + h * a.v_sh, tid);
+    for (int i = 0; i < kRopes; ++i) {
+      mbar_init(BAR(B_RFULL + i), 1);
+      mbar_init(BAR(B_REMPTY + i), 1);
     }
-    m = mn;
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(BAR(B_SFULL + i), 1);
+      mbar_init(BAR(B_PREADY + i), 4);       // lane 0 of the tile's four softmax warps
+      mbar_init(BAR(B_PVDONE + i), 1);
+      mbar_init(BAR(B_OFREE + i), 4);
+      mbar_init(BAR(B_DRAIN + i), 1);
+    }
+    for (int i = 0; i < kItems; ++i) {
+      mbar_init(BAR(B_IFULL + i), 1);
+      mbar_init(BAR(B_IEMPTY + i), 10);      // eight softmax and two MMA warps
+    }
+    *abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (tid < a.dv)
-    reinterpret_cast<__nv_bfloat16*>(a.out)[((size_t)t * a.H + h) * a.dv + tid] =
-        __float2bfloat16_rn(n <= 0 ? 0.f : o / l);
+  if (warp == 8) tmem_alloc(sb + kMiscOff, kTmemCols);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = warp_uniform(*reinterpret_cast<volatile uint32_t*>(sm + kMiscOff));
+  pdl_launch_dependents();
+  pdl_wait();   // nothing global before the grid before this one is done
+
+  const LatentPrefillArgs& a = p.a;
+  const int nkc = (a.dn + 63) >> 6, nvc = (a.dv + 63) >> 6;   // 64-wide chunks of k_nope, v
+  const bool rope = a.dr > 0;
+
+  // Item info n of this CTA (0, 1, ..), read by every consumer warp; false when the CTA gives up.
+  const auto next_item = [&](int n, Item& it) -> bool {
+    const int s = n % kItems;
+    if (!warp_wait(BAR(B_IFULL + s), (uint32_t)((n / kItems) & 1), abort_flag)) return false;
+    const volatile int* src = reinterpret_cast<const volatile int*>(items + s);
+    int* dst = reinterpret_cast<int*>(&it);
+#pragma unroll
+    for (int i = 0; i < (int)(sizeof(Item) / 4); ++i) dst[i] = (int)warp_uniform((uint32_t)src[i]);
+    __syncwarp();
+    if (lane == 0) mbar_arrive(BAR(B_IEMPTY + s));
+    return true;
+  };
+
+  if (warp == 10) {
+    // ================================ schedule and copies =================================
+    // Tiles of 256 queries of the sequences b0 + lane, their bounds, and the inclusive sum over the lanes.
+    // A sequence with bad bounds has none, nor has one that begins before an earlier sequence's end (no
+    // two items write one row).  `highest`: the largest bound of the sequences before b0.
+    const auto tiles_at = [&](int b0, int& highest, int& q0, int& q1, int& k0, int& k1, int& mine, bool& bad) {
+      const int b = b0 + lane;
+      q0 = q1 = k0 = k1 = 0;
+      bad = false;
+      if (b < a.B) {
+        q0 = __ldg(a.cu_q + b), q1 = __ldg(a.cu_q + b + 1);
+        k0 = __ldg(a.cu_k + b), k1 = __ldg(a.cu_k + b + 1);
+      }
+      int top = b < a.B ? q0 : 0;              // largest bound up to and with this sequence's first
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, top, o);
+        if (lane >= o) top = max(top, x);
+      }
+      top = max(top, highest);
+      if (b < a.B)
+        bad = q0 < top || q1 < q0 || q1 > a.num_q || k0 < 0 || k1 < k0 || k1 > a.num_k;
+      mine = bad ? 0 : (q1 - q0 + 2 * kTile - 1) / (2 * kTile);
+      int scan = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, scan, o);
+        if (lane >= o) scan += x;
+      }
+      highest = __shfl_sync(0xffffffffu, top, 31);
+      return scan;
+    };
+    int total = 0;
+    for (int b0 = 0, highest = 0; b0 < a.B; b0 += 32) {
+      int q0, q1, k0, k1, mine;
+      bool bad;
+      const int scan = tiles_at(b0, highest, q0, q1, k0, k1, mine, bad);
+      if (bad) flag_error(SPA_ERR_INDEX);
+      total += __shfl_sync(0xffffffffu, scan, 31);
+    }
+    const long long n_items = (long long)total * a.H;
+    int n = 0, pair = 0, rp = 0, qs = 0;
+    uint32_t pair_ph = 0, rope_ph = 0;
+    int pair_fills = 0, rope_fills = 0;
+    bool ok = true;
+    for (; ok; ++n) {
+      // the n-th item of this CTA: rounds of gridDim items, every other one backwards
+      const long long i = (long long)n * gridDim.x + ((n & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+      Item it = {};
+      if (i < n_items) {
+        const int tile = total - 1 - (int)(i / a.H);
+        it.head = (int)(i % a.H);
+        int before = 0;                      // the sequence that holds the tile
+        for (int b0 = 0, highest = 0; b0 < a.B; b0 += 32) {
+          int q0, q1, k0, k1, mine;
+          bool bad;
+          const int scan = tiles_at(b0, highest, q0, q1, k0, k1, mine, bad);
+          const unsigned m = __ballot_sync(0xffffffffu, tile < before + scan);
+          if (m) {
+            const int k = __ffs(m) - 1;
+            const int first = before + __shfl_sync(0xffffffffu, scan - mine, k);
+            q0 = __shfl_sync(0xffffffffu, q0, k);
+            q1 = __shfl_sync(0xffffffffu, q1, k);
+            k0 = __shfl_sync(0xffffffffu, k0, k);
+            k1 = __shfl_sync(0xffffffffu, k1, k);
+            const int r = (tile - first) * 2 * kTile;
+            it.q0 = q0 + r;
+            it.n = min(2 * kTile, q1 - q0 - r);
+            it.k0 = k0;
+            it.nk = k1 - k0;
+            it.pos = it.nk - (q1 - q0) + r;
+            break;
+          }
+          before += __shfl_sync(0xffffffffu, scan, 31);
+        }
+        // (position of a tile's last query, and the key tiles up to it)
+        const int last0 = it.pos + min(it.n, kTile) - 1, last1 = it.pos + it.n - 1;
+        it.steps[0] = last0 >= 0 ? last0 / kTile + 1 : 0;
+        it.steps[1] = it.n > kTile && last1 >= 0 ? last1 / kTile + 1 : 0;
+      }
+      const int s = n % kItems;
+      ok = warp_wait(BAR(B_IEMPTY + s), (uint32_t)(((n / kItems) & 1) ^ 1), abort_flag);
+      if (!ok) break;
+      if (lane == 0) {
+        items[s] = it;
+        __threadfence_block();
+        mbar_arrive(BAR(B_IFULL + s));
+      }
+      __syncwarp();
+      if (it.n == 0) break;
+      const int steps = max(it.steps[0], it.steps[1]);
+      if (steps == 0) continue;
+      const bool lead = elect_one();
+      // the item's queries
+      ok = warp_wait(BAR(B_QEMPTY), (uint32_t)((qs & 1) ^ 1), abort_flag);
+      if (!ok) break;
+      ++qs;
+      if (lead) {
+        const int nt = it.steps[1] > 0 ? 2 : 1, nc = nkc + (rope ? 1 : 0);
+        mbar_arrive_expect_tx(BAR(B_QFULL), (uint32_t)(nt * nc * kChunk));
+        for (int t = 0; t < nt; ++t)
+          for (int c = 0; c < nc; ++c)
+            tma_box3(sb + kQOff + (t * 3 + (c < nkc ? c : 2)) * kChunk, &p.q, c < nkc ? 64 * c : a.dn,
+                     it.head, it.q0 + t * kTile, BAR(B_QFULL));
+      }
+      __syncwarp();
+      for (int j = 0; j < steps && ok; ++j) {
+        const int row = it.k0 + j * kTile;
+        for (int kv = 0; kv < 2 && ok; ++kv) {
+          ok = warp_wait(BAR(B_PEMPTY_SLOT + pair), pair_ph ^ 1, abort_flag);
+          if (!ok) break;
+          if (lead) {
+            const uint32_t full = BAR(B_PFULL_SLOT + pair), dst = sb + kPairOff + pair * 2 * kChunk;
+            const int nc = kv ? nvc : nkc;
+            mbar_arrive_expect_tx(full, (uint32_t)(nc * kChunk));
+            for (int c = 0; c < nc; ++c)
+              tma_box3(dst + c * kChunk, kv ? &p.v : &p.kn, 64 * c, it.head, row, full);
+          }
+          __syncwarp();
+          ++pair_fills;
+          if (++pair == kPairs) {
+            pair = 0;
+            pair_ph ^= 1;
+          }
+          if (kv == 0 && rope) {
+            ok = warp_wait(BAR(B_REMPTY + rp), rope_ph ^ 1, abort_flag);
+            if (!ok) break;
+            if (lead) {
+              mbar_arrive_expect_tx(BAR(B_RFULL + rp), (uint32_t)kChunk);
+              tma_box3(sb + kRopeOff + rp * kChunk, &p.kr, 0, 0, row, BAR(B_RFULL + rp));
+            }
+            __syncwarp();
+            ++rope_fills;
+            if (++rp == kRopes) {
+              rp = 0;
+              rope_ph ^= 1;
+            }
+          }
+        }
+      }
+    }
+    // copies in flight must land before the CTA ends (at once after a normal run)
+    if (lane == 0) {
+      if (qs > 0) mbar_wait_drain(BAR(B_QFULL), (uint32_t)((qs - 1) & 1));
+      for (int f = max(0, pair_fills - kPairs); f < pair_fills; ++f)
+        mbar_wait_drain(BAR(B_PFULL_SLOT + f % kPairs), (uint32_t)((f / kPairs) & 1));
+      for (int f = max(0, rope_fills - kRopes); f < rope_fills; ++f)
+        mbar_wait_drain(BAR(B_RFULL + f % kRopes), (uint32_t)((f / kRopes) & 1));
+    }
+    __syncwarp();
+  } else if (warp == 8) {
+    // ================================= MMAs of S ==========================================
+    // (bit 13 of the instruction descriptor negates A: a negative scale)
+    const uint32_t idS = idesc_bf16(kTile, kTile, 0, 0) | (p.negate ? 1u << 13 : 0u);
+    const uint64_t dq0 = sdesc(sb + kQOff, 16, 1024), dk0 = sdesc(sb + kPairOff, 16, 1024);
+    const uint64_t dr0 = sdesc(sb + kRopeOff, 16, 1024);
+    const bool lead = elect_one();
+    int seq = 0, rp = 0, qs = 0;                 // pairs seen (K and V), rope slots, items with queries
+    uint32_t rope_ph = 0;
+    int done[2] = {0, 0};                        // S issued of tile 0, 1
+    bool ok = true;
+    Item it;
+    for (int n = 0; ok && (ok = next_item(n, it)) && it.n > 0; ++n) {
+      const int steps = max(it.steps[0], it.steps[1]);
+      if (steps == 0) continue;
+      if (!(ok = warp_wait(BAR(B_QFULL), (uint32_t)(qs & 1), abort_flag))) break;
+      ++qs;
+      for (int j = 0; j < steps && ok; ++j, seq += 2) {
+        const int sl = seq % kPairs;
+        ok = warp_wait(BAR(B_PFULL_SLOT + sl), (uint32_t)((seq / kPairs) & 1), abort_flag);
+        if (ok && rope) ok = warp_wait(BAR(B_RFULL + rp), rope_ph, abort_flag);
+        if (!ok) break;
+        const uint64_t dk = desc_add(dk0, sl * 2 * kChunk), dr = desc_add(dr0, rp * kChunk);
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          if (j >= it.steps[t]) continue;
+          // S and P of the step before share these columns: its PV has to be over
+          if (done[t] > 0) ok = warp_wait(BAR(B_PVDONE + t), (uint32_t)((done[t] - 1) & 1), abort_flag);
+          if (!ok) break;
+          ++done[t];
+          tc_fence_after();
+          if (lead) {
+            const uint32_t dS = tmem + t * kTile;
+            const uint64_t dq = desc_add(dq0, t * 3 * kChunk);
+            for (int c = 0; c < nkc; ++c) {
+              const int ks = (min(64, a.dn - 64 * c) + 15) >> 4;
+#pragma unroll
+              for (int st = 0; st < 4; ++st)
+                if (st < ks)
+                  mma_bf16(dS, desc_add(dq, c * kChunk + st * 32), desc_add(dk, c * kChunk + st * 32), idS,
+                           (c | st) != 0);
+            }
+            if (rope) {
+              const int ks = (a.dr + 15) >> 4;
+#pragma unroll
+              for (int st = 0; st < 4; ++st)
+                if (st < ks)
+                  mma_bf16(dS, desc_add(dq, 2 * kChunk + st * 32), desc_add(dr, st * 32), idS, 1u);
+            }
+            mma_commit(BAR(B_SFULL + t));
+          }
+          __syncwarp();
+        }
+        if (!ok) break;
+        if (lead) {
+          mma_commit(BAR(B_PEMPTY_SLOT + sl));
+          if (rope) mma_commit(BAR(B_REMPTY + rp));
+          if (j == steps - 1) mma_commit(BAR(B_QEMPTY));
+        }
+        __syncwarp();
+        if (rope && ++rp == kRopes) {
+          rp = 0;
+          rope_ph ^= 1;
+        }
+      }
+    }
+    // nothing may still write TMEM when it is released
+    if (lead) {
+      mma_commit(BAR(B_DRAIN));
+      mbar_wait_drain(BAR(B_DRAIN), 0);
+    }
+    __syncwarp();
+  } else if (warp == 9) {
+    // ================================= MMAs of O ==========================================
+    const int nv = (a.dv + 15) & ~15;
+    const uint32_t idO = idesc_bf16(kTile, nv, 0, 1);
+    const uint64_t dv0 = sdesc(sb + kPairOff, kChunk, 1024);         // MN-major: 64 values a chunk
+    const bool lead = elect_one();
+    int seq = 1;
+    int done[2] = {0, 0}, opened[2] = {0, 0};
+    bool ok = true;
+    Item it;
+    for (int n = 0; ok && (ok = next_item(n, it)) && it.n > 0; ++n) {
+      const int steps = max(it.steps[0], it.steps[1]);
+      for (int j = 0; j < steps && ok; ++j, seq += 2) {
+        const int sl = seq % kPairs;
+        ok = warp_wait(BAR(B_PFULL_SLOT + sl), (uint32_t)((seq / kPairs) & 1), abort_flag);
+        if (!ok) break;
+        const uint64_t dv = desc_add(dv0, sl * 2 * kChunk);
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          if (j >= it.steps[t]) continue;
+          ok = warp_wait(BAR(B_PREADY + t), (uint32_t)(done[t] & 1), abort_flag);
+          if (ok && j == 0) {                    // O of the item before has been stored
+            ok = warp_wait(BAR(B_OFREE + t), (uint32_t)((opened[t] & 1) ^ 1), abort_flag);
+            ++opened[t];
+          }
+          if (!ok) break;
+          ++done[t];
+          tc_fence_after();
+          if (lead) {
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk)       // 16 keys a step
+              mma_bf16_ts(tmem + kOCol + t * kTile, tmem + t * kTile + kk * 8, desc_add(dv, kk * 2048), idO,
+                          (j > 0 || kk > 0) ? 1u : 0u);
+            mma_commit(BAR(B_PVDONE + t));
+          }
+          __syncwarp();
+        }
+        if (!ok) break;
+        if (lead) mma_commit(BAR(B_PEMPTY_SLOT + sl));
+        __syncwarp();
+      }
+    }
+    if (lead) {
+      mma_commit(BAR(B_DRAIN + 1));
+      mbar_wait_drain(BAR(B_DRAIN + 1), 0);
+    }
+    __syncwarp();
+  } else {
+    // ================================ softmax and epilogue ================================
+    const int t = warp >> 2, row = (warp & 3) * 32 + lane;      // query tile, row in it == TMEM lane
+    const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    const uint32_t sc = lanes + t * kTile, oc = lanes + kOCol + t * kTile;
+    const float s2 = p.scale_log2;
+    int done = 0;                                // steps of this tile done
+    int seq = 1;                                 // V slots seen
+    bool ok = true;
+    Item it;
+    for (int n = 0; ok && (ok = next_item(n, it)) && it.n > 0; ++n) {
+      const int steps = it.steps[t], all_steps = max(it.steps[0], it.steps[1]);
+      const int pos = it.pos + t * kTile + row;  // this query sees keys 0 .. pos
+      const int pos_min = it.pos + t * kTile + (warp & 3) * 32;
+      float m = -INFINITY, l = 0.f;
+      for (int j = 0; j < steps; ++j, ++done) {
+        if (!(ok = warp_wait(BAR(B_SFULL + t), (uint32_t)(done & 1), abort_flag))) break;
+        tc_fence_after();
+        const int left = pos - j * kTile;        // keys 0 .. left of the tile are visible
+        const bool masked = pos_min - j * kTile < kTile - 1;
+        float mx = -INFINITY;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          float x[32];
+          tmem_ld32(sc + 32 * c, x);
+          tmem_wait_ld();
+          if (masked) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) x[i] = 32 * c + i <= left ? x[i] : -INFINITY;
+          }
+          float y[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+          for (int i = 4; i < 32; ++i) y[i & 3] = fmaxf(y[i & 3], x[i]);
+          mx = fmaxf(mx, fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3])));
+        }
+        const float mt = mx == -INFINITY ? -INFINITY : mx * s2;
+        const float mn = mt > m + kTau ? mt : m;
+        const bool grow = __any_sync(0xffffffffu, mn != m);
+        const float ref = mn == -INFINITY ? 0.f : mn;
+        const float al = fast_exp2(m - ref);
+        m = mn;
+        l *= al;
+        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          float x[32];
+          tmem_ld32(sc + 32 * c, x);
+          tmem_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 32; ++i) x[i] = fast_exp2(fmaf(x[i], s2, -ref));
+          if (masked) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) x[i] = 32 * c + i <= left ? x[i] : 0.f;
+          }
+          uint32_t w[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) w[i] = pack_bf16x2(x[2 * i], x[2 * i + 1]);
+          // (columns 16c .. of S have been read: chunk c of P takes half of chunk c's columns or less)
+          tmem_st16(sc + 16 * c, w);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) sum[i & 3] += x[i];
+        }
+        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        if (grow && j > 0) {
+          // some row's maximum moved: rescale this warp's rows of O once PV of the step before is done
+          if (!(ok = warp_wait(BAR(B_PVDONE + t), (uint32_t)((done - 1) & 1), abort_flag))) break;
+          tc_fence_after();
+#pragma unroll 1
+          for (int c = 0; c < nvc * 2; ++c) {
+            float o[32];
+            tmem_ld32(oc + 32 * c, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] *= al;
+            tmem_st32(oc + 32 * c, o);
+          }
+        }
+        tmem_wait_st();
+        const int keys = it.nk - j * kTile;      // keys of the tile that are the sequence's
+        if (keys < kTile) {
+          // values of other rows: a probability of zero times a NaN would still be one.  (Both tiles'
+          // warps write the same zeros before their own PV.)
+          const int sq = seq + 2 * j, sl = sq % kPairs;
+          if (!(ok = warp_wait(BAR(B_PFULL_SLOT + sl), (uint32_t)((sq / kPairs) & 1), abort_flag))) break;
+          for (int u = (threadIdx.x & 127); u < (kTile - keys) * nvc * 8; u += 128) {
+            const int r = keys + u / (nvc * 8), w = u % (nvc * 8);
+            *reinterpret_cast<uint4*>(sm + kPairOff + sl * 2 * kChunk + (w >> 3) * kChunk + r * 128 +
+                                      (w & 7) * 16) = make_uint4(0, 0, 0, 0);
+          }
+          fence_proxy_async_smem();
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(BAR(B_PREADY + t));
+      }
+      if (!ok) break;
+      seq += 2 * all_steps;
+      // ---- epilogue ----
+      const bool mine = t * kTile + row < it.n;
+      uint4* dst = reinterpret_cast<uint4*>(a.out + ((size_t)(it.q0 + t * kTile + row) * a.H + it.head) * a.dv * 2);
+      const int nu = a.dv >> 3;                  // 16-byte units of a row
+      if (steps == 0) {
+        if (mine)
+          for (int u = 0; u < nu; ++u) dst[u] = make_uint4(0, 0, 0, 0);
+        continue;
+      }
+      if (!(ok = warp_wait(BAR(B_PVDONE + t), (uint32_t)((done - 1) & 1), abort_flag))) break;
+      tc_fence_after();
+      const float inv = m == -INFINITY ? 0.f : 1.f / l;
+#pragma unroll 1
+      for (int c = 0; c < nvc * 2; ++c) {
+        float o[32];
+        tmem_ld32(oc + 32 * c, o);
+        tmem_wait_ld();
+        if (mine) {
+#pragma unroll
+          for (int u = 0; u < 4; ++u)
+            if (4 * c + u < nu)
+              dst[4 * c + u] = make_uint4(pack_bf16x2(o[8 * u] * inv, o[8 * u + 1] * inv),
+                                          pack_bf16x2(o[8 * u + 2] * inv, o[8 * u + 3] * inv),
+                                          pack_bf16x2(o[8 * u + 4] * inv, o[8 * u + 5] * inv),
+                                          pack_bf16x2(o[8 * u + 6] * inv, o[8 * u + 7] * inv));
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(BAR(B_OFREE + t));
+    }
+  }
+#undef BAR
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 8) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
 }
 
 }  // namespace
 
-cudaError_t launch_latent_prefill(const LatentPrefillArgs& a, int, cudaStream_t stream) {
-  const long long blocks = (long long)a.num_q * a.H;
-  if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-  latent_prefill_simple<<<(unsigned)blocks, kTile, 0, stream>>>(a);
-  return cudaGetLastError();
+cudaError_t prepare_latent_prefill() {
+  return cudaFuncSetAttribute(latent_prefill_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
 }
 
+cudaError_t launch_latent_prefill(const LatentPrefillArgs& a, int sms, cudaStream_t stream) {
+  PrefillParams p = {};
+  p.a = a;
+  p.scale_log2 = fabsf(a.scale) * 1.4426950408889634f;
+  p.negate = a.scale < 0.f;
+  if (!encode_bf16_3d(&p.q, a.q, a.dn + a.dr, a.H, a.q_sh, a.num_q, a.q_st, 1, kTile))
+    return cudaErrorInvalidValue;
+  if (a.num_k > 0) {   // (without keys every output row is zero and none of these is used)
+    if (!encode_bf16_3d(&p.kn, a.k_nope, a.dn, a.H, a.kn_sh, a.num_k, a.kn_st, 1, kTile) ||
+        !encode_bf16_3d(&p.v, a.v, a.dv, a.H, a.v_sh, a.num_k, a.v_st, 1, kTile))
+      return cudaErrorInvalidValue;
+    if (a.dr > 0 && !encode_bf16_3d(&p.kr, a.k_rope, a.dr, 1, 0, a.num_k, a.kr_st, 1, kTile))
+      return cudaErrorInvalidValue;
+  }
+  // at most this many items; a CTA without one ends at once
+  const long long items = ((long long)a.num_q / (2 * kTile) + a.B + 1) * a.H;
+  const unsigned grid = (unsigned)(items < sms ? items : sms);
+  return launch_with_pdl(latent_prefill_kernel, dim3(grid), dim3(kThreads), kSmem, stream, 2LL * grid <= sms,
+                         p);
+}
+
+// This translation unit's copy of the device error word (see spa_device.cuh).
 cudaError_t read_and_clear_latent_prefill_error_word(int* value) {
   cudaError_t e = cudaMemcpyFromSymbol(value, g_spa_error, sizeof(int));
   if (e != cudaSuccess) return e;
