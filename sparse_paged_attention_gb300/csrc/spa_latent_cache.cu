@@ -7,9 +7,8 @@
 // The rotary part keeps two codes a value (about 8 bits) because it carries the position: its
 // rounding moves the scores of near and far entries against one another, and it is a ninth of the
 // row.  Both kernels are bound by HBM (a row's bytes in, a row's bytes out, no reuse).  One warp
-// takes one token: a row is at most 72 16-byte chunks, three a lane, all loaded before any is used;
-// the row maximum is a shuffle reduction; the slot's dependent loads (position, block table) run
-// beside the row's.  No shared memory and few registers, so that enough warps stay resident to
+// takes one token, all of whose row is loaded before any of it is used; the row maximum is a shuffle
+// reduction; the slot's dependent loads (position, block table) run beside the row's.  No shared memory and few registers, so that enough warps stay resident to
 // cover HBM's latency without a staged pipeline.
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -22,7 +21,7 @@ namespace spa {
 namespace {
 
 constexpr int kWarps = 4;            // tokens in flight a CTA
-constexpr int kChunks = (kLatMaxDim + kLatMaxRope) / 8 / 32 + 1;   // 16-byte chunks a lane (3)
+constexpr int kChunks = kLatMaxDim / 8 / 32;   // 16-byte chunks of the latent part a lane (2)
 
 // Pool row of token t, or -1 (a position, page, block or sequence that does not exist).
 __device__ __forceinline__ int token_row(const LatentCacheArgs& a, int t) {
@@ -49,42 +48,31 @@ __device__ __forceinline__ float2 e4m3x2_to_f32(uint32_t codes) {
   return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
 
-// Eight rotary values -> high and low codes.  IEEE divisions: the low code sees the quotient's
-// last bits, which the reciprocal path of the latent part is not held to.
-__device__ __forceinline__ void rope_codes(const uint4& u, float scale, uint2& high, uint2& low) {
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-  uint32_t h[4], l[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float x = __fdiv_rn(kvq_bf16_to_f32(w[i] & 0xFFFFu), scale);
-    const float y = __fdiv_rn(kvq_bf16_to_f32(w[i] >> 16), scale);
-    h[i] = kvq_e4m3x2(x, y);
-    const float2 v = e4m3x2_to_f32(h[i]);
-    l[i] = kvq_e4m3x2(x - v.x, y - v.y);
-  }
-  high = make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
-  low = make_uint2(l[0] | (l[1] << 16), l[2] | (l[3] << 16));
-}
+// A lane takes chunks lane and 32 + lane of the latent part and word lane of the rotary part (two values:
+// at most 64 of them).  Spread like that the rotary part's IEEE divisions and second codes cost every
+// lane two of each; as 16-byte chunks they kept eight lanes busy with eight of each while the others
+// waited, and the e4m3 write of 65,536 tokens took half as long again.
+struct NewRow {
+  uint4 u[kChunks];
+  uint32_t r;
+};
 
 template <bool kFp8>
 __global__ void __launch_bounds__(32 * kWarps) latent_write_kernel(const LatentCacheArgs a) {
   pdl_launch_dependents();
   pdl_wait();
   const int lane = threadIdx.x & 31;
-  const int L = a.pool.L, R = a.pool.R;
-  const int nl = L >> 3, n = (L + R) >> 3;   // chunks of the latent part, of the row
+  const int nl = a.pool.L >> 3, nr = a.pool.R >> 1;   // 16-byte chunks, 4-byte words
   const long long step = (long long)gridDim.x * kWarps;
   for (long long t = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5); t < a.T; t += step) {
-    uint4 u[kChunks];
+    NewRow x;
 #pragma unroll
     for (int i = 0; i < kChunks; ++i) {
       const int c = lane + 32 * i;
-      u[i] = make_uint4(0, 0, 0, 0);
-      if (c < nl)
-        u[i] = __ldg(reinterpret_cast<const uint4*>(a.latent + t * a.latent_stride) + c);
-      else if (c < n)
-        u[i] = __ldg(reinterpret_cast<const uint4*>(a.rope + t * a.rope_stride) + (c - nl));
+      x.u[i] = c < nl ? __ldg(reinterpret_cast<const uint4*>(a.latent + t * a.latent_stride) + c)
+                      : make_uint4(0, 0, 0, 0);
     }
+    x.r = lane < nr ? __ldg(reinterpret_cast<const uint32_t*>(a.rope + t * a.rope_stride) + lane) : 0u;
     const int row = token_row(a, (int)t);
     if (row < 0) {
       if (lane == 0) flag_error(SPA_ERR_INDEX);
@@ -95,12 +83,14 @@ __global__ void __launch_bounds__(32 * kWarps) latent_write_kernel(const LatentC
 #pragma unroll
       for (int i = 0; i < kChunks; ++i) {
         const int c = lane + 32 * i;
-        if (c < n) reinterpret_cast<uint4*>(dst)[c] = u[i];
+        if (c < nl) reinterpret_cast<uint4*>(dst)[c] = x.u[i];
       }
+      if (lane < nr) reinterpret_cast<uint32_t*>(dst + 2 * a.pool.L)[lane] = x.r;
     } else {
-      float amax = 0.f;
+      const float ra = kvq_bf16_to_f32(x.r & 0xFFFFu), rb = kvq_bf16_to_f32(x.r >> 16);
+      float amax = fmaxf(fabsf(ra), fabsf(rb));
 #pragma unroll
-      for (int i = 0; i < kChunks; ++i) amax = fmaxf(amax, chunk_absmax(u[i]));
+      for (int i = 0; i < kChunks; ++i) amax = fmaxf(amax, chunk_absmax(x.u[i]));
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
       const float scale = amax > 0.f ? __fdiv_rn(amax, 448.f) : 1.f;
@@ -109,14 +99,17 @@ __global__ void __launch_bounds__(32 * kWarps) latent_write_kernel(const LatentC
 #pragma unroll
       for (int i = 0; i < kChunks; ++i) {
         const int c = lane + 32 * i;
-        if (c < nl) {
-          *reinterpret_cast<uint2*>(dst + 8 * c) = kvq_chunk(u[i], scale, r, fast);
-        } else if (c < n) {
-          uint2 high, low;
-          rope_codes(u[i], scale, high, low);
-          *reinterpret_cast<uint2*>(dst + 8 * c) = high;
-          *reinterpret_cast<uint2*>(dst + R + 8 * c) = low;
-        }
+        if (c < nl) *reinterpret_cast<uint2*>(dst + 8 * c) = kvq_chunk(x.u[i], scale, r, fast);
+      }
+      if (lane < nr) {
+        // IEEE divisions: the low code sees the quotient's last bits, which the reciprocal path of the
+        // latent part is not held to
+        const float p = __fdiv_rn(ra, scale), q = __fdiv_rn(rb, scale);
+        const uint32_t high = kvq_e4m3x2(p, q);
+        const float2 v = e4m3x2_to_f32(high);
+        uint16_t* rope = reinterpret_cast<uint16_t*>(dst + a.pool.L) + lane;
+        rope[0] = (uint16_t)high;
+        rope[nr] = (uint16_t)kvq_e4m3x2(p - v.x, q - v.y);
       }
       if (lane == 0) a.pool.scale[row] = scale;
     }
@@ -133,54 +126,57 @@ __global__ void __launch_bounds__(32 * kWarps) latent_read_kernel(const LatentCa
   pdl_launch_dependents();
   pdl_wait();
   const int lane = threadIdx.x & 31;
-  const int L = a.pool.L, R = a.pool.R;
-  const int nl = L >> 3, n = (L + R) >> 3;
+  const int nl = a.pool.L >> 3, nr = a.pool.R >> 1;
   const long long step = (long long)gridDim.x * kWarps;
   for (long long t = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5); t < a.T; t += step) {
     const int row = token_row(a, (int)t);
     if (row < 0 && lane == 0) flag_error(SPA_ERR_INDEX);
     const uint8_t* src = a.pool.rows + (size_t)(row < 0 ? 0 : row) * a.pool.row_bytes;
     uint4* dst = reinterpret_cast<uint4*>(a.out + t * a.out_stride);
+    uint32_t* dst_r = reinterpret_cast<uint32_t*>(a.out + t * a.out_stride + 2 * a.pool.L);
     if constexpr (!kFp8) {
-      uint4 u[kChunks];
+      NewRow x;
 #pragma unroll
       for (int i = 0; i < kChunks; ++i) {
         const int c = lane + 32 * i;
-        u[i] = make_uint4(0, 0, 0, 0);
-        if (row >= 0 && c < n) u[i] = __ldg(reinterpret_cast<const uint4*>(src) + c);
+        x.u[i] = row >= 0 && c < nl ? __ldg(reinterpret_cast<const uint4*>(src) + c) : make_uint4(0, 0, 0, 0);
       }
+      x.r = row >= 0 && lane < nr ? __ldg(reinterpret_cast<const uint32_t*>(src + 2 * a.pool.L) + lane) : 0u;
 #pragma unroll
       for (int i = 0; i < kChunks; ++i) {
         const int c = lane + 32 * i;
-        if (c < n) dst[c] = u[i];
+        if (c < nl) dst[c] = x.u[i];
       }
+      if (lane < nr) dst_r[lane] = x.r;
     } else {
-      uint2 hi[kChunks], lo[kChunks];
-      float scale = 0.f;
-      if (row >= 0) scale = __ldg(a.pool.scale + row);
+      uint2 code[kChunks];
+      uint32_t high = 0, low = 0;
+      const float scale = row >= 0 ? __ldg(a.pool.scale + row) : 0.f;
 #pragma unroll
       for (int i = 0; i < kChunks; ++i) {
         const int c = lane + 32 * i;
-        hi[i] = lo[i] = make_uint2(0, 0);
-        if (row >= 0 && c < n) hi[i] = __ldg(reinterpret_cast<const uint2*>(src + 8 * c));
-        if (row >= 0 && c >= nl && c < n)
-          lo[i] = __ldg(reinterpret_cast<const uint2*>(src + R + 8 * c));
+        code[i] = row >= 0 && c < nl ? __ldg(reinterpret_cast<const uint2*>(src) + c) : make_uint2(0, 0);
+      }
+      if (row >= 0 && lane < nr) {
+        const uint16_t* rope = reinterpret_cast<const uint16_t*>(src + a.pool.L) + lane;
+        high = __ldg(rope);
+        low = __ldg(rope + nr);
       }
 #pragma unroll
       for (int i = 0; i < kChunks; ++i) {
         const int c = lane + 32 * i;
-        if (c < n) {
-          const uint32_t h[2] = {hi[i].x, hi[i].y}, l[2] = {lo[i].x, lo[i].y};
-          uint32_t o[4];
+        const uint32_t h[2] = {code[i].x, code[i].y};
+        uint32_t o[4];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float2 x = e4m3x2_to_f32((h[k >> 1] >> (16 * (k & 1))) & 0xFFFFu);
-            const float2 y = e4m3x2_to_f32((l[k >> 1] >> (16 * (k & 1))) & 0xFFFFu);
-            o[k] = c < nl ? bf16x2(x.x * scale, x.y * scale)
-                          : bf16x2((x.x + y.x) * scale, (x.y + y.y) * scale);
-          }
-          dst[c] = make_uint4(o[0], o[1], o[2], o[3]);
+        for (int k = 0; k < 4; ++k) {
+          const float2 v = e4m3x2_to_f32((h[k >> 1] >> (16 * (k & 1))) & 0xFFFFu);
+          o[k] = bf16x2(v.x * scale, v.y * scale);
         }
+        if (c < nl) dst[c] = make_uint4(o[0], o[1], o[2], o[3]);
+      }
+      if (lane < nr) {
+        const float2 v = e4m3x2_to_f32(high), w = e4m3x2_to_f32(low);
+        dst_r[lane] = bf16x2((v.x + w.x) * scale, (v.y + w.y) * scale);
       }
     }
   }
