@@ -56,7 +56,7 @@ struct Item {
 enum {
   B_QFULL = 0, B_QEMPTY, B_PFULL_SLOT, B_PEMPTY_SLOT = B_PFULL_SLOT + kPairs,
   B_RFULL = B_PEMPTY_SLOT + kPairs, B_REMPTY = B_RFULL + kRopes, B_SFULL = B_REMPTY + kRopes,
-  B_PREADY = B_SFULL + 2, B_PVDONE = B_PREADY + 2, B_OFREE = B_PVDONE + 2, B_IFULL = B_OFREE + 2,
+  B_PREADY = B_SFULL + 2, B_PVDONE = B_PREADY + 4, B_OFREE = B_PVDONE + 2, B_IFULL = B_OFREE + 2,
   B_IEMPTY = B_IFULL + kItems, B_DRAIN = B_IEMPTY + kItems, B_COUNT = B_DRAIN + 2
 };
 constexpr int kBarOff = kInfoOff + kItems * (int)sizeof(Item);
@@ -92,7 +92,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(BAR(B_SFULL + i), 1);
-      mbar_init(BAR(B_PREADY + i), 4);       // lane 0 of the tile's four softmax warps
+      mbar_init(BAR(B_PREADY + i), 4);       // lane 0 of the tile's four softmax warps: P's first half,
+      mbar_init(BAR(B_PREADY + 2 + i), 4);   // and its second
       mbar_init(BAR(B_PVDONE + i), 1);
       mbar_init(BAR(B_OFREE + i), 4);
       mbar_init(BAR(B_DRAIN + i), 1);
@@ -381,9 +382,18 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc_fence_after();
           if (lead) {
 #pragma unroll
-            for (int kk = 0; kk < 8; ++kk)       // 16 keys a step
+            for (int kk = 0; kk < 4; ++kk)       // 16 keys a step
               mma_bf16_ts(tmem + kOCol + t * kTile, tmem + t * kTile + kk * 8, desc_add(dv, kk * 2048), idO,
                           (j > 0 || kk > 0) ? 1u : 0u);
+          }
+          __syncwarp();
+          ok = warp_wait(BAR(B_PREADY + 2 + t), (uint32_t)((done[t] - 1) & 1), abort_flag);
+          if (!ok) break;
+          tc_fence_after();
+          if (lead) {
+#pragma unroll
+            for (int kk = 4; kk < 8; ++kk)
+              mma_bf16_ts(tmem + kOCol + t * kTile, tmem + t * kTile + kk * 8, desc_add(dv, kk * 2048), idO, 1u);
             mma_commit(BAR(B_PVDONE + t));
           }
           __syncwarp();
@@ -418,64 +428,43 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         const int left = pos - j * kTile;        // keys 0 .. left of the tile are visible
         const bool masked = pos_min - j * kTile < kTile - 1;
-        float mx = -INFINITY;
+        float x[4][32];                          // the row's 128 scores
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          float x[32];
-          tmem_ld32(sc + 32 * c, x);
-          tmem_wait_ld();
-          if (masked) {
+        for (int c = 0; c < 4; ++c) tmem_ld32(sc + 32 * c, x[c]);
+        tmem_wait_ld();
+        if (masked) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) x[i] = 32 * c + i <= left ? x[i] : -INFINITY;
-          }
-          float y[4] = {x[0], x[1], x[2], x[3]};
+          for (int c = 0; c < 4; ++c)
 #pragma unroll
-          for (int i = 4; i < 32; ++i) y[i & 3] = fmaxf(y[i & 3], x[i]);
-          mx = fmaxf(mx, fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3])));
+            for (int i = 0; i < 32; ++i) x[c][i] = 32 * c + i <= left ? x[c][i] : -INFINITY;
         }
+        float y[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+          for (int i = 0; i < 32; i += 2) y[c] = fmaxf(y[c], fmaxf(x[c][i], x[c][i + 1]));
+        const float mx = fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3]));
         const float mt = mx == -INFINITY ? -INFINITY : mx * s2;
         const float mn = mt > m + kTau ? mt : m;
         const bool grow = __any_sync(0xffffffffu, mn != m);
         const float ref = mn == -INFINITY ? 0.f : mn;
         const float al = fast_exp2(m - ref);
         m = mn;
-        l *= al;
-        float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          float x[32];
-          tmem_ld32(sc + 32 * c, x);
-          tmem_wait_ld();
-#pragma unroll
-          for (int i = 0; i < 32; ++i) x[i] = fast_exp2(fmaf(x[i], s2, -ref));
-          if (masked) {
-#pragma unroll
-            for (int i = 0; i < 32; ++i) x[i] = 32 * c + i <= left ? x[i] : 0.f;
-          }
-          uint32_t w[16];
-#pragma unroll
-          for (int i = 0; i < 16; ++i) w[i] = pack_bf16x2(x[2 * i], x[2 * i + 1]);
-          // (columns 16c .. of S have been read: chunk c of P takes half of chunk c's columns or less)
-          tmem_st16(sc + 16 * c, w);
-#pragma unroll
-          for (int i = 0; i < 32; ++i) sum[i & 3] += x[i];
-        }
-        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
         if (grow && j > 0) {
           // some row's maximum moved: rescale this warp's rows of O once PV of the step before is done
           if (!(ok = warp_wait(BAR(B_PVDONE + t), (uint32_t)((done - 1) & 1), abort_flag))) break;
           tc_fence_after();
 #pragma unroll 1
-          for (int c = 0; c < nvc * 2; ++c) {
-            float o[32];
-            tmem_ld32(oc + 32 * c, o);
+          for (int c = 0; c < nvc * 4; ++c) {
+            float o[16];
+            tmem_ld16(oc + 16 * c, o);
             tmem_wait_ld();
+            uint32_t w[16];
 #pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] *= al;
-            tmem_st32(oc + 32 * c, o);
+            for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(o[i] * al);
+            tmem_st16(oc + 16 * c, w);
           }
         }
-        tmem_wait_st();
         const int keys = it.nk - j * kTile;      // keys of the tile that are the sequence's
         if (keys < kTile) {
           // values of other rows: a probability of zero times a NaN would still be one.  (Both tiles'
@@ -489,9 +478,34 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           fence_proxy_async_smem();
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(BAR(B_PREADY + t));
+        // P in two halves of 64 keys: PV starts on the first while the second is worked out
+        l *= al;
+        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+#pragma unroll
+          for (int c = 2 * hf; c < 2 * hf + 2; ++c) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) x[c][i] = fast_exp2(fmaf(x[c][i], s2, -ref));
+            if (masked) {
+#pragma unroll
+              for (int i = 0; i < 32; ++i) x[c][i] = 32 * c + i <= left ? x[c][i] : 0.f;
+            }
+            uint32_t w[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) w[i] = pack_bf16x2(x[c][2 * i], x[c][2 * i + 1]);
+            tmem_st16(sc + 16 * c, w);
+          }
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(BAR(B_PREADY + 2 * hf + t));
+        }
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+          for (int i = 0; i < 32; ++i) sum[c] += x[c][i];
+        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
       }
       if (!ok) break;
       seq += 2 * all_steps;
