@@ -9,16 +9,18 @@
 //   S_t = Q_t K^T    tcgen05, M = 128 queries, N = 128 keys, both operands in shared memory
 //   O_t += P_t V     M = 128 queries, N = d_v, A = P_t from TMEM (bf16, in the columns of its own S_t)
 //
-// TMEM holds S_0, S_1, O_0, O_1 (128 columns each, fp32): while the softmax works on one query tile, the
-// tensor core works on the other.
+// TMEM holds one S (128 columns, fp32), P_0 and P_1 (64 each) and O_0, O_1 (128 each).  S is the query
+// tiles' in turn: it is free again as soon as a tile's softmax has its row in registers, so the next S
+// (the other tile's) is worked out under the exponentials of this one, and neither waits for PV.
 //
 //   warps 0-3, 4-7   softmax of tile 0, 1: a thread has one query's row of S: maximum, exponentials and
-//                    sum without any exchange; P back to TMEM; O rescaled only when a row's maximum has
+//                    sum without any exchange; P to TMEM; O rescaled only when a row's maximum has
 //                    grown by more than 2^8; epilogue
 //   warp 8           MMAs of S;  warp 9: MMAs of O (apart, so that neither one's waits keep the tensor
 //                    core idle)
-//   warp 10          schedule and tensor-map copies: Q once an item; K (nope) and V in turn through a ring
-//                    of three 32 KB slots, K (rope) through two of 16 KB
+//   warp 10          schedule and tensor-map copies: Q once an item; K in chunks of 64 dimensions (the
+//                    rotary ones last) through a ring of four, each free as soon as the second tile's
+//                    MMAs have read it; V through two slots
 //
 // Items (256 queries, head) go to CTAs statically, in an order that starts with the last queries (the
 // longest rows) of all heads and folds back and forth over the CTAs, so that long and short items add up
@@ -33,17 +35,17 @@ namespace {
 
 constexpr int kTile = 128;                       // queries of a tile, keys of a step
 constexpr int kChunk = kTile * 128;              // 128 rows of 64 bf16 values
-constexpr int kPairs = 3, kRopes = 2;            // ring slots
+constexpr int kKs = 4, kVs = 2;                  // ring slots: chunks of K, tiles of V
 constexpr int kThreads = 352;
 constexpr int kItems = 2;                        // item infos in flight
 constexpr int kTmemCols = 512;
-constexpr int kOCol = 256;
+constexpr int kPCol = 128, kOCol = 256;          // S: columns 0 .. 127
 constexpr float kTau = 8.f;                      // lazy rescale threshold (log2 units)
 
 constexpr int kQOff = 0;                                     // [2 tiles][3 chunks]
-constexpr int kPairOff = kQOff + 6 * kChunk;
-constexpr int kRopeOff = kPairOff + kPairs * 2 * kChunk;
-constexpr int kInfoOff = kRopeOff + kRopes * kChunk;
+constexpr int kKOff = kQOff + 6 * kChunk;
+constexpr int kVOff = kKOff + kKs * kChunk;
+constexpr int kInfoOff = kVOff + kVs * 2 * kChunk;
 
 struct Item {
   int q0, n;          // first query row, queries of the item (0: no more items)
@@ -54,9 +56,9 @@ struct Item {
 };
 
 enum {
-  B_QFULL = 0, B_QEMPTY, B_PFULL_SLOT, B_PEMPTY_SLOT = B_PFULL_SLOT + kPairs,
-  B_RFULL = B_PEMPTY_SLOT + kPairs, B_REMPTY = B_RFULL + kRopes, B_SFULL = B_REMPTY + kRopes,
-  B_PREADY = B_SFULL + 2, B_PVDONE = B_PREADY + 4, B_OFREE = B_PVDONE + 2, B_IFULL = B_OFREE + 2,
+  B_QFULL = 0, B_QEMPTY = B_QFULL + 2, B_KFULL = B_QEMPTY + 2, B_KEMPTY = B_KFULL + kKs,
+  B_VFULL = B_KEMPTY + kKs, B_VEMPTY = B_VFULL + kVs, B_SFULL = B_VEMPTY + kVs, B_SEMPTY = B_SFULL + 2,
+  B_PREADY = B_SEMPTY + 1, B_PVDONE = B_PREADY + 4, B_OFREE = B_PVDONE + 2, B_IFULL = B_OFREE + 2,
   B_IEMPTY = B_IFULL + kItems, B_DRAIN = B_IEMPTY + kItems, B_COUNT = B_DRAIN + 2
 };
 constexpr int kBarOff = kInfoOff + kItems * (int)sizeof(Item);
@@ -80,17 +82,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   Item* items = reinterpret_cast<Item*>(sm + kInfoOff);
 #define BAR(i) (sb + (uint32_t)kBarOff + 8u * (uint32_t)(i))
   if (threadIdx.x == 0) {
-    mbar_init(BAR(B_QFULL), 1);
-    mbar_init(BAR(B_QEMPTY), 1);
-    for (int i = 0; i < kPairs; ++i) {
-      mbar_init(BAR(B_PFULL_SLOT + i), 1);
-      mbar_init(BAR(B_PEMPTY_SLOT + i), 1);
+    for (int i = 0; i < kKs; ++i) {
+      mbar_init(BAR(B_KFULL + i), 1);
+      mbar_init(BAR(B_KEMPTY + i), 1);
     }
-    for (int i = 0; i < kRopes; ++i) {
-      mbar_init(BAR(B_RFULL + i), 1);
-      mbar_init(BAR(B_REMPTY + i), 1);
+    for (int i = 0; i < kVs; ++i) {
+      mbar_init(BAR(B_VFULL + i), 1);
+      mbar_init(BAR(B_VEMPTY + i), 1);
     }
+    mbar_init(BAR(B_SEMPTY), 4);             // lane 0 of the four softmax warps that have read it
     for (int i = 0; i < 2; ++i) {
+      mbar_init(BAR(B_QFULL + i), 1);
+      mbar_init(BAR(B_QEMPTY + i), 1);
       mbar_init(BAR(B_SFULL + i), 1);
       mbar_init(BAR(B_PREADY + i), 4);       // lane 0 of the tile's four softmax warps: P's first half,
       mbar_init(BAR(B_PREADY + 2 + i), 4);   // and its second
@@ -171,9 +174,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       total += __shfl_sync(0xffffffffu, scan, 31);
     }
     const long long n_items = (long long)total * a.H;
-    int n = 0, pair = 0, rp = 0, qs = 0;
-    uint32_t pair_ph = 0, rope_ph = 0;
-    int pair_fills = 0, rope_fills = 0;
+    const int nc = nkc + (rope ? 1 : 0);       // chunks of a key
+    int n = 0, qs[2] = {0, 0};                 // items, query tiles copied
+    uint32_t kc = 0, vc = 0;                   // chunks of K, tiles of V copied
     bool ok = true;
     for (; ok; ++n) {
       // the n-th item of this CTA: rounds of gridDim items, every other one backwards
@@ -224,125 +227,95 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (steps == 0) continue;
       const bool lead = elect_one();
       // the item's queries
-      ok = warp_wait(BAR(B_QEMPTY), (uint32_t)((qs & 1) ^ 1), abort_flag);
-      if (!ok) break;
-      ++qs;
-      if (lead) {
-        const int nt = it.steps[1] > 0 ? 2 : 1, nc = nkc + (rope ? 1 : 0);
-        mbar_arrive_expect_tx(BAR(B_QFULL), (uint32_t)(nt * nc * kChunk));
-        for (int t = 0; t < nt; ++t)
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        if (it.steps[t] == 0 || !ok) continue;
+        ok = warp_wait(BAR(B_QEMPTY + t), (uint32_t)((qs[t] & 1) ^ 1), abort_flag);
+        if (!ok) continue;
+        ++qs[t];
+        if (lead) {
+          mbar_arrive_expect_tx(BAR(B_QFULL + t), (uint32_t)(nc * kChunk));
           for (int c = 0; c < nc; ++c)
-            tma_box3(sb + kQOff + (t * 3 + (c < nkc ? c : 2)) * kChunk, &p.q, c < nkc ? 64 * c : a.dn,
-                     it.head, it.q0 + t * kTile, BAR(B_QFULL));
+            tma_box3(sb + kQOff + (t * 3 + c) * kChunk, &p.q, c < nkc ? 64 * c : a.dn, it.head,
+                     it.q0 + t * kTile, BAR(B_QFULL + t));
+        }
+        __syncwarp();
       }
-      __syncwarp();
       for (int j = 0; j < steps && ok; ++j) {
         const int row = it.k0 + j * kTile;
-        for (int kv = 0; kv < 2 && ok; ++kv) {
-          ok = warp_wait(BAR(B_PEMPTY_SLOT + pair), pair_ph ^ 1, abort_flag);
-          if (!ok) break;
+        for (int c = 0; c < nc; ++c, ++kc) {
+          const uint32_t sl = kc % kKs, full = BAR(B_KFULL + sl);
+          if (!(ok = warp_wait(BAR(B_KEMPTY + sl), ((kc / kKs) & 1) ^ 1, abort_flag))) break;
           if (lead) {
-            const uint32_t full = BAR(B_PFULL_SLOT + pair), dst = sb + kPairOff + pair * 2 * kChunk;
-            const int nc = kv ? nvc : nkc;
-            mbar_arrive_expect_tx(full, (uint32_t)(nc * kChunk));
-            for (int c = 0; c < nc; ++c)
-              tma_box3(dst + c * kChunk, kv ? &p.v : &p.kn, 64 * c, it.head, row, full);
+            mbar_arrive_expect_tx(full, (uint32_t)kChunk);
+            if (c < nkc) tma_box3(sb + kKOff + sl * kChunk, &p.kn, 64 * c, it.head, row, full);
+            else tma_box3(sb + kKOff + sl * kChunk, &p.kr, 0, 0, row, full);
           }
           __syncwarp();
-          ++pair_fills;
-          if (++pair == kPairs) {
-            pair = 0;
-            pair_ph ^= 1;
-          }
-          if (kv == 0 && rope) {
-            ok = warp_wait(BAR(B_REMPTY + rp), rope_ph ^ 1, abort_flag);
-            if (!ok) break;
-            if (lead) {
-              mbar_arrive_expect_tx(BAR(B_RFULL + rp), (uint32_t)kChunk);
-              tma_box3(sb + kRopeOff + rp * kChunk, &p.kr, 0, 0, row, BAR(B_RFULL + rp));
-            }
-            __syncwarp();
-            ++rope_fills;
-            if (++rp == kRopes) {
-              rp = 0;
-              rope_ph ^= 1;
-            }
-          }
         }
+        if (!ok) break;
+        const uint32_t sl = vc % kVs, full = BAR(B_VFULL + sl);
+        if (!(ok = warp_wait(BAR(B_VEMPTY + sl), ((vc / kVs) & 1) ^ 1, abort_flag))) break;
+        if (lead) {
+          mbar_arrive_expect_tx(full, (uint32_t)(nvc * kChunk));
+          for (int c = 0; c < nvc; ++c)
+            tma_box3(sb + kVOff + (sl * 2 + c) * kChunk, &p.v, 64 * c, it.head, row, full);
+        }
+        __syncwarp();
+        ++vc;
       }
     }
     // copies in flight must land before the CTA ends (at once after a normal run)
     if (lane == 0) {
-      if (qs > 0) mbar_wait_drain(BAR(B_QFULL), (uint32_t)((qs - 1) & 1));
-      for (int f = max(0, pair_fills - kPairs); f < pair_fills; ++f)
-        mbar_wait_drain(BAR(B_PFULL_SLOT + f % kPairs), (uint32_t)((f / kPairs) & 1));
-      for (int f = max(0, rope_fills - kRopes); f < rope_fills; ++f)
-        mbar_wait_drain(BAR(B_RFULL + f % kRopes), (uint32_t)((f / kRopes) & 1));
+      for (int t = 0; t < 2; ++t)
+        if (qs[t] > 0) mbar_wait_drain(BAR(B_QFULL + t), (uint32_t)((qs[t] - 1) & 1));
+      for (uint32_t f = kc > kKs ? kc - kKs : 0; f < kc; ++f)
+        mbar_wait_drain(BAR(B_KFULL + f % kKs), (f / kKs) & 1);
+      for (uint32_t f = vc > kVs ? vc - kVs : 0; f < vc; ++f)
+        mbar_wait_drain(BAR(B_VFULL + f % kVs), (f / kVs) & 1);
     }
     __syncwarp();
   } else if (warp == 8) {
     // ================================= MMAs of S ==========================================
     // (bit 13 of the instruction descriptor negates A: a negative scale)
     const uint32_t idS = idesc_bf16(kTile, kTile, 0, 0) | (p.negate ? 1u << 13 : 0u);
-    const uint64_t dq0 = sdesc(sb + kQOff, 16, 1024), dk0 = sdesc(sb + kPairOff, 16, 1024);
-    const uint64_t dr0 = sdesc(sb + kRopeOff, 16, 1024);
+    const uint64_t dq0 = sdesc(sb + kQOff, 16, 1024), dk0 = sdesc(sb + kKOff, 16, 1024);
     const bool lead = elect_one();
-    int seq = 0, rp = 0, qs = 0;                 // pairs seen (K and V), rope slots, items with queries
-    uint32_t rope_ph = 0;
-    int done[2] = {0, 0};                        // S issued of tile 0, 1
+    const int nc = nkc + (rope ? 1 : 0);
+    uint32_t kc = 0, issued = 0;                 // chunks of K seen, S issued
+    int qs[2] = {0, 0};                          // query tiles seen
     bool ok = true;
     Item it;
     for (int n = 0; ok && (ok = next_item(n, it)) && it.n > 0; ++n) {
       const int steps = max(it.steps[0], it.steps[1]);
-      if (steps == 0) continue;
-      if (!(ok = warp_wait(BAR(B_QFULL), (uint32_t)(qs & 1), abort_flag))) break;
-      ++qs;
-      for (int j = 0; j < steps && ok; ++j, seq += 2) {
-        const int sl = seq % kPairs;
-        ok = warp_wait(BAR(B_PFULL_SLOT + sl), (uint32_t)((seq / kPairs) & 1), abort_flag);
-        if (ok && rope) ok = warp_wait(BAR(B_RFULL + rp), rope_ph, abort_flag);
-        if (!ok) break;
-        const uint64_t dk = desc_add(dk0, sl * 2 * kChunk), dr = desc_add(dr0, rp * kChunk);
+      for (int j = 0; j < steps && ok; ++j, kc += nc) {
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-          if (j >= it.steps[t]) continue;
-          // S and P of the step before share these columns: its PV has to be over
-          if (done[t] > 0) ok = warp_wait(BAR(B_PVDONE + t), (uint32_t)((done[t] - 1) & 1), abort_flag);
-          if (!ok) break;
-          ++done[t];
-          tc_fence_after();
-          if (lead) {
-            const uint32_t dS = tmem + t * kTile;
-            const uint64_t dq = desc_add(dq0, t * 3 * kChunk);
-            for (int c = 0; c < nkc; ++c) {
-              const int ks = (min(64, a.dn - 64 * c) + 15) >> 4;
+          if (j >= it.steps[t] || !ok) continue;
+          const bool last = t == 1 || j >= it.steps[1];      // the last tile to read this step's keys
+          if (j == 0) ok = warp_wait(BAR(B_QFULL + t), (uint32_t)(qs[t]++ & 1), abort_flag);
+          // the S before has been read
+          if (ok && issued > 0) ok = warp_wait(BAR(B_SEMPTY), (issued - 1) & 1, abort_flag);
+          ++issued;
+          for (int c = 0; c < nc && ok; ++c) {
+            const uint32_t sl = (kc + c) % kKs;
+            if (!(ok = warp_wait(BAR(B_KFULL + sl), ((kc + c) / kKs) & 1, abort_flag))) break;
+            tc_fence_after();
+            if (lead) {
+              const int ks = ((c < nkc ? min(64, a.dn - 64 * c) : a.dr) + 15) >> 4;
+              const uint64_t dq = desc_add(dq0, (t * 3 + c) * kChunk), dk = desc_add(dk0, sl * kChunk);
 #pragma unroll
               for (int st = 0; st < 4; ++st)
-                if (st < ks)
-                  mma_bf16(dS, desc_add(dq, c * kChunk + st * 32), desc_add(dk, c * kChunk + st * 32), idS,
-                           (c | st) != 0);
+                if (st < ks) mma_bf16(tmem, desc_add(dq, st * 32), desc_add(dk, st * 32), idS, (c | st) != 0);
+              if (last) mma_commit(BAR(B_KEMPTY + sl));
             }
-            if (rope) {
-              const int ks = (a.dr + 15) >> 4;
-#pragma unroll
-              for (int st = 0; st < 4; ++st)
-                if (st < ks)
-                  mma_bf16(dS, desc_add(dq, 2 * kChunk + st * 32), desc_add(dr, st * 32), idS, 1u);
-            }
+            __syncwarp();
+          }
+          if (lead && ok) {
             mma_commit(BAR(B_SFULL + t));
+            if (j == it.steps[t] - 1) mma_commit(BAR(B_QEMPTY + t));
           }
           __syncwarp();
-        }
-        if (!ok) break;
-        if (lead) {
-          mma_commit(BAR(B_PEMPTY_SLOT + sl));
-          if (rope) mma_commit(BAR(B_REMPTY + rp));
-          if (j == steps - 1) mma_commit(BAR(B_QEMPTY));
-        }
-        __syncwarp();
-        if (rope && ++rp == kRopes) {
-          rp = 0;
-          rope_ph ^= 1;
         }
       }
     }
@@ -356,17 +329,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ================================= MMAs of O ==========================================
     const int nv = (a.dv + 15) & ~15;
     const uint32_t idO = idesc_bf16(kTile, nv, 0, 1);
-    const uint64_t dv0 = sdesc(sb + kPairOff, kChunk, 1024);         // MN-major: 64 values a chunk
+    const uint64_t dv0 = sdesc(sb + kVOff, kChunk, 1024);         // MN-major: 64 values a chunk
     const bool lead = elect_one();
-    int seq = 1;
+    uint32_t vc = 0;
     int done[2] = {0, 0}, opened[2] = {0, 0};
     bool ok = true;
     Item it;
     for (int n = 0; ok && (ok = next_item(n, it)) && it.n > 0; ++n) {
       const int steps = max(it.steps[0], it.steps[1]);
-      for (int j = 0; j < steps && ok; ++j, seq += 2) {
-        const int sl = seq % kPairs;
-        ok = warp_wait(BAR(B_PFULL_SLOT + sl), (uint32_t)((seq / kPairs) & 1), abort_flag);
+      for (int j = 0; j < steps && ok; ++j, ++vc) {
+        const uint32_t sl = vc % kVs;
+        ok = warp_wait(BAR(B_VFULL + sl), (vc / kVs) & 1, abort_flag);
         if (!ok) break;
         const uint64_t dv = desc_add(dv0, sl * 2 * kChunk);
 #pragma unroll
@@ -383,7 +356,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (lead) {
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)       // 16 keys a step
-              mma_bf16_ts(tmem + kOCol + t * kTile, tmem + t * kTile + kk * 8, desc_add(dv, kk * 2048), idO,
+              mma_bf16_ts(tmem + kOCol + t * kTile, tmem + kPCol + t * 64 + kk * 8, desc_add(dv, kk * 2048), idO,
                           (j > 0 || kk > 0) ? 1u : 0u);
           }
           __syncwarp();
@@ -393,13 +366,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (lead) {
 #pragma unroll
             for (int kk = 4; kk < 8; ++kk)
-              mma_bf16_ts(tmem + kOCol + t * kTile, tmem + t * kTile + kk * 8, desc_add(dv, kk * 2048), idO, 1u);
+              mma_bf16_ts(tmem + kOCol + t * kTile, tmem + kPCol + t * 64 + kk * 8, desc_add(dv, kk * 2048), idO, 1u);
             mma_commit(BAR(B_PVDONE + t));
           }
           __syncwarp();
         }
         if (!ok) break;
-        if (lead) mma_commit(BAR(B_PEMPTY_SLOT + sl));
+        if (lead) mma_commit(BAR(B_VEMPTY + sl));
         __syncwarp();
       }
     }
@@ -412,10 +385,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ================================ softmax and epilogue ================================
     const int t = warp >> 2, row = (warp & 3) * 32 + lane;      // query tile, row in it == TMEM lane
     const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-    const uint32_t sc = lanes + t * kTile, oc = lanes + kOCol + t * kTile;
+    const uint32_t pc = lanes + kPCol + t * 64, oc = lanes + kOCol + t * kTile;
     const float s2 = p.scale_log2;
     int done = 0;                                // steps of this tile done
-    int seq = 1;                                 // V slots seen
+    uint32_t vc = 0;                             // tiles of V seen
     bool ok = true;
     Item it;
     for (int n = 0; ok && (ok = next_item(n, it)) && it.n > 0; ++n) {
@@ -430,8 +403,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool masked = pos_min - j * kTile < kTile - 1;
         float x[4][32];                          // the row's 128 scores
 #pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld32(sc + 32 * c, x[c]);
+        for (int c = 0; c < 4; ++c) tmem_ld32(lanes + 32 * c, x[c]);
         tmem_wait_ld();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(BAR(B_SEMPTY));
         if (masked) {
 #pragma unroll
           for (int c = 0; c < 4; ++c)
@@ -450,10 +426,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float ref = mn == -INFINITY ? 0.f : mn;
         const float al = fast_exp2(m - ref);
         m = mn;
-        if (grow && j > 0) {
-          // some row's maximum moved: rescale this warp's rows of O once PV of the step before is done
+        if (j > 0) {
+          // PV of the step before has read P and added to O
           if (!(ok = warp_wait(BAR(B_PVDONE + t), (uint32_t)((done - 1) & 1), abort_flag))) break;
           tc_fence_after();
+        }
+        if (grow && j > 0) {
+          // some row's maximum moved: rescale this warp's rows of O
 #pragma unroll 1
           for (int c = 0; c < nvc * 4; ++c) {
             float o[16];
@@ -469,11 +448,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (keys < kTile) {
           // values of other rows: a probability of zero times a NaN would still be one.  (Both tiles'
           // warps write the same zeros before their own PV.)
-          const int sq = seq + 2 * j, sl = sq % kPairs;
-          if (!(ok = warp_wait(BAR(B_PFULL_SLOT + sl), (uint32_t)((sq / kPairs) & 1), abort_flag))) break;
+          const uint32_t sl = (vc + j) % kVs;
+          if (!(ok = warp_wait(BAR(B_VFULL + sl), ((vc + j) / kVs) & 1, abort_flag))) break;
           for (int u = (threadIdx.x & 127); u < (kTile - keys) * nvc * 8; u += 128) {
             const int r = keys + u / (nvc * 8), w = u % (nvc * 8);
-            *reinterpret_cast<uint4*>(sm + kPairOff + sl * 2 * kChunk + (w >> 3) * kChunk + r * 128 +
+            *reinterpret_cast<uint4*>(sm + kVOff + sl * 2 * kChunk + (w >> 3) * kChunk + r * 128 +
                                       (w & 7) * 16) = make_uint4(0, 0, 0, 0);
           }
           fence_proxy_async_smem();
@@ -494,7 +473,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t w[16];
 #pragma unroll
             for (int i = 0; i < 16; ++i) w[i] = pack_bf16x2(x[c][2 * i], x[c][2 * i + 1]);
-            tmem_st16(sc + 16 * c, w);
+            tmem_st16(pc + 16 * c, w);
           }
           tmem_wait_st();
           tc_fence_before();
@@ -508,7 +487,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
       }
       if (!ok) break;
-      seq += 2 * all_steps;
+      vc += all_steps;
       // ---- epilogue ----
       const bool mine = t * kTile + row < it.n;
       uint4* dst = reinterpret_cast<uint4*>(a.out + ((size_t)(it.q0 + t * kTile + row) * a.H + it.head) * a.dv * 2);
