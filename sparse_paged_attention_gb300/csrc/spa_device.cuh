@@ -435,6 +435,20 @@ __device__ __forceinline__ bool elect_one() {
   asm volatile("{ .reg .pred p; elect.sync _|p, 0xffffffff; selp.u32 %0, 1, 0, p; }" : "=r"(p));
   return p != 0;
 }
+// Two fp32 operations in one instruction: (x, y) = (x, y) s + b, (x, y) += (a, b).
+__device__ __forceinline__ void fma_f32x2(float& x, float& y, float s, float b) {
+  asm("{ .reg .b64 v, c, d; mov.b64 v, {%0, %1}; mov.b64 c, {%2, %2}; mov.b64 d, {%3, %3}; "
+      "fma.rn.f32x2 v, v, c, d; mov.b64 {%0, %1}, v; }"
+      : "+f"(x), "+f"(y)
+      : "f"(s), "f"(b));
+}
+__device__ __forceinline__ void add_f32x2(float& x, float& y, float a, float b) {
+  asm("{ .reg .b64 v, c; mov.b64 v, {%0, %1}; mov.b64 c, {%2, %3}; add.rn.f32x2 v, v, c; "
+      "mov.b64 {%0, %1}, v; }"
+      : "+f"(x), "+f"(y)
+      : "f"(a), "f"(b));
+}
+
 // A value the whole warp agrees on, known to the compiler as such.
 __device__ __forceinline__ uint32_t warp_uniform(uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); }
 

@@ -174,13 +174,23 @@ __global__ void __launch_bounds__(kThreads, 1)
       total += __shfl_sync(0xffffffffu, scan, 31);
     }
     const long long n_items = (long long)total * a.H;
+    // Rounds of one item a CTA; where a last round would leave half of the CTAs idle its items are taken
+    // by single tiles (which take half as long).
+    const long long whole = n_items / gridDim.x * gridDim.x;
+    const bool halves = 2 * (n_items - whole) <= gridDim.x;
     const int nc = nkc + (rope ? 1 : 0);       // chunks of a key
     int n = 0, qs[2] = {0, 0};                 // items, query tiles copied
     uint32_t kc = 0, vc = 0;                   // chunks of K, tiles of V copied
     bool ok = true;
     for (; ok; ++n) {
-      // the n-th item of this CTA: rounds of gridDim items, every other one backwards
-      const long long i = (long long)n * gridDim.x + ((n & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+      // the n-th item of this CTA; every other round goes backwards
+      long long i = (long long)n * gridDim.x + ((n & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+      int from = 0, upto = 2 * kTile;        // queries of the item that this CTA takes
+      if (halves && i >= whole) {
+        from = (int)(i - whole & 1) * kTile;
+        upto = from + kTile;
+        i = whole + (i - whole) / 2;
+      }
       Item it = {};
       if (i < n_items) {
         const int tile = total - 1 - (int)(i / a.H);
@@ -198,9 +208,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             q1 = __shfl_sync(0xffffffffu, q1, k);
             k0 = __shfl_sync(0xffffffffu, k0, k);
             k1 = __shfl_sync(0xffffffffu, k1, k);
-            const int r = (tile - first) * 2 * kTile;
+            const int r = (tile - first) * 2 * kTile + from;
             it.q0 = q0 + r;
-            it.n = min(2 * kTile, q1 - q0 - r);
+            it.n = max(0, min(upto - from, q1 - q0 - r));    // (0, a second half of nothing: the last)
             it.k0 = k0;
             it.nk = k1 - k0;
             it.pos = it.nk - (q1 - q0) + r;
@@ -293,25 +303,29 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int t = 0; t < 2; ++t) {
           if (j >= it.steps[t] || !ok) continue;
           const bool last = t == 1 || j >= it.steps[1];      // the last tile to read this step's keys
-          if (j == 0) ok = warp_wait(BAR(B_QFULL + t), (uint32_t)(qs[t]++ & 1), abort_flag);
+          if (t == 0 || it.steps[0] <= j)                    // the first
+            for (int c = 0; c < nc && ok; ++c)
+              ok = warp_wait(BAR(B_KFULL + (kc + c) % kKs), ((kc + c) / kKs) & 1, abort_flag);
+          if (ok && j == 0) ok = warp_wait(BAR(B_QFULL + t), (uint32_t)(qs[t]++ & 1), abort_flag);
           // the S before has been read
           if (ok && issued > 0) ok = warp_wait(BAR(B_SEMPTY), (issued - 1) & 1, abort_flag);
+          if (!ok) continue;
           ++issued;
-          for (int c = 0; c < nc && ok; ++c) {
-            const uint32_t sl = (kc + c) % kKs;
-            if (!(ok = warp_wait(BAR(B_KFULL + sl), ((kc + c) / kKs) & 1, abort_flag))) break;
-            tc_fence_after();
-            if (lead) {
+          tc_fence_after();
+          if (lead) {
+            for (int c = 0; c < nc; ++c) {
+              const uint32_t sl = (kc + c) % kKs;
               const int ks = ((c < nkc ? min(64, a.dn - 64 * c) : a.dr) + 15) >> 4;
               const uint64_t dq = desc_add(dq0, (t * 3 + c) * kChunk), dk = desc_add(dk0, sl * kChunk);
+              mma_bf16(tmem, dq, dk, idS, c != 0);
+              if (ks == 4) {
 #pragma unroll
-              for (int st = 0; st < 4; ++st)
-                if (st < ks) mma_bf16(tmem, desc_add(dq, st * 32), desc_add(dk, st * 32), idS, (c | st) != 0);
+                for (int st = 1; st < 4; ++st) mma_bf16(tmem, desc_add(dq, st * 32), desc_add(dk, st * 32), idS, 1u);
+              } else {
+                for (int st = 1; st < ks; ++st) mma_bf16(tmem, desc_add(dq, st * 32), desc_add(dk, st * 32), idS, 1u);
+              }
               if (last) mma_commit(BAR(B_KEMPTY + sl));
             }
-            __syncwarp();
-          }
-          if (lead && ok) {
             mma_commit(BAR(B_SFULL + t));
             if (j == it.steps[t] - 1) mma_commit(BAR(B_QEMPTY + t));
           }
@@ -465,7 +479,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int c = 2 * hf; c < 2 * hf + 2; ++c) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) x[c][i] = fast_exp2(fmaf(x[c][i], s2, -ref));
+            for (int i = 0; i < 32; i += 2) {
+              fma_f32x2(x[c][i], x[c][i + 1], s2, -ref);
+              x[c][i] = fast_exp2(x[c][i]);
+              x[c][i + 1] = fast_exp2(x[c][i + 1]);
+            }
             if (masked) {
 #pragma unroll
               for (int i = 0; i < 32; ++i) x[c][i] = 32 * c + i <= left ? x[c][i] : 0.f;
@@ -483,7 +501,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int c = 0; c < 4; ++c)
 #pragma unroll
-          for (int i = 0; i < 32; ++i) sum[c] += x[c][i];
+          for (int i = 0; i < 32; i += 2) add_f32x2(sum[c & 2], sum[(c & 2) + 1], x[c][i], x[c][i + 1]);
         l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
       }
       if (!ok) break;
@@ -549,8 +567,8 @@ cudaError_t launch_latent_prefill(const LatentPrefillArgs& a, int sms, cudaStrea
     if (a.dr > 0 && !encode_bf16_3d(&p.kr, a.k_rope, a.dr, 1, 0, a.num_k, a.kr_st, 1, kTile))
       return cudaErrorInvalidValue;
   }
-  // at most this many items; a CTA without one ends at once
-  const long long items = ((long long)a.num_q / (2 * kTile) + a.B + 1) * a.H;
+  // at most this many items, in two halves each; a CTA without one ends at once
+  const long long items = 2 * ((long long)a.num_q / (2 * kTile) + a.B + 1) * a.H;
   const unsigned grid = (unsigned)(items < sms ? items : sms);
   return launch_with_pdl(latent_prefill_kernel, dim3(grid), dim3(kThreads), kSmem, stream, 2LL * grid <= sms,
                          p);
