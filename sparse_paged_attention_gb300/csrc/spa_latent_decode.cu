@@ -51,6 +51,8 @@
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
+#include <type_traits>
+
 #include "spa_latent.h"
 #include "spa_launch.h"
 
@@ -150,7 +152,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(BAR(C::kFullB + i), p.boxed ? 1 : 128);   // armed by the loader, or cp.async's threads
       mbar_init(BAR(C::kEmptyB + i), 1);
     }
-    mbar_init(BAR(C::kQFullB), 4);
+    mbar_init(BAR(C::kQFullB), 8);           // two lanes of four q warps, or one of the softmax warps'
     mbar_init(BAR(C::kQEmptyB), 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(BAR(C::kSFullB + i), 1);
@@ -191,21 +193,77 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int g = blockIdx.x % p.groups;                  // this CTA's 64 heads
   const int slice = blockIdx.x / p.groups;
 
-  if (warp == 13) {
-    // ================================ schedule and loads ==================================
-    long long total = 0;
-    for (int t = lane; t < a.T; t += 32) {
-      int b;
-      bool bad;
-      total += tiles_of(token_len(a, t, b, bad));
+  // e4m3: the q of token t, the CTA's item-th, into shared memory as two terms: kPer threads a head (thread
+  // id `tid`), its pieces of eight values in turn, read twice: for the maximum and to convert.
+  const auto put_codes = [&](auto per_head, int t, int tid, int item) -> bool {
+    constexpr int kPer = decltype(per_head)::value;
+    const int h = tid / kPer, part = tid % kPer, hg = g * kHeads + h;
+    const int np = (L + R) >> 3, nlp = L >> 3, nrp = R >> 3;
+    constexpr int kPieces = (kLatMaxDim + kLatMaxRope) / 8 / kPer, kBatch = 6;
+    static_assert(kPieces % kBatch == 0, "batches of loads");
+    const uint4* ql = reinterpret_cast<const uint4*>(a.q_latent + t * a.ql_st + hg * a.ql_sh);
+    const uint4* qr = reinterpret_cast<const uint4*>(a.q_rope + t * a.qr_st + hg * a.qr_sh);
+    uint4 u[kBatch];
+    const auto load = [&](int i0) {            // a batch's loads in flight together
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const int pc = kPer * (i0 + i) + part;
+        u[i] = make_uint4(0, 0, 0, 0);
+        if (hg < a.H && pc < np) u[i] = __ldg(pc < nlp ? ql + pc : qr + (pc - nlp));
+      }
+    };
+    float m = 0.f;
+#pragma unroll 1
+    for (int i0 = 0; i0 < kPieces; i0 += kBatch) {
+      load(i0);
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const uint32_t w[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) m = fmaxf(m, fmaxf(fabsf(bf16_lo(w[e])), fabsf(bf16_hi(w[e]))));
+      }
     }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-    long long per = (total + p.slices - 1) / p.slices;
-    if (per < kMinTiles) per = kMinTiles;
-    const long long begin = per * slice;
-    const long long end = begin + per < total ? begin + per : total;
+    for (int o = 1; o < kPer; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    const float qs = m > 0.f ? pow2_floor(448.f / m) : 1.f;
+    if (!warp_wait(BAR(C::kQEmptyB), (uint32_t)((item & 1) ^ 1), abort_flag)) return false;
+    if (part == 0)
+      reinterpret_cast<float*>(sm + C::kQScaleOff)[(item & 3) * kHeads + h] = 0.03125f / qs;
+    // piece pc: bytes 8 pc of the row: chunk pc / 16, 16-byte unit (pc / 2) & 7, swizzled by row
+    const auto put = [&](int pc, uint2 hi, uint2 lo) {
+      uint8_t* d = sm + C::kQOff + (pc >> 4) * 16384 + h * 128 + ((((pc >> 1) & 7) ^ (h & 7)) << 4) +
+                   (pc & 1) * 8;
+      *reinterpret_cast<uint2*>(d) = hi;
+      *reinterpret_cast<uint2*>(d + 64 * 128) = lo;
+    };
+#pragma unroll 1
+    for (int i0 = 0; i0 < kPieces; i0 += kBatch) {
+      load(i0);
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const int pc = kPer * (i0 + i) + part;
+        const uint32_t w[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
+        uint32_t hi[4], lo[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float x = bf16_lo(w[e]) * qs, y = bf16_hi(w[e]) * qs;
+          hi[e] = e4m3x2(x, y);
+          const __half2_raw hr = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)hi[e], __NV_E4M3);
+          const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&hr));
+          lo[e] = e4m3x2(x - v.x, y - v.y);
+        }
+        const uint2 h2 = make_uint2(hi[0] | (hi[1] << 16), hi[2] | (hi[3] << 16));
+        const uint2 l2 = make_uint2(lo[0] | (lo[1] << 16), lo[2] | (lo[3] << 16));
+        if (pc < np) put(pc, h2, l2);
+        if (pc >= nlp && pc < np) put(pc + nrp, h2, l2);   // against the low codes of the rows too
+      }
+    }
+    for (int pc = np + nrp + part; pc < 16 * n_chunks; pc += kPer) put(pc, make_uint2(0, 0), make_uint2(0, 0));
+    return true;
+  };
 
+  if (warp == 13) {
+    // ================================ schedule and loads ==================================
     // the iterator: token t of the chunk of 32 whose lengths and sequences the lanes hold
     int t0 = 0, c_len = 0, c_seq = 0, c_bad = 0;
     auto load_chunk = [&](int at) {
@@ -218,10 +276,24 @@ __global__ void __launch_bounds__(kThreads, 1)
         c_bad = bad;
       }
     };
+    load_chunk(0);
+    long long total = lane < a.T ? tiles_of(c_len) : 0;
+    for (int t = lane + 32; t < a.T; t += 32) {
+      int b;
+      bool bad;
+      total += tiles_of(token_len(a, t, b, bad));
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+    long long per = (total + p.slices - 1) / p.slices;
+    if (per < kMinTiles) per = kMinTiles;
+    const long long begin = per * slice;
+    const long long end = begin + per < total ? begin + per : total;
+
     int it_t = 0, it_j = 0;                    // next tile: token, tile of the token
     if (begin < end) {
       long long before = 0;
-      for (load_chunk(0);; load_chunk(t0 + 32)) {
+      for (;; load_chunk(t0 + 32)) {
         const int n = t0 + lane < a.T ? tiles_of(c_len) : 0;
         int sum = n;                           // inclusive scan (32 tokens: below 2^31 tiles)
 #pragma unroll
@@ -543,7 +615,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // Each token's q is read into registers as soon as its first tile is announced, and put in
     // place once the token before has no S left to compute.
     const int tid = threadIdx.x - kSoftmax;
-    int items = 0, buf = 0, flags = 0;
+    int items = kFp8 ? 1 : 0, buf = 0, flags = 0;      // (e4m3: the first is the softmax warps')
     auto put_q = [&](int t) -> bool {
       if constexpr (!kFp8) {
         // TMEM lane 32w + l is head 32(w & 1) + l; its first (w < 2) or second half of the latents
@@ -594,81 +666,18 @@ __global__ void __launch_bounds__(kThreads, 1)
           *reinterpret_cast<uint4*>(sm + C::kQOff + hr * 128 + (((tid & 7) ^ (hr & 7)) << 4)) = v[i];
         }
       } else {
-        // two threads a head, its pieces of eight values in turn
-        const int h = tid >> 1, hg = g * kHeads + h;
-        const int np = (L + R) >> 3, nlp = L >> 3, nrp = R >> 3;
-        constexpr int kPieces = (kLatMaxDim + kLatMaxRope) / 16, kBatch = 12;
-        static_assert(kPieces % kBatch == 0, "batches of loads");
-        const uint4* ql = reinterpret_cast<const uint4*>(a.q_latent + t * a.ql_st + hg * a.ql_sh);
-        const uint4* qr = reinterpret_cast<const uint4*>(a.q_rope + t * a.qr_st + hg * a.qr_sh);
-        const auto load = [&](int i0, uint4 (&u)[kBatch]) {   // a batch's loads in flight together
-#pragma unroll
-          for (int i = 0; i < kBatch; ++i) {
-            const int pc = 2 * (i0 + i) + (tid & 1);
-            u[i] = make_uint4(0, 0, 0, 0);
-            if (hg < a.H && pc < np) u[i] = __ldg(pc < nlp ? ql + pc : qr + (pc - nlp));
-          }
-        };
-        float m = 0.f;
-#pragma unroll 1
-        for (int i0 = 0; i0 < kPieces; i0 += kBatch) {
-          uint4 u[kBatch];
-          load(i0, u);
-#pragma unroll
-          for (int i = 0; i < kBatch; ++i) {
-            const uint32_t w[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) m = fmaxf(m, fmaxf(fabsf(bf16_lo(w[e])), fabsf(bf16_hi(w[e]))));
-          }
-        }
-        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
-        const float qs = m > 0.f ? pow2_floor(448.f / m) : 1.f;
-        if (!warp_wait(BAR(C::kQEmptyB), (uint32_t)((items & 1) ^ 1), abort_flag)) return false;
-        if ((tid & 1) == 0)
-          reinterpret_cast<float*>(sm + C::kQScaleOff)[(items & 3) * kHeads + h] = 0.03125f / qs;
-        // piece pc: bytes 8 pc of the row: chunk pc / 16, 16-byte unit (pc / 2) & 7, swizzled by row
-        const auto put = [&](int pc, uint2 hi, uint2 lo) {
-          uint8_t* d = sm + C::kQOff + (pc >> 4) * 16384 + h * 128 + ((((pc >> 1) & 7) ^ (h & 7)) << 4) +
-                       (pc & 1) * 8;
-          *reinterpret_cast<uint2*>(d) = hi;
-          *reinterpret_cast<uint2*>(d + 64 * 128) = lo;
-        };
-#pragma unroll 1
-        for (int i0 = 0; i0 < kPieces; i0 += kBatch) {
-          uint4 u[kBatch];
-          load(i0, u);
-#pragma unroll
-          for (int i = 0; i < kBatch; ++i) {
-            const int pc = 2 * (i0 + i) + (tid & 1);
-            const uint32_t w[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
-            uint32_t hi[4], lo[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float x = bf16_lo(w[e]) * qs, y = bf16_hi(w[e]) * qs;
-              hi[e] = e4m3x2(x, y);
-              const __half2_raw hr = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)hi[e], __NV_E4M3);
-              const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&hr));
-              lo[e] = e4m3x2(x - v.x, y - v.y);
-            }
-            const uint2 h2 = make_uint2(hi[0] | (hi[1] << 16), hi[2] | (hi[3] << 16));
-            const uint2 l2 = make_uint2(lo[0] | (lo[1] << 16), lo[2] | (lo[3] << 16));
-            if (pc < np) put(pc, h2, l2);
-            if (pc >= nlp && pc < np) put(pc + nrp, h2, l2);   // against the low codes of the rows too
-          }
-        }
-        for (int pc = np + nrp + (tid & 1); pc < 16 * n_chunks; pc += 2)
-          put(pc, make_uint2(0, 0), make_uint2(0, 0));
+        if (!put_codes(std::integral_constant<int, 2>(), t, tid, items)) return false;
       }
       fence_proxy_async_smem();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(BAR(C::kQFullB));
+      if (lane < 2) mbar_arrive(BAR(C::kQFullB));
       ++items;
       return true;
     };
     // (a boxed CTA's first token does not wait for the page table; cp.async copies rows first)
     bool ok = true;
-    if (p.boxed) {
+    if (!kFp8 && p.boxed) {
       ok = warp_wait(BAR(C::kTokenB), 0, abort_flag);
       const int t = *reinterpret_cast<volatile int*>(sm + C::kMiscOff + 8);
       if (ok && t >= 0) ok = put_q(t);
@@ -709,7 +718,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(BAR(C::kInfoEmptyB + ri));
-      if ((flags & kFirst) && !(p.boxed && k == 0) && !put_q(t)) break;
+      if ((flags & kFirst) && !((kFp8 || p.boxed) && k == 0) && !put_q(t)) break;
     }
     cp_async_wait_all();
   } else {
@@ -748,7 +757,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       return __shfl_sync(0xffffffffu, (c >= 32) == (pair != 0) ? own : other, c & 31);
     };
     int flags = 0, buf = kBufs - 1;
-    ok = warp_wait(BAR(C::kInfoFullB), 0, abort_flag);
+    if (kFp8) {                                    // the first token's q: nothing else to do before it
+      ok = warp_wait(BAR(C::kTokenB), 0, abort_flag);
+      const int t = *reinterpret_cast<volatile int*>(sm + C::kMiscOff + 8);
+      if (ok && t >= 0) {
+        ok = put_codes(std::integral_constant<int, 4>(), t, tid, 0);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(BAR(C::kQFullB));
+      }
+    }
+    ok = warp_wait(BAR(C::kInfoFullB), 0, abort_flag) && ok;
     const bool any = named_bar_and(1, kSoftmax, ok && !(infos[0].flags & kEnd));
     for (int k = 0; any && !(flags & kFinal); ++k) {
       const int ri = k % kRing, s = k % C::kSBufs;
@@ -1052,15 +1071,23 @@ __global__ void __launch_bounds__(32 * kMergeWarps)
   __shared__ __align__(16) float sum[kMergeWarps][128];
   // of every cut token: the slice where it begins, its last slice, itself, units of the tokens before it
   __shared__ __align__(16) int4 item[kMergeMaxCuts];
+  __shared__ int2 cuts[kMergeMaxCuts];
+  __shared__ float2 stat[kMergeWarps];
   __shared__ int n_items, n_units;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int nq = (L + 127) >> 7;
   pdl_wait();
+#pragma unroll
+  for (int i = 0; i < kMergeMaxCuts / (32 * kMergeWarps); ++i) {     // (all loads in flight together)
+    const int s = threadIdx.x + i * 32 * kMergeWarps;
+    if (s < slices) cuts[s] = cut[(size_t)s * groups];
+  }
+  __syncthreads();
   if (warp == 0) {
     int n = 0, units = 0;
     for (int s0 = 0; s0 < slices; s0 += 32) {
       const int s = s0 + lane;
-      const int2 c = s < slices ? cut[(size_t)s * groups] : make_int2(-1, 0);
+      const int2 c = s < slices ? cuts[s] : make_int2(-1, 0);
       const unsigned m = __ballot_sync(0xffffffffu, c.x >= 0);
       const int mine = c.x < 0 ? 0 : (c.y - s + 1 <= kWarpParts ? (H + kMergeWarps - 1) / kMergeWarps : H * nq);
       int scan = mine;
@@ -1096,7 +1123,20 @@ __global__ void __launch_bounds__(32 * kMergeWarps)
     if (by_warp) {
       if (h >= H) continue;
       // (a lane's four channels of every 128; parts past n count as the first with weight 0)
+      float4 v[2][4];
+      const auto load = [&](int i0) {
+#pragma unroll
+        for (int z = 0; z < 2; ++z) {
+          const float* src = part + slot(i0 + z < n ? i0 + z : i0) * L;
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const int d = 4 * lane + 128 * q;
+            v[z][q] = d < L ? *reinterpret_cast<const float4*>(src + d) : make_float4(0.f, 0.f, 0.f, 0.f);
+          }
+        }
+      };
       const float mine = lane < n ? lse[slot(lane)] : -INFINITY;
+      load(0);
       float4 acc[4];
 #pragma unroll
       for (int q = 0; q < 4; ++q) acc[q] = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -1110,16 +1150,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps)
       for (int o = 4; o > 0; o >>= 1) tot += __shfl_xor_sync(0xffffffffu, tot, o);
       const float inv = M == -INFINITY ? 0.f : 1.f / tot;
       for (int i0 = 0; i0 < n; i0 += 2) {
-        float4 v[2][4];
-#pragma unroll
-        for (int z = 0; z < 2; ++z) {
-          const float* src = part + slot(i0 + z < n ? i0 + z : i0) * L;
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const int d = 4 * lane + 128 * q;
-            v[z][q] = d < L ? *reinterpret_cast<const float4*>(src + d) : make_float4(0.f, 0.f, 0.f, 0.f);
-          }
-        }
+        if (i0 > 0) load(i0);
 #pragma unroll
         for (int z = 0; z < 2; ++z) {
           const float f = __shfl_sync(0xffffffffu, w * inv, i0 + z);
@@ -1142,39 +1173,63 @@ __global__ void __launch_bounds__(32 * kMergeWarps)
       }
       continue;
     }
-    float M = -INFINITY;
-    for (int i = lane; i < n; i += 32) M = fmaxf(M, lse[slot(i)]);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    // (a NaN among the parts' sums is not seen by the maximum but comes back in its weight)
-    const float ref = M == -INFINITY ? 0.f : M;
-    float tot = 0.f;
-    for (int i = lane; i < n; i += 32) tot += exp2f(lse[slot(i)] - ref);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) tot += __shfl_xor_sync(0xffffffffu, tot, o);
+    // eight parts in flight, weighted against the largest of this warp's so far
     const int d = 128 * ((u - it.w) % nq) + 4 * lane;      // (L may end inside the last 128)
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-    for (int i = warp; i < n; i += kMergeWarps) {
-      const size_t at = slot(i);
-      const float w = exp2f(lse[at] - ref);
-      const float4 v = d < L ? *reinterpret_cast<const float4*>(part + at * L + d) : make_float4(0.f, 0.f, 0.f, 0.f);
-      acc.x = fmaf(w, v.x, acc.x);
-      acc.y = fmaf(w, v.y, acc.y);
-      acc.z = fmaf(w, v.z, acc.z);
-      acc.w = fmaf(w, v.w, acc.w);
+    float M = -INFINITY, tot = 0.f;
+    for (int i0 = warp; i0 < n; i0 += 8 * kMergeWarps) {
+      float e[8];
+      float4 v[8];
+#pragma unroll
+      for (int z = 0; z < 8; ++z) {
+        const int i = i0 + z * kMergeWarps;
+        e[z] = -INFINITY;
+        v[z] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (i < n) {
+          const size_t at = slot(i);
+          e[z] = lse[at];
+          if (d < L) v[z] = *reinterpret_cast<const float4*>(part + at * L + d);
+        }
+      }
+      float mx = M;
+#pragma unroll
+      for (int z = 0; z < 8; ++z) mx = fmaxf(mx, e[z]);
+      // (a NaN among the parts' sums is not seen by the maximum but comes back in its weight)
+      const float ref = mx == -INFINITY ? 0.f : mx, f = exp2f(M - ref);
+      M = mx;
+      tot *= f;
+      acc.x *= f;
+      acc.y *= f;
+      acc.z *= f;
+      acc.w *= f;
+#pragma unroll
+      for (int z = 0; z < 8; ++z) {
+        const float w = exp2f(e[z] - ref);
+        tot += w;
+        acc.x = fmaf(w, v[z].x, acc.x);
+        acc.y = fmaf(w, v[z].y, acc.y);
+        acc.z = fmaf(w, v[z].z, acc.z);
+        acc.w = fmaf(w, v[z].w, acc.w);
+      }
     }
     *reinterpret_cast<float4*>(&sum[warp][4 * lane]) = acc;
+    if (lane == 0) stat[warp] = make_float2(M, tot);
     __syncthreads();
-    const float inv = M == -INFINITY ? 0.f : 1.f / tot;
     const int e = 2 * threadIdx.x, de = 128 * ((u - it.w) % nq) + e;
     if (threadIdx.x < 64 && de < L) {
-      float x = 0.f, y = 0.f;
+      float all = -INFINITY, t = 0.f, x = 0.f, y = 0.f;
+#pragma unroll
+      for (int w = 0; w < kMergeWarps; ++w) all = fmaxf(all, stat[w].x);
+      const float ref = all == -INFINITY ? 0.f : all;
 #pragma unroll
       for (int w = 0; w < kMergeWarps; ++w) {
-        x += sum[w][e];
-        y += sum[w][e + 1];
+        const float f = exp2f(stat[w].x - ref);
+        t = fmaf(f, stat[w].y, t);
+        x = fmaf(f, sum[w][e], x);
+        y = fmaf(f, sum[w][e + 1], y);
       }
+      // (t is 0 where no part has an entry, NaN where a part's sum is)
+      const float inv = t == 0.f ? 0.f : 1.f / t;
       *reinterpret_cast<uint32_t*>(row + de) = pack_bf16x2(x * inv, y * inv);
     }
     __syncthreads();

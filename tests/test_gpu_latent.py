@@ -511,6 +511,19 @@ def test_prefill_long_at_some_rows(dev):
     prefill_case(dev, [400], [5000], 8, 128, 64, 128, seed=52, rows={0, 127, 128, 399})
 
 
+def test_prefill_items_by_halves(dev):
+    """Six items of 256 queries a head, a few more than the device has SMs: those of the second round are
+    taken by single tiles of 128 queries.  (One sequence's last item has no second tile.)"""
+    H = (torch.cuda.get_device_properties(dev).multi_processor_count + 20) // 6 + 1
+    prefill_case(dev, [300, 77, 700], [333, 77, 700], H, 32, 16, 32, seed=53,
+                 rows={0, 127, 128, 255, 256, 299, 300, 376, 377, 633, 1076})
+
+
+@pytest.mark.parametrize("scale", [-0.07, 0.0])
+def test_prefill_negative_and_zero_scale(dev, scale):
+    prefill_case(dev, [200, 30], [200, 170], 2, 128, 64, 128, seed=58, scale=scale)
+
+
 def test_prefill_other_sequences_stay_out(dev):
     """NaN in every row of the sequences before and after, and behind the last one."""
     def mutate(q, kv, kr):
