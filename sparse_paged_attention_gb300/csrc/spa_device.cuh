@@ -313,6 +313,13 @@ __device__ __forceinline__ void bulk_copy_cluster(uint32_t cluster_dst, uint32_t
       ::"r"(cluster_dst), "r"(src), "r"(bytes), "r"(cluster_bar)
       : "memory");
 }
+// Bulk copy from global to this CTA's shared memory, same alignment; its bytes count on `bar`.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+      "l"(src), "r"(bytes), "r"(bar)
+      : "memory");
+}
 // Cluster-wide barrier of all threads of all CTAs (every thread arrives once per phase).
 __device__ __forceinline__ void cluster_arrive() {
   asm volatile("barrier.cluster.arrive.release;" ::: "memory");

@@ -58,7 +58,7 @@ struct LatentDecodeArgs {
   int T, H;
 };
 cudaError_t prepare_latent_decode();   // per-device one-time attributes (dynamic shared memory)
-size_t latent_decode_workspace(const LatentDecodeArgs& a, int sms);
+size_t latent_decode_workspace(const LatentDecodeArgs& a, bool fp8, int sms);
 cudaError_t launch_latent_decode(const LatentDecodeArgs& a, bool fp8, void* workspace, int sms,
                                  cudaStream_t stream);
 cudaError_t read_and_clear_latent_decode_error_word(int* value);

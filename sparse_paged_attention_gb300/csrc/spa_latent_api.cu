@@ -163,7 +163,7 @@ int latent_decode(const spa_latent_pool_t* pool, const spa_latent_problem_t* pr,
   if (st) return st;
   spa::LatentDecodeArgs a;
   fill_decode(a, pool, pr, out, fp8);
-  const size_t need = spa::latent_decode_workspace(a, sms);
+  const size_t need = spa::latent_decode_workspace(a, fp8, sms);
   if (need > 0) {
     if (!workspace) return SPA_ERR_NULL;
     if (!aligned16(workspace)) return SPA_ERR_ALIGN;
@@ -218,7 +218,7 @@ size_t sparse_attn_latent_decode_workspace_size(const spa_latent_problem_t* prob
   if (spa::api_current_device(&dev, &sms) != SPA_OK) return 0;
   spa::LatentDecodeArgs a;
   fill_decode(a, pool, prob, nullptr, false);
-  return spa::latent_decode_workspace(a, sms);
+  return spa::latent_decode_workspace(a, pool->scale != nullptr, sms);
 }
 
 int sparse_attn_latent_decode(const spa_latent_pool_t* pool, const spa_latent_problem_t* prob,

@@ -51,8 +51,6 @@
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
-#include <type_traits>
-
 #include "spa_latent.h"
 #include "spa_launch.h"
 
@@ -121,6 +119,8 @@ struct DecodeParams {
   int2* cut;                   // [slices * groups]: the token cut at the end of a slice, its last slice
   float* lse;                  // [slices * groups][2][64], log2 units
   float* part;                 // [slices * groups][2][64][L]
+  uint8_t* q_codes;            // e4m3: [T * groups][chunks][64 rows of the high term, 64 of the low][128]
+  float* q_scale;              // e4m3: [T * groups][64], 2^-5 over the power of two in the codes
 };
 
 __device__ __forceinline__ int tiles_of(int len) { return len > 0 ? (len + kKeys - 1) / kKeys : 1; }
@@ -134,6 +134,65 @@ __device__ __forceinline__ int token_len(const LatentDecodeArgs& a, int t, int& 
   bad = b < 0 || b >= a.pool.B || (long long)pos >= cap;
   if (b < 0 || b >= a.pool.B || pos < 0) return 0;
   return (int)((long long)pos + 1 < cap ? (long long)pos + 1 : cap);
+}
+
+// e4m3: q as two e4m3 terms times a power of two per head, in the order of the MMA's operand in shared
+// memory (a chunk of 128 columns: 64 rows of the high term, 64 of the low, swizzled), once a token
+// instead of once in every CTA that takes part in it (which measured 18,000 cycles before the first
+// product, the code being cold and its conversions slow).  A warp takes a head; the last R columns
+// repeat the rotary part, against the low codes of the rows.
+__global__ void __launch_bounds__(256)
+    latent_q_kernel(const __grid_constant__ LatentDecodeArgs a, int groups, uint8_t* __restrict__ codes,
+                    float* __restrict__ scales) {
+  pdl_launch_dependents();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int nlp = a.pool.L >> 3, nrp = a.pool.R >> 3, n_chunks = (a.pool.row_bytes + 127) >> 7;
+  const long long units = (long long)a.T * groups * (kHeads / 8);
+  for (long long u = blockIdx.x; u < units; u += gridDim.x) {
+    const long long tg = u / (kHeads / 8), t = tg / groups;
+    const int h = (int)(u % (kHeads / 8)) * 8 + warp, hg = (int)(tg % groups) * kHeads + h;
+    const uint4* ql = reinterpret_cast<const uint4*>(a.q_latent + t * a.ql_st + hg * a.ql_sh);
+    const uint4* qr = reinterpret_cast<const uint4*>(a.q_rope + t * a.qr_st + hg * a.qr_sh);
+    uint4 x[3];                                // pieces of eight values
+    uint32_t mb = 0;                           // largest magnitude (NaN if there is one)
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+      const int o = lane + 32 * i, r = o - nlp;
+      x[i] = make_uint4(0, 0, 0, 0);
+      if (hg < a.H && r < 2 * nrp) x[i] = r < 0 ? __ldg(ql + o) : __ldg(qr + (r < nrp ? r : r - nrp));
+      const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        mb = max(mb, w[e] & 0x7fffu);          // (bf16's bits order as their magnitudes do)
+        mb = max(mb, (w[e] >> 16) & 0x7fffu);
+      }
+    }
+    mb = __reduce_max_sync(0xffffffffu, mb);
+    const float m = bf16_lo(mb);
+    const bool finite = mb < 0x7f80u;          // (else the head's scores become NaN through its scale)
+    const float qs = finite && m > 0.f ? pow2_floor(448.f / m) : 1.f;
+    if (lane == 0) scales[tg * kHeads + h] = finite ? 0.03125f / qs : __int_as_float(0x7fffffff);
+    // piece o: chunk o / 16, 16-byte unit (o / 2) & 7 of the row
+    uint8_t* dst = codes + tg * ((long long)n_chunks * 16384) + h * 128;
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+      const int o = lane + 32 * i;
+      if (o >= 16 * n_chunks) continue;
+      const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+      uint32_t hi[4], lo[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float y = bf16_lo(w[e]) * qs, z = bf16_hi(w[e]) * qs;
+        hi[e] = e4m3x2(y, z);
+        const __half2_raw hr = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)hi[e], __NV_E4M3);
+        const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&hr));
+        lo[e] = e4m3x2(y - v.x, z - v.y);
+      }
+      uint8_t* d = dst + (o >> 4) * 16384 + ((((o >> 1) & 7) ^ (h & 7)) << 4) + (o & 1) * 8;
+      *reinterpret_cast<uint2*>(d) = make_uint2(hi[0] | (hi[1] << 16), hi[2] | (hi[3] << 16));
+      *reinterpret_cast<uint2*>(d + 8192) = make_uint2(lo[0] | (lo[1] << 16), lo[2] | (lo[3] << 16));
+    }
+  }
 }
 
 template <bool kFp8>
@@ -152,7 +211,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(BAR(C::kFullB + i), p.boxed ? 1 : 128);   // armed by the loader, or cp.async's threads
       mbar_init(BAR(C::kEmptyB + i), 1);
     }
-    mbar_init(BAR(C::kQFullB), 8);           // two lanes of four q warps, or one of the softmax warps'
+    mbar_init(BAR(C::kQFullB), kFp8 ? 1 : 4);
     mbar_init(BAR(C::kQEmptyB), 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(BAR(C::kSFullB + i), 1);
@@ -178,7 +237,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = warp_uniform(*reinterpret_cast<volatile uint32_t*>(sm + C::kMiscOff));
   pdl_launch_dependents();
-  pdl_wait();   // nothing global before the grid before this one is done
+  // Nothing global before the grid before this one is done: e4m3, latent_q_kernel, whose results only the
+  // q warps read (it began after everything before it was done).
+  if (!kFp8) pdl_wait();
 
   const LatentDecodeArgs& a = p.a;
   const int L = a.pool.L, R = a.pool.R, W = a.pool.row_bytes;
@@ -192,75 +253,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
   const int g = blockIdx.x % p.groups;                  // this CTA's 64 heads
   const int slice = blockIdx.x / p.groups;
-
-  // e4m3: the q of token t, the CTA's item-th, into shared memory as two terms: kPer threads a head (thread
-  // id `tid`), its pieces of eight values in turn, read twice: for the maximum and to convert.
-  const auto put_codes = [&](auto per_head, int t, int tid, int item) -> bool {
-    constexpr int kPer = decltype(per_head)::value;
-    const int h = tid / kPer, part = tid % kPer, hg = g * kHeads + h;
-    const int np = (L + R) >> 3, nlp = L >> 3, nrp = R >> 3;
-    constexpr int kPieces = (kLatMaxDim + kLatMaxRope) / 8 / kPer, kBatch = 6;
-    static_assert(kPieces % kBatch == 0, "batches of loads");
-    const uint4* ql = reinterpret_cast<const uint4*>(a.q_latent + t * a.ql_st + hg * a.ql_sh);
-    const uint4* qr = reinterpret_cast<const uint4*>(a.q_rope + t * a.qr_st + hg * a.qr_sh);
-    uint4 u[kBatch];
-    const auto load = [&](int i0) {            // a batch's loads in flight together
-#pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        const int pc = kPer * (i0 + i) + part;
-        u[i] = make_uint4(0, 0, 0, 0);
-        if (hg < a.H && pc < np) u[i] = __ldg(pc < nlp ? ql + pc : qr + (pc - nlp));
-      }
-    };
-    float m = 0.f;
-#pragma unroll 1
-    for (int i0 = 0; i0 < kPieces; i0 += kBatch) {
-      load(i0);
-#pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        const uint32_t w[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) m = fmaxf(m, fmaxf(fabsf(bf16_lo(w[e])), fabsf(bf16_hi(w[e]))));
-      }
-    }
-#pragma unroll
-    for (int o = 1; o < kPer; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    const float qs = m > 0.f ? pow2_floor(448.f / m) : 1.f;
-    if (!warp_wait(BAR(C::kQEmptyB), (uint32_t)((item & 1) ^ 1), abort_flag)) return false;
-    if (part == 0)
-      reinterpret_cast<float*>(sm + C::kQScaleOff)[(item & 3) * kHeads + h] = 0.03125f / qs;
-    // piece pc: bytes 8 pc of the row: chunk pc / 16, 16-byte unit (pc / 2) & 7, swizzled by row
-    const auto put = [&](int pc, uint2 hi, uint2 lo) {
-      uint8_t* d = sm + C::kQOff + (pc >> 4) * 16384 + h * 128 + ((((pc >> 1) & 7) ^ (h & 7)) << 4) +
-                   (pc & 1) * 8;
-      *reinterpret_cast<uint2*>(d) = hi;
-      *reinterpret_cast<uint2*>(d + 64 * 128) = lo;
-    };
-#pragma unroll 1
-    for (int i0 = 0; i0 < kPieces; i0 += kBatch) {
-      load(i0);
-#pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        const int pc = kPer * (i0 + i) + part;
-        const uint32_t w[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
-        uint32_t hi[4], lo[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float x = bf16_lo(w[e]) * qs, y = bf16_hi(w[e]) * qs;
-          hi[e] = e4m3x2(x, y);
-          const __half2_raw hr = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)hi[e], __NV_E4M3);
-          const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&hr));
-          lo[e] = e4m3x2(x - v.x, y - v.y);
-        }
-        const uint2 h2 = make_uint2(hi[0] | (hi[1] << 16), hi[2] | (hi[3] << 16));
-        const uint2 l2 = make_uint2(lo[0] | (lo[1] << 16), lo[2] | (lo[3] << 16));
-        if (pc < np) put(pc, h2, l2);
-        if (pc >= nlp && pc < np) put(pc + nrp, h2, l2);   // against the low codes of the rows too
-      }
-    }
-    for (int pc = np + nrp + part; pc < 16 * n_chunks; pc += kPer) put(pc, make_uint2(0, 0), make_uint2(0, 0));
-    return true;
-  };
 
   if (warp == 13) {
     // ================================ schedule and loads ==================================
@@ -615,7 +607,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     // Each token's q is read into registers as soon as its first tile is announced, and put in
     // place once the token before has no S left to compute.
     const int tid = threadIdx.x - kSoftmax;
-    int items = kFp8 ? 1 : 0, buf = 0, flags = 0;      // (e4m3: the first is the softmax warps')
+    int items = 0, buf = 0, flags = 0;
+    if (kFp8) pdl_wait();           // (for latent_q_kernel, launched right before)
     auto put_q = [&](int t) -> bool {
       if constexpr (!kFp8) {
         // TMEM lane 32w + l is head 32(w & 1) + l; its first (w < 2) or second half of the latents
@@ -666,18 +659,32 @@ __global__ void __launch_bounds__(kThreads, 1)
           *reinterpret_cast<uint4*>(sm + C::kQOff + hr * 128 + (((tid & 7) ^ (hr & 7)) << 4)) = v[i];
         }
       } else {
-        if (!put_codes(std::integral_constant<int, 2>(), t, tid, items)) return false;
+        // latent_q_kernel's codes and scales of 64 heads: two plain copies
+        if (warp == 8) {
+          if (!warp_wait(BAR(C::kQEmptyB), (uint32_t)((items & 1) ^ 1), abort_flag)) return false;
+          if (elect_one()) {
+            const size_t at = (size_t)t * p.groups + g;
+            const uint32_t bytes = (uint32_t)n_chunks * 16384;
+            mbar_arrive_expect_tx(BAR(C::kQFullB), bytes + kHeads * 4);
+            bulk_load(sb + C::kQOff, p.q_codes + at * bytes, bytes, BAR(C::kQFullB));
+            bulk_load(sb + C::kQScaleOff + (items & 3) * kHeads * 4, p.q_scale + at * kHeads, kHeads * 4,
+                      BAR(C::kQFullB));
+          }
+          __syncwarp();
+        }
+        ++items;
+        return true;
       }
       fence_proxy_async_smem();
       tc_fence_before();
       __syncwarp();
-      if (lane < 2) mbar_arrive(BAR(C::kQFullB));
+      if (lane == 0) mbar_arrive(BAR(C::kQFullB));
       ++items;
       return true;
     };
     // (a boxed CTA's first token does not wait for the page table; cp.async copies rows first)
     bool ok = true;
-    if (!kFp8 && p.boxed) {
+    if (p.boxed) {
       ok = warp_wait(BAR(C::kTokenB), 0, abort_flag);
       const int t = *reinterpret_cast<volatile int*>(sm + C::kMiscOff + 8);
       if (ok && t >= 0) ok = put_q(t);
@@ -718,9 +725,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(BAR(C::kInfoEmptyB + ri));
-      if ((flags & kFirst) && !((kFp8 || p.boxed) && k == 0) && !put_q(t)) break;
+      if ((flags & kFirst) && !(p.boxed && k == 0) && !put_q(t)) break;
     }
     cp_async_wait_all();
+    if (kFp8 && warp == 8 && items > 0) {      // (a copy in flight, where the CTA gave up)
+      mbar_wait_drain(BAR(C::kQFullB), (uint32_t)((items - 1) & 1));
+      __syncwarp();
+    }
   } else {
     // ================================ softmax and epilogue ================================
     const int tid = threadIdx.x;
@@ -757,17 +768,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       return __shfl_sync(0xffffffffu, (c >= 32) == (pair != 0) ? own : other, c & 31);
     };
     int flags = 0, buf = kBufs - 1;
-    if (kFp8) {                                    // the first token's q: nothing else to do before it
-      ok = warp_wait(BAR(C::kTokenB), 0, abort_flag);
-      const int t = *reinterpret_cast<volatile int*>(sm + C::kMiscOff + 8);
-      if (ok && t >= 0) {
-        ok = put_codes(std::integral_constant<int, 4>(), t, tid, 0);
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(BAR(C::kQFullB));
-      }
-    }
-    ok = warp_wait(BAR(C::kInfoFullB), 0, abort_flag) && ok;
+    ok = warp_wait(BAR(C::kInfoFullB), 0, abort_flag);
     const bool any = named_bar_and(1, kSoftmax, ok && !(infos[0].flags & kEnd));
     for (int k = 0; any && !(flags & kFinal); ++k) {
       const int ri = k % kRing, s = k % C::kSBufs;
@@ -1246,15 +1247,18 @@ int slices_of(const LatentDecodeArgs& a, int sms) {
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
 struct Workspace {
-  size_t cut, lse, part, bytes;
+  size_t cut, lse, part, codes, scale, bytes;
 };
-Workspace workspace_layout(const LatentDecodeArgs& a, int sms) {
+Workspace workspace_layout(const LatentDecodeArgs& a, bool fp8, int sms) {
   const size_t ctas = (size_t)slices_of(a, sms) * ((a.H + kHeads - 1) / kHeads);
   Workspace w;
   w.cut = 0;
   w.lse = align256(ctas * sizeof(int2));
   w.part = w.lse + align256(ctas * 2 * kHeads * sizeof(float));
-  w.bytes = w.part + ctas * 2 * kHeads * (size_t)a.pool.L * sizeof(float);
+  w.codes = align256(w.part + ctas * 2 * kHeads * (size_t)a.pool.L * sizeof(float));
+  const size_t tokens = fp8 ? (size_t)a.T * ((a.H + kHeads - 1) / kHeads) : 0;
+  w.scale = w.codes + tokens * ((a.pool.L + 2 * a.pool.R + 127) / 128) * 16384;
+  w.bytes = w.scale + tokens * kHeads * sizeof(float);
   return w;
 }
 
@@ -1262,7 +1266,7 @@ template <bool kFp8>
 cudaError_t launch(const DecodeParams& p, cudaStream_t stream, unsigned grid) {
   using C = Cfg<kFp8>;
   return launch_with_pdl(latent_decode_kernel<kFp8>, dim3(grid), dim3(kThreads), C::kSmem, stream,
-                         false, p);
+                         kFp8, p);
 }
 
 }  // namespace
@@ -1274,8 +1278,8 @@ cudaError_t prepare_latent_decode() {
   return e;
 }
 
-size_t latent_decode_workspace(const LatentDecodeArgs& a, int sms) {
-  return workspace_layout(a, sms).bytes;
+size_t latent_decode_workspace(const LatentDecodeArgs& a, bool fp8, int sms) {
+  return workspace_layout(a, fp8, sms).bytes;
 }
 
 cudaError_t launch_latent_decode(const LatentDecodeArgs& a, bool fp8, void* workspace, int sms,
@@ -1285,11 +1289,13 @@ cudaError_t launch_latent_decode(const LatentDecodeArgs& a, bool fp8, void* work
   p.groups = (a.H + kHeads - 1) / kHeads;
   p.slices = slices_of(a, sms);
   p.scale_log2 = a.scale * 1.4426950408889634f;
-  const Workspace w = workspace_layout(a, sms);
+  const Workspace w = workspace_layout(a, fp8, sms);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   p.cut = reinterpret_cast<int2*>(ws + w.cut);
   p.lse = reinterpret_cast<float*>(ws + w.lse);
   p.part = reinterpret_cast<float*>(ws + w.part);
+  p.q_codes = ws + w.codes;
+  p.q_scale = reinterpret_cast<float*>(ws + w.scale);
   // Pages of a multiple of 64 entries: a tile is 64 consecutive rows, and one tensor-map copy brings all
   // its whole 128-byte chunks in slot order (bf16: pairs of the two halves, so only where all pair
   // up); the chunks left over come one by one.  Other pages: cp.async, any row anywhere.
@@ -1315,7 +1321,18 @@ cudaError_t launch_latent_decode(const LatentDecodeArgs& a, bool fp8, void* work
     }
   }
   const unsigned grid = (unsigned)p.slices * (unsigned)p.groups;
-  cudaError_t e = fp8 ? launch<true>(p, stream, grid) : launch<false>(p, stream, grid);
+  cudaError_t e;
+  if (fp8) {
+    // The codes first.  Not as a dependent grid itself, so that what the decode kernel reads before it
+    // waits for the codes is there.
+    const long long units = (long long)a.T * p.groups * (kHeads / 8);
+    const unsigned blocks = (unsigned)(units < 8LL * sms ? units : 8LL * sms);
+    e = launch_with_pdl(latent_q_kernel, dim3(blocks), dim3(256), 0, stream, false, a, p.groups, p.q_codes,
+                        p.q_scale);
+    if (e == cudaSuccess) e = launch<true>(p, stream, grid);
+  } else {
+    e = launch<false>(p, stream, grid);
+  }
   if (e != cudaSuccess) return e;
   return launch_with_pdl(latent_merge_kernel, dim3(4 * (unsigned)sms), dim3(32 * kMergeWarps), 0,
                          stream, true, (const int2*)p.cut, (const float*)p.lse,
