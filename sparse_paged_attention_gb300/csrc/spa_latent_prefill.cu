@@ -69,7 +69,8 @@ static_assert(kSmem <= 232448, "shared memory budget");
 struct PrefillParams {
   CUtensorMap q, kn, kr, v;
   LatentPrefillArgs a;
-  float scale_log2;        // |scale| log2(e)
+  float scale_log2;        // |scale| log2(e), never 0 (times a masked key's -inf it would be NaN): a scale of
+  int q_zero;              // 0 is q = 0, read past the last row, instead
   int negate;              // scale < 0
 };
 
@@ -247,7 +248,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           mbar_arrive_expect_tx(BAR(B_QFULL + t), (uint32_t)(nc * kChunk));
           for (int c = 0; c < nc; ++c)
             tma_box3(sb + kQOff + (t * 3 + c) * kChunk, &p.q, c < nkc ? 64 * c : a.dn, it.head,
-                     it.q0 + t * kTile, BAR(B_QFULL + t));
+                     p.q_zero ? a.num_q : it.q0 + t * kTile, BAR(B_QFULL + t));
         }
         __syncwarp();
       }
@@ -484,10 +485,6 @@ __global__ void __launch_bounds__(kThreads, 1)
               x[c][i] = fast_exp2(x[c][i]);
               x[c][i + 1] = fast_exp2(x[c][i + 1]);
             }
-            if (masked) {
-#pragma unroll
-              for (int i = 0; i < 32; ++i) x[c][i] = 32 * c + i <= left ? x[c][i] : 0.f;
-            }
             uint32_t w[16];
 #pragma unroll
             for (int i = 0; i < 16; ++i) w[i] = pack_bf16x2(x[c][2 * i], x[c][2 * i + 1]);
@@ -558,6 +555,8 @@ cudaError_t launch_latent_prefill(const LatentPrefillArgs& a, int sms, cudaStrea
   p.a = a;
   p.scale_log2 = fabsf(a.scale) * 1.4426950408889634f;
   p.negate = a.scale < 0.f;
+  p.q_zero = p.scale_log2 == 0.f;
+  if (p.q_zero) p.scale_log2 = 1.f;
   if (!encode_bf16_3d(&p.q, a.q, a.dn + a.dr, a.H, a.q_sh, a.num_q, a.q_st, 1, kTile))
     return cudaErrorInvalidValue;
   if (a.num_k > 0) {   // (without keys every output row is zero and none of these is used)
