@@ -188,7 +188,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       long long i = (long long)n * gridDim.x + ((n & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
       int from = 0, upto = 2 * kTile;        // queries of the item that this CTA takes
       if (halves && i >= whole) {
-        from = (int)(i - whole & 1) * kTile;
+        from = (int)((i - whole) & 1) * kTile;
         upto = from + kTile;
         i = whole + (i - whole) / 2;
       }

@@ -334,6 +334,31 @@ def test_decode_scores_of_any_size(dev):
     decode_case(dev, [200, 70], 16, 128, 16, 16, True, seed=36, scale=-0.1)
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("lens", [[70], [4000]])
+def test_decode_query_that_is_not_finite(dev, lens, fp8):
+    """NaN or infinity in one head's query makes that head's output NaN and leaves the others alone."""
+    inp = latent_inputs(lens, 512, 64, 64, seed=31)
+    pool, _, _, _ = place(inp, fp8, dev)
+    g = torch.Generator().manual_seed(131)
+    ql = torch.randn((1, 70, 512), generator=g).to(torch.bfloat16).to(dev)
+    qr = torch.randn((1, 70, 64), generator=g).to(torch.bfloat16).to(dev)
+    pos = torch.tensor([lens[0] - 1], dtype=torch.int32, device=dev)
+    f = spa.sparse_attn_latent_decode_fp8 if fp8 else spa.sparse_attn_latent_decode
+    want = f(ql, qr, pool, pos, scale=0.04)
+    assert torch.isfinite(want).all()
+    ql[0, 3, 100] = float("nan")
+    ql[0, 66, 511] = float("inf")
+    qr[0, 40, 5] = float("-inf")
+    got = f(ql, qr, pool, pos, scale=0.04)
+    gone = torch.tensor([3, 40, 66], device=dev)
+    assert torch.isnan(got[0, gone]).all()
+    rest = torch.ones(70, dtype=torch.bool, device=dev)
+    rest[gone] = False
+    assert torch.equal(got[0, rest], want[0, rest])
+    assert spa.sparse_attn_paged_check_errors() == 0
+
+
 def test_decode_rows_of_very_different_scales(dev):
     """e4m3 rows whose scales differ by factors of 2^40."""
     def mutate(pool, inp, sid):
