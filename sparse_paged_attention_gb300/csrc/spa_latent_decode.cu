@@ -38,9 +38,10 @@
 //   warp 13     schedule and page tables, two tiles ahead; tensor-map copies (pages of a multiple of 64
 //               entries: a tile is then one box of rows by 128-byte chunks, a single copy)
 //
-// Schedule: the tiles of all tokens are one long line; each slice of CTAs (one CTA for every 64
-// heads) takes an equal stretch of it.  So the work is balanced whatever the sequence lengths,
-// without knowing them on the host.  A token whose tiles lie in one slice is finished there;
+// Schedule: the tiles of all tokens are one long line, each token with a few tiles' room for what it costs
+// beside them (its q, its epilogue); each slice of CTAs (one CTA for every 64 heads) takes an equal
+// stretch of it.  So the work is balanced whatever the sequence lengths, without knowing them on the
+// host.  A token whose tiles lie in one slice is finished there;
 // the parts of a token that was cut go to the workspace, normalised, with their log-sum-exp, and
 // latent_merge_kernel joins them in the order of the slices.
 //
@@ -50,9 +51,9 @@
 // more), the second the mantissa of the large ones.
 //
 // Measured (L = 512, R = 64, calls one after the other, inputs larger than L2):
-//   64 sequences of up to 16,004 entries, 128 heads, bf16: 190 us (759 TFLOP/s, 40% of the measured bf16
-//     rate; 3.2 TB/s); 13 of them are the merge
-//   48 sequences of up to 11,581 entries, 2 tokens each, 64 heads, e4m3: 150 us, where a tile is about
+//   64 sequences of up to 16,004 entries, 128 heads, bf16: 183 us (790 TFLOP/s, 42% of the measured bf16
+//     rate; 3.4 TB/s); 10 of them are the merge
+//   48 sequences of up to 11,581 entries, 2 tokens each, 64 heads, e4m3: 144 us, where a tile is about
 //     2,700 cycles of the softmax warps (swap, maxima, exponentials, the two terms of P, each a few
 //     hundred cycles and one after the other) against 1,730 of its MMAs
 //   one sequence of 131,071 entries, 16 heads, e4m3: 43 us; one of 4,097, 64 heads, bf16: 23 us, of which
@@ -80,6 +81,8 @@ constexpr int kSCol = 256, kQCol = 384;   // TMEM columns: O^T from 0, S, q
 constexpr int kSoftmax = 256;     // threads of the softmax warps
 constexpr int kThreads = kSoftmax + 224;
 constexpr int kMinTiles = 2;      // tiles of a slice at least: fewer would cost more in merging
+constexpr int kTokenCost = 6;     // what a token costs its CTA beside its tiles, in tiles (measured: 0 took 190
+                                  // and 150 us where 6 takes 183 and 144, see below)
 
 // first and last tile of this CTA's part of a token, its last tile of all, no tile at all
 enum { kFirst = 1, kLast = 2, kFinal = 4, kEnd = 8 };
@@ -281,22 +284,39 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     };
     load_chunk(0);
-    long long total = lane < a.T ? tiles_of(c_len) : 0;
-    for (int t = lane + 32; t < a.T; t += 32) {
-      int b;
-      bool bad;
-      total += tiles_of(token_len(a, t, b, bad));
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-    long long per = (total + p.slices - 1) / p.slices;
-    if (per < kMinTiles) per = kMinTiles;
-    const long long begin = per * slice;
-    const long long end = begin + per < total ? begin + per : total;
-
+    const auto quotient = [](long long x, long long y) {   // (a 64-bit division takes some 100 instructions)
+      return x < 0x80000000LL && y < 0x80000000LL ? (long long)((uint32_t)x / (uint32_t)y) : x / y;
+    };
+    // The line: a token that begins at w has its tile 0 there, and tile j > 0 at w + cost + j.  A slice takes
+    // the tiles from per * slice to before per * (slice + 1).  (cost < per, so that a token has tiles in
+    // every slice from its first to its last.)
+    int cost = 0;
+    long long per;
     int it_t = 0, it_j = 0;                    // next tile: token, tile of the token
-    if (begin < end) {
-      long long before = 0;
+    long long w_tok = 0;                       // where that token begins
+    int left_all = 0;                          // tiles to go
+    if (a.T == 1) {                            // nothing to weigh
+      const int n = tiles_of(__shfl_sync(0xffffffffu, c_len, 0));
+      const int each = max((n + p.slices - 1) / p.slices, kMinTiles);
+      it_j = (int)min((long long)each * slice, (long long)n);
+      left_all = min(each, n - it_j);
+      per = each;
+    } else {
+      long long total = lane < a.T ? tiles_of(c_len) : 0;
+      for (int t = lane + 32; t < a.T; t += 32) {
+        int b;
+        bool bad;
+        total += tiles_of(token_len(a, t, b, bad));
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+      cost = (int)min((long long)kTokenCost,
+                      max(quotient(total + p.slices - 1, p.slices), (long long)kMinTiles) - 1);
+      per = max(quotient(total + (long long)cost * a.T + p.slices - 1, p.slices), (long long)kMinTiles);
+      const long long begin = per * slice, end = begin + per;
+      bool found = false;
+      int chunk = 0;
+      long long w0 = 0;
       for (;; load_chunk(t0 + 32)) {
         const int n = t0 + lane < a.T ? tiles_of(c_len) : 0;
         int sum = n;                           // inclusive scan (32 tokens: below 2^31 tiles)
@@ -305,32 +325,39 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int x = __shfl_up_sync(0xffffffffu, sum, o);
           if (lane >= o) sum += x;
         }
-        const int all = __shfl_sync(0xffffffffu, sum, 31);
-        if (begin < before + all) {
-          const unsigned m = __ballot_sync(0xffffffffu, begin < before + sum);
+        const long long w = w0 + (sum - n) + (long long)cost * lane;
+        const auto before = [&](long long x) {   // tiles of this lane's token before x
+          return x <= w ? 0 : (int)min((long long)n, max(1LL, x - w - cost));
+        };
+        const int lo = before(begin);
+        left_all += before(end) - lo;
+        const unsigned m = __ballot_sync(0xffffffffu, lo < n);
+        if (!found && m) {
           const int k = __ffs(m) - 1;
+          found = true;
+          chunk = t0;
           it_t = t0 + k;
-          it_j = (int)(begin - before - (__shfl_sync(0xffffffffu, sum, k) -
-                                         __shfl_sync(0xffffffffu, n, k)));
-          break;
+          it_j = __shfl_sync(0xffffffffu, lo, k);
+          w_tok = __shfl_sync(0xffffffffu, w, k);
         }
-        before += all;
+        w0 += __shfl_sync(0xffffffffu, sum, 31) + 32LL * cost;
+        if (t0 + 32 >= a.T || w0 >= end) break;
       }
+      left_all = __reduce_add_sync(0xffffffffu, left_all);
+      if (t0 != chunk) load_chunk(chunk);
     }
-    const int ps_shift = (a.pool.ps & (a.pool.ps - 1)) == 0 ? __ffs(a.pool.ps) - 1 : -1;
     if (lane == 0) {                           // the first token's q can be on its way
-      *reinterpret_cast<volatile int*>(sm + C::kMiscOff + 8) = begin < end ? it_t : -1;
+      *reinterpret_cast<volatile int*>(sm + C::kMiscOff + 8) = left_all > 0 ? it_t : -1;
       mbar_arrive(BAR(C::kTokenB));
     }
     struct Tile {
       int t, flags, slot;
       int blk[2], off[2];                      // block and slot in it of entries lane, 32 + lane
     };
-    int left_all = begin < end ? (int)min(end - begin, (long long)0x7fffffff) : 0;   // tiles to go
     // The token of the next tile: its sequence, tiles to go, entries to go, whether its first tile is
     // this CTA's; and, boxed (tiles lie in one page each), the slot in the page and the blocks of tiles
     // c_tile .. c_tile + 31, one a lane.
-    int b_t = 0, left = 0, entries = 0, started = 0, off = 0, c_tile = 0, c_blk = -1;
+    int b_t = 0, n_tok = 0, left = 0, entries = 0, started = 0, off = 0, c_tile = 0, c_blk = -1;
     bool fresh = true;
     int2 cut = make_int2(-1, 0);
     const auto begin_token = [&]() {
@@ -340,11 +367,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       b_t = __shfl_sync(0xffffffffu, c_seq, k);
       started = it_j == 0;
       if (started && __shfl_sync(0xffffffffu, c_bad, k) && lane == 0) flag_error(SPA_ERR_INDEX);
-      left = tiles_of(len) - it_j;
+      n_tok = tiles_of(len);
+      left = n_tok - it_j;
       entries = len - it_j * kKeys;
       if (started && left > left_all)          // (the line ends inside it: the slice where it ends)
-        cut = make_int2(it_t, (int)((end - left_all + left - 1) / per));
-      if (p.boxed) off = (int)(((long long)it_j * kKeys) % a.pool.ps);
+        cut = make_int2(it_t, (int)quotient(w_tok + cost + n_tok - 1, per));
+      if (p.boxed) off = it_j % (a.pool.ps / kKeys) * kKeys;
       c_tile = it_j - 32;
       fresh = true;
     };
@@ -353,6 +381,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       x.t = -1;
       if (left_all == 0) return;
       if (left == 0) {
+        w_tok += cost + n_tok;
         ++it_t;
         it_j = 0;
         begin_token();
@@ -1076,6 +1105,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 constexpr int kMergeWarps = 8;
 constexpr int kMergeMaxCuts = 1024;
 constexpr int kWarpParts = 8;
+constexpr int kParts = 20;          // loads in flight a warp: all of its parts of 152 slices
 
 __global__ void __launch_bounds__(32 * kMergeWarps)
     latent_merge_kernel(const int2* __restrict__ cut, const float* __restrict__ lse,
@@ -1087,6 +1117,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps)
   __shared__ int2 cuts[kMergeMaxCuts];
   __shared__ float2 stat[kMergeWarps];
   __shared__ int n_items, n_units;
+  __shared__ int2 warp_sum[kMergeWarps];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int nq = (L + 127) >> 7;
   pdl_wait();
@@ -1096,29 +1127,34 @@ __global__ void __launch_bounds__(32 * kMergeWarps)
     if (s < slices) cuts[s] = cut[(size_t)s * groups];
   }
   __syncthreads();
-  if (warp == 0) {
-    int n = 0, units = 0;
-    for (int s0 = 0; s0 < slices; s0 += 32) {
-      const int s = s0 + lane;
-      const int2 c = s < slices ? cuts[s] : make_int2(-1, 0);
-      const unsigned m = __ballot_sync(0xffffffffu, c.x >= 0);
-      const int mine = c.x < 0 ? 0 : (c.y - s + 1 <= kWarpParts ? (H + kMergeWarps - 1) / kMergeWarps : H * nq);
-      int scan = mine;
+  // A thread takes a slice; the items and units before it are its warp's scan and the warps' before.
+  for (int s0 = 0; s0 < slices; s0 += 32 * kMergeWarps) {
+    const int s = s0 + threadIdx.x;
+    const int2 c = s < slices ? cuts[s] : make_int2(-1, 0);
+    const unsigned m = __ballot_sync(0xffffffffu, c.x >= 0);
+    const int mine = c.x < 0 ? 0 : (c.y - s + 1 <= kWarpParts ? (H + kMergeWarps - 1) / kMergeWarps : H * nq);
+    int scan = mine;
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int x = __shfl_up_sync(0xffffffffu, scan, o);
-        if (lane >= o) scan += x;
-      }
-      if (c.x >= 0) item[n + __popc(m & ((1u << lane) - 1u))] = make_int4(s, c.y, c.x, units + scan - mine);
-      n += __popc(m);
-      units += __shfl_sync(0xffffffffu, scan, 31);
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, scan, o);
+      if (lane >= o) scan += x;
     }
-    if (lane == 0) {
-      n_items = n;
-      n_units = units;
+    if (lane == 31) warp_sum[warp] = make_int2(__popc(m), scan);
+    __syncthreads();
+    int n = s0 == 0 ? 0 : n_items, units = s0 == 0 ? 0 : n_units;
+#pragma unroll
+    for (int w = 0; w < kMergeWarps; ++w) {
+      const int2 x = warp_sum[w];
+      if (w < warp) n += x.x, units += x.y;
     }
+    if (c.x >= 0) item[n + __popc(m & ((1u << lane) - 1u))] = make_int4(s, c.y, c.x, units + scan - mine);
+    __syncthreads();
+    if (threadIdx.x == 32 * kMergeWarps - 1) {
+      n_items = n + __popc(m);
+      n_units = units + scan;
+    }
+    __syncthreads();
   }
-  __syncthreads();
   for (int u = blockIdx.x; u < n_units; u += gridDim.x) {
     int lo = 0, hi = n_items - 1;          // the last token whose units begin at or before u
     while (lo < hi) {
@@ -1186,15 +1222,15 @@ __global__ void __launch_bounds__(32 * kMergeWarps)
       }
       continue;
     }
-    // eight parts in flight, weighted against the largest of this warp's so far
+    // kParts parts in flight, weighted against the largest of this warp's so far
     const int d = 128 * ((u - it.w) % nq) + 4 * lane;      // (L may end inside the last 128)
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     float M = -INFINITY, tot = 0.f;
-    for (int i0 = warp; i0 < n; i0 += 8 * kMergeWarps) {
-      float e[8];
-      float4 v[8];
+    for (int i0 = warp; i0 < n; i0 += kParts * kMergeWarps) {
+      float e[kParts];
+      float4 v[kParts];
 #pragma unroll
-      for (int z = 0; z < 8; ++z) {
+      for (int z = 0; z < kParts; ++z) {
         const int i = i0 + z * kMergeWarps;
         e[z] = -INFINITY;
         v[z] = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -1206,7 +1242,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps)
       }
       float mx = M;
 #pragma unroll
-      for (int z = 0; z < 8; ++z) mx = fmaxf(mx, e[z]);
+      for (int z = 0; z < kParts; ++z) mx = fmaxf(mx, e[z]);
       // (a NaN among the parts' sums is not seen by the maximum but comes back in its weight)
       const float ref = mx == -INFINITY ? 0.f : mx, f = exp2f(M - ref);
       M = mx;
@@ -1216,7 +1252,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps)
       acc.z *= f;
       acc.w *= f;
 #pragma unroll
-      for (int z = 0; z < 8; ++z) {
+      for (int z = 0; z < kParts; ++z) {
         const float w = exp2f(e[z] - ref);
         tot += w;
         acc.x = fmaf(w, v[z].x, acc.x);
