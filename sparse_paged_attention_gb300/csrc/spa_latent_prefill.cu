@@ -28,16 +28,17 @@
 // other data: masked as keys, blanked as values, not stored as queries.
 //
 // Measured (nope 128, rotary 64, v 128, 64 heads): 8,192 tokens in 0.91 ms (1,500 TFLOP/s: 80% of the
-// measured bf16 burst rate, 89% of the sustained one, the SM clock falling to 1.8 GHz), 2 x 1,024 tokens
-// after a prefix of 12,288 in 0.92 ms (1,210 TFLOP/s: 512 items on 152 CTAs are 3.4 rounds that take 3.5;
-// 4 without the halves).  A step of both tiles takes about 3,900 cycles against 2,560 of its MMAs: S keeps
-// shared memory busy all the time that it runs (8 KB an MMA of 64 cycles), so the copies of K and V
-// stretch it, and between two S pass a commit, the read into registers and an arrival, about 500
-// cycles, which PV fills only in part.  Steps on the way, 8,192 tokens: S_0 and S_1 apart with P in
-// their columns 1.29 ms, P in halves 1.15, one S buffer 0.99, two fp32 operations an instruction and
-// MMAs without waits between them 0.94, one mask instead of two 0.91.  Tried and slower: one warp for
-// both products in a fixed order (1.06 ms; 1.24 with the waits moved under the MMAs), five K chunks and
-// V by halves (1.06), prefetches of K and V into L2 (1.03).
+// measured bf16 burst rate; 1.00 ms and 1,373 TFLOP/s when the chip has been busy for seconds, 81% of
+// the sustained rate), 1,075 and 1,096 tokens after 12,000 in 0.92 ms (1,210 TFLOP/s: 512 items of two
+// tiles and 128 of one on 152 CTAs; 0.97 ms without the halves of the last round).  A step of
+// both tiles takes about 3,900 cycles against 2,560 of its MMAs: S keeps shared memory busy all the time
+// that it runs (8 KB an MMA of 64 cycles), so the copies of K and V stretch it, and between two S pass
+// a commit, the read into registers and an arrival, about 500 cycles, which PV fills only in part.
+// Steps on the way, 8,192 tokens: S_0 and S_1 apart with P in their columns 1.29 ms, P in halves 1.15,
+// one S buffer 0.99, two fp32 operations an instruction and MMAs without waits between them 0.94, one
+// mask instead of two 0.91.  Tried and slower: one warp for both products in a fixed order (1.06 ms;
+// 1.24 with the waits moved under the MMAs), five K chunks and V by halves (1.06), prefetches of K and
+// V into L2 (1.03).
 #include "spa_latent.h"
 #include "spa_launch.h"
 
