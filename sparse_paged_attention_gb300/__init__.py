@@ -603,11 +603,6 @@ def _launch_stream(stream, dev: int) -> int:
     return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
 
 
-def _stride(t, dim) -> int:
-    """A stride in elements; 0 for a dimension of one (whose stride is free)."""
-    return 0 if t.shape[dim] <= 1 else t.stride(dim)
-
-
 def _latent_index(positions, seq_of_token, n, dev):
     """Checked positions and sequence ids of n tokens: their addresses (0: none)."""
     if positions.dtype is not torch.int32 or not positions.is_contiguous() or positions.numel() != n:
@@ -623,12 +618,17 @@ def _latent_index(positions, seq_of_token, n, dev):
 
 
 def _latent_rows(name, t, dims, width, dev):
-    """A bf16 tensor of `dims` dimensions with unit last stride and (if given) last size, on `dev`."""
-    if t.dtype is not torch.bfloat16 or t.dim() != dims or \
-            (width is not None and t.shape[-1] != width) or (t.stride(-1) != 1 and t.shape[-1] > 1):
+    """Shape and leading strides (0 for a dimension of one, whose stride is free) of a bf16 tensor on
+    `dev` of `dims` dimensions with unit last stride and (if given) last size."""
+    shape, st = t.shape, t.stride()
+    if t.dtype is not torch.bfloat16 or len(shape) != dims or \
+            (width is not None and shape[-1] != width) or (st[-1] != 1 and shape[-1] > 1):
         raise ValueError(f"{name} must be a bf16 tensor of {dims} dimensions with unit last stride"
                          + ("" if width is None else f" and {width} values a row"))
-    _same_device(name, t, dev)
+    if t.get_device() != dev:
+        _same_device(name, t, dev)
+    first = st[0] if shape[0] > 1 else 0
+    return (shape, first) if dims == 2 else (shape, first, st[1] if shape[1] > 1 else 0)
 
 
 def _num_seqs(num_seqs, rows):
@@ -643,21 +643,20 @@ def _latent_write(fp8, latent, rope, positions, pool, *, seq_of_token=None, num_
                   stream=None):
     lib = load_library()
     packed, L, R, dev, seqs = _latent_pool(pool, fp8)
-    _latent_rows("latent", latent, 2, L, dev)
-    T = latent.shape[0]
+    (T, _), stride = _latent_rows("latent", latent, 2, L, dev)
     rope_ptr = rope_stride = 0
     if R > 0:
         if rope is None:
             raise ValueError("the pool's rows have a rotary part: rope is missing")
-        _latent_rows("rope", rope, 2, R, dev)
-        if rope.shape[0] != T:
+        (n, _), rope_stride = _latent_rows("rope", rope, 2, R, dev)
+        if n != T:
             raise ValueError("latent and rope must have the same number of rows")
-        rope_ptr, rope_stride = rope.data_ptr(), _stride(rope, 0)
+        rope_ptr = rope.data_ptr()
     pos, seq = _latent_index(positions, seq_of_token, T, dev)
     B = _num_seqs(num_seqs, seqs)
     _current_device(dev)
     fn = lib.sparse_attn_latent_write_fp8 if fp8 else lib.sparse_attn_latent_write
-    st = fn(latent.data_ptr(), _stride(latent, 0), rope_ptr, rope_stride, T, pos, seq, B, packed,
+    st = fn(latent.data_ptr(), stride, rope_ptr, rope_stride, T, pos, seq, B, packed,
             _launch_stream(stream, dev))
     if st != 0:
         raise SpaError(st, fn.__name__)
@@ -683,12 +682,13 @@ def _latent_read(fp8, positions, pool, *, seq_of_token=None, num_seqs=None, out=
     _current_device(dev)
     if out is None:
         out = torch.empty((n, width), dtype=torch.bfloat16, device=pool.rows.device)
+        stride = width if n > 1 else 0
     else:
-        _latent_rows("out", out, 2, width, dev)
-        if out.shape[0] != n:
+        (rows, _), stride = _latent_rows("out", out, 2, width, dev)
+        if rows != n:
             raise ValueError(f"out must have {n} rows")
     fn = lib.sparse_attn_latent_read_fp8 if fp8 else lib.sparse_attn_latent_read
-    st = fn(packed, n, pos, seq, _num_seqs(num_seqs, seqs), out.data_ptr(), _stride(out, 0),
+    st = fn(packed, n, pos, seq, _num_seqs(num_seqs, seqs), out.data_ptr(), stride,
             _launch_stream(stream, dev))
     if st != 0:
         raise SpaError(st, fn.__name__)
@@ -710,16 +710,15 @@ def _latent_decode_args(fp8, q_latent, q_rope, pool, positions, *, scale, seq_of
     """Checked arguments of a latent decode: (C function, its arguments, device index, out, workspace)."""
     lib = load_library()
     packed, L, R, dev, seqs = _latent_pool(pool, fp8)
-    _latent_rows("q_latent", q_latent, 3, L, dev)
-    T, H = q_latent.shape[0], q_latent.shape[1]
+    (T, H, _), ql_st, ql_sh = _latent_rows("q_latent", q_latent, 3, L, dev)
     qr = qr_st = qr_sh = 0
     if R > 0:
         if q_rope is None:
             raise ValueError("the pool's rows have a rotary part: q_rope is missing")
-        _latent_rows("q_rope", q_rope, 3, R, dev)
-        if q_rope.shape[0] != T or q_rope.shape[1] != H:
+        (t, h, _), qr_st, qr_sh = _latent_rows("q_rope", q_rope, 3, R, dev)
+        if t != T or h != H:
             raise ValueError("q_latent and q_rope must have the same tokens and heads")
-        qr, qr_st, qr_sh = q_rope.data_ptr(), _stride(q_rope, 0), _stride(q_rope, 1)
+        qr = q_rope.data_ptr()
     pos, seq = _latent_index(positions, seq_of_token, T, dev)
     B = _num_seqs(num_seqs, seqs)
     if out is not None:
@@ -731,12 +730,12 @@ def _latent_decode_args(fp8, q_latent, q_rope, pool, positions, *, scale, seq_of
     _current_device(dev)
     if out is None:
         out = torch.empty((T, H, L), dtype=torch.bfloat16, device=q_latent.device)
-    prob = _LATENT_PROBLEM.pack(T, B, H, scale, pos, seq, q_latent.data_ptr(), qr, _stride(q_latent, 0),
-                                _stride(q_latent, 1), qr_st, qr_sh)
+    prob = _LATENT_PROBLEM.pack(T, B, H, scale, pos, seq, q_latent.data_ptr(), qr, ql_st, ql_sh, qr_st,
+                                qr_sh)
     if workspace is None:
         nbytes = lib.sparse_attn_latent_decode_workspace_size(prob, packed)
-        workspace = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=q_latent.device)
-        nbytes = workspace.numel()
+        nbytes = max(nbytes, 16)
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=q_latent.device)
     else:
         nbytes = workspace.numel() * workspace.element_size()
     fn = lib.sparse_attn_latent_decode_fp8 if fp8 else lib.sparse_attn_latent_decode
@@ -795,22 +794,20 @@ def sparse_attn_latent_prefill(q, k_nope, k_rope, v, cu_q, cu_k, *, scale, out=N
     sees their last key (see the C header)."""
     lib = load_library()
     dev = q.get_device()
-    for name, t in (("q", q), ("k_nope", k_nope), ("v", v)):
-        _latent_rows(name, t, 3, None, dev)
-    Tq, H, dk = q.shape
-    Tk, _, dn = k_nope.shape
-    dv = v.shape[2]
+    (Tq, H, dk), q_st, q_sh = _latent_rows("q", q, 3, None, dev)
+    (Tk, k_heads, dn), kn_st, kn_sh = _latent_rows("k_nope", k_nope, 3, None, dev)
+    (v_rows, v_heads, dv), v_st, v_sh = _latent_rows("v", v, 3, None, dev)
     dr = dk - dn
-    if k_nope.shape[1] != H or v.shape[1] != H or v.shape[0] != Tk or dr < 0:
+    if k_heads != H or v_heads != H or v_rows != Tk or dr < 0:
         raise ValueError("q, k_nope and v must agree in heads, keys and widths")
     kr = kr_st = 0
     if dr > 0:
         if k_rope is None:
             raise ValueError("q has a rotary part: k_rope is missing")
-        _latent_rows("k_rope", k_rope, 2, dr, dev)
-        if k_rope.shape[0] != Tk:
+        (kr_rows, _), kr_st = _latent_rows("k_rope", k_rope, 2, dr, dev)
+        if kr_rows != Tk:
             raise ValueError("k_rope must have as many rows as k_nope")
-        kr, kr_st = k_rope.data_ptr(), _stride(k_rope, 0)
+        kr = k_rope.data_ptr()
     n = cu_q.numel()
     for name, t in (("cu_q", cu_q), ("cu_k", cu_k)):
         if t.dtype is not torch.int32 or t.dim() != 1 or not t.is_contiguous() or n < 1 or \
@@ -825,8 +822,7 @@ def sparse_attn_latent_prefill(q, k_nope, k_rope, v, cu_q, cu_k, *, scale, out=N
     if out is None:
         out = torch.empty((Tq, H, dv), dtype=torch.bfloat16, device=q.device)
     prob = _LATENT_PREFILL.pack(Tq, Tk, n - 1, H, dn, dr, dv, scale, q.data_ptr(), k_nope.data_ptr(),
-                                kr, v.data_ptr(), _stride(q, 0), _stride(q, 1), _stride(k_nope, 0),
-                                _stride(k_nope, 1), kr_st, _stride(v, 0), _stride(v, 1),
+                                kr, v.data_ptr(), q_st, q_sh, kn_st, kn_sh, kr_st, v_st, v_sh,
                                 cu_q.data_ptr(), cu_k.data_ptr())
     st = lib.sparse_attn_latent_prefill(prob, out.data_ptr(), _launch_stream(stream, dev))
     if st != 0:
