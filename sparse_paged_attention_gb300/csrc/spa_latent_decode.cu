@@ -1382,10 +1382,12 @@ cudaError_t launch_latent_decode(const LatentDecodeArgs& a, bool fp8, void* work
     e = launch<false>(p, stream, grid);
   }
   if (e != cudaSuccess) return e;
-  return launch_with_pdl(latent_merge_kernel, dim3(4 * (unsigned)sms), dim3(32 * kMergeWarps), 0,
-                         stream, true, (const int2*)p.cut, (const float*)p.lse,
-                         (const float*)p.part, reinterpret_cast<__nv_bfloat16*>(a.out), p.slices,
-                         p.groups, a.H, a.pool.L);
+  // (no more units than this; blocks without one would only delay the others' start)
+  const long long units = (long long)a.T * a.H * ((a.pool.L + 127) / 128);
+  const unsigned blocks = (unsigned)(units < 4LL * sms ? units : 4LL * sms);
+  return launch_with_pdl(latent_merge_kernel, dim3(blocks), dim3(32 * kMergeWarps), 0, stream, true,
+                         (const int2*)p.cut, (const float*)p.lse, (const float*)p.part,
+                         reinterpret_cast<__nv_bfloat16*>(a.out), p.slices, p.groups, a.H, a.pool.L);
 }
 
 // This translation unit's copy of the device error word (see spa_device.cuh).
