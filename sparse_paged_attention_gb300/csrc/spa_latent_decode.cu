@@ -140,10 +140,8 @@ struct DecodeParams {
 
 __device__ __forceinline__ int tiles_of(int len) { return len > 0 ? (len + kKeys - 1) / kKeys : 1; }
 
-// Entries of token t (0 for a token that attends to nothing) and its sequence.
-__device__ __forceinline__ int token_len(const LatentDecodeArgs& a, int t, int& b, bool& bad) {
-  const int pos = __ldg(a.positions + t);
-  b = a.seq_of_token ? __ldg(a.seq_of_token + t) : 0;
+// Entries of a token (0 for one that attends to nothing) at position `pos` of sequence b.
+__device__ __forceinline__ int token_len(const LatentDecodeArgs& a, int pos, int b, bool& bad) {
   long long cap = (long long)a.pool.bt_stride * a.pool.ps;
   cap = cap < 0x7fffffc0LL ? cap : 0x7fffffc0LL;   // (a tile's entries stay below 2^31)
   bad = b < 0 || b >= a.pool.B || (long long)pos >= cap;
@@ -278,8 +276,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int t = at + lane;
       c_len = c_seq = c_bad = 0;
       if (t < a.T) {
+        const int pos = __ldg(a.positions + t);
+        if (a.seq_of_token) c_seq = __ldg(a.seq_of_token + t);
         bool bad;
-        c_len = token_len(a, t, c_seq, bad);
+        c_len = token_len(a, pos, c_seq, bad);
         c_bad = bad;
       }
     };
@@ -303,10 +303,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       per = each;
     } else {
       long long total = lane < a.T ? tiles_of(c_len) : 0;
-      for (int t = lane + 32; t < a.T; t += 32) {
-        int b;
-        bool bad;
-        total += tiles_of(token_len(a, t, b, bad));
+      for (int t0 = 32; t0 < a.T; t0 += 4 * 32) {   // (four tokens' loads of a lane in flight)
+        int pos[4], seq[4] = {0, 0, 0, 0};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int t = min(t0 + 32 * i + lane, a.T - 1);
+          pos[i] = __ldg(a.positions + t);
+          if (a.seq_of_token) seq[i] = __ldg(a.seq_of_token + t);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          bool bad;
+          if (t0 + 32 * i + lane < a.T) total += tiles_of(token_len(a, pos[i], seq[i], bad));
+        }
       }
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);

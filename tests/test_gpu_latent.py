@@ -456,6 +456,45 @@ def test_decode_on_two_streams_at_once(dev):
         assert torch.equal(c.out.view(torch.int16), out.view(torch.int16))
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+def test_decode_chain_without_synchronisation(dev, fp8):
+    """Write and decode step after step on one stream, q and the new rows in buffers that the next step
+    overwrites, one workspace: every step's output is that of the same call made alone afterwards."""
+    start, steps, H = 300, 40, 64
+    inp = latent_inputs([start + steps, 77], 512, 64, 64, seed=33)
+    rows, scale = inp.pool(fp8)
+    pool = spa.LatentPool(rows.to(dev), inp.block_table.to(dev), 64, scale.to(dev) if fp8 else None)
+    write = spa.sparse_attn_latent_write_fp8 if fp8 else spa.sparse_attn_latent_write
+    decode = spa.sparse_attn_latent_decode_fp8 if fp8 else spa.sparse_attn_latent_decode
+    x, r = inp.latent.to(dev), inp.rope.to(dev)
+    keep = torch.ones(len(x), dtype=torch.bool)
+    keep[start:start + steps] = False
+    keep = keep.to(dev)
+    write(x[keep], r[keep], inp.positions.to(dev)[keep], pool, seq_of_token=inp.seq_of_token.to(dev)[keep])
+    g = torch.Generator().manual_seed(133)
+    qs = torch.randn((steps, 2, H, 576), generator=g).to(torch.bfloat16).to(dev)
+    pos = torch.tensor([[start + i, 76] for i in range(steps)], dtype=torch.int32, device=dev)
+    sid = torch.tensor([0, 1], dtype=torch.int32, device=dev)
+    q, p, row, rope = qs[0].clone(), pos[0].clone(), x[:1].clone(), r[:1].clone()
+    n = spa.sparse_attn_latent_decode_workspace_size(q[..., :512], pool, p, fp8=fp8)
+    ws = torch.empty(n, dtype=torch.uint8, device=dev)
+    outs = torch.empty((steps, 2, H, 512), dtype=torch.bfloat16, device=dev)
+    torch.cuda.synchronize()
+    for i in range(steps):
+        row.copy_(x[start + i:start + i + 1])
+        rope.copy_(r[start + i:start + i + 1])
+        p.copy_(pos[i])
+        q.copy_(qs[i])
+        write(row, rope, p[:1], pool)
+        decode(q[..., :512], q[..., 512:], pool, p, scale=0.04, seq_of_token=sid, workspace=ws, out=outs[i])
+    torch.cuda.synchronize()
+    for i in range(steps):
+        alone = decode(qs[i][..., :512], qs[i][..., 512:], pool, pos[i], scale=0.04, seq_of_token=sid)
+        torch.cuda.synchronize()
+        assert torch.equal(outs[i], alone), i
+    assert torch.isfinite(outs).all() and spa.sparse_attn_paged_check_errors() == 0
+
+
 def test_decode_and_cache_past_4_gigabytes(dev):
     """Rows whose byte offsets pass 2^32: pages at the end of a large pool."""
     ps, nb = 64, 64000                               # 64000 * 64 rows of 1152 bytes: 4.7 GB
@@ -542,6 +581,14 @@ def test_prefill_items_by_halves(dev):
     H = (torch.cuda.get_device_properties(dev).multi_processor_count + 20) // 6 + 1
     prefill_case(dev, [300, 77, 700], [333, 77, 700], H, 32, 16, 32, seed=53,
                  rows={0, 127, 128, 255, 256, 299, 300, 376, 377, 633, 1076})
+
+
+def test_prefill_many_sequences(dev):
+    """More sequences than a warp has lanes, several times over, some of them empty."""
+    nq = [(7 * i) % 40 if i % 5 else 0 for i in range(100)]
+    nq[70] = 300
+    nk = [n + (11 * i) % 50 for i, n in enumerate(nq)]
+    prefill_case(dev, nq, nk, 3, 32, 16, 32, seed=59)
 
 
 @pytest.mark.parametrize("scale", [-0.07, 0.0])
