@@ -60,7 +60,8 @@
 //     about 5 are the way to the first product, 3 the parts' stores and 8 the merge, its launch included
 // Also tried and slower: a softmax of two groups of four warps on alternate e4m3 tiles (181 us against
 // 153: the code twice as long costs more in instruction fetches than the overlap gives), a prefetch of
-// the next tile into L2, a separate warp for copies, S waiting on half tiles, longer and shorter polls.
+// the next tile into L2, a separate warp for copies, S waiting on half tiles, the next tile's S read under
+// the sum of this one's weights (190 and 147 us against 183 and 143), longer and shorter polls.
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
@@ -303,18 +304,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       per = each;
     } else {
       long long total = lane < a.T ? tiles_of(c_len) : 0;
-      for (int t0 = 32; t0 < a.T; t0 += 4 * 32) {   // (four tokens' loads of a lane in flight)
+      for (int at = 32; at < a.T; at += 4 * 32) {   // (four tokens' loads of a lane in flight)
         int pos[4], seq[4] = {0, 0, 0, 0};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const int t = min(t0 + 32 * i + lane, a.T - 1);
+          const int t = min(at + 32 * i + lane, a.T - 1);
           pos[i] = __ldg(a.positions + t);
           if (a.seq_of_token) seq[i] = __ldg(a.seq_of_token + t);
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           bool bad;
-          if (t0 + 32 * i + lane < a.T) total += tiles_of(token_len(a, pos[i], seq[i], bad));
+          if (at + 32 * i + lane < a.T) total += tiles_of(token_len(a, pos[i], seq[i], bad));
         }
       }
 #pragma unroll
