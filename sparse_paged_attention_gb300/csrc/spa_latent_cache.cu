@@ -12,10 +12,10 @@
 // enough warps stay resident to cover HBM's latency without a staged pipeline (one, with the next row's
 // loads under this row's codes, measured slower: 42 us against 31 for 65,536 e4m3 rows).
 //
-// Measured, L = 512, R = 64: 65,536 rows written as e4m3 in 28.6 us (4.1 TB/s; 60% of the measured copy
-// rate: the codes' arithmetic keeps the issue slots 68% busy), read back in 24.7 us (4.8 TB/s, 70%);
-// 30,001 bf16 rows written in about 11 us of the GPU's time.  Eight tokens take 2 us, and the call's
-// host side 14 us.
+// Measured, L = 512, R = 64: 65,536 rows written as e4m3 in 27.4 us (4.3 TB/s; 63% of the measured copy
+// rate; with one value an instruction the codes' arithmetic kept the issue slots 68% busy, and it took
+// 31), read back in 23 us (5.1 TB/s, 76%); 30,001 bf16 rows written in 14.6 us, launch included.  Eight
+// tokens take 2 us, and the call's host side 13.
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 

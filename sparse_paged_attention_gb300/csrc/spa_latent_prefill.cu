@@ -28,7 +28,7 @@
 // other data: masked as keys, blanked as values, not stored as queries.
 //
 // Measured (nope 128, rotary 64, v 128, 64 heads): 8,192 tokens in 0.91 ms (1,500 TFLOP/s: 80% of the
-// measured bf16 burst rate; 1.00 ms and 1,373 TFLOP/s when the chip has been busy for seconds, 81% of
+// measured bf16 burst rate; 0.99 ms and 1,386 TFLOP/s when the chip has been busy for seconds, 82% of
 // the sustained rate), 1,075 and 1,096 tokens after 12,000 in 0.92 ms (1,210 TFLOP/s: 512 items of two
 // tiles and 128 of one on 152 CTAs; 0.97 ms without the halves of the last round).  A step of
 // both tiles takes about 3,900 cycles against 2,560 of its MMAs: S keeps shared memory busy all the time
