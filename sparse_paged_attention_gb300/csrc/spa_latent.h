@@ -18,13 +18,14 @@ struct LatentPoolDev {
   const int32_t* bt;      // [B][bt_stride]
   long long num_blocks;
   int ps, bt_stride, B;
+  int ps_shift;           // log2 of ps, or -1
   int L, R;               // latent and rotary widths
   int row_bytes;          // 2 (L + R), or L + 2 R
 };
 
 // Row of the entry at position x >= 0 of sequence b (checked by the caller), or -1.
 __device__ __forceinline__ int latent_row(const LatentPoolDev& p, int b, int x) {
-  const int page = x / p.ps;
+  const int page = p.ps_shift >= 0 ? x >> p.ps_shift : x / p.ps;
   if (page >= p.bt_stride) return -1;
   const int blk = __ldg(p.bt + (size_t)b * p.bt_stride + page);
   if (blk < 0 || (long long)blk >= p.num_blocks) return -1;

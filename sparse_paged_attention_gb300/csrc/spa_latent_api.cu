@@ -38,6 +38,9 @@ void fill_pool(spa::LatentPoolDev& d, const spa_latent_pool_t* pl, int num_seqs,
   d.bt = pl->block_table;
   d.num_blocks = pl->num_blocks;
   d.ps = pl->page_size;
+  d.ps_shift = -1;
+  for (int i = 0; i < 31; ++i)
+    if (d.ps == 1 << i) d.ps_shift = i;
   d.bt_stride = pl->bt_stride;
   d.B = num_seqs;
   d.L = pl->latent_dim;

@@ -12,10 +12,11 @@
 // enough warps stay resident to cover HBM's latency without a staged pipeline (one, with the next row's
 // loads under this row's codes, measured slower: 42 us against 31 for 65,536 e4m3 rows).
 //
-// Measured, L = 512, R = 64: 65,536 rows written as e4m3 in 27.4 us (4.3 TB/s; 63% of the measured copy
-// rate; with one value an instruction the codes' arithmetic kept the issue slots 68% busy, and it took
-// 31), read back in 23 us (5.1 TB/s, 76%); 30,001 bf16 rows written in 14.6 us, launch included.  Eight
-// tokens take 2 us, and the call's host side 13.
+// Measured, L = 512, R = 64: 65,536 rows written as e4m3 in 24.8 us (4.8 TB/s, 70% of the measured copy
+// rate; its arithmetic keeps two thirds of the issue slots busy: with one value an instruction it took
+// 31, with IEEE divisions for the rotary part and 12 CTAs an SM 27.4), read back in 22.9 us (5.2 TB/s,
+// 76%); 30,001 bf16 rows written in 14.5 us, launch included (two to four rows in flight a warp: the
+// same or slower).  Eight tokens take 2 us, and the call's host side 13.
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
@@ -27,7 +28,10 @@ namespace spa {
 namespace {
 
 constexpr int kWarps = 4;            // tokens in flight a CTA
-constexpr int kChunks = kLatMaxDim / 8 / 32;   // 16-byte chunks of the latent part a lane (2)
+constexpr int kBlocks = 16;          // CTAs an SM, all resident: 64 warps of 32 registers (e4m3 write of 65,536
+                                     // rows: 26.3 us; with 41 registers and 12 of the 16 resident 28.1)
+constexpr int kChunks = kLatMaxDim / 8 / 32;   // 16-byte chunks of the latent part a lane
+static_assert(kChunks == 2, "the write's slow path picks one of two");
 
 // Pool row of token t, or -1 (a position, page, block or sequence that does not exist).
 __device__ __forceinline__ int token_row(const LatentCacheArgs& a, int t) {
@@ -44,19 +48,26 @@ __device__ __forceinline__ uint32_t absmax_bf16x2(uint32_t m, uint32_t w) {
   return r;
 }
 
-// kvq_chunk's reciprocal path, the same operations two values an instruction; x's sign is put into the
-// codes, four at a time, instead of into the quotients.
+// (x0, x1) / scale by kvq_div's operations, two values an instruction: r = RN(1 / scale), one correction
+// with the exact residual; the sign of a zero is lost.  For a scale that is RN(m / 448) of a bf16 m (what
+// a row has) and bf16 x the quotients are the correctly rounded ones: true of all 128 x 128 mantissas
+// wherever the residual is exact (|x| >= 2^-100); below that they are too small to have codes.
+__device__ __forceinline__ void div_bf16x2(float& x0, float& x1, float scale, float r) {
+  asm("{ .reg .b64 x, r, s, q, e; mov.b64 x, {%0, %1}; mov.b64 r, {%2, %2}; mov.b64 s, {%3, %3}; "
+      "mul.rn.f32x2 q, x, r; fma.rn.f32x2 e, q, s, x; fma.rn.f32x2 q, e, r, q; mov.b64 {%0, %1}, q; }"
+      : "+f"(x0), "+f"(x1)
+      : "f"(r), "f"(-scale));
+}
+
+// kvq_chunk's reciprocal path; x's sign is put into the codes, four at a time, instead of into the
+// quotients.
 __device__ __forceinline__ uint2 latent_codes(const uint4& u, float scale, float r) {
   const uint32_t w[4] = {u.x, u.y, u.z, u.w};
   uint32_t c[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const float x0 = __uint_as_float(w[i] << 16), x1 = __uint_as_float(w[i] & 0xffff0000u);
-    float q0 = x0, q1 = x1;
-    asm("{ .reg .b64 x, r, s, q, e; mov.b64 x, {%0, %1}; mov.b64 r, {%2, %2}; mov.b64 s, {%3, %3}; "
-        "mul.rn.f32x2 q, x, r; fma.rn.f32x2 e, q, s, x; fma.rn.f32x2 q, e, r, q; mov.b64 {%0, %1}, q; }"
-        : "+f"(q0), "+f"(q1)
-        : "f"(r), "f"(-scale));
+    float q0 = __uint_as_float(w[i] << 16), q1 = __uint_as_float(w[i] & 0xffff0000u);
+    div_bf16x2(q0, q1, scale, r);
     c[i] = kvq_e4m3x2(q0, q1);
   }
   const auto with_signs = [](uint32_t codes, uint32_t upper) {
@@ -73,8 +84,8 @@ __device__ __forceinline__ float2 e4m3x2_to_f32(uint32_t codes) {
 }
 
 // A lane takes chunks lane and 32 + lane of the latent part and word lane of the rotary part (two values:
-// at most 64 of them).  Spread like that the rotary part's IEEE divisions and second codes cost every
-// lane two of each; as 16-byte chunks they kept eight lanes busy with eight of each while the others
+// at most 64 of them).  Spread like that the rotary part's quotients and second codes cost every lane two
+// of each; as 16-byte chunks they kept eight lanes busy with eight of each while the others
 // waited, and the e4m3 write of 65,536 tokens took half as long again.
 struct NewRow {
   uint4 u[kChunks];
@@ -82,7 +93,7 @@ struct NewRow {
 };
 
 template <bool kFp8>
-__global__ void __launch_bounds__(32 * kWarps) latent_write_kernel(const LatentCacheArgs a) {
+__global__ void __launch_bounds__(32 * kWarps, kBlocks) latent_write_kernel(const LatentCacheArgs a) {
   pdl_launch_dependents();
   pdl_wait();
   const int lane = threadIdx.x & 31;
@@ -122,17 +133,27 @@ __global__ void __launch_bounds__(32 * kWarps) latent_write_kernel(const LatentC
       const float scale = amax > 0.f ? __fdiv_rn(amax, 448.f) : 1.f;
       const float r = __frcp_rn(scale);
       const bool fast = kvq_fast_scale(scale);
+      float p = ra, q = rb;
+      if (fast) {
 #pragma unroll
-      for (int i = 0; i < kChunks; ++i) {
-        const int c = lane + 32 * i;
-        if (c < nl)
-          *reinterpret_cast<uint2*>(dst + 8 * c) =
-              fast ? latent_codes(x.u[i], scale, r) : kvq_chunk(x.u[i], scale, r, false);
+        for (int i = 0; i < kChunks; ++i) {
+          const int c = lane + 32 * i;
+          if (c < nl) *reinterpret_cast<uint2*>(dst + 8 * c) = latent_codes(x.u[i], scale, r);
+        }
+        div_bf16x2(p, q, scale, r);
+        p = copysignf(p, ra);
+        q = copysignf(q, rb);
+      } else {
+#pragma unroll 1
+        for (int i = 0; i < kChunks; ++i) {
+          const int c = lane + 32 * i;
+          if (c < nl) *reinterpret_cast<uint2*>(dst + 8 * c) = kvq_chunk(i == 0 ? x.u[0] : x.u[1], scale, r, false);
+        }
+        p = __fdiv_rn(ra, scale);
+        q = __fdiv_rn(rb, scale);
       }
       if (lane < nr) {
-        // IEEE divisions: the low code sees the quotient's last bits, which the reciprocal path of the
-        // latent part is not held to
-        const float p = __fdiv_rn(ra, scale), q = __fdiv_rn(rb, scale);
+        // (the low code sees the quotient's last bits)
         const uint32_t high = kvq_e4m3x2(p, q);
         const float2 v = e4m3x2_to_f32(high);
         uint16_t* rope = reinterpret_cast<uint16_t*>(dst + a.pool.L) + lane;
@@ -150,7 +171,7 @@ __device__ __forceinline__ uint32_t bf16x2(float x, float y) {
 }
 
 template <bool kFp8>
-__global__ void __launch_bounds__(32 * kWarps) latent_read_kernel(const LatentCacheArgs a) {
+__global__ void __launch_bounds__(32 * kWarps, kBlocks) latent_read_kernel(const LatentCacheArgs a) {
   pdl_launch_dependents();
   pdl_wait();
   const int lane = threadIdx.x & 31;
@@ -211,7 +232,7 @@ __global__ void __launch_bounds__(32 * kWarps) latent_read_kernel(const LatentCa
 }
 
 unsigned cache_blocks(int T, int sms) {
-  const long long b = ((long long)T + kWarps - 1) / kWarps, cap = 16LL * sms;
+  const long long b = ((long long)T + kWarps - 1) / kWarps, cap = (long long)kBlocks * sms;
   return (unsigned)(b < cap ? b : cap);
 }
 

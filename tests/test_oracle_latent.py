@@ -103,3 +103,25 @@ def test_queries_before_the_first_key_see_nothing():
     res = latent.prefill(q, k, np.zeros((3, 0)), v, [0, 5], [0, 3], scale=1.0)
     assert not res[0][0].any() and not res[1][0].any()
     assert np.allclose(res[2][0], v[0]) and res[4][1]["p"].shape == (2, 3)
+
+
+def test_quotients_of_the_write_are_the_rounded_ones():
+    """x / scale by a correctly rounded reciprocal and one correction, as the e4m3 write works it out, for
+    every mantissa of a bf16 x and every scale that a row can have (up to powers of two)."""
+    from fractions import Fraction
+
+    def rn(x):                                       # to 24 bits, nearest even
+        if x == 0:
+            return x
+        e = x.numerator.bit_length() - x.denominator.bit_length()
+        e -= abs(x) < Fraction(2) ** e
+        ulp = Fraction(2) ** (e - 23)
+        return round(x / ulp) * ulp
+
+    for m in range(128, 256):
+        scale = rn(Fraction(m, 448))
+        r = rn(1 / scale)
+        for n in range(128, 256):
+            x = Fraction(n)
+            q = rn(x * r)
+            assert rn(q + rn(x - q * scale) * r) == rn(x / scale), (m, n)
