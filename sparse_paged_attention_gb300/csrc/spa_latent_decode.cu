@@ -562,13 +562,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (kFp8) {
           for (int c = 0; c < n_chunks; ++c) {
             const int steps = (W - c * 128 + 31) >> 5;             // 32-byte steps left in the row
+            const uint64_t dqc = desc_add(dq0, c * 16384), dkc = desc_add(dk, c * kChunkBytes);
+            mma_f8(dS, dqc, dkc, idS8, c != 0);
+            if (steps >= 4) {
 #pragma unroll
-            for (int st = 0; st < 4; ++st)
-              if (st < steps)
-                mma_f8(dS, desc_add(dq0, c * 16384 + st * 32), desc_add(dk, c * kChunkBytes + st * 32),
-                       idS8, (c | st) != 0);
+              for (int st = 1; st < 4; ++st) mma_f8(dS, desc_add(dqc, st * 32), desc_add(dkc, st * 32), idS8, 1u);
+            } else {
+              for (int st = 1; st < steps; ++st) mma_f8(dS, desc_add(dqc, st * 32), desc_add(dkc, st * 32), idS8, 1u);
+            }
           }
         } else {
+#pragma unroll 1
           for (int i = 0; i < nh; ++i) {
             const uint32_t id = nh + i < nl ? idS2 : idS1;         // (an odd last chunk stands alone)
 #pragma unroll
@@ -626,6 +630,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lead) {
         const uint32_t acc0 = first ? 0u : 1u;
         const uint64_t dp = desc_add(dp0, kFp8 ? (k & 1) * 8192 : buf * C::kBufBytes);
+#pragma unroll 1
         for (int mt = 0; mt < n_mt; ++mt) {
           const uint32_t dO = tmem + mt * 64;
           const uint64_t dv = desc_add(dv0, buf * C::kBufBytes + mt * C::kPerTile * kChunkBytes);
