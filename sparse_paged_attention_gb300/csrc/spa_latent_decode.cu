@@ -51,17 +51,20 @@
 // more), the second the mantissa of the large ones.
 //
 // Measured (L = 512, R = 64, calls one after the other, inputs larger than L2):
-//   64 sequences of up to 16,004 entries, 128 heads, bf16: 183 us (790 TFLOP/s, 42% of the measured bf16
+//   64 sequences of up to 16,004 entries, 128 heads, bf16: 179 us (810 TFLOP/s, 43% of the measured bf16
 //     rate; 3.4 TB/s); 10 of them are the merge
-//   48 sequences of up to 11,581 entries, 2 tokens each, 64 heads, e4m3: 144 us, where a tile is about
-//     2,700 cycles of the softmax warps (swap, maxima, exponentials, the two terms of P, each a few
+//   48 sequences of up to 11,581 entries, 2 tokens each, 64 heads, e4m3: 131 us, where a tile is about
+//     2,500 cycles of the softmax warps (swap, maxima, exponentials, the two terms of P, each a few
 //     hundred cycles and one after the other) against 1,730 of its MMAs
-//   one sequence of 131,071 entries, 16 heads, e4m3: 43 us; one of 4,097, 64 heads, bf16: 23 us, of which
+//   one sequence of 131,071 entries, 16 heads, e4m3: 40 us; one of 4,097, 64 heads, bf16: 23 us, of which
 //     about 5 are the way to the first product, 3 the parts' stores and 8 the merge, its launch included
+// The loops that issue MMAs are kept short (no predicates in the whole chunks, not unrolled across them):
+// with both, 145, 184 and 44 us where these are 131, 179 and 40.
 // Also tried and slower: a softmax of two groups of four warps on alternate e4m3 tiles (181 us against
 // 153: the code twice as long costs more in instruction fetches than the overlap gives), a prefetch of
 // the next tile into L2, a separate warp for copies, S waiting on half tiles, the next tile's S read under
-// the sum of this one's weights (190 and 147 us against 183 and 143), longer and shorter polls.
+// the sum of this one's weights (190 and 147 us against 183 and 143), longer and shorter polls; and, no
+// faster, e4m3's swap in one round.
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
@@ -83,7 +86,7 @@ constexpr int kSoftmax = 256;     // threads of the softmax warps
 constexpr int kThreads = kSoftmax + 224;
 constexpr int kMinTiles = 2;      // tiles of a slice at least: fewer would cost more in merging
 constexpr int kTokenCost = 6;     // what a token costs its CTA beside its tiles, in tiles (measured: 0 took 190
-                                  // and 150 us where 6 takes 183 and 144, see below)
+                                  // and 150 us where 6 took 183 and 144)
 
 // first and last tile of this CTA's part of a token, its last tile of all, no tile at all
 enum { kFirst = 1, kLast = 2, kFinal = 4, kEnd = 8 };
