@@ -24,8 +24,9 @@
 //
 // Items (256 queries, head) go to CTAs statically, sequence after sequence, in an order that starts with
 // the last queries (the longest rows) of all heads and folds back and forth over the CTAs, so that long
-// and short items add up alike.  The copies zero-fill what lies past a width (any multiple of 8); rows past a sequence's end are
-// other data: masked as keys, blanked as values, not stored as queries.
+// and short items add up alike; a last round that would leave half of the CTAs idle is shared out by
+// single tiles.  The copies zero-fill what lies past a width (any multiple of 8); rows past a sequence's
+// end are other data: masked as keys, blanked as values, not stored as queries.
 //
 // Measured (nope 128, rotary 64, v 128, 64 heads): 8,192 tokens in 0.91 ms (1,500 TFLOP/s: 80% of the
 // measured bf16 burst rate; 0.99 ms and 1,386 TFLOP/s when the chip has been busy for seconds, 82% of
