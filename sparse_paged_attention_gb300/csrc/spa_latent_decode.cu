@@ -69,6 +69,7 @@
 #include <cuda_fp8.h>
 
 #include "spa_latent.h"
+#include "spa_latent_ring.h"
 #include "spa_launch.h"
 
 namespace spa {
@@ -78,7 +79,7 @@ namespace {
 constexpr int kHeads = 64;        // heads of a CTA
 constexpr int kKeys = 64;         // entries of a tile
 constexpr int kChunkBytes = kKeys * 128;
-constexpr int kBufs = 3;          // tiles of rows in shared memory
+constexpr int kBufs = LatentTileRing::kSlots;   // tiles of rows in shared memory
 constexpr int kRing = 4;          // tile infos in flight
 constexpr int kTmemCols = 512;
 constexpr int kSCol = 256, kQCol = 384;   // TMEM columns: O^T from 0, S, q
@@ -115,12 +116,21 @@ struct Cfg {
   static constexpr int kQScaleOff = kRedOff + (kFp8 ? 2 : 1) * 4 * kHeads * 4;    // e4m3: float [4][64]
   static constexpr int kInfoOff = kQScaleOff + (kFp8 ? 4 * kHeads * 4 : 0);
   static constexpr int kBarOff = kInfoOff + kRing * (int)sizeof(Info);
-  // barriers (each in its own word; those of one kind side by side)
+  // Barriers (each in its own word; those of one kind side by side).  EMPTY of a tile's buffer, completed
+  // by the MMAs of O that read it, is also what the softmax warps wait for before they touch O.  Every wait
+  // by parity is at most one phase from its barrier, whatever the warps' pace:
+  //   FULL, EMPTY, P-ready, by tile k modulo three: S of tile k needs FULL of its buffer, whose copy
+  //     waited for EMPTY of tile k - 3, and that for P-ready of tile k - 3.  So whoever has S of tile k
+  //     finds EMPTY and P-ready of its slot at phase k / 3, and those of tiles k - 1 and k - 2 no more
+  //     than one phase from theirs; and none of them goes on to tile k + 3 before P of tile k.
+  //   S full, S free: S of tile k waits for the softmax to have read the S before it in that buffer.
+  //   q full, q free, O free: completed once a token, each by the side that waits for the other.
+  //   info full, info free: all fourteen readers arrive before a slot is written again.
   static constexpr int kFullB = 0, kEmptyB = kFullB + kBufs, kQFullB = kEmptyB + kBufs,
                        kQEmptyB = kQFullB + 1, kSFullB = kQEmptyB + 1, kSEmptyB = kSFullB + 2,
-                       kPFullB = kSEmptyB + 2, kPvDoneB = kPFullB + 2, kOFreeB = kPvDoneB + 2,
-                       kInfoFullB = kOFreeB + 1, kInfoEmptyB = kInfoFullB + kRing,
-                       kDrainB = kInfoEmptyB + kRing, kTokenB = kDrainB + 2, kNumB = kTokenB + 1;
+                       kPFullB = kSEmptyB + 2, kOFreeB = kPFullB + kBufs, kInfoFullB = kOFreeB + 1,
+                       kInfoEmptyB = kInfoFullB + kRing, kDrainB = kInfoEmptyB + kRing,
+                       kTokenB = kDrainB + 2, kNumB = kTokenB + 1;
   static constexpr int kMiscOff = kBarOff + kNumB * 8;   // TMEM base, abort flag, first token
   static constexpr int kSmem = kMiscOff + 12;
   static_assert(kSmem <= 232448, "shared memory budget");
@@ -227,16 +237,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < kBufs; ++i) {
       mbar_init(BAR(C::kFullB + i), p.boxed ? 1 : 128);   // armed by the loader, or cp.async's threads
       mbar_init(BAR(C::kEmptyB + i), 1);
+      // (lane 0 of every softmax warp arrives: an arrival of every thread on one barrier takes the
+      // barrier a cycle or two each, hundreds of cycles a tile)
+      mbar_init(BAR(C::kPFullB + i), 8);
     }
     mbar_init(BAR(C::kQFullB), kFp8 ? 1 : 4);
     mbar_init(BAR(C::kQEmptyB), 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(BAR(C::kSFullB + i), 1);
-      // (lane 0 of every warp arrives for it: an arrival of every thread on one barrier takes the
-      // barrier a cycle or two each, hundreds of cycles a tile)
       mbar_init(BAR(C::kSEmptyB + i), 8);
-      mbar_init(BAR(C::kPvDoneB + i), 1);
-      mbar_init(BAR(C::kPFullB + i), 8);
       mbar_init(BAR(C::kDrainB + i), 1);
     }
     mbar_init(BAR(C::kOFreeB), 8);
@@ -463,8 +472,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     next_tile(nxt);
     take();
     const int total_rows = (int)(a.pool.num_blocks * a.pool.ps);
-    int k = 0, buf = 0, fills = 0;
-    uint32_t buf_ph = 0;
+    int k = 0, fills = 0;
+    LatentTileRing at;
     bool ok = true;
     if (t_cur < 0) {                           // nothing to do: tell the others
       if (lane == 0) {
@@ -475,12 +484,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (; t_cur >= 0; ++k) {
       if (p.boxed) {                           // its copy first: everything else can wait for that
-        ok = warp_wait(BAR(C::kEmptyB + buf), buf_ph ^ 1, abort_flag);
+        ok = warp_wait(BAR(C::kEmptyB + at.slot), at.parity ^ 1, abort_flag);
         if (!ok) break;
         // a tile without entries starts past the last row and is filled with zeros
         const int base = (int)warp_uniform(row[0] >= 0 ? row[0] : total_rows);
         if (elect_one()) {
-          const uint32_t dst = sb + C::kKOff + buf * C::kBufBytes, full = BAR(C::kFullB + buf);
+          const uint32_t dst = sb + C::kKOff + at.slot * C::kBufBytes, full = BAR(C::kFullB + at.slot);
           mbar_arrive_expect_tx(full, (uint32_t)(n_chunks * kChunkBytes));
           if (p.whole > 0) {
             if (kFp8) tma_box3(dst, &p.block, 0, base, 0, full);
@@ -491,10 +500,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
         ++fills;
-        if (++buf == kBufs) {
-          buf = 0;
-          buf_ph ^= 1;
-        }
+        at.next();
       }
       // publish the tile
       const int ri = k % kRing;
@@ -543,8 +549,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint64_t dq0 = sdesc(sb + C::kQOff, 16, 1024);
     const uint64_t dk0 = sdesc(sb + C::kKOff, 16, 1024);            // rows, K-major
     const bool lead = elect_one();
-    int buf = 0;
-    uint32_t full_ph = 0, q_ph = 0;
+    LatentTileRing at;
+    uint32_t q_ph = 0;
     for (int k = 0;; ++k) {
       const int ri = k % kRing, sn = k % C::kSBufs;
       if (!warp_wait(BAR(C::kInfoFullB + ri), (uint32_t)((k / kRing) & 1), abort_flag)) break;
@@ -555,13 +561,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!warp_wait(BAR(C::kQFullB), q_ph, abort_flag)) break;
         q_ph ^= 1;
       }
-      if (!warp_wait(BAR(C::kFullB + buf), full_ph, abort_flag)) break;
+      if (!warp_wait(BAR(C::kFullB + at.slot), at.parity, abort_flag)) break;
       if (!warp_wait(BAR(C::kSEmptyB + sn), ((k / C::kSBufs) & 1) ^ 1, abort_flag)) break;
       if (!p.boxed) fence_proxy_async_smem();   // (rows copied by cp.async)
       tc_fence_after();
       if (lead) {
         const uint32_t dS = tmem + kSCol + sn * 64;
-        const uint64_t dk = desc_add(dk0, buf * C::kBufBytes);
+        const uint64_t dk = desc_add(dk0, at.slot * C::kBufBytes);
         if (kFp8) {
           for (int c = 0; c < n_chunks; ++c) {
             const int steps = (W - c * 128 + 31) >> 5;             // 32-byte steps left in the row
@@ -593,10 +599,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (flags & kLast) mma_commit(BAR(C::kQEmptyB));
       }
       __syncwarp();
-      if (++buf == kBufs) {
-        buf = 0;
-        full_ph ^= 1;
-      }
+      at.next();
       if (flags & kFinal) break;
     }
     // nothing may still write TMEM when it is released
@@ -613,13 +616,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint64_t dp0 = kFp8 ? sdesc64(sb + C::kPOff, 16, 512)
                               : sdesc(sb + C::kKOff + 8 * kChunkBytes, 16, 1024);
     const bool lead = elect_one();
-    int buf = 0;
+    LatentTileRing at;
     uint32_t o_ph = 0;
     bool any = warp_wait(BAR(C::kInfoFullB), 0, abort_flag);
     if (any) any = !(warp_uniform(*reinterpret_cast<volatile int*>(&infos[0].flags)) & kEnd);
     for (int k = 0; any; ++k) {
       const int ri = k % kRing;
-      if (!warp_wait(BAR(C::kPFullB + (k & 1)), (uint32_t)((k >> 1) & 1), abort_flag)) break;
+      if (!warp_wait(BAR(C::kPFullB + at.slot), at.parity, abort_flag)) break;
       // (P of the tile comes after its S, and that after its info)
       const int flags = (int)warp_uniform(*reinterpret_cast<volatile int*>(&infos[ri].flags));
       if (lead) mbar_arrive(BAR(C::kInfoEmptyB + ri));
@@ -632,11 +635,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_after();
       if (lead) {
         const uint32_t acc0 = first ? 0u : 1u;
-        const uint64_t dp = desc_add(dp0, kFp8 ? (k & 1) * 8192 : buf * C::kBufBytes);
+        const uint64_t dp = desc_add(dp0, kFp8 ? (k & 1) * 8192 : at.slot * C::kBufBytes);
 #pragma unroll 1
         for (int mt = 0; mt < n_mt; ++mt) {
           const uint32_t dO = tmem + mt * 64;
-          const uint64_t dv = desc_add(dv0, buf * C::kBufBytes + mt * C::kPerTile * kChunkBytes);
+          const uint64_t dv = desc_add(dv0, at.slot * C::kBufBytes + mt * C::kPerTile * kChunkBytes);
           if (!kFp8) {
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)               // 16 entries a step
@@ -649,11 +652,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         }
-        mma_commit(BAR(C::kEmptyB + buf));
-        mma_commit(BAR(C::kPvDoneB + (k & 1)));
+        mma_commit(BAR(C::kEmptyB + at.slot));
       }
       __syncwarp();
-      if (++buf == kBufs) buf = 0;
+      at.next();
       if (flags & kFinal) break;
     }
     if (lead) {
@@ -666,7 +668,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // Each token's q is read into registers as soon as its first tile is announced, and put in
     // place once the token before has no S left to compute.
     const int tid = threadIdx.x - kSoftmax;
-    int items = 0, buf = 0, flags = 0;
+    int items = 0, flags = 0;
     if (kFp8) pdl_wait();           // (for latent_q_kernel, launched right before)
     auto put_q = [&](int t) -> bool {
       if constexpr (!kFp8) {
@@ -748,7 +750,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int t = *reinterpret_cast<volatile int*>(sm + C::kMiscOff + 8);
       if (ok && t >= 0) ok = put_q(t);
     }
-    uint32_t buf_ph = 0;
+    LatentTileRing at;
     for (int k = 0; ok && !(flags & kFinal); ++k) {
       const int ri = k % kRing;
       if (!warp_wait(BAR(C::kInfoFullB + ri), (uint32_t)((k / kRing) & 1), abort_flag)) break;
@@ -765,22 +767,19 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int row = infos[ri].row[r0 + 16 * i];
           src[i] = row >= 0 ? a.pool.rows + (size_t)row * W : nullptr;
         }
-        const uint32_t dst = sb + C::kKOff + buf * C::kBufBytes + r0 * 128 + ((jj ^ (r0 & 7)) << 4);
-        if (!warp_wait(BAR(C::kEmptyB + buf), buf_ph ^ 1, abort_flag)) break;
+        const uint32_t dst = sb + C::kKOff + at.slot * C::kBufBytes + r0 * 128 + ((jj ^ (r0 & 7)) << 4);
+        if (!warp_wait(BAR(C::kEmptyB + at.slot), at.parity ^ 1, abort_flag)) break;
         for (int c = 0; c < n_chunks; ++c) {
-          const int at = c * 128 + jj * 16;
+          const int col = c * 128 + jj * 16;
           const uint32_t d = dst + slot_of(c) * kChunkBytes;
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const bool has = src[i] != nullptr && at < W;
-            cp_async_16(d + i * 2048, has ? src[i] + at : a.pool.rows, has ? 16u : 0u);
+            const bool has = src[i] != nullptr && col < W;
+            cp_async_16(d + i * 2048, has ? src[i] + col : a.pool.rows, has ? 16u : 0u);
           }
         }
-        cp_async_arrive_noinc(BAR(C::kFullB + buf));
-        if (++buf == kBufs) {
-          buf = 0;
-          buf_ph ^= 1;
-        }
+        cp_async_arrive_noinc(BAR(C::kFullB + at.slot));
+        at.next();
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(BAR(C::kInfoEmptyB + ri));
@@ -826,12 +825,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto column = [&](float own, float other, int c) {
       return __shfl_sync(0xffffffffu, (c >= 32) == (pair != 0) ? own : other, c & 31);
     };
-    int flags = 0, buf = kBufs - 1;
+    int flags = 0;
+    LatentTileRing at, at1, at2;                   // this tile, the one before, the one before that
+    // the MMAs of O of a tile are done
+    const auto pv_done = [&](const LatentTileRing& tile) {
+      return warp_wait(BAR(C::kEmptyB + tile.slot), tile.parity, abort_flag);
+    };
     ok = warp_wait(BAR(C::kInfoFullB), 0, abort_flag);
     const bool any = named_bar_and(1, kSoftmax, ok && !(infos[0].flags & kEnd));
     for (int k = 0; any && !(flags & kFinal); ++k) {
       const int ri = k % kRing, s = k % C::kSBufs;
-      if (++buf == kBufs) buf = 0;
+      if (k > 0) {
+        at2 = at1;
+        at1 = at;
+        at.next();
+      }
       ok = warp_wait(BAR(C::kSFullB + s), (uint32_t)((k / C::kSBufs) & 1), abort_flag) && ok;
       tc_fence_after();
       // (S of the tile comes after its info)
@@ -847,7 +855,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       float x[16];
       uint8_t* pb = kFp8 ? sm + C::kPOff + (k & 1) * 8192
-                         : sm + C::kKOff + buf * C::kBufBytes + 8 * kChunkBytes;   // P of this tile
+                         : sm + C::kKOff + at.slot * C::kBufBytes + 8 * kChunkBytes;   // P of this tile
       {
         float th[16];
         const uint32_t sa = lane_base + kSCol + (kFp8 ? s * 64 : half * 64) + 16 * ch;
@@ -862,8 +870,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int j = 0; j < 16; ++j) th[j] = x[j] = 0.f;
         }
         // e4m3: PV of the tile two before has read the P buffer
-        if (kFp8 && k >= 2)
-          ok = warp_wait(BAR(C::kPvDoneB + (k & 1)), (uint32_t)(((k - 2) >> 1) & 1), abort_flag) && ok;
+        if (kFp8 && k >= 2) ok = pv_done(at2) && ok;
         // The warps of the other block have the other part of S: swap the entries that are not one's
         // own with one of them, eight at a time, through a quarter of P's rows.  A warp's second eight
         // go where it has just read, so one barrier a round is enough.
@@ -993,7 +1000,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int r = 32 * e + __ffs(gone) - 1;
             gone &= gone - 1;
             for (int u = tid; u < n_mt * C::kPerTile * 8; u += kSoftmax)   // 16-byte units of its values
-              *reinterpret_cast<uint4*>(sm + C::kKOff + buf * C::kBufBytes + (u >> 3) * kChunkBytes +
+              *reinterpret_cast<uint4*>(sm + C::kKOff + at.slot * C::kBufBytes + (u >> 3) * kChunkBytes +
                                         r * 128 + (u & 7) * 16) = make_uint4(0, 0, 0, 0);
           }
         }
@@ -1001,7 +1008,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (grow && !first) {
         // the running maximum of some head moved: rescale its quarter of O (sixteen heads) once PV of
         // the tile before is done
-        ok = warp_wait(BAR(C::kPvDoneB + ((k - 1) & 1)), (uint32_t)(((k - 1) >> 1) & 1), abort_flag) && ok;
+        ok = pv_done(at1) && ok;
         tc_fence_after();
         const uint32_t g0 = pair ? grow1 : grow0, g1 = pair ? grow0 : grow1;   // heads 0-31, 32-63
 #pragma unroll 1
@@ -1032,7 +1039,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) {
-        mbar_arrive(BAR(C::kPFullB + (k & 1)));
+        mbar_arrive(BAR(C::kPFullB + at.slot));
         mbar_arrive(BAR(C::kInfoEmptyB + ri));
       }
       // (nobody waits for the denominators)
@@ -1053,7 +1060,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const size_t pslot = (size_t)blockIdx.x * 2 + (slot > 0 ? 1 : 0);
       if (slot >= 0 && part == 0)
         p.lse[pslot * kHeads + head] = m == -INFINITY ? -INFINITY : m + __log2f(ls);
-      ok = warp_wait(BAR(C::kPvDoneB + (k & 1)), (uint32_t)((k >> 1) & 1), abort_flag) && ok;
+      ok = pv_done(at) && ok;
       tc_fence_after();
       // TMEM lane -> channel of tile i of O^T: d0 + i dstep; sixteen heads (columns) at a time
       const int ln = quad * 32 + lane;
