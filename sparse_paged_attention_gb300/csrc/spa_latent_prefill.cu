@@ -269,6 +269,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       for (int j = 0; j < steps && ok; ++j) {
         const int row = it.k0 + j * kTile;
+        // Where the keys end inside the tile, a softmax warp will wait for its V by parity.  That needs the
+        // fill before in the slot to have landed, which a query tile that had no part in it (of an item of
+        // one query tile, before one whose first tile sees no key) has not seen: seen here, before
+        // the keys without which there is no S.
+        if (it.nk - j * kTile < kTile && vc >= kVs) {
+          const uint32_t f = vc - kVs;
+          if (!(ok = warp_wait(BAR(B_VFULL + f % kVs), (f / kVs) & 1, abort_flag))) break;
+        }
         for (int c = 0; c < nc; ++c, ++kc) {
           const uint32_t sl = kc % kKs, full = BAR(B_KFULL + sl);
           if (!(ok = warp_wait(BAR(B_KEMPTY + sl), ((kc / kKs) & 1) ^ 1, abort_flag))) break;

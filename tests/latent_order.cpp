@@ -10,6 +10,8 @@
 //   latent_order decode FP8 BOXED PRING GROW TILES...   tiles of each token; GROW: bit k set where the
 //       maximum moves at tile k; PRING: slots of the P-ready and PV-done barriers where they are a ring
 //       of their own (0: the kernel's, at the tile's slot of the ring of rows)
+//   latent_order prefill CHUNKS VORDER S0,S1,RAGGED...  key steps of both query tiles of each item, and
+//       whether the last step ends inside a tile; VORDER: the loader waits for V as the kernel does
 // prints "ok STATES" or "WHAT AT ..."
 #include <cstdio>
 #include <cstdlib>
@@ -234,6 +236,103 @@ void decode(bool fp8, bool boxed, int pring, unsigned grow, const std::vector<in
   m.run();
 }
 
+struct Item { int steps[2]; bool ragged; };
+
+void prefill(int chunks, bool vorder, const std::vector<Item>& items) {
+  constexpr int kKs = 4, kVs = 2, kItems = 2;
+  Model m;
+  m.queues = 2;
+  Warp load{"loader", {}}, s{"S", {}}, o{"O", {}}, soft[2] = {{"softmax 0", {}}, {"softmax 1", {}}};
+  auto next_item = [&](Warp& w, int n) {
+    m.wait(w, m.bar("I_FULL", n % kItems), n / kItems, (n / kItems) & 1);
+    m.arrive(w, m.bar("I_EMPTY", n % kItems, 4));
+  };
+  auto bar = [&](const char* kind, int slot) { return m.bar(kind, slot); };
+  int kc = 0, vc = 0, issued = 0, l_qs[2] = {}, s_qs[2] = {}, done[2] = {}, opened[2] = {};
+  for (int n = 0; n <= (int)items.size(); ++n) {
+    m.wait(load, m.bar("I_EMPTY", n % kItems, 4), n / kItems - 1, (uint32_t)((n / kItems) & 1) ^ 1);
+    m.arrive(load, bar("I_FULL", n % kItems));
+    next_item(s, n);
+    next_item(o, n);
+    next_item(soft[0], n);
+    next_item(soft[1], n);
+    if (n == (int)items.size()) break;
+    const Item& it = items[n];
+    const int steps = it.steps[0] > it.steps[1] ? it.steps[0] : it.steps[1];
+    for (int t = 0; t < 2; ++t) {
+      if (it.steps[t] == 0) continue;
+      m.wait(load, bar("Q_EMPTY", t), l_qs[t] - 1, (uint32_t)(l_qs[t] & 1) ^ 1);
+      ++l_qs[t];
+      m.issue(load, -1, {bar("Q_FULL", t)});
+    }
+    int sdone[2] = {done[0], done[1]};
+    for (int j = 0; j < steps; ++j, kc += chunks, ++vc) {
+      const bool ends = it.ragged && j == steps - 1;
+      // loader
+      if (vorder && ends && vc >= kVs)
+        m.wait(load, bar("V_FULL", vc % kVs), vc / kVs - 1, (uint32_t)(vc / kVs - 1) & 1);
+      for (int c = 0; c < chunks; ++c) {
+        const int f = kc + c;
+        m.wait(load, bar("K_EMPTY", f % kKs), f / kKs - 1, (uint32_t)((f / kKs) & 1) ^ 1);
+        m.issue(load, -1, {bar("K_FULL", f % kKs)});
+      }
+      m.wait(load, bar("V_EMPTY", vc % kVs), vc / kVs - 1, (uint32_t)((vc / kVs) & 1) ^ 1);
+      m.issue(load, -1, {bar("V_FULL", vc % kVs)});
+      // S
+      for (int t = 0; t < 2; ++t) {
+        if (j >= it.steps[t]) continue;
+        const bool last = t == 1 || j >= it.steps[1];
+        if (t == 0 || it.steps[0] <= j)
+          for (int c = 0; c < chunks; ++c)
+            m.wait(s, bar("K_FULL", (kc + c) % kKs), (kc + c) / kKs, ((kc + c) / kKs) & 1);
+        if (j == 0) {
+          m.wait(s, bar("Q_FULL", t), s_qs[t], s_qs[t] & 1);
+          ++s_qs[t];
+        }
+        if (issued > 0) m.wait(s, bar("S_EMPTY", 0), issued - 1, (issued - 1) & 1);
+        ++issued;
+        if (last)
+          for (int c = 0; c < chunks; ++c) m.issue(s, 0, {bar("K_EMPTY", (kc + c) % kKs)});
+        m.issue(s, 0, {bar("S_FULL", t)});
+        if (j == it.steps[t] - 1) m.issue(s, 0, {bar("Q_EMPTY", t)});
+      }
+      // O
+      m.wait(o, bar("V_FULL", vc % kVs), vc / kVs, (vc / kVs) & 1);
+      for (int t = 0; t < 2; ++t) {
+        if (j >= it.steps[t]) continue;
+        m.wait(o, bar("P_READY", t), done[t], done[t] & 1);
+        if (j == 0) {
+          m.wait(o, bar("O_FREE", t), opened[t] - 1, (uint32_t)(opened[t] & 1) ^ 1);
+          ++opened[t];
+        }
+        m.wait(o, bar("P_READY", 2 + t), done[t], done[t] & 1);
+        ++done[t];
+        m.issue(o, 1, {bar("PV_DONE", t)});
+      }
+      m.issue(o, 1, {bar("V_EMPTY", vc % kVs)});
+      // softmax
+      for (int t = 0; t < 2; ++t) {
+        if (j >= it.steps[t]) continue;
+        Warp& w = soft[t];
+        m.wait(w, bar("S_FULL", t), sdone[t], sdone[t] & 1);
+        m.arrive(w, bar("S_EMPTY", 0));
+        if (j > 0) m.wait(w, bar("PV_DONE", t), sdone[t] - 1, (uint32_t)(sdone[t] - 1) & 1);
+        if (ends) m.wait(w, bar("V_FULL", vc % kVs), vc / kVs, (vc / kVs) & 1);
+        m.arrive(w, bar("P_READY", t));
+        m.arrive(w, bar("P_READY", 2 + t));
+        ++sdone[t];
+      }
+    }
+    for (int t = 0; t < 2; ++t) {
+      if (it.steps[t] == 0) continue;
+      m.wait(soft[t], bar("PV_DONE", t), sdone[t] - 1, (uint32_t)(sdone[t] - 1) & 1);
+      m.arrive(soft[t], bar("O_FREE", t));
+    }
+  }
+  m.warps = {load, s, o, soft[0], soft[1]};
+  m.run();
+}
+
 }  // namespace
 
 int main(int argc, char** argv) {
@@ -241,6 +340,16 @@ int main(int argc, char** argv) {
     std::vector<int> tokens;
     for (int i = 6; i < argc; ++i) tokens.push_back(std::atoi(argv[i]));
     decode(std::atoi(argv[2]), std::atoi(argv[3]), std::atoi(argv[4]), (unsigned)std::atoi(argv[5]), tokens);
+  } else if (argc > 4 && !std::strcmp(argv[1], "prefill")) {
+    std::vector<Item> items;
+    for (int i = 4; i < argc; ++i) {
+      Item it;
+      int r = 0;
+      if (std::sscanf(argv[i], "%d,%d,%d", &it.steps[0], &it.steps[1], &r) != 3) return 2;
+      it.ragged = r;
+      items.push_back(it);
+    }
+    prefill(std::atoi(argv[2]), std::atoi(argv[3]), items);
   } else {
     return 2;
   }

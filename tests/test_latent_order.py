@@ -50,3 +50,34 @@ def test_two_barriers_over_three_buffers_are_not_enough(order):
     for tiles in ([3], [3, 2], [7]):
         assert order("decode", 0, 1, 2, 0, *tiles).startswith("early at softmax, PV_DONE"), tiles
         assert order("decode", 1, 1, 2, 0, *tiles).startswith("ok"), tiles
+
+
+# items of a CTA: key steps of the first and the second query tile, and whether the last ends in a tile
+ITEMS = ["1,0,1", "2,0,1", "0,1,1", "1,1,1", "1,2,1", "2,2,0", "2,3,1"]
+
+
+def item_lists(n):
+    lists = [[]]
+    for _ in range(n):
+        lists = [x + [i] for x in lists for i in ITEMS]
+    return [x for x in lists if sum(max(map(int, i.split(",")[:2])) for i in x) <= 4]
+
+
+@pytest.mark.parametrize("first", ITEMS)
+def test_prefill_waits_are_within_a_phase(order, first):
+    for items in [x for n in (1, 2) for x in item_lists(n) if x[0] == first]:
+        assert order("prefill", 1, 1, *items).startswith("ok"), items
+
+
+def test_prefill_waits_with_three_chunks_a_key(order):
+    for items in (["2,3,1"], ["2,0,1", "0,1,1"]):
+        assert order("prefill", 3, 1, *items).startswith("ok"), items
+
+
+def test_prefill_without_the_loaders_wait_is_early(order):
+    """An item of one query tile, then one whose first query tile sees no key: without the loader's
+    wait, the second query tile's wait for V may be two phases from its barrier."""
+    for items in (["2,0,1", "0,1,1"], ["1,0,1", "2,0,1", "0,1,1"]):
+        for chunks in (1, 3):
+            assert order("prefill", chunks, 0, *items).startswith("early at softmax 1, V_FULL"), items
+            assert order("prefill", chunks, 1, *items).startswith("ok"), items
