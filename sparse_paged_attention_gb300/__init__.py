@@ -569,6 +569,7 @@ def _latent_pool(pool, fp8: bool):
         raise ValueError("pool rows must be a contiguous [num_blocks, page_size, row] tensor")
     if bt.dtype is not torch.int32 or bt.dim() != 2 or not bt.is_contiguous():
         raise ValueError("block_table must be a contiguous int32 [num_seqs, stride] tensor")
+    _same_device("block_table", bt, rows.get_device())
     nb, ps, width = rows.shape
     scale = 0
     if fp8:
