@@ -220,6 +220,26 @@ def _stream(stream) -> int:
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
+def _empty(shape, dtype, device, stream):
+    """torch.empty for what a call on `stream` (None: the current one) writes.
+
+    On another stream than the current one the memory is taken from that stream's: what was freed
+    on the current stream may still be in use by work queued there, and what is freed before the call has
+    run may be handed out there."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    handle, current = _stream(stream), torch.cuda.current_stream(device)
+    if handle == current.cuda_stream:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(handle, device=device) if handle else \
+            torch.cuda.default_stream(device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(current)       # (where the caller goes on to use it)
+    return t
+
+
 def _check_q(q):
     if q.dtype != torch.bfloat16 or q.dim() != 3 or not q.is_contiguous():
         raise ValueError("q must be a contiguous bf16 [num_tokens, num_heads, head_dim] tensor")
@@ -682,7 +702,7 @@ def _latent_read(fp8, positions, pool, *, seq_of_token=None, num_seqs=None, out=
     pos, seq = _latent_index(positions, seq_of_token, n, dev)
     _current_device(dev)
     if out is None:
-        out = torch.empty((n, width), dtype=torch.bfloat16, device=pool.rows.device)
+        out = _empty((n, width), torch.bfloat16, pool.rows.device, stream)
         stride = width if n > 1 else 0
     else:
         (rows, _), stride = _latent_rows("out", out, 2, width, dev)
@@ -707,8 +727,9 @@ def sparse_attn_latent_read_fp8(positions, pool, **kw):
 
 
 def _latent_decode_args(fp8, q_latent, q_rope, pool, positions, *, scale, seq_of_token=None,
-                        num_seqs=None, out=None, workspace=None):
-    """Checked arguments of a latent decode: (C function, its arguments, device index, out, workspace)."""
+                        num_seqs=None, out=None, workspace=None, stream=None):
+    """Checked arguments of a latent decode on `stream`: (C function, its arguments, device index, out,
+    workspace)."""
     lib = load_library()
     packed, L, R, dev, seqs = _latent_pool(pool, fp8)
     (T, H, _), ql_st, ql_sh = _latent_rows("q_latent", q_latent, 3, L, dev)
@@ -730,13 +751,13 @@ def _latent_decode_args(fp8, q_latent, q_rope, pool, positions, *, scale, seq_of
         _same_device("workspace", workspace, dev)
     _current_device(dev)
     if out is None:
-        out = torch.empty((T, H, L), dtype=torch.bfloat16, device=q_latent.device)
+        out = _empty((T, H, L), torch.bfloat16, q_latent.device, stream)
     prob = _LATENT_PROBLEM.pack(T, B, H, scale, pos, seq, q_latent.data_ptr(), qr, ql_st, ql_sh, qr_st,
                                 qr_sh)
     if workspace is None:
         nbytes = lib.sparse_attn_latent_decode_workspace_size(prob, packed)
         nbytes = max(nbytes, 16)
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=q_latent.device)
+        workspace = _empty(nbytes, torch.uint8, q_latent.device, stream)
     else:
         nbytes = workspace.numel() * workspace.element_size()
     fn = lib.sparse_attn_latent_decode_fp8 if fp8 else lib.sparse_attn_latent_decode
@@ -744,7 +765,8 @@ def _latent_decode_args(fp8, q_latent, q_rope, pool, positions, *, scale, seq_of
 
 
 def _latent_decode(fp8, q_latent, q_rope, pool, positions, stream=None, **kw):
-    fn, args, dev, out, workspace = _latent_decode_args(fp8, q_latent, q_rope, pool, positions, **kw)
+    fn, args, dev, out, workspace = _latent_decode_args(fp8, q_latent, q_rope, pool, positions,
+                                                        stream=stream, **kw)
     st = fn(*args, _launch_stream(stream, dev))
     if st != 0:
         raise SpaError(st, fn.__name__)
@@ -754,8 +776,8 @@ def _latent_decode(fp8, q_latent, q_rope, pool, positions, stream=None, **kw):
 def sparse_attn_latent_decode(q_latent, q_rope, pool, positions, **kw):
     """Absorbed latent attention of ``q_latent`` [T, H, L] and ``q_rope`` [T, H, R] (None without a
     rotary part) over a paged bf16 latent pool: bf16 [T, H, L] (see the C header).  Token t attends
-    to entries 0 .. positions[t] of its sequence; the workspace is allocated with torch if none is
-    given."""
+    to entries 0 .. positions[t] of its sequence; the workspace is allocated with torch, on the call's
+    stream, if none is given."""
     return _latent_decode(False, q_latent, q_rope, pool, positions, **kw)
 
 
@@ -778,7 +800,8 @@ def bind_latent_decode(q_latent, q_rope, pool, positions, *, fp8=False, stream=N
                        **kw) -> BoundCall:
     """``sparse_attn_latent_decode[_fp8]`` on fixed tensors, as a zero-argument callable (workspace
     and output are allocated here once when not given)."""
-    fn, args, _, out, workspace = _latent_decode_args(fp8, q_latent, q_rope, pool, positions, **kw)
+    fn, args, _, out, workspace = _latent_decode_args(fp8, q_latent, q_rope, pool, positions,
+                                                      stream=stream, **kw)
     call = BoundCall(fn, args, (q_latent, q_rope, pool, positions, kw.get("seq_of_token"), out,
                                 workspace), stream)
     call.out = out
@@ -821,7 +844,7 @@ def sparse_attn_latent_prefill(q, k_nope, k_rope, v, cu_q, cu_k, *, scale, out=N
         _same_device("out", out, dev)
     _current_device(dev)
     if out is None:
-        out = torch.empty((Tq, H, dv), dtype=torch.bfloat16, device=q.device)
+        out = _empty((Tq, H, dv), torch.bfloat16, q.device, stream)
     prob = _LATENT_PREFILL.pack(Tq, Tk, n - 1, H, dn, dr, dv, scale, q.data_ptr(), k_nope.data_ptr(),
                                 kr, v.data_ptr(), q_st, q_sh, kn_st, kn_sh, kr_st, v_st, v_sh,
                                 cu_q.data_ptr(), cu_k.data_ptr())

@@ -1,9 +1,9 @@
-"""The Python layer of latent attention on the GPU: block tables on the host."""
+"""The Python layer of latent attention on the GPU: block tables on the host, calls on other streams."""
 import pytest
 import torch
 
 import sparse_paged_attention_gb300 as spa
-from test_gpu_latent import dev, place  # noqa: F401
+from test_gpu_latent import decode_case, dev, place  # noqa: F401
 from workloads import latent_inputs
 
 pytestmark = pytest.mark.gpu
@@ -23,3 +23,34 @@ def test_block_table_on_the_host_is_refused(dev, fp8):  # noqa: F811
                                                                             scale=1.0)):
         with pytest.raises(ValueError, match="block_table"):
             call()
+
+
+@pytest.mark.parametrize("raw", [False, True])
+@pytest.mark.parametrize("fp8", [False, True])
+def test_calls_on_another_stream_keep_their_memory(dev, fp8, raw):  # noqa: F811
+    """Calls on a side stream that is busy, and meanwhile allocations of the workspace's and the outputs'
+    sizes on the current stream: neither side finds the other's bytes in its memory."""
+    pool, ql, qr, pos, sid, want = decode_case(dev, [3000, 50], 64, 512, 64, 64, fp8, seed=45)
+    suffix = "_fp8" if fp8 else ""
+    decode = getattr(spa, "sparse_attn_latent_decode" + suffix)
+    read = getattr(spa, "sparse_attn_latent_read" + suffix)
+    args = (ql.to(dev), qr.to(dev), pool, pos.to(dev))
+    kw = dict(scale=576 ** -0.5, seq_of_token=sid.to(dev))
+    at = torch.arange(2000, dtype=torch.int32, device=dev)
+    rows = read(at, pool)
+    n = spa.sparse_attn_latent_decode_workspace_size(ql, pool, pos, fp8=fp8)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(50_000_000)
+    stream = side.cuda_stream if raw else side
+    outs, held = [], []
+    for _ in range(3):
+        outs.append((decode(*args, stream=stream, **kw), read(at, pool, stream=stream)))
+        for size in (n, want.numel() * 2, rows.numel() * 2):
+            held.append(torch.full((size,), 0xA5, dtype=torch.uint8, device=dev))
+    torch.cuda.synchronize()
+    for out, got in outs:
+        assert torch.equal(out.view(torch.int16), want.view(torch.int16))
+        assert torch.equal(got.view(torch.int16), rows.view(torch.int16))
+    assert all(bool((x == 0xA5).all()) for x in held)

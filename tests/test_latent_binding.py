@@ -1,5 +1,7 @@
 """Latent attention: what the Python layer refuses before the library is called, on tensors that only
 claim a device (CPU only: nothing is launched)."""
+import contextlib
+
 import pytest
 import torch
 
@@ -12,6 +14,9 @@ class OnDevice(torch.Tensor):
 
     def get_device(self):
         return self.index
+
+    def record_stream(self, stream):
+        pass
 
 
 class OnOtherDevice(OnDevice):
@@ -60,3 +65,70 @@ def test_block_table_elsewhere_is_refused(where):
                                    fp8=pool is e4m3)
         with pytest.raises(ValueError, match="block_table"):
             spa.sparse_attn_latent_decode_workspace_size(zeros(3, 2, 64), pool, pos, fp8=pool is e4m3)
+
+
+class FakeLibrary:
+    """Entry points that note the stream they are called on (their last argument)."""
+
+    def __init__(self):
+        self.streams = []
+
+    def __getattr__(self, name):
+        def call(*args):
+            self.streams.append(args[-1])
+            return 0
+        call.__name__ = name
+        return (lambda *_: 4096) if name.endswith("workspace_size") else call
+
+
+@pytest.fixture
+def device(monkeypatch):
+    """One GPU whose current stream is 7; notes the stream that every torch.empty is made on."""
+    lib, now, made = FakeLibrary(), [7], []
+    empty = torch.empty
+
+    class Stream:
+        def __init__(self, handle, device=None):
+            self.cuda_stream = handle
+
+    @contextlib.contextmanager
+    def on(stream):
+        now.append(stream.cuda_stream)
+        yield
+        now.pop()
+
+    def note_empty(*args, device=None, **kw):
+        made.append(now[-1])
+        return claim(empty(*args, **kw))
+    monkeypatch.setattr(spa, "load_library", lambda: lib)
+    monkeypatch.setattr(torch, "empty", note_empty)
+    monkeypatch.setattr(torch.cuda, "stream", on)
+    monkeypatch.setattr(torch.cuda, "ExternalStream", Stream)
+    monkeypatch.setattr(torch.cuda, "default_stream", lambda device=None: Stream(0))
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: Stream(now[-1]))
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda dev: now[-1], raising=False)
+    return lib, made, Stream
+
+
+@pytest.mark.parametrize("given", [None, 7, 9, "object", 0])
+def test_memory_comes_from_the_stream_of_the_call(device, given):
+    """out and workspace of a call on another stream than the current one are that stream's memory."""
+    lib, made, Stream = device
+    stream = Stream(9) if given == "object" else given
+    want = 7 if given is None else 9 if given == "object" else given
+    bt, pos = zeros(1, 4, dtype=torch.int32), zeros(3, dtype=torch.int32)
+    cu = zeros(2, dtype=torch.int32)
+    for pool, suffix in zip(pools(bt), ("", "_fp8")):
+        getattr(spa, "sparse_attn_latent_read" + suffix)(pos, pool, stream=stream)
+        assert made == [want]
+        getattr(spa, "sparse_attn_latent_decode" + suffix)(zeros(3, 2, 64), zeros(3, 2, 16), pool, pos,
+                                                           scale=1.0, stream=stream)
+        assert made == [want] * 3                    # out and workspace
+        spa.bind_latent_decode(zeros(3, 2, 64), zeros(3, 2, 16), pool, pos, scale=1.0, fp8=bool(suffix),
+                               stream=stream)()
+        assert made == [want] * 5
+        made.clear()
+    spa.sparse_attn_latent_prefill(zeros(3, 2, 24), zeros(3, 2, 16), zeros(3, 8), zeros(3, 2, 16), cu, cu,
+                                   scale=1.0, stream=stream)
+    assert made == [want] and lib.streams == [want] * 7
