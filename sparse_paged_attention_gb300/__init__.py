@@ -220,24 +220,28 @@ def _stream(stream) -> int:
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
-def _empty(shape, dtype, device, stream):
-    """torch.empty for what a call on `stream` (None: the current one) writes.
+def _made_on(stream, device, make):
+    """make(), a tensor on `device` that a call on `stream` (None: the current one) writes.
 
-    On another stream than the current one the memory is taken from that stream's: what was freed
+    On another stream than the current one it is made there, from that stream's memory: what was freed
     on the current stream may still be in use by work queued there, and what is freed before the call has
     run may be handed out there."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return make()
     handle, current = _stream(stream), torch.cuda.current_stream(device)
     if handle == current.cuda_stream:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return make()
     if not hasattr(stream, "cuda_stream"):
         stream = torch.cuda.ExternalStream(handle, device=device) if handle else \
             torch.cuda.default_stream(device)
     with torch.cuda.stream(stream):
-        t = torch.empty(shape, dtype=dtype, device=device)
+        t = make()
     t.record_stream(current)       # (where the caller goes on to use it)
     return t
+
+
+def _empty(shape, dtype, device, stream):
+    return _made_on(stream, device, lambda: torch.empty(shape, dtype=dtype, device=device))
 
 
 def _check_q(q):
@@ -250,7 +254,7 @@ def _prefill(fp8, q, win, cmp, topk_idx, positions, *, window, ratio, scale, seq
     lib = load_library()
     _check_q(q)
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty(q.shape, q.dtype, q.device, stream)
     prob = _problem_c(q, win, topk_idx, positions, seq_of_token, window, ratio, scale, num_seqs)
     w, c = _pool_c(win, fp8), _pool_c(cmp, fp8)
     fn = lib.sparse_attn_paged_prefill_fp8 if fp8 else lib.sparse_attn_paged_prefill
@@ -283,11 +287,11 @@ def _decode(fp8, q, win, cmp, topk_idx, positions, *, window, ratio, scale, seq_
     lib = load_library()
     _check_q(q)
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty(q.shape, q.dtype, q.device, stream)
     prob = _problem_c(q, win, topk_idx, positions, seq_of_token, window, ratio, scale, num_seqs)
     if workspace is None:
         nbytes = int(lib.sparse_attn_paged_decode_workspace_size(ctypes.byref(prob)))
-        workspace = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=q.device)
+        workspace = _empty(max(nbytes, 16), torch.uint8, q.device, stream)
     w, c = _pool_c(win, fp8), _pool_c(cmp, fp8)
     fn = lib.sparse_attn_paged_decode_fp8 if fp8 else lib.sparse_attn_paged_decode
     st = fn(q.data_ptr(), ctypes.byref(w), ctypes.byref(c) if c is not None else None,
@@ -315,7 +319,7 @@ def sparse_attn_paged_decode_noalloc(q, win, cmp, topk_idx, positions, *, window
     lib = load_library()
     _check_q(q)
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty(q.shape, q.dtype, q.device, stream)
     prob = _problem_c(q, win, topk_idx, positions, seq_of_token, window, ratio, scale, num_seqs)
     w, c = _pool_c(win, False), _pool_c(cmp, False)
     st = lib.sparse_attn_paged_decode_noalloc(q.data_ptr(), ctypes.byref(w),
@@ -374,7 +378,7 @@ def bind_prefill(q, win, cmp, topk_idx, positions, *, window, ratio, scale, seq_
     lib = load_library()
     _check_q(q)
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty(q.shape, q.dtype, q.device, stream)
     prob = _problem_c(q, win, topk_idx, positions, seq_of_token, window, ratio, scale, num_seqs)
     w, c = _pool_c(win, fp8), _pool_c(cmp, fp8)
     fn = lib.sparse_attn_paged_prefill_fp8 if fp8 else lib.sparse_attn_paged_prefill
@@ -409,7 +413,7 @@ def bind_prefill_host(q, win, cmp, topk_idx, positions, *, window, ratio, scale,
     if staging is None:
         nbytes = int(lib.sparse_attn_paged_prefill_host_staging_size(ctypes.byref(prob),
                                                                      int(chunk_tokens)))
-        staging = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=win.kv.device)
+        staging = _empty(max(nbytes, 256), torch.uint8, win.kv.device, stream)
     w, c = _pool_c(win, fp8), _pool_c(cmp, fp8)
     fn = lib.sparse_attn_paged_prefill_host_fp8 if fp8 else lib.sparse_attn_paged_prefill_host
     args = (q.data_ptr(), ctypes.byref(w), ctypes.byref(c) if c is not None else None,
@@ -442,11 +446,11 @@ def bind_decode(q, win, cmp, topk_idx, positions, *, window, ratio, scale, seq_o
     lib = load_library()
     _check_q(q)
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty(q.shape, q.dtype, q.device, stream)
     prob = _problem_c(q, win, topk_idx, positions, seq_of_token, window, ratio, scale, num_seqs)
     if workspace is None:
         nbytes = int(lib.sparse_attn_paged_decode_workspace_size(ctypes.byref(prob)))
-        workspace = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=q.device)
+        workspace = _empty(max(nbytes, 16), torch.uint8, q.device, stream)
     w, c = _pool_c(win, fp8), _pool_c(cmp, fp8)
     fn = lib.sparse_attn_paged_decode_fp8 if fp8 else lib.sparse_attn_paged_decode
     args = (q.data_ptr(), ctypes.byref(w), ctypes.byref(c) if c is not None else None,
@@ -484,7 +488,7 @@ def sparse_attn_gated_pool(kv, gate, out=None, *, out_dtype=torch.float32, strea
         raise ValueError("kv and gate must have the same shape")
     B, R, D = (int(x) for x in kv.shape)
     if out is None:
-        out = torch.empty((B, D), dtype=out_dtype, device=kv.device)
+        out = _empty((B, D), out_dtype, kv.device, stream)
     if out.dtype not in (torch.float32, torch.bfloat16) or tuple(out.shape) != (B, D) or \
             (D > 1 and out.stride(1) != 1):
         raise ValueError("out must be an fp32 or bf16 [B, D] tensor with unit last stride")
@@ -524,7 +528,7 @@ def sparse_attn_indexer_logits(q, weights, key_pool, block_table, positions, *, 
     if num_cols is None:
         raise ValueError("Full mode needs num_cols")
     if out is None:
-        out = torch.empty((T, num_cols), dtype=torch.float32, device=q.device)
+        out = _empty((T, num_cols), torch.float32, q.device, stream)
     B = int(block_table.shape[0]) if num_seqs is None else int(num_seqs)
     pool = SpaPoolC(key_pool.data_ptr(), None, None, block_table.data_ptr(), key_pool.shape[0],
                     key_pool.shape[1], block_table.shape[1])
@@ -549,7 +553,7 @@ def sparse_attn_indexer_topk(logits, k, *, cand=None, out=None, stream=None):
         raise ValueError("cand must be a contiguous int32 tensor shaped like logits")
     T, N = int(logits.shape[0]), int(logits.shape[1])
     if out is None:
-        out = torch.empty((T, int(k)), dtype=torch.int32, device=logits.device)
+        out = _empty((T, int(k)), torch.int32, logits.device, stream)
     st = lib.sparse_attn_indexer_topk(logits.data_ptr(), T, N, _ptr(cand), int(k),
                                       out.data_ptr(), _stream(stream))
     if st != 0:
@@ -861,7 +865,8 @@ def sparse_attn_paged_resolve_columns(win, cmp, topk_idx, positions, *, window, 
     lib = load_library()
     T = int(positions.shape[0])
     K = 0 if topk_idx is None else int(topk_idx.shape[1])
-    cols = torch.full((T, window + K), -1, dtype=torch.int32, device=positions.device)
+    dev = positions.device
+    cols = _made_on(stream, dev, lambda: torch.full((T, window + K), -1, dtype=torch.int32, device=dev))
     dummy_q = torch.empty((T, 1, head_dim), dtype=torch.bfloat16, device="meta")
     prob = _problem_c(dummy_q, win, topk_idx, positions, seq_of_token, window, ratio, 1.0,
                       num_seqs)
