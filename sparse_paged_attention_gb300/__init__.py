@@ -244,6 +244,13 @@ def _empty(shape, dtype, device, stream):
     return _made_on(stream, device, lambda: torch.empty(shape, dtype=dtype, device=device))
 
 
+def _bytes(name, t) -> int:
+    """Bytes from a memory argument's address on (a view with gaps or repeats has fewer)."""
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.numel() * t.element_size()
+
+
 def _check_q(q):
     if q.dtype != torch.bfloat16 or q.dim() != 3 or not q.is_contiguous():
         raise ValueError("q must be a contiguous bf16 [num_tokens, num_heads, head_dim] tensor")
@@ -296,7 +303,7 @@ def _decode(fp8, q, win, cmp, topk_idx, positions, *, window, ratio, scale, seq_
     fn = lib.sparse_attn_paged_decode_fp8 if fp8 else lib.sparse_attn_paged_decode
     st = fn(q.data_ptr(), ctypes.byref(w), ctypes.byref(c) if c is not None else None,
             ctypes.byref(prob), out.data_ptr(), workspace.data_ptr(),
-            workspace.numel() * workspace.element_size(), _stream(stream))
+            _bytes("workspace", workspace), _stream(stream))
     if st != 0:
         raise SpaError(st, fn.__name__)
     return out
@@ -418,7 +425,7 @@ def bind_prefill_host(q, win, cmp, topk_idx, positions, *, window, ratio, scale,
     fn = lib.sparse_attn_paged_prefill_host_fp8 if fp8 else lib.sparse_attn_paged_prefill_host
     args = (q.data_ptr(), ctypes.byref(w), ctypes.byref(c) if c is not None else None,
             ctypes.byref(prob), out.data_ptr(), int(chunk_tokens), staging.data_ptr(),
-            staging.numel() * staging.element_size())
+            _bytes("staging", staging))
     call = BoundCall(fn, args, (q, win, cmp, topk_idx, positions, seq_of_token, out, staging,
                                 w, c, prob), stream)
     call.out = out
@@ -455,7 +462,7 @@ def bind_decode(q, win, cmp, topk_idx, positions, *, window, ratio, scale, seq_o
     fn = lib.sparse_attn_paged_decode_fp8 if fp8 else lib.sparse_attn_paged_decode
     args = (q.data_ptr(), ctypes.byref(w), ctypes.byref(c) if c is not None else None,
             ctypes.byref(prob), out.data_ptr(), workspace.data_ptr(),
-            workspace.numel() * workspace.element_size())
+            _bytes("workspace", workspace))
     call = BoundCall(fn, args, (q, win, cmp, topk_idx, positions, seq_of_token, out, workspace,
                                 w, c, prob), stream)
     call.out = out
@@ -763,7 +770,7 @@ def _latent_decode_args(fp8, q_latent, q_rope, pool, positions, *, scale, seq_of
         nbytes = max(nbytes, 16)
         workspace = _empty(nbytes, torch.uint8, q_latent.device, stream)
     else:
-        nbytes = workspace.numel() * workspace.element_size()
+        nbytes = _bytes("workspace", workspace)
     fn = lib.sparse_attn_latent_decode_fp8 if fp8 else lib.sparse_attn_latent_decode
     return fn, (packed, prob, out.data_ptr(), workspace.data_ptr(), nbytes), dev, out, workspace
 

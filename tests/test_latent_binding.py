@@ -132,3 +132,20 @@ def test_memory_comes_from_the_stream_of_the_call(device, given):
     spa.sparse_attn_latent_prefill(zeros(3, 2, 24), zeros(3, 2, 16), zeros(3, 8), zeros(3, 2, 16), cu, cu,
                                    scale=1.0, stream=stream)
     assert made == [want] and lib.streams == [want] * 7
+
+
+def test_workspaces_with_gaps_or_repeats_are_refused(device):
+    """The bytes of a workspace are counted from its address on, which only holds for contiguous ones."""
+    bt, pos = zeros(1, 4, dtype=torch.int32), zeros(3, dtype=torch.int32)
+    paged = spa.PagedPool(zeros(4, 8, 2, 64), bt)
+    topk = zeros(3, 8, dtype=torch.int32)
+    for ws in (zeros(1, dtype=torch.uint8).expand(4096), zeros(8192, dtype=torch.uint8)[::2]):
+        for pool, suffix in zip(pools(bt), ("", "_fp8")):
+            args = (zeros(3, 2, 64), zeros(3, 2, 16), pool, pos)
+            with pytest.raises(ValueError, match="workspace"):
+                getattr(spa, "sparse_attn_latent_decode" + suffix)(*args, scale=1.0, workspace=ws)
+            with pytest.raises(ValueError, match="workspace"):
+                spa.bind_latent_decode(*args, scale=1.0, workspace=ws, fp8=bool(suffix))
+        for decode in (spa.sparse_attn_paged_decode, spa.bind_decode):
+            with pytest.raises(ValueError, match="workspace"):
+                decode(zeros(3, 2, 64), paged, None, topk, pos, window=16, ratio=4, scale=1.0, workspace=ws)
