@@ -7,6 +7,7 @@
 #include <mutex>
 
 #include "sparse_attn_paged.h"
+#include "spa_errors.h"
 #include "spa_indexer.h"
 #include "spa_latent.h"
 #include "spa_launch.h"
@@ -757,18 +758,9 @@ int sparse_attn_paged_check_errors(void* stream) {
   e = spa::read_and_clear_kv_write_error_word(&w);
   if (e != cudaSuccess) return cuda_fail(e, "device error word");
   int x = 0;
-  e = spa::read_and_clear_indexer_error_word(&x);
+  e = spa::collect_error_words(&x);
   if (e != cudaSuccess) return cuda_fail(e, "device error word");
-  int latent = 0;
-  for (cudaError_t (*word)(int*) : {spa::read_and_clear_latent_cache_error_word,
-                                    spa::read_and_clear_latent_decode_error_word,
-                                    spa::read_and_clear_latent_prefill_error_word}) {
-    int y = 0;
-    e = word(&y);
-    if (e != cudaSuccess) return cuda_fail(e, "device error word");
-    latent |= y;
-  }
-  return v | w | x | latent;
+  return v | w | x;
 }
 
 const char* sparse_attn_paged_strerror(int status) {

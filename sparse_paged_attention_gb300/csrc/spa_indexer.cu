@@ -21,6 +21,7 @@
 // written as -inf without an MMA.
 #include <cuda_bf16.h>
 
+#include "spa_errors.h"
 #include "spa_indexer.h"
 #include "spa_indexer_math.cuh"
 
@@ -234,11 +235,8 @@ __global__ void __launch_bounds__(kIdxThreads, kIdxCtasPerSm) indexer_kernel(con
 }  // namespace
 
 // This translation unit's copy of the device error word (see spa_device.cuh).
-cudaError_t read_and_clear_indexer_error_word(int* value) {
-  cudaError_t e = cudaMemcpyFromSymbol(value, g_spa_error, sizeof(int));
-  if (e != cudaSuccess) return e;
-  const int zero = 0;
-  return cudaMemcpyToSymbol(g_spa_error, &zero, sizeof(int));
+cudaError_t indexer_error_word(int** word) {
+  return cudaGetSymbolAddress(reinterpret_cast<void**>(word), g_spa_error);
 }
 
 int indexer_smem_bytes(int nq) { return idx_layout(nq).used + 1024; }

@@ -31,7 +31,6 @@ struct IndexerArgs {
 };
 int indexer_smem_bytes(int nq);   // dynamic shared memory of a CTA whose groups hold nq queries
 cudaError_t launch_indexer(const IndexerArgs& a, bool cand, int num_sms, cudaStream_t stream);
-cudaError_t read_and_clear_indexer_error_word(int* value);
 
 // Top-k selection over the logits rows.
 constexpr int kIdxTopkMax = 2048;

@@ -45,7 +45,6 @@ struct LatentCacheArgs {        // write and read
 };
 cudaError_t launch_latent_write(const LatentCacheArgs& a, bool fp8, int sms, cudaStream_t stream);
 cudaError_t launch_latent_read(const LatentCacheArgs& a, bool fp8, int sms, cudaStream_t stream);
-cudaError_t read_and_clear_latent_cache_error_word(int* value);
 
 struct LatentDecodeArgs {
   LatentPoolDev pool;
@@ -62,7 +61,6 @@ cudaError_t prepare_latent_decode();   // per-device one-time attributes (dynami
 size_t latent_decode_workspace(const LatentDecodeArgs& a, bool fp8, int sms);
 cudaError_t launch_latent_decode(const LatentDecodeArgs& a, bool fp8, void* workspace, int sms,
                                  cudaStream_t stream);
-cudaError_t read_and_clear_latent_decode_error_word(int* value);
 
 struct LatentPrefillArgs {
   const uint8_t *q, *k_nope, *k_rope, *v;   // bf16, strides in bytes
@@ -74,6 +72,5 @@ struct LatentPrefillArgs {
 };
 cudaError_t prepare_latent_prefill();
 cudaError_t launch_latent_prefill(const LatentPrefillArgs& a, int sms, cudaStream_t stream);
-cudaError_t read_and_clear_latent_prefill_error_word(int* value);
 
 }  // namespace spa

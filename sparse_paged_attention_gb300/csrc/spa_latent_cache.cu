@@ -21,6 +21,7 @@
 #include <cuda_fp8.h>
 
 #include "spa_kvwrite_quant.cuh"
+#include "spa_errors.h"
 #include "spa_latent.h"
 
 namespace spa {
@@ -251,11 +252,8 @@ cudaError_t launch_latent_read(const LatentCacheArgs& a, bool fp8, int sms, cuda
 }
 
 // This translation unit's copy of the device error word (see spa_device.cuh).
-cudaError_t read_and_clear_latent_cache_error_word(int* value) {
-  cudaError_t e = cudaMemcpyFromSymbol(value, g_spa_error, sizeof(int));
-  if (e != cudaSuccess) return e;
-  const int zero = 0;
-  return cudaMemcpyToSymbol(g_spa_error, &zero, sizeof(int));
+cudaError_t latent_cache_error_word(int** word) {
+  return cudaGetSymbolAddress(reinterpret_cast<void**>(word), g_spa_error);
 }
 
 }  // namespace spa

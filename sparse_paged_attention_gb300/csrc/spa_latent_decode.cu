@@ -68,6 +68,7 @@
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
+#include "spa_errors.h"
 #include "spa_latent.h"
 #include "spa_latent_ring.h"
 #include "spa_launch.h"
@@ -1416,11 +1417,8 @@ cudaError_t launch_latent_decode(const LatentDecodeArgs& a, bool fp8, void* work
 }
 
 // This translation unit's copy of the device error word (see spa_device.cuh).
-cudaError_t read_and_clear_latent_decode_error_word(int* value) {
-  cudaError_t e = cudaMemcpyFromSymbol(value, g_spa_error, sizeof(int));
-  if (e != cudaSuccess) return e;
-  const int zero = 0;
-  return cudaMemcpyToSymbol(g_spa_error, &zero, sizeof(int));
+cudaError_t latent_decode_error_word(int** word) {
+  return cudaGetSymbolAddress(reinterpret_cast<void**>(word), g_spa_error);
 }
 
 }  // namespace spa

@@ -40,6 +40,7 @@
 // mask instead of two 0.91.  Tried and slower: one warp for both products in a fixed order (1.06 ms;
 // 1.24 with the waits moved under the MMAs), five K chunks and V by halves (1.06), prefetches of K and
 // V into L2 (1.03).
+#include "spa_errors.h"
 #include "spa_latent.h"
 #include "spa_launch.h"
 
@@ -597,11 +598,8 @@ cudaError_t launch_latent_prefill(const LatentPrefillArgs& a, int sms, cudaStrea
 }
 
 // This translation unit's copy of the device error word (see spa_device.cuh).
-cudaError_t read_and_clear_latent_prefill_error_word(int* value) {
-  cudaError_t e = cudaMemcpyFromSymbol(value, g_spa_error, sizeof(int));
-  if (e != cudaSuccess) return e;
-  const int zero = 0;
-  return cudaMemcpyToSymbol(g_spa_error, &zero, sizeof(int));
+cudaError_t latent_prefill_error_word(int** word) {
+  return cudaGetSymbolAddress(reinterpret_cast<void**>(word), g_spa_error);
 }
 
 }  // namespace spa
