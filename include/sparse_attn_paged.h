@@ -386,8 +386,10 @@ int sparse_attn_latent_read_fp8(const spa_latent_pool_t* pool, int32_t num_rows,
  * on unmapped pages, past the block table or outside the pool are left out and set SPA_ERR_INDEX,
  * as does a sequence id outside [0, num_seqs), whose output rows are zero.  What is left out never
  * enters the sums, whatever its bytes hold (rows past a sequence's last may be uninitialised).
- * Softmax statistics, scores and sums are fp32; the probabilities enter the value product as bf16
- * (bf16 pools) or as an e5m2 and an e4m3 term (e4m3 pools).
+ * Softmax statistics, scores and sums are fp32.  The probabilities enter the value product as bf16
+ * (bf16 pools); e4m3 pools: each weight p_j scale_j within 2^-11 of itself, or 2^-27 of the
+ * sequence's largest where that is more, and the queries as two e4m3 terms, within 2^-17 of a
+ * head's largest value each.
  * workspace: device memory, 16-byte aligned, of at least
  * sparse_attn_latent_decode_workspace_size(prob, pool) bytes (of the pool that is decoded: with its
  * scale, if it is an e4m3 one) for partial results of sequences that are split over several SMs and,

@@ -46,9 +46,16 @@
 // latent_merge_kernel joins them in the order of the slices.
 //
 // e4m3 rows enter the MMAs as codes.  q becomes q_hi + q_lo (e4m3, times a power of two per head);
-// the row's scale multiplies the score.  The weights p_j scale_j enter as an e5m2 and an e4m3 term:
-// the first has the exponents to keep small weights of long sequences (22 bits below the largest and
-// more), the second the mantissa of the large ones.
+// the row's scale multiplies the score.  The weights p_j scale_j enter as f16 numbers cut into three e5m2
+// terms, each the nearest to what the terms before it leave, in a unit that puts the largest weight of the
+// sequence so far between 2^10 and 2^15 (the last binade but one of e5m2).  So a weight is off
+//   by 2^-11 of itself at most (f16's rounding: the terms lose nothing more), or, below about 2^-16 of
+//   the largest, by 2^-17 of the unit, 2^-27 of the largest.
+// Small weights matter as much as large ones: 100,000 entries at 2^-13 of the largest outweigh it.  With an
+// e5m2 and an e4m3 term (ten bits less of range, and 7 us less for the 48 sequences below) such a tail came
+// out up to 11% short.  A reference that may be exceeded by 2^4, 2^5 or 2^6 before O is rescaled took
+// 141, 138 and 138 us.  A row of zeros, whose stored scale is 1, would raise the reference by the seven or
+// so bits that this is above other rows': its scale counts as 0 here (its score is 0 and so are its values).
 //
 // Measured (L = 512, R = 64, calls one after the other, inputs larger than L2):
 //   64 sequences of up to 16,004 entries, 128 heads, bf16: 179 us (810 TFLOP/s, 43% of the measured bf16
@@ -90,6 +97,11 @@ constexpr int kMinTiles = 2;      // tiles of a slice at least: fewer would cost
 constexpr int kTokenCost = 6;     // what a token costs its CTA beside its tiles, in tiles (measured: 0 took 190
                                   // and 150 us where 6 took 183 and 144)
 
+// e4m3: the unit of the weights, and how far (log2) one may exceed the reference before O is rescaled.  Their
+// product is 2^15, so that a weight rounds to an e5m2 number.
+constexpr float kPUnit = 1024.f;
+constexpr float kTau8 = 5.f;
+
 // first and last tile of this CTA's part of a token, its last tile of all, no tile at all
 enum { kFirst = 1, kLast = 2, kFinal = 4, kEnd = 8 };
 
@@ -99,7 +111,7 @@ struct Cfg {
   static constexpr int kPerTile = kFp8 ? 1 : 2;      // slots of 128 channels
   static constexpr int kBufBytes = kSlots * kChunkBytes;
   static constexpr int kSBufs = kFp8 ? 2 : 1;        // S buffers in TMEM (64 or 128 columns)
-  static constexpr float kTau = kFp8 ? 6.f : 8.f;    // lazy rescale threshold (log2 units)
+  static constexpr float kTau = kFp8 ? kTau8 : 8.f;    // lazy rescale threshold (log2 units)
   struct Info {
     int t, flags, slot, pad;
     uint32_t valid[2];                               // bit j: entry j (32 + j) takes part
@@ -112,8 +124,10 @@ struct Cfg {
   static constexpr int kQBytes = kFp8 ? 5 * 16384 : 8192;
   static constexpr int kQOff = 0;
   static constexpr int kKOff = kQBytes;
-  static constexpr int kPOff = kKOff + kBufs * kBufBytes;            // e4m3: two P buffers
-  static constexpr int kRedOff = kPOff + (kFp8 ? 2 * 8192 : 0);      // float [4][64], e4m3 two of them
+  // P's first 8 KB take the place of the tile's last slot (e4m3: the first two terms); e4m3's third term
+  // has a place of its own for each buffer
+  static constexpr int kPOff = kKOff + kBufs * kBufBytes;
+  static constexpr int kRedOff = kPOff + (kFp8 ? kBufs * 4096 : 0);  // float [4][64], e4m3 two of them
   static constexpr int kQScaleOff = kRedOff + (kFp8 ? 2 : 1) * 4 * kHeads * 4;    // e4m3: float [4][64]
   static constexpr int kInfoOff = kQScaleOff + (kFp8 ? 4 * kHeads * 4 : 0);
   static constexpr int kBarOff = kInfoOff + kRing * (int)sizeof(Info);
@@ -150,7 +164,7 @@ struct DecodeParams {
   float* lse;                  // [slices * groups][2][64], log2 units
   float* part;                 // [slices * groups][2][64][L]
   uint8_t* q_codes;            // e4m3: [T * groups][chunks][64 rows of the high term, 64 of the low][128]
-  float* q_scale;              // e4m3: [T * groups][64], 2^-5 over the power of two in the codes
+  float* q_scale;              // e4m3: [T * groups][64], 1 / kPUnit over the power of two in the codes
 };
 
 __device__ __forceinline__ int tiles_of(int len) { return len > 0 ? (len + kKeys - 1) / kKeys : 1; }
@@ -199,7 +213,7 @@ __global__ void __launch_bounds__(256)
     const float m = bf16_lo(mb);
     const bool finite = mb < 0x7f80u;          // (else the head's scores become NaN through its scale)
     const float qs = finite && m > 0.f ? pow2_floor(448.f / m) : 1.f;
-    if (lane == 0) scales[tg * kHeads + h] = finite ? 0.03125f / qs : __int_as_float(0x7fffffff);
+    if (lane == 0) scales[tg * kHeads + h] = finite ? (1.f / kPUnit) / qs : __int_as_float(0x7fffffff);
     // piece o: chunk o / 16, 16-byte unit (o / 2) & 7 of the row
     uint8_t* dst = codes + tg * ((long long)n_chunks * 16384) + h * 128;
 #pragma unroll
@@ -221,6 +235,22 @@ __global__ void __launch_bounds__(256)
       *reinterpret_cast<uint2*>(d + 8192) = make_uint2(lo[0] | (lo[1] << 16), lo[2] | (lo[3] << 16));
     }
   }
+}
+
+// The scale of an e4m3 row (-1: none), 0 if its codes are nothing but zeros (of either sign).  Out of line:
+// hardly ever called, and the decode kernel's code is long as it is.
+__device__ __noinline__ float without_zero_row(const uint8_t* rows, int width, int row, float scale) {
+  if (row < 0 || scale != 1.f) return scale;
+  const uint4* src = reinterpret_cast<const uint4*>(rows + (size_t)row * width);
+  uint32_t any = 0;
+  for (int i = 0; i < (width >> 4) && any == 0; i += 4) {
+#pragma unroll
+    for (int z = 0; z < 4; ++z) {
+      const uint4 u = i + z < (width >> 4) ? __ldg(src + i + z) : make_uint4(0, 0, 0, 0);
+      any |= (u.x | u.y | u.z | u.w) & 0x7f7f7f7fu;
+    }
+  }
+  return any ? scale : 0.f;
 }
 
 template <bool kFp8>
@@ -515,11 +545,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         info.row[lane + 32] = row[1];
       }
       if (kFp8) {
+        // (a scale of exactly 1 is that of a row of zeros or, rarely, of one whose largest value is 448)
+        if (__any_sync(0xffffffffu, sc[0] == 1.f || sc[1] == 1.f)) {
+          sc[0] = without_zero_row(a.pool.rows, W, row[0], sc[0]);
+          sc[1] = without_zero_row(a.pool.rows, W, row[1], sc[1]);
+        }
         // the maximum of a tile is taken over p_j |scale_j|, the weights that enter the value
         // product (a scale below 2^-60 counts as that: the sums of p_j alone must stay finite)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          info.scale[lane + 32 * e] = 32.f * sc[e];
+          info.scale[lane + 32 * e] = kPUnit * sc[e];
           info.lscale[lane + 32 * e] = row[e] >= 0 ? fmaxf(__log2f(fabsf(sc[e])), -60.f) : -INFINITY;
         }
       }
@@ -612,10 +647,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == 14) {
     // ================================= MMAs of O ==========================================
     const uint32_t idO = kFp8 ? idesc_e4m3(128, 64, 1, 0) : idesc_bf16(128, 64, 1, 0);
-    const uint32_t idO5 = idO | (1u << 10);            // B in e5m2: the high term of P
+    const uint32_t idO5 = idO | (1u << 10);            // B in e5m2: the terms of P
     const uint64_t dv0 = sdesc(sb + C::kKOff, kChunkBytes, 1024);   // rows, MN-major
-    const uint64_t dp0 = kFp8 ? sdesc64(sb + C::kPOff, 16, 512)
-                              : sdesc(sb + C::kKOff + 8 * kChunkBytes, 16, 1024);
+    const uint32_t p_at = sb + C::kKOff + (C::kSlots - 1) * kChunkBytes;
+    const uint64_t dp0 = kFp8 ? sdesc64(p_at, 16, 512) : sdesc(p_at, 16, 1024);
+    const uint64_t dp3 = sdesc64(sb + C::kPOff, 16, 512);           // e4m3's third term
     const bool lead = elect_one();
     LatentTileRing at;
     uint32_t o_ph = 0;
@@ -636,7 +672,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_after();
       if (lead) {
         const uint32_t acc0 = first ? 0u : 1u;
-        const uint64_t dp = desc_add(dp0, kFp8 ? (k & 1) * 8192 : at.slot * C::kBufBytes);
+        const uint64_t dp = desc_add(dp0, at.slot * C::kBufBytes), dq = desc_add(dp3, at.slot * 4096);
 #pragma unroll 1
         for (int mt = 0; mt < n_mt; ++mt) {
           const uint32_t dO = tmem + mt * 64;
@@ -649,7 +685,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int kk = 0; kk < 2; ++kk) {             // 32 entries a step
               mma_f8(dO, desc_add(dv, kk * 4096), desc_add(dp, kk * 32), idO5, kk ? 1u : acc0);
-              mma_f8(dO, desc_add(dv, kk * 4096), desc_add(dp, 4096 + kk * 32), idO, 1u);
+              mma_f8(dO, desc_add(dv, kk * 4096), desc_add(dp, 4096 + kk * 32), idO5, 1u);
+              mma_f8(dO, desc_add(dv, kk * 4096), desc_add(dq, kk * 32), idO5, 1u);
             }
           }
         }
@@ -827,7 +864,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       return __shfl_sync(0xffffffffu, (c >= 32) == (pair != 0) ? own : other, c & 31);
     };
     int flags = 0;
-    LatentTileRing at, at1, at2;                   // this tile, the one before, the one before that
+    LatentTileRing at, at1;                        // this tile, the one before
     // the MMAs of O of a tile are done
     const auto pv_done = [&](const LatentTileRing& tile) {
       return warp_wait(BAR(C::kEmptyB + tile.slot), tile.parity, abort_flag);
@@ -837,7 +874,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int k = 0; any && !(flags & kFinal); ++k) {
       const int ri = k % kRing, s = k % C::kSBufs;
       if (k > 0) {
-        at2 = at1;
         at1 = at;
         at.next();
       }
@@ -855,8 +891,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         l = 0.f;
       }
       float x[16];
-      uint8_t* pb = kFp8 ? sm + C::kPOff + (k & 1) * 8192
-                         : sm + C::kKOff + at.slot * C::kBufBytes + 8 * kChunkBytes;   // P of this tile
+      // P of this tile: in its last slot, whose rotary part only S needed
+      uint8_t* pb = sm + C::kKOff + at.slot * C::kBufBytes + (C::kSlots - 1) * kChunkBytes;
       {
         float th[16];
         const uint32_t sa = lane_base + kSCol + (kFp8 ? s * 64 : half * 64) + 16 * ch;
@@ -870,8 +906,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int j = 0; j < 16; ++j) th[j] = x[j] = 0.f;
         }
-        // e4m3: PV of the tile two before has read the P buffer
-        if (kFp8 && k >= 2) ok = pv_done(at2) && ok;
         // The warps of the other block have the other part of S: swap the entries that are not one's
         // own with one of them, eight at a time, through a quarter of P's rows.  A warp's second eight
         // go where it has just read, so one barrier a round is enough.
@@ -899,7 +933,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t valid = ((half ? vb : va) >> (16 * ch)) & 0xffffu;
       float mt = -INFINITY, arg = 1.f;              // log2 of the weights: arg x
       if (kFp8) {
-        // (info.scale holds 2^5 times the rows' scales, and this table 2^-5 over the heads')
+        // (info.scale holds kPUnit times the rows' scales, and this table 1 / kPUnit over the heads')
         arg = p.scale_log2 *
               reinterpret_cast<const float*>(sm + C::kQScaleOff)[(items & 3) * kHeads + head];
         const float4* ks4 = reinterpret_cast<const float4*>(info.scale + e0);
@@ -967,30 +1001,34 @@ __global__ void __launch_bounds__(kThreads, 1)
                          pack_bf16x2(e[6], e[7]));
         }
       } else {
-        // u = 2^5 p scale (at most 2^11, as tau = 6) in f16, whose upper byte is an e5m2 number: that
-        // byte rounded to nearest is the high term, what it leaves (an eighth at most, exact in f16)
-        // the low term in e4m3
+        // u = kPUnit p scale (at most 2^15) in f16, whose upper byte is an e5m2 number: the nearest one by
+        // adding half a step to the bits, then the same of what it leaves (exact in f16), and again.
+        // (A NaN's bits run over here; it comes back through the denominator.)
         const float4* ks4 = reinterpret_cast<const float4*>(info.scale + e0);
-        uint32_t hw[4], lw[4];                     // one 16-byte unit: sixteen entries
+        uint32_t w[3][4];                          // of each term one 16-byte unit: sixteen entries
+        const auto upper = [](uint32_t f16x2) { return (f16x2 + 0x00800080u) & 0xff00ff00u; };
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           const float4 c = ks4[q];
           const float* e = x + 4 * q;
-          uint32_t h2[2], l2[2];
+          uint32_t t[3][2];
 #pragma unroll
           for (int z = 0; z < 2; ++z) {
-            const __half2 y = z ? __floats2half2_rn(e[2] * c.z, e[3] * c.w) : __floats2half2_rn(e[0] * c.x, e[1] * c.y);
-            h2[z] = (*reinterpret_cast<const uint32_t*>(&y) + 0x00800080u) & 0xff00ff00u;
-            const __half2 rest = __hsub2(y, *reinterpret_cast<const __half2*>(&h2[z]));
-            l2[z] = (uint32_t)__nv_cvt_halfraw2_to_fp8x2(*reinterpret_cast<const __half2_raw*>(&rest),
-                                                         __NV_SATFINITE, __NV_E4M3);
+            __half2 y = z ? __floats2half2_rn(e[2] * c.z, e[3] * c.w) : __floats2half2_rn(e[0] * c.x, e[1] * c.y);
+#pragma unroll
+            for (int i = 0; i < 3; ++i) {
+              t[i][z] = upper(*reinterpret_cast<const uint32_t*>(&y));
+              if (i < 2) y = __hsub2(y, *reinterpret_cast<const __half2*>(&t[i][z]));
+            }
           }
-          hw[q] = __byte_perm(h2[0], h2[1], 0x7531);
-          lw[q] = __byte_perm(l2[0], l2[1], 0x5410);
+#pragma unroll
+          for (int i = 0; i < 3; ++i) w[i][q] = __byte_perm(t[i][0], t[i][1], 0x7531);
         }
-        uint8_t* d = pb + head * 64 + ((part ^ ((head >> 1) & 3)) << 4);
-        *reinterpret_cast<uint4*>(d) = make_uint4(hw[0], hw[1], hw[2], hw[3]);
-        *reinterpret_cast<uint4*>(d + 4096) = make_uint4(lw[0], lw[1], lw[2], lw[3]);
+        const int unit = head * 64 + ((part ^ ((head >> 1) & 3)) << 4);
+        *reinterpret_cast<uint4*>(pb + unit) = make_uint4(w[0][0], w[0][1], w[0][2], w[0][3]);
+        *reinterpret_cast<uint4*>(pb + 4096 + unit) = make_uint4(w[1][0], w[1][1], w[1][2], w[1][3]);
+        *reinterpret_cast<uint4*>(sm + C::kPOff + at.slot * 4096 + unit) =
+            make_uint4(w[2][0], w[2][1], w[2][2], w[2][3]);
       }
       if ((va & vb) != 0xffffffffu) {
         // entries that take no part: their rows hold other data or none, and a probability of zero
@@ -1055,12 +1093,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!exchange(l, own, other)) break;
       const float ls = (own[0] + own[1]) + (own[2] + own[3]);
       const float lso = (other[0] + other[1]) + (other[2] + other[3]);
-      constexpr float kUnit = kFp8 ? 1.f / 32.f : 1.f;
-      const float inv = m == -INFINITY ? 0.f : kUnit / ls, invo = mo == -INFINITY ? 0.f : kUnit / lso;
+      // (0: no entry at all.  A NaN among the scores is in the sum, whatever the maximum is.)
+      constexpr float kUnit = kFp8 ? 1.f / kPUnit : 1.f;
+      const float inv = ls == 0.f ? 0.f : kUnit / ls, invo = lso == 0.f ? 0.f : kUnit / lso;
       const int Hg = min(kHeads, a.H - g * kHeads);
       const size_t pslot = (size_t)blockIdx.x * 2 + (slot > 0 ? 1 : 0);
       if (slot >= 0 && part == 0)
-        p.lse[pslot * kHeads + head] = m == -INFINITY ? -INFINITY : m + __log2f(ls);
+        p.lse[pslot * kHeads + head] = ls == 0.f ? -INFINITY : m + __log2f(ls);
       ok = pv_done(at) && ok;
       tc_fence_after();
       // TMEM lane -> channel of tile i of O^T: d0 + i dstep; sixteen heads (columns) at a time

@@ -216,7 +216,7 @@ void decode(bool fp8, bool boxed, int pring, unsigned grow, const std::vector<in
     // softmax
     m.wait(soft, s_full(k), sp, sp & 1);
     m.arrive(soft, s_empty(k));
-    if (fp8 && k >= 2) wait_pv(k - 2, at2);
+    if (pring && fp8 && k >= 2) wait_pv(k - 2, at2);   // (its P had two places of its own then)
     if ((grow >> k & 1) && !t.first) wait_pv(k - 1, at1);
     m.arrive(soft, p_full(k, at));
     m.arrive(soft, info_empty(k));
