@@ -392,10 +392,12 @@ int sparse_attn_latent_read_fp8(const spa_latent_pool_t* pool, int32_t num_rows,
  * head's largest value each.
  * workspace: device memory, 16-byte aligned, of at least
  * sparse_attn_latent_decode_workspace_size(prob, pool) bytes (of the pool that is decoded: with its
- * scale, if it is an e4m3 one) for partial results of sequences that are split over several SMs and,
- * e4m3, for the queries' codes (1.1 times the queries' bytes, heads rounded up to 64); contents
- * scratch, nothing has to be cleared.  Calls that can run at the same time need workspaces of their
- * own; calls ordered on one stream (or graphs launched one after the other) may share one.
+ * scale, if it is an e4m3 one): partial results of sequences that are split over several SMs, which
+ * do not grow with the tokens, and, e4m3, the queries' codes,
+ *     num_tokens * ceil(num_heads / 64) * (ceil((latent_dim + 2 rope_dim) / 128) * 16384 + 256)
+ * bytes.  Contents scratch, nothing has to be cleared.  Calls that can run at the same time need
+ * workspaces of their own; calls ordered on one stream (or graphs launched one after the other) may
+ * share one.
  */
 typedef struct spa_latent_problem {
   int32_t num_tokens;

@@ -54,3 +54,22 @@ def test_calls_on_another_stream_keep_their_memory(dev, fp8, raw):  # noqa: F811
         assert torch.equal(out.view(torch.int16), want.view(torch.int16))
         assert torch.equal(got.view(torch.int16), rows.view(torch.int16))
     assert all(bool((x == 0xA5).all()) for x in held)
+
+
+@pytest.mark.parametrize("L,R,H", [(512, 64, 64), (64, 0, 16), (512, 8, 130), (448, 40, 20)])
+def test_decode_workspace_is_what_the_header_says(dev, L, R, H):  # noqa: F811
+    """bf16: no more for more tokens.  e4m3: the queries' codes on top, by the header's formula."""
+    table = torch.zeros((1, 1), dtype=torch.int32, device=dev)
+    bf16 = spa.LatentPool(torch.zeros((1, 64, L + R), dtype=torch.bfloat16, device=dev), table, R)
+    e4m3 = spa.LatentPool(torch.zeros((1, 64, L + 2 * R), dtype=torch.uint8, device=dev), table, R,
+                          torch.ones(64, device=dev))
+
+    def size(pool, tokens):
+        return spa.sparse_attn_latent_decode_workspace_size(
+            torch.empty((tokens, H, L), dtype=torch.bfloat16, device=dev), pool,
+            torch.zeros(tokens, dtype=torch.int32, device=dev), fp8=pool is e4m3)
+    codes = -(-H // 64) * (-(-(L + 2 * R) // 128) * 16384 + 256)
+    parts = size(bf16, 1)
+    for tokens in (1, 2, 7, 100):
+        assert size(bf16, tokens) == parts
+        assert parts + tokens * codes <= size(e4m3, tokens) < parts + tokens * codes + 256
