@@ -364,14 +364,17 @@ class BoundCall:
     between calls), with no per-call marshalling: what a serving loop or a timing loop wants.  The
     call goes to the stream given at bind time, or, if none was given, to torch's current stream at
     the time of the call (so that it can be recorded into a CUDA graph on the capturing stream).
-    The tensors are referenced here, so they stay alive as long as the object does.
+    The tensors are referenced here, so they stay alive as long as the object does.  Where the device of
+    the tensors is known it has to be the current one at the time of the call too.
     """
 
-    def __init__(self, fn, args, keep, stream=None):
-        self._fn, self._args, self._keep = fn, args, keep
+    def __init__(self, fn, args, keep, stream=None, device=None):
+        self._fn, self._args, self._keep, self._device = fn, args, keep, device
         self._stream = None if stream is None else _stream(stream)
 
     def __call__(self):
+        if self._device is not None:
+            _current_device(self._device)
         s = self._stream if self._stream is not None else \
             torch.cuda.current_stream().cuda_stream
         st = self._fn(*self._args, s)
@@ -811,10 +814,10 @@ def bind_latent_decode(q_latent, q_rope, pool, positions, *, fp8=False, stream=N
                        **kw) -> BoundCall:
     """``sparse_attn_latent_decode[_fp8]`` on fixed tensors, as a zero-argument callable (workspace
     and output are allocated here once when not given)."""
-    fn, args, _, out, workspace = _latent_decode_args(fp8, q_latent, q_rope, pool, positions,
-                                                      stream=stream, **kw)
+    fn, args, dev, out, workspace = _latent_decode_args(fp8, q_latent, q_rope, pool, positions,
+                                                        stream=stream, **kw)
     call = BoundCall(fn, args, (q_latent, q_rope, pool, positions, kw.get("seq_of_token"), out,
-                                workspace), stream)
+                                workspace), stream, dev)
     call.out = out
     call.workspace = workspace
     return call

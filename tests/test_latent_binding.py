@@ -149,3 +149,18 @@ def test_workspaces_with_gaps_or_repeats_are_refused(device):
         for decode in (spa.sparse_attn_paged_decode, spa.bind_decode):
             with pytest.raises(ValueError, match="workspace"):
                 decode(zeros(3, 2, 64), paged, None, topk, pos, window=16, ratio=4, scale=1.0, workspace=ws)
+
+
+def test_bound_call_on_another_device_is_refused(device, monkeypatch):
+    """A bound call goes to the current device's stream, so its tensors have to be there."""
+    lib, _, _ = device
+    bt, pos = zeros(1, 4, dtype=torch.int32), zeros(3, dtype=torch.int32)
+    for fp8, pool in enumerate(pools(bt)):
+        call = spa.bind_latent_decode(zeros(3, 2, 64), zeros(3, 2, 16), pool, pos, scale=1.0, fp8=bool(fp8))
+        call()
+        assert len(lib.streams) == fp8 + 1
+        with monkeypatch.context() as m:
+            m.setattr(torch._C, "_cuda_getDevice", lambda: 1)
+            with pytest.raises(ValueError, match="current device"):
+                call()
+        assert len(lib.streams) == fp8 + 1
