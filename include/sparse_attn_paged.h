@@ -382,6 +382,7 @@ int sparse_attn_latent_read_fp8(const spa_latent_pool_t* pool, int32_t num_rows,
  *   both 16-byte aligned, strides multiples of 8 elements and, where the dimension is over 1, at
  *   least the row's width.
  *   out:      bf16 [num_tokens][num_heads][latent_dim], 16-byte aligned, not overlapping an input.
+ * scale: any value whose product with log2(e) is a finite fp32 number.
  * A negative position attends to nothing: its output rows are zero (padding of a batch).  Entries
  * on unmapped pages, past the block table or outside the pool are left out and set SPA_ERR_INDEX,
  * as does a sequence id outside [0, num_seqs), whose output rows are zero.  What is left out never
@@ -430,6 +431,7 @@ int sparse_attn_latent_decode_fp8(const spa_latent_pool_t* pool, const spa_laten
  *   k_nope: bf16 [num_k] x [num_heads] rows of nope_dim;  v: the same, rows of v_dim
  *   k_rope: bf16 [num_k] rows of rope_dim (NULL when rope_dim == 0)
  *   out:    bf16 [num_q][num_heads][v_dim], 16-byte aligned, not overlapping an input
+ *   scale:  any value whose product with log2(e) is a finite fp32 number
  *   cu_q, cu_k: device int32 [num_seqs + 1], non-decreasing, within [0, num_q] and [0, num_k].  A
  *           sequence whose bounds are not, or that begins before an earlier one ends, is left out
  *           (its output rows keep their bytes) and sets SPA_ERR_INDEX.  Query rows of no sequence keep

@@ -13,6 +13,9 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 // element strides up to 2^38: byte offsets stay in 63 bits, and a tensor map holds 2^40 bytes
 bool stride_ok(int64_t s) { return s >= 0 && s <= (1ll << 38); }
 
+// The kernels take the scale times log2(e) in fp32.
+bool scale_ok(float s) { return std::isfinite(s * 1.4426950408889634f); }
+
 // Geometry that needs no pointer: checked even when there is nothing to do.
 int check_dims(const spa_latent_pool_t* pl) {
   if (pl->latent_dim < 1 || pl->rope_dim < 0) return SPA_ERR_SHAPE;
@@ -110,7 +113,7 @@ int latent_read(const spa_latent_pool_t* pool, int32_t n, const int32_t* positio
 // The sizes of a decode call; *work says whether there is anything to compute.
 int check_decode(const spa_latent_pool_t* pool, const spa_latent_problem_t* pr, bool* work) {
   if (!pool || !pr) return SPA_ERR_NULL;
-  if (pr->num_tokens < 0 || pr->num_seqs < 1 || pr->num_heads < 1 || !std::isfinite(pr->scale) ||
+  if (pr->num_tokens < 0 || pr->num_seqs < 1 || pr->num_heads < 1 || !scale_ok(pr->scale) ||
       !stride_ok(pr->q_latent_stride_t) || !stride_ok(pr->q_latent_stride_h) ||
       !stride_ok(pr->q_rope_stride_t) || !stride_ok(pr->q_rope_stride_h))
     return SPA_ERR_SHAPE;
@@ -238,7 +241,7 @@ int sparse_attn_latent_decode_fp8(const spa_latent_pool_t* pool, const spa_laten
 int sparse_attn_latent_prefill(const spa_latent_prefill_t* pr, void* out, void* stream) {
   if (!pr) return SPA_ERR_NULL;
   if (pr->num_q < 0 || pr->num_k < 0 || pr->num_seqs < 0 || pr->num_heads < 1 || pr->nope_dim < 1 ||
-      pr->rope_dim < 0 || pr->v_dim < 1 || !std::isfinite(pr->scale))
+      pr->rope_dim < 0 || pr->v_dim < 1 || !scale_ok(pr->scale))
     return SPA_ERR_SHAPE;
   if (pr->nope_dim % 8 != 0 || pr->nope_dim > 128 || pr->v_dim % 8 != 0 || pr->v_dim > 128 ||
       pr->rope_dim % 8 != 0 || pr->rope_dim > 64)
