@@ -345,8 +345,8 @@ typedef struct spa_latent_pool {
  * rotary part's high code likewise and its low code e4m3(x / scale - high), the difference in fp32
  * (exact).  A NaN element gives NaN codes and does not enter the maximum.
  * A token that cannot be placed is skipped and sets SPA_ERR_INDEX, as in the K/V write; slots that
- * no token addresses keep their bytes.  Two tokens writing one slot: the later write is not
- * defined.
+ * no token addresses keep their bytes.  Two tokens writing one slot: what the slot holds then is not
+ * defined (it may be parts of both).
  */
 int sparse_attn_latent_write(const void* latent, int64_t latent_stride, const void* rope,
                              int64_t rope_stride, int32_t num_tokens, const int32_t* positions,

@@ -13,10 +13,11 @@
 // loads under this row's codes, measured slower: 42 us against 31 for 65,536 e4m3 rows).
 //
 // Measured, L = 512, R = 64: 65,536 rows written as e4m3 in 24.8 us (4.8 TB/s, 70% of the measured copy
-// rate; its arithmetic keeps two thirds of the issue slots busy: with one value an instruction it took
-// 31, with IEEE divisions for the rotary part and 12 CTAs an SM 27.4), read back in 22.9 us (5.2 TB/s,
-// 76%); 30,001 bf16 rows written in 14.5 us, launch included (two to four rows in flight a warp: the
-// same or slower).  Eight tokens take 2 us, and the call's host side 13.
+// rate; its arithmetic takes two thirds of the issue slots: with one value an instruction it took
+// 31, with IEEE divisions for the rotary part and 12 CTAs an SM 27.4), read back in 22.8 us (5.2 TB/s,
+// 76%); 65,536 bf16 rows written in 26.8 us and read in 27.0 (5.6 TB/s, 83%), 30,001 of them in pages of 24
+// written in 14.4, launch included (two to four rows in flight a warp: the same or slower).  Eight tokens
+// take 2 us, and the call's host side 13.
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
@@ -30,7 +31,8 @@ namespace {
 
 constexpr int kWarps = 4;            // tokens in flight a CTA
 constexpr int kBlocks = 16;          // CTAs an SM, all resident: 64 warps of 32 registers (e4m3 write of 65,536
-                                     // rows: 26.3 us; with 41 registers and 12 of the 16 resident 28.1)
+                                     // rows: 26.3 us where 41 registers, and 12 CTAs resident, took 28.1; the
+                                     // rotary part's divisions as above brought 24.8)
 constexpr int kChunks = kLatMaxDim / 8 / 32;   // 16-byte chunks of the latent part a lane
 static_assert(kChunks == 2, "the write's slow path picks one of two");
 

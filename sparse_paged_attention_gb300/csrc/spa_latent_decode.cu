@@ -3,10 +3,11 @@
 //
 //   s_j = scale (q_c . c_j + q_r . r_j),   out = sum_j softmax(s)_j c_j,   j <= position
 //
-// Each row is read once from HBM and used by every head: 2 (2L + R) flops a head and row, so 64 heads
+// A row serves 64 heads of a token once it is in shared memory: 2 (2L + R) flops a head and row, so 64 heads
 // do about 121 flops a byte of a bf16 row (L = 512, R = 64) and 128 heads 242, where the machine
-// turns from HBM-bound to tensor-bound.  Both limits matter, so the products run on the tcgen05 tensor
-// cores from one copy of the row in shared memory, in tiles of 64 entries and 64 heads:
+// turns from HBM-bound to tensor-bound.  (More heads copy it again for every 64, and so does every further
+// token of its sequence: from L2, or from HBM where other rows have come between.)  Both limits matter, so the
+// products run on the tcgen05 tensor cores from one copy of the row, in tiles of 64 entries and 64 heads:
 //
 //   S[h][j]   = q_h . x_j           bf16: M = 128 stacks the two halves of the latent dimension,
 //                                   [q_h first half; q_h second half] against [rows' first half;
@@ -21,7 +22,7 @@
 // one is loaded, one multiplied, one waits for its softmax.  P takes the place of its own tile's
 // rotary chunk, which nobody reads any more.  TMEM: O^T 256 columns, S 128, q 128.  (e4m3 queries stay
 // in shared memory: there is room, and TMEM then has two S buffers, which measured faster, 194 us
-// against 217 for 48 sequences of 1 to 12,000 entries, two tokens each.)
+// against 217 for the 48 sequences below at the time.)
 //
 // What bounds a tile is shared memory's 128 bytes a cycle as much as the tensor core (bf16, L = 512,
 // R = 64: the MMAs read 184 KB, the copy writes 74, the softmax moves 40: 2,330 cycles, against 2,090
@@ -52,26 +53,27 @@
 //   by 2^-11 of itself at most (f16's rounding: the terms lose nothing more), or, below about 2^-16 of
 //   the largest, by 2^-17 of the unit, 2^-27 of the largest.
 // Small weights matter as much as large ones: 100,000 entries at 2^-13 of the largest outweigh it.  With an
-// e5m2 and an e4m3 term (ten bits less of range, and 7 us less for the 48 sequences below) such a tail came
-// out up to 11% short.  A reference that may be exceeded by 2^4, 2^5 or 2^6 before O is rescaled took
+// e5m2 and an e4m3 term (ten bits less of range; 128 us for the 48 sequences below where this takes 138) the
+// weights of such a tail were off by up to 11%.  A reference that may be exceeded by 2^4, 2^5 or 2^6 before O is rescaled took
 // 141, 138 and 138 us.  A row of zeros, whose stored scale is 1, would raise the reference by the seven or
 // so bits that this is above other rows': its scale counts as 0 here (its score is 0 and so are its values).
 //
 // Measured (L = 512, R = 64, calls one after the other, inputs larger than L2):
-//   64 sequences of up to 16,004 entries, 128 heads, bf16: 179 us (810 TFLOP/s, 43% of the measured bf16
-//     rate; 3.4 TB/s); 10 of them are the merge
-//   48 sequences of up to 11,581 entries, 2 tokens each, 64 heads, e4m3: 131 us, where a tile is about
-//     2,500 cycles of the softmax warps (swap, maxima, exponentials, the two terms of P, each a few
-//     hundred cycles and one after the other) against 1,730 of its MMAs
-//   one sequence of 131,071 entries, 16 heads, e4m3: 40 us; one of 4,097, 64 heads, bf16: 23 us, of which
+//   64 sequences of up to 16,004 entries, 128 heads, bf16: 182 us (797 TFLOP/s, 42% of the measured bf16
+//     rate; 3.4 TB/s), some 10 of them the merge; 107 tiles a CTA, tensor cores active 55% of the kernel
+//   48 sequences of up to 11,581 entries, 2 tokens each, 64 heads, e4m3: 138 us; 63 tiles a CTA, tensor cores
+//     active 36%: of about 3,900 cycles a tile, everything counted, 2,110 are its 44 MMAs; the softmax warps'
+//     parts (swap, maxima, exponentials, the three terms of P) follow one after the other
+//   one sequence of 131,071 entries, 16 heads, e4m3: 39 us; one of 4,097, 64 heads, bf16: 22.5 us, of which
 //     about 5 are the way to the first product, 3 the parts' stores and 8 the merge, its launch included
-// The loops that issue MMAs are kept short (no predicates in the whole chunks, not unrolled across them):
-// with both, 145, 184 and 44 us where these are 131, 179 and 40.
-// Also tried and slower: a softmax of two groups of four warps on alternate e4m3 tiles (181 us against
-// 153: the code twice as long costs more in instruction fetches than the overlap gives), a prefetch of
-// the next tile into L2, a separate warp for copies, S waiting on half tiles, the next tile's S read under
-// the sum of this one's weights (190 and 147 us against 183 and 143), longer and shorter polls; and, no
-// faster, e4m3's swap in one round.
+// Figures of variants, each against the kernel of its time:
+//   The loops that issue MMAs are kept short (no predicates in the whole chunks, not unrolled across them): 145,
+//   184 and 44 us became 131, 179 and 40.
+//   Tried and slower: a softmax of two groups of four warps on alternate e4m3 tiles (181 us against 153: the
+//   code twice as long costs more in instruction fetches than the overlap gives), a prefetch of the next tile
+//   into L2, a separate warp for copies, S waiting on half tiles, the next tile's S read under the sum of this
+//   one's weights (190 and 147 us against 183 and 143), longer and shorter polls; and, no faster, e4m3's
+//   swap in one round.
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
