@@ -42,9 +42,12 @@ cudaError_t collect_error_words(int* value) {
     }
     g_known[dev] = true;
   }
-  // On the legacy stream, as the copy after it and the copies of the other words.
-  collect_kernel<<<1, 1>>>(g_words[dev]);
-  e = cudaGetLastError();
+  // On the legacy stream, as the copy after it and the copies of the other words.  (The launch's own status: the
+  // last error may be one that somebody else left.)
+  cudaLaunchConfig_t c = {};
+  c.gridDim = dim3(1);
+  c.blockDim = dim3(1);
+  e = cudaLaunchKernelEx(&c, collect_kernel, g_words[dev]);
   if (e != cudaSuccess) return e;
   return cudaMemcpyFromSymbol(value, g_collected, sizeof(int));
 }

@@ -52,6 +52,21 @@ def test_words_of_the_indexer_and_the_latent_kernels(dev):
     assert spa.sparse_attn_paged_check_errors() == 0
 
 
+def test_an_error_left_by_another_call_is_not_reported(dev):
+    """A CUDA call of someone else that was refused (a copy of no such direction) is not the check's."""
+    lib = spa.load_library()
+    lib.cudaMemcpy.argtypes = [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int]
+    lib.cudaPeekAtLastError.argtypes, lib.cudaGetLastError.argtypes = [], []
+    host = ctypes.c_int(0)
+    refused = lib.cudaMemcpy(ctypes.addressof(host), ctypes.addressof(host), 4, 77)
+    assert refused != 0 and lib.cudaPeekAtLastError() == refused
+    try:
+        assert spa.sparse_attn_paged_check_errors() == 0
+        assert lib.cudaPeekAtLastError() == refused      # (nor is it taken away)
+    finally:
+        lib.cudaGetLastError()
+
+
 def test_cost_does_not_grow_with_the_kernels(dev):
     """No more than a read and a clear of three words, as it was before the latent kernels (six small
     blocking copies; half more for the spread of such times, where a word each would take twice as long)."""
