@@ -458,6 +458,128 @@ typedef struct spa_latent_prefill {
 
 int sparse_attn_latent_prefill(const spa_latent_prefill_t* prob, void* out, void* stream);
 
+/*
+ * Latent attention of drafted tokens (a tree checked at once).  The n_b = cu_tokens[b + 1] - cu_tokens[b]
+ * drafted tokens of sequence b are query rows cu_tokens[b] .., and their own rows lie in the cache behind the
+ * sequence's context: entries 0 .. context_lens[b] - 1 are the context, entry context_lens[b] + i is drafted
+ * token i (sparse_attn_latent_append with `entries` puts it there, at the angle of its depth).  Token i
+ * attends to the whole context and to the drafted tokens that its mask names, as a rule its ancestors and
+ * itself:
+ *     bit (i' % 32) of tree_mask[cu_tokens[b] + i][i' / 32] set  <=>  it sees drafted token i'
+ *     (drafted tokens past 32 mask_words, which have no bit, are not seen; bits past n_b mean nothing)
+ * tree_mask NULL: every token sees those before it and itself.  Scores, softmax, output, q_latent,
+ * q_rope, strides and scale are as in sparse_attn_latent_decode; a token that sees nothing gives zeros.
+ *   context_lens: device int32 [num_seqs], >= 0;  cu_tokens: device int32 [num_seqs + 1], non-decreasing,
+ *   within [0, num_tokens].  A sequence whose bounds are not, that begins before an earlier one ends, whose
+ *   context length is negative or whose entries do not fit its row of the block table is left out (its
+ *   output rows keep their bytes) and sets SPA_ERR_INDEX.  Query rows of no sequence keep their bytes.
+ * Entries on unmapped pages or outside the pool are left out and set SPA_ERR_INDEX.  What a token does not
+ * see never enters its sums, whatever its bytes hold.
+ * workspace: as for the decode, of sparse_attn_latent_tree_decode_workspace_size(prob, pool) bytes.
+ */
+typedef struct spa_latent_tree {
+  int32_t num_tokens;
+  int32_t num_seqs;
+  int32_t num_heads;
+  int32_t mask_words;           /* 32-bit words of a token's mask, >= 1 (0 without masks)     */
+  float scale;
+  int32_t reserved;             /* 0                                                          */
+  const int32_t* context_lens;
+  const int32_t* cu_tokens;
+  const uint32_t* tree_mask;    /* device [num_tokens][mask_words] or NULL                    */
+  const void* q_latent;
+  const void* q_rope;
+  int64_t q_latent_stride_t, q_latent_stride_h;
+  int64_t q_rope_stride_t, q_rope_stride_h;
+} spa_latent_tree_t;
+
+size_t sparse_attn_latent_tree_decode_workspace_size(const spa_latent_tree_t* prob,
+                                                     const spa_latent_pool_t* pool);
+int sparse_attn_latent_tree_decode(const spa_latent_pool_t* pool, const spa_latent_tree_t* prob, void* out,
+                                   void* workspace, size_t workspace_bytes, void* stream);
+int sparse_attn_latent_tree_decode_fp8(const spa_latent_pool_t* pool, const spa_latent_tree_t* prob, void* out,
+                                       void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * ---- Rotary positions, norms of heads, and appends that do both on the way ----
+ *
+ * Rotation of rope_dim values of a row, from value rope_start on, by the token's position p:
+ *     (a, b)_i -> rope_scale * (a cos t_i - b sin t_i, b cos t_i + a sin t_i),   t_i = 2 pi p turns[i] / 2^64
+ * (inverse: by -t_i).  interleaved: pair i is values 2i and 2i + 1 of the part; else i and i + rope_dim / 2.
+ *   turns: device int64 [rope_dim / 2], the frequencies in turns a position as 64-bit binary fractions (a
+ *          frequency of f radians is f / (2 pi) 2^64): the angle is that of the given frequency at
+ *          every 32-bit position.  Frequencies scaled for long contexts are other numbers here, and an
+ *          amplitude goes into rope_scale (finite).  NULL when rope_dim == 0.
+ * rope_dim: a multiple of 8, 0 .. 256; rope_start: a multiple of 8; rope_start + rope_dim <= head_dim.
+ * Rows are bf16, 16-byte aligned, strides in elements, multiples of 8.  Everything between the input's
+ * and the output's rounding is fp32.
+ */
+typedef struct spa_head_rows {  /* [num_tokens] x [num_heads] rows of head_dim values */
+  const void* x;
+  void* out;                    /* x itself, with its strides, or memory that does not overlap it */
+  const void* weight;           /* norm weights [head_dim], fp32 or bf16; NULL: ones               */
+  int64_t x_stride_t, x_stride_h;
+  int64_t out_stride_t, out_stride_h;
+  int32_t num_heads;
+  int32_t reserved;             /* 0 */
+} spa_head_rows_t;
+
+typedef struct spa_rope_problem {
+  int32_t num_tokens;
+  int32_t head_dim;             /* a multiple of 8, 8 .. 1024 */
+  int32_t rope_dim, rope_start;
+  int32_t interleaved, inverse;
+  int32_t weight_dtype;         /* 0: fp32, 1: bf16 (16-byte aligned) */
+  int32_t reserved;             /* 0 */
+  float rope_scale, eps;
+  const int32_t* positions;     /* device [num_tokens], any value */
+  const int64_t* turns;
+  spa_head_rows_t q, k;         /* k.num_heads == 0: q alone */
+} spa_rope_problem_t;
+
+/* The rotation alone (values outside the rotated part are copied; in place they are not touched). */
+int sparse_attn_rope(const spa_rope_problem_t* prob, void* stream);
+/* RMS norm of every head of q and k, y = x / sqrt(mean(x^2) + eps) * weight over its head_dim values, then the
+ * rotation, in one pass.  eps > 0. */
+int sparse_attn_norm_rope(const spa_rope_problem_t* prob, void* stream);
+
+/*
+ * Appends: the rows of new tokens into their pool slots, normalised (norm != 0, over the row's
+ * values, by weight and eps) and rotated on the way.
+ *   paged pools:  k, v are bf16 [num_tokens] rows of head_dim (a multiple of 64, 64 .. 512).  K is normalised
+ *                 and rotated, V stored as it is.  _fp8: one scale for each, max|y| / 448 (1 for a row of
+ *                 zeros), codes of y / scale; V's codes and scale are those of the K/V write.
+ *   latent pools: k is the latent part (latent_dim values: normalised), v the rotary part (rope_dim values:
+ *                 rotated; NULL when there is none); head_dim and rope_dim are the pool's, rope_start is
+ *                 0.  _fp8: one scale a row over both, two codes a rotary value, as in the latent write.
+ * Values are quantised from fp32, without a rounding to bf16 in between.  A NaN gives NaN codes and does not
+ * enter a maximum.
+ *   positions: of the rotation, device [num_tokens], any value;  entries: the tokens' places in their
+ *   sequences' caches, device [num_tokens] (NULL: the positions), seq_of_token (NULL: sequence 0).  A token that
+ *   cannot be placed is skipped and sets SPA_ERR_INDEX, as in the K/V write.
+ */
+typedef struct spa_append {
+  int32_t num_tokens, num_seqs;
+  int32_t head_dim;
+  int32_t rope_dim, rope_start, interleaved;
+  int32_t norm;
+  int32_t weight_dtype;         /* 0: fp32, 1: bf16 (16-byte aligned) */
+  float rope_scale, eps;
+  const int32_t* positions;
+  const int32_t* entries;
+  const int32_t* seq_of_token;
+  const int64_t* turns;
+  const void* k;
+  const void* v;
+  const void* weight;           /* [head_dim] or NULL: ones */
+  int64_t k_stride, v_stride;   /* elements */
+} spa_append_t;
+
+int sparse_attn_paged_kv_append(const spa_append_t* prob, const spa_pool_t* pool, void* stream);
+int sparse_attn_paged_kv_append_fp8(const spa_append_t* prob, const spa_pool_t* pool, void* stream);
+int sparse_attn_latent_append(const spa_append_t* prob, const spa_latent_pool_t* pool, void* stream);
+int sparse_attn_latent_append_fp8(const spa_append_t* prob, const spa_latent_pool_t* pool, void* stream);
+
 /* Synchronises `stream`, returns the device error word (an OR of SPA_ERR_INDEX and
  * SPA_ERR_TIMEOUT, 0 if clean) accumulated since the last check on the current device, and
  * clears it.  Returns SPA_ERR_CUDA if the synchronisation itself fails. */

@@ -12,6 +12,7 @@ Pools are any object with ``kv`` ([num_blocks, page_size, 2, head_dim] bf16 or u
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 import struct
 from typing import NamedTuple, Optional
@@ -29,7 +30,11 @@ __all__ = [
     "bind_decode", "LatentPool", "sparse_attn_latent_write", "sparse_attn_latent_write_fp8",
     "sparse_attn_latent_read", "sparse_attn_latent_read_fp8", "sparse_attn_latent_decode",
     "sparse_attn_latent_decode_fp8", "sparse_attn_latent_decode_workspace_size",
-    "bind_latent_decode", "sparse_attn_latent_prefill",
+    "bind_latent_decode", "sparse_attn_latent_prefill", "RotaryTable", "sparse_attn_rotary_table",
+    "sparse_attn_rope", "sparse_attn_norm_rope", "sparse_attn_paged_kv_append",
+    "sparse_attn_paged_kv_append_fp8", "sparse_attn_latent_append", "sparse_attn_latent_append_fp8",
+    "sparse_attn_latent_tree_decode", "sparse_attn_latent_tree_decode_fp8",
+    "sparse_attn_latent_tree_decode_workspace_size", "bind_latent_tree_decode",
     "sparse_attn_paged_check_errors", "sparse_attn_paged_strerror", "SPA_STATUS",
 ]
 
@@ -89,6 +94,46 @@ class SpaLatentPrefillC(ctypes.Structure):
                 ("k_rope_stride_t", ctypes.c_int64),
                 ("v_stride_t", ctypes.c_int64), ("v_stride_h", ctypes.c_int64),
                 ("cu_q", ctypes.c_void_p), ("cu_k", ctypes.c_void_p)]
+
+
+class SpaLatentTreeC(ctypes.Structure):
+    _fields_ = [("num_tokens", ctypes.c_int32), ("num_seqs", ctypes.c_int32),
+                ("num_heads", ctypes.c_int32), ("mask_words", ctypes.c_int32),
+                ("scale", ctypes.c_float), ("reserved", ctypes.c_int32),
+                ("context_lens", ctypes.c_void_p), ("cu_tokens", ctypes.c_void_p),
+                ("tree_mask", ctypes.c_void_p), ("q_latent", ctypes.c_void_p),
+                ("q_rope", ctypes.c_void_p),
+                ("q_latent_stride_t", ctypes.c_int64), ("q_latent_stride_h", ctypes.c_int64),
+                ("q_rope_stride_t", ctypes.c_int64), ("q_rope_stride_h", ctypes.c_int64)]
+
+
+class SpaHeadRowsC(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("out", ctypes.c_void_p), ("weight", ctypes.c_void_p),
+                ("x_stride_t", ctypes.c_int64), ("x_stride_h", ctypes.c_int64),
+                ("out_stride_t", ctypes.c_int64), ("out_stride_h", ctypes.c_int64),
+                ("num_heads", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class SpaRopeProblemC(ctypes.Structure):
+    _fields_ = [("num_tokens", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("rope_dim", ctypes.c_int32), ("rope_start", ctypes.c_int32),
+                ("interleaved", ctypes.c_int32), ("inverse", ctypes.c_int32),
+                ("weight_dtype", ctypes.c_int32), ("reserved", ctypes.c_int32),
+                ("rope_scale", ctypes.c_float), ("eps", ctypes.c_float),
+                ("positions", ctypes.c_void_p), ("turns", ctypes.c_void_p),
+                ("q", SpaHeadRowsC), ("k", SpaHeadRowsC)]
+
+
+class SpaAppendC(ctypes.Structure):
+    _fields_ = [("num_tokens", ctypes.c_int32), ("num_seqs", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("rope_dim", ctypes.c_int32),
+                ("rope_start", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("norm", ctypes.c_int32), ("weight_dtype", ctypes.c_int32),
+                ("rope_scale", ctypes.c_float), ("eps", ctypes.c_float),
+                ("positions", ctypes.c_void_p), ("entries", ctypes.c_void_p),
+                ("seq_of_token", ctypes.c_void_p), ("turns", ctypes.c_void_p),
+                ("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("weight", ctypes.c_void_p),
+                ("k_stride", ctypes.c_int64), ("v_stride", ctypes.c_int64)]
 
 
 class SpaError(RuntimeError):
@@ -163,6 +208,21 @@ def load_library():
         f.restype = ctypes.c_int
     lib.sparse_attn_latent_prefill.argtypes = [P, P, P]
     lib.sparse_attn_latent_prefill.restype = ctypes.c_int
+    lib.sparse_attn_latent_tree_decode_workspace_size.argtypes = [P, P]
+    lib.sparse_attn_latent_tree_decode_workspace_size.restype = ctypes.c_size_t
+    for name in ("sparse_attn_latent_tree_decode", "sparse_attn_latent_tree_decode_fp8"):
+        f = getattr(lib, name)
+        f.argtypes = [P, P, P, P, ctypes.c_size_t, P]
+        f.restype = ctypes.c_int
+    for name in ("sparse_attn_rope", "sparse_attn_norm_rope"):
+        f = getattr(lib, name)
+        f.argtypes = [P, P]
+        f.restype = ctypes.c_int
+    for name in ("sparse_attn_paged_kv_append", "sparse_attn_paged_kv_append_fp8",
+                 "sparse_attn_latent_append", "sparse_attn_latent_append_fp8"):
+        f = getattr(lib, name)
+        f.argtypes = [P, P, P]
+        f.restype = ctypes.c_int
     lib.sparse_attn_paged_check_errors.argtypes = [P]
     lib.sparse_attn_paged_check_errors.restype = ctypes.c_int
     lib.sparse_attn_paged_strerror.argtypes = [ctypes.c_int]
@@ -866,6 +926,355 @@ def sparse_attn_latent_prefill(q, k_nope, k_rope, v, cu_q, cu_k, *, scale, out=N
     if st != 0:
         raise SpaError(st, "sparse_attn_latent_prefill")
     return out
+
+
+# ---- rotary positions, norms of heads, appends ------------------------------------------------
+class RotaryTable(NamedTuple):
+    """Rotary frequencies on the GPU (see the C header): ``turns`` int64 [rope_dim / 2], turns a position
+    as 64-bit binary fractions; ``interleaved``: pairs (2i, 2i + 1), else (i, i + rope_dim / 2); ``scale``:
+    the amplitude of rotated values.  Made by :func:`sparse_attn_rotary_table`."""
+    turns: torch.Tensor
+    interleaved: bool = True
+    scale: float = 1.0
+
+
+def sparse_attn_rotary_table(rope_dim, *, base=10000.0, interleaved=True, scaling=None, factor=1.0,
+                             original_length=4096, beta_fast=32.0, beta_slow=1.0, scale=None,
+                             inv_freq=None, device="cuda") -> RotaryTable:
+    """The table of ``rope_dim / 2`` frequencies base^(-2i / rope_dim), radians a position.
+
+    ``scaling``: None; "linear" (positions divided by ``factor``); "ntk" (the base grows by
+    factor^(d / (d - 2)), so that the slowest pair turns as slowly as with "linear"); "yarn" (pairs that
+    turn more than ``beta_fast`` times within ``original_length`` stay, those below ``beta_slow`` times are
+    divided by the factor, between them a ramp; the amplitude is 0.1 ln(factor) + 1).  ``scale``: another
+    amplitude.  ``inv_freq``: the frequencies themselves (a sequence or tensor), in place of all that."""
+    n = int(rope_dim) // 2
+    if int(rope_dim) != 2 * n or n < 0:
+        raise ValueError("rope_dim must be even")
+    if scaling not in (None, "linear", "ntk", "yarn"):
+        raise ValueError(f"scaling must be None, 'linear', 'ntk' or 'yarn', not {scaling!r}")
+    if not (math.isfinite(factor) and factor > 0.0 and math.isfinite(base) and base > 1.0):
+        raise ValueError("base must be over 1 and factor positive")
+    amplitude = 1.0
+    if inv_freq is not None:
+        freq = [float(f) for f in inv_freq]
+        if len(freq) != n or not all(math.isfinite(f) for f in freq):
+            raise ValueError(f"inv_freq must be {n} finite frequencies")
+    else:
+        if scaling == "ntk":
+            if n < 2:
+                raise ValueError("'ntk' needs a rope_dim of 4 or more")
+            base = base * factor ** (rope_dim / (rope_dim - 2))
+        freq = [base ** (-2.0 * i / rope_dim) for i in range(n)]
+        if scaling == "linear":
+            freq = [f / factor for f in freq]
+        elif scaling == "yarn":
+            def pair(turns):         # the pair (a real number) that turns so often within original_length
+                return rope_dim * math.log(original_length / (turns * 2.0 * math.pi)) / (2.0 * math.log(base))
+            if not (0.0 < beta_slow <= beta_fast and original_length > 0):
+                raise ValueError("'yarn' needs 0 < beta_slow <= beta_fast and a positive original_length")
+            lo, hi = max(math.floor(pair(beta_fast)), 0), min(math.ceil(pair(beta_slow)), n - 1)
+            ramp = [min(max((i - lo) / max(hi - lo, 0.001), 0.0), 1.0) for i in range(n)]
+            freq = [f / factor * r + f * (1.0 - r) for f, r in zip(freq, ramp)]
+            amplitude = 0.1 * math.log(factor) + 1.0 if factor > 1.0 else 1.0
+    if scale is not None:
+        amplitude = float(scale)
+    # (whole turns a position change nothing; the remainder to the nearest of 2^64 parts, as a signed word)
+    words = [round(math.fmod(f / (2.0 * math.pi), 1.0) * 2.0 ** 64) % (1 << 64) for f in freq]
+    turns = torch.tensor([w - (1 << 64) if w >= 1 << 63 else w for w in words], dtype=torch.int64)
+    return RotaryTable(turns.to(device), bool(interleaved), amplitude)
+
+
+_ROPE = struct.Struct("=iiiiiiiiffQQ" + 2 * "QQQqqqqii")      # SpaRopeProblemC
+_APPEND = struct.Struct("=iiiiiiiiffQQQQQQQqq")               # SpaAppendC
+_LATENT_TREE = struct.Struct("=iiiifiQQQQQqqqq")              # SpaLatentTreeC
+_NO_ROWS = (0, 0, 0, 0, 0, 0, 0, 0, 0)
+
+
+def _rotary(table, dev):
+    """(rope_dim, address, interleaved, amplitude) of a checked table (None: no rotation)."""
+    if table is None:
+        return 0, 0, 0, 1.0
+    turns = table.turns
+    if turns.dtype is not torch.int64 or turns.dim() != 1 or not turns.is_contiguous():
+        raise ValueError("a rotary table's turns must be a contiguous int64 [rope_dim / 2] tensor")
+    _same_device("the rotary table", turns, dev)
+    n = turns.numel()
+    return 2 * n, turns.data_ptr() if n else 0, int(table.interleaved), table.scale
+
+
+def _weight(name, weight, width, dev):
+    """(address, dtype code) of checked norm weights (None: ones)."""
+    if weight is None:
+        return 0, -1
+    if weight.dtype not in (torch.float32, torch.bfloat16) or weight.numel() != width or \
+            weight.dim() != 1 or not weight.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous fp32 or bf16 [{width}] tensor")
+    _same_device(name, weight, dev)
+    return weight.data_ptr(), int(weight.dtype is torch.bfloat16)
+
+
+def _rope_out(name, x, out, stream):
+    if out is None:
+        return _empty(x.shape, torch.bfloat16, x.device, stream)
+    if out.shape != x.shape:
+        raise ValueError(f"{name} must have its input's shape")
+    return out
+
+
+def _rope_positions(positions, n, dev):
+    if positions.dtype is not torch.int32 or not positions.is_contiguous() or positions.numel() != n:
+        raise ValueError(f"positions must be a contiguous int32 tensor of {n} entries")
+    _same_device("positions", positions, dev)
+    return positions.data_ptr()
+
+
+def sparse_attn_rope(x, positions, table, *, start=None, inverse=False, out=None, stream=None):
+    """Rotates part of every head of ``x`` (bf16 [T, H, D], strided views allowed) by the angles of the
+    tokens' ``positions`` (int32 [T]): values ``start`` .. of a head (default: its last ones).  ``inverse``
+    takes a rotation off again (what an attention whose values were rotated with its keys needs of its
+    output).  Returns ``out``: a new tensor, or the one given, ``x`` itself among them (in place)."""
+    lib = load_library()
+    dev = x.get_device()
+    (T, H, D), st, sh = _latent_rows("x", x, 3, None, dev)
+    R, turns, interleaved, amplitude = _rotary(table, dev)
+    pos = _rope_positions(positions, T, dev)
+    _current_device(dev)
+    out = _rope_out("out", x, out, stream)
+    _, ot, oh = _latent_rows("out", out, 3, D, dev)
+    prob = _ROPE.pack(T, D, R, D - R if start is None else start, interleaved, bool(inverse), 0, 0, amplitude,
+                      1.0, pos, turns, x.data_ptr(), out.data_ptr(), 0, st, sh, ot, oh, H, 0, *_NO_ROWS)
+    s = lib.sparse_attn_rope(prob, _launch_stream(stream, dev))
+    if s != 0:
+        raise SpaError(s, "sparse_attn_rope")
+    return out
+
+
+def sparse_attn_norm_rope(q, k, positions, table, *, q_weight=None, k_weight=None, eps=1e-6, start=None,
+                          q_out=None, k_out=None, stream=None):
+    """RMS norm of every head of ``q`` [T, Hq, D] and ``k`` [T, Hk, D] (None: q alone; bf16, strided views
+    allowed) over its D values, by the weights (fp32 or bf16 [D], both of one type; None: ones), then the
+    rotation of part of it as in :func:`sparse_attn_rope` (``table`` None: none), in one pass.  Returns
+    (q_out, k_out): new tensors, or those given (in place if they are the inputs)."""
+    lib = load_library()
+    dev = q.get_device()
+    (T, H, D), st, sh = _latent_rows("q", q, 3, None, dev)
+    R, turns, interleaved, amplitude = _rotary(table, dev)
+    pos = _rope_positions(positions, T, dev)
+    qw, qd = _weight("q_weight", q_weight, D, dev)
+    kw, kd = _weight("k_weight", k_weight, D, dev)
+    if qd >= 0 and kd >= 0 and qd != kd:
+        raise ValueError("q_weight and k_weight must have one type")
+    _current_device(dev)
+    k_rows = _NO_ROWS
+    if k is not None:
+        (n, kh, _), kt, ks = _latent_rows("k", k, 3, D, dev)
+        if n != T:
+            raise ValueError("q and k must have the same tokens")
+        k_out = _rope_out("k_out", k, k_out, stream)
+        _, ot, oh = _latent_rows("k_out", k_out, 3, D, dev)
+        k_rows = (k.data_ptr(), k_out.data_ptr(), kw, kt, ks, ot, oh, kh, 0)
+    q_out = _rope_out("q_out", q, q_out, stream)
+    _, ot, oh = _latent_rows("q_out", q_out, 3, D, dev)
+    prob = _ROPE.pack(T, D, R, D - R if start is None else start, interleaved, 0, max(qd, kd, 0), 0, amplitude,
+                      eps, pos, turns, q.data_ptr(), q_out.data_ptr(), qw, st, sh, ot, oh, H, 0, *k_rows)
+    s = lib.sparse_attn_norm_rope(prob, _launch_stream(stream, dev))
+    if s != 0:
+        raise SpaError(s, "sparse_attn_norm_rope")
+    return q_out, k_out
+
+
+def _append_struct(k, v, positions, R, start, k_width, k_stride, v_stride, B, dev, weight, eps, entries,
+                   seq_of_token, turns, interleaved, amplitude, T):
+    pos, seq = _latent_index(positions, seq_of_token, T, dev)
+    at = 0
+    if entries is not None:
+        if entries.dtype is not torch.int32 or not entries.is_contiguous() or entries.numel() != T:
+            raise ValueError(f"entries must be a contiguous int32 tensor of {T} entries")
+        _same_device("entries", entries, dev)
+        at = entries.data_ptr()
+    wp, wd = _weight("weight", weight, k_width, dev)
+    if weight is not None and eps is None:
+        raise ValueError("weight is the norm's: it needs eps")
+    return _APPEND.pack(T, B, k_width, R, start, interleaved, eps is not None, max(wd, 0), amplitude,
+                        0.0 if eps is None else eps, pos, at, seq, turns, k.data_ptr(),
+                        0 if v is None else v.data_ptr(), wp, k_stride, v_stride)
+
+
+def _kv_append(fp8, k, v, positions, pool, table, *, weight=None, eps=None, start=None, entries=None,
+               seq_of_token=None, num_seqs=None, stream=None):
+    lib = load_library()
+    c = _pool_c(pool, fp8)
+    dev = pool.kv.get_device()
+    _same_device("block_table", pool.block_table, dev)
+    rows = c.num_blocks * c.page_size
+    for name, t in (("k_scale", pool.k_scale), ("v_scale", pool.v_scale)) if fp8 else ():
+        if t is None or t.dtype is not torch.float32 or not t.is_contiguous() or t.numel() != rows:
+            raise ValueError(f"an e4m3 pool needs a contiguous fp32 {name} of num_blocks * page_size")
+        _same_device(name, t, dev)
+    D = pool.kv.shape[3]
+    (T, _), k_stride = _latent_rows("k", k, 2, D, dev)
+    (n, _), v_stride = _latent_rows("v", v, 2, D, dev)
+    if n != T:
+        raise ValueError("k and v must have the same number of rows")
+    R, turns, interleaved, amplitude = _rotary(table, dev)
+    B = _num_seqs(num_seqs, pool.block_table.shape[0])
+    prob = _append_struct(k, v, positions, R, D - R if start is None else start, D, k_stride, v_stride, B, dev,
+                          weight, eps, entries, seq_of_token, turns, interleaved, amplitude, T)
+    _current_device(dev)
+    fn = lib.sparse_attn_paged_kv_append_fp8 if fp8 else lib.sparse_attn_paged_kv_append
+    st = fn(prob, ctypes.byref(c), _launch_stream(stream, dev))
+    if st != 0:
+        raise SpaError(st, fn.__name__)
+
+
+def sparse_attn_paged_kv_append(k, v, positions, pool, table, **kw):
+    """New tokens' K rows (bf16 [T, D], row stride free), normalised (where ``eps`` is given, by
+    ``weight``) and rotated by ``positions`` (``table`` None: not), and V rows, as they are, into their
+    slots of a bf16 pool: entry ``entries[t]`` (default: the position) of sequence ``seq_of_token[t]``.
+    ``start``: first rotated value (default: the last ones of the row are rotated)."""
+    _kv_append(False, k, v, positions, pool, table, **kw)
+
+
+def sparse_attn_paged_kv_append_fp8(k, v, positions, pool, table, **kw):
+    """The same into an e4m3 pool, one scale for each K and V row."""
+    _kv_append(True, k, v, positions, pool, table, **kw)
+
+
+def _latent_append(fp8, latent, rope, positions, pool, table, *, weight=None, eps=None, entries=None,
+                   seq_of_token=None, num_seqs=None, stream=None):
+    lib = load_library()
+    packed, L, R, dev, seqs = _latent_pool(pool, fp8)
+    (T, _), stride = _latent_rows("latent", latent, 2, L, dev)
+    rope_stride = 0
+    if R > 0:
+        if rope is None or table is None:
+            raise ValueError("the pool's rows have a rotary part: rope or its table is missing")
+        (n, _), rope_stride = _latent_rows("rope", rope, 2, R, dev)
+        if n != T:
+            raise ValueError("latent and rope must have the same number of rows")
+    else:
+        rope = table = None
+    width, turns, interleaved, amplitude = _rotary(table, dev)
+    if width != R:
+        raise ValueError(f"the rotary table is for {width} values, the pool's rotary part has {R}")
+    B = _num_seqs(num_seqs, seqs)
+    prob = _append_struct(latent, rope, positions, R, 0, L, stride, rope_stride, B, dev, weight, eps, entries,
+                          seq_of_token, turns, interleaved, amplitude, T)
+    _current_device(dev)
+    fn = lib.sparse_attn_latent_append_fp8 if fp8 else lib.sparse_attn_latent_append
+    st = fn(prob, packed, _launch_stream(stream, dev))
+    if st != 0:
+        raise SpaError(st, fn.__name__)
+
+
+def sparse_attn_latent_append(latent, rope, positions, pool, table, **kw):
+    """Rows of new tokens into a bf16 latent pool: ``latent`` [T, L] normalised (where ``eps`` is given, by
+    ``weight``), ``rope`` [T, R] rotated by ``positions`` (views of one projection's output will do).  They
+    go to entry ``entries[t]`` (default: the position) of sequence ``seq_of_token[t]``."""
+    _latent_append(False, latent, rope, positions, pool, table, **kw)
+
+
+def sparse_attn_latent_append_fp8(latent, rope, positions, pool, table, **kw):
+    """The same into an e4m3 pool (one scale a row, two codes a rotary value)."""
+    _latent_append(True, latent, rope, positions, pool, table, **kw)
+
+
+# ---- latent attention of drafted trees --------------------------------------------------------
+def _latent_tree_args(fp8, q_latent, q_rope, pool, context_lens, cu_tokens, tree_mask=None, *, scale,
+                      out=None, workspace=None, stream=None):
+    """Checked arguments of a tree decode on `stream`: (C function, its arguments, device index, out,
+    workspace)."""
+    lib = load_library()
+    packed, L, R, dev, seqs = _latent_pool(pool, fp8)
+    (T, H, _), ql_st, ql_sh = _latent_rows("q_latent", q_latent, 3, L, dev)
+    qr = qr_st = qr_sh = 0
+    if R > 0:
+        if q_rope is None:
+            raise ValueError("the pool's rows have a rotary part: q_rope is missing")
+        (t, h, _), qr_st, qr_sh = _latent_rows("q_rope", q_rope, 3, R, dev)
+        if t != T or h != H:
+            raise ValueError("q_latent and q_rope must have the same tokens and heads")
+        qr = q_rope.data_ptr()
+    B = context_lens.numel()
+    if B > seqs:
+        raise ValueError("context_lens has more sequences than the block table rows")
+    for name, t, n in (("context_lens", context_lens, B), ("cu_tokens", cu_tokens, B + 1)):
+        if t.dtype is not torch.int32 or t.dim() != 1 or not t.is_contiguous() or t.numel() != n:
+            raise ValueError(f"{name} must be a contiguous int32 [{n}] tensor")
+        _same_device(name, t, dev)
+    mask = words = 0
+    if tree_mask is not None:
+        if tree_mask.dtype is not torch.int32 or tree_mask.dim() != 2 or tree_mask.shape[0] != T or \
+                tree_mask.shape[1] < 1 or not tree_mask.is_contiguous():
+            raise ValueError("tree_mask must be a contiguous int32 [num_tokens, words] tensor")
+        _same_device("tree_mask", tree_mask, dev)
+        mask, words = tree_mask.data_ptr(), tree_mask.shape[1]
+    if out is not None:
+        if out.dtype is not torch.bfloat16 or tuple(out.shape) != (T, H, L) or not out.is_contiguous():
+            raise ValueError("out must be a contiguous bf16 [num_tokens, num_heads, latent_dim] tensor")
+        _same_device("out", out, dev)
+    if workspace is not None:
+        _same_device("workspace", workspace, dev)
+    _current_device(dev)
+    if out is None:
+        out = _empty((T, H, L), torch.bfloat16, q_latent.device, stream)
+    prob = _LATENT_TREE.pack(T, B, H, words, scale, 0, context_lens.data_ptr(), cu_tokens.data_ptr(), mask,
+                             q_latent.data_ptr(), qr, ql_st, ql_sh, qr_st, qr_sh)
+    if workspace is None:
+        nbytes = max(lib.sparse_attn_latent_tree_decode_workspace_size(prob, packed), 16)
+        workspace = _empty(nbytes, torch.uint8, q_latent.device, stream)
+    else:
+        nbytes = _bytes("workspace", workspace)
+    fn = lib.sparse_attn_latent_tree_decode_fp8 if fp8 else lib.sparse_attn_latent_tree_decode
+    return fn, (packed, prob, out.data_ptr(), workspace.data_ptr(), nbytes), dev, out, workspace
+
+
+def _latent_tree_decode(fp8, *args, stream=None, **kw):
+    fn, c_args, dev, out, workspace = _latent_tree_args(fp8, *args, stream=stream, **kw)
+    st = fn(*c_args, _launch_stream(stream, dev))
+    if st != 0:
+        raise SpaError(st, fn.__name__)
+    return out
+
+
+def sparse_attn_latent_tree_decode(q_latent, q_rope, pool, context_lens, cu_tokens, tree_mask=None, **kw):
+    """Absorbed latent attention of drafted tokens over a paged bf16 latent pool: bf16 [T, H, L].
+
+    Sequence b's drafted tokens are rows ``cu_tokens[b] : cu_tokens[b + 1]`` of ``q_latent`` [T, H, L] and
+    ``q_rope`` [T, H, R]; in the cache they are entries ``context_lens[b] + i``, behind the context.  Each
+    sees the whole context and the drafted tokens i' whose bit i' % 32 of ``tree_mask[t, i' // 32]`` (int32)
+    is set; without a mask those before it and itself (see the C header).  Rows of no sequence keep
+    their bytes (a new ``out`` is not initialised).  The workspace is allocated with torch, on the call's
+    stream, if none is given."""
+    return _latent_tree_decode(False, q_latent, q_rope, pool, context_lens, cu_tokens, tree_mask, **kw)
+
+
+def sparse_attn_latent_tree_decode_fp8(q_latent, q_rope, pool, context_lens, cu_tokens, tree_mask=None, **kw):
+    """The same over an e4m3 latent pool."""
+    return _latent_tree_decode(True, q_latent, q_rope, pool, context_lens, cu_tokens, tree_mask, **kw)
+
+
+def sparse_attn_latent_tree_decode_workspace_size(q_latent, pool, num_seqs, *, fp8=False) -> int:
+    """Bytes of workspace that a tree decode of these shapes needs."""
+    lib = load_library()
+    packed, _, _, _, _ = _latent_pool(pool, fp8)
+    prob = _LATENT_TREE.pack(q_latent.shape[0], int(num_seqs), q_latent.shape[1], 0, 1.0, 0, 0, 0, 0,
+                             q_latent.data_ptr(), 0, 0, 0, 0, 0)
+    return int(lib.sparse_attn_latent_tree_decode_workspace_size(prob, packed))
+
+
+def bind_latent_tree_decode(q_latent, q_rope, pool, context_lens, cu_tokens, tree_mask=None, *, fp8=False,
+                            stream=None, **kw) -> BoundCall:
+    """``sparse_attn_latent_tree_decode[_fp8]`` on fixed tensors, as a zero-argument callable (workspace
+    and output are allocated here once when not given)."""
+    fn, args, dev, out, workspace = _latent_tree_args(fp8, q_latent, q_rope, pool, context_lens, cu_tokens,
+                                                      tree_mask, stream=stream, **kw)
+    call = BoundCall(fn, args, (q_latent, q_rope, pool, context_lens, cu_tokens, tree_mask, out, workspace),
+                     stream, dev)
+    call.out = out
+    call.workspace = workspace
+    return call
 
 
 def sparse_attn_paged_resolve_columns(win, cmp, topk_idx, positions, *, window, ratio,

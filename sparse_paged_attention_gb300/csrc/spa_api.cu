@@ -43,6 +43,7 @@ int current_device(int* dev, int* sms) {
     e = spa::prepare_attn_kernels();
     if (e == cudaSuccess) e = spa::prepare_latent_decode();
     if (e == cudaSuccess) e = spa::prepare_latent_prefill();
+    if (e == cudaSuccess) e = spa::prepare_latent_tree();
     if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute");
     g_sms[*dev] = n;
     for (int i = 1; i <= 4; ++i) {

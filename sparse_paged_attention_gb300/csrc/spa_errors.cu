@@ -8,7 +8,7 @@ namespace spa {
 namespace {
 
 constexpr int kMaxDevices = 64;
-constexpr int kWords = 4;
+constexpr int kWords = 6;
 struct Words {
   int* at[kWords];
 };
@@ -36,7 +36,8 @@ cudaError_t collect_error_words(int* value) {
   if (!g_known[dev]) {
     int i = 0;
     for (cudaError_t (*word)(int**) : {indexer_error_word, latent_cache_error_word,
-                                       latent_decode_error_word, latent_prefill_error_word}) {
+                                       latent_decode_error_word, latent_prefill_error_word,
+                                       latent_tree_error_word, rotary_error_word}) {
       e = word(&g_words[dev].at[i++]);
       if (e != cudaSuccess) return e;
     }

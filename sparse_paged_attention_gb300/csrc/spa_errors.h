@@ -10,6 +10,8 @@ cudaError_t indexer_error_word(int** word);
 cudaError_t latent_cache_error_word(int** word);
 cudaError_t latent_decode_error_word(int** word);
 cudaError_t latent_prefill_error_word(int** word);
+cudaError_t latent_tree_error_word(int** word);
+cudaError_t rotary_error_word(int** word);
 
 // The OR of those words on the current device, which are cleared: one kernel and one copy, whatever their
 // number, where a read and a clear of each are two blocking copies a word.

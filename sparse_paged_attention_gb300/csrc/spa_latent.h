@@ -62,6 +62,23 @@ size_t latent_decode_workspace(const LatentDecodeArgs& a, bool fp8, int sms);
 cudaError_t launch_latent_decode(const LatentDecodeArgs& a, bool fp8, void* workspace, int sms,
                                  cudaStream_t stream);
 
+struct LatentTreeArgs {
+  LatentPoolDev pool;
+  const uint8_t* q_latent;      // bf16, strides in bytes
+  const uint8_t* q_rope;
+  long long ql_st, ql_sh, qr_st, qr_sh;
+  uint8_t* out;                 // bf16 [T][H][L]
+  const int32_t* context_lens;  // [B]
+  const int32_t* cu_tokens;     // [B + 1]
+  const uint32_t* mask;         // [T][mask_words], or NULL: every token sees those before it
+  float scale;
+  int T, H, mask_words;
+};
+cudaError_t prepare_latent_tree();
+size_t latent_tree_workspace(const LatentTreeArgs& a, bool fp8, int sms);
+cudaError_t launch_latent_tree(const LatentTreeArgs& a, bool fp8, void* workspace, int sms,
+                               cudaStream_t stream);
+
 struct LatentPrefillArgs {
   const uint8_t *q, *k_nope, *k_rope, *v;   // bf16, strides in bytes
   long long q_st, q_sh, kn_st, kn_sh, kr_st, v_st, v_sh;

@@ -6,6 +6,7 @@
 #include "sparse_attn_paged.h"
 #include "spa_latent.h"
 #include "spa_launch.h"
+#include "spa_rotary.h"
 
 namespace {
 
@@ -180,9 +181,134 @@ int latent_decode(const spa_latent_pool_t* pool, const spa_latent_problem_t* pr,
   return e == cudaSuccess ? SPA_OK : spa::api_cuda_fail(e, "latent decode kernel launch");
 }
 
+int latent_append(const spa_append_t* pr, const spa_latent_pool_t* pool, void* stream, bool fp8) {
+  if (!pr || !pool) return SPA_ERR_NULL;
+  int st = check_dims(pool);
+  if (st) return st;
+  if (pr->head_dim != pool->latent_dim || pr->rope_dim != pool->rope_dim || pr->rope_start != 0)
+    return SPA_ERR_SHAPE;
+  st = spa::check_rotary(pr->rope_dim, 0, pr->rope_dim, pr->rope_scale, pr->turns);
+  if (st) return st;
+  st = spa::check_append(pr, pool->latent_dim, pool->rope_dim);
+  if (st || pr->num_tokens == 0) return st;
+  st = check_pool(pool, fp8);
+  if (st) return st;
+  int dev = 0, sms = 0;
+  st = spa::api_current_device(&dev, &sms);
+  if (st) return st;
+  spa::AppendArgs a;
+  spa::fill_append(a, pr);
+  fill_pool(a.pool, pool, pr->num_seqs, fp8);
+  a.k_scale = a.pool.scale;
+  const cudaError_t e = spa::launch_latent_append(a, fp8, sms, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? SPA_OK : spa::api_cuda_fail(e, "latent append kernel launch");
+}
+
+// The sizes of a tree decode; *work says whether there is anything to compute.
+int check_tree(const spa_latent_pool_t* pool, const spa_latent_tree_t* pr, bool* work) {
+  if (!pool || !pr) return SPA_ERR_NULL;
+  if (pr->num_tokens < 0 || pr->num_seqs < 0 || pr->num_heads < 1 || pr->mask_words < 0 ||
+      (pr->tree_mask && pr->mask_words < 1) || !scale_ok(pr->scale) || !stride_ok(pr->q_latent_stride_t) ||
+      !stride_ok(pr->q_latent_stride_h) || !stride_ok(pr->q_rope_stride_t) || !stride_ok(pr->q_rope_stride_h))
+    return SPA_ERR_SHAPE;
+  const int st = check_dims(pool);
+  if (st) return st;
+  if ((long long)pr->num_tokens * pr->num_heads > 0x3fffffffLL || pr->mask_words > (1 << 20))
+    return SPA_ERR_UNSUPPORTED;
+  *work = pr->num_tokens > 0 && pr->num_seqs > 0;
+  return SPA_OK;
+}
+
+void fill_tree(spa::LatentTreeArgs& a, const spa_latent_pool_t* pool, const spa_latent_tree_t* pr, void* out,
+               bool fp8) {
+  std::memset(&a, 0, sizeof a);
+  fill_pool(a.pool, pool, pr->num_seqs, fp8);
+  a.q_latent = static_cast<const uint8_t*>(pr->q_latent);
+  a.q_rope = static_cast<const uint8_t*>(pr->q_rope);
+  a.ql_st = 2 * pr->q_latent_stride_t;
+  a.ql_sh = 2 * pr->q_latent_stride_h;
+  a.qr_st = 2 * pr->q_rope_stride_t;
+  a.qr_sh = 2 * pr->q_rope_stride_h;
+  a.out = static_cast<uint8_t*>(out);
+  a.context_lens = pr->context_lens;
+  a.cu_tokens = pr->cu_tokens;
+  a.mask = pr->tree_mask;
+  a.scale = pr->scale;
+  a.T = pr->num_tokens;
+  a.H = pr->num_heads;
+  a.mask_words = pr->mask_words;
+}
+
+int latent_tree(const spa_latent_pool_t* pool, const spa_latent_tree_t* pr, void* out, void* workspace,
+                size_t workspace_bytes, void* stream, bool fp8) {
+  bool work = false;
+  int st = check_tree(pool, pr, &work);
+  if (st || !work) return st;
+  const bool has_rope = pool->rope_dim > 0;
+  const auto rows_ok = [&](int64_t st, int64_t sh, int width) {
+    return (pr->num_tokens <= 1 || st >= width) && (pr->num_heads <= 1 || sh >= width);
+  };
+  if (!rows_ok(pr->q_latent_stride_t, pr->q_latent_stride_h, pool->latent_dim) ||
+      (has_rope && !rows_ok(pr->q_rope_stride_t, pr->q_rope_stride_h, pool->rope_dim)))
+    return SPA_ERR_SHAPE;
+  if (!pr->context_lens || !pr->cu_tokens || !pr->q_latent || (has_rope && !pr->q_rope) || !out)
+    return SPA_ERR_NULL;
+  st = check_pool(pool, fp8);
+  if (st) return st;
+  if (!aligned16(out) || !aligned16(pr->q_latent) || pr->q_latent_stride_t % 8 != 0 ||
+      pr->q_latent_stride_h % 8 != 0)
+    return SPA_ERR_ALIGN;
+  if (has_rope && (!aligned16(pr->q_rope) || pr->q_rope_stride_t % 8 != 0 || pr->q_rope_stride_h % 8 != 0))
+    return SPA_ERR_ALIGN;
+  int dev = 0, sms = 0;
+  st = spa::api_current_device(&dev, &sms);
+  if (st) return st;
+  spa::LatentTreeArgs a;
+  fill_tree(a, pool, pr, out, fp8);
+  const size_t need = spa::latent_tree_workspace(a, fp8, sms);
+  if (need > 0) {
+    if (!workspace) return SPA_ERR_NULL;
+    if (!aligned16(workspace)) return SPA_ERR_ALIGN;
+    if (workspace_bytes < need) return SPA_ERR_WORKSPACE;
+  }
+  const cudaError_t e = spa::launch_latent_tree(a, fp8, workspace, sms, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? SPA_OK : spa::api_cuda_fail(e, "latent tree decode kernel launch");
+}
+
 }  // namespace
 
 extern "C" {
+
+int sparse_attn_latent_append(const spa_append_t* prob, const spa_latent_pool_t* pool, void* stream) {
+  return latent_append(prob, pool, stream, false);
+}
+
+int sparse_attn_latent_append_fp8(const spa_append_t* prob, const spa_latent_pool_t* pool, void* stream) {
+  return latent_append(prob, pool, stream, true);
+}
+
+size_t sparse_attn_latent_tree_decode_workspace_size(const spa_latent_tree_t* prob,
+                                                     const spa_latent_pool_t* pool) {
+  bool work = false;
+  if (check_tree(pool, prob, &work) || !work || pool->num_blocks < 1 || pool->page_size < 1 ||
+      pool->bt_stride < 1)
+    return 0;
+  int dev = 0, sms = 0;
+  if (spa::api_current_device(&dev, &sms) != SPA_OK) return 0;
+  spa::LatentTreeArgs a;
+  fill_tree(a, pool, prob, nullptr, false);
+  return spa::latent_tree_workspace(a, pool->scale != nullptr, sms);
+}
+
+int sparse_attn_latent_tree_decode(const spa_latent_pool_t* pool, const spa_latent_tree_t* prob, void* out,
+                                   void* workspace, size_t workspace_bytes, void* stream) {
+  return latent_tree(pool, prob, out, workspace, workspace_bytes, stream, false);
+}
+
+int sparse_attn_latent_tree_decode_fp8(const spa_latent_pool_t* pool, const spa_latent_tree_t* prob, void* out,
+                                       void* workspace, size_t workspace_bytes, void* stream) {
+  return latent_tree(pool, prob, out, workspace, workspace_bytes, stream, true);
+}
 
 int sparse_attn_latent_write(const void* latent, int64_t latent_stride, const void* rope,
                              int64_t rope_stride, int32_t num_tokens, const int32_t* positions,

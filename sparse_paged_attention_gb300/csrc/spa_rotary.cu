@@ -1,0 +1,540 @@
+// spa_rotary.cu - what lies between a layer's projections and its attention: the norm of every head, the
+// rotation of its rotary part by the token's position, and both on the way into a paged cache.
+//
+//   y = x rsqrt(mean(x^2) + eps) w,      (a, b)_i -> m (a cos t - b sin t, b cos t + a sin t),  t = pos f_i
+//
+// All of it is a row in, a row out: bound by HBM, or by latency where there are few rows.  A warp takes a
+// token's rows of several heads, all loads in flight before any is used; statistics and rotation are
+// fp32, with one rounding at the end.  The token's angles are worked out once a warp and serve its heads.
+//
+// Angles: a position times a frequency loses the angle's fraction in fp32 (at position 2^20 a step is 1/16
+// of a radian).  The frequencies come as turns a position in 64-bit binary fractions, so the product modulo
+// 2^64 is the fraction of a turn, exactly that of the given frequency at any position; its upper 32 bits
+// go to fp32 (off by 2^-32 turns and 2^-25 of itself).  In 64-bit floating point, which this machine
+// does at a sixty-fourth of the rate, the angles of 65,536 tokens alone would take about 10 us.
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+
+#include "spa_errors.h"
+#include "spa_kvwrite_quant.cuh"
+#include "spa_rotary.h"
+
+namespace spa {
+
+namespace {
+
+constexpr int kWarps = 4;
+
+// cos and sin (times the amplitude; sin negated for the inverse) of pairs 2w and 2w + 1.
+struct Angles {
+  float c[2], s[2];
+};
+__device__ __forceinline__ Angles angles(const RotaryDev& r, int pos, int w) {
+  Angles a;
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    const long long t = (long long)pos * __ldg(r.turns + 2 * w + e);
+    // half turns in [-1, 1)
+    sincospif((float)(int)(t >> 32) * 0x1p-31f, &a.s[e], &a.c[e]);
+    a.c[e] *= r.scale;
+    a.s[e] *= r.inverse ? -r.scale : r.scale;
+  }
+  return a;
+}
+
+// Pairs 2w and 2w + 1 of a row's rotary part: (a, b) of each.  Interleaved they are four values in a row, in
+// halves two of the first and two of the second half.
+struct Pairs {
+  uint32_t u, v;
+};
+__device__ __forceinline__ Pairs load_pairs(const uint8_t* part, const RotaryDev& r, int w) {
+  Pairs p;
+  if (r.half) {
+    p.u = *reinterpret_cast<const uint32_t*>(part + 4 * w);
+    p.v = *reinterpret_cast<const uint32_t*>(part + r.R + 4 * w);
+  } else {
+    const uint2 x = *reinterpret_cast<const uint2*>(part + 8 * w);
+    p.u = x.x;
+    p.v = x.y;
+  }
+  return p;
+}
+// The four values in the order in which they lie: half: a0 a1, b0 b1; else a0 b0, a1 b1.
+__device__ __forceinline__ void rotate(float (&x)[4], const RotaryDev& r, const Angles& t) {
+  const float a0 = x[0], b0 = r.half ? x[2] : x[1], a1 = r.half ? x[1] : x[2], b1 = x[3];
+  const float a2 = a0 * t.c[0] - b0 * t.s[0], b2 = b0 * t.c[0] + a0 * t.s[0];
+  const float a3 = a1 * t.c[1] - b1 * t.s[1], b3 = b1 * t.c[1] + a1 * t.s[1];
+  x[0] = a2;
+  x[1] = r.half ? a3 : b2;
+  x[2] = r.half ? b2 : a3;
+  x[3] = b3;
+}
+__device__ __forceinline__ void unpack(const Pairs& p, float (&x)[4]) {
+  x[0] = bf16_lo(p.u);
+  x[1] = bf16_hi(p.u);
+  x[2] = bf16_lo(p.v);
+  x[3] = bf16_hi(p.v);
+}
+__device__ __forceinline__ void store_pairs(uint8_t* part, const RotaryDev& r, int w, const float (&x)[4]) {
+  const uint32_t u = pack_bf16x2(x[0], x[1]), v = pack_bf16x2(x[2], x[3]);
+  if (r.half) {
+    *reinterpret_cast<uint32_t*>(part + 4 * w) = u;
+    *reinterpret_cast<uint32_t*>(part + r.R + 4 * w) = v;
+  } else {
+    *reinterpret_cast<uint2*>(part + 8 * w) = make_uint2(u, v);
+  }
+}
+
+// Weights of eight adjacent values, or of the values of pairs 2w and 2w + 1.
+__device__ __forceinline__ void weight8(const void* w, bool bf16, int at, float (&x)[8]) {
+  if (bf16) {
+    const uint4 u = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(w) + at));
+    const uint32_t v[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x[2 * i] = bf16_lo(v[i]);
+      x[2 * i + 1] = bf16_hi(v[i]);
+    }
+  } else {
+    const float4* f = reinterpret_cast<const float4*>(static_cast<const float*>(w) + at);
+    const float4 u = __ldg(f), v = __ldg(f + 1);
+    x[0] = u.x, x[1] = u.y, x[2] = u.z, x[3] = u.w;
+    x[4] = v.x, x[5] = v.y, x[6] = v.z, x[7] = v.w;
+  }
+}
+__device__ __forceinline__ float weight1(const void* w, bool bf16, int at) {
+  return bf16 ? bf16_lo(__ldg(static_cast<const uint16_t*>(w) + at)) : __ldg(static_cast<const float*>(w) + at);
+}
+__device__ __forceinline__ void weight_pairs(const void* wt, bool bf16, const RotaryDev& r, int w, float (&x)[4]) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e) x[e] = weight1(wt, bf16, r.start + (r.half ? 2 * w + (e & 1) + (e >> 1) * (r.R / 2) : 4 * w + e));
+}
+
+__device__ __forceinline__ float warp_sum(float x) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  return x;
+}
+__device__ __forceinline__ float sum_squares(const uint4& u) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+  float s = 0.f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    s = fmaf(bf16_lo(w[i]), bf16_lo(w[i]), s);
+    s = fmaf(bf16_hi(w[i]), bf16_hi(w[i]), s);
+  }
+  return s;
+}
+
+// The column of 16-byte chunk c of the values that are not rotated.
+__device__ __forceinline__ int plain_column(const RotaryDev& r, int c) { return 8 * c < r.start ? 8 * c : 8 * c + r.R; }
+
+// kC: 16-byte chunks a lane of the values that are not rotated (0: none, or they stay where they are);
+// kW: fours of rotated values a lane; kRows: heads of a token a warp takes at once.
+template <int kC, int kW, int kRows, bool kNorm>
+__global__ void __launch_bounds__(32 * kWarps) rope_kernel(const RopeArgs a, int units_q, int units_k) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const int lane = threadIdx.x & 31;
+  const int per_token = units_q + units_k;
+  const int units = a.T * per_token;             // (checked by the caller to fit)
+  const int n_plain = (a.D - a.rot.R) >> 3, n_pairs = a.rot.R >> 2;
+  for (int u = blockIdx.x * kWarps + (threadIdx.x >> 5); u < units; u += gridDim.x * kWarps) {
+    const int t = u / per_token, g = u - t * per_token;
+    const bool is_k = g >= units_q;
+    const HeadRows& x = is_k ? a.k : a.q;
+    const int h0 = (is_k ? g - units_q : g) * kRows;
+    const int pos = __ldg(a.positions + t);
+    const uint8_t* src = x.x + t * x.x_st + h0 * x.x_sh;
+    uint8_t* dst = x.out + t * x.out_st + h0 * x.out_sh;
+    const int rows = min(kRows, x.H - h0);
+    uint4 plain[kRows][kC ? kC : 1];
+    Pairs pair[kRows][kW];
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+      const uint8_t* row = src + (i < rows ? i : 0) * x.x_sh;
+#pragma unroll
+      for (int c = 0; c < kC; ++c)
+        plain[i][c] = lane + 32 * c < n_plain
+                          ? *reinterpret_cast<const uint4*>(row + 2 * plain_column(a.rot, lane + 32 * c))
+                          : make_uint4(0, 0, 0, 0);
+#pragma unroll
+      for (int w = 0; w < kW; ++w) {
+        pair[i][w].u = pair[i][w].v = 0;
+        if (lane + 32 * w < n_pairs) pair[i][w] = load_pairs(row + 2 * a.rot.start, a.rot, lane + 32 * w);
+      }
+    }
+    float inv[kRows];
+    if constexpr (kNorm) {
+#pragma unroll
+      for (int i = 0; i < kRows; ++i) {
+        float s = 0.f;
+#pragma unroll
+        for (int c = 0; c < kC; ++c) s += sum_squares(plain[i][c]);
+#pragma unroll
+        for (int w = 0; w < kW; ++w) s += sum_squares(make_uint4(pair[i][w].u, pair[i][w].v, 0, 0));
+        inv[i] = s;
+      }
+#pragma unroll
+      for (int i = 0; i < kRows; ++i) inv[i] = rsqrtf(warp_sum(inv[i]) / (float)a.D + a.eps);
+    }
+#pragma unroll
+    for (int c = 0; c < kC; ++c) {
+      if (lane + 32 * c >= n_plain) continue;
+      const int col = plain_column(a.rot, lane + 32 * c);
+      float wt[8];
+      if (kNorm && x.weight) weight8(x.weight, a.weight_bf16, col, wt);
+#pragma unroll
+      for (int i = 0; i < kRows; ++i) {
+        if (i >= rows) break;
+        uint4 o = plain[i][c];
+        if constexpr (kNorm) {
+          uint32_t v[4] = {o.x, o.y, o.z, o.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            float p = bf16_lo(v[e]) * inv[i], q = bf16_hi(v[e]) * inv[i];
+            if (x.weight) p *= wt[2 * e], q *= wt[2 * e + 1];
+            v[e] = pack_bf16x2(p, q);
+          }
+          o = make_uint4(v[0], v[1], v[2], v[3]);
+        }
+        *reinterpret_cast<uint4*>(dst + i * x.out_sh + 2 * col) = o;
+      }
+    }
+#pragma unroll
+    for (int w = 0; w < kW; ++w) {
+      if (lane + 32 * w >= n_pairs) continue;
+      const Angles an = angles(a.rot, pos, lane + 32 * w);
+      float wt[4];
+      if (kNorm && x.weight) weight_pairs(x.weight, a.weight_bf16, a.rot, lane + 32 * w, wt);
+#pragma unroll
+      for (int i = 0; i < kRows; ++i) {
+        if (i >= rows) break;
+        float v[4];
+        unpack(pair[i][w], v);
+        if constexpr (kNorm) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            v[e] *= inv[i];
+            if (x.weight) v[e] *= wt[e];
+          }
+        }
+        rotate(v, a.rot, an);
+        store_pairs(dst + i * x.out_sh + 2 * a.rot.start, a.rot, lane + 32 * w, v);
+      }
+    }
+  }
+}
+
+template <int kC, int kW, int kRows>
+cudaError_t launch_rope_as(const RopeArgs& a, bool norm, int sms, cudaStream_t stream) {
+  const int uq = (a.q.H + kRows - 1) / kRows, uk = (a.k.H + kRows - 1) / kRows;
+  const long long blocks = ((long long)a.T * (uq + uk) + kWarps - 1) / kWarps, cap = 16LL * sms;
+  const unsigned grid = (unsigned)(blocks < cap ? blocks : cap);
+  return launch_with_pdl(norm ? rope_kernel<kC, kW, kRows, true> : rope_kernel<kC, kW, kRows, false>, dim3(grid),
+                         dim3(32 * kWarps), 0, stream, 2LL * grid <= sms, a, uq, uk);
+}
+
+template <int kC, int kRows>
+cudaError_t launch_rope_width(const RopeArgs& a, bool norm, int sms, cudaStream_t stream) {
+  return a.rot.R <= 128 ? launch_rope_as<kC, 1, kRows>(a, norm, sms, stream)
+                        : launch_rope_as<kC, 2, kRows>(a, norm, sms, stream);
+}
+
+// ---- appends --------------------------------------------------------------------------------
+__device__ __forceinline__ int append_row(const AppendArgs& a, int t) {
+  const int x = __ldg(a.entries + t);
+  const int b = a.seq_of_token ? __ldg(a.seq_of_token + t) : 0;
+  if (x < 0 || b < 0 || b >= a.pool.B) return -1;
+  return latent_row(a.pool, b, x);
+}
+
+// Codes of two, four values over the scale: by its reciprocal where that is a normal number (the quotient is
+// then off by two units in its last place, next to which the values' own roundings are no smaller), else divided.
+struct Quotient {
+  float scale, r;
+  bool fast;
+  __device__ __forceinline__ float operator()(float x) const { return fast ? x * r : __fdiv_rn(x, scale); }
+};
+__device__ __forceinline__ Quotient quotient(float scale) {
+  return Quotient{scale, __frcp_rn(scale), kvq_fast_scale(scale)};
+}
+__device__ __forceinline__ uint32_t codes4(const Quotient& q, float a, float b, float c, float d) {
+  return kvq_e4m3x2(q(a), q(b)) | (kvq_e4m3x2(q(c), q(d)) << 16);
+}
+__device__ __forceinline__ float row_scale(float amax) { return amax > 0.f ? __fdiv_rn(amax, 448.f) : 1.f; }
+__device__ __forceinline__ float warp_max(float m) {   // of values >= 0 (their bits order as they do)
+  return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m)));
+}
+
+// A row's values in fp32: a lane's 16-byte chunks (two: rows of up to 512) and fours of rotated ones.
+template <int kW>
+struct Row {
+  float x[2][8], r[kW][4];
+};
+
+template <int kW>
+__device__ __forceinline__ void norm_row(Row<kW>& y, const AppendArgs& a, int width, int n_plain, int n_pairs,
+                                         bool rotary_too) {
+  const int lane = threadIdx.x & 31;
+  float s = 0.f;
+#pragma unroll
+  for (int c = 0; c < 2; ++c)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) s = fmaf(y.x[c][e], y.x[c][e], s);
+  if (rotary_too) {
+#pragma unroll
+    for (int w = 0; w < kW; ++w)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s = fmaf(y.r[w][e], y.r[w][e], s);
+  }
+  const float inv = rsqrtf(warp_sum(s) / (float)width + a.eps);
+#pragma unroll
+  for (int c = 0; c < 2; ++c) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) y.x[c][e] *= inv;
+    if (a.weight && lane + 32 * c < n_plain) {
+      float wt[8];
+      weight8(a.weight, a.weight_bf16, rotary_too ? plain_column(a.rot, lane + 32 * c) : 8 * (lane + 32 * c), wt);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) y.x[c][e] *= wt[e];
+    }
+  }
+  if (rotary_too) {
+#pragma unroll
+    for (int w = 0; w < kW; ++w) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) y.r[w][e] *= inv;
+      if (a.weight && lane + 32 * w < n_pairs) {
+        float wt[4];
+        weight_pairs(a.weight, a.weight_bf16, a.rot, lane + 32 * w, wt);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) y.r[w][e] *= wt[e];
+      }
+    }
+  }
+}
+
+template <int kW>
+__device__ __forceinline__ float row_amax(const Row<kW>& y) {
+  float m = 0.f;                                 // (a NaN does not enter it)
+#pragma unroll
+  for (int c = 0; c < 2; ++c)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(y.x[c][e]));
+#pragma unroll
+  for (int w = 0; w < kW; ++w)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) m = fmaxf(m, fabsf(y.r[w][e]));
+  return warp_max(m);
+}
+__device__ __forceinline__ void unpack8(const uint4& u, float (&x)[8]) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[2 * i] = bf16_lo(w[i]);
+    x[2 * i + 1] = bf16_hi(w[i]);
+  }
+}
+__device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
+  return make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
+                    pack_bf16x2(x[6], x[7]));
+}
+
+constexpr int kAppendBlocks = 8;                 // CTAs an SM
+
+// K rows (normalised, rotated) and V rows (as they are) of new tokens into their slots.  A warp a token.
+template <bool kFp8>
+__global__ void __launch_bounds__(32 * kWarps, kAppendBlocks) kv_append_kernel(const AppendArgs a) {
+  pdl_launch_dependents();
+  pdl_wait();
+  constexpr int kW = kRopeMaxPart / 128;
+  const int lane = threadIdx.x & 31, D = a.pool.L;
+  const int n_plain = (D - a.rot.R) >> 3, n_pairs = a.rot.R >> 2, n_all = D >> 3;
+  const long long step = (long long)gridDim.x * kWarps;
+  for (long long t = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5); t < a.T; t += step) {
+    const uint8_t *k = a.k + t * a.k_st, *v = a.v + t * a.v_st;
+    uint4 kx[2], vx[2];
+    Pairs kp[kW];
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      kx[c] = vx[c] = make_uint4(0, 0, 0, 0);
+      if (lane + 32 * c < n_plain)
+        kx[c] = __ldg(reinterpret_cast<const uint4*>(k + 2 * plain_column(a.rot, lane + 32 * c)));
+      if (lane + 32 * c < n_all) vx[c] = __ldg(reinterpret_cast<const uint4*>(v) + lane + 32 * c);
+    }
+#pragma unroll
+    for (int w = 0; w < kW; ++w) {
+      kp[w].u = kp[w].v = 0;
+      if (lane + 32 * w < n_pairs) kp[w] = load_pairs(k + 2 * a.rot.start, a.rot, lane + 32 * w);
+    }
+    const int pos = __ldg(a.positions + t), row = append_row(a, (int)t);
+    if (row < 0) {
+      if (lane == 0) flag_error(SPA_ERR_INDEX);
+      continue;
+    }
+    Row<kW> y;
+#pragma unroll
+    for (int c = 0; c < 2; ++c) unpack8(kx[c], y.x[c]);
+#pragma unroll
+    for (int w = 0; w < kW; ++w) unpack(kp[w], y.r[w]);
+    if (a.norm) norm_row(y, a, D, n_plain, n_pairs, true);
+#pragma unroll
+    for (int w = 0; w < kW; ++w)
+      if (lane + 32 * w < n_pairs) rotate(y.r[w], a.rot, angles(a.rot, pos, lane + 32 * w));
+    if constexpr (!kFp8) {
+      uint8_t* dst = a.pool.rows + (size_t)row * 4 * D;
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        if (lane + 32 * c < n_plain)
+          *reinterpret_cast<uint4*>(dst + 2 * plain_column(a.rot, lane + 32 * c)) = pack8(y.x[c]);
+        if (lane + 32 * c < n_all) reinterpret_cast<uint4*>(dst + 2 * D)[lane + 32 * c] = vx[c];
+      }
+#pragma unroll
+      for (int w = 0; w < kW; ++w)
+        if (lane + 32 * w < n_pairs) store_pairs(dst + 2 * a.rot.start, a.rot, lane + 32 * w, y.r[w]);
+    } else {
+      const Quotient q = quotient(row_scale(row_amax(y)));
+      uint32_t vm = 0;                           // (bf16's bits order as their magnitudes do)
+#pragma unroll
+      for (int c = 0; c < 2; ++c)
+        for (const uint32_t z : {vx[c].x, vx[c].y, vx[c].z, vx[c].w}) {
+          asm("max.bf16x2 %0, %0, %1;" : "+r"(vm) : "r"(z & 0x7fff7fffu));
+        }
+      vm = __reduce_max_sync(0xffffffffu, max(vm & 0xffffu, vm >> 16));
+      const float vs = row_scale(bf16_lo(vm)), vr = __frcp_rn(vs);
+      const bool vfast = kvq_fast_scale(vs);
+      uint8_t* dst = a.pool.rows + (size_t)row * 2 * D;
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const float* e = y.x[c];
+        if (lane + 32 * c < n_plain)
+          *reinterpret_cast<uint2*>(dst + plain_column(a.rot, lane + 32 * c)) =
+              make_uint2(codes4(q, e[0], e[1], e[2], e[3]), codes4(q, e[4], e[5], e[6], e[7]));
+        if (lane + 32 * c < n_all) reinterpret_cast<uint2*>(dst + D)[lane + 32 * c] = kvq_chunk(vx[c], vs, vr, vfast);
+      }
+#pragma unroll
+      for (int w = 0; w < kW; ++w) {
+        if (lane + 32 * w >= n_pairs) continue;
+        const uint32_t code = codes4(q, y.r[w][0], y.r[w][1], y.r[w][2], y.r[w][3]);
+        uint8_t* part = dst + a.rot.start;
+        if (a.rot.half) {
+          *reinterpret_cast<uint16_t*>(part + 2 * (lane + 32 * w)) = (uint16_t)code;
+          *reinterpret_cast<uint16_t*>(part + a.rot.R / 2 + 2 * (lane + 32 * w)) = (uint16_t)(code >> 16);
+        } else {
+          *reinterpret_cast<uint32_t*>(part + 4 * (lane + 32 * w)) = code;
+        }
+      }
+      if (lane == 0) {
+        a.k_scale[row] = q.scale;
+        a.v_scale[row] = vs;
+      }
+    }
+  }
+}
+
+// Latent rows [norm(c) | rotated r] of new tokens into their slots; e4m3: r as a high and a low code.
+template <bool kFp8>
+__global__ void __launch_bounds__(32 * kWarps, kAppendBlocks) latent_append_kernel(const AppendArgs a) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const int lane = threadIdx.x & 31, L = a.pool.L;
+  const int nl = L >> 3, n_pairs = a.rot.R >> 2;
+  const long long step = (long long)gridDim.x * kWarps;
+  for (long long t = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5); t < a.T; t += step) {
+    const uint8_t* k = a.k + t * a.k_st;
+    uint4 x[2];
+    Pairs p;
+    p.u = p.v = 0;
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+      x[c] = lane + 32 * c < nl ? __ldg(reinterpret_cast<const uint4*>(k) + lane + 32 * c) : make_uint4(0, 0, 0, 0);
+    if (lane < n_pairs) p = load_pairs(a.v + t * a.v_st, a.rot, lane);
+    const int pos = __ldg(a.positions + t), row = append_row(a, (int)t);
+    if (row < 0) {
+      if (lane == 0) flag_error(SPA_ERR_INDEX);
+      continue;
+    }
+    Row<1> y;
+#pragma unroll
+    for (int c = 0; c < 2; ++c) unpack8(x[c], y.x[c]);
+    unpack(p, y.r[0]);
+    if (a.norm) norm_row(y, a, L, nl, n_pairs, false);
+    if (lane < n_pairs) rotate(y.r[0], a.rot, angles(a.rot, pos, lane));
+    uint8_t* dst = a.pool.rows + (size_t)row * a.pool.row_bytes;
+    if constexpr (!kFp8) {
+#pragma unroll
+      for (int c = 0; c < 2; ++c)
+        if (lane + 32 * c < nl) reinterpret_cast<uint4*>(dst)[lane + 32 * c] = pack8(y.x[c]);
+      if (lane < n_pairs) store_pairs(dst + 2 * L, a.rot, lane, y.r[0]);
+    } else {
+      const Quotient q = quotient(row_scale(row_amax(y)));
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const float* e = y.x[c];
+        if (lane + 32 * c < nl)
+          reinterpret_cast<uint2*>(dst)[lane + 32 * c] =
+              make_uint2(codes4(q, e[0], e[1], e[2], e[3]), codes4(q, e[4], e[5], e[6], e[7]));
+      }
+      if (lane < n_pairs) {
+        uint32_t high[2], low[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const float c = q(y.r[0][2 * i]), d = q(y.r[0][2 * i + 1]);
+          high[i] = kvq_e4m3x2(c, d);
+          const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)high[i], __NV_E4M3);
+          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+          low[i] = kvq_e4m3x2(c - f.x, d - f.y);
+        }
+        uint8_t* part = dst + L;
+        const int R = a.rot.R;
+        if (a.rot.half) {
+          *reinterpret_cast<uint16_t*>(part + 2 * lane) = (uint16_t)high[0];
+          *reinterpret_cast<uint16_t*>(part + R / 2 + 2 * lane) = (uint16_t)high[1];
+          *reinterpret_cast<uint16_t*>(part + R + 2 * lane) = (uint16_t)low[0];
+          *reinterpret_cast<uint16_t*>(part + R + R / 2 + 2 * lane) = (uint16_t)low[1];
+        } else {
+          *reinterpret_cast<uint32_t*>(part + 4 * lane) = high[0] | (high[1] << 16);
+          *reinterpret_cast<uint32_t*>(part + R + 4 * lane) = low[0] | (low[1] << 16);
+        }
+      }
+      if (lane == 0) a.k_scale[row] = q.scale;
+    }
+  }
+}
+
+unsigned append_blocks(int T, int sms) {
+  const long long b = ((long long)T + kWarps - 1) / kWarps, cap = (long long)kAppendBlocks * sms;
+  return (unsigned)(b < cap ? b : cap);
+}
+
+}  // namespace
+
+cudaError_t launch_rope(const RopeArgs& a, bool norm, int sms, cudaStream_t stream) {
+  // In place and without a norm the values that are not rotated stay as they are.
+  const bool in_place = !norm && a.q.x == a.q.out && (a.k.H == 0 || a.k.x == a.k.out);
+  const int chunks = in_place ? 0 : (a.D - a.rot.R) / 8;
+  if (chunks == 0) return launch_rope_width<0, 8>(a, norm, sms, stream);
+  if (chunks <= 32) return launch_rope_width<1, 4>(a, norm, sms, stream);
+  if (chunks <= 64) return launch_rope_width<2, 4>(a, norm, sms, stream);
+  return launch_rope_width<4, 2>(a, norm, sms, stream);
+}
+
+cudaError_t launch_kv_append(const AppendArgs& a, bool fp8, int sms, cudaStream_t stream) {
+  const unsigned blocks = append_blocks(a.T, sms);
+  return launch_with_pdl(fp8 ? kv_append_kernel<true> : kv_append_kernel<false>, dim3(blocks), dim3(32 * kWarps), 0,
+                         stream, 2LL * blocks <= sms, a);
+}
+
+cudaError_t launch_latent_append(const AppendArgs& a, bool fp8, int sms, cudaStream_t stream) {
+  const unsigned blocks = append_blocks(a.T, sms);
+  return launch_with_pdl(fp8 ? latent_append_kernel<true> : latent_append_kernel<false>, dim3(blocks),
+                         dim3(32 * kWarps), 0, stream, 2LL * blocks <= sms, a);
+}
+
+// This translation unit's copy of the device error word (see spa_device.cuh).
+cudaError_t rotary_error_word(int** word) {
+  return cudaGetSymbolAddress(reinterpret_cast<void**>(word), g_spa_error);
+}
+
+}  // namespace spa
