@@ -32,6 +32,22 @@ __device__ __forceinline__ int latent_row(const LatentPoolDev& p, int b, int x) 
   return (int)((long long)blk * p.ps + (x - page * p.ps));   // (num_blocks * ps <= 2^30)
 }
 
+// The scale of an e4m3 row (-1: none), 0 if its codes are nothing but zeros (of either sign), where `scale` says
+// nothing.  Out of line: hardly ever called, and the kernels' code is long as it is.
+static __device__ __noinline__ float latent_scale_of(const uint8_t* rows, int width, int row, float scale) {
+  if (row < 0 || scale != 1.f) return scale;
+  const uint4* src = reinterpret_cast<const uint4*>(rows + (size_t)row * width);
+  uint32_t any = 0;
+  for (int i = 0; i < (width >> 4) && any == 0; i += 4) {
+#pragma unroll
+    for (int z = 0; z < 4; ++z) {
+      const uint4 u = i + z < (width >> 4) ? __ldg(src + i + z) : make_uint4(0, 0, 0, 0);
+      any |= (u.x | u.y | u.z | u.w) & 0x7f7f7f7fu;
+    }
+  }
+  return any ? scale : 0.f;
+}
+
 struct LatentCacheArgs {        // write and read
   LatentPoolDev pool;
   const uint8_t* latent;        // write: bf16 rows, strides in bytes

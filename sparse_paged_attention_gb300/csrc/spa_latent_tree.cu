@@ -4,118 +4,1290 @@
 //
 //   s_j = scale (q_c . c_j + q_r . r_j),   out = sum_j softmax(s)_j c_j
 //
-// One block a token and head, 64 entries at a time: scores by warps, then every thread its channels.
+// All heads of all drafted tokens of a sequence are rows of one matrix against the same cached rows: n H of
+// them, each 2 (2L + R) flops a cached row, so from 128 rows on the tensor cores are the bound.  A unit is 128 such
+// rows; a pair of CTAs takes it (64 rows each) with tcgen05 MMAs of both (cta_group::2, M = 128):
+//
+//   S[row][j]  = q_row . x_j      N = 128 entries, of which each CTA brings 64: whole rows of the cache
+//   O[row][d] += P[row][j] c_j[d] N = 256 channels a MMA, of which each CTA brings 128: of all 128 entries
+//
+// One CTA alone cannot hold O of 128 rows and L = 512 beside S (512 columns of TMEM), and with 64 rows its MMAs
+// run at half the rate or wait for their operands: measured, 77 cycles for M = 128, N = 64, K = 16 with both
+// operands in shared memory, where the pair's M = 128, N = 128 takes 32 (the full rate of both).  The price is that
+// a CTA reads its share of channels of all entries besides its entries' whole rows: 1.85 times the tile.
+//
+// TMEM of a CTA (rows 0-63 in lanes 0-63 and, their other half of the columns, in lanes 64-127): O 256
+// columns, two S of 64.  Shared memory: q, P, and a ring of 16 KB fills (two 128-byte chunks of 64 entries)
+// in the order in which the MMAs take them: K of tile k + 1 before V of tile k, so that S of the next tile runs
+// under the softmax of this one (at a unit's first tile V of the last comes first: q has to change).
+//
+//   warps 0-7    softmax: a thread has a row and 32 of a tile's entries; epilogue
+//   warp 8       (of the first CTA) issues all MMAs
+//   warp 9       schedule, page tables, copies of cached rows (TMA)
+//   warp 10      sees every fill land, cleans it where a tile holds what not all rows may see, and tells the MMAs
+//   warps 11-14  q of a unit; cached rows by cp.async where pages are not a multiple of eight entries
+//
+// Cleaning: a masked entry has a weight of zero, but zero times a NaN or infinity is none.  Rows that do not
+// exist are zeroed.  A drafted token's row that is not finite makes the score of whoever sees it NaN or
+// infinite; its values are taken as zero, so that those who do not see it are not touched.
+//
+// Schedule: the tiles of all units are one line, each unit with kUnitCost tiles' room for its q and its epilogue;
+// each pair takes an equal stretch.  Units cut by that leave normalised parts with their log-sum-exp, which
+// tree_merge_kernel joins in the order of the pairs.
+//
+// e4m3 rows enter as codes: q as two e4m3 terms times a power of two a row, the weights p_j scale_j as three e5m2
+// terms of an f16 number (see spa_latent_decode.cu).
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+
 #include "spa_errors.h"
 #include "spa_latent.h"
+#include "spa_latent_ring.h"
 #include "spa_launch.h"
 
 namespace spa {
 
 namespace {
 
-constexpr int kTile = 64;
-constexpr int kThreads = 256;
+constexpr int kRows = 64;            // rows of a CTA
+constexpr int kUnitRows = 128;       // of a pair
+constexpr int kGroup = 64;           // entries of a fill
+constexpr int kTile = 128;           // entries of a tile
+constexpr int kChunk = kGroup * 128;
+constexpr int kFill = 2 * kChunk;
+constexpr int kInfos = 4;            // tile infos in flight
+constexpr int kSoftmax = 256;
+constexpr int kThreads = kSoftmax + 7 * 32;
+constexpr int kTmemCols = 512;
+constexpr int kSCol = 256;           // O from column 0, two S of 64 columns
+constexpr int kUnitCost = 2;         // tiles' worth of a unit's q and epilogue
+constexpr int kMaxSlices = 128;
+
+constexpr float kPUnit = 1024.f;     // e4m3: unit of the weights (times 2^5 at most: an e5m2 number)
+
+enum { kFirst = 1, kLast = 2, kFinal = 4, kEnd = 8, kClean = 16 };
 
 template <bool kFp8>
-__device__ __forceinline__ float row_value(const LatentPoolDev& p, const uint8_t* row, float scale, int d) {
-  if (!kFp8) return bf16_lo(reinterpret_cast<const uint16_t*>(row)[d]);
-  const auto value = [](uint8_t c) {
-    __nv_fp8_e4m3 v;
-    v.__x = c;
-    return (float)v;
+struct Cfg {
+  static constexpr int kSlots = kFp8 ? 7 : 8;
+  static constexpr int kCw = kFp8 ? 128 : 64;        // channels of a chunk
+  static constexpr int kMaxChunks = kFp8 ? 5 : 9;    // of a row
+  static constexpr float kTau = kFp8 ? 5.f : 8.f;    // lazy rescale threshold (log2 units)
+  struct Info {
+    int flags, slot, first_row, rows;                // part slot (-1: none); global row of the unit, its rows
+    int tok0, unit_row, rel, seq;                    // sequence's first token, unit's first row in it, base - context
+    uint32_t valid[4];                               // bit i of word w: entry 32 w + i exists
+    float scale[kFp8 ? kTile : 1];                   // kPUnit times the rows' scales, and log2 of their sizes
+    float lscale[kFp8 ? kTile : 1];
   };
-  return (value(row[d]) + (d < p.L ? 0.f : value(row[d + p.R]))) * scale;
+  static constexpr int kQBytes = kFp8 ? kMaxChunks * 2 * kChunk : kMaxChunks * kChunk;
+  static constexpr int kPBytes = kFp8 ? 3 * kChunk : 2 * kChunk;
+  static constexpr int kQOff = 0;
+  static constexpr int kPOff = kQOff + kQBytes;
+  static constexpr int kRingOff = kPOff + kPBytes;
+  static constexpr int kRedOff = kRingOff + kSlots * kFill;        // float [2][4][64]
+  static constexpr int kQScaleOff = kRedOff + 2 * 4 * kRows * 4;   // e4m3: float [2][64]
+  static constexpr int kRowOff = kQScaleOff + (kFp8 ? 2 * kRows * 4 : 0);   // int [kInfos][128]
+  static constexpr int kInfoOff = kRowOff + kInfos * kTile * 4;
+  static constexpr int kBarOff = (kInfoOff + kInfos * (int)sizeof(Info) + 7) & ~7;
+  // Barriers at the same place in both CTAs.  Those marked L are used in the first CTA alone, whose MMA warp
+  // waits for both; those marked 2 are completed in both by the MMAs' commits.  Every wait by parity comes when
+  // that phase is the next to complete or the last that did: each role passes every phase of what it waits for.
+  static constexpr int bFull = 0, bReady = bFull + kSlots /* L */, bEmpty = bReady + kSlots /* 2 */,
+                       bSFull = bEmpty + kSlots /* 2 */, bSEmpty = bSFull + 2 /* L */,
+                       bPReady = bSEmpty + 2 /* L */, bPvDone = bPReady + 1 /* 2 */, bQFull = bPvDone + 1 /* L */,
+                       bQLocal = bQFull + 1, bQEmpty = bQLocal + 1 /* 2 */, bOFree = bQEmpty + 1 /* L */,
+                       bInfoFull = bOFree + 1, bInfoEmpty = bInfoFull + kInfos, bDrain = bInfoEmpty + kInfos,
+                       kNumB = bDrain + 1;
+  static constexpr int kMiscOff = kBarOff + kNumB * 8;             // TMEM base, abort flag
+  static constexpr int kSmem = kMiscOff + 16;
+  static_assert(kSmem <= 232448, "shared memory budget");
+};
+
+struct Part {                 // the unit cut at the end of a slice: its first row, rows, last slice (-1: none)
+  int row, rows, last, pad;
+};
+
+struct TreeParams {
+  CUtensorMap chunk;          // the pool's rows, boxes of 128 bytes by `box` rows
+  LatentTreeArgs a;
+  int box;                    // rows of a box: 8, 16, 32 or 64 (0: cp.async)
+  int slices;
+  float scale_log2;
+  Part* cut;                  // [slices]
+  float* lse;                 // [slices][2][128], log2 units
+  float* part;                // [slices][2][128][L]
+  uint8_t* q_codes;           // e4m3: [q slots][2 CTAs][chunks][64 rows of the high term, 64 of the low][128]
+  float* q_scale;             // e4m3: [q slots][128], 1 / kPUnit over the power of two in the codes
+};
+
+// The q slot of unit g of sequence b, whose first token is lo: no two units share one, and there are at most
+// T H / 128 + B of them.
+__host__ __device__ __forceinline__ long long q_slot(long long lo, int H, int b, int g) {
+  return lo * H / kUnitRows + b + g;
+}
+
+// MMAs of the pair, issued by one thread of its first CTA; operands and results at the same places in both.
+template <bool kFp8>
+__device__ __forceinline__ void mma_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  if constexpr (kFp8)
+    asm volatile(
+        "{ .reg .pred p; setp.ne.b32 p, %4, 0; "
+        "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p; }" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+  else
+    asm volatile(
+        "{ .reg .pred p; setp.ne.b32 p, %4, 0; "
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p; }" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+// Arrive on `bar` in both CTAs once every MMA of this thread so far has completed.
+__device__ __forceinline__ void commit_pair(uint32_t bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+      "h"((uint16_t)3)
+      : "memory");
+}
+__device__ __forceinline__ bool warp_wait_cluster(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
+  const bool ok = mbar_wait_cluster(bar, parity, abort_flag);
+  return __all_sync(0xffffffffu, ok);
+}
+
+// A sequence as the schedule sees it: its tokens and entries, units and tiles of a unit (no units: none to do).
+struct Seq {
+  int lo, n, ctx, tiles;
+  long long units;
+  bool bad;
+};
+// Sequences b0 + lane; `top`: the largest bound before them, and then after.
+__device__ __forceinline__ Seq load_seqs(const LatentTreeArgs& a, int b0, int& top) {
+  const int lane = threadIdx.x & 31, b = b0 + lane;
+  Seq s = {};
+  int hi = 0;
+  if (b < a.pool.B) {
+    s.lo = __ldg(a.cu_tokens + b);
+    hi = __ldg(a.cu_tokens + b + 1);
+    s.ctx = __ldg(a.context_lens + b);
+  }
+  int highest = b < a.pool.B ? s.lo : 0;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int x = __shfl_up_sync(0xffffffffu, highest, o);
+    if (lane >= o) highest = max(highest, x);
+  }
+  highest = max(highest, top);
+  top = __shfl_sync(0xffffffffu, highest, 31);
+  if (b >= a.pool.B) return s;
+  long long cap = (long long)a.pool.bt_stride * a.pool.ps;
+  cap = cap < 0x7fffff00LL ? cap : 0x7fffff00LL;    // (a tile's entries stay below 2^31)
+  s.bad = s.lo < highest || hi < s.lo || hi > a.T || s.ctx < 0 || (long long)s.ctx + hi - s.lo > cap;
+  if (s.bad || hi == s.lo) return s;
+  s.n = hi - s.lo;
+  s.tiles = (s.ctx + s.n + kTile - 1) / kTile;
+  s.units = ((long long)s.n * a.H + kUnitRows - 1) / kUnitRows;
+  return s;
+}
+
+// e4m3: q as two e4m3 terms times a power of two a row, in the order of the MMA's operand.  A warp takes a row; the
+// last R columns repeat the rotary part, against the low codes of the rows.  (Rows of a unit's last that
+// belong to no token keep what they hold: their results are not stored.)
+__global__ void __launch_bounds__(256) tree_q_kernel(const __grid_constant__ LatentTreeArgs a, uint8_t* __restrict__ codes,
+                                                     float* __restrict__ scales) {
+  pdl_launch_dependents();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int nlp = a.pool.L >> 3, nrp = a.pool.R >> 3, n_chunks = (a.pool.row_bytes + 127) >> 7;
+  int top = 0;
+  for (int b0 = 0; b0 < a.pool.B; b0 += 32) {
+    const Seq all = load_seqs(a, b0, top);
+    for (int k = 0; k < 32 && b0 + k < a.pool.B; ++k) {
+      const int lo = __shfl_sync(0xffffffffu, all.lo, k), n = __shfl_sync(0xffffffffu, all.n, k);
+      const long long rows = (long long)n * a.H;
+      for (long long r = (long long)blockIdx.x * 8 + warp; r < rows; r += (long long)gridDim.x * 8) {
+        const long long t = lo + r / a.H, h = r % a.H;
+        const uint4* ql = reinterpret_cast<const uint4*>(a.q_latent + t * a.ql_st + h * a.ql_sh);
+        const uint4* qr = reinterpret_cast<const uint4*>(a.q_rope + t * a.qr_st + h * a.qr_sh);
+        uint4 x[3];                              // pieces of eight values
+        uint32_t mb = 0;                         // largest magnitude (NaN if there is one)
+#pragma unroll
+        for (int i = 0; i < 3; ++i) {
+          const int o = lane + 32 * i, z = o - nlp;
+          x[i] = make_uint4(0, 0, 0, 0);
+          if (z < 2 * nrp) x[i] = z < 0 ? __ldg(ql + o) : __ldg(qr + (z < nrp ? z : z - nrp));
+          const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) mb = max(mb, max(w[e] & 0x7fffu, (w[e] >> 16) & 0x7fffu));
+        }
+        mb = __reduce_max_sync(0xffffffffu, mb);
+        const float m = bf16_lo(mb);
+        const bool finite = mb < 0x7f80u;        // (else the row's scores become NaN through its scale)
+        const float qs = finite && m > 0.f ? pow2_floor(448.f / m) : 1.f;
+        const long long slot = q_slot(lo, a.H, b0 + k, 0) + r / kUnitRows;
+        const int ur = (int)(r % kUnitRows), half = ur / kRows, hr = ur % kRows;
+        if (lane == 0) scales[slot * kUnitRows + ur] = finite ? (1.f / kPUnit) / qs : __int_as_float(0x7fffffff);
+        uint8_t* dst = codes + (slot * 2 + half) * ((long long)n_chunks * 2 * kChunk) + hr * 128;
+#pragma unroll
+        for (int i = 0; i < 3; ++i) {
+          const int o = lane + 32 * i;           // piece o: chunk o / 16, 16-byte unit (o / 2) & 7 of the row
+          if (o >= 16 * n_chunks) continue;
+          const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+          uint32_t high[4], low[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float y = bf16_lo(w[e]) * qs, z = bf16_hi(w[e]) * qs;
+            high[e] = e4m3x2(y, z);
+            const __half2_raw hh = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)high[e], __NV_E4M3);
+            const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&hh));
+            low[e] = e4m3x2(y - v.x, z - v.y);
+          }
+          uint8_t* d = dst + (o >> 4) * (2 * kChunk) + ((((o >> 1) & 7) ^ (hr & 7)) << 4) + (o & 1) * 8;
+          *reinterpret_cast<uint2*>(d) = make_uint2(high[0] | (high[1] << 16), high[2] | (high[3] << 16));
+          *reinterpret_cast<uint2*>(d + kChunk) = make_uint2(low[0] | (low[1] << 16), low[2] | (low[3] << 16));
+        }
+      }
+    }
+  }
+}
+
+// A 16-byte piece of cached values with zeros for what is not finite.
+template <bool kFp8>
+__device__ __forceinline__ uint4 finite_only(uint4 u) {
+  uint32_t* w = reinterpret_cast<uint32_t*>(&u);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (kFp8) {
+#pragma unroll
+      for (int b = 0; b < 32; b += 8)
+        if (((w[i] >> b) & 0x7fu) == 0x7fu) w[i] &= ~(0xffu << b);
+    } else {
+      if ((w[i] & 0x7f80u) == 0x7f80u) w[i] &= 0xffff0000u;
+      if ((w[i] & 0x7f800000u) == 0x7f800000u) w[i] &= 0xffffu;
+    }
+  }
+  return u;
 }
 
 template <bool kFp8>
-__global__ void __launch_bounds__(kThreads) latent_tree_kernel(const LatentTreeArgs a) {
-  __shared__ float q[kLatMaxDim + kLatMaxRope], s[kTile];
-  __shared__ int rows[kTile], seq;
-  const int t = blockIdx.x / a.H, h = blockIdx.x % a.H, L = a.pool.L, R = a.pool.R;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    latent_tree_kernel(const __grid_constant__ TreeParams p) {
+  using C = Cfg<kFp8>;
+  extern __shared__ __align__(1024) uint8_t sm[];
+  const uint32_t sb = smem_u32(sm);
+  const int warp = (int)warp_uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
+  const int rank = (int)cluster_ctarank();
+  const int slice = blockIdx.x >> 1;
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + C::kMiscOff + 4);
+  typename C::Info* infos = reinterpret_cast<typename C::Info*>(sm + C::kInfoOff);
+#define BAR(i) (sb + (uint32_t)C::kBarOff + 8u * (uint32_t)(i))
+  const auto lead_bar = [&](int i) { return mapa_cluster(BAR(i), 0); };   // in the first CTA
+
   if (threadIdx.x == 0) {
-    seq = -1;
-    int top = 0;
-    for (int b = 0; b < a.pool.B; ++b) {
-      const int lo = a.cu_tokens[b], hi = a.cu_tokens[b + 1];
-      const bool bad = lo < top || hi < lo || hi > a.T || a.context_lens[b] < 0 ||
-                       (long long)a.context_lens[b] + (hi - lo) > (long long)a.pool.bt_stride * a.pool.ps;
-      top = max(top, lo);
-      if (bad && blockIdx.x == 0) flag_error(SPA_ERR_INDEX);
-      if (!bad && t >= lo && t < hi) seq = b;
+    for (int i = 0; i < C::kSlots; ++i) {
+      mbar_init(BAR(C::bFull + i), p.box ? 1 : 128);
+      mbar_init(BAR(C::bReady + i), 2);
+      mbar_init(BAR(C::bEmpty + i), 1);
     }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(BAR(C::bSFull + i), 1);
+      mbar_init(BAR(C::bSEmpty + i), 16);
+    }
+    mbar_init(BAR(C::bPReady), 16);
+    mbar_init(BAR(C::bPvDone), 1);
+    mbar_init(BAR(C::bQFull), kFp8 ? 2 : 8);
+    mbar_init(BAR(C::bQLocal), 1);
+    mbar_init(BAR(C::bQEmpty), 1);
+    mbar_init(BAR(C::bOFree), 16);
+    for (int i = 0; i < kInfos; ++i) {
+      mbar_init(BAR(C::bInfoFull + i), 1);
+      mbar_init(BAR(C::bInfoEmpty + i), rank == 0 ? 14 : 13);   // softmax, cleaning and q warps, MMA warp
+    }
+    mbar_init(BAR(C::bDrain), 1);
+    *abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  for (int d = threadIdx.x; d < L + R; d += kThreads)
-    q[d] = bf16_lo(d < L ? reinterpret_cast<const uint16_t*>(a.q_latent + t * a.ql_st + h * a.ql_sh)[d]
-                         : reinterpret_cast<const uint16_t*>(a.q_rope + t * a.qr_st + h * a.qr_sh)[d - L]);
+  if (warp == 8) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(sb + C::kMiscOff),
+                 "r"(kTmemCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
   __syncthreads();
-  const int b = seq;
-  if (b < 0) return;
-  const int ctx = a.context_lens[b], first = a.cu_tokens[b], len = ctx + a.cu_tokens[b + 1] - first;
-  float m = -INFINITY, l = 0.f, o[2] = {0.f, 0.f};
-  for (int j0 = 0; j0 < len; j0 += kTile) {
-    if (threadIdx.x < kTile) {
-      const int j = j0 + threadIdx.x, i = j - ctx;
-      bool seen = j < len;
-      if (seen && i >= 0)
-        seen = a.mask ? i < 32 * a.mask_words && (a.mask[(size_t)t * a.mask_words + (i >> 5)] >> (i & 31) & 1u)
-                      : i <= t - first;
-      int row = -1;
-      if (j < len && (row = latent_row(a.pool, b, j)) < 0) flag_error(SPA_ERR_INDEX);
-      rows[threadIdx.x] = seen ? row : -1;
-    }
-    __syncthreads();
-    for (int i = warp; i < kTile; i += kThreads / 32) {
-      const int row = rows[i];
-      float x = 0.f;
-      if (row >= 0) {
-        const uint8_t* src = a.pool.rows + (size_t)row * a.pool.row_bytes;
-        const float sc = kFp8 ? a.pool.scale[row] : 1.f;
-        for (int d = lane; d < L + R; d += 32) x = fmaf(q[d], row_value<kFp8>(a.pool, src, sc, d), x);
-      }
-#pragma unroll
-      for (int e = 16; e > 0; e >>= 1) x += __shfl_xor_sync(0xffffffffu, x, e);
-      if (lane == 0) s[i] = row >= 0 ? x * a.scale : -INFINITY;
-    }
-    __syncthreads();
-    float mt = m;
-    for (int i = 0; i < kTile; ++i) mt = fmaxf(mt, s[i]);
-    const float ref = mt == -INFINITY ? 0.f : mt, f = __expf(m - ref);
-    l *= f;
-    o[0] *= f;
-    o[1] *= f;
-    m = mt;
-    for (int i = 0; i < kTile; ++i) {
-      const int row = rows[i];
-      if (row < 0) continue;
-      const float p = __expf(s[i] - ref);
-      l += p;
-      const uint8_t* src = a.pool.rows + (size_t)row * a.pool.row_bytes;
-      const float sc = kFp8 ? a.pool.scale[row] : 1.f;
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int d = threadIdx.x + e * kThreads;
-        if (d < L) o[e] = fmaf(p, row_value<kFp8>(a.pool, src, sc, d), o[e]);
+  cluster_arrive();
+  cluster_wait();
+  tc_fence_after();
+  const uint32_t tmem = warp_uniform(*reinterpret_cast<volatile uint32_t*>(sm + C::kMiscOff));
+  pdl_launch_dependents();
+  pdl_wait();   // nothing global before the grid before this one is done
+
+  const LatentTreeArgs& a = p.a;
+  const int L = a.pool.L, W = a.pool.row_bytes;
+  const int n_chunks = (W + 127) >> 7;                         // of a row
+  const int n_half = ((L + C::kCw - 1) / C::kCw + 1) >> 1;     // chunks of values a CTA brings
+  const int k_fills = (n_chunks + 1) >> 1, v_pairs = (n_half + 1) >> 1;
+
+  // The fills in order, for the roles that follow them: K of tile k, V of tile k - 1 (before it, where tile k
+  // is the first of a unit).  `k_part(k)` and `v_part(k)` return false to give up.
+  if (warp == 9) {
+    // ================================ schedule and loads ==================================
+    int top = 0, s0 = 0;
+    Seq cur = load_seqs(a, 0, top);
+    if (slice == 0 && rank == 0 && cur.bad) flag_error(SPA_ERR_INDEX);
+    long long tiles = cur.units * cur.tiles, units = cur.units;
+    {
+      int t = top;
+      for (int b0 = 32; b0 < a.pool.B; b0 += 32) {
+        const Seq s = load_seqs(a, b0, t);
+        if (slice == 0 && rank == 0 && s.bad) flag_error(SPA_ERR_INDEX);
+        tiles += s.units * s.tiles;
+        units += s.units;
       }
     }
-    __syncthreads();
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      tiles += __shfl_xor_sync(0xffffffffu, tiles, o);
+      units += __shfl_xor_sync(0xffffffffu, units, o);
+    }
+    // The line: a unit that begins at w has its tile 0 there, and tile j > 0 at w + cost + j.  A slice takes the
+    // tiles from per * slice to before per * (slice + 1).  (cost < per, so that a unit has tiles in every slice
+    // from its first to its last.)
+    const long long each = (tiles + p.slices - 1) / p.slices;
+    const long long cost = min((long long)(units > 1 ? kUnitCost : 0), max(each, 1LL) - 1);
+    const long long per = max((tiles + cost * units + p.slices - 1) / p.slices, 1LL);
+    const long long begin = per * slice, end = begin + per;
+    int it_s = 0;                                // next tile: sequence (in the chunk), unit, tile of the unit
+    long long it_u = 0, w_unit = 0, left_all = 0;
+    int it_j = 0;
+    {
+      bool found = false;
+      int chunk = 0, chunk_top = 0, t = 0;
+      long long w0 = 0;
+      for (int b0 = 0; b0 < a.pool.B; b0 += 32) {
+        const int t_before = t;
+        const Seq s = load_seqs(a, b0, t);
+        const long long span = s.tiles + cost, mine = s.units * span;
+        long long sum = mine;                    // inclusive scan
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const long long x = __shfl_up_sync(0xffffffffu, sum, o);
+          if (lane >= o) sum += x;
+        }
+        const long long w = w0 + sum - mine;
+        const auto before = [&](long long x) {   // tiles of this lane's sequence before x
+          if (x <= w || s.units == 0) return 0LL;
+          const long long u = min((x - w) / span, s.units);
+          const long long y = x - w - u * span;
+          return u * s.tiles + (u < s.units && y > 0 ? min((long long)s.tiles, max(1LL, y - cost)) : 0);
+        };
+        const long long lo = before(begin), hi = before(end);
+        left_all += hi - lo;
+        const unsigned m = __ballot_sync(0xffffffffu, lo < s.units * s.tiles);
+        if (!found && m) {
+          const int k = __ffs(m) - 1;
+          found = true;
+          chunk = b0;
+          chunk_top = t_before;
+          it_s = k;
+          const long long l = __shfl_sync(0xffffffffu, lo, k), wk = __shfl_sync(0xffffffffu, w, k);
+          const int tl = __shfl_sync(0xffffffffu, s.tiles, k);
+          it_u = l / tl;
+          it_j = (int)(l % tl);
+          w_unit = wk + it_u * (tl + cost);
+        }
+        w0 += __shfl_sync(0xffffffffu, sum, 31);
+        if (w0 >= end) break;
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) left_all += __shfl_xor_sync(0xffffffffu, left_all, o);
+      if (chunk != 0) {
+        s0 = chunk;
+        top = chunk_top;
+        cur = load_seqs(a, s0, top);
+      }
+    }
+    // The current unit
+    int u_lo = 0, u_n = 0, u_ctx = 0, u_tiles = 0, u_seq = 0, u_len = 0;
+    long long u_units = 0;
+    bool started = false, fresh = true;
+    int left = 0;
+    Part cut = {0, 0, -1, 0};
+    const auto begin_unit = [&]() {
+      while (it_u >= __shfl_sync(0xffffffffu, cur.units, it_s)) {   // (there is a unit to come)
+        it_u = 0;
+        if (++it_s == 32) {
+          it_s = 0;
+          s0 += 32;
+          cur = load_seqs(a, s0, top);
+        }
+      }
+      u_lo = __shfl_sync(0xffffffffu, cur.lo, it_s);
+      u_n = __shfl_sync(0xffffffffu, cur.n, it_s);
+      u_ctx = __shfl_sync(0xffffffffu, cur.ctx, it_s);
+      u_tiles = __shfl_sync(0xffffffffu, cur.tiles, it_s);
+      u_units = __shfl_sync(0xffffffffu, cur.units, it_s);
+      u_seq = s0 + it_s;
+      u_len = u_ctx + u_n;
+      started = it_j == 0;
+      left = u_tiles - it_j;
+      fresh = true;
+      if (started && left > left_all) {          // (the line ends inside it)
+        const long long unit_row = it_u * kUnitRows;
+        cut.row = (int)((long long)u_lo * a.H + unit_row);
+        cut.rows = (int)min((long long)kUnitRows, (long long)u_n * a.H - unit_row);
+        cut.last = (int)((w_unit + cost + u_tiles - 1) / per);
+      }
+    };
+    struct Tile {
+      int flags, slot, base, first_row, rows, tok0, unit_row, rel, valid_len;
+      int blk[4];                                // boxed: of box `lane`; else of entries lane + 32 e
+    };
+    const int boxes = p.box ? kTile / p.box : 0;
+    if (left_all > 0) begin_unit();
+    const auto next_tile = [&](Tile& x) {        // the next tile, its block-table reads under way
+      x.flags = kEnd;
+      if (left_all == 0) return;
+      if (left == 0) {
+        w_unit += cost + u_tiles;
+        ++it_u;
+        it_j = 0;
+        begin_unit();
+      }
+      const bool last = left == 1 || left_all == 1;
+      x.base = it_j * kTile;
+      x.slot = started && left == 1 ? -1 : (started ? 1 : 0);
+      x.unit_row = (int)(it_u * kUnitRows);
+      x.first_row = (int)((long long)u_lo * a.H + it_u * kUnitRows);
+      x.rows = (int)min((long long)kUnitRows, (long long)u_n * a.H - it_u * kUnitRows);
+      x.tok0 = u_lo;
+      x.rel = x.base - u_ctx;
+      x.valid_len = u_len - x.base;
+      x.flags = (fresh ? kFirst : 0) | (last ? kLast : 0) | (left_all == 1 ? kFinal : 0);
+      // (the q slot of the unit goes with the sequence; see the published info)
+      x.blk[0] = x.blk[1] = x.blk[2] = x.blk[3] = -2;
+      const int32_t* bt = a.pool.bt + (size_t)u_seq * a.pool.bt_stride;
+      if (p.box) {
+        const int key = lane * p.box;
+        if (lane < boxes && key < x.valid_len) x.blk[0] = __ldg(bt + (x.base + key) / a.pool.ps);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int key = lane + 32 * e;
+          if (key < x.valid_len) x.blk[e] = __ldg(bt + (x.base + key) / a.pool.ps);
+        }
+      }
+      fresh = false;
+      --left_all;
+      --left;
+      ++it_j;
+    };
+    const int total_rows = (int)(a.pool.num_blocks * a.pool.ps);
+    Ring<C::kSlots> at;
+    long long fills = 0;
+    bool ok = true;
+    // a fill: chunks c0, c0 + 1 (below c_end) of entry group `grp` of the tile whose boxes begin at `rows`
+    const auto fill = [&](int rows, int grp, int c0, int c_end) -> bool {
+      if (!warp_wait(BAR(C::bEmpty + at.slot), at.parity ^ 1, abort_flag)) return false;
+      const uint32_t dst = sb + C::kRingOff + at.slot * kFill, full = BAR(C::bFull + at.slot);
+      const int n = min(2, c_end - c0), per_group = kGroup / p.box;
+      if (lane == 0) mbar_arrive_expect_tx(full, (uint32_t)(n * kChunk));
+      __syncwarp();
+      const int c = lane / per_group, bx = lane % per_group;
+      const int row = __shfl_sync(0xffffffffu, rows, (grp * per_group + bx) & 31);
+      if (c < n) tma_row(dst + c * kChunk + bx * p.box * 128, &p.chunk, (c0 + c) * 128, row, full);
+      __syncwarp();
+      ++fills;
+      at.next();
+      return true;
+    };
+    const auto k_part = [&](int rows) {
+      for (int f = 0; f < k_fills && ok; ++f) ok = fill(rows, rank, 2 * f, n_chunks);
+    };
+    const auto v_part = [&](int rows) {
+      for (int grp = 0; grp < 2; ++grp)
+        for (int f = 0; f < v_pairs && ok; ++f)
+          ok = fill(rows, grp, rank * n_half + 2 * f, rank * n_half + n_half);
+    };
+    Tile nxt = {}, x = {};
+    int box_rows = 0, prev_rows = 0;
+    next_tile(nxt);
+    for (int k = 0; ok; ++k) {
+      x = nxt;
+      const int seq = u_seq;
+      // rows of the tile
+      int rows4[4];
+      uint32_t valid[4];
+      bool clean = false;
+      if (!(x.flags & kEnd)) {
+        if (p.box) {
+          const bool good = x.blk[0] >= 0 && (long long)x.blk[0] < a.pool.num_blocks;
+          if (x.blk[0] != -2 && !good) flag_error(SPA_ERR_INDEX);
+          const int key = x.base + lane * p.box;
+          // a box without entries starts past the last row and is filled with zeros
+          box_rows = good ? x.blk[0] * a.pool.ps + key % a.pool.ps : total_rows;
+          const unsigned okb = __ballot_sync(0xffffffffu, good);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int i = lane + 32 * e, bx = i / p.box;
+            const bool v = ((okb >> bx) & 1u) && i < x.valid_len;
+            rows4[e] = __shfl_sync(0xffffffffu, box_rows, bx) + (i - bx * p.box);
+            if (!v) rows4[e] = -1;
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int i = lane + 32 * e;
+            const bool good = x.blk[e] >= 0 && (long long)x.blk[e] < a.pool.num_blocks;
+            if (x.blk[e] != -2 && !good) flag_error(SPA_ERR_INDEX);
+            rows4[e] = good ? x.blk[e] * a.pool.ps + (x.base + i) % a.pool.ps : -1;
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          valid[e] = __ballot_sync(0xffffffffu, rows4[e] >= 0);
+          clean |= valid[e] != 0xffffffffu;
+        }
+        clean |= x.rel + kTile > 0;              // drafted tokens' entries among them
+      }
+      float sc[4] = {0.f, 0.f, 0.f, 0.f};
+      if (kFp8 && !(x.flags & kEnd)) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (rows4[e] >= 0) sc[e] = __ldg(a.pool.scale + rows4[e]);
+      }
+      if (!(x.flags & kEnd)) next_tile(nxt);
+      // publish the tile (before its copies: the MMAs go by its flags)
+      const int ri = k % kInfos;
+      ok = warp_wait(BAR(C::bInfoEmpty + ri), ((k / kInfos) & 1) ^ 1, abort_flag);
+      if (!ok) break;
+      typename C::Info& info = infos[ri];
+      if (x.flags & kEnd) {                      // (nothing to do at all: k is 0)
+        if (lane == 0) {
+          info.flags = kEnd;
+          __threadfence_block();
+          mbar_arrive(BAR(C::bInfoFull + ri));
+        }
+        break;
+      }
+      if (!p.box) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          reinterpret_cast<int*>(sm + C::kRowOff)[ri * kTile + lane + 32 * e] = rows4[e];
+      }
+      if constexpr (kFp8) {
+        bool one = false;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) one |= sc[e] == 1.f;
+        if (__any_sync(0xffffffffu, one)) {
+#pragma unroll 1
+          for (int e = 0; e < 4; ++e) {
+            const float s = latent_scale_of(a.pool.rows, W, e == 0 ? rows4[0] : e == 1 ? rows4[1] : e == 2 ? rows4[2] : rows4[3],
+                                            e == 0 ? sc[0] : e == 1 ? sc[1] : e == 2 ? sc[2] : sc[3]);
+            if (e == 0) sc[0] = s;
+            else if (e == 1) sc[1] = s;
+            else if (e == 2) sc[2] = s;
+            else sc[3] = s;
+          }
+        }
+        // the maximum of a tile is taken over p_j |scale_j|, the weights that enter the value product (a scale
+        // below 2^-60 counts as that: the sums of p_j alone must stay finite)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          info.scale[lane + 32 * e] = kPUnit * sc[e];
+          info.lscale[lane + 32 * e] = rows4[e] >= 0 ? fmaxf(__log2f(fabsf(sc[e])), -60.f) : -INFINITY;
+        }
+      }
+      if (lane == 0) {
+        info.flags = x.flags | (clean ? kClean : 0);
+        info.slot = x.slot;
+        info.first_row = x.first_row;
+        info.rows = x.rows;
+        info.tok0 = x.tok0;
+        info.unit_row = x.unit_row;
+        info.rel = x.rel;
+        info.seq = seq;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) info.valid[e] = valid[e];
+      }
+      __threadfence_block();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(BAR(C::bInfoFull + ri));
+      if (p.box) {
+        const bool first = x.flags & kFirst;
+        if (first && k > 0) v_part(prev_rows);
+        k_part(box_rows);
+        if (!first) v_part(prev_rows);
+        prev_rows = box_rows;
+        if (x.flags & kFinal) v_part(box_rows);
+      }
+      if (x.flags & kFinal) break;
+    }
+    if (lane == 0) {
+      if (rank == 0) p.cut[slice] = cut;
+      // copies in flight must land before the CTA ends (at once after a normal run)
+      for (long long f = max(0LL, fills - C::kSlots); f < fills; ++f)
+        mbar_wait_drain(BAR(C::bFull + (int)(f % C::kSlots)), (uint32_t)((f / C::kSlots) & 1));
+    }
+    __syncwarp();
+  } else if (warp == 8) {
+    // ================================= MMAs ==============================================
+    if (rank == 0) {
+      const uint32_t idS = kFp8 ? idesc_e4m3(128, 128, 0, 0) : idesc_bf16(128, 128, 0, 0);
+      // (A of the value product: P in bf16, or in e5m2)
+      const auto idO = [&](int n) { return kFp8 ? idesc_e4m3(128, n, 0, 1) | (1u << 7) : idesc_bf16(128, n, 0, 1); };
+      const uint64_t dq = sdesc(sb + C::kQOff, 16, 1024), dp = sdesc(sb + C::kPOff, 16, 1024);
+      const uint64_t dk0 = sdesc(sb + C::kRingOff, 16, 1024), dv0 = sdesc(sb + C::kRingOff, kChunk, 1024);
+      const bool lead = elect_one();
+      Ring<C::kSlots> at;
+      uint32_t units = 0;                        // begun
+      bool o_first = true;                       // of the tile whose PV comes next
+      bool ok = true;
+      const auto pv = [&](int k) {               // O of tile k
+        ok = ok && warp_wait_cluster(BAR(C::bPReady), (uint32_t)(k & 1), abort_flag);
+        if (ok && o_first && units > 1) ok = warp_wait_cluster(BAR(C::bOFree), (units - 2) & 1, abort_flag);
+        for (int grp = 0; grp < 2 && ok; ++grp) {
+          for (int f = 0; f < v_pairs; ++f) {
+            ok = warp_wait_cluster(BAR(C::bReady + at.slot), at.parity, abort_flag);
+            if (!ok) break;
+            tc_fence_after();
+            if (lead) {
+              const int n = min(2, n_half - 2 * f);       // chunks of the fill
+              const uint64_t dv = desc_add(dv0, at.slot * kFill);
+              if (kFp8) {
+                for (int c = 0; c < n; ++c) {             // 128 channels of each CTA
+                  const uint32_t d = tmem + (2 * f + c) * 128;
+#pragma unroll
+                  for (int kk = 0; kk < 2; ++kk) {        // 32 entries a step
+                    const uint64_t b = desc_add(dv, c * kChunk + kk * 4096), pa = desc_add(dp, grp * 64 + kk * 32);
+                    mma_pair<kFp8>(d, pa, b, idO(256), !(o_first && grp == 0 && kk == 0));
+                    mma_pair<kFp8>(d, desc_add(pa, kChunk), b, idO(256), 1u);
+                    mma_pair<kFp8>(d, desc_add(pa, 2 * kChunk), b, idO(256), 1u);
+                  }
+                }
+              } else {
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)            // 16 entries a step
+                  mma_pair<kFp8>(tmem + f * 128, desc_add(dp, grp * kChunk + kk * 32), desc_add(dv, kk * 2048),
+                                 idO(n * 128), !(o_first && grp == 0 && kk == 0));
+              }
+              commit_pair(BAR(C::bEmpty + at.slot));
+            }
+            __syncwarp();
+            at.next();
+          }
+        }
+        if (ok && lead) commit_pair(BAR(C::bPvDone));
+        __syncwarp();
+      };
+      for (int k = 0; ok; ++k) {
+        const int ri = k % kInfos;
+        if (!warp_wait(BAR(C::bInfoFull + ri), (uint32_t)((k / kInfos) & 1), abort_flag)) break;
+        const int flags = (int)warp_uniform(*reinterpret_cast<volatile int*>(&infos[ri].flags));
+        __syncwarp();
+        if (lane == 0) mbar_arrive(BAR(C::bInfoEmpty + ri));
+        if (flags & kEnd) break;
+        const bool first = flags & kFirst;
+        if (first) {
+          if (k > 0) pv(k - 1);
+          if (!ok) break;
+          ++units;
+          ok = warp_wait_cluster(BAR(C::bQFull), (units - 1) & 1, abort_flag);
+        }
+        // S of tile k
+        const int sn = k & 1;
+        if (ok && k >= 2) ok = warp_wait_cluster(BAR(C::bSEmpty + sn), (uint32_t)(((k >> 1) & 1) ^ 1), abort_flag);
+        for (int f = 0; f < k_fills && ok; ++f) {
+          ok = warp_wait_cluster(BAR(C::bReady + at.slot), at.parity, abort_flag);
+          if (!ok) break;
+          tc_fence_after();
+          if (lead) {
+            const uint32_t dS = tmem + kSCol + sn * 64;
+            const int n = min(2, n_chunks - 2 * f);
+            for (int c = 0; c < n; ++c) {
+              const int ch = 2 * f + c, steps = min(4, (W - ch * 128 + 31) >> 5);
+              const uint64_t b = desc_add(dk0, at.slot * kFill + c * kChunk);
+              const uint64_t q = desc_add(dq, ch * (kFp8 ? 2 : 1) * kChunk);
+              for (int st = 0; st < steps; ++st) {
+                mma_pair<kFp8>(dS, desc_add(q, st * 32), desc_add(b, st * 32), idS, (ch | st) != 0);
+                if (kFp8) mma_pair<kFp8>(dS, desc_add(q, kChunk + st * 32), desc_add(b, st * 32), idS, 1u);
+              }
+            }
+            commit_pair(BAR(C::bEmpty + at.slot));
+          }
+          __syncwarp();
+          at.next();
+        }
+        if (!ok) break;
+        if (lead) {
+          commit_pair(BAR(C::bSFull + sn));
+          if (flags & kLast) commit_pair(BAR(C::bQEmpty));
+        }
+        __syncwarp();
+        if (!first) pv(k - 1);
+        o_first = first;
+        if (flags & kFinal) {
+          pv(k);
+          break;
+        }
+      }
+      // nothing may still write TMEM when it is released
+      if (lead) {
+        asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(BAR(C::bDrain))
+                     : "memory");
+        mbar_wait_drain(BAR(C::bDrain), 0);
+      }
+      __syncwarp();
+    }
+  } else if (warp == 10) {
+    // ===================== every fill as it lands: cleaned, handed on =====================
+    Ring<C::kSlots> at;
+    bool ok = true;
+    const auto hand_on = [&](bool clean, const typename C::Info& info, int grp, int n) {
+      ok = warp_wait(BAR(C::bFull + at.slot), at.parity, abort_flag);
+      if (!ok) return;
+      if (clean) {
+        uint8_t* src = sm + C::kRingOff + at.slot * kFill;
+        for (int r = 0; r < kGroup; ++r) {
+          const int i = grp * kGroup + r;
+          const bool exists = (info.valid[i >> 5] >> (i & 31)) & 1u;
+          if (exists && info.rel + i < 0) continue;            // context: everybody sees it
+          if (lane < 8 * n) {
+            uint4* u = reinterpret_cast<uint4*>(src + (lane >> 3) * kChunk + r * 128) + (lane & 7);
+            const uint4 old = *u, now = exists ? finite_only<kFp8>(old) : make_uint4(0, 0, 0, 0);
+            if (now.x != old.x || now.y != old.y || now.z != old.z || now.w != old.w) *u = now;
+          }
+        }
+      }
+      if (clean || !p.box) fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(lead_bar(C::bReady + at.slot));
+      at.next();
+    };
+    const auto v_part = [&](int k) {
+      const int ri = k % kInfos;
+      const typename C::Info& info = infos[ri];
+      const bool clean = info.flags & kClean;
+      for (int grp = 0; grp < 2 && ok; ++grp)
+        for (int f = 0; f < v_pairs && ok; ++f) hand_on(clean, info, grp, min(2, n_half - 2 * f));
+      __syncwarp();
+      if (lane == 0) mbar_arrive(BAR(C::bInfoEmpty + ri));
+    };
+    for (int k = 0; ok; ++k) {
+      const int ri = k % kInfos;
+      if (!warp_wait(BAR(C::bInfoFull + ri), (uint32_t)((k / kInfos) & 1), abort_flag)) break;
+      const int flags = *reinterpret_cast<volatile int*>(&infos[ri].flags);
+      if (flags & kEnd) break;
+      const bool first = flags & kFirst;
+      if (first && k > 0) v_part(k - 1);
+      for (int f = 0; f < k_fills && ok; ++f) hand_on(false, infos[ri], 0, 2);
+      if (!first && ok) v_part(k - 1);
+      if ((flags & kFinal) && ok) v_part(k);
+      if (flags & kFinal) break;
+    }
+  } else if (warp > 10) {
+    // ======================= q of every unit; rows by cp.async ============================
+    const int tid = threadIdx.x - 11 * 32;
+    Ring<C::kSlots> at;
+    uint32_t units = 0;
+    bool ok = true;
+    // a fill: chunks c0, c0 + 1 (below c_end) of entry group grp of the tile of info ri
+    const auto fill = [&](int ri, int grp, int c0, int c_end) {
+      if (!ok) return;
+      const int* rows = reinterpret_cast<const int*>(sm + C::kRowOff) + ri * kTile + grp * kGroup;
+      const int jj = tid & 7, r0 = tid >> 3, n = min(2, c_end - c0);
+      if (!(ok = warp_wait(BAR(C::bEmpty + at.slot), at.parity ^ 1, abort_flag))) return;
+      const uint32_t dst = sb + C::kRingOff + at.slot * kFill + r0 * 128 + ((jj ^ (r0 & 7)) << 4);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int row = rows[r0 + 16 * i];
+        const uint8_t* src = a.pool.rows + (size_t)(row < 0 ? 0 : row) * W;
+        for (int c = 0; c < n; ++c) {
+          const int col = (c0 + c) * 128 + jj * 16;
+          const bool has = row >= 0 && col < W;
+          cp_async_16(dst + c * kChunk + i * 2048, has ? src + col : a.pool.rows, has ? 16u : 0u);
+        }
+      }
+      cp_async_arrive_noinc(BAR(C::bFull + at.slot));
+      at.next();
+    };
+    const auto v_part = [&](int k) {
+      const int ri = k % kInfos;
+      if (!p.box)
+        for (int grp = 0; grp < 2; ++grp)
+          for (int f = 0; f < v_pairs; ++f) fill(ri, grp, rank * n_half + 2 * f, rank * n_half + n_half);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(BAR(C::bInfoEmpty + ri));
+    };
+    for (int k = 0; ok; ++k) {
+      const int ri = k % kInfos;
+      if (!warp_wait(BAR(C::bInfoFull + ri), (uint32_t)((k / kInfos) & 1), abort_flag)) break;
+      const typename C::Info& info = infos[ri];
+      const int flags = info.flags;
+      if (flags & kEnd) break;
+      const bool first = flags & kFirst;
+      if (first && k > 0) v_part(k - 1);
+      if (!p.box)
+        for (int f = 0; f < k_fills; ++f) fill(ri, rank, 2 * f, n_chunks);
+      if (!first) v_part(k - 1);
+      if (first && ok) {
+        const uint32_t ph = (units & 1) ^ 1;
+        ++units;
+        if (kFp8) {
+          if (warp == 11) {
+            ok = warp_wait(BAR(C::bQEmpty), ph, abort_flag);
+            if (ok && elect_one()) {
+              const long long slot = q_slot(info.tok0, a.H, info.seq, info.unit_row / kUnitRows);
+              const uint32_t bytes = (uint32_t)n_chunks * 2 * kChunk;
+              mbar_arrive_expect_tx(BAR(C::bQLocal), bytes + kRows * 4);
+              bulk_load(sb + C::kQOff, p.q_codes + (slot * 2 + rank) * bytes, bytes, BAR(C::bQLocal));
+              bulk_load(sb + C::kQScaleOff + (units & 1) * kRows * 4, p.q_scale + slot * kUnitRows + rank * kRows, kRows * 4,
+                        BAR(C::bQLocal));
+            }
+            __syncwarp();
+            if (ok) ok = warp_wait(BAR(C::bQLocal), ph ^ 1, abort_flag);
+            if (ok && lane == 0) mbar_arrive_cluster(lead_bar(C::bQFull));
+          }
+        } else {
+          ok = warp_wait(BAR(C::bQEmpty), ph, abort_flag);
+          if (ok) {
+            const int jj = tid & 7;
+#pragma unroll 1
+            for (int i = 0; i < 4; ++i) {
+              const int r = (tid >> 3) + 16 * i, ur = rank * kRows + r;
+              const bool has = ur < info.rows;
+              const int sr = info.unit_row + (has ? ur : 0);
+              const long long t = info.tok0 + sr / a.H, h = sr % a.H;
+              const uint8_t *ql = a.q_latent + t * a.ql_st + h * a.ql_sh, *qr = a.q_rope + t * a.qr_st + h * a.qr_sh;
+              const uint32_t dst = sb + C::kQOff + r * 128 + ((jj ^ (r & 7)) << 4);
+              for (int c = 0; c < n_chunks; ++c) {
+                const int col = c * 128 + jj * 16;
+                const bool in = has && col < W;
+                const uint8_t* src = !in ? a.q_latent : (col < 2 * L ? ql + col : qr + (col - 2 * L));
+                cp_async_16(dst + c * kChunk, src, in ? 16u : 0u);
+              }
+            }
+            cp_async_wait_all();
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(lead_bar(C::bQFull));
+          }
+        }
+      }
+      if ((flags & kFinal) && ok) v_part(k);
+      if (flags & kFinal) break;
+    }
+    cp_async_wait_all();
+    if (kFp8 && warp == 11 && units > 0) {       // (a copy in flight, where the CTA gave up)
+      mbar_wait_drain(BAR(C::bQLocal), (units - 1) & 1);
+      __syncwarp();
+    }
+  } else {
+    // ================================ softmax and epilogue ================================
+    // TMEM lanes 32 quad ..: rows 32 (quad & 1) .., entry group (of S) or channel half (of O) quad >> 1; this
+    // warp takes the columns of half `ch` of each
+    const int quad = warp & 3, ch = warp >> 2, grp = quad >> 1;
+    const int row = (quad & 1) * 32 + lane, word = 2 * grp + ch;
+    const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
+    float* red = reinterpret_cast<float*>(sm + C::kRedOff);
+    uint8_t* pb = sm + C::kPOff;
+    float m = -INFINITY, l = 0.f;
+    uint32_t units = 0;
+    int reds = 0;
+    bool ok = true;
+    // the four parts' values of this thread's row
+    const auto exchange = [&](float mine, float (&own)[4]) {
+      float* r = red + (reds & 1) * 4 * kRows;
+      ++reds;
+      r[word * kRows + row] = mine;
+      ok = named_bar_and(1, kSoftmax, ok);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) own[e] = r[e * kRows + row];
+      return ok;
+    };
+    for (int k = 0;; ++k) {
+      const int ri = k % kInfos, sn = k & 1;
+      ok = warp_wait(BAR(C::bInfoFull + ri), (uint32_t)((k / kInfos) & 1), abort_flag) && ok;
+      const typename C::Info& info = infos[ri];
+      const int flags = ok ? info.flags : kEnd, slot = info.slot;
+      // (all eight warps agree: where one gave up, they leave together)
+      if (!named_bar_and(1, kSoftmax, ok && !(flags & kEnd))) break;
+      const bool first = flags & kFirst, last = flags & kLast;
+      const int n_rows = info.rows, first_row = info.first_row;
+      uint32_t seen = info.valid[word];
+      {
+        // entries 32 word + i of the tile, drafted ones by the mask of this row's token
+        const int rel = info.rel + 32 * word;
+        if (rel > -32) {
+          const int ur = rank * kRows + row;
+          uint32_t bits = 0;
+          if (ur < n_rows) {
+            const int i = (info.unit_row + ur) / a.H;            // the row's drafted token
+            if (a.mask) {
+              const uint32_t* mk = a.mask + (size_t)(info.tok0 + i) * a.mask_words;
+              const int at = rel < 0 ? 0 : rel >> 5;
+              const uint32_t w0 = at < a.mask_words ? __ldg(mk + at) : 0u;
+              if (rel < 0) bits = (w0 << -rel) | ((1u << -rel) - 1u);
+              else {
+                const uint32_t w1 = at + 1 < a.mask_words ? __ldg(mk + at + 1) : 0u;
+                bits = __funnelshift_r(w0, w1, rel & 31);
+              }
+            } else {
+              const int n = i - rel + 1;                         // entries up to token i's
+              bits = n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u;
+            }
+          }
+          seen &= bits;
+        }
+      }
+      ok = warp_wait(BAR(C::bSFull + sn), (uint32_t)((k >> 1) & 1), abort_flag) && ok;
+      __syncwarp();
+      tc_fence_after();
+      if (first) {
+        ++units;
+        m = -INFINITY;
+        l = 0.f;
+      }
+      float x[32];
+      tmem_ld32(lanes + kSCol + sn * 64 + 32 * ch, x);
+      tmem_wait_ld();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(lead_bar(C::bSEmpty + sn));
+      float arg = p.scale_log2;                  // log2 of the weights: arg x
+      float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+      if constexpr (kFp8) {
+        arg *= reinterpret_cast<const float*>(sm + C::kQScaleOff)[(units & 1) * kRows + row];
+        const float4* ks = reinterpret_cast<const float4*>(info.scale + 32 * word);
+        const float4* ls = reinterpret_cast<const float4*>(info.lscale + 32 * word);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float4 c = ks[j], d = ls[j];
+          const float cs[4] = {c.x, c.y, c.z, c.w}, ds[4] = {d.x, d.y, d.z, d.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            float& v = x[4 * j + e];
+            v *= cs[e];
+            const float z = fmaf(arg, v, ds[e]);
+            mx[e] = fmaxf(mx[e], (seen >> (4 * j + e)) & 1u ? z : -INFINITY);
+          }
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 32; ++j) x[j] *= arg;
+        if (seen != 0xffffffffu) {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) x[j] = (seen >> j) & 1u ? x[j] : -INFINITY;
+        }
+#pragma unroll
+        for (int j = 0; j < 32; ++j) mx[j & 3] = fmaxf(mx[j & 3], x[j]);
+      }
+      const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+      // Most tiles leave every running maximum within tau of what it was: one vote tells, and the maxima are
+      // exchanged only where one has to move.
+      float al = 1.f;
+      bool grow = false;
+      if (!named_bar_and(1, kSoftmax, ok && !(mt > m + C::kTau))) {
+        float own[4];
+        exchange(mt, own);
+        const float t = fmaxf(fmaxf(own[0], own[1]), fmaxf(own[2], own[3]));
+        const float n = t > m + C::kTau ? t : m;
+        if (n != m) {
+          al = fast_exp2(m - n);
+          l *= al;
+          m = n;
+        }
+        grow = __any_sync(0xffffffffu, al != 1.f);
+      }
+      // (a row without any entry so far: everything is masked, the reference does not matter)
+      const float ref = m == -INFINITY ? 0.f : m;
+      if constexpr (kFp8) {
+#pragma unroll
+        for (int j = 0; j < 32; ++j) x[j] = (seen >> j) & 1u ? fast_exp2(fmaf(arg, x[j], -ref)) : 0.f;
+      } else {
+#pragma unroll
+        for (int j = 0; j < 32; ++j) x[j] = fast_exp2(x[j] - ref);
+      }
+      float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int j = 0; j < 32; ++j) sum[j & 3] += x[j];
+      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+      // the products of the tile before have read P and added to O
+      if (k > 0) ok = warp_wait(BAR(C::bPvDone), (uint32_t)((k - 1) & 1), abort_flag) && ok;
+      if (grow && !first) {
+        tc_fence_after();
+        const int n_mt = kFp8 ? n_half : v_pairs;
+#pragma unroll 1
+        for (int c = 0; c < 2 * n_mt; ++c) {     // 32 columns a time: of 128-channel block c / 2
+          const uint32_t at = lanes + (c >> 1) * 128 + 64 * ch + 32 * (c & 1);
+          float o[32];
+          tmem_ld32(at, o);
+          tmem_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] *= al;
+          tmem_st32(at, o);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+      }
+      if constexpr (kFp8) {
+        // u = kPUnit p scale in f16 as three e5m2 terms, each the nearest to what is left
+        const float4* ks = reinterpret_cast<const float4*>(info.scale + 32 * word);
+        const auto upper = [](uint32_t f16x2) { return (f16x2 + 0x00800080u) & 0xff00ff00u; };
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {            // sixteen entries: a 16-byte unit of each term
+          uint32_t w[3][4];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const float4 c = ks[4 * u + q];
+            const float* e = x + 16 * u + 4 * q;
+            const float f[4] = {e[0] == 0.f ? 0.f : e[0] * c.x, e[1] == 0.f ? 0.f : e[1] * c.y,
+                                e[2] == 0.f ? 0.f : e[2] * c.z, e[3] == 0.f ? 0.f : e[3] * c.w};
+            uint32_t t[3][2];
+#pragma unroll
+            for (int z = 0; z < 2; ++z) {
+              __half2 y = __floats2half2_rn(f[2 * z], f[2 * z + 1]);
+#pragma unroll
+              for (int i = 0; i < 3; ++i) {
+                t[i][z] = upper(*reinterpret_cast<const uint32_t*>(&y));
+                if (i < 2) y = __hsub2(y, *reinterpret_cast<const __half2*>(&t[i][z]));
+              }
+            }
+#pragma unroll
+            for (int i = 0; i < 3; ++i) w[i][q] = __byte_perm(t[i][0], t[i][1], 0x7531);
+          }
+          const int at = row * 128 + (((2 * word + u) ^ (row & 7)) << 4);
+#pragma unroll
+          for (int i = 0; i < 3; ++i)
+            *reinterpret_cast<uint4*>(pb + i * kChunk + at) = make_uint4(w[i][0], w[i][1], w[i][2], w[i][3]);
+        }
+      } else {
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {            // 16-byte unit: eight entries
+          const float* e = x + 8 * u;
+          *reinterpret_cast<uint4*>(pb + grp * kChunk + row * 128 + (((4 * ch + u) ^ (row & 7)) << 4)) =
+              make_uint4(pack_bf16x2(e[0], e[1]), pack_bf16x2(e[2], e[3]), pack_bf16x2(e[4], e[5]),
+                         pack_bf16x2(e[6], e[7]));
+        }
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive_cluster(lead_bar(C::bPReady));
+        mbar_arrive(BAR(C::bInfoEmpty + ri));
+      }
+      if (last) {
+        // ---- epilogue: denominators, then O ----
+        float own[4];
+        exchange(l, own);
+        const float ls = (own[0] + own[1]) + (own[2] + own[3]);
+        // (0: no entry at all.  A NaN among the scores is in the sum, whatever the maximum is.)
+        const float inv = ls == 0.f ? 0.f : (kFp8 ? 1.f / kPUnit : 1.f) / ls;
+        const int ur = rank * kRows + row;
+        const bool mine = ur < n_rows;
+        const size_t prow = ((size_t)slice * 2 + (slot > 0 ? 1 : 0)) * kUnitRows + ur;
+        if (slot >= 0 && word == 0) p.lse[prow] = ls == 0.f ? -INFINITY : m + __log2f(ls);
+        ok = warp_wait(BAR(C::bPvDone), (uint32_t)(k & 1), abort_flag) && ok;
+        tc_fence_after();
+        const int n_mt = kFp8 ? n_half : v_pairs;
+#pragma unroll 1
+        for (int c = 0; c < 2 * n_mt; ++c) {
+          const int col = 64 * ch + 32 * (c & 1), block = c >> 1;
+          const int d = grp * n_half * C::kCw + block * 128 + col;
+          // (bf16: the last block of an odd number of chunks is one chunk wide)
+          const bool there = (kFp8 || 2 * block + 1 < n_half || col < 64) && d < L;
+          float o[32];
+          tmem_ld32(lanes + block * 128 + col, o);
+          tmem_wait_ld();
+          if (there && mine) {                   // (d and L are multiples of 32: all 32 channels exist)
+            if (slot >= 0) {
+              float4* dst = reinterpret_cast<float4*>(p.part + prow * L + d);
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                dst[e] = make_float4(o[4 * e] * inv, o[4 * e + 1] * inv, o[4 * e + 2] * inv, o[4 * e + 3] * inv);
+            } else {
+              uint4* dst = reinterpret_cast<uint4*>(a.out + ((size_t)first_row + ur) * L * 2 + d * 2);
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                dst[e] = make_uint4(pack_bf16x2(o[8 * e] * inv, o[8 * e + 1] * inv),
+                                    pack_bf16x2(o[8 * e + 2] * inv, o[8 * e + 3] * inv),
+                                    pack_bf16x2(o[8 * e + 4] * inv, o[8 * e + 5] * inv),
+                                    pack_bf16x2(o[8 * e + 6] * inv, o[8 * e + 7] * inv));
+            }
+          }
+          __syncwarp();                          // (the loads from TMEM are the whole warp's)
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(lead_bar(C::bOFree));
+      }
+      if (flags & kFinal) break;
+    }
   }
-  const float inv = l == 0.f ? 0.f : 1.f / l;
-  for (int e = 0; e < 2; ++e) {
-    const int d = threadIdx.x + e * kThreads;
-    if (d < L) reinterpret_cast<__nv_bfloat16*>(a.out)[((size_t)t * a.H + h) * L + d] = __float2bfloat16(o[e] * inv);
+#undef BAR
+  __syncwarp();
+  tc_fence_before();
+  cluster_arrive();
+  cluster_wait();
+  if (warp == 8) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
   }
+}
+
+// Joins the parts of the units that were cut: out = sum_i 2^(lse_i - M) O_i / sum_i 2^(lse_i - M), in the
+// order of the slices.  A warp takes 128 channels of a row, eight parts in flight.  Bound by reading the parts.
+constexpr int kMergeWarps = 8;
+
+__global__ void __launch_bounds__(32 * kMergeWarps)
+    tree_merge_kernel(const Part* __restrict__ cut, const float* __restrict__ lse, const float* __restrict__ part,
+                      __nv_bfloat16* __restrict__ out, int slices, int L) {
+  __shared__ int4 item[kMaxSlices];       // row, slice, last slice, rows of the items up to and with this one
+  __shared__ int n_items;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nq = (L + 127) >> 7;
+  pdl_wait();
+  if (warp == 0) {
+    int n = 0, rows = 0;
+    for (int s0 = 0; s0 < slices; s0 += 32) {
+      Part c = {0, 0, -1, 0};
+      if (s0 + lane < slices) c = cut[s0 + lane];
+      const unsigned m = __ballot_sync(0xffffffffu, c.last >= 0);
+      int scan = c.last >= 0 ? c.rows : 0;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, scan, o);
+        if (lane >= o) scan += x;
+      }
+      if (c.last >= 0) item[n + __popc(m & ((1u << lane) - 1u))] = make_int4(c.row, s0 + lane, c.last, rows + scan);
+      n += __popc(m);
+      rows += __shfl_sync(0xffffffffu, scan, 31);
+    }
+    if (lane == 0) n_items = n;
+  }
+  __syncthreads();
+  if (n_items == 0) return;
+  const int work = item[n_items - 1].w * nq;
+  for (int u = blockIdx.x * kMergeWarps + warp; u < work; u += gridDim.x * kMergeWarps) {
+    const int r_all = u / nq, d = (u % nq) * 128 + 4 * lane;
+    int i = 0;
+    while (item[i].w <= r_all) ++i;
+    const int4 it = item[i];
+    const int r = r_all - (i ? item[i - 1].w : 0), n = it.z - it.y + 1;
+    const auto at = [&](int s) { return ((size_t)(it.y + s) * 2 + (s == 0 ? 1 : 0)) * kUnitRows + r; };
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    float M = -INFINITY, tot = 0.f;
+    for (int s0 = 0; s0 < n; s0 += 8) {
+      float e[8];
+      float4 v[8];
+#pragma unroll
+      for (int z = 0; z < 8; ++z) {
+        e[z] = -INFINITY;
+        v[z] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (s0 + z < n) {
+          e[z] = lse[at(s0 + z)];
+          if (d < L) v[z] = *reinterpret_cast<const float4*>(part + at(s0 + z) * L + d);
+        }
+      }
+      float mx = M;
+#pragma unroll
+      for (int z = 0; z < 8; ++z) mx = fmaxf(mx, e[z]);
+      // (a NaN among the parts' sums is not seen by the maximum but comes back in its weight)
+      const float ref = mx == -INFINITY ? 0.f : mx, f = exp2f(M - ref);
+      M = mx;
+      tot *= f;
+      acc.x *= f;
+      acc.y *= f;
+      acc.z *= f;
+      acc.w *= f;
+#pragma unroll
+      for (int z = 0; z < 8; ++z) {
+        const float w = exp2f(e[z] - ref);
+        tot += w;
+        acc.x = fmaf(w, v[z].x, acc.x);
+        acc.y = fmaf(w, v[z].y, acc.y);
+        acc.z = fmaf(w, v[z].z, acc.z);
+        acc.w = fmaf(w, v[z].w, acc.w);
+      }
+    }
+    const float inv = tot == 0.f ? 0.f : 1.f / tot;
+    if (d < L)
+      *reinterpret_cast<uint2*>(out + ((size_t)it.x + r) * L + d) =
+          make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+  }
+}
+
+size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
+
+int slices_of(int sms) { return sms / 2 < 1 ? 1 : sms / 2 > kMaxSlices ? kMaxSlices : sms / 2; }
+
+struct Workspace {
+  size_t cut, lse, part, codes, scale, bytes;
+};
+Workspace workspace_layout(const LatentTreeArgs& a, bool fp8, int sms) {
+  const size_t slots = (size_t)slices_of(sms) * 2 * kUnitRows;
+  Workspace w;
+  w.cut = 0;
+  w.lse = align256(slices_of(sms) * sizeof(Part));
+  w.part = w.lse + align256(slots * sizeof(float));
+  w.codes = align256(w.part + slots * (size_t)a.pool.L * sizeof(float));
+  const size_t units = fp8 ? (size_t)((long long)a.T * a.H / kUnitRows + a.pool.B + 1) : 0;
+  w.scale = w.codes + units * 2 * ((a.pool.L + 2 * a.pool.R + 127) / 128) * 2 * kChunk;
+  w.bytes = w.scale + units * kUnitRows * sizeof(float);
+  return w;
 }
 
 }  // namespace
 
-cudaError_t prepare_latent_tree() { return cudaSuccess; }
+cudaError_t prepare_latent_tree() {
+  const auto most = cudaFuncAttributeMaxDynamicSharedMemorySize;
+  cudaError_t e = cudaFuncSetAttribute(latent_tree_kernel<false>, most, Cfg<false>::kSmem);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(latent_tree_kernel<true>, most, Cfg<true>::kSmem);
+  return e;
+}
 
-size_t latent_tree_workspace(const LatentTreeArgs&, bool, int) { return 0; }
+size_t latent_tree_workspace(const LatentTreeArgs& a, bool fp8, int sms) {
+  return workspace_layout(a, fp8, sms).bytes;
+}
 
-cudaError_t launch_latent_tree(const LatentTreeArgs& a, bool fp8, void*, int, cudaStream_t stream) {
-  return launch_with_pdl(fp8 ? latent_tree_kernel<true> : latent_tree_kernel<false>, dim3((unsigned)a.T * a.H),
-                         dim3(kThreads), 0, stream, false, a);
+cudaError_t launch_latent_tree(const LatentTreeArgs& a, bool fp8, void* workspace, int sms, cudaStream_t stream) {
+  TreeParams p = {};
+  p.a = a;
+  p.slices = slices_of(sms);
+  p.scale_log2 = a.scale * 1.4426950408889634f;
+  const Workspace w = workspace_layout(a, fp8, sms);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  p.cut = reinterpret_cast<Part*>(ws + w.cut);
+  p.lse = reinterpret_cast<float*>(ws + w.lse);
+  p.part = reinterpret_cast<float*>(ws + w.part);
+  p.q_codes = ws + w.codes;
+  p.q_scale = reinterpret_cast<float*>(ws + w.scale);
+  // Pages of a multiple of eight entries: boxes of as many rows as divide the page (at most a fill's 64).
+  p.box = 0;
+  for (int b = 8; b <= kGroup; b *= 2)
+    if (a.pool.ps % b == 0) p.box = b;
+  if (p.box) {
+    const unsigned long long W = a.pool.row_bytes;
+    const unsigned long long d[2] = {W, (unsigned long long)(a.pool.num_blocks * a.pool.ps)}, st[1] = {W};
+    const unsigned bx[2] = {128, (unsigned)p.box};
+    if (!encode_bytes(&p.chunk, a.pool.rows, 2, d, st, bx)) return cudaErrorInvalidValue;
+  }
+  const long long rows = (long long)a.T * a.H;
+  cudaError_t e = cudaSuccess;
+  if (fp8) {
+    const long long blocks = (rows + 7) / 8;
+    e = launch_with_pdl(tree_q_kernel, dim3((unsigned)(blocks < 8LL * sms ? blocks : 8LL * sms)), dim3(256), 0, stream,
+                        false, a, p.q_codes, p.q_scale);
+    if (e != cudaSuccess) return e;
+  }
+  if (fp8)
+    e = launch_with_pdl(latent_tree_kernel<true>, dim3(2 * p.slices), dim3(kThreads), Cfg<true>::kSmem, stream, true, p);
+  else
+    e = launch_with_pdl(latent_tree_kernel<false>, dim3(2 * p.slices), dim3(kThreads), Cfg<false>::kSmem, stream, false,
+                        p);
+  if (e != cudaSuccess) return e;
+  const long long units = (rows * ((a.pool.L + 127) / 128) + kMergeWarps - 1) / kMergeWarps;
+  return launch_with_pdl(tree_merge_kernel, dim3((unsigned)(units < 4LL * sms ? units : 4LL * sms)), dim3(32 * kMergeWarps),
+                         0, stream, true, (const Part*)p.cut, (const float*)p.lse, (const float*)p.part,
+                         reinterpret_cast<__nv_bfloat16*>(a.out), p.slices, a.pool.L);
 }
 
 // This translation unit's copy of the device error word (see spa_device.cuh).
