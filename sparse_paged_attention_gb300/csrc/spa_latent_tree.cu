@@ -110,8 +110,9 @@ struct Part {                 // the unit cut at the end of a slice: its first r
 
 struct TreeParams {
   CUtensorMap chunk;          // the pool's rows, boxes of 128 bytes by `box` rows
+  CUtensorMap pair;           // the same by whole 128-byte chunks, boxes of two chunks of 64 rows (box 64)
   LatentTreeArgs a;
-  int box;                    // rows of a box: 8, 16, 32 or 64 (0: cp.async)
+  int box, box_shift;         // rows of a box: 8, 16, 32 or 64 (0: cp.async), and log2 of them
   int slices;
   float scale_log2;
   Part* cut;                  // [slices]
@@ -150,9 +151,11 @@ __device__ __forceinline__ void commit_pair(uint32_t bar) {
       "h"((uint16_t)3)
       : "memory");
 }
-__device__ __forceinline__ bool warp_wait_cluster(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
-  const bool ok = mbar_wait_cluster(bar, parity, abort_flag);
-  return __all_sync(0xffffffffu, ok);
+// Arrive on a barrier of either CTA (a shared::cluster address).  What the MMAs wait for is a CTA's own shared or
+// tensor memory, read by that CTA's own tensor core, so the arrival orders it within the CTA: at cluster
+// scope an arrival took its warp 980 cycles, and a tile of 128 entries 15,000 instead of 5,000.
+__device__ __forceinline__ void mbar_arrive_pair(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 
 // A sequence as the schedule sees it: its tokens and entries, units and tiles of a unit (no units: none to do).
@@ -442,7 +445,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       int flags, slot, base, first_row, rows, tok0, unit_row, rel, valid_len;
       int blk[4];                                // boxed: of box `lane`; else of entries lane + 32 e
     };
-    const int boxes = p.box ? kTile / p.box : 0;
+    const auto page_of = [&](int key) { return a.pool.ps_shift >= 0 ? key >> a.pool.ps_shift : key / a.pool.ps; };
+    const int my_key = p.box ? lane << p.box_shift : lane;        // first entry of this lane's box
+    const bool has_box = p.box && my_key < kTile;
     if (left_all > 0) begin_unit();
     const auto next_tile = [&](Tile& x) {        // the next tile, its block-table reads under way
       x.flags = kEnd;
@@ -467,14 +472,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       x.blk[0] = x.blk[1] = x.blk[2] = x.blk[3] = -2;
       const int32_t* bt = a.pool.bt + (size_t)u_seq * a.pool.bt_stride;
       if (p.box) {
-        const int key = lane * p.box;
-        if (lane < boxes && key < x.valid_len) x.blk[0] = __ldg(bt + (x.base + key) / a.pool.ps);
+        if (has_box && my_key < x.valid_len) x.blk[0] = __ldg(bt + page_of(x.base + my_key));
       } else {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int key = lane + 32 * e;
-          if (key < x.valid_len) x.blk[e] = __ldg(bt + (x.base + key) / a.pool.ps);
-        }
+        for (int e = 0; e < 4; ++e)
+          if (lane + 32 * e < x.valid_len) x.blk[e] = __ldg(bt + page_of(x.base + lane + 32 * e));
       }
       fresh = false;
       --left_all;
@@ -485,16 +487,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     Ring<C::kSlots> at;
     long long fills = 0;
     bool ok = true;
-    // a fill: chunks c0, c0 + 1 (below c_end) of entry group `grp` of the tile whose boxes begin at `rows`
+    // A fill: chunks c0, c0 + 1 (below c_end) of entry group `grp` of the tile whose boxes begin at `rows`.  Lane
+    // (chunk, box of the group) copies one box; with boxes of 64 rows one lane both chunks.
+    const int per_group = kGroup >> p.box_shift, my_c = lane >> (6 - p.box_shift), my_box = lane & (per_group - 1);
+    const uint32_t my_off = my_c * kChunk + ((my_box << p.box_shift) << 7);
+    const bool lead = elect_one();
     const auto fill = [&](int rows, int grp, int c0, int c_end) -> bool {
       if (!warp_wait(BAR(C::bEmpty + at.slot), at.parity ^ 1, abort_flag)) return false;
       const uint32_t dst = sb + C::kRingOff + at.slot * kFill, full = BAR(C::bFull + at.slot);
-      const int n = min(2, c_end - c0), per_group = kGroup / p.box;
-      if (lane == 0) mbar_arrive_expect_tx(full, (uint32_t)(n * kChunk));
-      __syncwarp();
-      const int c = lane / per_group, bx = lane % per_group;
-      const int row = __shfl_sync(0xffffffffu, rows, (grp * per_group + bx) & 31);
-      if (c < n) tma_row(dst + c * kChunk + bx * p.box * 128, &p.chunk, (c0 + c) * 128, row, full);
+      const int n = min(2, c_end - c0);
+      const int row = __shfl_sync(0xffffffffu, rows, grp * per_group + my_box);
+      if (lead) mbar_arrive_expect_tx(full, (uint32_t)(n * kChunk));
+      if (p.box == kGroup && n == 2 && (c0 + 2) * 128 <= W) {
+        if (lead) tma_box3(dst, &p.pair, 0, row, c0, full);
+      } else {
+        __syncwarp();
+        if (my_c < n) tma_row(dst + my_off, &p.chunk, (c0 + my_c) * 128, row, full);
+      }
       __syncwarp();
       ++fills;
       at.next();
@@ -522,31 +531,39 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (p.box) {
           const bool good = x.blk[0] >= 0 && (long long)x.blk[0] < a.pool.num_blocks;
           if (x.blk[0] != -2 && !good) flag_error(SPA_ERR_INDEX);
-          const int key = x.base + lane * p.box;
           // a box without entries starts past the last row and is filled with zeros
-          box_rows = good ? x.blk[0] * a.pool.ps + key % a.pool.ps : total_rows;
-          const unsigned okb = __ballot_sync(0xffffffffu, good);
+          const int key = x.base + my_key;
+          box_rows = good ? x.blk[0] * a.pool.ps + (key - page_of(key) * a.pool.ps) : total_rows;
+          const uint32_t okb = __ballot_sync(0xffffffffu, good);
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const int i = lane + 32 * e, bx = i / p.box;
-            const bool v = ((okb >> bx) & 1u) && i < x.valid_len;
-            rows4[e] = __shfl_sync(0xffffffffu, box_rows, bx) + (i - bx * p.box);
-            if (!v) rows4[e] = -1;
+            // a bit an entry: the boxes' bits spread, cut off at the sequence's end
+            const uint32_t b = okb >> ((32 * e) >> p.box_shift);
+            uint32_t m = p.box >= 32   ? 0u - (b & 1u)
+                         : p.box == 16 ? (b & 1u) * 0xffffu | (b >> 1 & 1u) * 0xffff0000u
+                                       : (b & 1u) * 0xffu | (b >> 1 & 1u) * 0xff00u | (b >> 2 & 1u) * 0xff0000u |
+                                             (b >> 3 & 1u) * 0xff000000u;
+            const int n = x.valid_len - 32 * e;
+            if (n < 32) m &= n <= 0 ? 0u : (1u << n) - 1u;
+            valid[e] = m;
+            if constexpr (kFp8) {
+              const int i = lane + 32 * e;
+              rows4[e] = __shfl_sync(0xffffffffu, box_rows, i >> p.box_shift) + (i & (p.box - 1));
+              if (!(m >> lane & 1u)) rows4[e] = -1;
+            }
           }
         } else {
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const int i = lane + 32 * e;
+            const int key = x.base + lane + 32 * e;
             const bool good = x.blk[e] >= 0 && (long long)x.blk[e] < a.pool.num_blocks;
             if (x.blk[e] != -2 && !good) flag_error(SPA_ERR_INDEX);
-            rows4[e] = good ? x.blk[e] * a.pool.ps + (x.base + i) % a.pool.ps : -1;
+            rows4[e] = good ? x.blk[e] * a.pool.ps + (key - page_of(key) * a.pool.ps) : -1;
+            valid[e] = __ballot_sync(0xffffffffu, good);
           }
         }
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          valid[e] = __ballot_sync(0xffffffffu, rows4[e] >= 0);
-          clean |= valid[e] != 0xffffffffu;
-        }
+        for (int e = 0; e < 4; ++e) clean |= valid[e] != 0xffffffffu;
         clean |= x.rel + kTile > 0;              // drafted tokens' entries among them
       }
       float sc[4] = {0.f, 0.f, 0.f, 0.f};
@@ -643,32 +660,36 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       bool o_first = true;                       // of the tile whose PV comes next
       bool ok = true;
       const auto pv = [&](int k) {               // O of tile k
-        ok = ok && warp_wait_cluster(BAR(C::bPReady), (uint32_t)(k & 1), abort_flag);
-        if (ok && o_first && units > 1) ok = warp_wait_cluster(BAR(C::bOFree), (units - 2) & 1, abort_flag);
+        ok = ok && warp_wait(BAR(C::bPReady), (uint32_t)(k & 1), abort_flag);
+        if (ok && o_first && units > 1) ok = warp_wait(BAR(C::bOFree), (units - 2) & 1, abort_flag);
         for (int grp = 0; grp < 2 && ok; ++grp) {
           for (int f = 0; f < v_pairs; ++f) {
-            ok = warp_wait_cluster(BAR(C::bReady + at.slot), at.parity, abort_flag);
+            ok = warp_wait(BAR(C::bReady + at.slot), at.parity, abort_flag);
             if (!ok) break;
             tc_fence_after();
             if (lead) {
               const int n = min(2, n_half - 2 * f);       // chunks of the fill
-              const uint64_t dv = desc_add(dv0, at.slot * kFill);
+              uint64_t b = desc_add(dv0, at.slot * kFill);
+              const uint64_t pa = desc_add(dp, grp * (kFp8 ? 64 : kChunk));
+              const uint32_t acc = !(o_first && grp == 0);
               if (kFp8) {
+                uint32_t d = tmem + f * 256;
+#pragma unroll 1
                 for (int c = 0; c < n; ++c) {             // 128 channels of each CTA
-                  const uint32_t d = tmem + (2 * f + c) * 128;
 #pragma unroll
                   for (int kk = 0; kk < 2; ++kk) {        // 32 entries a step
-                    const uint64_t b = desc_add(dv, c * kChunk + kk * 4096), pa = desc_add(dp, grp * 64 + kk * 32);
-                    mma_pair<kFp8>(d, pa, b, idO(256), !(o_first && grp == 0 && kk == 0));
-                    mma_pair<kFp8>(d, desc_add(pa, kChunk), b, idO(256), 1u);
-                    mma_pair<kFp8>(d, desc_add(pa, 2 * kChunk), b, idO(256), 1u);
+                    mma_pair<kFp8>(d, desc_add(pa, kk * 32), desc_add(b, kk * 4096), idO(256), kk ? 1u : acc);
+                    mma_pair<kFp8>(d, desc_add(pa, kChunk + kk * 32), desc_add(b, kk * 4096), idO(256), 1u);
+                    mma_pair<kFp8>(d, desc_add(pa, 2 * kChunk + kk * 32), desc_add(b, kk * 4096), idO(256), 1u);
                   }
+                  b = desc_add(b, kChunk);
+                  d += 128;
                 }
               } else {
+                const uint32_t id = idO(n * 128);
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk)            // 16 entries a step
-                  mma_pair<kFp8>(tmem + f * 128, desc_add(dp, grp * kChunk + kk * 32), desc_add(dv, kk * 2048),
-                                 idO(n * 128), !(o_first && grp == 0 && kk == 0));
+                  mma_pair<kFp8>(tmem + f * 128, desc_add(pa, kk * 32), desc_add(b, kk * 2048), id, kk ? 1u : acc);
               }
               commit_pair(BAR(C::bEmpty + at.slot));
             }
@@ -691,26 +712,42 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           if (k > 0) pv(k - 1);
           if (!ok) break;
           ++units;
-          ok = warp_wait_cluster(BAR(C::bQFull), (units - 1) & 1, abort_flag);
+          ok = warp_wait(BAR(C::bQFull), (units - 1) & 1, abort_flag);
         }
         // S of tile k
         const int sn = k & 1;
-        if (ok && k >= 2) ok = warp_wait_cluster(BAR(C::bSEmpty + sn), (uint32_t)(((k >> 1) & 1) ^ 1), abort_flag);
+        if (ok && k >= 2) ok = warp_wait(BAR(C::bSEmpty + sn), (uint32_t)(((k >> 1) & 1) ^ 1), abort_flag);
         for (int f = 0; f < k_fills && ok; ++f) {
-          ok = warp_wait_cluster(BAR(C::bReady + at.slot), at.parity, abort_flag);
+          ok = warp_wait(BAR(C::bReady + at.slot), at.parity, abort_flag);
           if (!ok) break;
           tc_fence_after();
           if (lead) {
             const uint32_t dS = tmem + kSCol + sn * 64;
+            // (the loops that issue are short: no predicates in whole chunks, not unrolled across them)
             const int n = min(2, n_chunks - 2 * f);
+            uint64_t b = desc_add(dk0, at.slot * kFill), q = desc_add(dq, f * (kFp8 ? 4 : 2) * kChunk);
+            uint32_t acc = f != 0;
+#pragma unroll 1
             for (int c = 0; c < n; ++c) {
-              const int ch = 2 * f + c, steps = min(4, (W - ch * 128 + 31) >> 5);
-              const uint64_t b = desc_add(dk0, at.slot * kFill + c * kChunk);
-              const uint64_t q = desc_add(dq, ch * (kFp8 ? 2 : 1) * kChunk);
-              for (int st = 0; st < steps; ++st) {
-                mma_pair<kFp8>(dS, desc_add(q, st * 32), desc_add(b, st * 32), idS, (ch | st) != 0);
-                if (kFp8) mma_pair<kFp8>(dS, desc_add(q, kChunk + st * 32), desc_add(b, st * 32), idS, 1u);
+              const int steps = (W - (2 * f + c) * 128 + 31) >> 5;       // 32-byte steps left in the row
+              mma_pair<kFp8>(dS, q, b, idS, acc);
+              if (kFp8) mma_pair<kFp8>(dS, desc_add(q, kChunk), b, idS, 1u);
+              acc = 1u;
+              if (steps >= 4) {
+#pragma unroll
+                for (int st = 1; st < 4; ++st) {
+                  mma_pair<kFp8>(dS, desc_add(q, st * 32), desc_add(b, st * 32), idS, 1u);
+                  if (kFp8) mma_pair<kFp8>(dS, desc_add(q, kChunk + st * 32), desc_add(b, st * 32), idS, 1u);
+                }
+              } else {
+#pragma unroll 1
+                for (int st = 1; st < steps; ++st) {
+                  mma_pair<kFp8>(dS, desc_add(q, st * 32), desc_add(b, st * 32), idS, 1u);
+                  if (kFp8) mma_pair<kFp8>(dS, desc_add(q, kChunk + st * 32), desc_add(b, st * 32), idS, 1u);
+                }
               }
+              b = desc_add(b, kChunk);
+              q = desc_add(q, (kFp8 ? 2 : 1) * kChunk);
             }
             commit_pair(BAR(C::bEmpty + at.slot));
           }
@@ -747,20 +784,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (!ok) return;
       if (clean) {
         uint8_t* src = sm + C::kRingOff + at.slot * kFill;
-        for (int r = 0; r < kGroup; ++r) {
-          const int i = grp * kGroup + r;
-          const bool exists = (info.valid[i >> 5] >> (i & 31)) & 1u;
-          if (exists && info.rel + i < 0) continue;            // context: everybody sees it
-          if (lane < 8 * n) {
-            uint4* u = reinterpret_cast<uint4*>(src + (lane >> 3) * kChunk + r * 128) + (lane & 7);
-            const uint4 old = *u, now = exists ? finite_only<kFp8>(old) : make_uint4(0, 0, 0, 0);
-            if (now.x != old.x || now.y != old.y || now.z != old.z || now.w != old.w) *u = now;
+        const uint32_t lo = info.valid[2 * grp], hi = info.valid[2 * grp + 1];
+        const int ctx = max(-info.rel - grp * kGroup, 0);      // the first row that not all may see
+        // from the first row that needs it: two a step, a half-warp each, four steps' loads in flight
+        const int gone = ~lo ? __ffs(~lo) - 1 : ~hi ? 31 + __ffs(~hi) : kGroup;
+        const int c = (lane >> 3) & 1, half = lane >> 4;
+        for (int r0 = min(ctx, gone) & ~1; r0 < kGroup; r0 += 8) {
+          uint4 old[4];
+          uint4* at_row[4];
+          bool exists[4];
+#pragma unroll
+          for (int z = 0; z < 4; ++z) {
+            const int r = min(r0 + 2 * z + half, kGroup - 1);
+            exists[z] = ((r < 32 ? lo >> r : hi >> (r - 32)) & 1u) != 0;
+            at_row[z] = reinterpret_cast<uint4*>(src + c * kChunk + r * 128) + (lane & 7);
+            old[z] = *at_row[z];
+          }
+#pragma unroll
+          for (int z = 0; z < 4; ++z) {
+            const uint4 now = exists[z] ? finite_only<kFp8>(old[z]) : make_uint4(0, 0, 0, 0);
+            if (c < n && (now.x != old[z].x || now.y != old[z].y || now.z != old[z].z || now.w != old[z].w))
+              *at_row[z] = now;
           }
         }
       }
       if (clean || !p.box) fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(lead_bar(C::bReady + at.slot));
+      if (lane == 0) mbar_arrive_pair(lead_bar(C::bReady + at.slot));
       at.next();
     };
     const auto v_part = [&](int k) {
@@ -845,7 +895,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
             __syncwarp();
             if (ok) ok = warp_wait(BAR(C::bQLocal), ph ^ 1, abort_flag);
-            if (ok && lane == 0) mbar_arrive_cluster(lead_bar(C::bQFull));
+            if (ok && lane == 0) mbar_arrive_pair(lead_bar(C::bQFull));
           }
         } else {
           ok = warp_wait(BAR(C::bQEmpty), ph, abort_flag);
@@ -869,7 +919,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             cp_async_wait_all();
             fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(lead_bar(C::bQFull));
+            if (lane == 0) mbar_arrive_pair(lead_bar(C::bQFull));
           }
         }
       }
@@ -952,7 +1002,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       tmem_wait_ld();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(lead_bar(C::bSEmpty + sn));
+      if (lane == 0) mbar_arrive_pair(lead_bar(C::bSEmpty + sn));
       float arg = p.scale_log2;                  // log2 of the weights: arg x
       float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
       if constexpr (kFp8) {
@@ -1072,7 +1122,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) {
-        mbar_arrive_cluster(lead_bar(C::bPReady));
+        mbar_arrive_pair(lead_bar(C::bPReady));
         mbar_arrive(BAR(C::bInfoEmpty + ri));
       }
       if (last) {
@@ -1118,7 +1168,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(lead_bar(C::bOFree));
+        if (lane == 0) mbar_arrive_pair(lead_bar(C::bOFree));
       }
       if (flags & kFinal) break;
     }
@@ -1269,6 +1319,12 @@ cudaError_t launch_latent_tree(const LatentTreeArgs& a, bool fp8, void* workspac
     const unsigned long long d[2] = {W, (unsigned long long)(a.pool.num_blocks * a.pool.ps)}, st[1] = {W};
     const unsigned bx[2] = {128, (unsigned)p.box};
     if (!encode_bytes(&p.chunk, a.pool.rows, 2, d, st, bx)) return cudaErrorInvalidValue;
+    while (1 << p.box_shift < p.box) ++p.box_shift;
+    if (p.box == kGroup && W >= 256) {
+      const unsigned long long d3[3] = {128, d[1], W / 128}, st3[2] = {W, 128};
+      const unsigned bx3[3] = {128, kGroup, 2};
+      if (!encode_bytes(&p.pair, a.pool.rows, 3, d3, st3, bx3)) return cudaErrorInvalidValue;
+    }
   }
   const long long rows = (long long)a.T * a.H;
   cudaError_t e = cudaSuccess;
