@@ -17,15 +17,19 @@
 // a CTA reads its share of channels of all entries besides its entries' whole rows: 1.85 times the tile.
 //
 // TMEM of a CTA (rows 0-63 in lanes 0-63 and, their other half of the columns, in lanes 64-127): O 256
-// columns, two S of 64.  Shared memory: q, P, and a ring of 16 KB fills (two 128-byte chunks of 64 entries)
-// in the order in which the MMAs take them: K of tile k + 1 before V of tile k, so that S of the next tile runs
-// under the softmax of this one (at a unit's first tile V of the last comes first: q has to change).
+// columns, two S of 64.  Shared memory: q, P, and two rings of cached rows: K (the CTA's own 64 entries of a tile,
+// whole rows, three 128-byte chunks a fill) and V (its channels of all 128 entries, two chunks of 64 a fill).
 //
 //   warps 0-7    softmax: a thread has a row and 32 of a tile's entries; epilogue
-//   warp 8       (of the first CTA) issues all MMAs
-//   warp 9       schedule, page tables, copies of cached rows (TMA)
-//   warp 10      sees every fill land, cleans it where a tile holds what not all rows may see, and tells the MMAs
-//   warps 11-14  q of a unit; cached rows by cp.async where pages are not a multiple of eight entries
+//   warps 8, 11  (of the first CTA) issue the MMAs of S, and those of O
+//   warp 9       schedule, page tables, copies of K, which complete on the first CTA's barrier
+//   warp 10      sees every fill of V land, cleans it where a tile holds what not all rows may see, and tells the
+//                first CTA
+//   warps 12-15  q of a unit; warp 12 the copies of V.  Where pages are not a multiple of eight entries, all cached
+//                rows by cp.async
+//
+// A role's code runs once a tile, from the second-level instruction cache (some six cycles an instruction), so it is
+// their instruction counts that decide: one warp for all copies and one for all MMAs took 7,100 cycles a tile.
 //
 // Cleaning: a masked entry has a weight of zero, but zero times a NaN or infinity is none.  Rows that do not
 // exist are zeroed.  A drafted token's row that is not finite makes the score of whoever sees it NaN or
@@ -42,7 +46,6 @@
 
 #include "spa_errors.h"
 #include "spa_latent.h"
-#include "spa_latent_ring.h"
 #include "spa_launch.h"
 
 namespace spa {
@@ -54,10 +57,10 @@ constexpr int kUnitRows = 128;       // of a pair
 constexpr int kGroup = 64;           // entries of a fill
 constexpr int kTile = 128;           // entries of a tile
 constexpr int kChunk = kGroup * 128;
-constexpr int kFill = 2 * kChunk;
+constexpr int kKFill = 3, kVFill = 2;   // chunks of a fill
 constexpr int kInfos = 4;            // tile infos in flight
 constexpr int kSoftmax = 256;
-constexpr int kThreads = kSoftmax + 7 * 32;
+constexpr int kThreads = kSoftmax + 8 * 32;
 constexpr int kTmemCols = 512;
 constexpr int kSCol = 256;           // O from column 0, two S of 64 columns
 constexpr int kUnitCost = 2;         // tiles' worth of a unit's q and epilogue
@@ -69,7 +72,7 @@ enum { kFirst = 1, kLast = 2, kFinal = 4, kEnd = 8, kClean = 16 };
 
 template <bool kFp8>
 struct Cfg {
-  static constexpr int kSlots = kFp8 ? 7 : 8;
+  static constexpr int kKSlots = 3, kVSlots = kFp8 ? 2 : 4;
   static constexpr int kCw = kFp8 ? 128 : 64;        // channels of a chunk
   static constexpr int kMaxChunks = kFp8 ? 5 : 9;    // of a row
   static constexpr float kTau = kFp8 ? 5.f : 8.f;    // lazy rescale threshold (log2 units)
@@ -77,6 +80,7 @@ struct Cfg {
     int flags, slot, first_row, rows;                // part slot (-1: none); global row of the unit, its rows
     int tok0, unit_row, rel, seq;                    // sequence's first token, unit's first row in it, base - context
     uint32_t valid[4];                               // bit i of word w: entry 32 w + i exists
+    int boxes[16];                                   // first rows of the tile's boxes
     float scale[kFp8 ? kTile : 1];                   // kPUnit times the rows' scales, and log2 of their sizes
     float lscale[kFp8 ? kTile : 1];
   };
@@ -84,21 +88,27 @@ struct Cfg {
   static constexpr int kPBytes = kFp8 ? 3 * kChunk : 2 * kChunk;
   static constexpr int kQOff = 0;
   static constexpr int kPOff = kQOff + kQBytes;
-  static constexpr int kRingOff = kPOff + kPBytes;
-  static constexpr int kRedOff = kRingOff + kSlots * kFill;        // float [2][4][64]
+  static constexpr int kKOff = kPOff + kPBytes;
+  static constexpr int kVOff = kKOff + kKSlots * kKFill * kChunk;
+  static constexpr int kVEnd = kVOff + kVSlots * kVFill * kChunk;
+  static constexpr int kRedOff = kVEnd;                            // float [2][4][64]
   static constexpr int kQScaleOff = kRedOff + 2 * 4 * kRows * 4;   // e4m3: float [2][64]
-  static constexpr int kRowOff = kQScaleOff + (kFp8 ? 2 * kRows * 4 : 0);   // int [kInfos][128]
-  static constexpr int kInfoOff = kRowOff + kInfos * kTile * 4;
-  static constexpr int kBarOff = (kInfoOff + kInfos * (int)sizeof(Info) + 7) & ~7;
+  static constexpr int kInfoOff = kQScaleOff + (kFp8 ? 2 * kRows * 4 : 0);
+  static constexpr int kInfoEnd = kInfoOff + kInfos * (int)sizeof(Info);
+  // Without boxes, the rows of the tiles' entries: int [kInfos][128].  bf16: in the last slot of V, which is
+  // then not used.
+  static constexpr int kRowOff = kFp8 ? kInfoEnd : kVEnd - kVFill * kChunk;
+  static constexpr int kBarOff = ((kFp8 ? kRowOff + kInfos * kTile * 4 : kInfoEnd) + 7) & ~7;
   // Barriers at the same place in both CTAs.  Those marked L are used in the first CTA alone, whose MMA warp
   // waits for both; those marked 2 are completed in both by the MMAs' commits.  Every wait by parity comes when
   // that phase is the next to complete or the last that did: each role passes every phase of what it waits for.
-  static constexpr int bFull = 0, bReady = bFull + kSlots /* L */, bEmpty = bReady + kSlots /* 2 */,
-                       bSFull = bEmpty + kSlots /* 2 */, bSEmpty = bSFull + 2 /* L */,
-                       bPReady = bSEmpty + 2 /* L */, bPvDone = bPReady + 1 /* 2 */, bQFull = bPvDone + 1 /* L */,
-                       bQLocal = bQFull + 1, bQEmpty = bQLocal + 1 /* 2 */, bOFree = bQEmpty + 1 /* L */,
-                       bInfoFull = bOFree + 1, bInfoEmpty = bInfoFull + kInfos, bDrain = bInfoEmpty + kInfos,
-                       kNumB = bDrain + 1;
+  static constexpr int bKFull = 0 /* cp.async */, bKReady = bKFull + kKSlots /* L */, bKEmpty = bKReady + kKSlots /* 2 */,
+                       bVFull = bKEmpty + kKSlots, bVReady = bVFull + kVSlots /* L */,
+                       bVEmpty = bVReady + kVSlots /* 2 */, bSFull = bVEmpty + kVSlots /* 2 */,
+                       bSEmpty = bSFull + 2 /* L */, bPReady = bSEmpty + 2 /* L */, bPvDone = bPReady + 1 /* 2 */,
+                       bQFull = bPvDone + 1 /* L */, bQLocal = bQFull + 1, bQEmpty = bQLocal + 1 /* 2 */,
+                       bOFree = bQEmpty + 1 /* L */, bInfoFull = bOFree + 1, bInfoEmpty = bInfoFull + kInfos,
+                       bDrain = bInfoEmpty + kInfos, kNumB = bDrain + 2;
   static constexpr int kMiscOff = kBarOff + kNumB * 8;             // TMEM base, abort flag
   static constexpr int kSmem = kMiscOff + 16;
   static_assert(kSmem <= 232448, "shared memory budget");
@@ -110,7 +120,7 @@ struct Part {                 // the unit cut at the end of a slice: its first r
 
 struct TreeParams {
   CUtensorMap chunk;          // the pool's rows, boxes of 128 bytes by `box` rows
-  CUtensorMap pair;           // the same by whole 128-byte chunks, boxes of two chunks of 64 rows (box 64)
+  CUtensorMap k_box, v_box;   // the same by whole 128-byte chunks, boxes of a fill's chunks by 64 rows (box 64)
   LatentTreeArgs a;
   int box, box_shift;         // rows of a box: 8, 16, 32 or 64 (0: cp.async), and log2 of them
   int slices;
@@ -157,6 +167,35 @@ __device__ __forceinline__ void commit_pair(uint32_t bar) {
 __device__ __forceinline__ void mbar_arrive_pair(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
+
+// Copies of a CTA of the pair into its own shared memory that complete on a barrier of the first CTA.
+__device__ __forceinline__ void tma_row_pair(uint32_t dst, const CUtensorMap* map, int x, int r, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
+      " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(r), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void tma_box3_pair(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
+      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
+      : "memory");
+}
+
+// A ring whose length is not known at compile time (see spa_latent_ring.h).
+struct Slots {
+  int n, slot = 0;
+  uint32_t parity = 0;
+  __device__ explicit Slots(int count) : n(count) {}
+  __device__ __forceinline__ void next() {
+    if (++slot == n) {
+      slot = 0;
+      parity ^= 1;
+    }
+  }
+};
 
 // A sequence as the schedule sees it: its tokens and entries, units and tiles of a unit (no units: none to do).
 struct Seq {
@@ -286,10 +325,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const auto lead_bar = [&](int i) { return mapa_cluster(BAR(i), 0); };   // in the first CTA
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < C::kSlots; ++i) {
-      mbar_init(BAR(C::bFull + i), p.box ? 1 : 128);
-      mbar_init(BAR(C::bReady + i), 2);
-      mbar_init(BAR(C::bEmpty + i), 1);
+    for (int i = 0; i < C::kKSlots; ++i) {
+      mbar_init(BAR(C::bKFull + i), 128);
+      mbar_init(BAR(C::bKReady + i), p.box ? 1 : 2);     // armed by the first CTA's loader, or both's warps 10
+      mbar_init(BAR(C::bKEmpty + i), 1);
+    }
+    for (int i = 0; i < C::kVSlots; ++i) {
+      mbar_init(BAR(C::bVFull + i), p.box ? 1 : 128);
+      mbar_init(BAR(C::bVReady + i), 2);
+      mbar_init(BAR(C::bVEmpty + i), 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(BAR(C::bSFull + i), 1);
@@ -303,9 +347,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     mbar_init(BAR(C::bOFree), 16);
     for (int i = 0; i < kInfos; ++i) {
       mbar_init(BAR(C::bInfoFull + i), 1);
-      mbar_init(BAR(C::bInfoEmpty + i), rank == 0 ? 14 : 13);   // softmax, cleaning and q warps, MMA warp
+      mbar_init(BAR(C::bInfoEmpty + i), rank == 0 ? 15 : 13);   // softmax, cleaning and q warps, MMA warps
     }
     mbar_init(BAR(C::bDrain), 1);
+    mbar_init(BAR(C::bDrain + 1), 1);
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -328,10 +373,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const int L = a.pool.L, W = a.pool.row_bytes;
   const int n_chunks = (W + 127) >> 7;                         // of a row
   const int n_half = ((L + C::kCw - 1) / C::kCw + 1) >> 1;     // chunks of values a CTA brings
-  const int k_fills = (n_chunks + 1) >> 1, v_pairs = (n_half + 1) >> 1;
-
-  // The fills in order, for the roles that follow them: K of tile k, V of tile k - 1 (before it, where tile k
-  // is the first of a unit).  `k_part(k)` and `v_part(k)` return false to give up.
+  const int k_fills = (n_chunks + kKFill - 1) / kKFill, v_pairs = (n_half + 1) >> 1;
+  Slots ks(C::kKSlots), vs(p.box || kFp8 ? C::kVSlots : C::kVSlots - 1);   // where a role is in the rings
+  // (lanes that copy boxes: chunk of the fill and box of the group)
+  const int per_group = kGroup >> p.box_shift, my_c = lane >> (6 - p.box_shift), my_box = lane & (per_group - 1);
+  const uint32_t my_off = my_c * kChunk + ((my_box << p.box_shift) << 7);
   if (warp == 9) {
     // ================================ schedule and loads ==================================
     int top = 0, s0 = 0;
@@ -484,41 +530,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       ++it_j;
     };
     const int total_rows = (int)(a.pool.num_blocks * a.pool.ps);
-    Ring<C::kSlots> at;
     long long fills = 0;
     bool ok = true;
-    // A fill: chunks c0, c0 + 1 (below c_end) of entry group `grp` of the tile whose boxes begin at `rows`.  Lane
-    // (chunk, box of the group) copies one box; with boxes of 64 rows one lane both chunks.
-    const int per_group = kGroup >> p.box_shift, my_c = lane >> (6 - p.box_shift), my_box = lane & (per_group - 1);
-    const uint32_t my_off = my_c * kChunk + ((my_box << p.box_shift) << 7);
     const bool lead = elect_one();
-    const auto fill = [&](int rows, int grp, int c0, int c_end) -> bool {
-      if (!warp_wait(BAR(C::bEmpty + at.slot), at.parity ^ 1, abort_flag)) return false;
-      const uint32_t dst = sb + C::kRingOff + at.slot * kFill, full = BAR(C::bFull + at.slot);
-      const int n = min(2, c_end - c0);
-      const int row = __shfl_sync(0xffffffffu, rows, grp * per_group + my_box);
-      if (lead) mbar_arrive_expect_tx(full, (uint32_t)(n * kChunk));
-      if (p.box == kGroup && n == 2 && (c0 + 2) * 128 <= W) {
-        if (lead) tma_box3(dst, &p.pair, 0, row, c0, full);
-      } else {
+    // K of a tile: this CTA's 64 entries, of whose boxes this lane's begins at `row`
+    const auto k_part = [&](int row) {
+      for (int f = 0; f < k_fills; ++f) {
+        if (!(ok = warp_wait(BAR(C::bKEmpty + ks.slot), ks.parity ^ 1, abort_flag))) return;
+        const uint32_t dst = sb + C::kKOff + ks.slot * (kKFill * kChunk), ready = lead_bar(C::bKReady + ks.slot);
+        const int c0 = f * kKFill, n = min(kKFill, n_chunks - c0);
+        if (lead && rank == 0) mbar_arrive_expect_tx(BAR(C::bKReady + ks.slot), (uint32_t)(2 * n * kChunk));
+        if (p.box == kGroup && (c0 + kKFill) * 128 <= W) {
+          if (lead) tma_box3_pair(dst, &p.k_box, 0, row, c0, ready);
+        } else if (my_c < n) {
+          tma_row_pair(dst + my_off, &p.chunk, (c0 + my_c) * 128, row, ready);
+        }
         __syncwarp();
-        if (my_c < n) tma_row(dst + my_off, &p.chunk, (c0 + my_c) * 128, row, full);
+        ++fills;
+        ks.next();
       }
-      __syncwarp();
-      ++fills;
-      at.next();
-      return true;
-    };
-    const auto k_part = [&](int rows) {
-      for (int f = 0; f < k_fills && ok; ++f) ok = fill(rows, rank, 2 * f, n_chunks);
-    };
-    const auto v_part = [&](int rows) {
-      for (int grp = 0; grp < 2; ++grp)
-        for (int f = 0; f < v_pairs && ok; ++f)
-          ok = fill(rows, grp, rank * n_half + 2 * f, rank * n_half + n_half);
     };
     Tile nxt = {}, x = {};
-    int box_rows = 0, prev_rows = 0;
+    int box_rows = 0;
     next_tile(nxt);
     for (int k = 0; ok; ++k) {
       x = nxt;
@@ -586,7 +619,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         break;
       }
-      if (!p.box) {
+      if (p.box) {
+        if (lane < 16) info.boxes[lane] = box_rows;
+      } else {
 #pragma unroll
         for (int e = 0; e < 4; ++e)
           reinterpret_cast<int*>(sm + C::kRowOff)[ri * kTile + lane + 32 * e] = rows4[e];
@@ -629,49 +664,114 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       __threadfence_block();
       __syncwarp();
       if (lane == 0) mbar_arrive(BAR(C::bInfoFull + ri));
-      if (p.box) {
-        const bool first = x.flags & kFirst;
-        if (first && k > 0) v_part(prev_rows);
-        k_part(box_rows);
-        if (!first) v_part(prev_rows);
-        prev_rows = box_rows;
-        if (x.flags & kFinal) v_part(box_rows);
-      }
+      if (p.box) k_part(__shfl_sync(0xffffffffu, box_rows, rank * per_group + my_box));
       if (x.flags & kFinal) break;
     }
     if (lane == 0) {
       if (rank == 0) p.cut[slice] = cut;
-      // copies in flight must land before the CTA ends (at once after a normal run)
-      for (long long f = max(0LL, fills - C::kSlots); f < fills; ++f)
-        mbar_wait_drain(BAR(C::bFull + (int)(f % C::kSlots)), (uint32_t)((f / C::kSlots) & 1));
+      // (a slot is free again only after its copies have landed: the last fills' copies are seen by the MMAs, or,
+      // where those gave up, here)
+      if (rank == 0)
+        for (long long f = max(0LL, fills - C::kKSlots); f < fills; ++f)
+          mbar_wait_drain(BAR(C::bKReady + (int)(f % C::kKSlots)), (uint32_t)((f / C::kKSlots) & 1));
     }
     __syncwarp();
   } else if (warp == 8) {
-    // ================================= MMAs ==============================================
+    // ================================= MMAs of S ==========================================
     if (rank == 0) {
       const uint32_t idS = kFp8 ? idesc_e4m3(128, 128, 0, 0) : idesc_bf16(128, 128, 0, 0);
-      // (A of the value product: P in bf16, or in e5m2)
-      const auto idO = [&](int n) { return kFp8 ? idesc_e4m3(128, n, 0, 1) | (1u << 7) : idesc_bf16(128, n, 0, 1); };
-      const uint64_t dq = sdesc(sb + C::kQOff, 16, 1024), dp = sdesc(sb + C::kPOff, 16, 1024);
-      const uint64_t dk0 = sdesc(sb + C::kRingOff, 16, 1024), dv0 = sdesc(sb + C::kRingOff, kChunk, 1024);
+      const uint64_t dq = sdesc(sb + C::kQOff, 16, 1024), dk0 = sdesc(sb + C::kKOff, 16, 1024);
+      constexpr uint32_t kQChunk = (kFp8 ? 2 : 1) * kChunk;
       const bool lead = elect_one();
-      Ring<C::kSlots> at;
-      uint32_t units = 0;                        // begun
-      bool o_first = true;                       // of the tile whose PV comes next
-      bool ok = true;
-      const auto pv = [&](int k) {               // O of tile k
-        ok = ok && warp_wait(BAR(C::bPReady), (uint32_t)(k & 1), abort_flag);
-        if (ok && o_first && units > 1) ok = warp_wait(BAR(C::bOFree), (units - 2) & 1, abort_flag);
+      uint32_t units = 0;
+      for (int k = 0;; ++k) {
+        const int ri = k % kInfos, sn = k & 1;
+        if (!warp_wait(BAR(C::bInfoFull + ri), (uint32_t)((k / kInfos) & 1), abort_flag)) break;
+        const int flags = (int)warp_uniform(*reinterpret_cast<volatile int*>(&infos[ri].flags));
+        if (lead) mbar_arrive(BAR(C::bInfoEmpty + ri));
+        if (flags & kEnd) break;
+        if ((flags & kFirst) && !warp_wait(BAR(C::bQFull), units++ & 1, abort_flag)) break;
+        if (k >= 2 && !warp_wait(BAR(C::bSEmpty + sn), (uint32_t)(((k >> 1) & 1) ^ 1), abort_flag)) break;
+        const uint32_t dS = tmem + kSCol + sn * 64;
+        uint64_t q = dq;
+        uint32_t acc = 0;
+        int left = W;                            // bytes of the row to come
+        bool ok = true;
+        for (int f = 0; f < k_fills; ++f) {
+          if (!(ok = warp_wait(BAR(C::bKReady + ks.slot), ks.parity, abort_flag))) break;
+          tc_fence_after();
+          if (lead) {
+            // (the loops that issue are short: no predicates in whole chunks, not unrolled across them)
+            uint64_t b = desc_add(dk0, ks.slot * (kKFill * kChunk));
+            const int stop = left - kKFill * 128;
+#pragma unroll 1
+            for (; left > stop && left > 0; left -= 128) {
+              mma_pair<kFp8>(dS, q, b, idS, acc);
+              if (kFp8) mma_pair<kFp8>(dS, desc_add(q, kChunk), b, idS, 1u);
+              acc = 1u;
+              if (left > 96) {
+#pragma unroll
+                for (int st = 1; st < 4; ++st) {
+                  mma_pair<kFp8>(dS, desc_add(q, st * 32), desc_add(b, st * 32), idS, 1u);
+                  if (kFp8) mma_pair<kFp8>(dS, desc_add(q, kChunk + st * 32), desc_add(b, st * 32), idS, 1u);
+                }
+              } else {
+#pragma unroll 1
+                for (int st = 1; st * 32 < left; ++st) {
+                  mma_pair<kFp8>(dS, desc_add(q, st * 32), desc_add(b, st * 32), idS, 1u);
+                  if (kFp8) mma_pair<kFp8>(dS, desc_add(q, kChunk + st * 32), desc_add(b, st * 32), idS, 1u);
+                }
+              }
+              b = desc_add(b, kChunk);
+              q = desc_add(q, kQChunk);
+            }
+            commit_pair(BAR(C::bKEmpty + ks.slot));
+            if (f == k_fills - 1) {
+              commit_pair(BAR(C::bSFull + sn));
+              if (flags & kLast) commit_pair(BAR(C::bQEmpty));
+            }
+          }
+          __syncwarp();
+          ks.next();
+        }
+        if (!ok || (flags & kFinal)) break;
+      }
+      // nothing may still write TMEM when it is released
+      if (lead) {
+        asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(BAR(C::bDrain))
+                     : "memory");
+        mbar_wait_drain(BAR(C::bDrain), 0);
+      }
+      __syncwarp();
+    }
+  } else if (warp == 11) {
+    // ================================= MMAs of O ==========================================
+    if (rank == 0) {
+      // (A: P in bf16, or in e5m2)
+      const auto idO = [&](int n) { return kFp8 ? idesc_e4m3(128, n, 0, 1) | (1u << 7) : idesc_bf16(128, n, 0, 1); };
+      const uint64_t dp = sdesc(sb + C::kPOff, 16, 1024), dv0 = sdesc(sb + C::kVOff, kChunk, 1024);
+      const bool lead = elect_one();
+      uint32_t units = 0;
+      for (int k = 0;; ++k) {
+        const int ri = k % kInfos;
+        if (!warp_wait(BAR(C::bInfoFull + ri), (uint32_t)((k / kInfos) & 1), abort_flag)) break;
+        const int flags = (int)warp_uniform(*reinterpret_cast<volatile int*>(&infos[ri].flags));
+        if (lead) mbar_arrive(BAR(C::bInfoEmpty + ri));
+        if (flags & kEnd) break;
+        if (!warp_wait(BAR(C::bPReady), (uint32_t)(k & 1), abort_flag)) break;
+        const bool first = flags & kFirst;
+        // (O of the unit before has been stored)
+        if (first && units++ > 0 && !warp_wait(BAR(C::bOFree), units & 1, abort_flag)) break;
+        bool ok = true;
         for (int grp = 0; grp < 2 && ok; ++grp) {
+          const uint64_t pa = desc_add(dp, grp * (kFp8 ? 64 : kChunk));
+          const uint32_t acc = !(first && grp == 0);
           for (int f = 0; f < v_pairs; ++f) {
-            ok = warp_wait(BAR(C::bReady + at.slot), at.parity, abort_flag);
-            if (!ok) break;
+            if (!(ok = warp_wait(BAR(C::bVReady + vs.slot), vs.parity, abort_flag))) break;
             tc_fence_after();
             if (lead) {
-              const int n = min(2, n_half - 2 * f);       // chunks of the fill
-              uint64_t b = desc_add(dv0, at.slot * kFill);
-              const uint64_t pa = desc_add(dp, grp * (kFp8 ? 64 : kChunk));
-              const uint32_t acc = !(o_first && grp == 0);
+              const int n = min(kVFill, n_half - kVFill * f);      // chunks of the fill
+              uint64_t b = desc_add(dv0, vs.slot * (kVFill * kChunk));
               if (kFp8) {
                 uint32_t d = tmem + f * 256;
 #pragma unroll 1
@@ -686,140 +786,78 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                   d += 128;
                 }
               } else {
-                const uint32_t id = idO(n * 128);
+                const uint32_t id = n == 2 ? idO(256) : idO(128);
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk)            // 16 entries a step
                   mma_pair<kFp8>(tmem + f * 128, desc_add(pa, kk * 32), desc_add(b, kk * 2048), id, kk ? 1u : acc);
               }
-              commit_pair(BAR(C::bEmpty + at.slot));
+              commit_pair(BAR(C::bVEmpty + vs.slot));
+              if (grp == 1 && f == v_pairs - 1) commit_pair(BAR(C::bPvDone));
             }
             __syncwarp();
-            at.next();
+            vs.next();
           }
         }
-        if (ok && lead) commit_pair(BAR(C::bPvDone));
-        __syncwarp();
-      };
-      for (int k = 0; ok; ++k) {
-        const int ri = k % kInfos;
-        if (!warp_wait(BAR(C::bInfoFull + ri), (uint32_t)((k / kInfos) & 1), abort_flag)) break;
-        const int flags = (int)warp_uniform(*reinterpret_cast<volatile int*>(&infos[ri].flags));
-        __syncwarp();
-        if (lane == 0) mbar_arrive(BAR(C::bInfoEmpty + ri));
-        if (flags & kEnd) break;
-        const bool first = flags & kFirst;
-        if (first) {
-          if (k > 0) pv(k - 1);
-          if (!ok) break;
-          ++units;
-          ok = warp_wait(BAR(C::bQFull), (units - 1) & 1, abort_flag);
-        }
-        // S of tile k
-        const int sn = k & 1;
-        if (ok && k >= 2) ok = warp_wait(BAR(C::bSEmpty + sn), (uint32_t)(((k >> 1) & 1) ^ 1), abort_flag);
-        for (int f = 0; f < k_fills && ok; ++f) {
-          ok = warp_wait(BAR(C::bReady + at.slot), at.parity, abort_flag);
-          if (!ok) break;
-          tc_fence_after();
-          if (lead) {
-            const uint32_t dS = tmem + kSCol + sn * 64;
-            // (the loops that issue are short: no predicates in whole chunks, not unrolled across them)
-            const int n = min(2, n_chunks - 2 * f);
-            uint64_t b = desc_add(dk0, at.slot * kFill), q = desc_add(dq, f * (kFp8 ? 4 : 2) * kChunk);
-            uint32_t acc = f != 0;
-#pragma unroll 1
-            for (int c = 0; c < n; ++c) {
-              const int steps = (W - (2 * f + c) * 128 + 31) >> 5;       // 32-byte steps left in the row
-              mma_pair<kFp8>(dS, q, b, idS, acc);
-              if (kFp8) mma_pair<kFp8>(dS, desc_add(q, kChunk), b, idS, 1u);
-              acc = 1u;
-              if (steps >= 4) {
-#pragma unroll
-                for (int st = 1; st < 4; ++st) {
-                  mma_pair<kFp8>(dS, desc_add(q, st * 32), desc_add(b, st * 32), idS, 1u);
-                  if (kFp8) mma_pair<kFp8>(dS, desc_add(q, kChunk + st * 32), desc_add(b, st * 32), idS, 1u);
-                }
-              } else {
-#pragma unroll 1
-                for (int st = 1; st < steps; ++st) {
-                  mma_pair<kFp8>(dS, desc_add(q, st * 32), desc_add(b, st * 32), idS, 1u);
-                  if (kFp8) mma_pair<kFp8>(dS, desc_add(q, kChunk + st * 32), desc_add(b, st * 32), idS, 1u);
-                }
-              }
-              b = desc_add(b, kChunk);
-              q = desc_add(q, (kFp8 ? 2 : 1) * kChunk);
-            }
-            commit_pair(BAR(C::bEmpty + at.slot));
-          }
-          __syncwarp();
-          at.next();
-        }
-        if (!ok) break;
-        if (lead) {
-          commit_pair(BAR(C::bSFull + sn));
-          if (flags & kLast) commit_pair(BAR(C::bQEmpty));
-        }
-        __syncwarp();
-        if (!first) pv(k - 1);
-        o_first = first;
-        if (flags & kFinal) {
-          pv(k);
-          break;
-        }
+        if (!ok || (flags & kFinal)) break;
       }
-      // nothing may still write TMEM when it is released
       if (lead) {
-        asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(BAR(C::bDrain))
+        asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(BAR(C::bDrain + 1))
                      : "memory");
-        mbar_wait_drain(BAR(C::bDrain), 0);
+        mbar_wait_drain(BAR(C::bDrain + 1), 0);
       }
       __syncwarp();
     }
   } else if (warp == 10) {
     // ===================== every fill as it lands: cleaned, handed on =====================
-    Ring<C::kSlots> at;
     bool ok = true;
-    const auto hand_on = [&](bool clean, const typename C::Info& info, int grp, int n) {
-      ok = warp_wait(BAR(C::bFull + at.slot), at.parity, abort_flag);
-      if (!ok) return;
-      if (clean) {
-        uint8_t* src = sm + C::kRingOff + at.slot * kFill;
-        const uint32_t lo = info.valid[2 * grp], hi = info.valid[2 * grp + 1];
-        const int ctx = max(-info.rel - grp * kGroup, 0);      // the first row that not all may see
-        // from the first row that needs it: two a step, a half-warp each, four steps' loads in flight
-        const int gone = ~lo ? __ffs(~lo) - 1 : ~hi ? 31 + __ffs(~hi) : kGroup;
-        const int c = (lane >> 3) & 1, half = lane >> 4;
-        for (int r0 = min(ctx, gone) & ~1; r0 < kGroup; r0 += 8) {
-          uint4 old[4];
-          uint4* at_row[4];
-          bool exists[4];
-#pragma unroll
-          for (int z = 0; z < 4; ++z) {
-            const int r = min(r0 + 2 * z + half, kGroup - 1);
-            exists[z] = ((r < 32 ? lo >> r : hi >> (r - 32)) & 1u) != 0;
-            at_row[z] = reinterpret_cast<uint4*>(src + c * kChunk + r * 128) + (lane & 7);
-            old[z] = *at_row[z];
-          }
-#pragma unroll
-          for (int z = 0; z < 4; ++z) {
-            const uint4 now = exists[z] ? finite_only<kFp8>(old[z]) : make_uint4(0, 0, 0, 0);
-            if (c < n && (now.x != old[z].x || now.y != old[z].y || now.z != old[z].z || now.w != old[z].w))
-              *at_row[z] = now;
-          }
-        }
+    const auto k_part = [&]() {                  // (cp.async)
+      for (int f = 0; f < k_fills && ok; ++f) {
+        if (!(ok = warp_wait(BAR(C::bKFull + ks.slot), ks.parity, abort_flag))) return;
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_pair(lead_bar(C::bKReady + ks.slot));
+        ks.next();
       }
-      if (clean || !p.box) fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive_pair(lead_bar(C::bReady + at.slot));
-      at.next();
     };
     const auto v_part = [&](int k) {
       const int ri = k % kInfos;
       const typename C::Info& info = infos[ri];
       const bool clean = info.flags & kClean;
-      for (int grp = 0; grp < 2 && ok; ++grp)
-        for (int f = 0; f < v_pairs && ok; ++f) hand_on(clean, info, grp, min(2, n_half - 2 * f));
-      __syncwarp();
+      for (int grp = 0; grp < 2; ++grp)
+        for (int f = 0; f < v_pairs; ++f) {
+          if (!(ok = warp_wait(BAR(C::bVFull + vs.slot), vs.parity, abort_flag))) return;
+          if (clean) {
+            const int n = min(kVFill, n_half - kVFill * f);
+            uint8_t* src = sm + C::kVOff + vs.slot * (kVFill * kChunk);
+            const uint32_t lo = info.valid[2 * grp], hi = info.valid[2 * grp + 1];
+            const int ctx = max(-info.rel - grp * kGroup, 0);      // the first row that not all may see
+            // from the first row that needs it: two a step, a half-warp each, four steps' loads in flight
+            const int gone = ~lo ? __ffs(~lo) - 1 : ~hi ? 31 + __ffs(~hi) : kGroup;
+            const int c = (lane >> 3) & 1, half = lane >> 4;
+            for (int r0 = min(ctx, gone) & ~1; r0 < kGroup; r0 += 8) {
+              uint4 old[4];
+              uint4* at_row[4];
+              bool exists[4];
+#pragma unroll
+              for (int z = 0; z < 4; ++z) {
+                const int r = min(r0 + 2 * z + half, kGroup - 1);
+                exists[z] = ((r < 32 ? lo >> r : hi >> (r - 32)) & 1u) != 0;
+                at_row[z] = reinterpret_cast<uint4*>(src + c * kChunk + r * 128) + (lane & 7);
+                old[z] = *at_row[z];
+              }
+#pragma unroll
+              for (int z = 0; z < 4; ++z) {
+                const uint4 now = exists[z] ? finite_only<kFp8>(old[z]) : make_uint4(0, 0, 0, 0);
+                if (c < n && (now.x != old[z].x || now.y != old[z].y || now.z != old[z].z || now.w != old[z].w))
+                  *at_row[z] = now;
+              }
+            }
+          }
+          if (clean || !p.box) fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_pair(lead_bar(C::bVReady + vs.slot));
+          vs.next();
+        }
       if (lane == 0) mbar_arrive(BAR(C::bInfoEmpty + ri));
     };
     for (int k = 0; ok; ++k) {
@@ -827,26 +865,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (!warp_wait(BAR(C::bInfoFull + ri), (uint32_t)((k / kInfos) & 1), abort_flag)) break;
       const int flags = *reinterpret_cast<volatile int*>(&infos[ri].flags);
       if (flags & kEnd) break;
-      const bool first = flags & kFirst;
-      if (first && k > 0) v_part(k - 1);
-      for (int f = 0; f < k_fills && ok; ++f) hand_on(false, infos[ri], 0, 2);
-      if (!first && ok) v_part(k - 1);
-      if ((flags & kFinal) && ok) v_part(k);
+      if (p.box) {
+        v_part(k);
+      } else {                                   // (in the order of the copies)
+        k_part();
+        if (k > 0 && ok) v_part(k - 1);
+        if ((flags & kFinal) && ok) v_part(k);
+      }
       if (flags & kFinal) break;
     }
-  } else if (warp > 10) {
-    // ======================= q of every unit; rows by cp.async ============================
-    const int tid = threadIdx.x - 11 * 32;
-    Ring<C::kSlots> at;
+  } else if (warp > 11) {
+    // ============ q of every unit; copies of V (warp 12), or all rows by cp.async ==========
+    const int tid = threadIdx.x - 12 * 32;
+    const bool lead = elect_one();
     uint32_t units = 0;
+    long long fills = 0;
     bool ok = true;
-    // a fill: chunks c0, c0 + 1 (below c_end) of entry group grp of the tile of info ri
-    const auto fill = [&](int ri, int grp, int c0, int c_end) {
-      if (!ok) return;
+    // cp.async of a fill: n chunks from c0 on of entry group grp of the tile of info ri
+    const auto fill = [&](int ri, int grp, uint32_t dst0, uint32_t full, int c0, int n) {
       const int* rows = reinterpret_cast<const int*>(sm + C::kRowOff) + ri * kTile + grp * kGroup;
-      const int jj = tid & 7, r0 = tid >> 3, n = min(2, c_end - c0);
-      if (!(ok = warp_wait(BAR(C::bEmpty + at.slot), at.parity ^ 1, abort_flag))) return;
-      const uint32_t dst = sb + C::kRingOff + at.slot * kFill + r0 * 128 + ((jj ^ (r0 & 7)) << 4);
+      const int jj = tid & 7, r0 = tid >> 3;
+      const uint32_t dst = dst0 + r0 * 128 + ((jj ^ (r0 & 7)) << 4);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int row = rows[r0 + 16 * i];
@@ -857,14 +896,41 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           cp_async_16(dst + c * kChunk + i * 2048, has ? src + col : a.pool.rows, has ? 16u : 0u);
         }
       }
-      cp_async_arrive_noinc(BAR(C::bFull + at.slot));
-      at.next();
+      cp_async_arrive_noinc(full);
+    };
+    const auto k_part = [&](int ri) {
+      for (int f = 0; f < k_fills && ok; ++f) {
+        if (!(ok = warp_wait(BAR(C::bKEmpty + ks.slot), ks.parity ^ 1, abort_flag))) return;
+        fill(ri, rank, sb + C::kKOff + ks.slot * (kKFill * kChunk), BAR(C::bKFull + ks.slot), f * kKFill,
+             min(kKFill, n_chunks - f * kKFill));
+        ks.next();
+      }
     };
     const auto v_part = [&](int k) {
       const int ri = k % kInfos;
-      if (!p.box)
-        for (int grp = 0; grp < 2; ++grp)
-          for (int f = 0; f < v_pairs; ++f) fill(ri, grp, rank * n_half + 2 * f, rank * n_half + n_half);
+      if (!p.box || warp == 12) {
+        for (int grp = 0; grp < 2; ++grp) {
+          const int row = p.box ? infos[ri].boxes[grp * per_group + my_box] : 0;
+          for (int f = 0; f < v_pairs; ++f) {
+            if (!(ok = warp_wait(BAR(C::bVEmpty + vs.slot), vs.parity ^ 1, abort_flag))) return;
+            const uint32_t dst = sb + C::kVOff + vs.slot * (kVFill * kChunk), full = BAR(C::bVFull + vs.slot);
+            const int c0 = rank * n_half + f * kVFill, n = min(kVFill, n_half - f * kVFill);
+            if (!p.box) {
+              fill(ri, grp, dst, full, c0, n);
+            } else {
+              if (lead) mbar_arrive_expect_tx(full, (uint32_t)(n * kChunk));
+              if (p.box == kGroup && n == kVFill && (c0 + kVFill) * 128 <= W) {
+                if (lead) tma_box3(dst, &p.v_box, 0, row, c0, full);
+              } else if (my_c < n) {
+                tma_row(dst + my_off, &p.chunk, (c0 + my_c) * 128, row, full);
+              }
+              __syncwarp();
+              ++fills;
+            }
+            vs.next();
+          }
+        }
+      }
       __syncwarp();
       if (lane == 0) mbar_arrive(BAR(C::bInfoEmpty + ri));
     };
@@ -875,15 +941,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const int flags = info.flags;
       if (flags & kEnd) break;
       const bool first = flags & kFirst;
-      if (first && k > 0) v_part(k - 1);
-      if (!p.box)
-        for (int f = 0; f < k_fills; ++f) fill(ri, rank, 2 * f, n_chunks);
-      if (!first) v_part(k - 1);
+      if (!p.box) {
+        k_part(ri);
+        if (k > 0 && ok) v_part(k - 1);
+      }
       if (first && ok) {
         const uint32_t ph = (units & 1) ^ 1;
         ++units;
         if (kFp8) {
-          if (warp == 11) {
+          if (warp == 12) {
             ok = warp_wait(BAR(C::bQEmpty), ph, abort_flag);
             if (ok && elect_one()) {
               const long long slot = q_slot(info.tok0, a.H, info.seq, info.unit_row / kUnitRows);
@@ -923,14 +989,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           }
         }
       }
-      if ((flags & kFinal) && ok) v_part(k);
+      if ((p.box || (flags & kFinal)) && ok) v_part(k);
       if (flags & kFinal) break;
     }
     cp_async_wait_all();
-    if (kFp8 && warp == 11 && units > 0) {       // (a copy in flight, where the CTA gave up)
-      mbar_wait_drain(BAR(C::bQLocal), (units - 1) & 1);
-      __syncwarp();
+    // copies in flight must land before the CTA ends (at once after a normal run)
+    if (warp == 12 && lane == 0) {
+      if (kFp8 && units > 0) mbar_wait_drain(BAR(C::bQLocal), (units - 1) & 1);
+      for (long long f = max(0LL, fills - vs.n); f < fills; ++f)
+        mbar_wait_drain(BAR(C::bVFull + (int)(f % vs.n)), (uint32_t)((f / vs.n) & 1));
     }
+    __syncwarp();
   } else {
     // ================================ softmax and epilogue ================================
     // TMEM lanes 32 quad ..: rows 32 (quad & 1) .., entry group (of S) or channel half (of O) quad >> 1; this
@@ -954,13 +1023,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       for (int e = 0; e < 4; ++e) own[e] = r[e * kRows + row];
       return ok;
     };
-    for (int k = 0;; ++k) {
+    // A wait that gives up does not leave the loop: every warp reaches every barrier, and all leave together, where
+    // they agree that one of them gave up.
+    int flags = 0;
+    ok = warp_wait(BAR(C::bInfoFull), 0, abort_flag);
+    const bool any = named_bar_and(1, kSoftmax, ok && !(infos[0].flags & kEnd));
+    for (int k = 0; any && !(flags & kFinal); ++k) {
       const int ri = k % kInfos, sn = k & 1;
-      ok = warp_wait(BAR(C::bInfoFull + ri), (uint32_t)((k / kInfos) & 1), abort_flag) && ok;
+      if (k > 0) ok = warp_wait(BAR(C::bInfoFull + ri), (uint32_t)((k / kInfos) & 1), abort_flag) && ok;
       const typename C::Info& info = infos[ri];
-      const int flags = ok ? info.flags : kEnd, slot = info.slot;
-      // (all eight warps agree: where one gave up, they leave together)
-      if (!named_bar_and(1, kSoftmax, ok && !(flags & kEnd))) break;
+      const int slot = info.slot;
+      flags = info.flags;
       const bool first = flags & kFirst, last = flags & kLast;
       const int n_rows = info.rows, first_row = info.first_row;
       uint32_t seen = info.valid[word];
@@ -1038,7 +1111,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       bool grow = false;
       if (!named_bar_and(1, kSoftmax, ok && !(mt > m + C::kTau))) {
         float own[4];
-        exchange(mt, own);
+        if (!exchange(mt, own)) break;           // (all eight warps, or none)
         const float t = fmaxf(fmaxf(own[0], own[1]), fmaxf(own[2], own[3]));
         const float n = t > m + C::kTau ? t : m;
         if (n != m) {
@@ -1128,7 +1201,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (last) {
         // ---- epilogue: denominators, then O ----
         float own[4];
-        exchange(l, own);
+        if (!exchange(l, own)) break;
         const float ls = (own[0] + own[1]) + (own[2] + own[3]);
         // (0: no entry at all.  A NaN among the scores is in the sum, whatever the maximum is.)
         const float inv = ls == 0.f ? 0.f : (kFp8 ? 1.f / kPUnit : 1.f) / ls;
@@ -1170,7 +1243,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive_pair(lead_bar(C::bOFree));
       }
-      if (flags & kFinal) break;
     }
   }
 #undef BAR
@@ -1320,10 +1392,11 @@ cudaError_t launch_latent_tree(const LatentTreeArgs& a, bool fp8, void* workspac
     const unsigned bx[2] = {128, (unsigned)p.box};
     if (!encode_bytes(&p.chunk, a.pool.rows, 2, d, st, bx)) return cudaErrorInvalidValue;
     while (1 << p.box_shift < p.box) ++p.box_shift;
-    if (p.box == kGroup && W >= 256) {
+    if (p.box == kGroup && W >= 128) {
       const unsigned long long d3[3] = {128, d[1], W / 128}, st3[2] = {W, 128};
-      const unsigned bx3[3] = {128, kGroup, 2};
-      if (!encode_bytes(&p.pair, a.pool.rows, 3, d3, st3, bx3)) return cudaErrorInvalidValue;
+      const unsigned kb[3] = {128, kGroup, kKFill}, vb[3] = {128, kGroup, kVFill};
+      if (!encode_bytes(&p.k_box, a.pool.rows, 3, d3, st3, kb) || !encode_bytes(&p.v_box, a.pool.rows, 3, d3, st3, vb))
+        return cudaErrorInvalidValue;
     }
   }
   const long long rows = (long long)a.T * a.H;
