@@ -22,10 +22,11 @@
 //
 //   warps 0-7    softmax: a thread has a row and 32 of a tile's entries; epilogue
 //   warps 8, 11  (of the first CTA) issue the MMAs of S, and those of O
-//   warp 9       schedule, page tables, copies of K, which complete on the first CTA's barrier
+//   warp 9       schedule, page tables
 //   warp 10      sees every fill of V land, cleans it where a tile holds what not all rows may see, and tells the
 //                first CTA
-//   warps 12-15  q of a unit; warp 12 the copies of V.  Where pages are not a multiple of eight entries, all cached
+//   warps 12-15  q of a unit; warp 12 the copies of V, warp 13 those of K, which complete on the first CTA's
+//                barrier.  Where pages are not a multiple of eight entries, all cached
 //                rows by cp.async
 //
 // A role's code runs once a tile, from the second-level instruction cache (some six cycles an instruction), so it is
@@ -124,7 +125,9 @@ struct TreeParams {
   LatentTreeArgs a;
   int box, box_shift;         // rows of a box: 8, 16, 32 or 64 (0: cp.async), and log2 of them
   int slices;
+  // |scale| log2(e); bf16: never 0 (times a masked score's -inf it would be NaN), a scale of 0 is q = 0 instead
   float scale_log2;
+  int q_zero, negate;
   Part* cut;                  // [slices]
   float* lse;                 // [slices][2][128], log2 units
   float* part;                // [slices][2][128][L]
@@ -530,26 +533,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       ++it_j;
     };
     const int total_rows = (int)(a.pool.num_blocks * a.pool.ps);
-    long long fills = 0;
     bool ok = true;
-    const bool lead = elect_one();
-    // K of a tile: this CTA's 64 entries, of whose boxes this lane's begins at `row`
-    const auto k_part = [&](int row) {
-      for (int f = 0; f < k_fills; ++f) {
-        if (!(ok = warp_wait(BAR(C::bKEmpty + ks.slot), ks.parity ^ 1, abort_flag))) return;
-        const uint32_t dst = sb + C::kKOff + ks.slot * (kKFill * kChunk), ready = lead_bar(C::bKReady + ks.slot);
-        const int c0 = f * kKFill, n = min(kKFill, n_chunks - c0);
-        if (lead && rank == 0) mbar_arrive_expect_tx(BAR(C::bKReady + ks.slot), (uint32_t)(2 * n * kChunk));
-        if (p.box == kGroup && (c0 + kKFill) * 128 <= W) {
-          if (lead) tma_box3_pair(dst, &p.k_box, 0, row, c0, ready);
-        } else if (my_c < n) {
-          tma_row_pair(dst + my_off, &p.chunk, (c0 + my_c) * 128, row, ready);
-        }
-        __syncwarp();
-        ++fills;
-        ks.next();
-      }
-    };
     Tile nxt = {}, x = {};
     int box_rows = 0;
     next_tile(nxt);
@@ -664,22 +648,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       __threadfence_block();
       __syncwarp();
       if (lane == 0) mbar_arrive(BAR(C::bInfoFull + ri));
-      if (p.box) k_part(__shfl_sync(0xffffffffu, box_rows, rank * per_group + my_box));
       if (x.flags & kFinal) break;
     }
-    if (lane == 0) {
-      if (rank == 0) p.cut[slice] = cut;
-      // (a slot is free again only after its copies have landed: the last fills' copies are seen by the MMAs, or,
-      // where those gave up, here)
-      if (rank == 0)
-        for (long long f = max(0LL, fills - C::kKSlots); f < fills; ++f)
-          mbar_wait_drain(BAR(C::bKReady + (int)(f % C::kKSlots)), (uint32_t)((f / C::kKSlots) & 1));
-    }
+    if (rank == 0 && lane == 0) p.cut[slice] = cut;
     __syncwarp();
   } else if (warp == 8) {
     // ================================= MMAs of S ==========================================
     if (rank == 0) {
-      const uint32_t idS = kFp8 ? idesc_e4m3(128, 128, 0, 0) : idesc_bf16(128, 128, 0, 0);
+      // (bit 13 negates A: a negative scale)
+      const uint32_t idS = (kFp8 ? idesc_e4m3(128, 128, 0, 0) : idesc_bf16(128, 128, 0, 0)) | (p.negate ? 1u << 13 : 0u);
       const uint64_t dq = sdesc(sb + C::kQOff, 16, 1024), dk0 = sdesc(sb + C::kKOff, 16, 1024);
       constexpr uint32_t kQChunk = (kFp8 ? 2 : 1) * kChunk;
       const bool lead = elect_one();
@@ -693,38 +670,42 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if ((flags & kFirst) && !warp_wait(BAR(C::bQFull), units++ & 1, abort_flag)) break;
         if (k >= 2 && !warp_wait(BAR(C::bSEmpty + sn), (uint32_t)(((k >> 1) & 1) ^ 1), abort_flag)) break;
         const uint32_t dS = tmem + kSCol + sn * 64;
-        uint64_t q = dq;
-        uint32_t acc = 0;
-        int left = W;                            // bytes of the row to come
         bool ok = true;
         for (int f = 0; f < k_fills; ++f) {
           if (!(ok = warp_wait(BAR(C::bKReady + ks.slot), ks.parity, abort_flag))) break;
           tc_fence_after();
-          if (lead) {
-            // (the loops that issue are short: no predicates in whole chunks, not unrolled across them)
-            uint64_t b = desc_add(dk0, ks.slot * (kKFill * kChunk));
-            const int stop = left - kKFill * 128;
-#pragma unroll 1
-            for (; left > stop && left > 0; left -= 128) {
-              mma_pair<kFp8>(dS, q, b, idS, acc);
-              if (kFp8) mma_pair<kFp8>(dS, desc_add(q, kChunk), b, idS, 1u);
-              acc = 1u;
-              if (left > 96) {
+          // (the loops that issue are short, without predicates in whole chunks, and all but the issue itself is the
+          // whole warp's, so that it stays in uniform registers)
+          const uint64_t b0 = desc_add(dk0, ks.slot * (kKFill * kChunk)), q0 = desc_add(dq, f * kKFill * kQChunk);
+          const int n = min(kKFill, n_chunks - f * kKFill), left = W - f * kKFill * 128;   // chunks, bytes to come
+          const uint32_t acc = f != 0;
+          const auto chunk = [&](int c, uint32_t acc0) {
 #pragma unroll
-                for (int st = 1; st < 4; ++st) {
-                  mma_pair<kFp8>(dS, desc_add(q, st * 32), desc_add(b, st * 32), idS, 1u);
-                  if (kFp8) mma_pair<kFp8>(dS, desc_add(q, kChunk + st * 32), desc_add(b, st * 32), idS, 1u);
-                }
-              } else {
-#pragma unroll 1
-                for (int st = 1; st * 32 < left; ++st) {
-                  mma_pair<kFp8>(dS, desc_add(q, st * 32), desc_add(b, st * 32), idS, 1u);
-                  if (kFp8) mma_pair<kFp8>(dS, desc_add(q, kChunk + st * 32), desc_add(b, st * 32), idS, 1u);
+            for (int st = 0; st < 4; ++st) {
+              const uint64_t q = desc_add(q0, c * kQChunk + st * 32), b = desc_add(b0, c * kChunk + st * 32);
+              mma_pair<kFp8>(dS, q, b, idS, st ? 1u : acc0);
+              if (kFp8) mma_pair<kFp8>(dS, desc_add(q, kChunk), b, idS, 1u);
+            }
+          };
+          if (left >= kKFill * 128) {
+            if (lead) {
+              chunk(0, acc);
+              chunk(1, 1u);
+              chunk(2, 1u);
+            }
+          } else {
+            for (int c = 0; c < n; ++c) {
+              const int steps = min(4, (left - c * 128 + 31) >> 5);
+              for (int st = 0; st < steps; ++st) {
+                const uint64_t q = desc_add(q0, c * kQChunk + st * 32), b = desc_add(b0, c * kChunk + st * 32);
+                if (lead) {
+                  mma_pair<kFp8>(dS, q, b, idS, (acc | c | st) != 0);
+                  if (kFp8) mma_pair<kFp8>(dS, desc_add(q, kChunk), b, idS, 1u);
                 }
               }
-              b = desc_add(b, kChunk);
-              q = desc_add(q, kQChunk);
             }
+          }
+          if (lead) {
             commit_pair(BAR(C::bKEmpty + ks.slot));
             if (f == k_fills - 1) {
               commit_pair(BAR(C::bSFull + sn));
@@ -769,21 +750,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           for (int f = 0; f < v_pairs; ++f) {
             if (!(ok = warp_wait(BAR(C::bVReady + vs.slot), vs.parity, abort_flag))) break;
             tc_fence_after();
+            const int n = min(kVFill, n_half - kVFill * f);        // chunks of the fill
+            const uint64_t b = desc_add(dv0, vs.slot * (kVFill * kChunk));
             if (lead) {
-              const int n = min(kVFill, n_half - kVFill * f);      // chunks of the fill
-              uint64_t b = desc_add(dv0, vs.slot * (kVFill * kChunk));
               if (kFp8) {
-                uint32_t d = tmem + f * 256;
 #pragma unroll 1
                 for (int c = 0; c < n; ++c) {             // 128 channels of each CTA
+                  const uint64_t bc = desc_add(b, c * kChunk);
+                  const uint32_t d = tmem + f * 256 + c * 128;
 #pragma unroll
                   for (int kk = 0; kk < 2; ++kk) {        // 32 entries a step
-                    mma_pair<kFp8>(d, desc_add(pa, kk * 32), desc_add(b, kk * 4096), idO(256), kk ? 1u : acc);
-                    mma_pair<kFp8>(d, desc_add(pa, kChunk + kk * 32), desc_add(b, kk * 4096), idO(256), 1u);
-                    mma_pair<kFp8>(d, desc_add(pa, 2 * kChunk + kk * 32), desc_add(b, kk * 4096), idO(256), 1u);
+                    mma_pair<kFp8>(d, desc_add(pa, kk * 32), desc_add(bc, kk * 4096), idO(256), kk ? 1u : acc);
+                    mma_pair<kFp8>(d, desc_add(pa, kChunk + kk * 32), desc_add(bc, kk * 4096), idO(256), 1u);
+                    mma_pair<kFp8>(d, desc_add(pa, 2 * kChunk + kk * 32), desc_add(bc, kk * 4096), idO(256), 1u);
                   }
-                  b = desc_add(b, kChunk);
-                  d += 128;
                 }
               } else {
                 const uint32_t id = n == 2 ? idO(256) : idO(128);
@@ -875,7 +855,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (flags & kFinal) break;
     }
   } else if (warp > 11) {
-    // ============ q of every unit; copies of V (warp 12), or all rows by cp.async ==========
+    // ======= q of every unit; copies of V (warp 12) and K (13), or all rows by cp.async =====
     const int tid = threadIdx.x - 12 * 32;
     const bool lead = elect_one();
     uint32_t units = 0;
@@ -898,9 +878,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
       cp_async_arrive_noinc(full);
     };
+    // K of a tile: this CTA's 64 entries
     const auto k_part = [&](int ri) {
-      for (int f = 0; f < k_fills && ok; ++f) {
+      const int row = p.box ? infos[ri].boxes[rank * per_group + my_box] : 0;
+      for (int f = 0; f < k_fills; ++f) {
         if (!(ok = warp_wait(BAR(C::bKEmpty + ks.slot), ks.parity ^ 1, abort_flag))) return;
+        if (p.box) {
+          const uint32_t dst = sb + C::kKOff + ks.slot * (kKFill * kChunk), ready = lead_bar(C::bKReady + ks.slot);
+          const int c0 = f * kKFill, n = min(kKFill, n_chunks - c0);
+          if (lead && rank == 0) mbar_arrive_expect_tx(BAR(C::bKReady + ks.slot), (uint32_t)(2 * n * kChunk));
+          if (p.box == kGroup && (c0 + kKFill) * 128 <= W) {
+            if (lead) tma_box3_pair(dst, &p.k_box, 0, row, c0, ready);
+          } else if (my_c < n) {
+            tma_row_pair(dst + my_off, &p.chunk, (c0 + my_c) * 128, row, ready);
+          }
+          __syncwarp();
+          ++fills;
+          ks.next();
+          continue;
+        }
         fill(ri, rank, sb + C::kKOff + ks.slot * (kKFill * kChunk), BAR(C::bKFull + ks.slot), f * kKFill,
              min(kKFill, n_chunks - f * kKFill));
         ks.next();
@@ -944,6 +940,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (!p.box) {
         k_part(ri);
         if (k > 0 && ok) v_part(k - 1);
+      } else if (warp == 13) {
+        k_part(ri);
       }
       if (first && ok) {
         const uint32_t ph = (units & 1) ^ 1;
@@ -970,7 +968,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll 1
             for (int i = 0; i < 4; ++i) {
               const int r = (tid >> 3) + 16 * i, ur = rank * kRows + r;
-              const bool has = ur < info.rows;
+              const bool has = ur < info.rows && !p.q_zero;
               const int sr = info.unit_row + (has ? ur : 0);
               const long long t = info.tok0 + sr / a.H, h = sr % a.H;
               const uint8_t *ql = a.q_latent + t * a.ql_st + h * a.ql_sh, *qr = a.q_rope + t * a.qr_st + h * a.qr_sh;
@@ -999,6 +997,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       for (long long f = max(0LL, fills - vs.n); f < fills; ++f)
         mbar_wait_drain(BAR(C::bVFull + (int)(f % vs.n)), (uint32_t)((f / vs.n) & 1));
     }
+    if (warp == 13 && lane == 0 && rank == 0)    // (both CTAs' copies of K complete here)
+      for (long long f = max(0LL, fills - C::kKSlots); f < fills; ++f)
+        mbar_wait_drain(BAR(C::bKReady + (int)(f % C::kKSlots)), (uint32_t)((f / C::kKSlots) & 1));
     __syncwarp();
   } else {
     // ================================ softmax and epilogue ================================
@@ -1095,8 +1096,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           }
         }
       } else {
-#pragma unroll
-        for (int j = 0; j < 32; ++j) x[j] *= arg;
         if (seen != 0xffffffffu) {
 #pragma unroll
           for (int j = 0; j < 32; ++j) x[j] = (seen >> j) & 1u ? x[j] : -INFINITY;
@@ -1104,7 +1103,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int j = 0; j < 32; ++j) mx[j & 3] = fmaxf(mx[j & 3], x[j]);
       }
-      const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+      float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+      if (!kFp8) mt *= arg;                      // (a positive number)
       // Most tiles leave every running maximum within tau of what it was: one vote tells, and the maxima are
       // exchanged only where one has to move.
       float al = 1.f;
@@ -1128,12 +1128,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         for (int j = 0; j < 32; ++j) x[j] = (seen >> j) & 1u ? fast_exp2(fmaf(arg, x[j], -ref)) : 0.f;
       } else {
 #pragma unroll
-        for (int j = 0; j < 32; ++j) x[j] = fast_exp2(x[j] - ref);
+        for (int j = 0; j < 32; j += 2) {
+          fma_f32x2(x[j], x[j + 1], arg, -ref);
+          x[j] = fast_exp2(x[j]);
+          x[j + 1] = fast_exp2(x[j + 1]);
+        }
       }
-      float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int j = 0; j < 32; ++j) sum[j & 3] += x[j];
-      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
       // the products of the tile before have read P and added to O
       if (k > 0) ok = warp_wait(BAR(C::bPvDone), (uint32_t)((k - 1) & 1), abort_flag) && ok;
       if (grow && !first) {
@@ -1198,6 +1198,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         mbar_arrive_pair(lead_bar(C::bPReady));
         mbar_arrive(BAR(C::bInfoEmpty + ri));
       }
+      // (nobody waits for the denominators)
+      float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int j = 0; j < 32; j += 2) add_f32x2(sum[j & 2], sum[(j & 2) + 1], x[j], x[j + 1]);
+      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
       if (last) {
         // ---- epilogue: denominators, then O ----
         float own[4];
@@ -1374,7 +1379,10 @@ cudaError_t launch_latent_tree(const LatentTreeArgs& a, bool fp8, void* workspac
   TreeParams p = {};
   p.a = a;
   p.slices = slices_of(sms);
-  p.scale_log2 = a.scale * 1.4426950408889634f;
+  p.scale_log2 = fabsf(a.scale) * 1.4426950408889634f;
+  p.negate = a.scale < 0.f;
+  p.q_zero = !fp8 && p.scale_log2 == 0.f;
+  if (p.q_zero) p.scale_log2 = 1.f;
   const Workspace w = workspace_layout(a, fp8, sms);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   p.cut = reinterpret_cast<Part*>(ws + w.cut);
