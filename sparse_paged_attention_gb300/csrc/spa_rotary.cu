@@ -25,20 +25,30 @@ namespace {
 
 constexpr int kWarps = 4;
 
-// cos and sin (times the amplitude; sin negated for the inverse) of pairs 2w and 2w + 1.
+// cos and sin (times the amplitude; sin negated for the inverse) of a pair.
+__device__ __forceinline__ float2 cos_sin(const RotaryDev& r, int pos, int pair) {
+  const long long t = (long long)pos * __ldg(r.turns + pair);
+  float c, s;
+  sincospif((float)(int)(t >> 32) * 0x1p-31f, &s, &c);     // (half turns in [-1, 1))
+  return make_float2(c * r.scale, s * (r.inverse ? -r.scale : r.scale));
+}
+// Those of pairs 2w and 2w + 1.
 struct Angles {
-  float c[2], s[2];
+  float2 t[2];
 };
 __device__ __forceinline__ Angles angles(const RotaryDev& r, int pos, int w) {
+  return Angles{{cos_sin(r, pos, 2 * w), cos_sin(r, pos, 2 * w + 1)}};
+}
+// The same for w = lane & 15 of a rotary part of at most 64 values: a lane works out one pair (the function is some
+// 25 instructions) and takes its two from others.
+__device__ __forceinline__ Angles angles_shared(const RotaryDev& r, int pos) {
+  const int lane = threadIdx.x & 31, from = (lane & 15) * 2;
+  float2 mine = make_float2(0.f, 0.f);
+  if (2 * lane < r.R) mine = cos_sin(r, pos, lane);
   Angles a;
 #pragma unroll
-  for (int e = 0; e < 2; ++e) {
-    const long long t = (long long)pos * __ldg(r.turns + 2 * w + e);
-    // half turns in [-1, 1)
-    sincospif((float)(int)(t >> 32) * 0x1p-31f, &a.s[e], &a.c[e]);
-    a.c[e] *= r.scale;
-    a.s[e] *= r.inverse ? -r.scale : r.scale;
-  }
+  for (int e = 0; e < 2; ++e)
+    a.t[e] = make_float2(__shfl_sync(0xffffffffu, mine.x, from + e), __shfl_sync(0xffffffffu, mine.y, from + e));
   return a;
 }
 
@@ -62,8 +72,8 @@ __device__ __forceinline__ Pairs load_pairs(const uint8_t* part, const RotaryDev
 // The four values in the order in which they lie: half: a0 a1, b0 b1; else a0 b0, a1 b1.
 __device__ __forceinline__ void rotate(float (&x)[4], const RotaryDev& r, const Angles& t) {
   const float a0 = x[0], b0 = r.half ? x[2] : x[1], a1 = r.half ? x[1] : x[2], b1 = x[3];
-  const float a2 = a0 * t.c[0] - b0 * t.s[0], b2 = b0 * t.c[0] + a0 * t.s[0];
-  const float a3 = a1 * t.c[1] - b1 * t.s[1], b3 = b1 * t.c[1] + a1 * t.s[1];
+  const float a2 = a0 * t.t[0].x - b0 * t.t[0].y, b2 = b0 * t.t[0].x + a0 * t.t[0].y;
+  const float a3 = a1 * t.t[1].x - b1 * t.t[1].y, b3 = b1 * t.t[1].x + a1 * t.t[1].y;
   x[0] = a2;
   x[1] = r.half ? a3 : b2;
   x[2] = r.half ? b2 : a3;
@@ -102,12 +112,17 @@ __device__ __forceinline__ void weight8(const void* w, bool bf16, int at, float 
     x[4] = v.x, x[5] = v.y, x[6] = v.z, x[7] = v.w;
   }
 }
-__device__ __forceinline__ float weight1(const void* w, bool bf16, int at) {
-  return bf16 ? bf16_lo(__ldg(static_cast<const uint16_t*>(w) + at)) : __ldg(static_cast<const float*>(w) + at);
-}
 __device__ __forceinline__ void weight_pairs(const void* wt, bool bf16, const RotaryDev& r, int w, float (&x)[4]) {
-#pragma unroll
-  for (int e = 0; e < 4; ++e) x[e] = weight1(wt, bf16, r.start + (r.half ? 2 * w + (e & 1) + (e >> 1) * (r.R / 2) : 4 * w + e));
+  const int at = r.start + (r.half ? 2 * w : 4 * w), to = r.half ? at + r.R / 2 : at + 2;
+  if (bf16) {
+    const uint16_t* p = static_cast<const uint16_t*>(wt);
+    const uint32_t u = __ldg(reinterpret_cast<const uint32_t*>(p + at)), v = __ldg(reinterpret_cast<const uint32_t*>(p + to));
+    x[0] = bf16_lo(u), x[1] = bf16_hi(u), x[2] = bf16_lo(v), x[3] = bf16_hi(v);
+  } else {
+    const float* p = static_cast<const float*>(wt);
+    const float2 u = __ldg(reinterpret_cast<const float2*>(p + at)), v = __ldg(reinterpret_cast<const float2*>(p + to));
+    x[0] = u.x, x[1] = u.y, x[2] = v.x, x[3] = v.y;
+  }
 }
 
 __device__ __forceinline__ float warp_sum(float x) {
@@ -129,16 +144,29 @@ __device__ __forceinline__ float sum_squares(const uint4& u) {
 // The column of 16-byte chunk c of the values that are not rotated.
 __device__ __forceinline__ int plain_column(const RotaryDev& r, int c) { return 8 * c < r.start ? 8 * c : 8 * c + r.R; }
 
-// kC: 16-byte chunks a lane of the values that are not rotated (0: none, or they stay where they are);
-// kW: fours of rotated values a lane; kRows: heads of a token a warp takes at once.
+// (x, y) *= (a, b), two values an instruction
+__device__ __forceinline__ void mul_f32x2(float& x, float& y, float a, float b) {
+  asm("{ .reg .b64 v, c; mov.b64 v, {%0, %1}; mov.b64 c, {%2, %3}; mul.rn.f32x2 v, v, c; mov.b64 {%0, %1}, v; }"
+      : "+f"(x), "+f"(y)
+      : "f"(a), "f"(b));
+}
+
+// kC: 16-byte chunks a lane of the values that are not rotated (0: none, or they stay where they are); kW: fours of
+// rotated values a lane and row, or 0: rows of at most 64 rotated values, two rows at once, a half-warp each;
+// kRows: heads of a token a warp takes at once.
 template <int kC, int kW, int kRows, bool kNorm>
 __global__ void __launch_bounds__(32 * kWarps) rope_kernel(const RopeArgs a, int units_q, int units_k) {
   pdl_launch_dependents();
   pdl_wait();
+  constexpr int kP = kW ? kRows * kW : (kRows + 1) / 2;    // fours of rotated values a lane
   const int lane = threadIdx.x & 31;
+  // row (of the group) and four (of the row) of slot i
+  const auto row_of = [&](int i) { return kW ? i / (kW ? kW : 1) : 2 * i + (lane >> 4); };
+  const auto four_of = [&](int i) { return kW ? lane + 32 * (i % (kW ? kW : 1)) : lane & 15; };
   const int per_token = units_q + units_k;
   const int units = a.T * per_token;             // (checked by the caller to fit)
   const int n_plain = (a.D - a.rot.R) >> 3, n_pairs = a.rot.R >> 2;
+  const float inv_d = 1.f / (float)a.D;
   for (int u = blockIdx.x * kWarps + (threadIdx.x >> 5); u < units; u += gridDim.x * kWarps) {
     const int t = u / per_token, g = u - t * per_token;
     const bool is_k = g >= units_q;
@@ -149,7 +177,7 @@ __global__ void __launch_bounds__(32 * kWarps) rope_kernel(const RopeArgs a, int
     uint8_t* dst = x.out + t * x.out_st + h0 * x.out_sh;
     const int rows = min(kRows, x.H - h0);
     uint4 plain[kRows][kC ? kC : 1];
-    Pairs pair[kRows][kW];
+    Pairs pair[kP];
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
       const uint8_t* row = src + (i < rows ? i : 0) * x.x_sh;
@@ -158,11 +186,12 @@ __global__ void __launch_bounds__(32 * kWarps) rope_kernel(const RopeArgs a, int
         plain[i][c] = lane + 32 * c < n_plain
                           ? *reinterpret_cast<const uint4*>(row + 2 * plain_column(a.rot, lane + 32 * c))
                           : make_uint4(0, 0, 0, 0);
+    }
 #pragma unroll
-      for (int w = 0; w < kW; ++w) {
-        pair[i][w].u = pair[i][w].v = 0;
-        if (lane + 32 * w < n_pairs) pair[i][w] = load_pairs(row + 2 * a.rot.start, a.rot, lane + 32 * w);
-      }
+    for (int i = 0; i < kP; ++i) {
+      const int r = row_of(i), w = four_of(i);
+      pair[i].u = pair[i].v = 0;
+      if (w < n_pairs && r < rows) pair[i] = load_pairs(src + r * x.x_sh + 2 * a.rot.start, a.rot, w);
     }
     float inv[kRows];
     if constexpr (kNorm) {
@@ -171,19 +200,31 @@ __global__ void __launch_bounds__(32 * kWarps) rope_kernel(const RopeArgs a, int
         float s = 0.f;
 #pragma unroll
         for (int c = 0; c < kC; ++c) s += sum_squares(plain[i][c]);
-#pragma unroll
-        for (int w = 0; w < kW; ++w) s += sum_squares(make_uint4(pair[i][w].u, pair[i][w].v, 0, 0));
         inv[i] = s;
       }
 #pragma unroll
-      for (int i = 0; i < kRows; ++i) inv[i] = rsqrtf(warp_sum(inv[i]) / (float)a.D + a.eps);
+      for (int i = 0; i < kP; ++i) {
+        const float s = sum_squares(make_uint4(pair[i].u, pair[i].v, 0, 0));
+        if (kW) {
+          inv[i / (kW ? kW : 1)] += s;
+        } else {
+          inv[2 * i] += lane < 16 ? s : 0.f;
+          if (2 * i + 1 < kRows) inv[2 * i + 1] += lane < 16 ? 0.f : s;
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kRows; ++i) inv[i] = rsqrtf(fmaf(warp_sum(inv[i]), inv_d, a.eps));
     }
 #pragma unroll
     for (int c = 0; c < kC; ++c) {
       if (lane + 32 * c >= n_plain) continue;
       const int col = plain_column(a.rot, lane + 32 * c);
       float wt[8];
-      if (kNorm && x.weight) weight8(x.weight, a.weight_bf16, col, wt);
+      if constexpr (kNorm) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) wt[e] = 1.f;
+        if (x.weight) weight8(x.weight, a.weight_bf16, col, wt);
+      }
 #pragma unroll
       for (int i = 0; i < kRows; ++i) {
         if (i >= rows) break;
@@ -192,8 +233,9 @@ __global__ void __launch_bounds__(32 * kWarps) rope_kernel(const RopeArgs a, int
           uint32_t v[4] = {o.x, o.y, o.z, o.w};
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            float p = bf16_lo(v[e]) * inv[i], q = bf16_hi(v[e]) * inv[i];
-            if (x.weight) p *= wt[2 * e], q *= wt[2 * e + 1];
+            float p = bf16_lo(v[e]), q = bf16_hi(v[e]);
+            mul_f32x2(p, q, inv[i], inv[i]);
+            mul_f32x2(p, q, wt[2 * e], wt[2 * e + 1]);
             v[e] = pack_bf16x2(p, q);
           }
           o = make_uint4(v[0], v[1], v[2], v[3]);
@@ -201,27 +243,32 @@ __global__ void __launch_bounds__(32 * kWarps) rope_kernel(const RopeArgs a, int
         *reinterpret_cast<uint4*>(dst + i * x.out_sh + 2 * col) = o;
       }
     }
+    Angles an[kW ? kW : 1];
+    if constexpr (kW == 0) {
+      an[0] = angles_shared(a.rot, pos);
+    } else {
 #pragma unroll
-    for (int w = 0; w < kW; ++w) {
-      if (lane + 32 * w >= n_pairs) continue;
-      const Angles an = angles(a.rot, pos, lane + 32 * w);
-      float wt[4];
-      if (kNorm && x.weight) weight_pairs(x.weight, a.weight_bf16, a.rot, lane + 32 * w, wt);
+      for (int w = 0; w < kW; ++w)
+        if (lane + 32 * w < n_pairs) an[w] = angles(a.rot, pos, lane + 32 * w);
+    }
 #pragma unroll
-      for (int i = 0; i < kRows; ++i) {
-        if (i >= rows) break;
-        float v[4];
-        unpack(pair[i][w], v);
-        if constexpr (kNorm) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            v[e] *= inv[i];
-            if (x.weight) v[e] *= wt[e];
-          }
-        }
-        rotate(v, a.rot, an);
-        store_pairs(dst + i * x.out_sh + 2 * a.rot.start, a.rot, lane + 32 * w, v);
+    for (int i = 0; i < kP; ++i) {
+      const int r = row_of(i), w = four_of(i);
+      if (w >= n_pairs || r >= rows) continue;
+      float v[4];
+      unpack(pair[i], v);
+      if constexpr (kNorm) {
+        float wt[4] = {1.f, 1.f, 1.f, 1.f};
+        if (x.weight) weight_pairs(x.weight, a.weight_bf16, a.rot, w, wt);
+        const float f = kW ? inv[i / (kW ? kW : 1)]
+                           : lane < 16 ? inv[2 * i < kRows ? 2 * i : 0] : inv[2 * i + 1 < kRows ? 2 * i + 1 : 0];
+        mul_f32x2(v[0], v[1], f, f);
+        mul_f32x2(v[2], v[3], f, f);
+        mul_f32x2(v[0], v[1], wt[0], wt[1]);
+        mul_f32x2(v[2], v[3], wt[2], wt[3]);
       }
+      rotate(v, a.rot, an[kW ? i % (kW ? kW : 1) : 0]);
+      store_pairs(dst + r * x.out_sh + 2 * a.rot.start, a.rot, w, v);
     }
   }
 }
@@ -229,16 +276,17 @@ __global__ void __launch_bounds__(32 * kWarps) rope_kernel(const RopeArgs a, int
 template <int kC, int kW, int kRows>
 cudaError_t launch_rope_as(const RopeArgs& a, bool norm, int sms, cudaStream_t stream) {
   const int uq = (a.q.H + kRows - 1) / kRows, uk = (a.k.H + kRows - 1) / kRows;
-  const long long blocks = ((long long)a.T * (uq + uk) + kWarps - 1) / kWarps, cap = 16LL * sms;
+  const long long blocks = ((long long)a.T * (uq + uk) + kWarps - 1) / kWarps, cap = 64LL * sms;
   const unsigned grid = (unsigned)(blocks < cap ? blocks : cap);
   return launch_with_pdl(norm ? rope_kernel<kC, kW, kRows, true> : rope_kernel<kC, kW, kRows, false>, dim3(grid),
                          dim3(32 * kWarps), 0, stream, 2LL * grid <= sms, a, uq, uk);
 }
 
-template <int kC, int kRows>
+template <int kC, int kRows, int kWide = kRows>
 cudaError_t launch_rope_width(const RopeArgs& a, bool norm, int sms, cudaStream_t stream) {
-  return a.rot.R <= 128 ? launch_rope_as<kC, 1, kRows>(a, norm, sms, stream)
-                        : launch_rope_as<kC, 2, kRows>(a, norm, sms, stream);
+  if (a.rot.R <= 64) return launch_rope_as<kC, 0, kRows>(a, norm, sms, stream);
+  return a.rot.R <= 128 ? launch_rope_as<kC, 1, kWide>(a, norm, sms, stream)
+                        : launch_rope_as<kC, 2, kWide>(a, norm, sms, stream);
 }
 
 // ---- appends --------------------------------------------------------------------------------
@@ -249,19 +297,6 @@ __device__ __forceinline__ int append_row(const AppendArgs& a, int t) {
   return latent_row(a.pool, b, x);
 }
 
-// Codes of two, four values over the scale: by its reciprocal where that is a normal number (the quotient is
-// then off by two units in its last place, next to which the values' own roundings are no smaller), else divided.
-struct Quotient {
-  float scale, r;
-  bool fast;
-  __device__ __forceinline__ float operator()(float x) const { return fast ? x * r : __fdiv_rn(x, scale); }
-};
-__device__ __forceinline__ Quotient quotient(float scale) {
-  return Quotient{scale, __frcp_rn(scale), kvq_fast_scale(scale)};
-}
-__device__ __forceinline__ uint32_t codes4(const Quotient& q, float a, float b, float c, float d) {
-  return kvq_e4m3x2(q(a), q(b)) | (kvq_e4m3x2(q(c), q(d)) << 16);
-}
 __device__ __forceinline__ float row_scale(float amax) { return amax > 0.f ? __fdiv_rn(amax, 448.f) : 1.f; }
 __device__ __forceinline__ float warp_max(float m) {   // of values >= 0 (their bits order as they do)
   return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m)));
@@ -272,62 +307,6 @@ template <int kW>
 struct Row {
   float x[2][8], r[kW][4];
 };
-
-template <int kW>
-__device__ __forceinline__ void norm_row(Row<kW>& y, const AppendArgs& a, int width, int n_plain, int n_pairs,
-                                         bool rotary_too) {
-  const int lane = threadIdx.x & 31;
-  float s = 0.f;
-#pragma unroll
-  for (int c = 0; c < 2; ++c)
-#pragma unroll
-    for (int e = 0; e < 8; ++e) s = fmaf(y.x[c][e], y.x[c][e], s);
-  if (rotary_too) {
-#pragma unroll
-    for (int w = 0; w < kW; ++w)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) s = fmaf(y.r[w][e], y.r[w][e], s);
-  }
-  const float inv = rsqrtf(warp_sum(s) / (float)width + a.eps);
-#pragma unroll
-  for (int c = 0; c < 2; ++c) {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) y.x[c][e] *= inv;
-    if (a.weight && lane + 32 * c < n_plain) {
-      float wt[8];
-      weight8(a.weight, a.weight_bf16, rotary_too ? plain_column(a.rot, lane + 32 * c) : 8 * (lane + 32 * c), wt);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) y.x[c][e] *= wt[e];
-    }
-  }
-  if (rotary_too) {
-#pragma unroll
-    for (int w = 0; w < kW; ++w) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) y.r[w][e] *= inv;
-      if (a.weight && lane + 32 * w < n_pairs) {
-        float wt[4];
-        weight_pairs(a.weight, a.weight_bf16, a.rot, lane + 32 * w, wt);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) y.r[w][e] *= wt[e];
-      }
-    }
-  }
-}
-
-template <int kW>
-__device__ __forceinline__ float row_amax(const Row<kW>& y) {
-  float m = 0.f;                                 // (a NaN does not enter it)
-#pragma unroll
-  for (int c = 0; c < 2; ++c)
-#pragma unroll
-    for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(y.x[c][e]));
-#pragma unroll
-  for (int w = 0; w < kW; ++w)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) m = fmaxf(m, fabsf(y.r[w][e]));
-  return warp_max(m);
-}
 __device__ __forceinline__ void unpack8(const uint4& u, float (&x)[8]) {
   const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
@@ -336,26 +315,135 @@ __device__ __forceinline__ void unpack8(const uint4& u, float (&x)[8]) {
     x[2 * i + 1] = bf16_hi(w[i]);
   }
 }
+template <int N>
+__device__ __forceinline__ void scale_by(float (&x)[N], float f) {
+#pragma unroll
+  for (int e = 0; e < N; e += 2) mul_f32x2(x[e], x[e + 1], f, f);
+}
+template <int N>
+__device__ __forceinline__ void scale_by(float (&x)[N], const float (&w)[N]) {
+#pragma unroll
+  for (int e = 0; e < N; e += 2) mul_f32x2(x[e], x[e + 1], w[e], w[e + 1]);
+}
+template <int N>
+__device__ __forceinline__ float abs_max(const float (&x)[N], float m) {   // (a NaN does not enter it)
+#pragma unroll
+  for (int e = 0; e < N; ++e) m = fmaxf(m, fabsf(x[e]));
+  return m;
+}
+template <int N>
+__device__ __forceinline__ float squares(const float (&x)[N], float s) {
+#pragma unroll
+  for (int e = 0; e < N; ++e) s = fmaf(x[e], x[e], s);
+  return s;
+}
+
+// A row, normalised: its values and the weights are multiplied here.  `rotary_too`: the rotary part is part of the
+// row that is normalised (a K row), else the row is the chunks alone (a latent row).
+template <int kW>
+__device__ __forceinline__ void norm_row(Row<kW>& y, const AppendArgs& a, int width, int n_plain, int n_pairs,
+                                         bool rotary_too) {
+  const int lane = threadIdx.x & 31;
+  float s = squares(y.x[1], squares(y.x[0], 0.f));
+  if (rotary_too) {
+#pragma unroll
+    for (int w = 0; w < kW; ++w) s = squares(y.r[w], s);
+  }
+  const float inv = rsqrtf(warp_sum(s) / (float)width + a.eps);
+#pragma unroll
+  for (int c = 0; c < 2; ++c) {
+    scale_by(y.x[c], inv);
+    if (a.weight && lane + 32 * c < n_plain) {
+      float wt[8];
+      weight8(a.weight, a.weight_bf16, rotary_too ? plain_column(a.rot, lane + 32 * c) : 8 * (lane + 32 * c), wt);
+      scale_by(y.x[c], wt);
+    }
+  }
+  if (rotary_too) {
+#pragma unroll
+    for (int w = 0; w < kW; ++w) {
+      scale_by(y.r[w], inv);
+      if (a.weight && lane + 32 * w < n_pairs) {
+        float wt[4];
+        weight_pairs(a.weight, a.weight_bf16, a.rot, lane + 32 * w, wt);
+        scale_by(y.r[w], wt);
+      }
+    }
+  }
+}
+
+template <int kW>
+__device__ __forceinline__ float row_amax(const Row<kW>& y) {
+  float m = abs_max(y.x[1], abs_max(y.x[0], 0.f));
+#pragma unroll
+  for (int w = 0; w < kW; ++w) m = abs_max(y.r[w], m);
+  return warp_max(m);
+}
+
+// Values over the row's scale, in place: by its reciprocal where that is a normal number (the quotient is then off by
+// two units in its last place, next to which the values' own roundings are no smaller), else divided.  Out of
+// line: rows with so small a scale are rare, and sixteen divisions a lane would be most of the kernel's code.
+template <int kW>
+__device__ __noinline__ void divide_row(Row<kW>& y, float scale) {
+#pragma unroll 1
+  for (int c = 0; c < 2; ++c)
+#pragma unroll 1
+    for (int e = 0; e < 8; ++e) y.x[c][e] = __fdiv_rn(y.x[c][e], scale);
+#pragma unroll 1
+  for (int w = 0; w < kW; ++w)
+#pragma unroll 1
+    for (int e = 0; e < 4; ++e) y.r[w][e] = __fdiv_rn(y.r[w][e], scale);
+}
+template <int kW>
+__device__ __forceinline__ void over_scale(Row<kW>& y, float scale) {
+  if (!kvq_fast_scale(scale)) {
+    Row<kW> z = y;                               // (a copy: the row itself stays in registers)
+    divide_row(z, scale);
+    y = z;
+    return;
+  }
+  const float r = __frcp_rn(scale);
+  scale_by(y.x[0], r);
+  scale_by(y.x[1], r);
+#pragma unroll
+  for (int w = 0; w < kW; ++w) scale_by(y.r[w], r);
+}
+__device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d) {
+  return kvq_e4m3x2(a, b) | (kvq_e4m3x2(c, d) << 16);
+}
+__device__ __forceinline__ uint2 codes8(const float (&e)[8]) {
+  return make_uint2(codes4(e[0], e[1], e[2], e[3]), codes4(e[4], e[5], e[6], e[7]));
+}
 __device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
   return make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
                     pack_bf16x2(x[6], x[7]));
 }
+// Four codes of a rotary part (of bytes).
+__device__ __forceinline__ void store_codes(uint8_t* part, const RotaryDev& r, int w, uint32_t code) {
+  if (r.half) {
+    *reinterpret_cast<uint16_t*>(part + 2 * w) = (uint16_t)code;
+    *reinterpret_cast<uint16_t*>(part + r.R / 2 + 2 * w) = (uint16_t)(code >> 16);
+  } else {
+    *reinterpret_cast<uint32_t*>(part + 4 * w) = code;
+  }
+}
 
 constexpr int kAppendBlocks = 8;                 // CTAs an SM
 
-// K rows (normalised, rotated) and V rows (as they are) of new tokens into their slots.  A warp a token.
-template <bool kFp8>
+// K rows (normalised, rotated) and V rows (as they are) of new tokens into their slots.  A warp a token; kW: fours
+// of rotated values a lane, 0: at most 64 values.
+template <bool kFp8, int kW>
 __global__ void __launch_bounds__(32 * kWarps, kAppendBlocks) kv_append_kernel(const AppendArgs a) {
   pdl_launch_dependents();
   pdl_wait();
-  constexpr int kW = kRopeMaxPart / 128;
+  constexpr int kR = kW ? kW : 1;
   const int lane = threadIdx.x & 31, D = a.pool.L;
   const int n_plain = (D - a.rot.R) >> 3, n_pairs = a.rot.R >> 2, n_all = D >> 3;
   const long long step = (long long)gridDim.x * kWarps;
   for (long long t = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5); t < a.T; t += step) {
     const uint8_t *k = a.k + t * a.k_st, *v = a.v + t * a.v_st;
     uint4 kx[2], vx[2];
-    Pairs kp[kW];
+    Pairs kp[kR];
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
       kx[c] = vx[c] = make_uint4(0, 0, 0, 0);
@@ -364,7 +452,7 @@ __global__ void __launch_bounds__(32 * kWarps, kAppendBlocks) kv_append_kernel(c
       if (lane + 32 * c < n_all) vx[c] = __ldg(reinterpret_cast<const uint4*>(v) + lane + 32 * c);
     }
 #pragma unroll
-    for (int w = 0; w < kW; ++w) {
+    for (int w = 0; w < kR; ++w) {
       kp[w].u = kp[w].v = 0;
       if (lane + 32 * w < n_pairs) kp[w] = load_pairs(k + 2 * a.rot.start, a.rot, lane + 32 * w);
     }
@@ -373,15 +461,19 @@ __global__ void __launch_bounds__(32 * kWarps, kAppendBlocks) kv_append_kernel(c
       if (lane == 0) flag_error(SPA_ERR_INDEX);
       continue;
     }
-    Row<kW> y;
+    Row<kR> y;
 #pragma unroll
     for (int c = 0; c < 2; ++c) unpack8(kx[c], y.x[c]);
 #pragma unroll
-    for (int w = 0; w < kW; ++w) unpack(kp[w], y.r[w]);
+    for (int w = 0; w < kR; ++w) unpack(kp[w], y.r[w]);
     if (a.norm) norm_row(y, a, D, n_plain, n_pairs, true);
+    if constexpr (kW == 0) {
+      rotate(y.r[0], a.rot, angles_shared(a.rot, pos));    // (zeros where a lane has none)
+    } else {
 #pragma unroll
-    for (int w = 0; w < kW; ++w)
-      if (lane + 32 * w < n_pairs) rotate(y.r[w], a.rot, angles(a.rot, pos, lane + 32 * w));
+      for (int w = 0; w < kR; ++w)
+        if (lane + 32 * w < n_pairs) rotate(y.r[w], a.rot, angles(a.rot, pos, lane + 32 * w));
+    }
     if constexpr (!kFp8) {
       uint8_t* dst = a.pool.rows + (size_t)row * 4 * D;
 #pragma unroll
@@ -391,10 +483,11 @@ __global__ void __launch_bounds__(32 * kWarps, kAppendBlocks) kv_append_kernel(c
         if (lane + 32 * c < n_all) reinterpret_cast<uint4*>(dst + 2 * D)[lane + 32 * c] = vx[c];
       }
 #pragma unroll
-      for (int w = 0; w < kW; ++w)
+      for (int w = 0; w < kR; ++w)
         if (lane + 32 * w < n_pairs) store_pairs(dst + 2 * a.rot.start, a.rot, lane + 32 * w, y.r[w]);
     } else {
-      const Quotient q = quotient(row_scale(row_amax(y)));
+      const float ks = row_scale(row_amax(y));
+      over_scale(y, ks);
       uint32_t vm = 0;                           // (bf16's bits order as their magnitudes do)
 #pragma unroll
       for (int c = 0; c < 2; ++c)
@@ -403,30 +496,27 @@ __global__ void __launch_bounds__(32 * kWarps, kAppendBlocks) kv_append_kernel(c
         }
       vm = __reduce_max_sync(0xffffffffu, max(vm & 0xffffu, vm >> 16));
       const float vs = row_scale(bf16_lo(vm)), vr = __frcp_rn(vs);
-      const bool vfast = kvq_fast_scale(vs);
       uint8_t* dst = a.pool.rows + (size_t)row * 2 * D;
+      uint2* dst_v = reinterpret_cast<uint2*>(dst + D);
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        const float* e = y.x[c];
+      for (int c = 0; c < 2; ++c)
         if (lane + 32 * c < n_plain)
-          *reinterpret_cast<uint2*>(dst + plain_column(a.rot, lane + 32 * c)) =
-              make_uint2(codes4(q, e[0], e[1], e[2], e[3]), codes4(q, e[4], e[5], e[6], e[7]));
-        if (lane + 32 * c < n_all) reinterpret_cast<uint2*>(dst + D)[lane + 32 * c] = kvq_chunk(vx[c], vs, vr, vfast);
+          *reinterpret_cast<uint2*>(dst + plain_column(a.rot, lane + 32 * c)) = codes8(y.x[c]);
+      if (kvq_fast_scale(vs)) {
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+          if (lane + 32 * c < n_all) dst_v[lane + 32 * c] = kvq_chunk(vx[c], vs, vr, true);
+      } else {
+#pragma unroll 1
+        for (int c = 0; c < 2; ++c)
+          if (lane + 32 * c < n_all) dst_v[lane + 32 * c] = kvq_chunk(c == 0 ? vx[0] : vx[1], vs, vr, false);
       }
 #pragma unroll
-      for (int w = 0; w < kW; ++w) {
-        if (lane + 32 * w >= n_pairs) continue;
-        const uint32_t code = codes4(q, y.r[w][0], y.r[w][1], y.r[w][2], y.r[w][3]);
-        uint8_t* part = dst + a.rot.start;
-        if (a.rot.half) {
-          *reinterpret_cast<uint16_t*>(part + 2 * (lane + 32 * w)) = (uint16_t)code;
-          *reinterpret_cast<uint16_t*>(part + a.rot.R / 2 + 2 * (lane + 32 * w)) = (uint16_t)(code >> 16);
-        } else {
-          *reinterpret_cast<uint32_t*>(part + 4 * (lane + 32 * w)) = code;
-        }
-      }
+      for (int w = 0; w < kR; ++w)
+        if (lane + 32 * w < n_pairs)
+          store_codes(dst + a.rot.start, a.rot, lane + 32 * w, codes4(y.r[w][0], y.r[w][1], y.r[w][2], y.r[w][3]));
       if (lane == 0) {
-        a.k_scale[row] = q.scale;
+        a.k_scale[row] = ks;
         a.v_scale[row] = vs;
       }
     }
@@ -460,7 +550,7 @@ __global__ void __launch_bounds__(32 * kWarps, kAppendBlocks) latent_append_kern
     for (int c = 0; c < 2; ++c) unpack8(x[c], y.x[c]);
     unpack(p, y.r[0]);
     if (a.norm) norm_row(y, a, L, nl, n_pairs, false);
-    if (lane < n_pairs) rotate(y.r[0], a.rot, angles(a.rot, pos, lane));
+    rotate(y.r[0], a.rot, angles_shared(a.rot, pos));      // (zeros where a lane has none)
     uint8_t* dst = a.pool.rows + (size_t)row * a.pool.row_bytes;
     if constexpr (!kFp8) {
 #pragma unroll
@@ -468,37 +558,25 @@ __global__ void __launch_bounds__(32 * kWarps, kAppendBlocks) latent_append_kern
         if (lane + 32 * c < nl) reinterpret_cast<uint4*>(dst)[lane + 32 * c] = pack8(y.x[c]);
       if (lane < n_pairs) store_pairs(dst + 2 * L, a.rot, lane, y.r[0]);
     } else {
-      const Quotient q = quotient(row_scale(row_amax(y)));
+      const float scale = row_scale(row_amax(y));
+      over_scale(y, scale);
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        const float* e = y.x[c];
-        if (lane + 32 * c < nl)
-          reinterpret_cast<uint2*>(dst)[lane + 32 * c] =
-              make_uint2(codes4(q, e[0], e[1], e[2], e[3]), codes4(q, e[4], e[5], e[6], e[7]));
-      }
+      for (int c = 0; c < 2; ++c)
+        if (lane + 32 * c < nl) reinterpret_cast<uint2*>(dst)[lane + 32 * c] = codes8(y.x[c]);
       if (lane < n_pairs) {
         uint32_t high[2], low[2];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const float c = q(y.r[0][2 * i]), d = q(y.r[0][2 * i + 1]);
+          const float c = y.r[0][2 * i], d = y.r[0][2 * i + 1];
           high[i] = kvq_e4m3x2(c, d);
           const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)high[i], __NV_E4M3);
           const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
           low[i] = kvq_e4m3x2(c - f.x, d - f.y);
         }
-        uint8_t* part = dst + L;
-        const int R = a.rot.R;
-        if (a.rot.half) {
-          *reinterpret_cast<uint16_t*>(part + 2 * lane) = (uint16_t)high[0];
-          *reinterpret_cast<uint16_t*>(part + R / 2 + 2 * lane) = (uint16_t)high[1];
-          *reinterpret_cast<uint16_t*>(part + R + 2 * lane) = (uint16_t)low[0];
-          *reinterpret_cast<uint16_t*>(part + R + R / 2 + 2 * lane) = (uint16_t)low[1];
-        } else {
-          *reinterpret_cast<uint32_t*>(part + 4 * lane) = high[0] | (high[1] << 16);
-          *reinterpret_cast<uint32_t*>(part + R + 4 * lane) = low[0] | (low[1] << 16);
-        }
+        store_codes(dst + L, a.rot, lane, high[0] | (high[1] << 16));
+        store_codes(dst + L + a.rot.R, a.rot, lane, low[0] | (low[1] << 16));
       }
-      if (lane == 0) a.k_scale[row] = q.scale;
+      if (lane == 0) a.k_scale[row] = scale;
     }
   }
 }
@@ -514,7 +592,7 @@ cudaError_t launch_rope(const RopeArgs& a, bool norm, int sms, cudaStream_t stre
   // In place and without a norm the values that are not rotated stay as they are.
   const bool in_place = !norm && a.q.x == a.q.out && (a.k.H == 0 || a.k.x == a.k.out);
   const int chunks = in_place ? 0 : (a.D - a.rot.R) / 8;
-  if (chunks == 0) return launch_rope_width<0, 8>(a, norm, sms, stream);
+  if (chunks == 0) return launch_rope_width<0, 16, 4>(a, norm, sms, stream);
   if (chunks <= 32) return launch_rope_width<1, 4>(a, norm, sms, stream);
   if (chunks <= 64) return launch_rope_width<2, 4>(a, norm, sms, stream);
   return launch_rope_width<4, 2>(a, norm, sms, stream);
@@ -522,8 +600,9 @@ cudaError_t launch_rope(const RopeArgs& a, bool norm, int sms, cudaStream_t stre
 
 cudaError_t launch_kv_append(const AppendArgs& a, bool fp8, int sms, cudaStream_t stream) {
   const unsigned blocks = append_blocks(a.T, sms);
-  return launch_with_pdl(fp8 ? kv_append_kernel<true> : kv_append_kernel<false>, dim3(blocks), dim3(32 * kWarps), 0,
-                         stream, 2LL * blocks <= sms, a);
+  const auto kern = a.rot.R <= 64 ? (fp8 ? kv_append_kernel<true, 0> : kv_append_kernel<false, 0>)
+                                  : (fp8 ? kv_append_kernel<true, 2> : kv_append_kernel<false, 2>);
+  return launch_with_pdl(kern, dim3(blocks), dim3(32 * kWarps), 0, stream, 2LL * blocks <= sms, a);
 }
 
 cudaError_t launch_latent_append(const AppendArgs& a, bool fp8, int sms, cudaStream_t stream) {
