@@ -995,37 +995,44 @@ def _rotary(table, dev):
     """(rope_dim, address, interleaved, amplitude) of a checked table (None: no rotation)."""
     if table is None:
         return 0, 0, 0, 1.0
-    turns = table.turns
+    turns, interleaved, scale = table
     if turns.dtype is not torch.int64 or turns.dim() != 1 or not turns.is_contiguous():
         raise ValueError("a rotary table's turns must be a contiguous int64 [rope_dim / 2] tensor")
-    _same_device("the rotary table", turns, dev)
+    if turns.get_device() != dev:
+        _same_device("the rotary table", turns, dev)
     n = turns.numel()
-    return 2 * n, turns.data_ptr() if n else 0, int(table.interleaved), table.scale
+    return 2 * n, turns.data_ptr() if n else 0, interleaved, scale
 
 
 def _weight(name, weight, width, dev):
     """(address, dtype code) of checked norm weights (None: ones)."""
     if weight is None:
         return 0, -1
-    if weight.dtype not in (torch.float32, torch.bfloat16) or weight.numel() != width or \
+    dtype = weight.dtype
+    if (dtype is not torch.bfloat16 and dtype is not torch.float32) or weight.numel() != width or \
             weight.dim() != 1 or not weight.is_contiguous():
         raise ValueError(f"{name} must be a contiguous fp32 or bf16 [{width}] tensor")
-    _same_device(name, weight, dev)
-    return weight.data_ptr(), int(weight.dtype is torch.bfloat16)
+    if weight.get_device() != dev:
+        _same_device(name, weight, dev)
+    return weight.data_ptr(), 1 if dtype is torch.bfloat16 else 0
 
 
-def _rope_out(name, x, out, stream):
+def _rope_out(name, x, out, shape, dev, stream):
+    """Output of x's shape, made on `stream` if none is given, and its leading strides."""
     if out is None:
-        return _empty(x.shape, torch.bfloat16, x.device, stream)
-    if out.shape != x.shape:
+        out = x.new_empty(shape) if stream is None else _empty(shape, torch.bfloat16, x.device, stream)
+        return out, shape[1] * shape[2], shape[2]
+    if out.shape != shape:
         raise ValueError(f"{name} must have its input's shape")
-    return out
+    _, st, sh = _latent_rows(name, out, 3, shape[2], dev)
+    return out, st, sh
 
 
 def _rope_positions(positions, n, dev):
     if positions.dtype is not torch.int32 or not positions.is_contiguous() or positions.numel() != n:
         raise ValueError(f"positions must be a contiguous int32 tensor of {n} entries")
-    _same_device("positions", positions, dev)
+    if positions.get_device() != dev:
+        _same_device("positions", positions, dev)
     return positions.data_ptr()
 
 
@@ -1036,12 +1043,12 @@ def sparse_attn_rope(x, positions, table, *, start=None, inverse=False, out=None
     output).  Returns ``out``: a new tensor, or the one given, ``x`` itself among them (in place)."""
     lib = load_library()
     dev = x.get_device()
-    (T, H, D), st, sh = _latent_rows("x", x, 3, None, dev)
+    shape, st, sh = _latent_rows("x", x, 3, None, dev)
+    T, H, D = shape
     R, turns, interleaved, amplitude = _rotary(table, dev)
     pos = _rope_positions(positions, T, dev)
     _current_device(dev)
-    out = _rope_out("out", x, out, stream)
-    _, ot, oh = _latent_rows("out", out, 3, D, dev)
+    out, ot, oh = _rope_out("out", x, out, shape, dev, stream)
     prob = _ROPE.pack(T, D, R, D - R if start is None else start, interleaved, bool(inverse), 0, 0, amplitude,
                       1.0, pos, turns, x.data_ptr(), out.data_ptr(), 0, st, sh, ot, oh, H, 0, *_NO_ROWS)
     s = lib.sparse_attn_rope(prob, _launch_stream(stream, dev))
@@ -1058,7 +1065,8 @@ def sparse_attn_norm_rope(q, k, positions, table, *, q_weight=None, k_weight=Non
     (q_out, k_out): new tensors, or those given (in place if they are the inputs)."""
     lib = load_library()
     dev = q.get_device()
-    (T, H, D), st, sh = _latent_rows("q", q, 3, None, dev)
+    shape, st, sh = _latent_rows("q", q, 3, None, dev)
+    T, H, D = shape
     R, turns, interleaved, amplitude = _rotary(table, dev)
     pos = _rope_positions(positions, T, dev)
     qw, qd = _weight("q_weight", q_weight, D, dev)
@@ -1068,14 +1076,12 @@ def sparse_attn_norm_rope(q, k, positions, table, *, q_weight=None, k_weight=Non
     _current_device(dev)
     k_rows = _NO_ROWS
     if k is not None:
-        (n, kh, _), kt, ks = _latent_rows("k", k, 3, D, dev)
-        if n != T:
+        k_shape, kt, ks = _latent_rows("k", k, 3, D, dev)
+        if k_shape[0] != T:
             raise ValueError("q and k must have the same tokens")
-        k_out = _rope_out("k_out", k, k_out, stream)
-        _, ot, oh = _latent_rows("k_out", k_out, 3, D, dev)
-        k_rows = (k.data_ptr(), k_out.data_ptr(), kw, kt, ks, ot, oh, kh, 0)
-    q_out = _rope_out("q_out", q, q_out, stream)
-    _, ot, oh = _latent_rows("q_out", q_out, 3, D, dev)
+        k_out, ot, oh = _rope_out("k_out", k, k_out, k_shape, dev, stream)
+        k_rows = (k.data_ptr(), k_out.data_ptr(), kw, kt, ks, ot, oh, k_shape[1], 0)
+    q_out, ot, oh = _rope_out("q_out", q, q_out, shape, dev, stream)
     prob = _ROPE.pack(T, D, R, D - R if start is None else start, interleaved, 0, max(qd, kd, 0), 0, amplitude,
                       eps, pos, turns, q.data_ptr(), q_out.data_ptr(), qw, st, sh, ot, oh, H, 0, *k_rows)
     s = lib.sparse_attn_norm_rope(prob, _launch_stream(stream, dev))

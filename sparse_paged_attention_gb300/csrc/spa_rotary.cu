@@ -338,36 +338,30 @@ __device__ __forceinline__ float squares(const float (&x)[N], float s) {
   return s;
 }
 
-// A row, normalised: its values and the weights are multiplied here.  `rotary_too`: the rotary part is part of the
-// row that is normalised (a K row), else the row is the chunks alone (a latent row).
+// A K row, normalised.
 template <int kW>
-__device__ __forceinline__ void norm_row(Row<kW>& y, const AppendArgs& a, int width, int n_plain, int n_pairs,
-                                         bool rotary_too) {
+__device__ __forceinline__ void norm_row(Row<kW>& y, const AppendArgs& a, int width, int n_plain, int n_pairs) {
   const int lane = threadIdx.x & 31;
   float s = squares(y.x[1], squares(y.x[0], 0.f));
-  if (rotary_too) {
 #pragma unroll
-    for (int w = 0; w < kW; ++w) s = squares(y.r[w], s);
-  }
+  for (int w = 0; w < kW; ++w) s = squares(y.r[w], s);
   const float inv = rsqrtf(warp_sum(s) / (float)width + a.eps);
 #pragma unroll
   for (int c = 0; c < 2; ++c) {
     scale_by(y.x[c], inv);
     if (a.weight && lane + 32 * c < n_plain) {
       float wt[8];
-      weight8(a.weight, a.weight_bf16, rotary_too ? plain_column(a.rot, lane + 32 * c) : 8 * (lane + 32 * c), wt);
+      weight8(a.weight, a.weight_bf16, plain_column(a.rot, lane + 32 * c), wt);
       scale_by(y.x[c], wt);
     }
   }
-  if (rotary_too) {
 #pragma unroll
-    for (int w = 0; w < kW; ++w) {
-      scale_by(y.r[w], inv);
-      if (a.weight && lane + 32 * w < n_pairs) {
-        float wt[4];
-        weight_pairs(a.weight, a.weight_bf16, a.rot, lane + 32 * w, wt);
-        scale_by(y.r[w], wt);
-      }
+  for (int w = 0; w < kW; ++w) {
+    scale_by(y.r[w], inv);
+    if (a.weight && lane + 32 * w < n_pairs) {
+      float wt[4];
+      weight_pairs(a.weight, a.weight_bf16, a.rot, lane + 32 * w, wt);
+      scale_by(y.r[w], wt);
     }
   }
 }
@@ -382,24 +376,27 @@ __device__ __forceinline__ float row_amax(const Row<kW>& y) {
 
 // Values over the row's scale, in place: by its reciprocal where that is a normal number (the quotient is then off by
 // two units in its last place, next to which the values' own roundings are no smaller), else divided.  Out of
-// line: rows with so small a scale are rare, and sixteen divisions a lane would be most of the kernel's code.
-template <int kW>
-__device__ __noinline__ void divide_row(Row<kW>& y, float scale) {
-#pragma unroll 1
-  for (int c = 0; c < 2; ++c)
-#pragma unroll 1
-    for (int e = 0; e < 8; ++e) y.x[c][e] = __fdiv_rn(y.x[c][e], scale);
-#pragma unroll 1
-  for (int w = 0; w < kW; ++w)
-#pragma unroll 1
-    for (int e = 0; e < 4; ++e) y.r[w][e] = __fdiv_rn(y.r[w][e], scale);
+// line: rows with so small a scale are rare, and a division for every value would be most of the kernel's code.
+__device__ __noinline__ float divided(float x, float scale) { return __fdiv_rn(x, scale); }
+template <int kC, int kR>
+__device__ __forceinline__ void divide(float (&x)[kC][8], float (&r)[kR], float scale) {
+#pragma unroll
+  for (int c = 0; c < kC; ++c)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[c][e] = divided(x[c][e], scale);
+#pragma unroll
+  for (int e = 0; e < kR; ++e) r[e] = divided(r[e], scale);
 }
 template <int kW>
 __device__ __forceinline__ void over_scale(Row<kW>& y, float scale) {
   if (!kvq_fast_scale(scale)) {
-    Row<kW> z = y;                               // (a copy: the row itself stays in registers)
-    divide_row(z, scale);
-    y = z;
+#pragma unroll
+    for (int w = 0; w < kW; ++w) {
+      if (w == 0) divide(y.x, y.r[0], scale);
+      else
+#pragma unroll
+        for (int e = 0; e < 4; ++e) y.r[w][e] = divided(y.r[w][e], scale);
+    }
     return;
   }
   const float r = __frcp_rn(scale);
@@ -428,7 +425,7 @@ __device__ __forceinline__ void store_codes(uint8_t* part, const RotaryDev& r, i
   }
 }
 
-constexpr int kAppendBlocks = 8;                 // CTAs an SM
+constexpr int kAppendBlocks = 8, kLatentBlocks = 8;   // CTAs an SM
 
 // K rows (normalised, rotated) and V rows (as they are) of new tokens into their slots.  A warp a token; kW: fours
 // of rotated values a lane, 0: at most 64 values.
@@ -466,7 +463,7 @@ __global__ void __launch_bounds__(32 * kWarps, kAppendBlocks) kv_append_kernel(c
     for (int c = 0; c < 2; ++c) unpack8(kx[c], y.x[c]);
 #pragma unroll
     for (int w = 0; w < kR; ++w) unpack(kp[w], y.r[w]);
-    if (a.norm) norm_row(y, a, D, n_plain, n_pairs, true);
+    if (a.norm) norm_row(y, a, D, n_plain, n_pairs);
     if constexpr (kW == 0) {
       rotate(y.r[0], a.rot, angles_shared(a.rot, pos));    // (zeros where a lane has none)
     } else {
@@ -523,66 +520,107 @@ __global__ void __launch_bounds__(32 * kWarps, kAppendBlocks) kv_append_kernel(c
   }
 }
 
-// Latent rows [norm(c) | rotated r] of new tokens into their slots; e4m3: r as a high and a low code.
+// Latent rows [norm(c) | rotated r] of new tokens into their slots; e4m3: r as a high and a low code.  A half-warp a
+// token (four 16-byte chunks a lane, and its rotary part fills sixteen lanes): what is done once a row, addresses,
+// reductions and angles, then costs two rows one instruction.  With a warp a token it was 419 instructions a row, and
+// the e4m3 append of 65,536 rows took 35 us.
 template <bool kFp8>
-__global__ void __launch_bounds__(32 * kWarps, kAppendBlocks) latent_append_kernel(const AppendArgs a) {
+__global__ void __launch_bounds__(32 * kWarps, kLatentBlocks) latent_append_kernel(const AppendArgs a) {
   pdl_launch_dependents();
   pdl_wait();
-  const int lane = threadIdx.x & 31, L = a.pool.L;
+  constexpr int kC = kLatMaxDim / 8 / 16;
+  const int w = threadIdx.x & 15, L = a.pool.L;
   const int nl = L >> 3, n_pairs = a.rot.R >> 2;
-  const long long step = (long long)gridDim.x * kWarps;
-  for (long long t = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5); t < a.T; t += step) {
+  const float inv_l = 1.f / (float)L;
+  const long long step = 2LL * gridDim.x * kWarps;
+  // (both halves of a warp take the same trips)
+  for (long long t0 = 2LL * (blockIdx.x * kWarps + (threadIdx.x >> 5)); t0 < a.T; t0 += step) {
+    const long long t = t0 + ((threadIdx.x >> 4) & 1);
+    const bool there = t < a.T;
     const uint8_t* k = a.k + t * a.k_st;
-    uint4 x[2];
+    uint4 raw[kC];
     Pairs p;
     p.u = p.v = 0;
 #pragma unroll
-    for (int c = 0; c < 2; ++c)
-      x[c] = lane + 32 * c < nl ? __ldg(reinterpret_cast<const uint4*>(k) + lane + 32 * c) : make_uint4(0, 0, 0, 0);
-    if (lane < n_pairs) p = load_pairs(a.v + t * a.v_st, a.rot, lane);
-    const int pos = __ldg(a.positions + t), row = append_row(a, (int)t);
-    if (row < 0) {
-      if (lane == 0) flag_error(SPA_ERR_INDEX);
-      continue;
+    for (int c = 0; c < kC; ++c)
+      raw[c] = there && w + 16 * c < nl ? __ldg(reinterpret_cast<const uint4*>(k) + w + 16 * c) : make_uint4(0, 0, 0, 0);
+    if (there && w < n_pairs) p = load_pairs(a.v + t * a.v_st, a.rot, w);
+    int row = -1, pos = 0;
+    if (there) {
+      pos = __ldg(a.positions + t);
+      row = append_row(a, (int)t);
+      if (row < 0 && w == 0) flag_error(SPA_ERR_INDEX);
     }
-    Row<1> y;
+    float x[kC][8], r[4];
+    float s = 0.f;
 #pragma unroll
-    for (int c = 0; c < 2; ++c) unpack8(x[c], y.x[c]);
-    unpack(p, y.r[0]);
-    if (a.norm) norm_row(y, a, L, nl, n_pairs, false);
-    rotate(y.r[0], a.rot, angles_shared(a.rot, pos));      // (zeros where a lane has none)
-    uint8_t* dst = a.pool.rows + (size_t)row * a.pool.row_bytes;
-    if constexpr (!kFp8) {
+    for (int c = 0; c < kC; ++c) {
+      unpack8(raw[c], x[c]);
+      if (a.norm) s = squares(x[c], s);
+    }
+    unpack(p, r);
+    if (a.norm) {
 #pragma unroll
-      for (int c = 0; c < 2; ++c)
-        if (lane + 32 * c < nl) reinterpret_cast<uint4*>(dst)[lane + 32 * c] = pack8(y.x[c]);
-      if (lane < n_pairs) store_pairs(dst + 2 * L, a.rot, lane, y.r[0]);
-    } else {
-      const float scale = row_scale(row_amax(y));
-      over_scale(y, scale);
+      for (int o = 8; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+      const float inv = rsqrtf(fmaf(s, inv_l, a.eps));
 #pragma unroll
-      for (int c = 0; c < 2; ++c)
-        if (lane + 32 * c < nl) reinterpret_cast<uint2*>(dst)[lane + 32 * c] = codes8(y.x[c]);
-      if (lane < n_pairs) {
-        uint32_t high[2], low[2];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const float c = y.r[0][2 * i], d = y.r[0][2 * i + 1];
-          high[i] = kvq_e4m3x2(c, d);
-          const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)high[i], __NV_E4M3);
-          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
-          low[i] = kvq_e4m3x2(c - f.x, d - f.y);
+      for (int c = 0; c < kC; ++c) {
+        scale_by(x[c], inv);
+        if (a.weight && w + 16 * c < nl) {
+          float wt[8];
+          weight8(a.weight, a.weight_bf16, 8 * (w + 16 * c), wt);
+          scale_by(x[c], wt);
         }
-        store_codes(dst + L, a.rot, lane, high[0] | (high[1] << 16));
-        store_codes(dst + L + a.rot.R, a.rot, lane, low[0] | (low[1] << 16));
       }
-      if (lane == 0) a.k_scale[row] = scale;
+    }
+    if (w < n_pairs) rotate(r, a.rot, angles(a.rot, pos, w));
+    uint8_t* dst = a.pool.rows + (size_t)(row < 0 ? 0 : row) * a.pool.row_bytes;
+    if constexpr (!kFp8) {
+      if (row >= 0) {
+#pragma unroll
+        for (int c = 0; c < kC; ++c)
+          if (w + 16 * c < nl) reinterpret_cast<uint4*>(dst)[w + 16 * c] = pack8(x[c]);
+        if (w < n_pairs) store_pairs(dst + 2 * L, a.rot, w, r);
+      }
+    } else {
+      float m = abs_max(r, 0.f);
+#pragma unroll
+      for (int c = 0; c < kC; ++c) m = abs_max(x[c], m);
+#pragma unroll
+      for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+      const float scale = row_scale(m);
+      if (kvq_fast_scale(scale)) {
+        const float f = __frcp_rn(scale);
+#pragma unroll
+        for (int c = 0; c < kC; ++c) scale_by(x[c], f);
+        scale_by(r, f);
+      } else {
+        divide(x, r, scale);
+      }
+      if (row >= 0) {
+#pragma unroll
+        for (int c = 0; c < kC; ++c)
+          if (w + 16 * c < nl) reinterpret_cast<uint2*>(dst)[w + 16 * c] = codes8(x[c]);
+        if (w < n_pairs) {
+          uint32_t high[2], low[2];
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            high[i] = kvq_e4m3x2(r[2 * i], r[2 * i + 1]);
+            const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)high[i], __NV_E4M3);
+            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+            low[i] = kvq_e4m3x2(r[2 * i] - f.x, r[2 * i + 1] - f.y);
+          }
+          store_codes(dst + L, a.rot, w, high[0] | (high[1] << 16));
+          store_codes(dst + L + a.rot.R, a.rot, w, low[0] | (low[1] << 16));
+        }
+        if (w == 0) a.k_scale[row] = scale;
+      }
     }
   }
 }
 
-unsigned append_blocks(int T, int sms) {
-  const long long b = ((long long)T + kWarps - 1) / kWarps, cap = (long long)kAppendBlocks * sms;
+unsigned append_blocks(long long warps, long long cap) {
+  const long long b = (warps + kWarps - 1) / kWarps;
   return (unsigned)(b < cap ? b : cap);
 }
 
@@ -599,14 +637,14 @@ cudaError_t launch_rope(const RopeArgs& a, bool norm, int sms, cudaStream_t stre
 }
 
 cudaError_t launch_kv_append(const AppendArgs& a, bool fp8, int sms, cudaStream_t stream) {
-  const unsigned blocks = append_blocks(a.T, sms);
+  const unsigned blocks = append_blocks(a.T, 2LL * kAppendBlocks * sms);
   const auto kern = a.rot.R <= 64 ? (fp8 ? kv_append_kernel<true, 0> : kv_append_kernel<false, 0>)
                                   : (fp8 ? kv_append_kernel<true, 2> : kv_append_kernel<false, 2>);
   return launch_with_pdl(kern, dim3(blocks), dim3(32 * kWarps), 0, stream, 2LL * blocks <= sms, a);
 }
 
 cudaError_t launch_latent_append(const AppendArgs& a, bool fp8, int sms, cudaStream_t stream) {
-  const unsigned blocks = append_blocks(a.T, sms);
+  const unsigned blocks = append_blocks(((long long)a.T + 1) / 2, (long long)kLatentBlocks * sms);
   return launch_with_pdl(fp8 ? latent_append_kernel<true> : latent_append_kernel<false>, dim3(blocks),
                          dim3(32 * kWarps), 0, stream, 2LL * blocks <= sms, a);
 }
