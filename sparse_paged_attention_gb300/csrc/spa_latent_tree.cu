@@ -17,17 +17,19 @@
 // a CTA reads its share of channels of all entries besides its entries' whole rows: 1.85 times the tile.
 //
 // TMEM of a CTA (rows 0-63 in lanes 0-63 and, their other half of the columns, in lanes 64-127): O 256
-// columns, two S of 64.  Shared memory: q, P, and two rings of cached rows: K (the CTA's own 64 entries of a tile,
+// columns, four S of 64.  Shared memory: q, P, and two rings of cached rows: K (the CTA's own 64 entries of a tile,
 // whole rows, three 128-byte chunks a fill) and V (its channels of all 128 entries, two chunks of 64 a fill).
 //
-//   warps 0-7    softmax: a thread has a row and 32 of a tile's entries; epilogue
-//   warps 8, 11  (of the first CTA) issue the MMAs of S, and those of O
-//   warp 9       schedule, page tables
-//   warp 10      sees every fill of V land, cleans it where a tile holds what not all rows may see, and tells the
-//                first CTA
-//   warps 12-15  q of a unit; warp 12 the copies of V, warp 13 those of K, which complete on the first CTA's
-//                barrier.  Where pages are not a multiple of eight entries, all cached
-//                rows by cp.async
+//   softmax warps  (8, e4m3 16) a thread has a row and 32 (16) of a tile's entries; epilogue
+//   roles 0, 3     (of the first CTA) issue the MMAs of S, and those of O
+//   role 1         schedule, page tables
+//   role 2         sees every fill of V land, cleans it where a tile holds what not all rows may see, and tells the
+//                  first CTA
+//   roles 4-7      q of a unit; role 4 the copies of V, role 5 those of K, which complete on the first CTA's
+//                  barrier.  Where pages are not a multiple of eight entries, all cached rows by cp.async
+//
+// The running maximum of a row, which its 4 (8) threads have to agree on, costs no barrier: a thread's maximum of
+// tile k + 1 is put into shared memory before the exponentials of tile k, and read a tile later.
 //
 // A role's code runs once a tile, from the second-level instruction cache (some six cycles an instruction), so it is
 // their instruction counts that decide: one warp for all copies and one for all MMAs took 7,100 cycles a tile.
@@ -60,10 +62,11 @@ constexpr int kTile = 128;           // entries of a tile
 constexpr int kChunk = kGroup * 128;
 constexpr int kKFill = 3, kVFill = 2;   // chunks of a fill
 constexpr int kInfos = 4;            // tile infos in flight
-constexpr int kSoftmax = 256;
-constexpr int kThreads = kSoftmax + 8 * 32;
+constexpr int kRoles = 8;            // warps besides the softmax warps
+constexpr int kSBufs = 4;            // S buffers in TMEM
+constexpr int kQScales = 8;          // units whose scales of q may be in use: S runs up to kSBufs tiles ahead
 constexpr int kTmemCols = 512;
-constexpr int kSCol = 256;           // O from column 0, two S of 64 columns
+constexpr int kSCol = 256;           // O from column 0, S of 64 columns each
 constexpr int kUnitCost = 2;         // tiles' worth of a unit's q and epilogue
 constexpr int kMaxSlices = 128;
 
@@ -74,6 +77,12 @@ enum { kFirst = 1, kLast = 2, kFinal = 4, kEnd = 8, kClean = 16 };
 template <bool kFp8>
 struct Cfg {
   static constexpr int kKSlots = 3, kVSlots = kFp8 ? 2 : 4;
+  // Softmax warps: e4m3's longer arithmetic is faster on sixteen (278 us against 308), bf16's on eight (459 against
+  // 484, both at the time)
+  static constexpr int kSoftmaxWarps = kFp8 ? 16 : 8;
+  static constexpr int kThreads = 32 * (kSoftmaxWarps + kRoles);
+  static constexpr int kParts = kSoftmaxWarps / 2, kKeys = kTile / kParts;   // threads of a row, entries of a thread
+  static constexpr int kMaxBytes = kFp8 ? 4 : 2;     // of a partial maximum: e4m3's reference has to be exact
   static constexpr int kCw = kFp8 ? 128 : 64;        // channels of a chunk
   static constexpr int kMaxChunks = kFp8 ? 5 : 9;    // of a row
   static constexpr float kTau = kFp8 ? 5.f : 8.f;    // lazy rescale threshold (log2 units)
@@ -92,9 +101,11 @@ struct Cfg {
   static constexpr int kKOff = kPOff + kPBytes;
   static constexpr int kVOff = kKOff + kKSlots * kKFill * kChunk;
   static constexpr int kVEnd = kVOff + kVSlots * kVFill * kChunk;
-  static constexpr int kRedOff = kVEnd;                            // float [2][4][64]
-  static constexpr int kQScaleOff = kRedOff + 2 * 4 * kRows * 4;   // e4m3: float [2][64]
-  static constexpr int kInfoOff = kQScaleOff + (kFp8 ? 2 * kRows * 4 : 0);
+  static constexpr int kMaxOff = kVEnd;                            // [3 tiles][64 rows][kParts]
+  static constexpr int kMaxTile = kRows * kParts * kMaxBytes;
+  static constexpr int kLOff = kMaxOff + 3 * kMaxTile;             // e4m3: float [kParts][64]
+  static constexpr int kQScaleOff = kLOff + (kFp8 ? kParts * kRows * 4 : 0);   // e4m3: float [kQScales][64]
+  static constexpr int kInfoOff = kQScaleOff + (kFp8 ? kQScales * kRows * 4 : 0);
   static constexpr int kInfoEnd = kInfoOff + kInfos * (int)sizeof(Info);
   // Without boxes, the rows of the tiles' entries: int [kInfos][128].  bf16: in the last slot of V, which is
   // then not used.
@@ -106,7 +117,8 @@ struct Cfg {
   static constexpr int bKFull = 0 /* cp.async */, bKReady = bKFull + kKSlots /* L */, bKEmpty = bKReady + kKSlots /* 2 */,
                        bVFull = bKEmpty + kKSlots, bVReady = bVFull + kVSlots /* L */,
                        bVEmpty = bVReady + kVSlots /* 2 */, bSFull = bVEmpty + kVSlots /* 2 */,
-                       bSEmpty = bSFull + 2 /* L */, bPReady = bSEmpty + 2 /* L */, bPvDone = bPReady + 1 /* 2 */,
+                       bSEmpty = bSFull + kSBufs /* L */, bPReady = bSEmpty + kSBufs /* L */,
+                       bMax = bPReady + 1, bLFull = bMax + 2, bLEmpty = bLFull + 1, bPvDone = bLEmpty + 1 /* 2 */,
                        bQFull = bPvDone + 1 /* L */, bQLocal = bQFull + 1, bQEmpty = bQLocal + 1 /* 2 */,
                        bOFree = bQEmpty + 1 /* L */, bInfoFull = bOFree + 1, bInfoEmpty = bInfoFull + kInfos,
                        bDrain = bInfoEmpty + kInfos, kNumB = bDrain + 2;
@@ -295,6 +307,14 @@ __global__ void __launch_bounds__(256) tree_q_kernel(const __grid_constant__ Lat
   }
 }
 
+// kN consecutive columns of this warp's TMEM lanes.
+template <int kN>
+__device__ __forceinline__ void tmem_ld(uint32_t at, float (&x)[kN]) {
+  static_assert(kN == 16 || kN == 32, "widths of the loads");
+  if constexpr (kN == 16) tmem_ld16(at, x);
+  else tmem_ld32(at, x);
+}
+
 // A 16-byte piece of cached values with zeros for what is not finite.
 template <bool kFp8>
 __device__ __forceinline__ uint4 finite_only(uint4 u) {
@@ -314,12 +334,13 @@ __device__ __forceinline__ uint4 finite_only(uint4 u) {
 }
 
 template <bool kFp8>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<kFp8>::kThreads, 1)
     latent_tree_kernel(const __grid_constant__ TreeParams p) {
   using C = Cfg<kFp8>;
   extern __shared__ __align__(1024) uint8_t sm[];
   const uint32_t sb = smem_u32(sm);
   const int warp = (int)warp_uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
+  const int role = warp - C::kSoftmaxWarps;      // (negative: softmax)
   const int rank = (int)cluster_ctarank();
   const int slice = blockIdx.x >> 1;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + C::kMiscOff + 4);
@@ -338,26 +359,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       mbar_init(BAR(C::bVReady + i), 2);
       mbar_init(BAR(C::bVEmpty + i), 1);
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < kSBufs; ++i) {
       mbar_init(BAR(C::bSFull + i), 1);
-      mbar_init(BAR(C::bSEmpty + i), 16);
+      mbar_init(BAR(C::bSEmpty + i), 2 * C::kSoftmaxWarps);
     }
-    mbar_init(BAR(C::bPReady), 16);
+    for (int i = 0; i < 2; ++i) mbar_init(BAR(C::bMax + i), C::kSoftmaxWarps);
+    mbar_init(BAR(C::bLFull), C::kSoftmaxWarps);
+    mbar_init(BAR(C::bLEmpty), C::kSoftmaxWarps);
+    mbar_init(BAR(C::bPReady), 2 * C::kSoftmaxWarps);
     mbar_init(BAR(C::bPvDone), 1);
     mbar_init(BAR(C::bQFull), kFp8 ? 2 : 8);
     mbar_init(BAR(C::bQLocal), 1);
     mbar_init(BAR(C::bQEmpty), 1);
-    mbar_init(BAR(C::bOFree), 16);
+    mbar_init(BAR(C::bOFree), 2 * C::kSoftmaxWarps);
     for (int i = 0; i < kInfos; ++i) {
       mbar_init(BAR(C::bInfoFull + i), 1);
-      mbar_init(BAR(C::bInfoEmpty + i), rank == 0 ? 15 : 13);   // softmax, cleaning and q warps, MMA warps
+      mbar_init(BAR(C::bInfoEmpty + i), C::kSoftmaxWarps + (rank == 0 ? 7 : 5));   // and the cleaning, q and MMA warps
     }
     mbar_init(BAR(C::bDrain), 1);
     mbar_init(BAR(C::bDrain + 1), 1);
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == 8) {
+  if (role == 0) {
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(sb + C::kMiscOff),
                  "r"(kTmemCols)
                  : "memory");
@@ -381,7 +405,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   // (lanes that copy boxes: chunk of the fill and box of the group)
   const int per_group = kGroup >> p.box_shift, my_c = lane >> (6 - p.box_shift), my_box = lane & (per_group - 1);
   const uint32_t my_off = my_c * kChunk + ((my_box << p.box_shift) << 7);
-  if (warp == 9) {
+  if (role == 1) {
     // ================================ schedule and loads ==================================
     int top = 0, s0 = 0;
     Seq cur = load_seqs(a, 0, top);
@@ -652,7 +676,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
     if (rank == 0 && lane == 0) p.cut[slice] = cut;
     __syncwarp();
-  } else if (warp == 8) {
+  } else if (role == 0) {
     // ================================= MMAs of S ==========================================
     if (rank == 0) {
       // (bit 13 negates A: a negative scale)
@@ -662,13 +686,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const bool lead = elect_one();
       uint32_t units = 0;
       for (int k = 0;; ++k) {
-        const int ri = k % kInfos, sn = k & 1;
+        const int ri = k % kInfos, sn = k % kSBufs;
         if (!warp_wait(BAR(C::bInfoFull + ri), (uint32_t)((k / kInfos) & 1), abort_flag)) break;
         const int flags = (int)warp_uniform(*reinterpret_cast<volatile int*>(&infos[ri].flags));
         if (lead) mbar_arrive(BAR(C::bInfoEmpty + ri));
         if (flags & kEnd) break;
         if ((flags & kFirst) && !warp_wait(BAR(C::bQFull), units++ & 1, abort_flag)) break;
-        if (k >= 2 && !warp_wait(BAR(C::bSEmpty + sn), (uint32_t)(((k >> 1) & 1) ^ 1), abort_flag)) break;
+        if (!warp_wait(BAR(C::bSEmpty + sn), (uint32_t)(((k / kSBufs) & 1) ^ 1), abort_flag)) break;
         const uint32_t dS = tmem + kSCol + sn * 64;
         bool ok = true;
         for (int f = 0; f < k_fills; ++f) {
@@ -725,7 +749,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
       __syncwarp();
     }
-  } else if (warp == 11) {
+  } else if (role == 3) {
     // ================================= MMAs of O ==========================================
     if (rank == 0) {
       // (A: P in bf16, or in e5m2)
@@ -787,7 +811,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
       __syncwarp();
     }
-  } else if (warp == 10) {
+  } else if (role == 2) {
     // ===================== every fill as it lands: cleaned, handed on =====================
     bool ok = true;
     const auto k_part = [&]() {                  // (cp.async)
@@ -854,9 +878,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
       if (flags & kFinal) break;
     }
-  } else if (warp > 11) {
-    // ======= q of every unit; copies of V (warp 12) and K (13), or all rows by cp.async =====
-    const int tid = threadIdx.x - 12 * 32;
+  } else if (role >= 4) {
+    // ======= q of every unit; copies of V (role 4) and K (5), or all rows by cp.async =====
+    const int tid = threadIdx.x - 32 * (C::kSoftmaxWarps + 4);
     const bool lead = elect_one();
     uint32_t units = 0;
     long long fills = 0;
@@ -904,7 +928,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     };
     const auto v_part = [&](int k) {
       const int ri = k % kInfos;
-      if (!p.box || warp == 12) {
+      if (!p.box || role == 4) {
         for (int grp = 0; grp < 2; ++grp) {
           const int row = p.box ? infos[ri].boxes[grp * per_group + my_box] : 0;
           for (int f = 0; f < v_pairs; ++f) {
@@ -940,21 +964,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (!p.box) {
         k_part(ri);
         if (k > 0 && ok) v_part(k - 1);
-      } else if (warp == 13) {
+      } else if (role == 5) {
         k_part(ri);
       }
       if (first && ok) {
         const uint32_t ph = (units & 1) ^ 1;
         ++units;
         if (kFp8) {
-          if (warp == 12) {
+          if (role == 4) {
             ok = warp_wait(BAR(C::bQEmpty), ph, abort_flag);
             if (ok && elect_one()) {
               const long long slot = q_slot(info.tok0, a.H, info.seq, info.unit_row / kUnitRows);
               const uint32_t bytes = (uint32_t)n_chunks * 2 * kChunk;
               mbar_arrive_expect_tx(BAR(C::bQLocal), bytes + kRows * 4);
               bulk_load(sb + C::kQOff, p.q_codes + (slot * 2 + rank) * bytes, bytes, BAR(C::bQLocal));
-              bulk_load(sb + C::kQScaleOff + (units & 1) * kRows * 4, p.q_scale + slot * kUnitRows + rank * kRows, kRows * 4,
+              bulk_load(sb + C::kQScaleOff + (units % kQScales) * kRows * 4, p.q_scale + slot * kUnitRows + rank * kRows, kRows * 4,
                         BAR(C::bQLocal));
             }
             __syncwarp();
@@ -992,59 +1016,52 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
     cp_async_wait_all();
     // copies in flight must land before the CTA ends (at once after a normal run)
-    if (warp == 12 && lane == 0) {
+    if (role == 4 && lane == 0) {
       if (kFp8 && units > 0) mbar_wait_drain(BAR(C::bQLocal), (units - 1) & 1);
       for (long long f = max(0LL, fills - vs.n); f < fills; ++f)
         mbar_wait_drain(BAR(C::bVFull + (int)(f % vs.n)), (uint32_t)((f / vs.n) & 1));
     }
-    if (warp == 13 && lane == 0 && rank == 0)    // (both CTAs' copies of K complete here)
+    if (role == 5 && lane == 0 && rank == 0)    // (both CTAs' copies of K complete here)
       for (long long f = max(0LL, fills - C::kKSlots); f < fills; ++f)
         mbar_wait_drain(BAR(C::bKReady + (int)(f % C::kKSlots)), (uint32_t)((f / C::kKSlots) & 1));
     __syncwarp();
   } else {
     // ================================ softmax and epilogue ================================
     // TMEM lanes 32 quad ..: rows 32 (quad & 1) .., entry group (of S) or channel half (of O) quad >> 1; this
-    // warp takes the columns of half `ch` of each
+    // warp takes part `ch` of each one's columns
+    constexpr int kKeys = C::kKeys, kParts = C::kParts;
+    constexpr int kOCols = 128 / (kParts / 2);   // columns of a 128-channel block of O
     const int quad = warp & 3, ch = warp >> 2, grp = quad >> 1;
-    const int row = (quad & 1) * 32 + lane, word = 2 * grp + ch;
+    const int row = (quad & 1) * 32 + lane, part = kParts / 2 * grp + ch, e0 = kKeys * part;   // first entry of a tile
     const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
-    float* red = reinterpret_cast<float*>(sm + C::kRedOff);
     uint8_t* pb = sm + C::kPOff;
     float m = -INFINITY, l = 0.f;
-    uint32_t units = 0;
-    int reds = 0;
-    bool ok = true;
-    // the four parts' values of this thread's row
-    const auto exchange = [&](float mine, float (&own)[4]) {
-      float* r = red + (reds & 1) * 4 * kRows;
-      ++reds;
-      r[word * kRows + row] = mine;
-      ok = named_bar_and(1, kSoftmax, ok);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) own[e] = r[e * kRows + row];
-      return ok;
+    uint32_t units = 0, units_next = 0;          // begun, by the tile at hand and by the one after it
+    // flags and visible entries (bits) of the tile at hand, and of the one after it
+    int flags = 0, flags_next = 0;
+    uint32_t seen = 0, seen_next = 0;
+    // q's scale for a row of unit u
+    const auto row_arg = [&](uint32_t u) {
+      return kFp8 ? p.scale_log2 * reinterpret_cast<const float*>(sm + C::kQScaleOff)[(u % kQScales) * kRows + row]
+                  : p.scale_log2;
     };
-    // A wait that gives up does not leave the loop: every warp reaches every barrier, and all leave together, where
-    // they agree that one of them gave up.
-    int flags = 0;
-    ok = warp_wait(BAR(C::bInfoFull), 0, abort_flag);
-    const bool any = named_bar_and(1, kSoftmax, ok && !(infos[0].flags & kEnd));
-    for (int k = 0; any && !(flags & kFinal); ++k) {
-      const int ri = k % kInfos, sn = k & 1;
-      if (k > 0) ok = warp_wait(BAR(C::bInfoFull + ri), (uint32_t)((k / kInfos) & 1), abort_flag) && ok;
-      const typename C::Info& info = infos[ri];
-      const int slot = info.slot;
-      flags = info.flags;
-      const bool first = flags & kFirst, last = flags & kLast;
-      const int n_rows = info.rows, first_row = info.first_row;
-      uint32_t seen = info.valid[word];
-      {
-        // entries 32 word + i of the tile, drafted ones by the mask of this row's token
-        const int rel = info.rel + 32 * word;
-        if (rel > -32) {
+    for (int k = -1;; ++k) {
+      if (!(flags & kFinal)) {
+        // ---- maxima of tile k + 1 ----
+        const int n = k + 1, ri = n % kInfos;
+        if (!warp_wait(BAR(C::bInfoFull + ri), (uint32_t)((n / kInfos) & 1), abort_flag)) break;
+        const typename C::Info& info = infos[ri];
+        flags_next = info.flags;
+        if (flags_next & kEnd) break;
+        if (flags_next & kFirst) ++units_next;
+        seen_next = info.valid[e0 >> 5] >> (e0 & 31);
+        if (kKeys < 32) seen_next &= (1u << (kKeys & 31)) - 1u;
+        const int rel = info.rel + e0;
+        if (rel > -kKeys) {
+          // drafted tokens among entries e0 ..: by the mask of this row's token
           const int ur = rank * kRows + row;
           uint32_t bits = 0;
-          if (ur < n_rows) {
+          if (ur < info.rows) {
             const int i = (info.unit_row + ur) / a.H;            // the row's drafted token
             if (a.mask) {
               const uint32_t* mk = a.mask + (size_t)(info.tok0 + i) * a.mask_words;
@@ -1056,92 +1073,127 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 bits = __funnelshift_r(w0, w1, rel & 31);
               }
             } else {
-              const int n = i - rel + 1;                         // entries up to token i's
-              bits = n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u;
+              const int c = i - rel + 1;                         // entries up to token i's
+              bits = c >= 32 ? 0xffffffffu : c <= 0 ? 0u : (1u << c) - 1u;
             }
           }
-          seen &= bits;
+          seen_next &= bits;
         }
+        if (!warp_wait(BAR(C::bSFull + n % kSBufs), (uint32_t)((n / kSBufs) & 1), abort_flag)) break;
+        __syncwarp();
+        tc_fence_after();
+        float x[kKeys];
+        tmem_ld(lanes + kSCol + (n % kSBufs) * 64 + kKeys * ch, x);
+        tmem_wait_ld();
+        const float arg = row_arg(units_next);
+        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        if constexpr (kFp8) {
+          // of the weights that enter the value product, p_j scale_j
+          const float4* ks = reinterpret_cast<const float4*>(info.scale + e0);
+          const float4* ls = reinterpret_cast<const float4*>(info.lscale + e0);
+#pragma unroll
+          for (int j = 0; j < kKeys / 4; ++j) {
+            const float4 c = ks[j], d = ls[j];
+            const float cs[4] = {c.x, c.y, c.z, c.w}, ds[4] = {d.x, d.y, d.z, d.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float z = fmaf(arg, x[4 * j + e] * cs[e], ds[e]);
+              mx[e] = fmaxf(mx[e], (seen_next >> (4 * j + e)) & 1u ? z : -INFINITY);
+            }
+          }
+        } else {
+          if (seen_next != 0xffffffffu) {
+#pragma unroll
+            for (int j = 0; j < kKeys; ++j) x[j] = (seen_next >> j) & 1u ? x[j] : -INFINITY;
+          }
+#pragma unroll
+          for (int j = 0; j < kKeys; ++j) mx[j & 3] = fmaxf(mx[j & 3], x[j]);
+        }
+        float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+        uint8_t* at = sm + C::kMaxOff + (n % 3) * C::kMaxTile + (row * kParts + part) * C::kMaxBytes;
+        // (The place is that of tile n - 3: everybody's P of that tile has been written, as the value products of tile
+        // n - 3 were waited for at tile n - 2.)
+        if (kFp8) *reinterpret_cast<float*>(at) = mt;
+        else *reinterpret_cast<__nv_bfloat16*>(at) = __float2bfloat16(mt * arg);    // (arg > 0)
+        __syncwarp();
+        // (two barriers: a warp is here for tile n + 1 before it has waited for tile n, not for n + 2)
+        if (lane == 0) mbar_arrive(BAR(C::bMax + (n & 1)));
+        __syncwarp();
       }
-      ok = warp_wait(BAR(C::bSFull + sn), (uint32_t)((k >> 1) & 1), abort_flag) && ok;
-      __syncwarp();
-      tc_fence_after();
+      if (k < 0) {
+        flags = flags_next;
+        seen = seen_next;
+        units = units_next;
+        continue;
+      }
+      // ---- weights of tile k ----
+      const int ri = k % kInfos;
+      const typename C::Info& info = infos[ri];
+      const bool first = flags & kFirst;
       if (first) {
-        ++units;
         m = -INFINITY;
         l = 0.f;
       }
-      float x[32];
-      tmem_ld32(lanes + kSCol + sn * 64 + 32 * ch, x);
+      float x[kKeys];
+      tmem_ld(lanes + kSCol + (k % kSBufs) * 64 + kKeys * ch, x);
+      if (!warp_wait(BAR(C::bMax + (k & 1)), (uint32_t)((k >> 1) & 1), abort_flag)) break;
+      float mt;
+      {
+        const uint8_t* at = sm + C::kMaxOff + (k % 3) * C::kMaxTile + row * kParts * C::kMaxBytes;
+        if constexpr (kFp8) {
+          const float4 u = *reinterpret_cast<const float4*>(at), v = *reinterpret_cast<const float4*>(at + 16);
+          mt = fmaxf(fmaxf(fmaxf(u.x, u.y), fmaxf(u.z, u.w)), fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w)));
+        } else {
+          const uint2 u = *reinterpret_cast<const uint2*>(at);
+          mt = fmaxf(fmaxf(bf16_lo(u.x), bf16_hi(u.x)), fmaxf(bf16_lo(u.y), bf16_hi(u.y)));
+        }
+      }
+      // lazy: the reference moves only where it is exceeded by more than tau
+      float al = 1.f;
+      if (mt > m + C::kTau) {
+        al = fast_exp2(m - mt);
+        l *= al;
+        m = mt;
+      }
+      const bool grow = __any_sync(0xffffffffu, al != 1.f);
+      __syncwarp();
       tmem_wait_ld();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive_pair(lead_bar(C::bSEmpty + sn));
-      float arg = p.scale_log2;                  // log2 of the weights: arg x
-      float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+      if (lane == 0) mbar_arrive_pair(lead_bar(C::bSEmpty + k % kSBufs));
+      // (a row without any entry so far: everything is masked, the reference does not matter)
+      const float arg = row_arg(units), ref = m == -INFINITY ? 0.f : m;
       if constexpr (kFp8) {
-        arg *= reinterpret_cast<const float*>(sm + C::kQScaleOff)[(units & 1) * kRows + row];
-        const float4* ks = reinterpret_cast<const float4*>(info.scale + 32 * word);
-        const float4* ls = reinterpret_cast<const float4*>(info.lscale + 32 * word);
+        const float4* ks = reinterpret_cast<const float4*>(info.scale + e0);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float4 c = ks[j], d = ls[j];
-          const float cs[4] = {c.x, c.y, c.z, c.w}, ds[4] = {d.x, d.y, d.z, d.w};
+        for (int j = 0; j < kKeys / 4; ++j) {
+          const float4 c = ks[j];
+          const float cs[4] = {c.x, c.y, c.z, c.w};
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            float& v = x[4 * j + e];
-            v *= cs[e];
-            const float z = fmaf(arg, v, ds[e]);
-            mx[e] = fmaxf(mx[e], (seen >> (4 * j + e)) & 1u ? z : -INFINITY);
-          }
+          for (int e = 0; e < 4; ++e)
+            x[4 * j + e] = (seen >> (4 * j + e)) & 1u ? fast_exp2(fmaf(arg, x[4 * j + e] * cs[e], -ref)) : 0.f;
         }
       } else {
         if (seen != 0xffffffffu) {
 #pragma unroll
-          for (int j = 0; j < 32; ++j) x[j] = (seen >> j) & 1u ? x[j] : -INFINITY;
+          for (int j = 0; j < kKeys; ++j) x[j] = (seen >> j) & 1u ? x[j] : -INFINITY;
         }
 #pragma unroll
-        for (int j = 0; j < 32; ++j) mx[j & 3] = fmaxf(mx[j & 3], x[j]);
-      }
-      float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-      if (!kFp8) mt *= arg;                      // (a positive number)
-      // Most tiles leave every running maximum within tau of what it was: one vote tells, and the maxima are
-      // exchanged only where one has to move.
-      float al = 1.f;
-      bool grow = false;
-      if (!named_bar_and(1, kSoftmax, ok && !(mt > m + C::kTau))) {
-        float own[4];
-        if (!exchange(mt, own)) break;           // (all eight warps, or none)
-        const float t = fmaxf(fmaxf(own[0], own[1]), fmaxf(own[2], own[3]));
-        const float n = t > m + C::kTau ? t : m;
-        if (n != m) {
-          al = fast_exp2(m - n);
-          l *= al;
-          m = n;
-        }
-        grow = __any_sync(0xffffffffu, al != 1.f);
-      }
-      // (a row without any entry so far: everything is masked, the reference does not matter)
-      const float ref = m == -INFINITY ? 0.f : m;
-      if constexpr (kFp8) {
-#pragma unroll
-        for (int j = 0; j < 32; ++j) x[j] = (seen >> j) & 1u ? fast_exp2(fmaf(arg, x[j], -ref)) : 0.f;
-      } else {
-#pragma unroll
-        for (int j = 0; j < 32; j += 2) {
+        for (int j = 0; j < kKeys; j += 2) {
           fma_f32x2(x[j], x[j + 1], arg, -ref);
           x[j] = fast_exp2(x[j]);
           x[j + 1] = fast_exp2(x[j + 1]);
         }
       }
       // the products of the tile before have read P and added to O
-      if (k > 0) ok = warp_wait(BAR(C::bPvDone), (uint32_t)((k - 1) & 1), abort_flag) && ok;
+      if (k > 0 && !warp_wait(BAR(C::bPvDone), (uint32_t)((k - 1) & 1), abort_flag)) break;
       if (grow && !first) {
+        __syncwarp();
         tc_fence_after();
         const int n_mt = kFp8 ? n_half : v_pairs;
 #pragma unroll 1
-        for (int c = 0; c < 2 * n_mt; ++c) {     // 32 columns a time: of 128-channel block c / 2
-          const uint32_t at = lanes + (c >> 1) * 128 + 64 * ch + 32 * (c & 1);
+        for (int c = 0; c < n_mt * kOCols / 32; ++c) {           // 32 columns a time of a 128-channel block
+          const uint32_t at = lanes + c / (kOCols / 32) * 128 + kOCols * ch + c % (kOCols / 32) * 32;
           float o[32];
           tmem_ld32(at, o);
           tmem_wait_ld();
@@ -1154,45 +1206,45 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
       if constexpr (kFp8) {
         // u = kPUnit p scale in f16 as three e5m2 terms, each the nearest to what is left
-        const float4* ks = reinterpret_cast<const float4*>(info.scale + 32 * word);
+        const float4* ks = reinterpret_cast<const float4*>(info.scale + e0);
         const auto upper = [](uint32_t f16x2) { return (f16x2 + 0x00800080u) & 0xff00ff00u; };
+        uint32_t w[3][4];                        // of each term one 16-byte unit: sixteen entries
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {            // sixteen entries: a 16-byte unit of each term
-          uint32_t w[3][4];
+        for (int q = 0; q < 4; ++q) {
+          const float4 c = ks[q];
+          const float* e = x + 4 * q;
+          // (a weight of zero stays one, whatever the scale of a row that is not seen)
+          const float f[4] = {e[0] == 0.f ? 0.f : e[0] * c.x, e[1] == 0.f ? 0.f : e[1] * c.y,
+                              e[2] == 0.f ? 0.f : e[2] * c.z, e[3] == 0.f ? 0.f : e[3] * c.w};
+          uint32_t t[3][2];
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const float4 c = ks[4 * u + q];
-            const float* e = x + 16 * u + 4 * q;
-            const float f[4] = {e[0] == 0.f ? 0.f : e[0] * c.x, e[1] == 0.f ? 0.f : e[1] * c.y,
-                                e[2] == 0.f ? 0.f : e[2] * c.z, e[3] == 0.f ? 0.f : e[3] * c.w};
-            uint32_t t[3][2];
+          for (int z = 0; z < 2; ++z) {
+            __half2 y = __floats2half2_rn(f[2 * z], f[2 * z + 1]);
 #pragma unroll
-            for (int z = 0; z < 2; ++z) {
-              __half2 y = __floats2half2_rn(f[2 * z], f[2 * z + 1]);
-#pragma unroll
-              for (int i = 0; i < 3; ++i) {
-                t[i][z] = upper(*reinterpret_cast<const uint32_t*>(&y));
-                if (i < 2) y = __hsub2(y, *reinterpret_cast<const __half2*>(&t[i][z]));
-              }
+            for (int i = 0; i < 3; ++i) {
+              t[i][z] = upper(*reinterpret_cast<const uint32_t*>(&y));
+              if (i < 2) y = __hsub2(y, *reinterpret_cast<const __half2*>(&t[i][z]));
             }
-#pragma unroll
-            for (int i = 0; i < 3; ++i) w[i][q] = __byte_perm(t[i][0], t[i][1], 0x7531);
           }
-          const int at = row * 128 + (((2 * word + u) ^ (row & 7)) << 4);
 #pragma unroll
-          for (int i = 0; i < 3; ++i)
-            *reinterpret_cast<uint4*>(pb + i * kChunk + at) = make_uint4(w[i][0], w[i][1], w[i][2], w[i][3]);
+          for (int i = 0; i < 3; ++i) w[i][q] = __byte_perm(t[i][0], t[i][1], 0x7531);
         }
+        const int at = row * 128 + ((part ^ (row & 7)) << 4);
+#pragma unroll
+        for (int i = 0; i < 3; ++i)
+          *reinterpret_cast<uint4*>(pb + i * kChunk + at) = make_uint4(w[i][0], w[i][1], w[i][2], w[i][3]);
       } else {
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {            // 16-byte unit: eight entries
+        for (int u = 0; u < kKeys / 8; ++u) {    // 16-byte unit: eight entries
           const float* e = x + 8 * u;
-          *reinterpret_cast<uint4*>(pb + grp * kChunk + row * 128 + (((4 * ch + u) ^ (row & 7)) << 4)) =
+          *reinterpret_cast<uint4*>(pb + grp * kChunk + row * 128 + (((kKeys / 8 * ch + u) ^ (row & 7)) << 4)) =
               make_uint4(pack_bf16x2(e[0], e[1]), pack_bf16x2(e[2], e[3]), pack_bf16x2(e[4], e[5]),
                          pack_bf16x2(e[6], e[7]));
         }
       }
       fence_proxy_async_smem();
+      __syncwarp();
+      const int slot = info.slot, n_rows = info.rows, first_row = info.first_row;
       __syncwarp();
       if (lane == 0) {
         mbar_arrive_pair(lead_bar(C::bPReady));
@@ -1201,25 +1253,39 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       // (nobody waits for the denominators)
       float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int j = 0; j < 32; j += 2) add_f32x2(sum[j & 2], sum[(j & 2) + 1], x[j], x[j + 1]);
+      for (int j = 0; j < kKeys; j += 2) add_f32x2(sum[j & 2], sum[(j & 2) + 1], x[j], x[j + 1]);
       l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-      if (last) {
+      if (flags & kLast) {
         // ---- epilogue: denominators, then O ----
-        float own[4];
-        if (!exchange(l, own)) break;
-        const float ls = (own[0] + own[1]) + (own[2] + own[3]);
+        if (!warp_wait(BAR(C::bPvDone), (uint32_t)(k & 1), abort_flag)) break;
+        // The parts' sums.  bf16: in the place of the maxima of tiles k and k - 1, which everybody has read by now;
+        // whoever goes on to the maxima of tile k + 2 waits until everybody has read the sums.
+        const auto sums = [&](int e) {
+          return reinterpret_cast<float*>(kFp8 ? sm + C::kLOff + e * kRows * 4
+                                               : sm + C::kMaxOff + (k + (e < 2 ? 0 : 2)) % 3 * C::kMaxTile +
+                                                     (e & 1) * kRows * 4);
+        };
+        sums(part)[row] = l;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(BAR(C::bLFull));
+        if (!warp_wait(BAR(C::bLFull), (units - 1) & 1, abort_flag)) break;
+        float ls = 0.f;
+#pragma unroll
+        for (int e = 0; e < kParts; ++e) ls += sums(e)[row];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(BAR(C::bLEmpty));
         // (0: no entry at all.  A NaN among the scores is in the sum, whatever the maximum is.)
         const float inv = ls == 0.f ? 0.f : (kFp8 ? 1.f / kPUnit : 1.f) / ls;
         const int ur = rank * kRows + row;
         const bool mine = ur < n_rows;
         const size_t prow = ((size_t)slice * 2 + (slot > 0 ? 1 : 0)) * kUnitRows + ur;
-        if (slot >= 0 && word == 0) p.lse[prow] = ls == 0.f ? -INFINITY : m + __log2f(ls);
-        ok = warp_wait(BAR(C::bPvDone), (uint32_t)(k & 1), abort_flag) && ok;
+        if (slot >= 0 && part == 0) p.lse[prow] = ls == 0.f ? -INFINITY : m + __log2f(ls);
+        __syncwarp();
         tc_fence_after();
         const int n_mt = kFp8 ? n_half : v_pairs;
 #pragma unroll 1
-        for (int c = 0; c < 2 * n_mt; ++c) {
-          const int col = 64 * ch + 32 * (c & 1), block = c >> 1;
+        for (int c = 0; c < n_mt * kOCols / 32; ++c) {
+          const int block = c / (kOCols / 32), col = kOCols * ch + c % (kOCols / 32) * 32;
           const int d = grp * n_half * C::kCw + block * 128 + col;
           // (bf16: the last block of an odd number of chunks is one chunk wide)
           const bool there = (kFp8 || 2 * block + 1 < n_half || col < 64) && d < L;
@@ -1247,7 +1313,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive_pair(lead_bar(C::bOFree));
+        if (!warp_wait(BAR(C::bLEmpty), (units - 1) & 1, abort_flag)) break;
       }
+      if (flags & kFinal) break;
+      flags = flags_next;
+      seen = seen_next;
+      units = units_next;
     }
   }
 #undef BAR
@@ -1255,7 +1326,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   tc_fence_before();
   cluster_arrive();
   cluster_wait();
-  if (warp == 8) {
+  if (role == 0) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
   }
@@ -1416,9 +1487,9 @@ cudaError_t launch_latent_tree(const LatentTreeArgs& a, bool fp8, void* workspac
     if (e != cudaSuccess) return e;
   }
   if (fp8)
-    e = launch_with_pdl(latent_tree_kernel<true>, dim3(2 * p.slices), dim3(kThreads), Cfg<true>::kSmem, stream, true, p);
+    e = launch_with_pdl(latent_tree_kernel<true>, dim3(2 * p.slices), dim3(Cfg<true>::kThreads), Cfg<true>::kSmem, stream, true, p);
   else
-    e = launch_with_pdl(latent_tree_kernel<false>, dim3(2 * p.slices), dim3(kThreads), Cfg<false>::kSmem, stream, false,
+    e = launch_with_pdl(latent_tree_kernel<false>, dim3(2 * p.slices), dim3(Cfg<false>::kThreads), Cfg<false>::kSmem, stream, false,
                         p);
   if (e != cudaSuccess) return e;
   const long long units = (rows * ((a.pool.L + 127) / 128) + kMergeWarps - 1) / kMergeWarps;
