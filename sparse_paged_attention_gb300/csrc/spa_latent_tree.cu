@@ -183,6 +183,17 @@ __device__ __forceinline__ void mbar_arrive_pair(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 
+// Waits whose polls are out of line.  Each role's loop is fetched anew every tile, and with the polls of some forty
+// waits in line the kernel was 139 KB of code, whose fetching took 5.6 of every 16 cycles of a warp.
+__device__ __noinline__ bool wait_on(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag));
+}
+__device__ __forceinline__ bool tree_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
+  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+  return wait_on(bar, parity, abort_flag);
+}
+__device__ __noinline__ void drain(uint32_t bar, uint32_t parity) { mbar_wait_drain(bar, parity); }
+
 // Copies of a CTA of the pair into its own shared memory that complete on a barrier of the first CTA.
 __device__ __forceinline__ void tma_row_pair(uint32_t dst, const CUtensorMap* map, int x, int r, uint32_t bar) {
   asm volatile(
@@ -212,6 +223,8 @@ struct Slots {
   }
 };
 
+__device__ __noinline__ long long quotient(long long x, long long y) { return x / y; }
+
 // A sequence as the schedule sees it: its tokens and entries, units and tiles of a unit (no units: none to do).
 struct Seq {
   int lo, n, ctx, tiles;
@@ -219,7 +232,7 @@ struct Seq {
   bool bad;
 };
 // Sequences b0 + lane; `top`: the largest bound before them, and then after.
-__device__ __forceinline__ Seq load_seqs(const LatentTreeArgs& a, int b0, int& top) {
+__device__ __noinline__ Seq load_seqs(const LatentTreeArgs& a, int b0, int& top) {
   const int lane = threadIdx.x & 31, b = b0 + lane;
   Seq s = {};
   int hi = 0;
@@ -428,9 +441,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<kFp8>::kThreads,
     // The line: a unit that begins at w has its tile 0 there, and tile j > 0 at w + cost + j.  A slice takes the
     // tiles from per * slice to before per * (slice + 1).  (cost < per, so that a unit has tiles in every slice
     // from its first to its last.)
-    const long long each = (tiles + p.slices - 1) / p.slices;
+    const long long each = quotient(tiles + p.slices - 1, p.slices);
     const long long cost = min((long long)(units > 1 ? kUnitCost : 0), max(each, 1LL) - 1);
-    const long long per = max((tiles + cost * units + p.slices - 1) / p.slices, 1LL);
+    const long long per = max(quotient(tiles + cost * units + p.slices - 1, p.slices), 1LL);
     const long long begin = per * slice, end = begin + per;
     int it_s = 0;                                // next tile: sequence (in the chunk), unit, tile of the unit
     long long it_u = 0, w_unit = 0, left_all = 0;
@@ -452,7 +465,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<kFp8>::kThreads,
         const long long w = w0 + sum - mine;
         const auto before = [&](long long x) {   // tiles of this lane's sequence before x
           if (x <= w || s.units == 0) return 0LL;
-          const long long u = min((x - w) / span, s.units);
+          const long long u = min(quotient(x - w, span), s.units);
           const long long y = x - w - u * span;
           return u * s.tiles + (u < s.units && y > 0 ? min((long long)s.tiles, max(1LL, y - cost)) : 0);
         };
@@ -467,8 +480,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<kFp8>::kThreads,
           it_s = k;
           const long long l = __shfl_sync(0xffffffffu, lo, k), wk = __shfl_sync(0xffffffffu, w, k);
           const int tl = __shfl_sync(0xffffffffu, s.tiles, k);
-          it_u = l / tl;
-          it_j = (int)(l % tl);
+          it_u = quotient(l, tl);
+          it_j = (int)(l - it_u * tl);
           w_unit = wk + it_u * (tl + cost);
         }
         w0 += __shfl_sync(0xffffffffu, sum, 31);
@@ -511,7 +524,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<kFp8>::kThreads,
         const long long unit_row = it_u * kUnitRows;
         cut.row = (int)((long long)u_lo * a.H + unit_row);
         cut.rows = (int)min((long long)kUnitRows, (long long)u_n * a.H - unit_row);
-        cut.last = (int)((w_unit + cost + u_tiles - 1) / per);
+        cut.last = (int)quotient(w_unit + cost + u_tiles - 1, per);
       }
     };
     struct Tile {
@@ -521,14 +534,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<kFp8>::kThreads,
     const auto page_of = [&](int key) { return a.pool.ps_shift >= 0 ? key >> a.pool.ps_shift : key / a.pool.ps; };
     const int my_key = p.box ? lane << p.box_shift : lane;        // first entry of this lane's box
     const bool has_box = p.box && my_key < kTile;
-    if (left_all > 0) begin_unit();
     const auto next_tile = [&](Tile& x) {        // the next tile, its block-table reads under way
       x.flags = kEnd;
       if (left_all == 0) return;
       if (left == 0) {
-        w_unit += cost + u_tiles;
-        ++it_u;
-        it_j = 0;
+        if (u_tiles > 0) {                       // (0: the line's first unit, which may begin at any tile)
+          w_unit += cost + u_tiles;
+          ++it_u;
+          it_j = 0;
+        }
         begin_unit();
       }
       const bool last = left == 1 || left_all == 1;
@@ -560,10 +574,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<kFp8>::kThreads,
     bool ok = true;
     Tile nxt = {}, x = {};
     int box_rows = 0;
-    next_tile(nxt);
-    for (int k = 0; ok; ++k) {
+    for (int k = -1; ok; ++k) {
       x = nxt;
       const int seq = u_seq;
+      if (k < 0 || !(x.flags & (kEnd | kFinal))) next_tile(nxt);
+      if (k < 0) continue;
       // rows of the tile
       int rows4[4];
       uint32_t valid[4];
@@ -613,10 +628,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<kFp8>::kThreads,
         for (int e = 0; e < 4; ++e)
           if (rows4[e] >= 0) sc[e] = __ldg(a.pool.scale + rows4[e]);
       }
-      if (!(x.flags & kEnd)) next_tile(nxt);
       // publish the tile (before its copies: the MMAs go by its flags)
       const int ri = k % kInfos;
-      ok = warp_wait(BAR(C::bInfoEmpty + ri), ((k / kInfos) & 1) ^ 1, abort_flag);
+      ok = tree_wait(BAR(C::bInfoEmpty + ri), ((k / kInfos) & 1) ^ 1, abort_flag);
       if (!ok) break;
       typename C::Info& info = infos[ri];
       if (x.flags & kEnd) {                      // (nothing to do at all: k is 0)
@@ -687,16 +701,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<kFp8>::kThreads,
       uint32_t units = 0;
       for (int k = 0;; ++k) {
         const int ri = k % kInfos, sn = k % kSBufs;
-        if (!warp_wait(BAR(C::bInfoFull + ri), (uint32_t)((k / kInfos) & 1), abort_flag)) break;
+        if (!tree_wait(BAR(C::bInfoFull + ri), (uint32_t)((k / kInfos) & 1), abort_flag)) break;
         const int flags = (int)warp_uniform(*reinterpret_cast<volatile int*>(&infos[ri].flags));
         if (lead) mbar_arrive(BAR(C::bInfoEmpty + ri));
         if (flags & kEnd) break;
-        if ((flags & kFirst) && !warp_wait(BAR(C::bQFull), units++ & 1, abort_flag)) break;
-        if (!warp_wait(BAR(C::bSEmpty + sn), (uint32_t)(((k / kSBufs) & 1) ^ 1), abort_flag)) break;
+        if ((flags & kFirst) && !tree_wait(BAR(C::bQFull), units++ & 1, abort_flag)) break;
+        if (!tree_wait(BAR(C::bSEmpty + sn), (uint32_t)(((k / kSBufs) & 1) ^ 1), abort_flag)) break;
         const uint32_t dS = tmem + kSCol + sn * 64;
         bool ok = true;
+#pragma unroll 1
         for (int f = 0; f < k_fills; ++f) {
-          if (!(ok = warp_wait(BAR(C::bKReady + ks.slot), ks.parity, abort_flag))) break;
+          if (!(ok = tree_wait(BAR(C::bKReady + ks.slot), ks.parity, abort_flag))) break;
           tc_fence_after();
           // (the loops that issue are short, without predicates in whole chunks, and all but the issue itself is the
           // whole warp's, so that it stays in uniform registers)
@@ -745,7 +760,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<kFp8>::kThreads,
       if (lead) {
         asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(BAR(C::bDrain))
                      : "memory");
-        mbar_wait_drain(BAR(C::bDrain), 0);
+        drain(BAR(C::bDrain), 0);
       }
       __syncwarp();
     }
@@ -759,20 +774,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<kFp8>::kThreads,
       uint32_t units = 0;
       for (int k = 0;; ++k) {
         const int ri = k % kInfos;
-        if (!warp_wait(BAR(C::bInfoFull + ri), (uint32_t)((k / kInfos) & 1), abort_flag)) break;
+        if (!tree_wait(BAR(C::bInfoFull + ri), (uint32_t)((k / kInfos) & 1), abort_flag)) break;
         const int flags = (int)warp_uniform(*reinterpret_cast<volatile int*>(&infos[ri].flags));
         if (lead) mbar_arrive(BAR(C::bInfoEmpty + ri));
         if (flags & kEnd) break;
-        if (!warp_wait(BAR(C::bPReady), (uint32_t)(k & 1), abort_flag)) break;
+        if (!tree_wait(BAR(C::bPReady), (uint32_t)(k & 1), abort_flag)) break;
         const bool first = flags & kFirst;
         // (O of the unit before has been stored)
-        if (first && units++ > 0 && !warp_wait(BAR(C::bOFree), units & 1, abort_flag)) break;
+        if (first && units++ > 0 && !tree_wait(BAR(C::bOFree), units & 1, abort_flag)) break;
         bool ok = true;
+#pragma unroll 1
         for (int grp = 0; grp < 2 && ok; ++grp) {
           const uint64_t pa = desc_add(dp, grp * (kFp8 ? 64 : kChunk));
           const uint32_t acc = !(first && grp == 0);
+#pragma unroll 1
           for (int f = 0; f < v_pairs; ++f) {
-            if (!(ok = warp_wait(BAR(C::bVReady + vs.slot), vs.parity, abort_flag))) break;
+            if (!(ok = tree_wait(BAR(C::bVReady + vs.slot), vs.parity, abort_flag))) break;
             tc_fence_after();
             const int n = min(kVFill, n_half - kVFill * f);        // chunks of the fill
             const uint64_t b = desc_add(dv0, vs.slot * (kVFill * kChunk));
@@ -807,7 +824,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<kFp8>::kThreads,
       if (lead) {
         asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(BAR(C::bDrain + 1))
                      : "memory");
-        mbar_wait_drain(BAR(C::bDrain + 1), 0);
+        drain(BAR(C::bDrain + 1), 0);
       }
       __syncwarp();
     }
@@ -815,8 +832,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<kFp8>::kThreads,
     // ===================== every fill as it lands: cleaned, handed on =====================
     bool ok = true;
     const auto k_part = [&]() {                  // (cp.async)
+#pragma unroll 1
       for (int f = 0; f < k_fills && ok; ++f) {
-        if (!(ok = warp_wait(BAR(C::bKFull + ks.slot), ks.parity, abort_flag))) return;
+        if (!(ok = tree_wait(BAR(C::bKFull + ks.slot), ks.parity, abort_flag))) return;
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive_pair(lead_bar(C::bKReady + ks.slot));
@@ -827,9 +845,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<kFp8>::kThreads,
       const int ri = k % kInfos;
       const typename C::Info& info = infos[ri];
       const bool clean = info.flags & kClean;
+#pragma unroll 1
       for (int grp = 0; grp < 2; ++grp)
+#pragma unroll 1
         for (int f = 0; f < v_pairs; ++f) {
-          if (!(ok = warp_wait(BAR(C::bVFull + vs.slot), vs.parity, abort_flag))) return;
+          if (!(ok = tree_wait(BAR(C::bVFull + vs.slot), vs.parity, abort_flag))) return;
           if (clean) {
             const int n = min(kVFill, n_half - kVFill * f);
             uint8_t* src = sm + C::kVOff + vs.slot * (kVFill * kChunk);
@@ -866,16 +886,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<kFp8>::kThreads,
     };
     for (int k = 0; ok; ++k) {
       const int ri = k % kInfos;
-      if (!warp_wait(BAR(C::bInfoFull + ri), (uint32_t)((k / kInfos) & 1), abort_flag)) break;
+      if (!tree_wait(BAR(C::bInfoFull + ri), (uint32_t)((k / kInfos) & 1), abort_flag)) break;
       const int flags = *reinterpret_cast<volatile int*>(&infos[ri].flags);
       if (flags & kEnd) break;
-      if (p.box) {
-        v_part(k);
-      } else {                                   // (in the order of the copies)
-        k_part();
-        if (k > 0 && ok) v_part(k - 1);
-        if ((flags & kFinal) && ok) v_part(k);
-      }
+      if (!p.box) k_part();
+      if (ok) v_part(k);
       if (flags & kFinal) break;
     }
   } else if (role >= 4) {
@@ -905,8 +920,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<kFp8>::kThreads,
     // K of a tile: this CTA's 64 entries
     const auto k_part = [&](int ri) {
       const int row = p.box ? infos[ri].boxes[rank * per_group + my_box] : 0;
+#pragma unroll 1
       for (int f = 0; f < k_fills; ++f) {
-        if (!(ok = warp_wait(BAR(C::bKEmpty + ks.slot), ks.parity ^ 1, abort_flag))) return;
+        if (!(ok = tree_wait(BAR(C::bKEmpty + ks.slot), ks.parity ^ 1, abort_flag))) return;
         if (p.box) {
           const uint32_t dst = sb + C::kKOff + ks.slot * (kKFill * kChunk), ready = lead_bar(C::bKReady + ks.slot);
           const int c0 = f * kKFill, n = min(kKFill, n_chunks - c0);
@@ -929,10 +945,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<kFp8>::kThreads,
     const auto v_part = [&](int k) {
       const int ri = k % kInfos;
       if (!p.box || role == 4) {
+#pragma unroll 1
         for (int grp = 0; grp < 2; ++grp) {
           const int row = p.box ? infos[ri].boxes[grp * per_group + my_box] : 0;
+#pragma unroll 1
           for (int f = 0; f < v_pairs; ++f) {
-            if (!(ok = warp_wait(BAR(C::bVEmpty + vs.slot), vs.parity ^ 1, abort_flag))) return;
+            if (!(ok = tree_wait(BAR(C::bVEmpty + vs.slot), vs.parity ^ 1, abort_flag))) return;
             const uint32_t dst = sb + C::kVOff + vs.slot * (kVFill * kChunk), full = BAR(C::bVFull + vs.slot);
             const int c0 = rank * n_half + f * kVFill, n = min(kVFill, n_half - f * kVFill);
             if (!p.box) {
@@ -956,23 +974,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<kFp8>::kThreads,
     };
     for (int k = 0; ok; ++k) {
       const int ri = k % kInfos;
-      if (!warp_wait(BAR(C::bInfoFull + ri), (uint32_t)((k / kInfos) & 1), abort_flag)) break;
+      if (!tree_wait(BAR(C::bInfoFull + ri), (uint32_t)((k / kInfos) & 1), abort_flag)) break;
       const typename C::Info& info = infos[ri];
       const int flags = info.flags;
       if (flags & kEnd) break;
       const bool first = flags & kFirst;
-      if (!p.box) {
-        k_part(ri);
-        if (k > 0 && ok) v_part(k - 1);
-      } else if (role == 5) {
-        k_part(ri);
-      }
+      if (!p.box || role == 5) k_part(ri);
       if (first && ok) {
         const uint32_t ph = (units & 1) ^ 1;
         ++units;
         if (kFp8) {
           if (role == 4) {
-            ok = warp_wait(BAR(C::bQEmpty), ph, abort_flag);
+            ok = tree_wait(BAR(C::bQEmpty), ph, abort_flag);
             if (ok && elect_one()) {
               const long long slot = q_slot(info.tok0, a.H, info.seq, info.unit_row / kUnitRows);
               const uint32_t bytes = (uint32_t)n_chunks * 2 * kChunk;
@@ -982,11 +995,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<kFp8>::kThreads,
                         BAR(C::bQLocal));
             }
             __syncwarp();
-            if (ok) ok = warp_wait(BAR(C::bQLocal), ph ^ 1, abort_flag);
+            if (ok) ok = tree_wait(BAR(C::bQLocal), ph ^ 1, abort_flag);
             if (ok && lane == 0) mbar_arrive_pair(lead_bar(C::bQFull));
           }
         } else {
-          ok = warp_wait(BAR(C::bQEmpty), ph, abort_flag);
+          ok = tree_wait(BAR(C::bQEmpty), ph, abort_flag);
           if (ok) {
             const int jj = tid & 7;
 #pragma unroll 1
@@ -1011,19 +1024,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<kFp8>::kThreads,
           }
         }
       }
-      if ((p.box || (flags & kFinal)) && ok) v_part(k);
+      if (ok) v_part(k);
       if (flags & kFinal) break;
     }
     cp_async_wait_all();
     // copies in flight must land before the CTA ends (at once after a normal run)
     if (role == 4 && lane == 0) {
-      if (kFp8 && units > 0) mbar_wait_drain(BAR(C::bQLocal), (units - 1) & 1);
+      if (kFp8 && units > 0) drain(BAR(C::bQLocal), (units - 1) & 1);
       for (long long f = max(0LL, fills - vs.n); f < fills; ++f)
-        mbar_wait_drain(BAR(C::bVFull + (int)(f % vs.n)), (uint32_t)((f / vs.n) & 1));
+        drain(BAR(C::bVFull + (int)(f % vs.n)), (uint32_t)((f / vs.n) & 1));
     }
     if (role == 5 && lane == 0 && rank == 0)    // (both CTAs' copies of K complete here)
       for (long long f = max(0LL, fills - C::kKSlots); f < fills; ++f)
-        mbar_wait_drain(BAR(C::bKReady + (int)(f % C::kKSlots)), (uint32_t)((f / C::kKSlots) & 1));
+        drain(BAR(C::bKReady + (int)(f % C::kKSlots)), (uint32_t)((f / C::kKSlots) & 1));
     __syncwarp();
   } else {
     // ================================ softmax and epilogue ================================
@@ -1049,7 +1062,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<kFp8>::kThreads,
       if (!(flags & kFinal)) {
         // ---- maxima of tile k + 1 ----
         const int n = k + 1, ri = n % kInfos;
-        if (!warp_wait(BAR(C::bInfoFull + ri), (uint32_t)((n / kInfos) & 1), abort_flag)) break;
+        if (!tree_wait(BAR(C::bInfoFull + ri), (uint32_t)((n / kInfos) & 1), abort_flag)) break;
         const typename C::Info& info = infos[ri];
         flags_next = info.flags;
         if (flags_next & kEnd) break;
@@ -1079,7 +1092,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<kFp8>::kThreads,
           }
           seen_next &= bits;
         }
-        if (!warp_wait(BAR(C::bSFull + n % kSBufs), (uint32_t)((n / kSBufs) & 1), abort_flag)) break;
+        if (!tree_wait(BAR(C::bSFull + n % kSBufs), (uint32_t)((n / kSBufs) & 1), abort_flag)) break;
         __syncwarp();
         tc_fence_after();
         float x[kKeys];
@@ -1136,7 +1149,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<kFp8>::kThreads,
       }
       float x[kKeys];
       tmem_ld(lanes + kSCol + (k % kSBufs) * 64 + kKeys * ch, x);
-      if (!warp_wait(BAR(C::bMax + (k & 1)), (uint32_t)((k >> 1) & 1), abort_flag)) break;
+      if (!tree_wait(BAR(C::bMax + (k & 1)), (uint32_t)((k >> 1) & 1), abort_flag)) break;
       float mt;
       {
         const uint8_t* at = sm + C::kMaxOff + (k % 3) * C::kMaxTile + row * kParts * C::kMaxBytes;
@@ -1186,7 +1199,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<kFp8>::kThreads,
         }
       }
       // the products of the tile before have read P and added to O
-      if (k > 0 && !warp_wait(BAR(C::bPvDone), (uint32_t)((k - 1) & 1), abort_flag)) break;
+      if (k > 0 && !tree_wait(BAR(C::bPvDone), (uint32_t)((k - 1) & 1), abort_flag)) break;
       if (grow && !first) {
         __syncwarp();
         tc_fence_after();
@@ -1257,7 +1270,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<kFp8>::kThreads,
       l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
       if (flags & kLast) {
         // ---- epilogue: denominators, then O ----
-        if (!warp_wait(BAR(C::bPvDone), (uint32_t)(k & 1), abort_flag)) break;
+        if (!tree_wait(BAR(C::bPvDone), (uint32_t)(k & 1), abort_flag)) break;
         // The parts' sums.  bf16: in the place of the maxima of tiles k and k - 1, which everybody has read by now;
         // whoever goes on to the maxima of tile k + 2 waits until everybody has read the sums.
         const auto sums = [&](int e) {
@@ -1268,7 +1281,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<kFp8>::kThreads,
         sums(part)[row] = l;
         __syncwarp();
         if (lane == 0) mbar_arrive(BAR(C::bLFull));
-        if (!warp_wait(BAR(C::bLFull), (units - 1) & 1, abort_flag)) break;
+        if (!tree_wait(BAR(C::bLFull), (units - 1) & 1, abort_flag)) break;
         float ls = 0.f;
 #pragma unroll
         for (int e = 0; e < kParts; ++e) ls += sums(e)[row];
@@ -1313,7 +1326,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<kFp8>::kThreads,
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive_pair(lead_bar(C::bOFree));
-        if (!warp_wait(BAR(C::bLEmpty), (units - 1) & 1, abort_flag)) break;
+        if (!tree_wait(BAR(C::bLEmpty), (units - 1) & 1, abort_flag)) break;
       }
       if (flags & kFinal) break;
       flags = flags_next;
