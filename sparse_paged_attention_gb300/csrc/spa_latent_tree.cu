@@ -76,9 +76,8 @@ enum { kFirst = 1, kLast = 2, kFinal = 4, kEnd = 8, kClean = 16 };
 
 template <bool kFp8>
 struct Cfg {
-  static constexpr int kKSlots = 3, kVSlots = kFp8 ? 2 : 4;
-  // Softmax warps: e4m3's longer arithmetic is faster on sixteen (278 us against 308), bf16's on eight (459 against
-  // 484, both at the time)
+  static constexpr int kKSlots = kFp8 ? 2 : 3, kVSlots = kFp8 ? 2 : 3;
+  // Softmax warps: e4m3's longer arithmetic is faster on sixteen (228 us against 250), bf16's on eight (441 against 464).
   static constexpr int kSoftmaxWarps = kFp8 ? 16 : 8;
   static constexpr int kThreads = 32 * (kSoftmaxWarps + kRoles);
   static constexpr int kParts = kSoftmaxWarps / 2, kKeys = kTile / kParts;   // threads of a row, entries of a thread
@@ -98,13 +97,12 @@ struct Cfg {
   static constexpr int kPBytes = kFp8 ? 3 * kChunk : 2 * kChunk;
   static constexpr int kQOff = 0;
   static constexpr int kPOff = kQOff + kQBytes;
-  static constexpr int kKOff = kPOff + kPBytes;
+  static constexpr int kKOff = kPOff + 2 * kPBytes;              // (P of two tiles)
   static constexpr int kVOff = kKOff + kKSlots * kKFill * kChunk;
   static constexpr int kVEnd = kVOff + kVSlots * kVFill * kChunk;
-  static constexpr int kMaxOff = kVEnd;                            // [3 tiles][64 rows][kParts]
+  static constexpr int kMaxOff = kVEnd;                            // [4 tiles][64 rows][kParts]
   static constexpr int kMaxTile = kRows * kParts * kMaxBytes;
-  static constexpr int kLOff = kMaxOff + 3 * kMaxTile;             // e4m3: float [kParts][64]
-  static constexpr int kQScaleOff = kLOff + (kFp8 ? kParts * kRows * 4 : 0);   // e4m3: float [kQScales][64]
+  static constexpr int kQScaleOff = kMaxOff + 4 * kMaxTile;        // e4m3: float [kQScales][64]
   static constexpr int kInfoOff = kQScaleOff + (kFp8 ? kQScales * kRows * 4 : 0);
   static constexpr int kInfoEnd = kInfoOff + kInfos * (int)sizeof(Info);
   // Without boxes, the rows of the tiles' entries: int [kInfos][128].  bf16: in the last slot of V, which is
@@ -118,8 +116,8 @@ struct Cfg {
                        bVFull = bKEmpty + kKSlots, bVReady = bVFull + kVSlots /* L */,
                        bVEmpty = bVReady + kVSlots /* 2 */, bSFull = bVEmpty + kVSlots /* 2 */,
                        bSEmpty = bSFull + kSBufs /* L */, bPReady = bSEmpty + kSBufs /* L */,
-                       bMax = bPReady + 1, bLFull = bMax + 2, bLEmpty = bLFull + 1, bPvDone = bLEmpty + 1 /* 2 */,
-                       bQFull = bPvDone + 1 /* L */, bQLocal = bQFull + 1, bQEmpty = bQLocal + 1 /* 2 */,
+                       bMax = bPReady + 2, bLFull = bMax + 2, bLEmpty = bLFull + 1, bPvDone = bLEmpty + 1 /* 2 */,
+                       bQFull = bPvDone + 2 /* L */, bQLocal = bQFull + 1, bQEmpty = bQLocal + 1 /* 2 */,
                        bOFree = bQEmpty + 1 /* L */, bInfoFull = bOFree + 1, bInfoEmpty = bInfoFull + kInfos,
                        bDrain = bInfoEmpty + kInfos, kNumB = bDrain + 2;
   static constexpr int kMiscOff = kBarOff + kNumB * 8;             // TMEM base, abort flag
@@ -182,6 +180,9 @@ __device__ __forceinline__ void commit_pair(uint32_t bar) {
 __device__ __forceinline__ void mbar_arrive_pair(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
+
+// A value the compiler does not know (so that it makes no copy of a loop for its first trip).
+__device__ __forceinline__ void opaque(int& x) { asm volatile("" : "+r"(x)); }
 
 // Waits whose polls are out of line.  Each role's loop is fetched anew every tile, and with the polls of some forty
 // waits in line the kernel was 139 KB of code, whose fetching took 5.6 of every 16 cycles of a warp.
@@ -328,6 +329,28 @@ __device__ __forceinline__ void tmem_ld(uint32_t at, float (&x)[kN]) {
   else tmem_ld32(at, x);
 }
 
+// 16-byte units u[0 .. 3] of the rows of four neighbouring lanes, transposed: lane j of the four then has unit j of all
+// four rows.
+__device__ __forceinline__ void transpose4(uint4 (&u)[4]) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int s = 1; s <= 2; s *= 2) {
+    const bool up = lane & s;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (i & s) continue;
+      uint4 &x = u[i], &y = u[i + s];            // lanes without bit s give y and take the other's x
+      uint4 give = up ? x : y;
+      give.x = __shfl_xor_sync(0xffffffffu, give.x, s);
+      give.y = __shfl_xor_sync(0xffffffffu, give.y, s);
+      give.z = __shfl_xor_sync(0xffffffffu, give.z, s);
+      give.w = __shfl_xor_sync(0xffffffffu, give.w, s);
+      if (up) x = give;
+      else y = give;
+    }
+  }
+}
+
 // A 16-byte piece of cached values with zeros for what is not finite.
 template <bool kFp8>
 __device__ __forceinline__ uint4 finite_only(uint4 u) {
@@ -346,7 +369,8 @@ __device__ __forceinline__ uint4 finite_only(uint4 u) {
   return u;
 }
 
-template <bool kFp8>
+// kBox: cached rows by tensor maps, else (pages that are not a multiple of eight entries) by cp.async.
+template <bool kFp8, bool kBox>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<kFp8>::kThreads, 1)
     latent_tree_kernel(const __grid_constant__ TreeParams p) {
   using C = Cfg<kFp8>;
@@ -359,16 +383,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<kFp8>::kThreads,
   volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + C::kMiscOff + 4);
   typename C::Info* infos = reinterpret_cast<typename C::Info*>(sm + C::kInfoOff);
 #define BAR(i) (sb + (uint32_t)C::kBarOff + 8u * (uint32_t)(i))
-  const auto lead_bar = [&](int i) { return mapa_cluster(BAR(i), 0); };   // in the first CTA
+  const uint32_t lead_bars = mapa_cluster(sb + (uint32_t)C::kBarOff, 0);
+  const auto lead_bar = [&](int i) { return lead_bars + 8u * (uint32_t)i; };   // in the first CTA
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::kKSlots; ++i) {
       mbar_init(BAR(C::bKFull + i), 128);
-      mbar_init(BAR(C::bKReady + i), p.box ? 1 : 2);     // armed by the first CTA's loader, or both's warps 10
+      mbar_init(BAR(C::bKReady + i), kBox ? 1 : 2);     // armed by the first CTA's loader, or both's warps 10
       mbar_init(BAR(C::bKEmpty + i), 1);
     }
     for (int i = 0; i < C::kVSlots; ++i) {
-      mbar_init(BAR(C::bVFull + i), p.box ? 1 : 128);
+      mbar_init(BAR(C::bVFull + i), kBox ? 1 : 128);
       mbar_init(BAR(C::bVReady + i), 2);
       mbar_init(BAR(C::bVEmpty + i), 1);
     }
@@ -379,8 +404,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<kFp8>::kThreads,
     for (int i = 0; i < 2; ++i) mbar_init(BAR(C::bMax + i), C::kSoftmaxWarps);
     mbar_init(BAR(C::bLFull), C::kSoftmaxWarps);
     mbar_init(BAR(C::bLEmpty), C::kSoftmaxWarps);
-    mbar_init(BAR(C::bPReady), 2 * C::kSoftmaxWarps);
-    mbar_init(BAR(C::bPvDone), 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(BAR(C::bPReady + i), 2 * C::kSoftmaxWarps);
+      mbar_init(BAR(C::bPvDone + i), 1);
+    }
     mbar_init(BAR(C::bQFull), kFp8 ? 2 : 8);
     mbar_init(BAR(C::bQLocal), 1);
     mbar_init(BAR(C::bQEmpty), 1);
@@ -413,8 +440,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<kFp8>::kThreads,
   const int L = a.pool.L, W = a.pool.row_bytes;
   const int n_chunks = (W + 127) >> 7;                         // of a row
   const int n_half = ((L + C::kCw - 1) / C::kCw + 1) >> 1;     // chunks of values a CTA brings
-  const int k_fills = (n_chunks + kKFill - 1) / kKFill, v_pairs = (n_half + 1) >> 1;
-  Slots ks(C::kKSlots), vs(p.box || kFp8 ? C::kVSlots : C::kVSlots - 1);   // where a role is in the rings
+  const int k_fills = (n_chunks + kKFill - 1) / kKFill;
+  const int v_fills = (n_half + kVFill - 1) / kVFill;          // of a group
+  Slots ks(C::kKSlots), vs(kBox || kFp8 ? C::kVSlots : C::kVSlots - 1);   // where a role is in the rings
   // (lanes that copy boxes: chunk of the fill and box of the group)
   const int per_group = kGroup >> p.box_shift, my_c = lane >> (6 - p.box_shift), my_box = lane & (per_group - 1);
   const uint32_t my_off = my_c * kChunk + ((my_box << p.box_shift) << 7);
@@ -532,8 +560,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<kFp8>::kThreads,
       int blk[4];                                // boxed: of box `lane`; else of entries lane + 32 e
     };
     const auto page_of = [&](int key) { return a.pool.ps_shift >= 0 ? key >> a.pool.ps_shift : key / a.pool.ps; };
-    const int my_key = p.box ? lane << p.box_shift : lane;        // first entry of this lane's box
-    const bool has_box = p.box && my_key < kTile;
+    const int my_key = kBox ? lane << p.box_shift : lane;        // first entry of this lane's box
+    const bool has_box = kBox && my_key < kTile;
     const auto next_tile = [&](Tile& x) {        // the next tile, its block-table reads under way
       x.flags = kEnd;
       if (left_all == 0) return;
@@ -558,7 +586,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<kFp8>::kThreads,
       // (the q slot of the unit goes with the sequence; see the published info)
       x.blk[0] = x.blk[1] = x.blk[2] = x.blk[3] = -2;
       const int32_t* bt = a.pool.bt + (size_t)u_seq * a.pool.bt_stride;
-      if (p.box) {
+      if (kBox) {
         if (has_box && my_key < x.valid_len) x.blk[0] = __ldg(bt + page_of(x.base + my_key));
       } else {
 #pragma unroll
@@ -574,7 +602,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<kFp8>::kThreads,
     bool ok = true;
     Tile nxt = {}, x = {};
     int box_rows = 0;
-    for (int k = -1; ok; ++k) {
+    int k = -1;
+    opaque(k);
+#pragma unroll 1
+    for (; ok; ++k) {
       x = nxt;
       const int seq = u_seq;
       if (k < 0 || !(x.flags & (kEnd | kFinal))) next_tile(nxt);
@@ -584,7 +615,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<kFp8>::kThreads,
       uint32_t valid[4];
       bool clean = false;
       if (!(x.flags & kEnd)) {
-        if (p.box) {
+        if (kBox) {
           const bool good = x.blk[0] >= 0 && (long long)x.blk[0] < a.pool.num_blocks;
           if (x.blk[0] != -2 && !good) flag_error(SPA_ERR_INDEX);
           // a box without entries starts past the last row and is filled with zeros
@@ -641,7 +672,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<kFp8>::kThreads,
         }
         break;
       }
-      if (p.box) {
+      if (kBox) {
         if (lane < 16) info.boxes[lane] = box_rows;
       } else {
 #pragma unroll
@@ -699,6 +730,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<kFp8>::kThreads,
       constexpr uint32_t kQChunk = (kFp8 ? 2 : 1) * kChunk;
       const bool lead = elect_one();
       uint32_t units = 0;
+#pragma unroll 1
       for (int k = 0;; ++k) {
         const int ri = k % kInfos, sn = k % kSBufs;
         if (!tree_wait(BAR(C::bInfoFull + ri), (uint32_t)((k / kInfos) & 1), abort_flag)) break;
@@ -772,52 +804,52 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<kFp8>::kThreads,
       const uint64_t dp = sdesc(sb + C::kPOff, 16, 1024), dv0 = sdesc(sb + C::kVOff, kChunk, 1024);
       const bool lead = elect_one();
       uint32_t units = 0;
+#pragma unroll 1
       for (int k = 0;; ++k) {
         const int ri = k % kInfos;
         if (!tree_wait(BAR(C::bInfoFull + ri), (uint32_t)((k / kInfos) & 1), abort_flag)) break;
         const int flags = (int)warp_uniform(*reinterpret_cast<volatile int*>(&infos[ri].flags));
         if (lead) mbar_arrive(BAR(C::bInfoEmpty + ri));
         if (flags & kEnd) break;
-        if (!tree_wait(BAR(C::bPReady), (uint32_t)(k & 1), abort_flag)) break;
+        if (!tree_wait(BAR(C::bPReady + (k & 1)), (uint32_t)((k >> 1) & 1), abort_flag)) break;
         const bool first = flags & kFirst;
         // (O of the unit before has been stored)
         if (first && units++ > 0 && !tree_wait(BAR(C::bOFree), units & 1, abort_flag)) break;
         bool ok = true;
 #pragma unroll 1
-        for (int grp = 0; grp < 2 && ok; ++grp) {
-          const uint64_t pa = desc_add(dp, grp * (kFp8 ? 64 : kChunk));
-          const uint32_t acc = !(first && grp == 0);
-#pragma unroll 1
-          for (int f = 0; f < v_pairs; ++f) {
-            if (!(ok = tree_wait(BAR(C::bVReady + vs.slot), vs.parity, abort_flag))) break;
-            tc_fence_after();
-            const int n = min(kVFill, n_half - kVFill * f);        // chunks of the fill
-            const uint64_t b = desc_add(dv0, vs.slot * (kVFill * kChunk));
-            if (lead) {
-              if (kFp8) {
-#pragma unroll 1
-                for (int c = 0; c < n; ++c) {             // 128 channels of each CTA
-                  const uint64_t bc = desc_add(b, c * kChunk);
-                  const uint32_t d = tmem + f * 256 + c * 128;
+        for (int f = 0; f < 2 * v_fills; ++f) {  // fill f of the tile: of group grp, from chunk c0 on
+          if (!(ok = tree_wait(BAR(C::bVReady + vs.slot), vs.parity, abort_flag))) break;
+          tc_fence_after();
+          const int grp = f >= v_fills, c0 = kVFill * (f - grp * v_fills);
+          const uint64_t pa = desc_add(dp, (k & 1) * C::kPBytes + grp * (kFp8 ? 64 : kChunk));
+          const uint64_t b = desc_add(dv0, vs.slot * (kVFill * kChunk));
+          const uint32_t d = tmem + c0 * C::kCw, acc = !(first && grp == 0);
+          if (lead) {
+            if (kFp8) {
+              // 128 channels of each CTA a chunk
+              const auto block = [&](int c) {
 #pragma unroll
-                  for (int kk = 0; kk < 2; ++kk) {        // 32 entries a step
-                    mma_pair<kFp8>(d, desc_add(pa, kk * 32), desc_add(bc, kk * 4096), idO(256), kk ? 1u : acc);
-                    mma_pair<kFp8>(d, desc_add(pa, kChunk + kk * 32), desc_add(bc, kk * 4096), idO(256), 1u);
-                    mma_pair<kFp8>(d, desc_add(pa, 2 * kChunk + kk * 32), desc_add(bc, kk * 4096), idO(256), 1u);
-                  }
+                for (int kk = 0; kk < 2; ++kk) {          // 32 entries a step
+                  const uint64_t pk = desc_add(pa, kk * 32), bk = desc_add(b, c * kChunk + kk * 4096);
+                  mma_pair<kFp8>(d + c * 128, pk, bk, idO(256), kk ? 1u : acc);
+                  mma_pair<kFp8>(d + c * 128, desc_add(pk, kChunk), bk, idO(256), 1u);
+                  mma_pair<kFp8>(d + c * 128, desc_add(pk, 2 * kChunk), bk, idO(256), 1u);
                 }
-              } else {
-                const uint32_t id = n == 2 ? idO(256) : idO(128);
+              };
+              block(0);
+              if (c0 + 1 < n_half) block(1);
+            } else {
+              // 128 channels of each CTA, or the last 64 of an odd number of chunks
+              const uint32_t id = c0 + 1 < n_half ? idO(256) : idO(128);
 #pragma unroll
-                for (int kk = 0; kk < 4; ++kk)            // 16 entries a step
-                  mma_pair<kFp8>(tmem + f * 128, desc_add(pa, kk * 32), desc_add(b, kk * 2048), id, kk ? 1u : acc);
-              }
-              commit_pair(BAR(C::bVEmpty + vs.slot));
-              if (grp == 1 && f == v_pairs - 1) commit_pair(BAR(C::bPvDone));
+              for (int kk = 0; kk < 4; ++kk)              // 16 entries a step
+                mma_pair<kFp8>(d, desc_add(pa, kk * 32), desc_add(b, kk * 2048), id, kk ? 1u : acc);
             }
-            __syncwarp();
-            vs.next();
+            commit_pair(BAR(C::bVEmpty + vs.slot));
+            if (f == 2 * v_fills - 1) commit_pair(BAR(C::bPvDone + (k & 1)));
           }
+          __syncwarp();
+          vs.next();
         }
         if (!ok || (flags & kFinal)) break;
       }
@@ -846,50 +878,45 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<kFp8>::kThreads,
       const typename C::Info& info = infos[ri];
       const bool clean = info.flags & kClean;
 #pragma unroll 1
-      for (int grp = 0; grp < 2; ++grp)
+      for (int f = 0; f < 2 * v_fills; ++f) {
+        if (!(ok = tree_wait(BAR(C::bVFull + vs.slot), vs.parity, abort_flag))) return;
+        if (clean) {
+          const int grp = f >= v_fills, n = min(kVFill, n_half - kVFill * (f - grp * v_fills));
+          uint8_t* src = sm + C::kVOff + vs.slot * (kVFill * kChunk);
+          const uint32_t lo = info.valid[2 * grp], hi = info.valid[2 * grp + 1];
+          const int ctx = max(-info.rel - grp * kGroup, 0);        // the first row that not all may see
+          // from the first row that needs it: two a step, a half-warp each, four steps' loads in flight
+          const int gone = ~lo ? __ffs(~lo) - 1 : ~hi ? 31 + __ffs(~hi) : kGroup;
+          const int c = (lane >> 3) & 1, half = lane >> 4;
+          uint4* at_row = reinterpret_cast<uint4*>(src + c * kChunk + half * 128) + (lane & 7);
 #pragma unroll 1
-        for (int f = 0; f < v_pairs; ++f) {
-          if (!(ok = tree_wait(BAR(C::bVFull + vs.slot), vs.parity, abort_flag))) return;
-          if (clean) {
-            const int n = min(kVFill, n_half - kVFill * f);
-            uint8_t* src = sm + C::kVOff + vs.slot * (kVFill * kChunk);
-            const uint32_t lo = info.valid[2 * grp], hi = info.valid[2 * grp + 1];
-            const int ctx = max(-info.rel - grp * kGroup, 0);      // the first row that not all may see
-            // from the first row that needs it: two a step, a half-warp each, four steps' loads in flight
-            const int gone = ~lo ? __ffs(~lo) - 1 : ~hi ? 31 + __ffs(~hi) : kGroup;
-            const int c = (lane >> 3) & 1, half = lane >> 4;
-            for (int r0 = min(ctx, gone) & ~1; r0 < kGroup; r0 += 8) {
-              uint4 old[4];
-              uint4* at_row[4];
-              bool exists[4];
+          for (int r0 = min(ctx, gone) & ~7; r0 < kGroup; r0 += 8) {
+            uint4 old[4];
+            const uint32_t exists = (r0 < 32 ? lo >> r0 : hi >> (r0 - 32)) >> half;
 #pragma unroll
-              for (int z = 0; z < 4; ++z) {
-                const int r = min(r0 + 2 * z + half, kGroup - 1);
-                exists[z] = ((r < 32 ? lo >> r : hi >> (r - 32)) & 1u) != 0;
-                at_row[z] = reinterpret_cast<uint4*>(src + c * kChunk + r * 128) + (lane & 7);
-                old[z] = *at_row[z];
-              }
+            for (int z = 0; z < 4; ++z) old[z] = at_row[(r0 + 2 * z) * 8];
 #pragma unroll
-              for (int z = 0; z < 4; ++z) {
-                const uint4 now = exists[z] ? finite_only<kFp8>(old[z]) : make_uint4(0, 0, 0, 0);
-                if (c < n && (now.x != old[z].x || now.y != old[z].y || now.z != old[z].z || now.w != old[z].w))
-                  *at_row[z] = now;
-              }
+            for (int z = 0; z < 4; ++z) {
+              const uint4 now = exists >> (2 * z) & 1u ? finite_only<kFp8>(old[z]) : make_uint4(0, 0, 0, 0);
+              if (c < n && (now.x != old[z].x || now.y != old[z].y || now.z != old[z].z || now.w != old[z].w))
+                at_row[(r0 + 2 * z) * 8] = now;
             }
           }
-          if (clean || !p.box) fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive_pair(lead_bar(C::bVReady + vs.slot));
-          vs.next();
         }
+        if (clean || !kBox) fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_pair(lead_bar(C::bVReady + vs.slot));
+        vs.next();
+      }
       if (lane == 0) mbar_arrive(BAR(C::bInfoEmpty + ri));
     };
+#pragma unroll 1
     for (int k = 0; ok; ++k) {
       const int ri = k % kInfos;
       if (!tree_wait(BAR(C::bInfoFull + ri), (uint32_t)((k / kInfos) & 1), abort_flag)) break;
       const int flags = *reinterpret_cast<volatile int*>(&infos[ri].flags);
       if (flags & kEnd) break;
-      if (!p.box) k_part();
+      if (!kBox) k_part();
       if (ok) v_part(k);
       if (flags & kFinal) break;
     }
@@ -919,11 +946,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<kFp8>::kThreads,
     };
     // K of a tile: this CTA's 64 entries
     const auto k_part = [&](int ri) {
-      const int row = p.box ? infos[ri].boxes[rank * per_group + my_box] : 0;
+      const int row = kBox ? infos[ri].boxes[rank * per_group + my_box] : 0;
 #pragma unroll 1
       for (int f = 0; f < k_fills; ++f) {
         if (!(ok = tree_wait(BAR(C::bKEmpty + ks.slot), ks.parity ^ 1, abort_flag))) return;
-        if (p.box) {
+        if (kBox) {
           const uint32_t dst = sb + C::kKOff + ks.slot * (kKFill * kChunk), ready = lead_bar(C::bKReady + ks.slot);
           const int c0 = f * kKFill, n = min(kKFill, n_chunks - c0);
           if (lead && rank == 0) mbar_arrive_expect_tx(BAR(C::bKReady + ks.slot), (uint32_t)(2 * n * kChunk));
@@ -944,34 +971,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<kFp8>::kThreads,
     };
     const auto v_part = [&](int k) {
       const int ri = k % kInfos;
-      if (!p.box || role == 4) {
+      if (!kBox || role == 4) {
 #pragma unroll 1
-        for (int grp = 0; grp < 2; ++grp) {
-          const int row = p.box ? infos[ri].boxes[grp * per_group + my_box] : 0;
-#pragma unroll 1
-          for (int f = 0; f < v_pairs; ++f) {
-            if (!(ok = tree_wait(BAR(C::bVEmpty + vs.slot), vs.parity ^ 1, abort_flag))) return;
-            const uint32_t dst = sb + C::kVOff + vs.slot * (kVFill * kChunk), full = BAR(C::bVFull + vs.slot);
-            const int c0 = rank * n_half + f * kVFill, n = min(kVFill, n_half - f * kVFill);
-            if (!p.box) {
-              fill(ri, grp, dst, full, c0, n);
-            } else {
-              if (lead) mbar_arrive_expect_tx(full, (uint32_t)(n * kChunk));
-              if (p.box == kGroup && n == kVFill && (c0 + kVFill) * 128 <= W) {
-                if (lead) tma_box3(dst, &p.v_box, 0, row, c0, full);
-              } else if (my_c < n) {
-                tma_row(dst + my_off, &p.chunk, (c0 + my_c) * 128, row, full);
-              }
-              __syncwarp();
-              ++fills;
+        for (int f = 0; f < 2 * v_fills; ++f) {
+          const int grp = f >= v_fills, c = kVFill * (f - grp * v_fills), c0 = rank * n_half + c;
+          const int row = kBox ? infos[ri].boxes[grp * per_group + my_box] : 0, n = min(kVFill, n_half - c);
+          if (!(ok = tree_wait(BAR(C::bVEmpty + vs.slot), vs.parity ^ 1, abort_flag))) return;
+          const uint32_t dst = sb + C::kVOff + vs.slot * (kVFill * kChunk), full = BAR(C::bVFull + vs.slot);
+          if (!kBox) {
+            fill(ri, grp, dst, full, c0, n);
+          } else {
+            if (lead) mbar_arrive_expect_tx(full, (uint32_t)(n * kChunk));
+            if (p.box == kGroup && n == kVFill && (c0 + kVFill) * 128 <= W) {
+              if (lead) tma_box3(dst, &p.v_box, 0, row, c0, full);
+            } else if (my_c < n) {
+              tma_row(dst + my_off, &p.chunk, (c0 + my_c) * 128, row, full);
             }
-            vs.next();
+            __syncwarp();
+            ++fills;
           }
+          vs.next();
         }
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(BAR(C::bInfoEmpty + ri));
     };
+#pragma unroll 1
     for (int k = 0; ok; ++k) {
       const int ri = k % kInfos;
       if (!tree_wait(BAR(C::bInfoFull + ri), (uint32_t)((k / kInfos) & 1), abort_flag)) break;
@@ -979,7 +1004,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<kFp8>::kThreads,
       const int flags = info.flags;
       if (flags & kEnd) break;
       const bool first = flags & kFirst;
-      if (!p.box || role == 5) k_part(ri);
+      if (!kBox || role == 5) k_part(ri);
       if (first && ok) {
         const uint32_t ph = (units & 1) ^ 1;
         ++units;
@@ -999,9 +1024,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<kFp8>::kThreads,
             if (ok && lane == 0) mbar_arrive_pair(lead_bar(C::bQFull));
           }
         } else {
+          // (on its way to L2 while the place is still in use: the unit is announced some tiles ahead)
+          const int jj = tid & 7;
+          for (int i = 0; i < 4; ++i) {
+            const int ur = rank * kRows + (tid >> 3) + 16 * i;
+            if (ur >= info.rows) break;
+            const int sr = info.unit_row + ur;
+            const uint8_t* ql = a.q_latent + (info.tok0 + sr / a.H) * a.ql_st + sr % a.H * a.ql_sh;
+            if (jj * 128 < 2 * L) asm volatile("prefetch.global.L2 [%0];" ::"l"(ql + jj * 128));
+          }
           ok = tree_wait(BAR(C::bQEmpty), ph, abort_flag);
           if (ok) {
-            const int jj = tid & 7;
 #pragma unroll 1
             for (int i = 0; i < 4; ++i) {
               const int r = (tid >> 3) + 16 * i, ur = rank * kRows + r;
@@ -1043,11 +1076,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<kFp8>::kThreads,
     // TMEM lanes 32 quad ..: rows 32 (quad & 1) .., entry group (of S) or channel half (of O) quad >> 1; this
     // warp takes part `ch` of each one's columns
     constexpr int kKeys = C::kKeys, kParts = C::kParts;
+    constexpr uint32_t kAll = 0xffffffffu >> (32 - kKeys);
     constexpr int kOCols = 128 / (kParts / 2);   // columns of a 128-channel block of O
     const int quad = warp & 3, ch = warp >> 2, grp = quad >> 1;
     const int row = (quad & 1) * 32 + lane, part = kParts / 2 * grp + ch, e0 = kKeys * part;   // first entry of a tile
     const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
     uint8_t* pb = sm + C::kPOff;
+    // this thread's units of P (e4m3: its unit of each term)
+    uint8_t* p_at = pb + row * 128 + (kFp8 ? ((part ^ (row & 7)) << 4) : grp * kChunk);
+    uint8_t* max_at = sm + C::kMaxOff + row * kParts * C::kMaxBytes;
     float m = -INFINITY, l = 0.f;
     uint32_t units = 0, units_next = 0;          // begun, by the tile at hand and by the one after it
     // flags and visible entries (bits) of the tile at hand, and of the one after it
@@ -1058,17 +1095,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<kFp8>::kThreads,
       return kFp8 ? p.scale_log2 * reinterpret_cast<const float*>(sm + C::kQScaleOff)[(u % kQScales) * kRows + row]
                   : p.scale_log2;
     };
-    for (int k = -1;; ++k) {
-      if (!(flags & kFinal)) {
-        // ---- maxima of tile k + 1 ----
-        const int n = k + 1, ri = n % kInfos;
+    // Maxima of tile n and weights of tile k, in turn: n runs one ahead of k, but for tiles whose S waits for what may
+    // itself wait for P of the tile before: the first of a unit (its q comes after that tile's V), and all without
+    // boxes (K comes after it).
+    int k = 0, n = 0;
+    bool all = false;                            // the last tile's maxima are done
+#pragma unroll 1
+    for (;;) {
+      if (!all) {
+        // ---- maxima of tile n ----
+        const int ri = n % kInfos;
         if (!tree_wait(BAR(C::bInfoFull + ri), (uint32_t)((n / kInfos) & 1), abort_flag)) break;
         const typename C::Info& info = infos[ri];
         flags_next = info.flags;
         if (flags_next & kEnd) break;
+        if (n == k || (kBox && !(flags_next & kFirst))) {
         if (flags_next & kFirst) ++units_next;
-        seen_next = info.valid[e0 >> 5] >> (e0 & 31);
-        if (kKeys < 32) seen_next &= (1u << (kKeys & 31)) - 1u;
+        seen_next = info.valid[e0 >> 5] >> (e0 & 31) & kAll;
         const int rel = info.rel + e0;
         if (rel > -kKeys) {
           // drafted tokens among entries e0 ..: by the mask of this row's token
@@ -1115,29 +1158,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<kFp8>::kThreads,
             }
           }
         } else {
-          if (seen_next != 0xffffffffu) {
+          if (seen_next != kAll) {
 #pragma unroll
             for (int j = 0; j < kKeys; ++j) x[j] = (seen_next >> j) & 1u ? x[j] : -INFINITY;
           }
 #pragma unroll
           for (int j = 0; j < kKeys; ++j) mx[j & 3] = fmaxf(mx[j & 3], x[j]);
         }
-        float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-        uint8_t* at = sm + C::kMaxOff + (n % 3) * C::kMaxTile + (row * kParts + part) * C::kMaxBytes;
-        // (The place is that of tile n - 3: everybody's P of that tile has been written, as the value products of tile
-        // n - 3 were waited for at tile n - 2.)
+        const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+        // (The place is that of tile n - 4, whose maxima everybody has read: its value products were waited for at tile
+        // n - 2.  Two barriers: a warp is here for tile n + 1 after it has waited for tile n, but before others have.)
+        uint8_t* at = max_at + n % 4 * C::kMaxTile + part * C::kMaxBytes;
         if (kFp8) *reinterpret_cast<float*>(at) = mt;
         else *reinterpret_cast<__nv_bfloat16*>(at) = __float2bfloat16(mt * arg);    // (arg > 0)
         __syncwarp();
-        // (two barriers: a warp is here for tile n + 1 before it has waited for tile n, not for n + 2)
         if (lane == 0) mbar_arrive(BAR(C::bMax + (n & 1)));
         __syncwarp();
-      }
-      if (k < 0) {
-        flags = flags_next;
-        seen = seen_next;
-        units = units_next;
-        continue;
+        ++n;
+        all = flags_next & kFinal;
+        if (n == k + 1) {
+          flags = flags_next;
+          seen = seen_next;
+          units = units_next;
+          continue;
+        }
+        }
       }
       // ---- weights of tile k ----
       const int ri = k % kInfos;
@@ -1152,7 +1197,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<kFp8>::kThreads,
       if (!tree_wait(BAR(C::bMax + (k & 1)), (uint32_t)((k >> 1) & 1), abort_flag)) break;
       float mt;
       {
-        const uint8_t* at = sm + C::kMaxOff + (k % 3) * C::kMaxTile + row * kParts * C::kMaxBytes;
+        const uint8_t* at = max_at + k % 4 * C::kMaxTile;
         if constexpr (kFp8) {
           const float4 u = *reinterpret_cast<const float4*>(at), v = *reinterpret_cast<const float4*>(at + 16);
           mt = fmaxf(fmaxf(fmaxf(u.x, u.y), fmaxf(u.z, u.w)), fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w)));
@@ -1187,7 +1232,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<kFp8>::kThreads,
             x[4 * j + e] = (seen >> (4 * j + e)) & 1u ? fast_exp2(fmaf(arg, x[4 * j + e] * cs[e], -ref)) : 0.f;
         }
       } else {
-        if (seen != 0xffffffffu) {
+        if (seen != kAll) {
 #pragma unroll
           for (int j = 0; j < kKeys; ++j) x[j] = (seen >> j) & 1u ? x[j] : -INFINITY;
         }
@@ -1198,30 +1243,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<kFp8>::kThreads,
           x[j + 1] = fast_exp2(x[j + 1]);
         }
       }
-      // the products of the tile before have read P and added to O
-      if (k > 0 && !tree_wait(BAR(C::bPvDone), (uint32_t)((k - 1) & 1), abort_flag)) break;
-      if (grow && !first) {
-        __syncwarp();
-        tc_fence_after();
-        const int n_mt = kFp8 ? n_half : v_pairs;
-#pragma unroll 1
-        for (int c = 0; c < n_mt * kOCols / 32; ++c) {           // 32 columns a time of a 128-channel block
-          const uint32_t at = lanes + c / (kOCols / 32) * 128 + kOCols * ch + c % (kOCols / 32) * 32;
-          float o[32];
-          tmem_ld32(at, o);
-          tmem_wait_ld();
-#pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] *= al;
-          tmem_st32(at, o);
-        }
-        tmem_wait_st();
-        tc_fence_before();
-      }
+      // P in registers: 16-byte units of eight entries, or (e4m3) of sixteen for each term
+      constexpr int kUnits = kFp8 ? 3 : kKeys / 8;
+      uint4 pu[kUnits];
       if constexpr (kFp8) {
         // u = kPUnit p scale in f16 as three e5m2 terms, each the nearest to what is left
         const float4* ks = reinterpret_cast<const float4*>(info.scale + e0);
         const auto upper = [](uint32_t f16x2) { return (f16x2 + 0x00800080u) & 0xff00ff00u; };
-        uint32_t w[3][4];                        // of each term one 16-byte unit: sixteen entries
+        uint32_t w[3][4];
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           const float4 c = ks[q];
@@ -1242,27 +1271,48 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<kFp8>::kThreads,
 #pragma unroll
           for (int i = 0; i < 3; ++i) w[i][q] = __byte_perm(t[i][0], t[i][1], 0x7531);
         }
-        const int at = row * 128 + ((part ^ (row & 7)) << 4);
 #pragma unroll
-        for (int i = 0; i < 3; ++i)
-          *reinterpret_cast<uint4*>(pb + i * kChunk + at) = make_uint4(w[i][0], w[i][1], w[i][2], w[i][3]);
+        for (int i = 0; i < 3; ++i) pu[i] = make_uint4(w[i][0], w[i][1], w[i][2], w[i][3]);
       } else {
 #pragma unroll
-        for (int u = 0; u < kKeys / 8; ++u) {    // 16-byte unit: eight entries
+        for (int u = 0; u < kUnits; ++u) {
           const float* e = x + 8 * u;
-          *reinterpret_cast<uint4*>(pb + grp * kChunk + row * 128 + (((kKeys / 8 * ch + u) ^ (row & 7)) << 4)) =
-              make_uint4(pack_bf16x2(e[0], e[1]), pack_bf16x2(e[2], e[3]), pack_bf16x2(e[4], e[5]),
-                         pack_bf16x2(e[6], e[7]));
+          pu[u] = make_uint4(pack_bf16x2(e[0], e[1]), pack_bf16x2(e[2], e[3]), pack_bf16x2(e[4], e[5]),
+                             pack_bf16x2(e[6], e[7]));
         }
       }
+      // the products of the tile before the last have read P
+      if (k > 1 && !tree_wait(BAR(C::bPvDone + (k & 1)), (uint32_t)(((k >> 1) & 1) ^ 1), abort_flag)) break;
+      if (grow && !first) {
+        // (and those of the last have added to O)
+        if (!tree_wait(BAR(C::bPvDone + ((k - 1) & 1)), (uint32_t)(((k - 1) >> 1) & 1), abort_flag)) break;
+        __syncwarp();
+        tc_fence_after();
+        const int n_mt = (n_half * C::kCw + 127) / 128;
+#pragma unroll 1
+        for (int c = 0; c < n_mt * kOCols / 32; ++c) {           // 32 columns a time of a 128-channel block
+          const uint32_t at = lanes + c / (kOCols / 32) * 128 + kOCols * ch + c % (kOCols / 32) * 32;
+          float o[32];
+          tmem_ld32(at, o);
+          tmem_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] *= al;
+          tmem_st32(at, o);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+      }
+#pragma unroll
+      for (int u = 0; u < kUnits; ++u)
+        *reinterpret_cast<uint4*>(p_at + (k & 1) * C::kPBytes +
+                                  (kFp8 ? u * kChunk : ((kUnits * ch + u) ^ (row & 7)) << 4)) = pu[u];
       fence_proxy_async_smem();
       __syncwarp();
-      const int slot = info.slot, n_rows = info.rows, first_row = info.first_row;
+      if (lane == 0) mbar_arrive_pair(lead_bar(C::bPReady + (k & 1)));
+      int slot = 0, n_rows = 0, first_row = 0;
+      if (flags & kLast) slot = info.slot, n_rows = info.rows, first_row = info.first_row;
       __syncwarp();
-      if (lane == 0) {
-        mbar_arrive_pair(lead_bar(C::bPReady));
-        mbar_arrive(BAR(C::bInfoEmpty + ri));
-      }
+      if (lane == 0) mbar_arrive(BAR(C::bInfoEmpty + ri));
       // (nobody waits for the denominators)
       float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -1270,14 +1320,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<kFp8>::kThreads,
       l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
       if (flags & kLast) {
         // ---- epilogue: denominators, then O ----
-        if (!tree_wait(BAR(C::bPvDone), (uint32_t)(k & 1), abort_flag)) break;
-        // The parts' sums.  bf16: in the place of the maxima of tiles k and k - 1, which everybody has read by now;
-        // whoever goes on to the maxima of tile k + 2 waits until everybody has read the sums.
-        const auto sums = [&](int e) {
-          return reinterpret_cast<float*>(kFp8 ? sm + C::kLOff + e * kRows * 4
-                                               : sm + C::kMaxOff + (k + (e < 2 ? 0 : 2)) % 3 * C::kMaxTile +
-                                                     (e & 1) * kRows * 4);
-        };
+        if (!tree_wait(BAR(C::bPvDone + (k & 1)), (uint32_t)((k >> 1) & 1), abort_flag)) break;
+        // The parts' sums, in P's place: its products are done, and whoever goes on waits until everybody has read them.
+        const auto sums = [&](int e) { return reinterpret_cast<float*>(pb + (k & 1) * C::kPBytes) + e * kRows; };
         sums(part)[row] = l;
         __syncwarp();
         if (lane == 0) mbar_arrive(BAR(C::bLFull));
@@ -1290,12 +1335,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<kFp8>::kThreads,
         // (0: no entry at all.  A NaN among the scores is in the sum, whatever the maximum is.)
         const float inv = ls == 0.f ? 0.f : (kFp8 ? 1.f / kPUnit : 1.f) / ls;
         const int ur = rank * kRows + row;
-        const bool mine = ur < n_rows;
         const size_t prow = ((size_t)slice * 2 + (slot > 0 ? 1 : 0)) * kUnitRows + ur;
         if (slot >= 0 && part == 0) p.lse[prow] = ls == 0.f ? -INFINITY : m + __log2f(ls);
         __syncwarp();
         tc_fence_after();
-        const int n_mt = kFp8 ? n_half : v_pairs;
+        const int n_mt = (n_half * C::kCw + 127) / 128;
 #pragma unroll 1
         for (int c = 0; c < n_mt * kOCols / 32; ++c) {
           const int block = c / (kOCols / 32), col = kOCols * ch + c % (kOCols / 32) * 32;
@@ -1305,21 +1349,37 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<kFp8>::kThreads,
           float o[32];
           tmem_ld32(lanes + block * 128 + col, o);
           tmem_wait_ld();
-          if (there && mine) {                   // (d and L are multiples of 32: all 32 channels exist)
-            if (slot >= 0) {
-              float4* dst = reinterpret_cast<float4*>(p.part + prow * L + d);
+          // (d and L are multiples of 32: all 32 channels exist.)  A lane's sixteen bytes at a time would touch 32 rows a
+          // store; of four lanes' units transposed, a store has 64 bytes of each of eight rows.
 #pragma unroll
-              for (int e = 0; e < 8; ++e)
-                dst[e] = make_float4(o[4 * e] * inv, o[4 * e + 1] * inv, o[4 * e + 2] * inv, o[4 * e + 3] * inv);
-            } else {
-              uint4* dst = reinterpret_cast<uint4*>(a.out + ((size_t)first_row + ur) * L * 2 + d * 2);
+          for (int e = 0; e < 32; ++e) o[e] *= inv;
+          const int u0 = rank * kRows + (row & ~3), unit = lane & 3;
+          const size_t prow0 = ((size_t)slice * 2 + (slot > 0 ? 1 : 0)) * kUnitRows + u0;
+          if (slot >= 0) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              uint4 u[4];
 #pragma unroll
               for (int e = 0; e < 4; ++e)
-                dst[e] = make_uint4(pack_bf16x2(o[8 * e] * inv, o[8 * e + 1] * inv),
-                                    pack_bf16x2(o[8 * e + 2] * inv, o[8 * e + 3] * inv),
-                                    pack_bf16x2(o[8 * e + 4] * inv, o[8 * e + 5] * inv),
-                                    pack_bf16x2(o[8 * e + 6] * inv, o[8 * e + 7] * inv));
+                u[e] = make_uint4(__float_as_uint(o[16 * h + 4 * e]), __float_as_uint(o[16 * h + 4 * e + 1]),
+                                  __float_as_uint(o[16 * h + 4 * e + 2]), __float_as_uint(o[16 * h + 4 * e + 3]));
+              transpose4(u);
+              uint4* dst = reinterpret_cast<uint4*>(p.part + prow0 * L + d + 16 * h) + unit;
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                if (there && u0 + e < n_rows) dst[(size_t)e * (L / 4)] = u[e];
             }
+          } else {
+            uint4 u[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              u[e] = make_uint4(pack_bf16x2(o[8 * e], o[8 * e + 1]), pack_bf16x2(o[8 * e + 2], o[8 * e + 3]),
+                                pack_bf16x2(o[8 * e + 4], o[8 * e + 5]), pack_bf16x2(o[8 * e + 6], o[8 * e + 7]));
+            transpose4(u);
+            uint4* dst = reinterpret_cast<uint4*>(a.out + (((size_t)first_row + u0) * L + d) * 2) + unit;
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (there && u0 + e < n_rows) dst[(size_t)e * (L / 8)] = u[e];
           }
           __syncwarp();                          // (the loads from TMEM are the whole warp's)
         }
@@ -1329,6 +1389,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<kFp8>::kThreads,
         if (!tree_wait(BAR(C::bLEmpty), (units - 1) & 1, abort_flag)) break;
       }
       if (flags & kFinal) break;
+      ++k;                                       // (where n is k now, the next trip sets these)
       flags = flags_next;
       seen = seen_next;
       units = units_next;
@@ -1446,12 +1507,22 @@ Workspace workspace_layout(const LatentTreeArgs& a, bool fp8, int sms) {
   return w;
 }
 
+template <bool kFp8>
+cudaError_t launch_tree(const TreeParams& p, cudaStream_t stream) {
+  using C = Cfg<kFp8>;
+  // (e4m3: a dependent of tree_q_kernel, launched right before)
+  return launch_with_pdl(p.box ? latent_tree_kernel<kFp8, true> : latent_tree_kernel<kFp8, false>, dim3(2 * p.slices),
+                         dim3(C::kThreads), C::kSmem, stream, kFp8, p);
+}
+
 }  // namespace
 
 cudaError_t prepare_latent_tree() {
   const auto most = cudaFuncAttributeMaxDynamicSharedMemorySize;
-  cudaError_t e = cudaFuncSetAttribute(latent_tree_kernel<false>, most, Cfg<false>::kSmem);
-  if (e == cudaSuccess) e = cudaFuncSetAttribute(latent_tree_kernel<true>, most, Cfg<true>::kSmem);
+  cudaError_t e = cudaFuncSetAttribute(latent_tree_kernel<false, true>, most, Cfg<false>::kSmem);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(latent_tree_kernel<false, false>, most, Cfg<false>::kSmem);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(latent_tree_kernel<true, true>, most, Cfg<true>::kSmem);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(latent_tree_kernel<true, false>, most, Cfg<true>::kSmem);
   return e;
 }
 
@@ -1499,11 +1570,8 @@ cudaError_t launch_latent_tree(const LatentTreeArgs& a, bool fp8, void* workspac
                         false, a, p.q_codes, p.q_scale);
     if (e != cudaSuccess) return e;
   }
-  if (fp8)
-    e = launch_with_pdl(latent_tree_kernel<true>, dim3(2 * p.slices), dim3(Cfg<true>::kThreads), Cfg<true>::kSmem, stream, true, p);
-  else
-    e = launch_with_pdl(latent_tree_kernel<false>, dim3(2 * p.slices), dim3(Cfg<false>::kThreads), Cfg<false>::kSmem, stream, false,
-                        p);
+  if (fp8) e = launch_tree<true>(p, stream);
+  else e = launch_tree<false>(p, stream);
   if (e != cudaSuccess) return e;
   const long long units = (rows * ((a.pool.L + 127) / 128) + kMergeWarps - 1) / kMergeWarps;
   return launch_with_pdl(tree_merge_kernel, dim3((unsigned)(units < 4LL * sms ? units : 4LL * sms)), dim3(32 * kMergeWarps),

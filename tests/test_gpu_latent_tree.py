@@ -80,6 +80,9 @@ SHAPES = [  # contexts, drafted, heads, L, R, page
     ([130], [20], 7, 64, 0, 16), ([500, 3], [9, 40], 48, 448, 40, 64), ([129, 66], [31, 65], 24, 192, 16, 40),
     ([30000], [4], 16, 512, 64, 64), ([20] * 70, [1 + i % 3 for i in range(70)], 16, 128, 64, 32),
     ([257, 640, 12], [17, 2, 29], 64, 320, 64, 64),
+    # several tiles and units a pair of CTAs: pages of seven, eight and 64 entries
+    ([5000, 900, 3000], [17, 9, 60], 128, 64, 16, 7), ([9000, 40], [30, 25], 64, 128, 8, 1),
+    ([5000, 900, 3000], [17, 9, 60], 128, 64, 16, 8), ([2500] * 9, [11] * 9, 128, 128, 64, 64),
 ]
 
 
