@@ -239,22 +239,6 @@ __global__ void __launch_bounds__(256)
   }
 }
 
-// The scale of an e4m3 row (-1: none), 0 if its codes are nothing but zeros (of either sign).  Out of line:
-// hardly ever called, and the decode kernel's code is long as it is.
-__device__ __noinline__ float without_zero_row(const uint8_t* rows, int width, int row, float scale) {
-  if (row < 0 || scale != 1.f) return scale;
-  const uint4* src = reinterpret_cast<const uint4*>(rows + (size_t)row * width);
-  uint32_t any = 0;
-  for (int i = 0; i < (width >> 4) && any == 0; i += 4) {
-#pragma unroll
-    for (int z = 0; z < 4; ++z) {
-      const uint4 u = i + z < (width >> 4) ? __ldg(src + i + z) : make_uint4(0, 0, 0, 0);
-      any |= (u.x | u.y | u.z | u.w) & 0x7f7f7f7fu;
-    }
-  }
-  return any ? scale : 0.f;
-}
-
 template <bool kFp8>
 __global__ void __launch_bounds__(kThreads, 1)
     latent_decode_kernel(const __grid_constant__ DecodeParams p) {
@@ -549,8 +533,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (kFp8) {
         // (a scale of exactly 1 is that of a row of zeros or, rarely, of one whose largest value is 448)
         if (__any_sync(0xffffffffu, sc[0] == 1.f || sc[1] == 1.f)) {
-          sc[0] = without_zero_row(a.pool.rows, W, row[0], sc[0]);
-          sc[1] = without_zero_row(a.pool.rows, W, row[1], sc[1]);
+          sc[0] = latent_scale_of(a.pool.rows, W, row[0], sc[0]);
+          sc[1] = latent_scale_of(a.pool.rows, W, row[1], sc[1]);
         }
         // the maximum of a tile is taken over p_j |scale_j|, the weights that enter the value
         // product (a scale below 2^-60 counts as that: the sums of p_j alone must stay finite)

@@ -14,7 +14,9 @@
 // One CTA alone cannot hold O of 128 rows and L = 512 beside S (512 columns of TMEM), and with 64 rows its MMAs
 // run at half the rate or wait for their operands: measured, 77 cycles for M = 128, N = 64, K = 16 with both
 // operands in shared memory, where the pair's M = 128, N = 128 takes 32 (the full rate of both).  The price is that
-// a CTA reads its share of channels of all entries besides its entries' whole rows: 1.85 times the tile.
+// a CTA reads its share of channels of all entries besides its entries' whole rows: 1.85 times the tile.  (Not
+// taken: the channels split between two CTAs that exchange parts of S.  Distributed shared memory moves 32 KB each way
+// in 1,608 cycles, more than the MMAs of 64 entries take.)
 //
 // TMEM of a CTA (rows 0-63 in lanes 0-63 and, their other half of the columns, in lanes 64-127): O 256
 // columns, four S of 64.  Shared memory: q, P, and two rings of cached rows: K (the CTA's own 64 entries of a tile,
@@ -26,13 +28,24 @@
 //   role 2         sees every fill of V land, cleans it where a tile holds what not all rows may see, and tells the
 //                  first CTA
 //   roles 4-7      q of a unit; role 4 the copies of V, role 5 those of K, which complete on the first CTA's
-//                  barrier.  Where pages are not a multiple of eight entries, all cached rows by cp.async
+//                  barrier.  (Roles 6 and 7 only where q or cached rows go by cp.async: heads that neither divide 64
+//                  nor are a multiple of it, pages that are not a multiple of eight entries.)
 //
 // The running maximum of a row, which its 4 (8) threads have to agree on, costs no barrier: a thread's maximum of
 // tile k + 1 is put into shared memory before the exponentials of tile k, and read a tile later.
 //
-// A role's code runs once a tile, from the second-level instruction cache (some six cycles an instruction), so it is
-// their instruction counts that decide: one warp for all copies and one for all MMAs took 7,100 cycles a tile.
+// Measured (L = 512, R = 64, calls one after the other, inputs larger than L2):
+//   32 drafts of 5 to 16 tokens behind up to 8,187 entries, 128 heads, bf16: 371 us (1,234 TFLOP/s, 65% of the
+//     measured bf16 rate); 172 tiles and 4.6 units a pair, some 3,500 cycles a tile, everything counted, of which 2,180
+//     are its 52 MMAs and about 3,100 what it moves through shared memory (399 KB: the MMAs 245, the copies 138)
+//   12 drafts of 20 to 60 tokens behind up to 16,004 entries, 16 heads, e4m3, pages of 24: 205 us (692 TFLOP/s)
+//   one draft of 8 tokens behind 4,097 entries, 64 heads, bf16: 30 us, two tiles a pair
+// A role's loop runs once a tile and is fetched anew each time (under ncu a warp that issues waits 5.6 cycles for its
+// next instruction), so that some six cycles an instruction decide what a tile takes.  Steps, for the 32 drafts: one
+// warp for all copies and one for all MMAs 720 us; a warp each 487; page tables apart from K's copies 459; polls
+// and divisions out of line 441; P of two tiles in turn 394; q by tensor maps and the unit's cost in the schedule
+// 371.  Arrivals on the other CTA's barriers at cluster scope, 980 cycles each, had taken 1,339.
+// Tried and slower: sixteen softmax warps for bf16 (464 for 441), V by whole groups through two slots (440 for 435).
 //
 // Cleaning: a masked entry has a weight of zero, but zero times a NaN or infinity is none.  Rows that do not
 // exist are zeroed.  A drafted token's row that is not finite makes the score of whoever sees it NaN or
@@ -67,7 +80,8 @@ constexpr int kSBufs = 4;            // S buffers in TMEM
 constexpr int kQScales = 8;          // units whose scales of q may be in use: S runs up to kSBufs tiles ahead
 constexpr int kTmemCols = 512;
 constexpr int kSCol = 256;           // O from column 0, S of 64 columns each
-constexpr int kUnitCost = 2;         // tiles' worth of a unit's q and epilogue
+constexpr int kUnitCost = 4;         // tiles' worth of a unit's q and epilogue (2, 3, 6: 392, 375, 377 us for 371,
+                                     // 32 drafts; 210, 204, 215 for 205, 12 e4m3 drafts)
 constexpr int kMaxSlices = 128;
 
 constexpr float kPUnit = 1024.f;     // e4m3: unit of the weights (times 2^5 at most: an e5m2 number)
@@ -77,7 +91,8 @@ enum { kFirst = 1, kLast = 2, kFinal = 4, kEnd = 8, kClean = 16 };
 template <bool kFp8>
 struct Cfg {
   static constexpr int kKSlots = kFp8 ? 2 : 3, kVSlots = kFp8 ? 2 : 3;
-  // Softmax warps: e4m3's longer arithmetic is faster on sixteen (228 us against 250), bf16's on eight (441 against 464).
+  // Softmax warps: e4m3's longer arithmetic is faster on sixteen (278 us against 308), bf16's on eight (441 against
+  // 464, both at the time).
   static constexpr int kSoftmaxWarps = kFp8 ? 16 : 8;
   static constexpr int kThreads = 32 * (kSoftmaxWarps + kRoles);
   static constexpr int kParts = kSoftmaxWarps / 2, kKeys = kTile / kParts;   // threads of a row, entries of a thread
@@ -112,7 +127,8 @@ struct Cfg {
   // Barriers at the same place in both CTAs.  Those marked L are used in the first CTA alone, whose MMA warp
   // waits for both; those marked 2 are completed in both by the MMAs' commits.  Every wait by parity comes when
   // that phase is the next to complete or the last that did: each role passes every phase of what it waits for.
-  static constexpr int bKFull = 0 /* cp.async */, bKReady = bKFull + kKSlots /* L */, bKEmpty = bKReady + kKSlots /* 2 */,
+  static constexpr int bKFull = 0 /* cp.async */, bKReady = bKFull + kKSlots /* L */,
+                       bKEmpty = bKReady + kKSlots /* 2 */,
                        bVFull = bKEmpty + kKSlots, bVReady = bVFull + kVSlots /* L */,
                        bVEmpty = bVReady + kVSlots /* 2 */, bSFull = bVEmpty + kVSlots /* 2 */,
                        bSEmpty = bSFull + kSBufs /* L */, bPReady = bSEmpty + kSBufs /* L */,
@@ -131,13 +147,14 @@ struct Part {                 // the unit cut at the end of a slice: its first r
 
 struct TreeParams {
   CUtensorMap chunk;          // the pool's rows, boxes of 128 bytes by `box` rows
+  CUtensorMap q_lat, q_rope;  // bf16, with q_box: q by 128-byte chunks, boxes of 64 rows
   CUtensorMap k_box, v_box;   // the same by whole 128-byte chunks, boxes of a fill's chunks by 64 rows (box 64)
   LatentTreeArgs a;
   int box, box_shift;         // rows of a box: 8, 16, 32 or 64 (0: cp.async), and log2 of them
   int slices;
   // |scale| log2(e); bf16: never 0 (times a masked score's -inf it would be NaN), a scale of 0 is q = 0 instead
   float scale_log2;
-  int q_zero, negate;
+  int q_zero, negate, q_box;
   Part* cut;                  // [slices]
   float* lse;                 // [slices][2][128], log2 units
   float* part;                // [slices][2][128][L]
@@ -181,11 +198,8 @@ __device__ __forceinline__ void mbar_arrive_pair(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 
-// A value the compiler does not know (so that it makes no copy of a loop for its first trip).
-__device__ __forceinline__ void opaque(int& x) { asm volatile("" : "+r"(x)); }
-
-// Waits whose polls are out of line.  Each role's loop is fetched anew every tile, and with the polls of some forty
-// waits in line the kernel was 139 KB of code, whose fetching took 5.6 of every 16 cycles of a warp.
+// Waits whose polls are out of line: each role's loop is fetched anew every tile, and the less there is of it the
+// better.
 __device__ __noinline__ bool wait_on(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
   return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag));
 }
@@ -203,7 +217,8 @@ __device__ __forceinline__ void tma_row_pair(uint32_t dst, const CUtensorMap* ma
       "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(r), "r"(bar)
       : "memory");
 }
-__device__ __forceinline__ void tma_box3_pair(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
+__device__ __forceinline__ void tma_box3_pair(uint32_t dst, const CUtensorMap* map, int x, int y, int z,
+                                              uint32_t bar) {
   asm volatile(
       "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
       " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
@@ -264,8 +279,8 @@ __device__ __noinline__ Seq load_seqs(const LatentTreeArgs& a, int b0, int& top)
 // e4m3: q as two e4m3 terms times a power of two a row, in the order of the MMA's operand.  A warp takes a row; the
 // last R columns repeat the rotary part, against the low codes of the rows.  (Rows of a unit's last that
 // belong to no token keep what they hold: their results are not stored.)
-__global__ void __launch_bounds__(256) tree_q_kernel(const __grid_constant__ LatentTreeArgs a, uint8_t* __restrict__ codes,
-                                                     float* __restrict__ scales) {
+__global__ void __launch_bounds__(256)
+    tree_q_kernel(const __grid_constant__ LatentTreeArgs a, uint8_t* __restrict__ codes, float* __restrict__ scales) {
   pdl_launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int nlp = a.pool.L >> 3, nrp = a.pool.R >> 3, n_chunks = (a.pool.row_bytes + 127) >> 7;
@@ -329,8 +344,8 @@ __device__ __forceinline__ void tmem_ld(uint32_t at, float (&x)[kN]) {
   else tmem_ld32(at, x);
 }
 
-// 16-byte units u[0 .. 3] of the rows of four neighbouring lanes, transposed: lane j of the four then has unit j of all
-// four rows.
+// 16-byte units u[0 .. 3] of the rows of four neighbouring lanes, transposed: lane j of the four then has unit j of
+// all four rows.
 __device__ __forceinline__ void transpose4(uint4 (&u)[4]) {
   const int lane = threadIdx.x & 31;
 #pragma unroll
@@ -408,13 +423,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<kFp8>::kThreads,
       mbar_init(BAR(C::bPReady + i), 2 * C::kSoftmaxWarps);
       mbar_init(BAR(C::bPvDone + i), 1);
     }
-    mbar_init(BAR(C::bQFull), kFp8 ? 2 : 8);
+    mbar_init(BAR(C::bQFull), kFp8 || p.q_box ? 2 : 8);
     mbar_init(BAR(C::bQLocal), 1);
     mbar_init(BAR(C::bQEmpty), 1);
     mbar_init(BAR(C::bOFree), 2 * C::kSoftmaxWarps);
     for (int i = 0; i < kInfos; ++i) {
       mbar_init(BAR(C::bInfoFull + i), 1);
-      mbar_init(BAR(C::bInfoEmpty + i), C::kSoftmaxWarps + (rank == 0 ? 7 : 5));   // and the cleaning, q and MMA warps
+      mbar_init(BAR(C::bInfoEmpty + i), C::kSoftmaxWarps + (rank == 0 ? 7 : 5));   // (roles 0 and 3: the first CTA)
     }
     mbar_init(BAR(C::bDrain), 1);
     mbar_init(BAR(C::bDrain + 1), 1);
@@ -602,10 +617,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<kFp8>::kThreads,
     bool ok = true;
     Tile nxt = {}, x = {};
     int box_rows = 0;
-    int k = -1;
-    opaque(k);
 #pragma unroll 1
-    for (; ok; ++k) {
+    for (int k = -1; ok; ++k) {
       x = nxt;
       const int seq = u_seq;
       if (k < 0 || !(x.flags & (kEnd | kFinal))) next_tile(nxt);
@@ -684,15 +697,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<kFp8>::kThreads,
 #pragma unroll
         for (int e = 0; e < 4; ++e) one |= sc[e] == 1.f;
         if (__any_sync(0xffffffffu, one)) {
-#pragma unroll 1
-          for (int e = 0; e < 4; ++e) {
-            const float s = latent_scale_of(a.pool.rows, W, e == 0 ? rows4[0] : e == 1 ? rows4[1] : e == 2 ? rows4[2] : rows4[3],
-                                            e == 0 ? sc[0] : e == 1 ? sc[1] : e == 2 ? sc[2] : sc[3]);
-            if (e == 0) sc[0] = s;
-            else if (e == 1) sc[1] = s;
-            else if (e == 2) sc[2] = s;
-            else sc[3] = s;
-          }
+#pragma unroll
+          for (int e = 0; e < 4; ++e) sc[e] = latent_scale_of(a.pool.rows, W, rows4[e], sc[e]);
         }
         // the maximum of a tile is taken over p_j |scale_j|, the weights that enter the value product (a scale
         // below 2^-60 counts as that: the sums of p_j alone must stay finite)
@@ -725,7 +731,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<kFp8>::kThreads,
     // ================================= MMAs of S ==========================================
     if (rank == 0) {
       // (bit 13 negates A: a negative scale)
-      const uint32_t idS = (kFp8 ? idesc_e4m3(128, 128, 0, 0) : idesc_bf16(128, 128, 0, 0)) | (p.negate ? 1u << 13 : 0u);
+      const uint32_t idS =
+          (kFp8 ? idesc_e4m3(128, 128, 0, 0) : idesc_bf16(128, 128, 0, 0)) | (p.negate ? 1u << 13 : 0u);
       const uint64_t dq = sdesc(sb + C::kQOff, 16, 1024), dk0 = sdesc(sb + C::kKOff, 16, 1024);
       constexpr uint32_t kQChunk = (kFp8 ? 2 : 1) * kChunk;
       const bool lead = elect_one();
@@ -1008,31 +1015,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<kFp8>::kThreads,
       if (first && ok) {
         const uint32_t ph = (units & 1) ^ 1;
         ++units;
-        if (kFp8) {
+        if (kFp8 || p.q_box) {
           if (role == 4) {
             ok = tree_wait(BAR(C::bQEmpty), ph, abort_flag);
-            if (ok && elect_one()) {
-              const long long slot = q_slot(info.tok0, a.H, info.seq, info.unit_row / kUnitRows);
-              const uint32_t bytes = (uint32_t)n_chunks * 2 * kChunk;
-              mbar_arrive_expect_tx(BAR(C::bQLocal), bytes + kRows * 4);
-              bulk_load(sb + C::kQOff, p.q_codes + (slot * 2 + rank) * bytes, bytes, BAR(C::bQLocal));
-              bulk_load(sb + C::kQScaleOff + (units % kQScales) * kRows * 4, p.q_scale + slot * kUnitRows + rank * kRows, kRows * 4,
-                        BAR(C::bQLocal));
+            if (ok && lead) {
+              if (kFp8) {
+                const long long slot = q_slot(info.tok0, a.H, info.seq, info.unit_row / kUnitRows);
+                const uint32_t bytes = (uint32_t)n_chunks * 2 * kChunk;
+                mbar_arrive_expect_tx(BAR(C::bQLocal), bytes + kRows * 4);
+                bulk_load(sb + C::kQOff, p.q_codes + (slot * 2 + rank) * bytes, bytes, BAR(C::bQLocal));
+                bulk_load(sb + C::kQScaleOff + (units % kQScales) * kRows * 4, p.q_scale + slot * kUnitRows + rank * kRows,
+                          kRows * 4, BAR(C::bQLocal));
+              } else {
+                // (rows behind the unit's last are other tokens' or past the last, then zeros: not stored)
+                const int sr = info.unit_row + rank * kRows, h = sr % a.H;
+                const int t = p.q_zero ? a.T : info.tok0 + sr / a.H;
+                mbar_arrive_expect_tx(BAR(C::bQLocal), (uint32_t)n_chunks * kChunk);
+                tma_box4(sb + C::kQOff, &p.q_lat, 0, h, t, 0, BAR(C::bQLocal));
+                if (a.pool.R > 0) tma_box3(sb + C::kQOff + (L >> 6) * kChunk, &p.q_rope, 0, h, t, BAR(C::bQLocal));
+              }
             }
             __syncwarp();
             if (ok) ok = tree_wait(BAR(C::bQLocal), ph ^ 1, abort_flag);
             if (ok && lane == 0) mbar_arrive_pair(lead_bar(C::bQFull));
           }
         } else {
-          // (on its way to L2 while the place is still in use: the unit is announced some tiles ahead)
           const int jj = tid & 7;
-          for (int i = 0; i < 4; ++i) {
-            const int ur = rank * kRows + (tid >> 3) + 16 * i;
-            if (ur >= info.rows) break;
-            const int sr = info.unit_row + ur;
-            const uint8_t* ql = a.q_latent + (info.tok0 + sr / a.H) * a.ql_st + sr % a.H * a.ql_sh;
-            if (jj * 128 < 2 * L) asm volatile("prefetch.global.L2 [%0];" ::"l"(ql + jj * 128));
-          }
           ok = tree_wait(BAR(C::bQEmpty), ph, abort_flag);
           if (ok) {
 #pragma unroll 1
@@ -1063,7 +1071,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<kFp8>::kThreads,
     cp_async_wait_all();
     // copies in flight must land before the CTA ends (at once after a normal run)
     if (role == 4 && lane == 0) {
-      if (kFp8 && units > 0) drain(BAR(C::bQLocal), (units - 1) & 1);
+      if ((kFp8 || p.q_box) && units > 0) drain(BAR(C::bQLocal), (units - 1) & 1);
       for (long long f = max(0LL, fills - vs.n); f < fills; ++f)
         drain(BAR(C::bVFull + (int)(f % vs.n)), (uint32_t)((f / vs.n) & 1));
     }
@@ -1110,78 +1118,78 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<kFp8>::kThreads,
         flags_next = info.flags;
         if (flags_next & kEnd) break;
         if (n == k || (kBox && !(flags_next & kFirst))) {
-        if (flags_next & kFirst) ++units_next;
-        seen_next = info.valid[e0 >> 5] >> (e0 & 31) & kAll;
-        const int rel = info.rel + e0;
-        if (rel > -kKeys) {
-          // drafted tokens among entries e0 ..: by the mask of this row's token
-          const int ur = rank * kRows + row;
-          uint32_t bits = 0;
-          if (ur < info.rows) {
-            const int i = (info.unit_row + ur) / a.H;            // the row's drafted token
-            if (a.mask) {
-              const uint32_t* mk = a.mask + (size_t)(info.tok0 + i) * a.mask_words;
-              const int at = rel < 0 ? 0 : rel >> 5;
-              const uint32_t w0 = at < a.mask_words ? __ldg(mk + at) : 0u;
-              if (rel < 0) bits = (w0 << -rel) | ((1u << -rel) - 1u);
-              else {
-                const uint32_t w1 = at + 1 < a.mask_words ? __ldg(mk + at + 1) : 0u;
-                bits = __funnelshift_r(w0, w1, rel & 31);
+          if (flags_next & kFirst) ++units_next;
+          seen_next = info.valid[e0 >> 5] >> (e0 & 31) & kAll;
+          const int rel = info.rel + e0;
+          if (rel > -kKeys) {
+            // drafted tokens among entries e0 ..: by the mask of this row's token
+            const int ur = rank * kRows + row;
+            uint32_t bits = 0;
+            if (ur < info.rows) {
+              const int i = (info.unit_row + ur) / a.H;            // the row's drafted token
+              if (a.mask) {
+                const uint32_t* mk = a.mask + (size_t)(info.tok0 + i) * a.mask_words;
+                const int at = rel < 0 ? 0 : rel >> 5;
+                const uint32_t w0 = at < a.mask_words ? __ldg(mk + at) : 0u;
+                if (rel < 0) bits = (w0 << -rel) | ((1u << -rel) - 1u);
+                else {
+                  const uint32_t w1 = at + 1 < a.mask_words ? __ldg(mk + at + 1) : 0u;
+                  bits = __funnelshift_r(w0, w1, rel & 31);
+                }
+              } else {
+                const int c = i - rel + 1;                         // entries up to token i's
+                bits = c >= 32 ? 0xffffffffu : c <= 0 ? 0u : (1u << c) - 1u;
               }
-            } else {
-              const int c = i - rel + 1;                         // entries up to token i's
-              bits = c >= 32 ? 0xffffffffu : c <= 0 ? 0u : (1u << c) - 1u;
             }
+            seen_next &= bits;
           }
-          seen_next &= bits;
-        }
-        if (!tree_wait(BAR(C::bSFull + n % kSBufs), (uint32_t)((n / kSBufs) & 1), abort_flag)) break;
-        __syncwarp();
-        tc_fence_after();
-        float x[kKeys];
-        tmem_ld(lanes + kSCol + (n % kSBufs) * 64 + kKeys * ch, x);
-        tmem_wait_ld();
-        const float arg = row_arg(units_next);
-        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-        if constexpr (kFp8) {
-          // of the weights that enter the value product, p_j scale_j
-          const float4* ks = reinterpret_cast<const float4*>(info.scale + e0);
-          const float4* ls = reinterpret_cast<const float4*>(info.lscale + e0);
+          if (!tree_wait(BAR(C::bSFull + n % kSBufs), (uint32_t)((n / kSBufs) & 1), abort_flag)) break;
+          __syncwarp();
+          tc_fence_after();
+          float x[kKeys];
+          tmem_ld(lanes + kSCol + (n % kSBufs) * 64 + kKeys * ch, x);
+          tmem_wait_ld();
+          const float arg = row_arg(units_next);
+          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+          if constexpr (kFp8) {
+            // of the weights that enter the value product, p_j scale_j
+            const float4* ks = reinterpret_cast<const float4*>(info.scale + e0);
+            const float4* ls = reinterpret_cast<const float4*>(info.lscale + e0);
 #pragma unroll
-          for (int j = 0; j < kKeys / 4; ++j) {
-            const float4 c = ks[j], d = ls[j];
-            const float cs[4] = {c.x, c.y, c.z, c.w}, ds[4] = {d.x, d.y, d.z, d.w};
+            for (int j = 0; j < kKeys / 4; ++j) {
+              const float4 c = ks[j], d = ls[j];
+              const float cs[4] = {c.x, c.y, c.z, c.w}, ds[4] = {d.x, d.y, d.z, d.w};
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float z = fmaf(arg, x[4 * j + e] * cs[e], ds[e]);
-              mx[e] = fmaxf(mx[e], (seen_next >> (4 * j + e)) & 1u ? z : -INFINITY);
+              for (int e = 0; e < 4; ++e) {
+                const float z = fmaf(arg, x[4 * j + e] * cs[e], ds[e]);
+                mx[e] = fmaxf(mx[e], (seen_next >> (4 * j + e)) & 1u ? z : -INFINITY);
+              }
             }
-          }
-        } else {
-          if (seen_next != kAll) {
+          } else {
+            if (seen_next != kAll) {
 #pragma unroll
-            for (int j = 0; j < kKeys; ++j) x[j] = (seen_next >> j) & 1u ? x[j] : -INFINITY;
-          }
+              for (int j = 0; j < kKeys; ++j) x[j] = (seen_next >> j) & 1u ? x[j] : -INFINITY;
+            }
 #pragma unroll
-          for (int j = 0; j < kKeys; ++j) mx[j & 3] = fmaxf(mx[j & 3], x[j]);
-        }
-        const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-        // (The place is that of tile n - 4, whose maxima everybody has read: its value products were waited for at tile
-        // n - 2.  Two barriers: a warp is here for tile n + 1 after it has waited for tile n, but before others have.)
-        uint8_t* at = max_at + n % 4 * C::kMaxTile + part * C::kMaxBytes;
-        if (kFp8) *reinterpret_cast<float*>(at) = mt;
-        else *reinterpret_cast<__nv_bfloat16*>(at) = __float2bfloat16(mt * arg);    // (arg > 0)
-        __syncwarp();
-        if (lane == 0) mbar_arrive(BAR(C::bMax + (n & 1)));
-        __syncwarp();
-        ++n;
-        all = flags_next & kFinal;
-        if (n == k + 1) {
-          flags = flags_next;
-          seen = seen_next;
-          units = units_next;
-          continue;
-        }
+            for (int j = 0; j < kKeys; ++j) mx[j & 3] = fmaxf(mx[j & 3], x[j]);
+          }
+          const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+          // (The place is that of tile n - 4, whose maxima everybody has read: its value products were waited for at tile
+          // n - 2.  Two barriers: a warp is here for tile n + 1 after it has waited for tile n, but before others have.)
+          uint8_t* at = max_at + n % 4 * C::kMaxTile + part * C::kMaxBytes;
+          if (kFp8) *reinterpret_cast<float*>(at) = mt;
+          else *reinterpret_cast<__nv_bfloat16*>(at) = __float2bfloat16(mt * arg);    // (arg > 0)
+          __syncwarp();
+          if (lane == 0) mbar_arrive(BAR(C::bMax + (n & 1)));
+          __syncwarp();
+          ++n;
+          all = flags_next & kFinal;
+          if (n == k + 1) {
+            flags = flags_next;
+            seen = seen_next;
+            units = units_next;
+            continue;
+          }
         }
       }
       // ---- weights of tile k ----
@@ -1243,6 +1251,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<kFp8>::kThreads,
           x[j + 1] = fast_exp2(x[j + 1]);
         }
       }
+      float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int j = 0; j < kKeys; j += 2) add_f32x2(sum[j & 2], sum[(j & 2) + 1], x[j], x[j + 1]);
+      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
       // P in registers: 16-byte units of eight entries, or (e4m3) of sixteen for each term
       constexpr int kUnits = kFp8 ? 3 : kKeys / 8;
       uint4 pu[kUnits];
@@ -1313,11 +1325,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<kFp8>::kThreads,
       if (flags & kLast) slot = info.slot, n_rows = info.rows, first_row = info.first_row;
       __syncwarp();
       if (lane == 0) mbar_arrive(BAR(C::bInfoEmpty + ri));
-      // (nobody waits for the denominators)
-      float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int j = 0; j < kKeys; j += 2) add_f32x2(sum[j & 2], sum[(j & 2) + 1], x[j], x[j + 1]);
-      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
       if (flags & kLast) {
         // ---- epilogue: denominators, then O ----
         if (!tree_wait(BAR(C::bPvDone + (k & 1)), (uint32_t)((k >> 1) & 1), abort_flag)) break;
@@ -1560,6 +1567,22 @@ cudaError_t launch_latent_tree(const LatentTreeArgs& a, bool fp8, void* workspac
       const unsigned kb[3] = {128, kGroup, kKFill}, vb[3] = {128, kGroup, kVFill};
       if (!encode_bytes(&p.k_box, a.pool.rows, 3, d3, st3, kb) || !encode_bytes(&p.v_box, a.pool.rows, 3, d3, st3, vb))
         return cudaErrorInvalidValue;
+    }
+  }
+  // bf16 q by tensor maps, where 64 rows are whole tokens or part of one (else by cp.async).
+  if (!fp8 && (a.H % kRows == 0 || kRows % a.H == 0)) {
+    p.q_box = 1;
+    const unsigned hb = a.H < kRows ? (unsigned)a.H : (unsigned)kRows, tb = kRows / hb;
+    const auto stride = [](long long n, long long s, long long other) { return (unsigned long long)(n > 1 ? s : other); };
+    const unsigned long long H = a.H, T = a.T, lh = stride(a.H, a.ql_sh, 2LL * a.pool.L), rh = stride(a.H, a.qr_sh, 2LL * a.pool.R);
+    const unsigned long long d[4] = {128, H, T, (unsigned long long)(a.pool.L / 64)};
+    const unsigned long long st[3] = {lh, stride(a.T, a.ql_st, lh * H), 128};
+    const unsigned bx[4] = {128, hb, tb, (unsigned)(a.pool.L / 64)};
+    if (!encode_bytes(&p.q_lat, a.q_latent, 4, d, st, bx)) return cudaErrorInvalidValue;
+    if (a.pool.R > 0) {
+      const unsigned long long dr[3] = {2ull * a.pool.R, H, T}, sr[2] = {rh, stride(a.T, a.qr_st, rh * H)};
+      const unsigned br[3] = {128, hb, tb};
+      if (!encode_bytes(&p.q_rope, a.q_rope, 3, dr, sr, br)) return cudaErrorInvalidValue;
     }
   }
   const long long rows = (long long)a.T * a.H;
