@@ -40,11 +40,13 @@
 //     are its 52 MMAs and about 3,100 what it moves through shared memory (399 KB: the MMAs 245, the copies 138)
 //   12 drafts of 20 to 60 tokens behind up to 16,004 entries, 16 heads, e4m3, pages of 24: 205 us (692 TFLOP/s)
 //   one draft of 8 tokens behind 4,097 entries, 64 heads, bf16: 30 us, two tiles a pair
-// A role's loop runs once a tile and is fetched anew each time (under ncu a warp that issues waits 5.6 cycles for its
-// next instruction), so that some six cycles an instruction decide what a tile takes.  Steps, for the 32 drafts: one
-// warp for all copies and one for all MMAs 720 us; a warp each 487; page tables apart from K's copies 459; polls
-// and divisions out of line 441; P of two tiles in turn 394; q by tensor maps and the unit's cost in the schedule
-// 371.  Arrivals on the other CTA's barriers at cluster scope, 980 cycles each, had taken 1,339.
+// These cycles are computed, from the MMAs' measured rate and 128 bytes a cycle of shared memory; by them shared
+// memory is what a bf16 tile waits for.  Under ncu tensor cores are active 58% of the kernel (e4m3 48%).  Before
+// it was the roles' code, each loop fetched anew for every tile: with 139 KB of it a warp that issued had waited 5.6
+// cycles for its next instruction, now 0.5.  Steps, for the 32 drafts: one warp for all copies and one for all MMAs
+// 720 us; a warp each 487; page tables apart from K's copies 459; polls and divisions out of line, one place for
+// each fill 441; P of two tiles in turn 394; q by tensor maps and the unit's cost in the schedule 371.  Arrivals
+// on the other CTA's barriers at cluster scope, 980 cycles each, had taken 1,339.
 // Tried and slower: sixteen softmax warps for bf16 (464 for 441), V by whole groups through two slots (440 for 435).
 //
 // Cleaning: a masked entry has a weight of zero, but zero times a NaN or infinity is none.  Rows that do not
@@ -1024,7 +1026,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<kFp8>::kThreads,
                 const uint32_t bytes = (uint32_t)n_chunks * 2 * kChunk;
                 mbar_arrive_expect_tx(BAR(C::bQLocal), bytes + kRows * 4);
                 bulk_load(sb + C::kQOff, p.q_codes + (slot * 2 + rank) * bytes, bytes, BAR(C::bQLocal));
-                bulk_load(sb + C::kQScaleOff + (units % kQScales) * kRows * 4, p.q_scale + slot * kUnitRows + rank * kRows,
+                bulk_load(sb + C::kQScaleOff + (units % kQScales) * kRows * 4,
+                          p.q_scale + slot * kUnitRows + rank * kRows,
                           kRows * 4, BAR(C::bQLocal));
               } else {
                 // (rows behind the unit's last are other tokens' or past the last, then zeros: not stored)
@@ -1573,8 +1576,11 @@ cudaError_t launch_latent_tree(const LatentTreeArgs& a, bool fp8, void* workspac
   if (!fp8 && (a.H % kRows == 0 || kRows % a.H == 0)) {
     p.q_box = 1;
     const unsigned hb = a.H < kRows ? (unsigned)a.H : (unsigned)kRows, tb = kRows / hb;
-    const auto stride = [](long long n, long long s, long long other) { return (unsigned long long)(n > 1 ? s : other); };
-    const unsigned long long H = a.H, T = a.T, lh = stride(a.H, a.ql_sh, 2LL * a.pool.L), rh = stride(a.H, a.qr_sh, 2LL * a.pool.R);
+    const auto stride = [](long long n, long long s, long long other) {
+      return (unsigned long long)(n > 1 ? s : other);
+    };
+    const unsigned long long H = a.H, T = a.T;
+    const unsigned long long lh = stride(a.H, a.ql_sh, 2LL * a.pool.L), rh = stride(a.H, a.qr_sh, 2LL * a.pool.R);
     const unsigned long long d[4] = {128, H, T, (unsigned long long)(a.pool.L / 64)};
     const unsigned long long st[3] = {lh, stride(a.T, a.ql_st, lh * H), 128};
     const unsigned bx[4] = {128, hb, tb, (unsigned)(a.pool.L / 64)};
