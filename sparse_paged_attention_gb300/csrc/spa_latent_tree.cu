@@ -35,17 +35,18 @@
 // tile k + 1 is put into shared memory before the exponentials of tile k, and read a tile later.
 //
 // Measured (L = 512, R = 64, calls one after the other, inputs larger than L2):
-//   32 drafts of 5 to 16 tokens behind up to 8,187 entries, 128 heads, bf16: 371 us (1,234 TFLOP/s, 65% of the
+//   32 drafts of 5 to 16 tokens behind up to 8,187 entries, 128 heads, bf16: 361 us (1,268 TFLOP/s, 67% of the
 //     measured bf16 rate); 172 tiles and 4.6 units a pair, some 3,500 cycles a tile, everything counted, of which 2,180
 //     are its 52 MMAs and about 3,100 what it moves through shared memory (399 KB: the MMAs 245, the copies 138)
-//   12 drafts of 20 to 60 tokens behind up to 16,004 entries, 16 heads, e4m3, pages of 24: 205 us (692 TFLOP/s)
+//   12 drafts of 20 to 60 tokens behind up to 16,004 entries, 16 heads, e4m3, pages of 24: 193 us (734 TFLOP/s)
 //   one draft of 8 tokens behind 4,097 entries, 64 heads, bf16: 30 us, two tiles a pair
 // These cycles are computed, from the MMAs' measured rate and 128 bytes a cycle of shared memory; by them shared
 // memory is what a bf16 tile waits for.  Under ncu tensor cores are active 58% of the kernel (e4m3 48%).  Before
 // it was the roles' code, each loop fetched anew for every tile: with 139 KB of it a warp that issued had waited 5.6
 // cycles for its next instruction, now 0.5.  Steps, for the 32 drafts: one warp for all copies and one for all MMAs
 // 720 us; a warp each 487; page tables apart from K's copies 459; polls and divisions out of line, one place for
-// each fill 441; P of two tiles in turn 394; q by tensor maps and the unit's cost in the schedule 371.  Arrivals
+// each fill 441; P of two tiles in turn 394; q by tensor maps and the unit's cost in the schedule 371;
+// the merge's search by ballots 361.  Arrivals
 // on the other CTA's barriers at cluster scope, 980 cycles each, had taken 1,339.
 // Tried and slower: sixteen softmax warps for bf16 (464 for 441), V by whole groups through two slots (440 for 435).
 //
@@ -281,18 +282,21 @@ __device__ __noinline__ Seq load_seqs(const LatentTreeArgs& a, int b0, int& top)
 // e4m3: q as two e4m3 terms times a power of two a row, in the order of the MMA's operand.  A warp takes a row; the
 // last R columns repeat the rotary part, against the low codes of the rows.  (Rows of a unit's last that
 // belong to no token keep what they hold: their results are not stored.)
+// A warp's rows are counted on from sequence to sequence: 12 drafts, 7,500 rows, in 11 us alone; with every sequence
+// begun at the first warp, which left most of them idle, it took 21.
 __global__ void __launch_bounds__(256)
     tree_q_kernel(const __grid_constant__ LatentTreeArgs a, uint8_t* __restrict__ codes, float* __restrict__ scales) {
   pdl_launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int nlp = a.pool.L >> 3, nrp = a.pool.R >> 3, n_chunks = (a.pool.row_bytes + 127) >> 7;
   int top = 0;
+  long long r = (long long)blockIdx.x * 8 + warp;   // this warp's next row, counted on through the sequences
   for (int b0 = 0; b0 < a.pool.B; b0 += 32) {
     const Seq all = load_seqs(a, b0, top);
     for (int k = 0; k < 32 && b0 + k < a.pool.B; ++k) {
       const int lo = __shfl_sync(0xffffffffu, all.lo, k), n = __shfl_sync(0xffffffffu, all.n, k);
       const long long rows = (long long)n * a.H;
-      for (long long r = (long long)blockIdx.x * 8 + warp; r < rows; r += (long long)gridDim.x * 8) {
+      for (; r < rows; r += (long long)gridDim.x * 8) {
         const long long t = lo + r / a.H, h = r % a.H;
         const uint4* ql = reinterpret_cast<const uint4*>(a.q_latent + t * a.ql_st + h * a.ql_sh);
         const uint4* qr = reinterpret_cast<const uint4*>(a.q_rope + t * a.qr_st + h * a.qr_sh);
@@ -334,6 +338,7 @@ __global__ void __launch_bounds__(256)
           *reinterpret_cast<uint2*>(d + kChunk) = make_uint2(low[0] | (low[1] << 16), low[2] | (low[3] << 16));
         }
       }
+      r -= rows;
     }
   }
 }
@@ -1417,7 +1422,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<kFp8>::kThreads,
 }
 
 // Joins the parts of the units that were cut: out = sum_i 2^(lse_i - M) O_i / sum_i 2^(lse_i - M), in the
-// order of the slices.  A warp takes 128 channels of a row, eight parts in flight.  Bound by reading the parts.
+// order of the slices.  A warp takes 128 channels of a row, eight parts in flight.  The 32 drafts above: 19 us alone
+// (27 while a row's item was looked for one by one, each step a load that waits for the last), one draft 9.  Four
+// CTAs an SM: with 6, 8 or 12 the call takes 1 to 2 us more.
 constexpr int kMergeWarps = 8;
 
 __global__ void __launch_bounds__(32 * kMergeWarps)
@@ -1450,8 +1457,9 @@ __global__ void __launch_bounds__(32 * kMergeWarps)
   const int work = item[n_items - 1].w * nq;
   for (int u = blockIdx.x * kMergeWarps + warp; u < work; u += gridDim.x * kMergeWarps) {
     const int r_all = u / nq, d = (u % nq) * 128 + 4 * lane;
-    int i = 0;
-    while (item[i].w <= r_all) ++i;
+    int i = 0;                               // items that end before the row (their ends never fall)
+    for (int b = 0; b < n_items; b += 32)
+      i += __popc(__ballot_sync(0xffffffffu, b + lane < n_items && item[b + lane].w <= r_all));
     const int4 it = item[i];
     const int r = r_all - (i ? item[i - 1].w : 0), n = it.z - it.y + 1;
     const auto at = [&](int s) { return ((size_t)(it.y + s) * 2 + (s == 0 ? 1 : 0)) * kUnitRows + r; };
@@ -1603,7 +1611,8 @@ cudaError_t launch_latent_tree(const LatentTreeArgs& a, bool fp8, void* workspac
   else e = launch_tree<false>(p, stream);
   if (e != cudaSuccess) return e;
   const long long units = (rows * ((a.pool.L + 127) / 128) + kMergeWarps - 1) / kMergeWarps;
-  return launch_with_pdl(tree_merge_kernel, dim3((unsigned)(units < 4LL * sms ? units : 4LL * sms)), dim3(32 * kMergeWarps),
+  const unsigned merge_blocks = (unsigned)(units < 4LL * sms ? units : 4LL * sms);
+  return launch_with_pdl(tree_merge_kernel, dim3(merge_blocks), dim3(32 * kMergeWarps),
                          0, stream, true, (const Part*)p.cut, (const float*)p.lse, (const float*)p.part,
                          reinterpret_cast<__nv_bfloat16*>(a.out), p.slices, a.pool.L);
 }
