@@ -519,7 +519,7 @@ typedef struct spa_head_rows {  /* [num_tokens] x [num_heads] rows of head_dim v
   void* out;                    /* x itself, with its strides, or memory that does not overlap it */
   const void* weight;           /* norm weights [head_dim], fp32 or bf16; NULL: ones               */
   int64_t x_stride_t, x_stride_h;
-  int64_t out_stride_t, out_stride_h;
+  int64_t out_stride_t, out_stride_h;   /* one of them spans the other's rows: no two overlap */
   int32_t num_heads;
   int32_t reserved;             /* 0 */
 } spa_head_rows_t;
@@ -556,7 +556,8 @@ int sparse_attn_norm_rope(const spa_rope_problem_t* prob, void* stream);
  * enter a maximum.
  *   positions: of the rotation, device [num_tokens], any value;  entries: the tokens' places in their
  *   sequences' caches, device [num_tokens] (NULL: the positions), seq_of_token (NULL: sequence 0).  A token that
- *   cannot be placed is skipped and sets SPA_ERR_INDEX, as in the K/V write.
+ *   cannot be placed is skipped and sets SPA_ERR_INDEX, as in the K/V write.  No two tokens of a call may go to
+ *   one place: what it holds then, row and scale, may be parts of both.
  */
 typedef struct spa_append {
   int32_t num_tokens, num_seqs;

@@ -1137,8 +1137,8 @@ def _kv_append(fp8, k, v, positions, pool, table, *, weight=None, eps=None, star
 def sparse_attn_paged_kv_append(k, v, positions, pool, table, **kw):
     """New tokens' K rows (bf16 [T, D], row stride free), normalised (where ``eps`` is given, by
     ``weight``) and rotated by ``positions`` (``table`` None: not), and V rows, as they are, into their
-    slots of a bf16 pool: entry ``entries[t]`` (default: the position) of sequence ``seq_of_token[t]``.
-    ``start``: first rotated value (default: the last ones of the row are rotated)."""
+    slots of a bf16 pool: entry ``entries[t]`` (default: the position) of sequence ``seq_of_token[t]``, no
+    two of a call in one place.  ``start``: first rotated value (default: the last ones of the row are rotated)."""
     _kv_append(False, k, v, positions, pool, table, **kw)
 
 

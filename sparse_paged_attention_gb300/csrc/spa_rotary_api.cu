@@ -29,8 +29,11 @@ int check_rows(const spa_head_rows_t& x, const spa_rope_problem_t* pr, bool norm
   const int64_t st[4] = {x.x_stride_t, x.x_stride_h, x.out_stride_t, x.out_stride_h};
   for (const int64_t s : st)
     if (!stride_ok(s)) return SPA_ERR_SHAPE;
-  // output rows are distinct
-  if ((pr->num_tokens > 1 && x.out_stride_t < pr->head_dim) || (x.num_heads > 1 && x.out_stride_h < pr->head_dim))
+  // output rows are distinct: a token's heads lie within its stride, or a head's tokens within its own
+  const int64_t D = pr->head_dim, ot = x.out_stride_t, oh = x.out_stride_h;
+  const int T = pr->num_tokens, H = x.num_heads;
+  if ((T > 1 && ot < D) || (H > 1 && oh < D) ||
+      (T > 1 && H > 1 && (ot - D) / (H - 1) < oh && (oh - D) / (T - 1) < ot))
     return SPA_ERR_SHAPE;
   if (x.x == x.out && ((pr->num_tokens > 1 && x.x_stride_t != x.out_stride_t) ||
                        (x.num_heads > 1 && x.x_stride_h != x.out_stride_h)))

@@ -157,3 +157,20 @@ def test_tree_refusals(lib, fp8):
     says("SPA_ERR_CUDA")
     says("SPA_ERR_CUDA", tree_mask=None, mask_words=0)
     assert lib.sparse_attn_latent_tree_decode_workspace_size(None, ctypes.byref(latent_pool())) == 0
+
+
+@pytest.mark.parametrize("norm", [False, True])
+@pytest.mark.parametrize("which", ["q", "k"])
+def test_output_rows_that_overlap_are_refused(lib, norm, which):
+    """Each stride alone leaves room for a row, but rows of several tokens and heads fall on one another."""
+    def says(code, T=4, **kw):
+        assert rope(lib, norm, num_tokens=T, **{which: kw}) == S[code], kw
+    for bad in (dict(out_stride_t=64), dict(out_stride_t=504), dict(out_stride_t=64, out_stride_h=248),
+                dict(out_stride_t=1 << 37, out_stride_h=1 << 36)):
+        says("SPA_ERR_SHAPE", **bad)
+    # tokens behind all heads, heads behind all tokens, and one token or head
+    for good in (dict(), dict(out_stride_t=64, out_stride_h=256), dict(out_stride_t=1 << 37, out_stride_h=1 << 34),
+                 dict(out_stride_t=64, num_heads=1)):
+        says("SPA_ERR_CUDA", **good)
+    says("SPA_ERR_CUDA", T=1, out_stride_t=64)
+    says("SPA_ERR_SHAPE", T=1 << 20, out_stride_t=1 << 37, out_stride_h=1 << 38)   # (their product passes 64 bits)
