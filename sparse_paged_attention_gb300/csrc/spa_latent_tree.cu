@@ -44,10 +44,9 @@
 // memory is what a bf16 tile waits for.  Under ncu tensor cores are active 58% of the kernel (e4m3 48%).  Before
 // it was the roles' code, each loop fetched anew for every tile: with 139 KB of it a warp that issued had waited 5.6
 // cycles for its next instruction, now 0.5.  Steps, for the 32 drafts: one warp for all copies and one for all MMAs
-// 720 us; a warp each 487; page tables apart from K's copies 459; polls and divisions out of line, one place for
-// each fill 441; P of two tiles in turn 394; q by tensor maps and the unit's cost in the schedule 371;
-// the merge's search by ballots 361.  Arrivals
-// on the other CTA's barriers at cluster scope, 980 cycles each, had taken 1,339.
+// 755 us; a warp each 487; page tables apart from K's copies 459; polls and divisions out of line, one place for
+// each fill 441; P of two tiles in turn 394; q by tensor maps and the unit's cost in the schedule 371; the merge's
+// search by ballots 361.  Arrivals on the other CTA's barriers at cluster scope, 980 cycles each, had taken 1,339.
 // Tried and slower: sixteen softmax warps for bf16 (464 for 441), V by whole groups through two slots (440 for 435).
 //
 // Cleaning: a masked entry has a weight of zero, but zero times a NaN or infinity is none.  Rows that do not
