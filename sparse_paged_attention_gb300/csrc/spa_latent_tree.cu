@@ -32,7 +32,9 @@
 //                  nor are a multiple of it, pages that are not a multiple of eight entries.)
 //
 // The running maximum of a row, which its 4 (8) threads have to agree on, costs no barrier: a thread's maximum of
-// tile k + 1 is put into shared memory before the exponentials of tile k, and read a tile later.
+// tile k + 1 goes into one word of shared memory a row and tile, by an atomic maximum (whose result does not depend
+// on an order), before the exponentials of tile k, and is read a tile later.  In fp32: as the reference of the
+// exponentials it may be off by no more than an exponent can hold, however large the scores are.
 //
 // Measured (L = 512, R = 64, calls one after the other, inputs larger than L2):
 //   32 drafts of 5 to 16 tokens behind up to 8,187 entries, 128 heads, bf16: 361 us (1,268 TFLOP/s, 67% of the
@@ -79,6 +81,7 @@ constexpr int kKFill = 3, kVFill = 2;   // chunks of a fill
 constexpr int kInfos = 4;            // tile infos in flight
 constexpr int kRoles = 8;            // warps besides the softmax warps
 constexpr int kSBufs = 4;            // S buffers in TMEM
+constexpr int kMaxTiles = 8;         // tiles whose maxima have a place: see the softmax warps
 constexpr int kQScales = 8;          // units whose scales of q may be in use: S runs up to kSBufs tiles ahead
 constexpr int kTmemCols = 512;
 constexpr int kSCol = 256;           // O from column 0, S of 64 columns each
@@ -98,7 +101,6 @@ struct Cfg {
   static constexpr int kSoftmaxWarps = kFp8 ? 16 : 8;
   static constexpr int kThreads = 32 * (kSoftmaxWarps + kRoles);
   static constexpr int kParts = kSoftmaxWarps / 2, kKeys = kTile / kParts;   // threads of a row, entries of a thread
-  static constexpr int kMaxBytes = kFp8 ? 4 : 2;     // of a partial maximum: e4m3's reference has to be exact
   static constexpr int kCw = kFp8 ? 128 : 64;        // channels of a chunk
   static constexpr int kMaxChunks = kFp8 ? 5 : 9;    // of a row
   static constexpr float kTau = kFp8 ? 5.f : 8.f;    // lazy rescale threshold (log2 units)
@@ -117,9 +119,8 @@ struct Cfg {
   static constexpr int kKOff = kPOff + 2 * kPBytes;              // (P of two tiles)
   static constexpr int kVOff = kKOff + kKSlots * kKFill * kChunk;
   static constexpr int kVEnd = kVOff + kVSlots * kVFill * kChunk;
-  static constexpr int kMaxOff = kVEnd;                            // [4 tiles][64 rows][kParts]
-  static constexpr int kMaxTile = kRows * kParts * kMaxBytes;
-  static constexpr int kQScaleOff = kMaxOff + 4 * kMaxTile;        // e4m3: float [kQScales][64]
+  static constexpr int kMaxOff = kVEnd;                            // int [kMaxTiles][64 rows], see ordered()
+  static constexpr int kQScaleOff = kMaxOff + kMaxTiles * kRows * 4;   // e4m3: float [kQScales][64]
   static constexpr int kInfoOff = kQScaleOff + (kFp8 ? kQScales * kRows * 4 : 0);
   static constexpr int kInfoEnd = kInfoOff + kInfos * (int)sizeof(Info);
   // Without boxes, the rows of the tiles' entries: int [kInfos][128].  bf16: in the last slot of V, which is
@@ -199,6 +200,9 @@ __device__ __forceinline__ void commit_pair(uint32_t bar) {
 __device__ __forceinline__ void mbar_arrive_pair(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
+
+// An fp32 number that is no NaN as an integer of the same order, and back.
+__device__ __forceinline__ int ordered(int bits) { return bits >= 0 ? bits : bits ^ 0x7fffffff; }
 
 // Waits whose polls are out of line: each role's loop is fetched anew every tile, and the less there is of it the
 // better.
@@ -442,6 +446,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<kFp8>::kThreads,
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
+  for (int i = threadIdx.x; i < kMaxTiles * kRows; i += C::kThreads)
+    reinterpret_cast<int*>(sm + C::kMaxOff)[i] = ordered(__float_as_int(-INFINITY));
   if (role == 0) {
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(sb + C::kMiscOff),
                  "r"(kTmemCols)
@@ -1099,7 +1105,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<kFp8>::kThreads,
     uint8_t* pb = sm + C::kPOff;
     // this thread's units of P (e4m3: its unit of each term)
     uint8_t* p_at = pb + row * 128 + (kFp8 ? ((part ^ (row & 7)) << 4) : grp * kChunk);
-    uint8_t* max_at = sm + C::kMaxOff + row * kParts * C::kMaxBytes;
+    int* max_at = reinterpret_cast<int*>(sm + C::kMaxOff) + row;
     float m = -INFINITY, l = 0.f;
     uint32_t units = 0, units_next = 0;          // begun, by the tile at hand and by the one after it
     // flags and visible entries (bits) of the tile at hand, and of the one after it
@@ -1181,11 +1187,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<kFp8>::kThreads,
             for (int j = 0; j < kKeys; ++j) mx[j & 3] = fmaxf(mx[j & 3], x[j]);
           }
           const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-          // (The place is that of tile n - 4, whose maxima everybody has read: its value products were waited for at tile
-          // n - 2.  Two barriers: a warp is here for tile n + 1 after it has waited for tile n, but before others have.)
-          uint8_t* at = max_at + n % 4 * C::kMaxTile + part * C::kMaxBytes;
-          if (kFp8) *reinterpret_cast<float*>(at) = mt;
-          else *reinterpret_cast<__nv_bfloat16*>(at) = __float2bfloat16(mt * arg);    // (arg > 0)
+          // The place for tile n + 2 is cleared: that of tile n - 6, whose maxima everybody has read, as the value
+          // products of tile n - 4 were waited for at tile n - 2; who writes there has waited for tile n.  (Two
+          // barriers: a warp is here for tile n + 1 after it has waited for tile n, but before others have.)
+          if (part == 0) max_at[(n + 2) % kMaxTiles * kRows] = ordered(__float_as_int(-INFINITY));
+          atomicMax(max_at + n % kMaxTiles * kRows, ordered(__float_as_int(kFp8 ? mt : mt * arg)));   // (bf16: arg > 0)
           __syncwarp();
           if (lane == 0) mbar_arrive(BAR(C::bMax + (n & 1)));
           __syncwarp();
@@ -1210,17 +1216,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<kFp8>::kThreads,
       float x[kKeys];
       tmem_ld(lanes + kSCol + (k % kSBufs) * 64 + kKeys * ch, x);
       if (!tree_wait(BAR(C::bMax + (k & 1)), (uint32_t)((k >> 1) & 1), abort_flag)) break;
-      float mt;
-      {
-        const uint8_t* at = max_at + k % 4 * C::kMaxTile;
-        if constexpr (kFp8) {
-          const float4 u = *reinterpret_cast<const float4*>(at), v = *reinterpret_cast<const float4*>(at + 16);
-          mt = fmaxf(fmaxf(fmaxf(u.x, u.y), fmaxf(u.z, u.w)), fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w)));
-        } else {
-          const uint2 u = *reinterpret_cast<const uint2*>(at);
-          mt = fmaxf(fmaxf(bf16_lo(u.x), bf16_hi(u.x)), fmaxf(bf16_lo(u.y), bf16_hi(u.y)));
-        }
-      }
+      const float mt = __int_as_float(ordered(*reinterpret_cast<volatile int*>(max_at + k % kMaxTiles * kRows)));
       // lazy: the reference moves only where it is exceeded by more than tau
       float al = 1.f;
       if (mt > m + C::kTau) {
