@@ -973,7 +973,8 @@ def sparse_attn_rotary_table(rope_dim, *, base=10000.0, interleaved=True, scalin
                 return rope_dim * math.log(original_length / (turns * 2.0 * math.pi)) / (2.0 * math.log(base))
             if not (0.0 < beta_slow <= beta_fast and original_length > 0):
                 raise ValueError("'yarn' needs 0 < beta_slow <= beta_fast and a positive original_length")
-            lo, hi = max(math.floor(pair(beta_fast)), 0), min(math.ceil(pair(beta_slow)), n - 1)
+            # (the ramp may end behind the last pair, which then keeps a part of its frequency)
+            lo, hi = max(math.floor(pair(beta_fast)), 0), min(math.ceil(pair(beta_slow)), rope_dim - 1)
             ramp = [min(max((i - lo) / max(hi - lo, 0.001), 0.0), 1.0) for i in range(n)]
             freq = [f / factor * r + f * (1.0 - r) for f, r in zip(freq, ramp)]
             amplitude = 0.1 * math.log(factor) + 1.0 if factor > 1.0 else 1.0
