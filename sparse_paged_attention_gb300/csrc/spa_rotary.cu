@@ -10,7 +10,7 @@
 // Angles: a position times a frequency loses the angle's fraction in fp32 (at position 2^20 a step is 1/16
 // of a radian).  The frequencies come as turns a position in 64-bit binary fractions, so the product modulo
 // 2^64 is the fraction of a turn, exactly that of the given frequency at any position; its upper 32 bits
-// go to fp32 (off by 2^-32 turns and 2^-25 of itself).  In 64-bit floating point, which this machine
+// go to fp32 (off by 2^-32 turns and 2^-24 of itself).  In 64-bit floating point, which this machine
 // does at a sixty-fourth of the rate, the angles of 65,536 tokens alone would take about 10 us.
 //
 // Measured (device time of calls in a graph, inputs that change; % of the measured copy rate):
@@ -26,6 +26,7 @@
 #include "spa_errors.h"
 #include "spa_kvwrite_quant.cuh"
 #include "spa_rotary.h"
+#include "spa_rotary_turn.h"
 
 namespace spa {
 
@@ -35,9 +36,8 @@ constexpr int kWarps = 4;
 
 // cos and sin (times the amplitude; sin negated for the inverse) of a pair.
 __device__ __forceinline__ float2 cos_sin(const RotaryDev& r, int pos, int pair) {
-  const long long t = (long long)pos * __ldg(r.turns + pair);
   float c, s;
-  sincospif((float)(int)(t >> 32) * 0x1p-31f, &s, &c);     // (half turns in [-1, 1))
+  sincospif((float)turn_of(pos, __ldg(r.turns + pair)) * 0x1p-31f, &s, &c);     // (half turns in [-1, 1))
   return make_float2(c * r.scale, s * (r.inverse ? -r.scale : r.scale));
 }
 // Those of pairs 2w and 2w + 1.
