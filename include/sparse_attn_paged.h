@@ -548,7 +548,7 @@ int sparse_attn_norm_rope(const spa_rope_problem_t* prob, void* stream);
  * values, by weight and eps) and rotated on the way.
  *   paged pools:  k, v are bf16 [num_tokens] rows of head_dim (a multiple of 64, 64 .. 512).  K is normalised
  *                 and rotated, V stored as it is.  _fp8: one scale for each, max|y| / 448 (1 for a row of
- *                 zeros), codes of y / scale; V's codes and scale are those of the K/V write.
+ *                 zeros, else 2^-149 at least), codes of y / scale; V's codes and scale are those of the K/V write.
  *   latent pools: k is the latent part (latent_dim values: normalised), v the rotary part (rope_dim values:
  *                 rotated; NULL when there is none); head_dim and rope_dim are the pool's, rope_start is
  *                 0.  _fp8: one scale a row over both, two codes a rotary value, as in the latent write.

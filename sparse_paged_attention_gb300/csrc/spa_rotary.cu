@@ -308,7 +308,11 @@ __device__ __forceinline__ int append_row(const AppendArgs& a, int t) {
   return latent_row(a.pool, b, x);
 }
 
-__device__ __forceinline__ float row_scale(float amax) { return amax > 0.f ? __fdiv_rn(amax, 448.f) : 1.f; }
+// (At least fp32's smallest number: normalised or rotated values may be so small that the quotient is zero, and zeros
+// over it would be NaN.)
+__device__ __forceinline__ float row_scale(float amax) {
+  return amax > 0.f ? fmaxf(__fdiv_rn(amax, 448.f), __int_as_float(1)) : 1.f;
+}
 __device__ __forceinline__ float warp_max(float m) {   // of values >= 0 (their bits order as they do)
   return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m)));
 }
