@@ -505,7 +505,9 @@ int sparse_attn_latent_tree_decode_fp8(const spa_latent_pool_t* pool, const spa_
  *
  * Rotation of rope_dim values of a row, from value rope_start on, by the token's position p:
  *     (a, b)_i -> rope_scale * (a cos t_i - b sin t_i, b cos t_i + a sin t_i),   t_i = 2 pi p turns[i] / 2^64
- * (inverse: by -t_i).  interleaved: pair i is values 2i and 2i + 1 of the part; else i and i + rope_dim / 2.
+ * (inverse: by -t_i; rope_scale multiplies all the same, so that it is the rotation's transpose, and x there
+ * and back is rope_scale^2 x).  interleaved: pair i is values 2i and 2i + 1 of the part; else i and
+ * i + rope_dim / 2.
  *   turns: device int64 [rope_dim / 2], the frequencies in turns a position as 64-bit binary fractions (a
  *          frequency of f radians is f / (2 pi) 2^64): the angle is that of the given frequency at
  *          every 32-bit position.  Frequencies scaled for long contexts are other numbers here, and an

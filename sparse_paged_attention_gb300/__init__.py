@@ -1040,8 +1040,9 @@ def _rope_positions(positions, n, dev):
 def sparse_attn_rope(x, positions, table, *, start=None, inverse=False, out=None, stream=None):
     """Rotates part of every head of ``x`` (bf16 [T, H, D], strided views allowed) by the angles of the
     tokens' ``positions`` (int32 [T]): values ``start`` .. of a head (default: its last ones).  ``inverse``
-    takes a rotation off again (what an attention whose values were rotated with its keys needs of its
-    output).  Returns ``out``: a new tensor, or the one given, ``x`` itself among them (in place)."""
+    turns by the opposite angles (what an attention whose values were rotated with its keys needs of its
+    output).  The table's ``scale`` multiplies either way, so x there and back is ``scale ** 2`` times x: the
+    inverse is the rotation's transpose.  Returns ``out``: a new tensor, or the one given, ``x`` itself among them (in place)."""
     lib = load_library()
     dev = x.get_device()
     shape, st, sh = _latent_rows("x", x, 3, None, dev)
