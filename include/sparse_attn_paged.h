@@ -518,7 +518,8 @@ int sparse_attn_latent_tree_decode_fp8(const spa_latent_pool_t* pool, const spa_
  */
 typedef struct spa_head_rows {  /* [num_tokens] x [num_heads] rows of head_dim values */
   const void* x;
-  void* out;                    /* x itself, with its strides, or memory that does not overlap it */
+  void* out;                    /* x itself, with its strides, or memory that does not overlap it; neither
+                                   the other tensor's x nor its out                               */
   const void* weight;           /* norm weights [head_dim], fp32 or bf16; NULL: ones               */
   int64_t x_stride_t, x_stride_h;
   int64_t out_stride_t, out_stride_h;   /* one of them spans the other's rows: no two overlap */

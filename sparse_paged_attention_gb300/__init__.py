@@ -1029,6 +1029,28 @@ def _rope_out(name, x, out, shape, dev, stream):
     return out, st, sh
 
 
+def _rows_meet(T, D, a, b):
+    """Whether [T, H, D] bf16 rows share memory; a, b: (address, H, strides of tokens and heads).  Exact where both
+    have the same strides, else only what begins at one address is seen."""
+    (pa, ha, ta, sa), (pb, hb, tb, sb) = a, b
+    if T == 0 or ha == 0 or hb == 0:
+        return False
+    span_a, span_b = (ha - 1) * sa + D, (hb - 1) * sb + D                     # of a token
+    d = (pb - pa) // 2
+    if d >= (T - 1) * ta + span_a or -d >= (T - 1) * tb + span_b:
+        return False
+    if ta != tb or (ha > 1 and hb > 1 and sa != sb):
+        return d == 0
+    if T > 1 and ta > 0 and d % ta >= span_a and ta - d % ta >= span_b:
+        return False                                                          # side by side in every token
+    for j in range(1 - ha, hb):                                               # one's head minus the other's
+        v = d + j * max(sa, sb)
+        n, r = divmod(v, ta) if T > 1 and ta > 0 else (0, v)                  # (and n tokens)
+        if (-D < r < D and abs(n) < T) or (T > 1 and 0 < ta - r < D and abs(n + 1) < T):
+            return True
+    return False
+
+
 def _rope_positions(positions, n, dev):
     if positions.dtype is not torch.int32 or not positions.is_contiguous() or positions.numel() != n:
         raise ValueError(f"positions must be a contiguous int32 tensor of {n} entries")
@@ -1064,7 +1086,8 @@ def sparse_attn_norm_rope(q, k, positions, table, *, q_weight=None, k_weight=Non
     """RMS norm of every head of ``q`` [T, Hq, D] and ``k`` [T, Hk, D] (None: q alone; bf16, strided views
     allowed) over its D values, by the weights (fp32 or bf16 [D], both of one type; None: ones), then the
     rotation of part of it as in :func:`sparse_attn_rope` (``table`` None: none), in one pass.  Returns
-    (q_out, k_out): new tensors, or those given (in place if they are the inputs)."""
+    (q_out, k_out): new tensors, or those given (in place if they are the inputs), which share no memory
+    with each other and the other's input."""
     lib = load_library()
     dev = q.get_device()
     shape, st, sh = _latent_rows("q", q, 3, None, dev)
@@ -1081,9 +1104,16 @@ def sparse_attn_norm_rope(q, k, positions, table, *, q_weight=None, k_weight=Non
         k_shape, kt, ks = _latent_rows("k", k, 3, D, dev)
         if k_shape[0] != T:
             raise ValueError("q and k must have the same tokens")
+        q_new, k_new = q_out is None, k_out is None
         k_out, ot, oh = _rope_out("k_out", k, k_out, k_shape, dev, stream)
         k_rows = (k.data_ptr(), k_out.data_ptr(), kw, kt, ks, ot, oh, k_shape[1], 0)
     q_out, ot, oh = _rope_out("q_out", q, q_out, shape, dev, stream)
+    if k is not None and not (q_new and k_new):
+        to_q, to_k = (q_out.data_ptr(), H, ot, oh), (k_rows[1], k_shape[1], *k_rows[5:7])
+        if (not q_new and _rows_meet(T, D, to_q, (k_rows[0], k_shape[1], kt, ks))) or \
+                (not k_new and _rows_meet(T, D, to_k, (q.data_ptr(), H, st, sh))) or \
+                (not q_new and not k_new and _rows_meet(T, D, to_q, to_k)):
+            raise ValueError("q_out and k_out must overlap neither each other nor the other's input")
     prob = _ROPE.pack(T, D, R, D - R if start is None else start, interleaved, 0, max(qd, kd, 0), 0, amplitude,
                       eps, pos, turns, q.data_ptr(), q_out.data_ptr(), qw, st, sh, ot, oh, H, 0, *k_rows)
     s = lib.sparse_attn_norm_rope(prob, _launch_stream(stream, dev))
