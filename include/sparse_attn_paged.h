@@ -474,7 +474,9 @@ int sparse_attn_latent_prefill(const spa_latent_prefill_t* prob, void* out, void
  *   context length is negative or whose entries do not fit its row of the block table is left out (its
  *   output rows keep their bytes) and sets SPA_ERR_INDEX.  Query rows of no sequence keep their bytes.
  * Entries on unmapped pages or outside the pool are left out and set SPA_ERR_INDEX.  What a token does not
- * see never enters its sums, whatever its bytes hold.
+ * see never enters its sums, whatever its bytes hold; of a row that is not finite and whose weight is zero (its
+ * score is -infinity) nothing need enter them.  Statistics and sums are fp32, the weights of the value product
+ * and e4m3's queries in fewer bits as in the decode.
  * workspace: as for the decode, of sparse_attn_latent_tree_decode_workspace_size(prob, pool) bytes.
  */
 typedef struct spa_latent_tree {

@@ -36,7 +36,9 @@
 // on an order), before the exponentials of tile k, and is read a tile later.  In fp32: as the reference of the
 // exponentials it may be off by no more than an exponent can hold, however large the scores are.
 //
-// Measured (L = 512, R = 64, calls one after the other, inputs larger than L2):
+// Measured (L = 512, R = 64, device time of calls in a graph, inputs that change from call to call; a call from Python
+// adds about 5 us).  In bursts, at 2,070 MHz: for seconds on end the 32 drafts reach the power limit, 1,700 MHz, and
+// take 394 us either way:
 //   32 drafts of 5 to 16 tokens behind up to 8,187 entries, 128 heads, bf16: 361 us (1,268 TFLOP/s, 67% of the
 //     measured bf16 rate); 172 tiles and 4.6 units a pair, some 3,500 cycles a tile, everything counted, of which 2,180
 //     are its 52 MMAs and about 3,100 what it moves through shared memory (399 KB: the MMAs 245, the copies 138)
@@ -50,6 +52,8 @@
 // each fill 441; P of two tiles in turn 394; q by tensor maps and the unit's cost in the schedule 371; the merge's
 // search by ballots 361.  Arrivals on the other CTA's barriers at cluster scope, 980 cycles each, had taken 1,339.
 // Tried and slower: sixteen softmax warps for bf16 (464 for 441), V by whole groups through two slots (440 for 435).
+// Maxima in fp32 by an atomic maximum cost what bf16 ones in places of their own did (360.2 for 359.7; e4m3, whose were
+// fp32 before, 193.0 for 193.9), and those were wrong: from scores of 3e4 on off by more than an exponent holds.
 //
 // Cleaning: a masked entry has a weight of zero, but zero times a NaN or infinity is none.  Rows that do not
 // exist are zeroed.  A drafted token's row that is not finite makes the score of whoever sees it NaN or
@@ -414,7 +418,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<kFp8>::kThreads,
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::kKSlots; ++i) {
       mbar_init(BAR(C::bKFull + i), 128);
-      mbar_init(BAR(C::bKReady + i), kBox ? 1 : 2);     // armed by the first CTA's loader, or both's warps 10
+      mbar_init(BAR(C::bKReady + i), kBox ? 1 : 2);     // armed by the first CTA's loader, or role 2 of both CTAs
       mbar_init(BAR(C::bKEmpty + i), 1);
     }
     for (int i = 0; i < C::kVSlots; ++i) {

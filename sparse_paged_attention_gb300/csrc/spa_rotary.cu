@@ -16,9 +16,9 @@
 // Measured (device time of calls in a graph, inputs that change; % of the measured copy rate):
 //   norm and rotation, 8,192 tokens, 64 + 1 heads of 512     173.5 us   6.28 TB/s  93%
 //   rotation of 8,192 x 128 heads of 64 in rows of 192        22.1 us   6.07 TB/s  89%
-//   norm and rotation, 3,001 tokens, 20 + 4 heads of 128      12.8 us   2.88 TB/s
-//   K/V append, 65,536 tokens, bf16                           46.7 us   5.76 TB/s  85%
-//   latent append, 65,536 tokens, e4m3                        27.9 us   4.25 TB/s  63%
+//   norm and rotation, 3,001 tokens, 20 + 4 heads of 128      12.8 us   2.88 TB/s  (issue slots 77% full)
+//   K/V append, 65,536 tokens, bf16                           46.7 us   5.76 TB/s  85%   (e4m3 49.5)
+//   latent append, 65,536 tokens, e4m3                        27.9 us   4.25 TB/s  63%   (bf16 29.0)
 //   one to eight tokens: 2 to 3 us, which is a launch
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
